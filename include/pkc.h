@@ -499,6 +499,90 @@ int pkc_cascade_decode_paged_prefix(
     size_t workspace_bytes, void* o, float* lse, int dtype, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Microscaled 4-bit (mx4) paged cache
+ * ---------------------------------------------------------------------- */
+
+/*
+ * The mx4 cache holds K and V at 4.25 bits per element (the microscaling
+ * formats' 4-bit float: blocks of 32 e2m1 elements under one power-of-two
+ * scale).  K and V each have two pools:
+ *   codes  [num_pages, page_size, num_kv_heads, 64] bytes, 16-byte aligned
+ *   scales [num_pages, page_size, num_kv_heads, 4] bytes, 4-byte aligned
+ * Block b of a row is elements 32 b .. 32 b + 31 and has scale byte s_b:
+ * 2^(s_b - 127), 255 stands for NaN and comes with zero codes.  Element
+ * 32 b + 4 u + i is nibble i (lowest first) of the 16-bit little-endian word
+ * 4 u + b of the row's codes; a nibble is sign, two exponent bits, one
+ * mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives.
+ *
+ * pkc_append_kv_mx4: quantise new tokens of every request to the end of its
+ * cache, in place (the mx4 counterpart of pkc_append_kv, for any number of
+ * tokens per request).
+ *   k_new, v_new [total_new, num_kv_heads, 128] of dtype (F16 or BF16)
+ *   new_indptr [batch + 1] int32, device: request b's new tokens are rows
+ *            new_indptr[b] .. new_indptr[b + 1] - 1 (cumulative lengths;
+ *            none, one or many); rows of no request are ignored
+ *   cache_seqlens [batch] int32, device: grown in place by the new tokens
+ * A block's scale is 2^e, e = max(floor(log2 amax) - 2, -126) with amax its
+ * largest magnitude, and its elements the nearest codes of x / 2^e (ties to
+ * the even code, 6 above 6); a block that holds an infinity or a NaN becomes
+ * NaN.  The pages of all new tokens must be in the block table.  A page id
+ * < 0 or >= num_pages (or past the table) is recorded as
+ * PKC_ERR_BLOCK_TABLE, and that request's length stays as it was (tokens of
+ * it that have a page may have been written behind its end); a request whose
+ * new_indptr range is not within 0 .. total_new keeps its length too and is
+ * recorded as PKC_ERR_PLAN.  One launch; the workspace's status block holds
+ * its counter, so a workspace must not be shared by two appends in flight.
+ */
+int pkc_append_kv_mx4(const void* k_new, const void* v_new,
+                      const int32_t* new_indptr, int total_new, void* k_codes,
+                      void* k_scales, void* v_codes, void* v_scales,
+                      const int32_t* block_table, int block_table_stride,
+                      int32_t* cache_seqlens, int batch, int num_kv_heads,
+                      int head_dim, int page_size, int64_t num_pages,
+                      int dtype, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/*
+ * Read tokens of an mx4 cache back as 16-bit rows: row t of k_out / v_out
+ * [total, num_kv_heads, 128] (dtype F16 or BF16) with
+ * out_indptr[b] <= t < out_indptr[b + 1] is token first[b] + t -
+ * out_indptr[b] of request b, its value rounded once (nearest even).  Rows of
+ * no request are left as they were; a row whose token has no page becomes
+ * zeros and PKC_ERR_BLOCK_TABLE is recorded.  first [batch] and out_indptr
+ * [batch + 1] are device int32; the cache's lengths are not consulted.
+ */
+int pkc_gather_kv_mx4(const void* k_codes, const void* k_scales,
+                      const void* v_codes, const void* v_scales,
+                      const int32_t* block_table, int block_table_stride,
+                      const int32_t* first, const int32_t* out_indptr,
+                      int total, int batch, int num_kv_heads, int head_dim,
+                      int page_size, int64_t num_pages, void* k_out,
+                      void* v_out, int dtype, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/*
+ * pkc_paged_decode_state over an mx4 cache: the same states, plan, workspace
+ * and status codes, with q and o of dtype (F16 or BF16), any page size and
+ * any number of KV heads.  Split requests are always joined by the
+ * standalone contraction kernel.  Accuracy beyond the format's: the scores
+ * are those of the cached values with float32 sums; probabilities enter the
+ * V product with 22 bits, and a value below 2^-26 of the largest cached
+ * |V| of its block of dims may count as zero.  A page id < 0 or >= num_pages
+ * is recorded as PKC_ERR_BLOCK_TABLE and its tokens take no part.
+ */
+int pkc_paged_decode_state_mx4(const void* q, const void* k_codes,
+                               const void* k_scales, const void* v_codes,
+                               const void* v_scales,
+                               const int32_t* block_table,
+                               int block_table_stride,
+                               const int32_t* cache_seqlens, int batch,
+                               int num_qo_heads, int num_kv_heads,
+                               int head_dim, int page_size, int64_t num_pages,
+                               float sm_scale, const int32_t* plan_host,
+                               void* workspace, size_t workspace_bytes,
+                               void* o, float* lse, int dtype, void* stream);
+
+/* ------------------------------------------------------------------------
  * Stage timing
  * ---------------------------------------------------------------------- */
 

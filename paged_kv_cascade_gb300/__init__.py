@@ -73,6 +73,12 @@ SIGNATURES = {
                                 _I64, _F, _P, _P, _SZ, _P, _P, _I, _P]),
     "pkc_cascade_decode_state": (_I, [_P, _P, _P, _P, _P, _I, _P, _P, _P, _I, _P, _I, _I, _I, _I,
                                       _I, _I64, _F, _P, _P, _SZ, _P, _P, _I, _P]),
+    "pkc_append_kv_mx4": (_I, [_P, _P, _P, _I, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I64, _I,
+                               _P, _SZ, _P]),
+    "pkc_gather_kv_mx4": (_I, [_P, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I64, _P, _P, _I,
+                               _P, _SZ, _P]),
+    "pkc_paged_decode_state_mx4": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I64, _F,
+                                        _P, _P, _SZ, _P, _P, _I, _P]),
 }
 
 _lib = None
@@ -355,6 +361,101 @@ def append_kv(k_new, v_new, k_cache, v_cache, block_table, cache_seqlens, worksp
         _ptr(k_new), _ptr(v_new), _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
         block_table.shape[1], _ptr(cache_seqlens), _ptr(append_mask), B, Hkv, D, ps, P, code,
         _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# Microscaled 4-bit (mx4) paged cache
+# ---------------------------------------------------------------------------
+
+def _expect_current(t):
+    """The library launches on the current device: refuse tensors of another."""
+    import torch
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _check_mx4(k_codes, k_scales, v_codes, v_scales, block_table, workspace):
+    """The four pools of an mx4 cache, its table and the workspace."""
+    import torch
+    u8 = (torch.uint8,)
+    _expect("k_codes", k_codes, u8, (None, None, None, 64))
+    _expect_current(k_codes)
+    P, ps, Hkv, _ = k_codes.shape
+    dev = k_codes.device
+    _expect("v_codes", v_codes, u8, (P, ps, Hkv, 64), dev)
+    _expect("k_scales", k_scales, u8, (P, ps, Hkv, 4), dev)
+    _expect("v_scales", v_scales, u8, (P, ps, Hkv, 4), dev)
+    _expect("block_table", block_table, (torch.int32,), (None, None), dev)
+    _expect("workspace", workspace, u8, (None,), dev)
+    return P, ps, Hkv, block_table.shape[0], dev
+
+
+def append_kv_mx4(k_new, v_new, new_indptr, k_codes, k_scales, v_codes, v_scales, block_table,
+                  cache_seqlens, workspace, stream=None):
+    """Quantise new tokens (k_new / v_new [T, Hkv, 128], rows new_indptr[b] ..
+    new_indptr[b+1]-1 for request b, device int32) to the end of every
+    request's mx4 cache and grow cache_seqlens, in place."""
+    import torch
+    P, ps, Hkv, B, dev = _check_mx4(k_codes, k_scales, v_codes, v_scales, block_table, workspace)
+    _expect("k_new", k_new, (torch.float16, torch.bfloat16), (None, Hkv, 128), dev)
+    _expect("v_new", v_new, (k_new.dtype,), tuple(k_new.shape), dev)
+    _expect("new_indptr", new_indptr, (torch.int32,), (B + 1,), dev)
+    _expect("cache_seqlens", cache_seqlens, (torch.int32,), (B,), dev)
+    _check(lib().pkc_append_kv_mx4(
+        _ptr(k_new), _ptr(v_new), _ptr(new_indptr), k_new.shape[0], _ptr(k_codes), _ptr(k_scales),
+        _ptr(v_codes), _ptr(v_scales), _ptr(block_table), block_table.shape[1], _ptr(cache_seqlens),
+        B, Hkv, 128, ps, P, _dtype_code(k_new), _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+def gather_kv_mx4(k_codes, k_scales, v_codes, v_scales, block_table, first, out_indptr, total,
+                  workspace, dtype=None, k=None, v=None, stream=None):
+    """Tokens of an mx4 cache as 16-bit rows [total, Hkv, 128] of dtype
+    (default torch.float16): row t of out_indptr[b] .. out_indptr[b+1]-1 is
+    token first[b] + t - out_indptr[b] of request b.  Rows of no request stay
+    as they were in given k and v (and are undefined in new ones)."""
+    import torch
+    P, ps, Hkv, B, dev = _check_mx4(k_codes, k_scales, v_codes, v_scales, block_table, workspace)
+    _expect("first", first, (torch.int32,), (B,), dev)
+    _expect("out_indptr", out_indptr, (torch.int32,), (B + 1,), dev)
+    if dtype is None:
+        dtype = torch.float16 if k is None else k.dtype
+    if dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"gather_kv_mx4: dtype must be torch.float16 or torch.bfloat16 (got {dtype})")
+    total = int(total)
+    if total < 0:
+        raise ValueError(f"gather_kv_mx4: total must be >= 0 (got {total})")
+    for name, t in (("k", k), ("v", v)):
+        if t is not None:
+            _expect(name, t, (dtype,), (total, Hkv, 128), dev)
+    k = torch.empty((total, Hkv, 128), dtype=dtype, device=dev) if k is None else k
+    v = torch.empty((total, Hkv, 128), dtype=dtype, device=dev) if v is None else v
+    _check(lib().pkc_gather_kv_mx4(
+        _ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _ptr(block_table),
+        block_table.shape[1], _ptr(first), _ptr(out_indptr), total, B, Hkv, 128, ps, P, _ptr(k),
+        _ptr(v), _dtype_code(k), _ptr(workspace), workspace.numel(), _stream(stream)))
+    return k, v
+
+
+def paged_decode_state_mx4(q, k_codes, k_scales, v_codes, v_scales, block_table, cache_seqlens,
+                           sm_scale, workspace, plan_buf=None, o=None, lse=None, stream=None):
+    """States of fp16 / bf16 q [B, Hq, 128] over each request's mx4 cache."""
+    import torch
+    P, ps, Hkv, B, dev = _check_mx4(k_codes, k_scales, v_codes, v_scales, block_table, workspace)
+    _expect("q", q, (torch.float16, torch.bfloat16), (B, None, 128), dev)
+    _expect("cache_seqlens", cache_seqlens, (torch.int32,), (B,), dev)
+    Hq = q.shape[1]
+    if o is not None:
+        _expect("o", o, (q.dtype,), (B, Hq, 128), dev)
+    if lse is not None:
+        _expect("lse", lse, (torch.float32,), (B, Hq), dev)
+    o = torch.empty_like(q) if o is None else o
+    lse = torch.empty((B, Hq), dtype=torch.float32, device=dev) if lse is None else lse
+    _check(lib().pkc_paged_decode_state_mx4(
+        _ptr(q), _ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _ptr(block_table),
+        block_table.shape[1], _ptr(cache_seqlens), B, Hq, Hkv, 128, ps, P, float(sm_scale),
+        _hptr(plan_buf), _ptr(workspace), workspace.numel(), _ptr(o), _ptr(lse), _dtype_code(q),
+        _stream(stream)))
+    return o, lse
 
 
 DECODE_KERNELS = {"auto": 0, "simt": 1, "mma": 2}

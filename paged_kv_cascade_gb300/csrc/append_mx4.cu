@@ -1,0 +1,236 @@
+// Quantising append to, and read-back from, an mx4 paged cache (the format:
+// mx4.cuh).
+//
+// Both kernels move one 256-byte row (a token's 128 values of one head, K or
+// V) per 16 lanes: lane 4 b + v holds elements 32 b + 8 v .. + 7, so a
+// block's shared exponent is a maximum over 4 lanes and the row's 64 code
+// bytes are re-ordered with two shuffles.  They are bound by HBM (a row is
+// 256 bytes in and 68 out, or the reverse) once there are a few thousand
+// rows, and by launch latency below that.
+//
+// Quantising (the microscaling rule): a block of largest magnitude amax gets
+// the exponent e = max(floor(log2 amax) - 2, -126), so that amax / 2^e lies
+// in [4, 8), and its elements become the nearest e2m1 values of x / 2^e
+// (ties to the even code, 6 above 6).  The division by a power of two is
+// exact in float32.  A block holding an infinity or a NaN gets scale 255
+// (NaN) and zero codes.
+#include <cuda_runtime.h>
+
+#include "mx4.cuh"
+
+namespace pkc {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kGroups = kThreads / 16;  // rows a block works on at once
+constexpr int kUnroll = 4;              // rows a 16-lane group has in flight
+
+// Request of row t of the ragged token list: indptr[b] <= t < indptr[b + 1],
+// or -1 (rows that no request owns).
+__device__ __forceinline__ int request_of(const int32_t* indptr, int batch, int t) {
+  int lo = 0, hi = batch;  // the last b in [0, batch] with indptr[b] <= t
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (indptr[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo < batch && indptr[lo] <= t && t < indptr[lo + 1] ? lo : -1;
+}
+
+struct Place {
+  int64_t slot;  // page * page_size + slot, -1: not to be touched
+  bool bad;      // a page that is not there
+};
+
+// Cache slot of row t: position base[b] + (t - indptr[b]) of its request.
+__device__ __forceinline__ Place place_of(const Mx4RowsParams& p, int t) {
+  const int b = request_of(p.indptr, p.batch, t);
+  if (b < 0) return {-1, false};
+  const int base = p.base[b];
+  const int64_t pos = (int64_t)base + ((int64_t)t - p.indptr[b]);
+  int64_t page_idx;
+  int slot;
+  PageDiv{p.page_size, p.page_shift}.split(pos, page_idx, slot);
+  int32_t page = -1;
+  if (base >= 0 && pos < INT32_MAX && page_idx < p.bt_stride) page = p.block_table[(int64_t)b * p.bt_stride + page_idx];
+  if (page < 0 || page >= p.num_pages) return {-1, true};
+  return {(int64_t)page * p.page_size + slot, false};
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) append_mx4_kernel(const Mx4RowsParams p) {
+  const int lane16 = threadIdx.x & 15, group = threadIdx.x >> 4;
+  const int64_t rows = (int64_t)p.total * 2 * p.hkv;  // (token, K | V, head)
+  bool any_bad = false;
+  for (int64_t r0 = (int64_t)blockIdx.x * kGroups; r0 < rows; r0 += (int64_t)gridDim.x * kGroups * kUnroll) {
+    uint4 x[kUnroll];
+    int64_t dst[kUnroll];
+    bool is_v[kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int64_t r = r0 + (int64_t)i * gridDim.x * kGroups + group;
+      dst[i] = -1;
+      is_v[i] = false;
+      x[i] = make_uint4(0, 0, 0, 0);
+      if (r < rows) {
+        const int64_t th = r / p.hkv;
+        const int h = (int)(r - th * p.hkv);
+        const int t = (int)(th >> 1);
+        is_v[i] = (th & 1) != 0;
+        const T* src = static_cast<const T*>(is_v[i] ? p.v_rows : p.k_rows);
+        x[i] = ldg_stream(src + ((int64_t)t * p.hkv + h) * PKC_HEAD_DIM + 8 * lane16);
+        const Place at = place_of(p, t);
+        any_bad = any_bad || at.bad;
+        if (at.slot >= 0) dst[i] = at.slot * p.hkv + h;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const float2 f[4] = {Elem<T>::to_f2(x[i].x), Elem<T>::to_f2(x[i].y), Elem<T>::to_f2(x[i].z),
+                           Elem<T>::to_f2(x[i].w)};
+      uint32_t top = 0;  // magnitude bits: ordered as integers, NaN above infinity
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        top = max(top, max(__float_as_uint(f[k].x) & 0x7fffffffu, __float_as_uint(f[k].y) & 0x7fffffffu));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const uint32_t e = top >> 23;
+      const bool nan = e == 255u;
+      const uint32_t s = nan ? 255u : (uint32_t)max((int)e - 2, 1);
+      const float mul = __uint_as_float(nan ? 0u : (254u - s) << 23);  // 2^(127 - s)
+      uint32_t w = to_e2m1x4(f[0].x * mul, f[0].y * mul, f[1].x * mul, f[1].y * mul) |
+                   (to_e2m1x4(f[2].x * mul, f[2].y * mul, f[3].x * mul, f[3].y * mul) << 16);
+      if (nan) w = 0;
+      // lane 4 b + v holds words (u = 2 v, b) and (u = 2 v + 1, b); lane
+      // 4 j + v stores 32-bit word j of 16-byte piece v: words
+      // (u = 2 v + j / 2, b = 2 (j % 2)) and (the same u, b + 1)
+      const int j = lane16 >> 2, v = lane16 & 3;
+      const uint32_t wa = __shfl_sync(0xffffffffu, w, 8 * (j & 1) + v, 16);
+      const uint32_t wb = __shfl_sync(0xffffffffu, w, 8 * (j & 1) + 4 + v, 16);
+      const uint32_t out = prmt(wa, wb, (j >> 1) ? 0x7632u : 0x5410u);
+      uint32_t sc = s << (8 * (lane16 >> 2));
+      sc |= __shfl_xor_sync(0xffffffffu, sc, 4);
+      sc |= __shfl_xor_sync(0xffffffffu, sc, 8);
+      if (dst[i] >= 0) {
+        uint8_t* codes = static_cast<uint8_t*>(is_v[i] ? p.v_codes : p.k_codes) + dst[i] * kMx4RowBytes;
+        *reinterpret_cast<uint32_t*>(codes + 16 * v + 4 * j) = out;
+        if (lane16 == 0)
+          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(is_v[i] ? p.v_scales : p.k_scales) + dst[i] * 4) = sc;
+      }
+    }
+  }
+  // The lengths grow once every block has read them: by the block that
+  // finishes last, which also resets the counter for the next launch.
+  int32_t* ctr = p.status + PKC_APPEND_COUNTER;
+  __shared__ int last, bad;
+  if (any_bad) {
+    report(p.status, PKC_ERR_BLOCK_TABLE);
+    atomicExch(ctr + 1, 1);
+  }
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x == 0) last = atomicAdd(ctr, 1) == (int)gridDim.x - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  if (threadIdx.x == 0) {
+    bad = atomicExch(ctr + 1, 0);
+    atomicExch(ctr, 0);
+  }
+  __syncthreads();
+  for (int b = threadIdx.x; b < p.batch; b += kThreads) {
+    const int t0 = p.indptr[b], t1 = p.indptr[b + 1], len = p.base[b];
+    if (t0 == t1) continue;
+    bool ok = t0 >= 0 && t0 < t1 && t1 <= p.total;
+    if (!ok) report(p.status, PKC_ERR_PLAN);
+    if (ok && bad) {  // some token had no page: which requests have all of theirs?
+      for (int64_t pos = len; ok && pos < (int64_t)len + (t1 - t0);) {
+        const int64_t page_idx = pos / p.page_size;
+        int32_t page = -1;
+        if (len >= 0 && page_idx < p.bt_stride) page = p.block_table[(int64_t)b * p.bt_stride + page_idx];
+        ok = page >= 0 && page < p.num_pages && (int64_t)len + (t1 - t0) <= INT32_MAX;
+        pos = (page_idx + 1) * p.page_size;
+      }
+    }
+    if (ok) p.lengths[b] = len + (t1 - t0);
+  }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) gather_mx4_kernel(const Mx4RowsParams p) {
+  const int lane16 = threadIdx.x & 15, group = threadIdx.x >> 4;
+  const int64_t rows = (int64_t)p.total * 2 * p.hkv;
+  for (int64_t r0 = (int64_t)blockIdx.x * kGroups; r0 < rows; r0 += (int64_t)gridDim.x * kGroups * kUnroll) {
+    uint32_t w[kUnroll], sc[kUnroll];
+    int64_t dst[kUnroll];
+    bool is_v[kUnroll];
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      const int64_t r = r0 + (int64_t)i * gridDim.x * kGroups + group;
+      dst[i] = -1;
+      w[i] = sc[i] = 0;
+      is_v[i] = false;
+      if (r < rows) {
+        const int64_t th = r / p.hkv;
+        const int h = (int)(r - th * p.hkv);
+        const int t = (int)(th >> 1);
+        is_v[i] = (th & 1) != 0;
+        const Place at = place_of(p, t);
+        if (at.bad) report(p.status, PKC_ERR_BLOCK_TABLE);
+        if (at.slot >= 0 || at.bad) dst[i] = (int64_t)t * p.hkv + h;  // a row without a page reads as zeros
+        if (at.slot >= 0) {
+          const int64_t row = at.slot * p.hkv + h;
+          w[i] = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(is_v[i] ? p.v_codes : p.k_codes) +
+                                                   row * kMx4RowBytes)[4 * (lane16 & 3) + (lane16 >> 2)];
+          sc[i] = reinterpret_cast<const uint32_t*>(is_v[i] ? p.v_scales : p.k_scales)[row];
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kUnroll; ++i) {
+      // the inverse of the append's re-ordering: lane 4 b + v takes the
+      // words (u = 2 v, b) and (u = 2 v + 1, b)
+      const int b = lane16 >> 2, v = lane16 & 3;
+      const uint32_t wa = __shfl_sync(0xffffffffu, w[i], 4 * (b >> 1) + v, 16);
+      const uint32_t wb = __shfl_sync(0xffffffffu, w[i], 4 * (2 + (b >> 1)) + v, 16);
+      uint32_t h2[4];
+      e2m1x8(prmt(wa, wb, (b & 1) ? 0x7632u : 0x5410u), h2);
+      const float s = mx4_scale((sc[i] >> (8 * b)) & 255u);
+      uint32_t out[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = Elem<__half>::to_f2(h2[k]);
+        out[k] = Elem<T>::from_f2(f.x * s, f.y * s);
+      }
+      if (dst[i] >= 0) {
+        T* row = static_cast<T*>(is_v[i] ? p.v_out : p.k_out) + dst[i] * PKC_HEAD_DIM;
+        *reinterpret_cast<uint4*>(row + 8 * lane16) = make_uint4(out[0], out[1], out[2], out[3]);
+      }
+    }
+  }
+}
+
+int blocks_for(const Mx4RowsParams& p) {
+  const int64_t rows = (int64_t)p.total * 2 * p.hkv;
+  const int64_t want = (rows + kGroups - 1) / kGroups;  // one row per 16 lanes while blocks are few
+  const int64_t most = (int64_t)num_sms() * (2048 / kThreads);
+  return (int)(want < most ? want : most);
+}
+
+}  // namespace
+
+int launch_append_mx4(const Mx4RowsParams& p, int dtype, void* stream) {
+  if (p.total <= 0 || p.batch <= 0) return 0;
+  if (dtype == PKC_BF16) append_mx4_kernel<__nv_bfloat16><<<blocks_for(p), kThreads, 0, (cudaStream_t)stream>>>(p);
+  else append_mx4_kernel<__half><<<blocks_for(p), kThreads, 0, (cudaStream_t)stream>>>(p);
+  return (int)cudaGetLastError();
+}
+
+int launch_gather_mx4(const Mx4RowsParams& p, int dtype, void* stream) {
+  if (p.total <= 0 || p.batch <= 0) return 0;
+  if (dtype == PKC_BF16) gather_mx4_kernel<__nv_bfloat16><<<blocks_for(p), kThreads, 0, (cudaStream_t)stream>>>(p);
+  else gather_mx4_kernel<__half><<<blocks_for(p), kThreads, 0, (cudaStream_t)stream>>>(p);
+  return (int)cudaGetLastError();
+}
+
+}  // namespace pkc

@@ -1,0 +1,133 @@
+// The microscaled 4-bit cache format ("mx4") and the helpers of its kernels.
+//
+// One head's 128 elements of one token are 4 blocks of 32 with a shared
+// power-of-two scale each (the microscaling formats' shared exponent, E8M0):
+//   codes  64 bytes: element 32 b + 4 u + i of the row is nibble i of the
+//          16-bit little-endian word 4 u + b  (b block 0..3, u 0..7, i 0..3)
+//   scales 4 bytes: s_b stands for 2^(s_b - 127); 255: NaN
+// A nibble is e2m1: sign, two exponent bits (bias 1), one mantissa bit, the
+// values 0 .5 1 1.5 2 3 4 6.  The word order puts the 8 codes that one lane
+// feeds to a tensor-core tile into one aligned load, for K (lane = 8
+// consecutive elements of every block: 16 bytes at 16 (lane % 4)) and for V
+// (4 elements of every block: 8 bytes at 8 (lane / 4)) alike.
+#pragma once
+#include "pkc_device.cuh"
+#include "pkc_internal.h"
+
+namespace pkc {
+
+constexpr int kMx4RowBytes = 64;
+
+// The 8 codes of a word -> 4 fp16 pairs (byte k -> r[k], low nibble first).
+// Every e2m1 value is an fp16 value.
+__device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&r)[4]) {
+  asm("{\n.reg .b8 a, b, c, d;\nmov.b32 {a, b, c, d}, %4;\n"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\ncvt.rn.f16x2.e2m1x2 %1, b;\n"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\ncvt.rn.f16x2.e2m1x2 %3, d;\n}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+}
+
+// Four values -> one 16-bit word of e2m1 codes (x0 in the low nibble), to
+// nearest, ties to even, saturating at 6.
+__device__ __forceinline__ uint32_t to_e2m1x4(float x0, float x1, float x2, float x3) {
+  uint32_t d;
+  asm("{\n.reg .b8 a, b;\ncvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\nmov.b32 %0, {a, b, a, b};\n}"
+      : "=r"(d)
+      : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
+  return d & 0xffffu;
+}
+
+// The float a scale byte stands for: 2^(s - 127), exactly (2^-127 is a
+// denormal), or NaN for 255.
+__device__ __forceinline__ float mx4_scale(uint32_t s) {
+  return __uint_as_float(s == 255u ? 0x7fffffffu : s == 0u ? 0x00400000u : s << 23);
+}
+
+// Quotient and remainder by the page size (shift >= 0: a power of two).
+struct PageDiv {
+  int size, shift;
+  template <typename I> __device__ __forceinline__ void split(I t, I& page, int& slot) const {
+    if (shift >= 0) {
+      page = t >> shift;
+      slot = (int)(t & (size - 1));
+    } else {
+      page = t / size;
+      slot = (int)(t - page * size);
+    }
+  }
+};
+
+// Asynchronous copies to shared memory, `ok` false: the bytes become zero
+// and nothing is read.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool ok) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void sts32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+
+// Query fragments (B operand of m16n8k16, n = query head lane / 4) for
+// products with 4-bit or 8-bit keys, whose fragments are fp16: qf[b][k] are
+// elements 32 b + 8 (lane % 4) + 2 k, + 1 of head lane / 4 (zero for heads
+// >= G).  fp16 queries are used as they are.  A bf16 row is scaled by the
+// power of two that brings its largest magnitude into [2^14, 2^15): then
+// every element down to 2^-22 of the largest is exact in fp16, and the
+// others are off by at most 2^-39 of it, far below the float32 sums'
+// rounding.  Returns the factor that undoes the scaling.
+template <typename T, int G>
+__device__ __forceinline__ float load_q_f16(const T* qrow0, int lane, uint32_t (&qf)[4][4]) {
+  const int g = lane >> 2, tg = lane & 3;
+  const T* row = qrow0 + (g < G ? g : 0) * PKC_HEAD_DIM;
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const uint4 u = *reinterpret_cast<const uint4*>(row + 32 * b + 8 * tg);
+    qf[b][0] = g < G ? u.x : 0u;
+    qf[b][1] = g < G ? u.y : 0u;
+    qf[b][2] = g < G ? u.z : 0u;
+    qf[b][3] = g < G ? u.w : 0u;
+  }
+  if constexpr (std::is_same_v<T, __half>) {
+    return 1.f;
+  } else {
+    uint32_t top = 0;  // largest magnitude's bf16 bits, lane's elements
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) top = max(top, max(qf[b][k] & 0x7fffu, (qf[b][k] >> 16) & 0x7fffu));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const int e = (int)(top >> 7);  // biased exponent; 255: not finite, 0: zero or denormal
+    const int shift = e == 255 || top == 0u ? 0 : min(14 - (e - 127), 126);
+    const float mul = __int_as_float((127 + shift) << 23);
+#pragma unroll
+    for (int b = 0; b < 4; ++b)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 f = Elem<__nv_bfloat16>::to_f2(qf[b][k]);
+        qf[b][k] = Elem<__half>::from_f2(f.x * mul, f.y * mul);
+      }
+    return __int_as_float((127 - shift) << 23);
+  }
+}
+
+}  // namespace pkc

@@ -11,8 +11,10 @@
 #define PKC_MAX_PREFIX_SPLITS 64
 // The status block at the start of every workspace: word 0 is the status
 // word (pkc_device_status), words 16-17 the dynamic decode queue's counters,
-// word 32 the result of pkc_selftest_wait_timeout.
+// words 18-19 the mx4 append's count of finished blocks and its flag for a
+// missing page, word 32 the result of pkc_selftest_wait_timeout.
 #define PKC_STATUS_BYTES 256
+#define PKC_APPEND_COUNTER 18
 
 namespace pkc {
 
@@ -219,7 +221,42 @@ struct AppendParams {
   int32_t* status;
 };
 
+// Ragged rows of an mx4 paged cache, to be quantised into it (append) or
+// read back from it (gather): request b's rows are indptr[b] ..
+// indptr[b + 1] - 1, row t at position base[b] + (t - indptr[b]).
+struct Mx4RowsParams {
+  const void* k_rows;      // append: [total, Hkv, 128] 16-bit
+  const void* v_rows;
+  void* k_out;             // gather: the same, written
+  void* v_out;
+  void* k_codes;           // [num_pages, page_size, Hkv, 64] bytes
+  void* k_scales;          // [num_pages, page_size, Hkv, 4] bytes
+  void* v_codes;
+  void* v_scales;
+  const int32_t* block_table;
+  const int32_t* indptr;   // [batch + 1]
+  const int32_t* base;     // [batch] first position of each request's rows
+  int32_t* lengths;        // append: == base, grown by the rows written
+  int64_t bt_stride, num_pages;
+  int total, batch, hkv, page_size, page_shift;  // page_shift >= 0: page_size = 1 << page_shift
+  int32_t* status;
+};
+
+// The decode over an mx4 cache: d.k_cache / d.v_cache are the codes.
+struct Mx4DecodeParams {
+  DecodeParams d;
+  const void* k_scales;    // [num_pages, page_size, Hkv, 4] bytes
+  const void* v_scales;
+  int page_shift;          // >= 0: page_size = 1 << page_shift
+  int hg;                  // KV heads per block (4, 2 or 1, dividing Hkv)
+  int num_ctas;            // CTAs of the plan (static schedule)
+};
+
 // Launchers (defined in the .cu files); return a cudaError_t value.
+int launch_append_mx4(const Mx4RowsParams& p, int dtype, void* stream);
+int launch_gather_mx4(const Mx4RowsParams& p, int dtype, void* stream);
+// n_work: chunks of the plan (0 without one)
+int launch_paged_decode_mx4(const Mx4DecodeParams& p, int n_work, int dtype, void* stream);
 int launch_merge_state(const void* va, const float* sa, const void* vb,
                        const float* sb, void* vo, float* so, int64_t rows,
                        int head_dim, int dtype, void* stream);

@@ -1,0 +1,100 @@
+"""Refusals of the compressed, bounded cache's entry points, without a GPU:
+bad arguments are rejected before any device work."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import mx4_reference as ref
+import paged_kv_cascade_gb300 as pkc
+from paged_kv_cascade_gb300 import build as pkc_build
+
+F, WS = ctypes.c_void_p(0x1000), ctypes.c_void_p(0x100000)
+OFF = ctypes.c_void_p(0x1008)  # 8-byte aligned only
+OFF2 = ctypes.c_void_p(0x1002)
+
+
+@pytest.fixture(scope="module")
+def L():
+    pkc_build.build()
+    return pkc.lib()
+
+
+def variants(good, changes):
+    """(position, value, expected code) applied one at a time to the good arguments."""
+    for pos, val, code in changes:
+        yield good[:pos] + [val] + good[pos + 1:], code
+
+
+def test_append_mx4_refuses(L):
+    # k_new v_new indptr total | kc ks vc vs | table stride lens | batch hkv d ps pages dtype ws bytes stream
+    good = [F, F, F, 4, F, F, F, F, F, 4, F, 2, 8, 128, 16, 10, 1, WS, 1 << 20, None]
+    for args, code in variants(good, [
+            (0, None, 1), (1, None, 1), (2, None, 1), (4, None, 1), (5, None, 1), (8, None, 1), (10, None, 1),
+            (0, OFF, 1), (4, OFF, 1), (6, OFF, 1), (5, OFF2, 1), (3, -1, 1), (9, 0, 1), (11, -1, 1), (12, 0, 1),
+            (13, 64, 2), (14, 0, 1), (15, -1, 1), (16, 0, 1), (16, 3, 1), (17, None, 3), (17, F, 3), (18, 16, 3)]):
+        if code == 3 and args[17] is F:
+            args[17] = ctypes.c_void_p(0x100010)
+        assert L.pkc_append_kv_mx4(*args) == code, (args, L.pkc_last_error())
+    assert L.pkc_append_kv_mx4(*good[:3], 0, *good[4:]) == 0   # no rows
+    assert L.pkc_append_kv_mx4(*good[:11], 0, *good[12:]) == 0  # no requests
+
+
+def test_gather_mx4_refuses(L):
+    # kc ks vc vs | table stride first indptr | total batch hkv d ps pages | k v dtype ws bytes stream
+    good = [F, F, F, F, F, 4, F, F, 4, 2, 8, 128, 16, 10, F, F, 1, WS, 1 << 20, None]
+    for args, code in variants(good, [
+            (0, None, 1), (3, None, 1), (4, None, 1), (6, None, 1), (7, None, 1), (14, None, 1), (15, None, 1),
+            (14, OFF, 1), (2, OFF, 1), (3, OFF2, 1), (5, 0, 1), (8, -2, 1), (11, 256, 2), (12, -4, 1), (16, 3, 1),
+            (18, 255, 3)]):
+        assert L.pkc_gather_kv_mx4(*args) == code, (args, L.pkc_last_error())
+    assert L.pkc_gather_kv_mx4(*good[:8], 0, *good[9:]) == 0
+
+
+def test_decode_mx4_refuses(L):
+    # q kc ks vc vs | table stride lens | batch hq hkv d ps pages scale plan ws bytes o lse dtype stream
+    good = [F, F, F, F, F, F, 4, F, 2, 16, 8, 128, 16, 10, 1.0, None, WS, 1 << 20, F, F, 1, None]
+    for args, code in variants(good, [
+            (0, None, 1), (1, None, 1), (4, None, 1), (5, None, 1), (7, None, 1), (18, None, 1), (19, None, 1),
+            (0, OFF, 1), (1, OFF, 1), (2, OFF2, 1), (18, OFF, 1), (6, 0, 1), (9, 12, 1), (9, 24, 2), (11, 64, 2),
+            (12, 0, 1), (13, -1, 1), (20, 0, 1), (17, 300, 3)]):
+        assert L.pkc_paged_decode_state_mx4(*args) == code, (args, L.pkc_last_error())
+    plan = pkc.plan([5, 6, 7], 4)  # of another batch
+    args = good[:15] + [ctypes.c_void_p(plan.ctypes.data)] + good[16:]
+    assert L.pkc_paged_decode_state_mx4(*args) == 7
+    assert L.pkc_paged_decode_state_mx4(*good[:8], 0, *good[9:]) == 0
+
+
+def test_binding_refuses_host_tensors():
+    u8 = torch.uint8
+    pools = [torch.zeros(4, 16, 2, n, dtype=u8) for n in (64, 4, 64, 4)]
+    bt, lens = torch.zeros(2, 4, dtype=torch.int32), torch.zeros(2, dtype=torch.int32)
+    ip, ws = torch.zeros(3, dtype=torch.int32), torch.zeros(1024, dtype=u8)
+    x, q = torch.zeros(2, 2, 128).half(), torch.zeros(2, 4, 128).half()
+    with pytest.raises(ValueError, match="CUDA"):
+        pkc.append_kv_mx4(x, x, ip, *pools, bt, lens, ws)
+    with pytest.raises(ValueError, match="CUDA"):
+        pkc.gather_kv_mx4(*pools, bt, lens, ip, 2, ws)
+    with pytest.raises(ValueError, match="CUDA"):
+        pkc.paged_decode_state_mx4(q, *pools, bt, lens, 0.1, ws)
+    with pytest.raises(ValueError, match="shape"):
+        pkc.paged_decode_state_mx4(q, pools[1], *pools[1:], bt, lens, 0.1, ws)
+    with pytest.raises(TypeError, match="dtype"):
+        pkc.paged_decode_state_mx4(q, pools[0].to(torch.int32), *pools[1:], bt, lens, 0.1, ws)
+
+
+def test_mx4_reference_is_the_nearest_code():
+    """The reference's own pins: hand-computed blocks, ties, saturation, zeros."""
+    x = np.zeros((1, 128))
+    x[0, :8] = [6.0, 5.0, 3.5, 2.5, 1.75, 1.25, 0.75, 0.25]
+    x[0, 32:36] = [7.9, -7.1, 0.24, -0.26]
+    x[0, 64] = 2.0 ** -140
+    x[0, 96] = np.inf
+    c, s = ref.quantise(x)
+    v = ref.values(c, s)
+    assert v[0, :8].tolist() == [6.0, 4.0, 4.0, 2.0, 2.0, 1.0, 1.0, 0.0]
+    assert v[0, 32:36].tolist() == [6.0, -6.0, 0.0, -0.5]
+    assert v[0, 64] == 0.0 and np.all(np.isnan(v[0, 96:]))
+    assert s[0].tolist() == [127, 127, 1, 255]
+    assert np.all(c.reshape(1, 8, 4, 2)[:, :, 3] == 0)  # a NaN block's codes

@@ -57,8 +57,10 @@ typedef enum {
 
 /* Element types.  PKC_E4M3 (8-bit float: 1 sign, 4 exponent bits with
  * bias 7, 3 mantissa bits; no infinities, S.1111.111 is NaN; largest
- * finite 448) is accepted only for a KV cache (pkc_paged_decode_state_fp8). */
-typedef enum { PKC_F32 = 0, PKC_F16 = 1, PKC_BF16 = 2, PKC_E4M3 = 3 } pkc_dtype;
+ * finite 448) is accepted only for a KV cache (pkc_paged_decode_state_fp8);
+ * PKC_MX4 names the microscaled 4-bit cache (pkc_append_kv_mx4) where a call
+ * takes caches of several kinds. */
+typedef enum { PKC_F32 = 0, PKC_F16 = 1, PKC_BF16 = 2, PKC_E4M3 = 3, PKC_MX4 = 4 } pkc_dtype;
 
 /* Library version, major * 10000 + minor * 100 + patch. */
 int pkc_version(void);
@@ -581,6 +583,97 @@ int pkc_paged_decode_state_mx4(const void* q, const void* k_codes,
                                float sm_scale, const int32_t* plan_host,
                                void* workspace, size_t workspace_bytes,
                                void* o, float* lse, int dtype, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Eviction by accumulated attention weight
+ * ---------------------------------------------------------------------- */
+
+/*
+ * Bounding a cache: every KV head of a request keeps its own `budget` slots
+ * -- the first `sinks`, the last `recent`, and those between that earlier
+ * queries gave the most attention -- moved to the front of the request's
+ * pages, so the request has one length and one block table as before and
+ * every other call works on it unchanged.  Keys are cached with their
+ * positions applied, so a token's slot does not matter.
+ *
+ * pkc_accumulate_weights: after an attention call, add the step's attention
+ * weights to each cached token's sum.  For request b, KV head h, t <
+ * cache_seqlens[b]:
+ *   weights[b, h, t] = decay * weights[b, h, t]
+ *                    + sum over h's query heads of exp(sm_scale q.k_t - lse)
+ *   q        [batch, num_qo_heads, 128] of dtype: the step's queries
+ *   lse      [batch, num_qo_heads] float32: the step's LSE as any of the
+ *            attention calls returned it (of a cascade: over prefix and
+ *            suffix, so that the weights are those of the whole row; a head
+ *            with -inf adds nothing)
+ *   k_cache  of kv_dtype: F16 or BF16 (dtype the same), E4M3 (dtype F16; the
+ *            keys are k_scale times the codes) or MX4 (dtype F16 or BF16;
+ *            codes, with k_scales).  k_scale is 1 and k_scales NULL otherwise
+ *   decay    in [0, 1]; 0 overwrites without reading the old weights
+ *   weights  [batch, num_kv_heads, weights_stride] float32; entries at or
+ *            behind the length stay as they are.  A token appended later
+ *            starts from the value found there (0 after pkc_evict_compact;
+ *            the caller zeroes a new buffer)
+ * A token whose page is not there keeps its weight (PKC_ERR_BLOCK_TABLE); a
+ * request longer than weights_stride has its first weights_stride tokens
+ * treated (PKC_ERR_PLAN).  Results do not depend on any order of execution.
+ */
+int pkc_accumulate_weights(const void* q, const float* lse,
+                           const void* k_cache, const void* k_scales,
+                           const int32_t* block_table, int block_table_stride,
+                           const int32_t* cache_seqlens, int batch,
+                           int num_qo_heads, int num_kv_heads, int head_dim,
+                           int page_size, int64_t num_pages, float sm_scale,
+                           float k_scale, float decay, float* weights,
+                           int64_t weights_stride, int dtype, int kv_dtype,
+                           void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * Choose the slots that each (request, KV head) keeps.  keep [batch,
+ * num_kv_heads, budget] int32: for a request longer than the budget, slots 0
+ * .. sinks - 1, the budget - sinks - recent slots between those and the last
+ * `recent` with the largest weights (of equal weights the lower slot; NaN
+ * counts as larger than any number, -0 as 0), and the last `recent`, all in
+ * ascending order; for any other request 0 .. length - 1, then -1.
+ * budget >= 1, sinks >= 0, recent >= 0, sinks + recent <= budget.  A request
+ * longer than weights_stride gets -1 throughout (PKC_ERR_PLAN).
+ */
+int pkc_evict_select(const float* weights, int64_t weights_stride,
+                     const int32_t* cache_seqlens, int batch, int num_kv_heads,
+                     int budget, int sinks, int recent, int32_t* keep,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Move the kept slots of every request longer than `budget` to its first
+ * `budget` slots, in place, and set its length to the budget; other requests
+ * stay as they are.
+ *   keep     [batch, num_kv_heads, budget] int32 (of pkc_evict_select, or the
+ *            caller's own choice): strictly ascending slots >= 0 below the
+ *            length, per KV head
+ *   k_cache, v_cache [num_pages, page_size, num_kv_heads, ...] of kv_dtype
+ *            F16, BF16, E4M3 or MX4 (codes; k_scales, v_scales move along,
+ *            NULL otherwise)
+ *   weights  NULL, or the accumulated weights [batch, num_kv_heads,
+ *            weights_stride]: they move along, and those between the budget
+ *            and the old length become 0
+ * Pages behind the new length are the caller's to free.  No page may be
+ * shared between two requests (or used twice by one) that are cut.  A
+ * request with a page id < 0 or >= num_pages below its length is left as it
+ * was (PKC_ERR_BLOCK_TABLE).  A (request, head) whose keep row does not
+ * ascend within the length, or whose weights row is shorter than it, is not
+ * moved (PKC_ERR_PLAN), while the request's length still becomes the budget.
+ * One launch; the workspace's status block holds its counter, so a workspace
+ * must not be shared by two compactions in flight.
+ */
+int pkc_evict_compact(const int32_t* keep, int budget, void* k_cache,
+                      void* v_cache, void* k_scales, void* v_scales,
+                      const int32_t* block_table, int block_table_stride,
+                      int32_t* cache_seqlens, float* weights,
+                      int64_t weights_stride, int batch, int num_kv_heads,
+                      int head_dim, int page_size, int64_t num_pages,
+                      int kv_dtype, void* workspace, size_t workspace_bytes,
+                      void* stream);
 
 /* ------------------------------------------------------------------------
  * Stage timing

@@ -21,7 +21,7 @@ PKC_OK = 0
 STATUS_NAMES = {0: "PKC_OK", 1: "PKC_ERR_INVALID_ARG", 2: "PKC_ERR_UNSUPPORTED",
                 3: "PKC_ERR_WORKSPACE", 4: "PKC_ERR_BLOCK_TABLE", 5: "PKC_ERR_CUDA",
                 6: "PKC_ERR_TIMEOUT", 7: "PKC_ERR_PLAN"}
-F32, F16, BF16, E4M3 = 0, 1, 2, 3
+F32, F16, BF16, E4M3, MX4 = 0, 1, 2, 3, 4
 
 # Header indices of the plan buffer (include/pkc.h).
 PLAN_FIELDS = ["MAGIC", "TOTAL_WORDS", "NUM_CTAS", "TILE_Q", "N_REQ", "KV_CHUNK",
@@ -79,6 +79,11 @@ SIGNATURES = {
                                _P, _SZ, _P]),
     "pkc_paged_decode_state_mx4": (_I, [_P, _P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I64, _F,
                                         _P, _P, _SZ, _P, _P, _I, _P]),
+    "pkc_accumulate_weights": (_I, [_P, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I64, _F, _F, _F,
+                                    _P, _I64, _I, _I, _P, _SZ, _P]),
+    "pkc_evict_select": (_I, [_P, _I64, _P, _I, _I, _I, _I, _I, _P, _P, _SZ, _P]),
+    "pkc_evict_compact": (_I, [_P, _I, _P, _P, _P, _P, _P, _I, _P, _P, _I64, _I, _I, _I, _I, _I64, _I,
+                               _P, _SZ, _P]),
 }
 
 _lib = None
@@ -456,6 +461,111 @@ def paged_decode_state_mx4(q, k_codes, k_scales, v_codes, v_scales, block_table,
         _hptr(plan_buf), _ptr(workspace), workspace.numel(), _ptr(o), _ptr(lse), _dtype_code(q),
         _stream(stream)))
     return o, lse
+
+
+# ---------------------------------------------------------------------------
+# Eviction by accumulated attention weight
+# ---------------------------------------------------------------------------
+
+def _kv_kind(cache, scales):
+    """(kv_dtype code, row length) of a cache: 16-bit, e4m3 codes, or mx4
+    codes (given with their scales)."""
+    import torch
+    if scales is not None:
+        return MX4, 64
+    if cache.dtype == torch.uint8:
+        return E4M3, 128
+    return _dtype_code(cache), 128
+
+
+def accumulate_weights(q, lse, k_cache, block_table, cache_seqlens, sm_scale, weights, workspace,
+                       decay=1.0, k_scale=1.0, k_scales=None, stream=None):
+    """weights[b, h, t] = decay * weights[b, h, t] + the attention weights that
+    q [B, Hq, 128] with LSE lse [B, Hq] gives cached token t, summed over KV
+    head h's query heads; weights [B, Hkv, W] float32, in place.  k_cache:
+    16-bit of q's dtype, e4m3 codes (fp16 q, k_scale), or mx4 codes with
+    k_scales."""
+    import torch
+    _expect("k_cache", k_cache, (torch.float16, torch.bfloat16, torch.uint8), (None, None, None, None))
+    _expect_current(k_cache)
+    kind, row = _kv_kind(k_cache, k_scales)
+    P, ps, Hkv, _ = k_cache.shape
+    dev = k_cache.device
+    _expect("k_cache", k_cache, (torch.uint8,) if k_scales is not None else (k_cache.dtype,),
+            (P, ps, Hkv, row), dev)
+    if k_scales is not None:
+        _expect("k_scales", k_scales, (torch.uint8,), (P, ps, Hkv, 4), dev)
+    _expect("q", q, (torch.float16, torch.bfloat16), (None, None, 128), dev)
+    B, Hq, _ = q.shape
+    _expect("lse", lse, (torch.float32,), (B, Hq), dev)
+    _expect("block_table", block_table, (torch.int32,), (B, None), dev)
+    _expect("cache_seqlens", cache_seqlens, (torch.int32,), (B,), dev)
+    _expect("weights", weights, (torch.float32,), (B, Hkv, None), dev)
+    _expect("workspace", workspace, (torch.uint8,), (None,), dev)
+    _check(lib().pkc_accumulate_weights(
+        _ptr(q), _ptr(lse), _ptr(k_cache), _ptr(k_scales), _ptr(block_table), block_table.shape[1],
+        _ptr(cache_seqlens), B, Hq, Hkv, 128, ps, P, float(sm_scale), float(k_scale), float(decay),
+        _ptr(weights), weights.shape[2], _dtype_code(q), kind, _ptr(workspace), workspace.numel(),
+        _stream(stream)))
+    return weights
+
+
+def evict_select(weights, cache_seqlens, budget, sinks, recent, workspace, keep=None, stream=None):
+    """The slots that each (request, KV head) keeps, [B, Hkv, budget] int32 in
+    ascending order: the first `sinks`, the last `recent`, and the largest of
+    weights [B, Hkv, W] between them (all, then -1, of a request within the
+    budget)."""
+    import torch
+    _expect("weights", weights, (torch.float32,), (None, None, None))
+    _expect_current(weights)
+    B, Hkv, W = weights.shape
+    dev = weights.device
+    budget, sinks, recent = int(budget), int(sinks), int(recent)
+    if budget < 1 or sinks < 0 or recent < 0 or sinks + recent > budget:
+        raise ValueError("evict_select: budget must be >= 1, sinks and recent >= 0 and together at most the "
+                         f"budget (got {budget}, {sinks}, {recent})")
+    _expect("cache_seqlens", cache_seqlens, (torch.int32,), (B,), dev)
+    _expect("workspace", workspace, (torch.uint8,), (None,), dev)
+    if keep is not None:
+        _expect("keep", keep, (torch.int32,), (B, Hkv, budget), dev)
+    keep = torch.empty((B, Hkv, budget), dtype=torch.int32, device=dev) if keep is None else keep
+    _check(lib().pkc_evict_select(_ptr(weights), W, _ptr(cache_seqlens), B, Hkv, budget, sinks, recent,
+                                  _ptr(keep), _ptr(workspace), workspace.numel(), _stream(stream)))
+    return keep
+
+
+def evict_compact(keep, k_cache, v_cache, block_table, cache_seqlens, workspace, weights=None,
+                  k_scales=None, v_scales=None, stream=None):
+    """Move the slots keep [B, Hkv, budget] of every request longer than the
+    budget to its first slots and cut its length, in place: K and V (16-bit,
+    e4m3 codes, or mx4 codes with their scales) and, given, the accumulated
+    weights [B, Hkv, W]."""
+    import torch
+    _expect("k_cache", k_cache, (torch.float16, torch.bfloat16, torch.uint8), (None, None, None, None))
+    _expect_current(k_cache)
+    if (k_scales is None) != (v_scales is None):
+        raise ValueError("evict_compact: k_scales and v_scales are given together")
+    kind, row = _kv_kind(k_cache, k_scales)
+    P, ps, Hkv, _ = k_cache.shape
+    dev = k_cache.device
+    kv_dtypes = (torch.uint8,) if k_scales is not None else (k_cache.dtype,)
+    _expect("k_cache", k_cache, kv_dtypes, (P, ps, Hkv, row), dev)
+    _expect("v_cache", v_cache, kv_dtypes, (P, ps, Hkv, row), dev)
+    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+        if t is not None:
+            _expect(name, t, (torch.uint8,), (P, ps, Hkv, 4), dev)
+    _expect("keep", keep, (torch.int32,), (None, Hkv, None), dev)
+    B, _, budget = keep.shape
+    _expect("block_table", block_table, (torch.int32,), (B, None), dev)
+    _expect("cache_seqlens", cache_seqlens, (torch.int32,), (B,), dev)
+    _expect("workspace", workspace, (torch.uint8,), (None,), dev)
+    if weights is not None:
+        _expect("weights", weights, (torch.float32,), (B, Hkv, None), dev)
+    _check(lib().pkc_evict_compact(
+        _ptr(keep), budget, _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
+        _ptr(block_table), block_table.shape[1], _ptr(cache_seqlens), _ptr(weights),
+        0 if weights is None else weights.shape[2], B, Hkv, 128, ps, P, kind, _ptr(workspace),
+        workspace.numel(), _stream(stream)))
 
 
 DECODE_KERNELS = {"auto": 0, "simt": 1, "mma": 2}

@@ -1,8 +1,10 @@
 // C ABI entry points of the compressed, bounded cache: the mx4 paged cache
-// (append, read-back, decode).
+// (append, read-back, decode) and eviction (accumulated attention weights,
+// select, compact).
 #include <cuda_runtime.h>
 
 #include <climits>
+#include <cmath>
 #include <cstring>
 
 #include "api_common.h"
@@ -29,6 +31,8 @@ int check_pool(const char* call, int batch, int hkv, int head_dim, int page_size
                      "%s: batch and num_pages must be >= 0, num_kv_heads, page_size and block_table_stride >= 1", call);
   if (head_dim != PKC_HEAD_DIM)
     return set_error(PKC_ERR_UNSUPPORTED, "%s: head_dim must be %d (got %d)", call, PKC_HEAD_DIM, head_dim);
+  if ((int64_t)block_table_stride * page_size > INT32_MAX - 65536)  // token positions are 32-bit
+    return set_error(PKC_ERR_UNSUPPORTED, "%s: a block table of more than 2^31 - 65537 tokens", call);
   return PKC_OK;
 }
 
@@ -155,6 +159,106 @@ int pkc_paged_decode_state_mx4(const void* q, const void* k_codes, const void* k
     if (e) return cuda_error(e, "contraction launch");
   }
   return PKC_OK;
+}
+
+int pkc_accumulate_weights(const void* q, const float* lse, const void* k_cache, const void* k_scales,
+                           const int32_t* block_table, int block_table_stride, const int32_t* cache_seqlens,
+                           int batch, int num_qo_heads, int num_kv_heads, int head_dim, int page_size,
+                           int64_t num_pages, float sm_scale, float k_scale, float decay, float* weights,
+                           int64_t weights_stride, int dtype, int kv_dtype, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  if (int rc = check_attn_dims(batch, num_qo_heads, num_kv_heads, head_dim, dtype)) return rc;
+  if (int rc = check_pool("accumulate_weights", batch, num_kv_heads, head_dim, page_size, block_table_stride,
+                          num_pages))
+    return rc;
+  const bool pair = kv_dtype == PKC_MX4 || (kv_dtype == PKC_E4M3 && dtype == PKC_F16) ||
+                    ((kv_dtype == PKC_F16 || kv_dtype == PKC_BF16) && dtype == kv_dtype);
+  if (!pair)
+    return set_error(PKC_ERR_INVALID_ARG,
+                     "accumulate_weights: no queries of dtype %d with a cache of kv_dtype %d (16-bit caches take "
+                     "their own type, e4m3 fp16, mx4 fp16 or bf16)",
+                     dtype, kv_dtype);
+  if (!(k_scale > 0.f) || !std::isfinite(k_scale) || (kv_dtype != PKC_E4M3 && k_scale != 1.f))
+    return set_error(PKC_ERR_INVALID_ARG, "accumulate_weights: k_scale must be finite and > 0, and 1 but for an e4m3 cache");
+  if (!(decay >= 0.f && decay <= 1.f))
+    return set_error(PKC_ERR_INVALID_ARG, "accumulate_weights: decay must be in [0, 1]");
+  if (weights_stride < 1) return set_error(PKC_ERR_INVALID_ARG, "accumulate_weights: weights_stride must be >= 1");
+  if (int rc = check_ws(workspace, workspace_bytes, PKC_STATUS_BYTES)) return rc;
+  if (batch == 0) return PKC_OK;
+  if (!q || !lse || !k_cache || !block_table || !cache_seqlens || !weights || (kv_dtype == PKC_MX4 && !k_scales))
+    return set_error(PKC_ERR_INVALID_ARG, "accumulate_weights: NULL pointer");
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned4(k_scales))
+    return set_error(PKC_ERR_INVALID_ARG, "accumulate_weights: q and k_cache must be 16-byte aligned, k_scales 4-byte");
+  WeightsParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = q; p.lse = lse; p.k_cache = k_cache; p.k_scales = k_scales;
+  p.block_table = block_table; p.cache_seqlens = cache_seqlens; p.weights = weights;
+  p.bt_stride = block_table_stride; p.num_pages = num_pages; p.w_stride = weights_stride;
+  p.batch = batch; p.hkv = num_kv_heads; p.g = num_qo_heads / num_kv_heads;
+  p.page_size = page_size; p.page_shift = page_shift_of(page_size);
+  p.scale_log2 = sm_scale * k_scale * 1.4426950408889634f;
+  p.decay = decay;
+  p.status = static_cast<int32_t*>(workspace);
+  const int e = launch_weights(p, dtype, kv_dtype, stream);
+  return e ? cuda_error(e, "accumulate_weights launch") : PKC_OK;
+}
+
+int pkc_evict_select(const float* weights, int64_t weights_stride, const int32_t* cache_seqlens, int batch,
+                     int num_kv_heads, int budget, int sinks, int recent, int32_t* keep, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  if (batch < 0 || num_kv_heads <= 0 || weights_stride < 1)
+    return set_error(PKC_ERR_INVALID_ARG, "evict_select: batch must be >= 0, num_kv_heads and weights_stride >= 1");
+  if (budget < 1 || sinks < 0 || recent < 0 || (int64_t)sinks + recent > budget)
+    return set_error(PKC_ERR_INVALID_ARG,
+                     "evict_select: budget must be >= 1, sinks and recent >= 0 and together at most the budget "
+                     "(got %d, %d, %d)",
+                     budget, sinks, recent);
+  if ((int64_t)batch * num_kv_heads > INT32_MAX / 8)
+    return set_error(PKC_ERR_UNSUPPORTED, "evict_select: more than 2^28 rows");
+  if (int rc = check_ws(workspace, workspace_bytes, PKC_STATUS_BYTES)) return rc;
+  if (batch == 0) return PKC_OK;
+  if (!weights || !cache_seqlens || !keep) return set_error(PKC_ERR_INVALID_ARG, "evict_select: NULL pointer");
+  SelectParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.weights = weights; p.cache_seqlens = cache_seqlens; p.keep = keep; p.w_stride = weights_stride;
+  p.batch = batch; p.hkv = num_kv_heads; p.budget = budget; p.sinks = sinks; p.recent = recent;
+  p.status = static_cast<int32_t*>(workspace);
+  const int e = launch_evict_select(p, stream);
+  return e ? cuda_error(e, "evict_select launch") : PKC_OK;
+}
+
+int pkc_evict_compact(const int32_t* keep, int budget, void* k_cache, void* v_cache, void* k_scales, void* v_scales,
+                      const int32_t* block_table, int block_table_stride, int32_t* cache_seqlens, float* weights,
+                      int64_t weights_stride, int batch, int num_kv_heads, int head_dim, int page_size,
+                      int64_t num_pages, int kv_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  if (int rc = check_pool("evict_compact", batch, num_kv_heads, head_dim, page_size, block_table_stride, num_pages))
+    return rc;
+  if (budget < 1) return set_error(PKC_ERR_INVALID_ARG, "evict_compact: budget must be >= 1 (got %d)", budget);
+  if (kv_dtype != PKC_F16 && kv_dtype != PKC_BF16 && kv_dtype != PKC_E4M3 && kv_dtype != PKC_MX4)
+    return set_error(PKC_ERR_INVALID_ARG, "evict_compact: kv_dtype must be PKC_F16, PKC_BF16, PKC_E4M3 or PKC_MX4 (got %d)",
+                     kv_dtype);
+  if (weights && weights_stride < 1) return set_error(PKC_ERR_INVALID_ARG, "evict_compact: weights_stride must be >= 1");
+  if ((int64_t)batch * num_kv_heads > INT32_MAX / 32)
+    return set_error(PKC_ERR_UNSUPPORTED, "evict_compact: more than 2^26 (request, head) rows");
+  if (int rc = check_ws(workspace, workspace_bytes, PKC_STATUS_BYTES)) return rc;
+  if (batch == 0) return PKC_OK;
+  const bool mx4 = kv_dtype == PKC_MX4;
+  if (!keep || !k_cache || !v_cache || !block_table || !cache_seqlens || (mx4 && (!k_scales || !v_scales)))
+    return set_error(PKC_ERR_INVALID_ARG, "evict_compact: NULL pointer");
+  if (!aligned16(k_cache) || !aligned16(v_cache) || (mx4 && (!aligned4(k_scales) || !aligned4(v_scales))))
+    return set_error(PKC_ERR_INVALID_ARG, "evict_compact: caches must be 16-byte aligned, scales 4-byte");
+  CompactParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.keep = keep; p.budget = budget; p.k_cache = k_cache; p.v_cache = v_cache;
+  p.k_scales = mx4 ? k_scales : nullptr; p.v_scales = mx4 ? v_scales : nullptr;
+  p.weights = weights; p.w_stride = weights_stride;
+  p.block_table = block_table; p.cache_seqlens = cache_seqlens;
+  p.bt_stride = block_table_stride; p.num_pages = num_pages;
+  p.batch = batch; p.hkv = num_kv_heads; p.page_size = page_size; p.page_shift = page_shift_of(page_size);
+  p.row_bytes = mx4 ? 64 : kv_dtype == PKC_E4M3 ? 128 : 256;
+  p.status = static_cast<int32_t*>(workspace);
+  const int e = launch_evict_compact(p, stream);
+  return e ? cuda_error(e, "evict_compact launch") : PKC_OK;
 }
 
 }  // extern "C"

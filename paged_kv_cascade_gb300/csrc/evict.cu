@@ -1,0 +1,391 @@
+// Eviction from a paged cache: which tokens a request keeps, and the move of
+// the kept ones to the front of its pages.
+//
+// Select.  Per (request, KV head) the kept slots are the first `sinks`, the
+// last `recent`, and of those between the m = budget - sinks - recent with
+// the largest accumulated weights, the lower slot of equal ones.  A weight's
+// bits become an unsigned key in the same order (NaN above infinity, the
+// two zeros equal), and the m-th largest key T is found digit by digit from
+// the top (11 + 11 + 10 bits): a histogram of the keys that agree with the
+// digits found so far, and the bin in which the count from above reaches m.
+// One more pass over the keys, in order, gives each kept slot its rank.  The
+// weights are read from memory once, into shared memory; a row is worked on
+// by a cluster of up to 8 blocks, which add up their histograms through
+// distributed shared memory, so that few long rows use the machine too.
+// What bounds it is the chain of passes and barriers per row, not HBM.
+//
+// Compact.  Row j of a (request, head) becomes row keep[j]; keep ascends
+// strictly, so keep[j] >= j.  A block moves one slice of one head's K or V
+// rows, chunk after chunk of new slots in order, each chunk in registers
+// before any of it is written.  The next chunk's rows lie at or behind its
+// own first slot, where nothing has been written yet, so its loads are in
+// flight while the current chunk is stored.  Bound by HBM: a kept row is
+// read once and written once.
+#include <cooperative_groups.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "mx4.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace pkc {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Select
+// ---------------------------------------------------------------------------
+
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kBinsPerThread = kBins / kSelThreads;
+
+__device__ __forceinline__ uint32_t order_key(float w) {
+  if (w != w) return 0xffffffffu;
+  const uint32_t u = __float_as_uint(w == 0.f ? 0.f : w);
+  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+
+struct SelectShared {
+  uint32_t hist[2][kBins];  // alternate between digits: one barrier per digit
+  int warp_sum[kSelWarps];
+  int gt[kSelWarps], eq[kSelWarps];
+  int cta_gt, cta_eq;
+  int bin, rest;
+};
+
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectParams p) {
+  extern __shared__ __align__(16) uint8_t smem_sel[];
+  SelectShared& S = *reinterpret_cast<SelectShared*>(smem_sel);
+  uint32_t* keys = reinterpret_cast<uint32_t*>(smem_sel + sizeof(SelectShared));
+  cg::cluster_group cluster = cg::this_cluster();
+  const int n_cta = p.cluster, rank = (int)(blockIdx.x % n_cta);
+  const int row = (int)(blockIdx.x / n_cta), b = row / p.hkv;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int32_t* keep = p.keep + (int64_t)row * p.budget;
+  const float* w = p.weights + (int64_t)row * p.w_stride;
+  int len = p.cache_seqlens[b];
+  const int at = rank * kSelThreads + tid, all = n_cta * kSelThreads;  // this thread in the row's cluster
+
+  if (len > p.w_stride) {  // (uniform over the cluster, as every early return)
+    if (at == 0) report(p.status, PKC_ERR_PLAN);
+    len = 0;
+  }
+  if (len <= p.budget) {
+    for (int j = at; j < p.budget; j += all) keep[j] = j < len ? j : -1;
+    return;
+  }
+  const int n = len - p.sinks - p.recent;       // slots to choose from
+  const int m = p.budget - p.sinks - p.recent;  // slots to choose, m < n
+  for (int j = at; j < p.sinks; j += all) keep[j] = j;
+  for (int j = at; j < p.recent; j += all) keep[p.budget - p.recent + j] = len - p.recent + j;
+  if (m == 0) return;
+
+  // This block's part of the choice: keys [lo, lo + mine).
+  const int per = (n + n_cta - 1) / n_cta;
+  const int lo = min(rank * per, n), mine = min(per, n - lo);
+  const bool cached = mine <= p.smem_keys;
+  const float* src = w + p.sinks + lo;
+  auto key_at = [&](int i) { return cached ? keys[i] : order_key(src[i]); };
+  for (int i = tid; i < 2 * kBins; i += kSelThreads) (&S.hist[0][0])[i] = 0;
+  if (cached) {
+    for (int i = tid; i < mine; i += kSelThreads) keys[i] = order_key(__ldcs(src + i));
+  }
+  __syncthreads();
+
+  uint32_t prefix = 0;  // digits found, in place
+  int rest = m;         // to be chosen among the keys that agree with them
+  for (int d = 0; d < 3; ++d) {
+    const int shift = d == 0 ? 21 : d == 1 ? 10 : 0, width = d == 2 ? 10 : 11;
+    uint32_t* hist = S.hist[d & 1];
+    for (int i0 = warp * 32; i0 < mine; i0 += kSelThreads) {  // (warp-uniform)
+      const int i = i0 + lane;
+      const uint32_t k = i < mine ? key_at(i) : 0u;
+      const bool in = i < mine && (d == 0 || (k >> (shift + width)) == (prefix >> (shift + width)));
+      const uint32_t digit = (k >> shift) & ((1u << width) - 1u);
+      // many keys alike (a row of zero weights) must not queue up on one bin
+      const uint32_t act = __ballot_sync(0xffffffffu, in);
+      if (act == 0u) continue;
+      const int first = __ffs(act) - 1;
+      const uint32_t lead = __shfl_sync(0xffffffffu, digit, first);
+      const uint32_t same = __ballot_sync(0xffffffffu, in && digit == lead);
+      if (lane == first) atomicAdd(&hist[lead], (uint32_t)__popc(same));
+      else if (in && digit != lead) atomicAdd(&hist[digit], 1u);
+    }
+    cluster.sync();  // every block's histogram is complete
+    // Total counts of this thread's bins, from the top: thread 0 has the highest.
+    uint32_t cnt[kBinsPerThread];
+    int sum = 0;
+#pragma unroll
+    for (int x = 0; x < kBinsPerThread; ++x) {
+      const int bin = kBins - 1 - (tid * kBinsPerThread + x);
+      cnt[x] = 0;
+      for (int c = 0; c < n_cta; ++c) cnt[x] += cluster.map_shared_rank(hist, c)[bin];
+      sum += (int)cnt[x];
+    }
+    int above = sum;  // inclusive scan over the block
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, above, x);
+      if (lane >= x) above += y;
+    }
+    if (lane == 31) S.warp_sum[warp] = above;
+    __syncthreads();
+    int before = 0;
+    for (int x = 0; x < warp; ++x) before += S.warp_sum[x];
+    above += before - sum;  // keys in higher bins than this thread's
+    if (above < rest && rest <= above + sum) {  // exactly one thread
+#pragma unroll
+      for (int x = 0; x < kBinsPerThread; ++x) {
+        const int c = (int)cnt[x];
+        if (above < rest && rest <= above + c) {
+          S.bin = kBins - 1 - (tid * kBinsPerThread + x);
+          S.rest = rest - above;
+        }
+        above += c;
+      }
+    }
+    __syncthreads();
+    prefix |= (uint32_t)S.bin << shift;
+    rest = S.rest;
+    if (d == 0) {  // the third digit uses this buffer again: all blocks are past it at the next barrier
+      __syncthreads();
+    } else if (d == 1) {
+      for (int i = tid; i < kBins; i += kSelThreads) S.hist[0][i] = 0;
+      __syncthreads();
+    }
+  }
+  // Keys above T = prefix are kept, and the first `rest` of those equal to it.
+  // Each warp takes a consecutive part: counts, then ranks.
+  const int part = ((mine + kSelWarps - 1) / kSelWarps + 31) & ~31;
+  const int w_lo = min(warp * part, mine), w_hi = min(w_lo + part, mine);
+  int gt = 0, eq = 0;
+  for (int i0 = w_lo; i0 < w_hi; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t k = i < w_hi ? key_at(i) : 0u;
+    gt += __popc(__ballot_sync(0xffffffffu, i < w_hi && k > prefix));
+    eq += __popc(__ballot_sync(0xffffffffu, i < w_hi && k == prefix));
+  }
+  if (lane == 0) {
+    S.gt[warp] = gt;
+    S.eq[warp] = eq;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    int a = 0, c = 0;
+    for (int x = 0; x < kSelWarps; ++x) {
+      a += S.gt[x];
+      c += S.eq[x];
+    }
+    S.cta_gt = a;
+    S.cta_eq = c;
+  }
+  cluster.sync();
+  int gt0 = 0, eq0 = 0;  // before this warp's part
+  for (int c = 0; c < rank; ++c) {
+    const SelectShared* o = cluster.map_shared_rank(&S, c);
+    gt0 += o->cta_gt;
+    eq0 += o->cta_eq;
+  }
+  for (int x = 0; x < warp; ++x) {
+    gt0 += S.gt[x];
+    eq0 += S.eq[x];
+  }
+  const uint32_t below = (1u << lane) - 1u;
+  for (int i0 = w_lo; i0 < w_hi; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t k = i < w_hi ? key_at(i) : 0u;
+    const bool is_gt = i < w_hi && k > prefix, is_eq = i < w_hi && k == prefix;
+    const uint32_t bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
+    const int g = gt0 + __popc(bg & below), e = eq0 + __popc(be & below);
+    if (is_gt || (is_eq && e < rest)) keep[p.sinks + g + min(e, rest)] = p.sinks + lo + i;
+    gt0 += __popc(bg);
+    eq0 += __popc(be);
+  }
+  cluster.sync();  // no block leaves while another reads its counts
+}
+
+// ---------------------------------------------------------------------------
+// Compact
+// ---------------------------------------------------------------------------
+
+constexpr int kMoveThreads = 256;
+constexpr int kMoveRows = 4;  // rows per thread and chunk (two chunks in registers)
+
+__device__ __forceinline__ uint4 load_cg(const uint4* p) { return __ldcg(p); }
+__device__ __forceinline__ uint32_t load_cg(const uint32_t* p) { return __ldcg(p); }
+
+// Move rows keep[j] -> j, j < n, in units of V (one unit of a row per
+// thread); at(slot) is this thread's unit of a slot, `row` its row within a
+// pass of `rows` rows.  Called by a whole block.
+template <typename V, typename At>
+__device__ __forceinline__ void move_rows(const int32_t* keep, int n, int row, int rows, At at) {
+  V buf[2][kMoveRows];
+  int32_t src[kMoveRows];
+  const int chunk = rows * kMoveRows;
+  auto indices = [&](int c) {
+#pragma unroll
+    for (int u = 0; u < kMoveRows; ++u) {
+      const int j = c + u * rows + row;
+      src[u] = j < n ? keep[j] : -1;
+    }
+  };
+  auto load = [&](V (&x)[kMoveRows]) {
+#pragma unroll
+    for (int u = 0; u < kMoveRows; ++u)
+      if (src[u] >= 0) x[u] = load_cg(at(src[u]));
+  };
+  auto store = [&](int c, const V (&x)[kMoveRows]) {
+#pragma unroll
+    for (int u = 0; u < kMoveRows; ++u) {
+      const int j = c + u * rows + row;
+      if (j < n) *at(j) = x[u];
+    }
+  };
+  indices(0);
+  load(buf[0]);
+  indices(chunk);
+  for (int c = 0; c < n; c += 2 * chunk) {
+    load(buf[1]);
+    indices(c + 2 * chunk);
+    __syncthreads();  // chunk c has been read by every thread
+    store(c, buf[0]);
+    if (c + chunk >= n) break;
+    load(buf[0]);
+    indices(c + 3 * chunk);
+    __syncthreads();
+    store(c + chunk, buf[1]);
+  }
+}
+
+__global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const CompactParams p) {
+  const int part = (int)(blockIdx.x % p.parts);
+  const int row = (int)(blockIdx.x / p.parts), b = row / p.hkv, h = row % p.hkv;
+  const int tid = threadIdx.x;
+  const int len = p.cache_seqlens[b], n = p.budget;
+  bool bad_page = false;
+  if (len > n) {
+    const int32_t* keep = p.keep + (int64_t)row * n;
+    const int32_t* bt_row = p.block_table + (int64_t)b * p.bt_stride;
+    const PageDiv pages{p.page_size, p.page_shift};
+    // Every page of the request must be there, and the row of kept slots
+    // ascend within its length; else nothing of it moves.
+    const int64_t n_pages = ((int64_t)len + p.page_size - 1) / p.page_size;
+    bad_page = n_pages > p.bt_stride;
+    if (!bad_page)
+      for (int64_t i = tid; i < n_pages; i += kMoveThreads) {
+        const int32_t id = bt_row[i];
+        bad_page = bad_page || id < 0 || id >= p.num_pages;
+      }
+    bool bad_keep = p.weights && len > p.w_stride;
+    for (int j = tid; j < n; j += kMoveThreads) {
+      const int32_t k = keep[j];
+      bad_keep = bad_keep || k < (j > 0 ? keep[j - 1] + 1 : 0) || k >= len;
+    }
+    bad_page = __syncthreads_or(bad_page);
+    bad_keep = __syncthreads_or(bad_keep);
+    if (bad_page || bad_keep) {
+      if (tid == 0) report(p.status, bad_page ? PKC_ERR_BLOCK_TABLE : PKC_ERR_PLAN);
+    } else {
+      // (strictly ascending and >= 0: keep[j] >= j)
+      auto token = [&](int slot) {  // row of (slot, this head) in the pools
+        int page, s;
+        pages.split(slot, page, s);
+        return ((int64_t)bt_row[page] * p.page_size + s) * p.hkv + h;
+      };
+      if (part < 2 * p.slices) {  // a slice of K's or V's rows
+        uint8_t* base = static_cast<uint8_t*>(part & 1 ? p.v_cache : p.k_cache);
+        const int units = p.row_bytes / 16 / p.slices;  // 16-byte units of a row in the slice
+        const int unit = (part >> 1) * units + tid % units;
+        move_rows<uint4>(keep, n, tid / units, kMoveThreads / units, [&](int slot) {
+          return reinterpret_cast<uint4*>(base + token(slot) * p.row_bytes) + unit;
+        });
+      } else if (part < 2 * p.slices + (p.k_scales ? 2 : 0)) {  // mx4 scales: 4 bytes a row
+        uint32_t* base = static_cast<uint32_t*>((part - 2 * p.slices) ? p.v_scales : p.k_scales);
+        move_rows<uint32_t>(keep, n, tid, kMoveThreads, [&](int slot) { return base + token(slot); });
+      } else {  // weights: the kept ones, zeros behind them
+        uint32_t* w = reinterpret_cast<uint32_t*>(p.weights) + (int64_t)row * p.w_stride;
+        move_rows<uint32_t>(keep, n, tid, kMoveThreads, [&](int slot) { return w + slot; });
+        __syncthreads();
+        for (int j = n + tid; j < len; j += kMoveThreads) w[j] = 0u;
+      }
+    }
+  }
+  // The lengths shrink once every block has read them: by the block that
+  // finishes last, which also resets the counter for the next launch.
+  int32_t* ctr = p.status + PKC_COMPACT_COUNTER;
+  __shared__ int last, any_bad;
+  if (bad_page && tid == 0) atomicExch(ctr + 1, 1);
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) last = atomicAdd(ctr, 1) == (int)gridDim.x - 1;
+  __syncthreads();
+  if (!last) return;
+  __threadfence();
+  if (tid == 0) {
+    any_bad = atomicExch(ctr + 1, 0);
+    atomicExch(ctr, 0);
+  }
+  __syncthreads();
+  for (int r = tid; r < p.batch; r += kMoveThreads) {
+    const int l = p.cache_seqlens[r];
+    if (l <= n) continue;
+    bool ok = true;
+    if (any_bad) {  // a request with a missing page keeps its length
+      const int64_t n_pages = ((int64_t)l + p.page_size - 1) / p.page_size;
+      ok = n_pages <= p.bt_stride;
+      for (int64_t i = 0; ok && i < n_pages; ++i) {
+        const int32_t id = p.block_table[(int64_t)r * p.bt_stride + i];
+        ok = id >= 0 && id < p.num_pages;
+      }
+    }
+    if (ok) p.cache_seqlens[r] = n;
+  }
+}
+
+}  // namespace
+
+int launch_evict_select(const SelectParams& p_in, void* stream) {
+  SelectParams p = p_in;
+  const int64_t rows = (int64_t)p.batch * p.hkv;
+  if (rows <= 0) return 0;
+  // Blocks per row: doubled while the machine has room for them and each
+  // still has 2048 keys of the longest row.
+  p.cluster = 1;
+  while (p.cluster < 8 && rows * p.cluster * 2 <= num_sms() && p.w_stride / (2 * p.cluster) >= 2048) p.cluster *= 2;
+  const int64_t per = (p.w_stride + p.cluster - 1) / p.cluster;
+  p.smem_keys = (int)std::min<int64_t>(per, 48 * 1024);
+  const int smem = (int)sizeof(SelectShared) + 4 * p.smem_keys;
+  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return (int)e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(rows * p.cluster));
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = (cudaStream_t)stream;
+  cudaLaunchAttribute la[1];
+  la[0].id = cudaLaunchAttributeClusterDimension;
+  la[0].val.clusterDim.x = (unsigned)p.cluster;
+  la[0].val.clusterDim.y = la[0].val.clusterDim.z = 1;
+  cfg.attrs = la;
+  cfg.numAttrs = 1;
+  return (int)cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
+}
+
+int launch_evict_compact(const CompactParams& p_in, void* stream) {
+  CompactParams p = p_in;
+  const int64_t rows = (int64_t)p.batch * p.hkv;
+  if (rows <= 0) return 0;
+  // Whole rows per block while that fills the machine (8 blocks per SM);
+  // else slices of a row, down to a 32-byte sector.
+  p.slices = 1;
+  while (p.row_bytes / p.slices > 32 && rows * 2 * p.slices < 8 * (int64_t)num_sms()) p.slices *= 2;
+  p.parts = 2 * p.slices + (p.k_scales ? 2 : 0) + (p.weights ? 1 : 0);
+  if (rows * p.parts > INT32_MAX) return (int)cudaErrorInvalidValue;
+  evict_compact_kernel<<<(unsigned)(rows * p.parts), kMoveThreads, 0, (cudaStream_t)stream>>>(p);
+  return (int)cudaGetLastError();
+}
+
+}  // namespace pkc

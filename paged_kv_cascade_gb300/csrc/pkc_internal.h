@@ -12,9 +12,11 @@
 // The status block at the start of every workspace: word 0 is the status
 // word (pkc_device_status), words 16-17 the dynamic decode queue's counters,
 // words 18-19 the mx4 append's count of finished blocks and its flag for a
-// missing page, word 32 the result of pkc_selftest_wait_timeout.
+// missing page, words 20-21 the same of the eviction's compact, word 32 the
+// result of pkc_selftest_wait_timeout.
 #define PKC_STATUS_BYTES 256
 #define PKC_APPEND_COUNTER 18
+#define PKC_COMPACT_COUNTER 20
 
 namespace pkc {
 
@@ -252,7 +254,53 @@ struct Mx4DecodeParams {
   int num_ctas;            // CTAs of the plan (static schedule)
 };
 
+// Accumulated attention weights (weights.cu).
+struct WeightsParams {
+  const void* q;             // [batch, hkv * g, 128]
+  const float* lse;          // [batch, hkv * g]
+  const void* k_cache;       // keys, or mx4 codes
+  const void* k_scales;      // mx4: [num_pages, page_size, Hkv, 4] bytes
+  const int32_t* block_table;
+  const int32_t* cache_seqlens;
+  float* weights;            // [batch, hkv, w_stride]
+  int64_t bt_stride, num_pages, w_stride;
+  int batch, hkv, g, page_size, page_shift;
+  float scale_log2, decay;   // scale_log2: sm_scale * k_scale * log2(e)
+  int hg, n_seg, seg_tokens; // set by the launcher: heads per block, segments of the longest request
+  int32_t* status;
+};
+
+// Eviction (evict.cu): which slots each (request, KV head) keeps.
+struct SelectParams {
+  const float* weights;      // [batch, hkv, w_stride]
+  const int32_t* cache_seqlens;
+  int32_t* keep;             // [batch, hkv, budget]
+  int64_t w_stride;
+  int batch, hkv, budget, sinks, recent;
+  int cluster, smem_keys;    // set by the launcher: blocks per row, keys of one block in shared memory
+  int32_t* status;
+};
+
+// Eviction (evict.cu): the kept slots moved to the front, in place.
+struct CompactParams {
+  const int32_t* keep;       // [batch, hkv, budget]
+  void* k_cache;             // [num_pages, page_size, hkv, row_bytes] bytes
+  void* v_cache;
+  void* k_scales;            // mx4: [num_pages, page_size, hkv, 4] bytes, or nullptr
+  void* v_scales;
+  float* weights;            // [batch, hkv, w_stride] or nullptr
+  const int32_t* block_table;
+  int32_t* cache_seqlens;
+  int64_t bt_stride, num_pages, w_stride;
+  int batch, hkv, budget, row_bytes, page_size, page_shift;
+  int slices, parts;         // set by the launcher: slices of a row, blocks per (request, head)
+  int32_t* status;
+};
+
 // Launchers (defined in the .cu files); return a cudaError_t value.
+int launch_evict_select(const SelectParams& p, void* stream);
+int launch_evict_compact(const CompactParams& p, void* stream);
+int launch_weights(const WeightsParams& p, int q_dtype, int kv_dtype, void* stream);
 int launch_append_mx4(const Mx4RowsParams& p, int dtype, void* stream);
 int launch_gather_mx4(const Mx4RowsParams& p, int dtype, void* stream);
 // n_work: chunks of the plan (0 without one)

@@ -98,3 +98,55 @@ def test_mx4_reference_is_the_nearest_code():
     assert v[0, 64] == 0.0 and np.all(np.isnan(v[0, 96:]))
     assert s[0].tolist() == [127, 127, 1, 255]
     assert np.all(c.reshape(1, 8, 4, 2)[:, :, 3] == 0)  # a NaN block's codes
+
+
+def test_accumulate_weights_refuses(L):
+    # q lse k ks table stride lens | batch hq hkv d ps pages sm k_scale decay w W dtype kv ws bytes stream
+    good = [F, F, F, None, F, 4, F, 2, 16, 8, 128, 16, 10, 1.0, 1.0, 1.0, F, 64, 1, 1, WS, 1 << 20, None]
+    nan, inf = float("nan"), float("inf")
+    for args, code in variants(good, [
+            (0, None, 1), (1, None, 1), (2, None, 1), (4, None, 1), (6, None, 1), (16, None, 1), (0, OFF, 1),
+            (2, OFF, 1), (5, 0, 1), (7, -1, 1), (8, 12, 1), (8, 24, 2), (10, 64, 2), (11, 0, 1), (11, 1 << 30, 2),
+            (12, -1, 1), (14, 0.0, 1), (14, 2.0, 1), (14, nan, 1), (15, -0.5, 1), (15, 1.5, 1), (15, nan, 1),
+            (15, inf, 1), (17, 0, 1), (18, 2, 1), (18, 0, 1), (19, 2, 1), (19, 0, 1), (19, 5, 1), (19, 4, 1),
+            (21, 100, 3)]):
+        assert L.pkc_accumulate_weights(*args) == code, (args, L.pkc_last_error())
+    # an e4m3 cache takes fp16 queries and a finite scale > 0
+    for args, code in variants(good[:19] + [3] + good[20:], [(18, 2, 1), (14, -1.0, 1), (14, inf, 1)]):
+        assert L.pkc_accumulate_weights(*args) == code
+    assert L.pkc_accumulate_weights(*good[:7], 0, *good[8:]) == 0
+
+
+def test_evict_select_refuses(L):
+    # w W lens batch hkv budget sinks recent keep ws bytes stream
+    good = [F, 64, F, 2, 8, 16, 4, 8, F, WS, 1 << 20, None]
+    for args, code in variants(good, [
+            (0, None, 1), (2, None, 1), (8, None, 1), (1, 0, 1), (3, -1, 1), (4, 0, 1), (5, 0, 1), (5, 11, 1),
+            (6, -1, 1), (7, -1, 1), (7, 13, 1), (6, 2 ** 31 - 1, 1), (3, 1 << 28, 2), (10, 255, 3)]):
+        assert L.pkc_evict_select(*args) == code, (args, L.pkc_last_error())
+    assert L.pkc_evict_select(*good[:3], 0, *good[4:]) == 0
+
+
+def test_evict_compact_refuses(L):
+    # keep budget k v ks vs table stride lens w W | batch hkv d ps pages kv ws bytes stream
+    good = [F, 16, F, F, None, None, F, 4, F, F, 64, 2, 8, 128, 16, 10, 1, WS, 1 << 20, None]
+    for args, code in variants(good, [
+            (0, None, 1), (2, None, 1), (3, None, 1), (6, None, 1), (8, None, 1), (1, 0, 1), (2, OFF, 1), (3, OFF, 1),
+            (7, 0, 1), (10, 0, 1), (11, -1, 1), (11, 1 << 26, 2), (12, 0, 1), (13, 64, 2), (14, 0, 1), (15, -1, 1),
+            (16, 0, 1), (16, 5, 1), (16, 4, 1), (18, 200, 3)]):
+        assert L.pkc_evict_compact(*args) == code, (args, L.pkc_last_error())
+    assert L.pkc_evict_compact(*good[:11], 0, *good[12:]) == 0
+
+
+def test_eviction_binding_refuses_before_any_call():
+    w, lens = torch.zeros(2, 2, 64), torch.zeros(2, dtype=torch.int32)
+    bt, ws = torch.zeros(2, 4, dtype=torch.int32), torch.zeros(1024, dtype=torch.uint8)
+    k = torch.zeros(4, 16, 2, 128).half()
+    with pytest.raises(ValueError, match="CUDA"):
+        pkc.evict_select(w, lens, 8, 1, 1, ws)
+    with pytest.raises(ValueError, match="CUDA"):
+        pkc.accumulate_weights(torch.zeros(2, 4, 128).half(), torch.zeros(2, 4), k, bt, lens, 0.1, w, ws)
+    with pytest.raises(ValueError, match="CUDA"):
+        pkc.evict_compact(torch.zeros(2, 2, 8, dtype=torch.int32), k, k, bt, lens, ws)
+    with pytest.raises(TypeError, match="dtype"):
+        pkc.evict_compact(torch.zeros(2, 2, 8, dtype=torch.int32), k.float(), k, bt, lens, ws)

@@ -568,7 +568,7 @@ int pkc_gather_kv_mx4(const void* k_codes, const void* k_scales,
  * any number of KV heads.  Split requests are always joined by the
  * standalone contraction kernel.  Accuracy beyond the format's: the scores
  * are those of the cached values with float32 sums; probabilities enter the
- * V product with 22 bits, and a value below 2^-26 of the largest cached
+ * V product with 22 bits, and a value below 2^-24 of the largest cached
  * |V| of its block of dims may count as zero.  A page id < 0 or >= num_pages
  * is recorded as PKC_ERR_BLOCK_TABLE and its tokens take no part.
  */

@@ -99,6 +99,8 @@ class PkcError(RuntimeError):
 def lib():
     """The loaded libpkc.so.  Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -119,22 +121,38 @@ def _check(rc):
         raise PkcError(rc, lib().pkc_last_error().decode())
 
 
+# A small call's time is the host's: the helpers below run a dozen times per
+# call, so they import torch once, compare devices by index and hand plain
+# integers to ctypes.
+_torch = None
+
+
+def _t():
+    """torch, imported on the first call that takes tensors."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
 def _dtype_code(t) -> int:
-    import torch
-    return {torch.float32: F32, torch.float16: F16, torch.bfloat16: BF16}[t.dtype]
+    torch = _torch or _t()
+    d = t.dtype
+    return F16 if d == torch.float16 else BF16 if d == torch.bfloat16 else {torch.float32: F32}[d]
 
 
 def _stream(stream):
-    import torch
+    torch = _torch or _t()
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        return stream
+    return stream.cuda_stream
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _host_i32(a):
@@ -154,9 +172,10 @@ def _hptr(a):
 def _expect(name, t, dtypes, shape, device=None):
     """t must be a contiguous CUDA tensor of one of `dtypes` whose shape
     matches `shape` (None entries match any size) on `device`."""
-    import torch
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, (_torch or _t()).Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
+    if t.shape == shape and t.dtype in dtypes and t.is_contiguous() and device is not None and t.device == device:
+        return
     if t.dtype not in dtypes:
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {list(dtypes)}")
     if len(t.shape) != len(shape) or any(w is not None and w != g for g, w in zip(t.shape, shape)):
@@ -374,14 +393,22 @@ def append_kv(k_new, v_new, k_cache, v_cache, block_table, cache_seqlens, worksp
 
 def _expect_current(t):
     """The library launches on the current device: refuse tensors of another."""
-    import torch
+    torch = _torch or _t()
     if t.device.index != torch.cuda.current_device():
         raise ValueError(f"tensors are on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
 
 
+def _expect_bytes(name, t, device):
+    """A byte buffer of any size."""
+    torch = _torch or _t()
+    if not (isinstance(t, torch.Tensor) and t.dtype == torch.uint8 and t.dim() == 1 and t.is_contiguous()
+            and t.device == device):
+        _expect(name, t, (torch.uint8,), (None,), device)
+
+
 def _check_mx4(k_codes, k_scales, v_codes, v_scales, block_table, workspace):
     """The four pools of an mx4 cache, its table and the workspace."""
-    import torch
+    torch = _torch or _t()
     u8 = (torch.uint8,)
     _expect("k_codes", k_codes, u8, (None, None, None, 64))
     _expect_current(k_codes)
@@ -391,7 +418,7 @@ def _check_mx4(k_codes, k_scales, v_codes, v_scales, block_table, workspace):
     _expect("k_scales", k_scales, u8, (P, ps, Hkv, 4), dev)
     _expect("v_scales", v_scales, u8, (P, ps, Hkv, 4), dev)
     _expect("block_table", block_table, (torch.int32,), (None, None), dev)
-    _expect("workspace", workspace, u8, (None,), dev)
+    _expect_bytes("workspace", workspace, dev)
     return P, ps, Hkv, block_table.shape[0], dev
 
 
@@ -400,7 +427,7 @@ def append_kv_mx4(k_new, v_new, new_indptr, k_codes, k_scales, v_codes, v_scales
     """Quantise new tokens (k_new / v_new [T, Hkv, 128], rows new_indptr[b] ..
     new_indptr[b+1]-1 for request b, device int32) to the end of every
     request's mx4 cache and grow cache_seqlens, in place."""
-    import torch
+    torch = _torch or _t()
     P, ps, Hkv, B, dev = _check_mx4(k_codes, k_scales, v_codes, v_scales, block_table, workspace)
     _expect("k_new", k_new, (torch.float16, torch.bfloat16), (None, Hkv, 128), dev)
     _expect("v_new", v_new, (k_new.dtype,), tuple(k_new.shape), dev)
@@ -418,7 +445,7 @@ def gather_kv_mx4(k_codes, k_scales, v_codes, v_scales, block_table, first, out_
     (default torch.float16): row t of out_indptr[b] .. out_indptr[b+1]-1 is
     token first[b] + t - out_indptr[b] of request b.  Rows of no request stay
     as they were in given k and v (and are undefined in new ones)."""
-    import torch
+    torch = _torch or _t()
     P, ps, Hkv, B, dev = _check_mx4(k_codes, k_scales, v_codes, v_scales, block_table, workspace)
     _expect("first", first, (torch.int32,), (B,), dev)
     _expect("out_indptr", out_indptr, (torch.int32,), (B + 1,), dev)
@@ -444,7 +471,7 @@ def gather_kv_mx4(k_codes, k_scales, v_codes, v_scales, block_table, first, out_
 def paged_decode_state_mx4(q, k_codes, k_scales, v_codes, v_scales, block_table, cache_seqlens,
                            sm_scale, workspace, plan_buf=None, o=None, lse=None, stream=None):
     """States of fp16 / bf16 q [B, Hq, 128] over each request's mx4 cache."""
-    import torch
+    torch = _torch or _t()
     P, ps, Hkv, B, dev = _check_mx4(k_codes, k_scales, v_codes, v_scales, block_table, workspace)
     _expect("q", q, (torch.float16, torch.bfloat16), (B, None, 128), dev)
     _expect("cache_seqlens", cache_seqlens, (torch.int32,), (B,), dev)
@@ -470,7 +497,7 @@ def paged_decode_state_mx4(q, k_codes, k_scales, v_codes, v_scales, block_table,
 def _kv_kind(cache, scales):
     """(kv_dtype code, row length) of a cache: 16-bit, e4m3 codes, or mx4
     codes (given with their scales)."""
-    import torch
+    torch = _torch or _t()
     if scales is not None:
         return MX4, 64
     if cache.dtype == torch.uint8:
@@ -485,7 +512,7 @@ def accumulate_weights(q, lse, k_cache, block_table, cache_seqlens, sm_scale, we
     head h's query heads; weights [B, Hkv, W] float32, in place.  k_cache:
     16-bit of q's dtype, e4m3 codes (fp16 q, k_scale), or mx4 codes with
     k_scales."""
-    import torch
+    torch = _torch or _t()
     _expect("k_cache", k_cache, (torch.float16, torch.bfloat16, torch.uint8), (None, None, None, None))
     _expect_current(k_cache)
     kind, row = _kv_kind(k_cache, k_scales)
@@ -501,7 +528,7 @@ def accumulate_weights(q, lse, k_cache, block_table, cache_seqlens, sm_scale, we
     _expect("block_table", block_table, (torch.int32,), (B, None), dev)
     _expect("cache_seqlens", cache_seqlens, (torch.int32,), (B,), dev)
     _expect("weights", weights, (torch.float32,), (B, Hkv, None), dev)
-    _expect("workspace", workspace, (torch.uint8,), (None,), dev)
+    _expect_bytes("workspace", workspace, dev)
     _check(lib().pkc_accumulate_weights(
         _ptr(q), _ptr(lse), _ptr(k_cache), _ptr(k_scales), _ptr(block_table), block_table.shape[1],
         _ptr(cache_seqlens), B, Hq, Hkv, 128, ps, P, float(sm_scale), float(k_scale), float(decay),
@@ -515,7 +542,7 @@ def evict_select(weights, cache_seqlens, budget, sinks, recent, workspace, keep=
     ascending order: the first `sinks`, the last `recent`, and the largest of
     weights [B, Hkv, W] between them (all, then -1, of a request within the
     budget)."""
-    import torch
+    torch = _torch or _t()
     _expect("weights", weights, (torch.float32,), (None, None, None))
     _expect_current(weights)
     B, Hkv, W = weights.shape
@@ -525,7 +552,7 @@ def evict_select(weights, cache_seqlens, budget, sinks, recent, workspace, keep=
         raise ValueError("evict_select: budget must be >= 1, sinks and recent >= 0 and together at most the "
                          f"budget (got {budget}, {sinks}, {recent})")
     _expect("cache_seqlens", cache_seqlens, (torch.int32,), (B,), dev)
-    _expect("workspace", workspace, (torch.uint8,), (None,), dev)
+    _expect_bytes("workspace", workspace, dev)
     if keep is not None:
         _expect("keep", keep, (torch.int32,), (B, Hkv, budget), dev)
     keep = torch.empty((B, Hkv, budget), dtype=torch.int32, device=dev) if keep is None else keep
@@ -540,7 +567,7 @@ def evict_compact(keep, k_cache, v_cache, block_table, cache_seqlens, workspace,
     budget to its first slots and cut its length, in place: K and V (16-bit,
     e4m3 codes, or mx4 codes with their scales) and, given, the accumulated
     weights [B, Hkv, W]."""
-    import torch
+    torch = _torch or _t()
     _expect("k_cache", k_cache, (torch.float16, torch.bfloat16, torch.uint8), (None, None, None, None))
     _expect_current(k_cache)
     if (k_scales is None) != (v_scales is None):
@@ -558,7 +585,7 @@ def evict_compact(keep, k_cache, v_cache, block_table, cache_seqlens, workspace,
     B, _, budget = keep.shape
     _expect("block_table", block_table, (torch.int32,), (B, None), dev)
     _expect("cache_seqlens", cache_seqlens, (torch.int32,), (B,), dev)
-    _expect("workspace", workspace, (torch.uint8,), (None,), dev)
+    _expect_bytes("workspace", workspace, dev)
     if weights is not None:
         _expect("weights", weights, (torch.float32,), (B, Hkv, None), dev)
     _check(lib().pkc_evict_compact(

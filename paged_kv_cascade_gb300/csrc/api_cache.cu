@@ -33,6 +33,8 @@ int check_pool(const char* call, int batch, int hkv, int head_dim, int page_size
     return set_error(PKC_ERR_UNSUPPORTED, "%s: head_dim must be %d (got %d)", call, PKC_HEAD_DIM, head_dim);
   if ((int64_t)block_table_stride * page_size > INT32_MAX - 65536)  // token positions are 32-bit
     return set_error(PKC_ERR_UNSUPPORTED, "%s: a block table of more than 2^31 - 65537 tokens", call);
+  if (num_pages > (int64_t)(UINT32_MAX - 1) / page_size)  // and slots of the pool
+    return set_error(PKC_ERR_UNSUPPORTED, "%s: a pool of more than 2^32 - 2 tokens", call);
   return PKC_OK;
 }
 

@@ -14,23 +14,23 @@
 //   s = sum_b 2^(s_b - 127) acc_b
 // is formed in float32.
 //
-// Values.  O^T's 128 dims are 4 blocks whose scales differ by token, so the
-// scale goes on the probabilities, one power of two per token and block:
-//   O_b += (p 2^(e_b - E_b + 11)) c_b
+// Values.  O^T = V^T P^T, the dims on the tile's 16 rows.  The dims are 4
+// blocks whose scales differ by token, so the scale goes on the
+// probabilities, one power of two per token and block:
+//   O_b += (p 2^(e_b - E_b)) c_b
 // with E_b the largest scale byte seen so far in block b (O_b is rescaled
-// when it grows) and p <= 2^4 (the softmax reference moves when a score
-// exceeds it by more).  A probability enters as an fp16 high part in rows
-// 0..7 of the tile and its remainder times 2^11 in rows 8..15, both at the
-// cost of one product; the product with the power of two is exact down to
-// 2^-24, where the largest are 2^11 and more.  So the error is at most 2^-22
-// of the weights plus 2^-25 of the largest cached |V| of the block of dims.
+// when it grows).  Probabilities are held times 2^11, at most 2^15 (the
+// softmax reference moves when a score exceeds it by more than 4), as an
+// fp16 high part and an fp16 remainder, one product each; the products with
+// the power of two are exact down to 2^-24.  So a probability enters with 22
+// bits, and what is lost is below 2^-24 of the largest cached |V| of the
+// block of dims.
 //
 // Work split.  A block is one work item -- a planned chunk (or request)
 // x HG KV heads -- of 4 warps; a warp takes every (4 / HG)-th group of 16
 // tokens of one KV head and keeps its own ring of cp.async stages, so no
 // warp waits for another until the item ends and any page size and head
-// count works.  The accumulators take 64 registers a thread: three blocks
-// (12 warps) per SM leave 160; at 16 warps and 128 the kernel spills.
+// count works.  Four blocks (16 warps of 128 registers) per SM.
 #include <cuda_runtime.h>
 
 #include "decode_common.cuh"
@@ -41,18 +41,19 @@ namespace {
 
 constexpr int D = PKC_HEAD_DIM;
 constexpr int kWarps = 4;
-constexpr int kBlocksPerSm = 3;
+constexpr int kBlocksPerSm = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 16;                     // tokens per warp and step
 constexpr int kStages = 4;
 constexpr int kCodes = kTile * kMx4RowBytes;  // K (or V) code bytes per stage
 constexpr int kScales = kTile * 4;
-constexpr int kValid = 2 * (kCodes + kScales);  // two words: bit 4 t of word k, token t + 8 k takes part
-constexpr int kStage = kValid + 128;
+constexpr int kStage = 2 * (kCodes + kScales);
 constexpr int kRing = kStages * kStage;       // per warp
 constexpr int kWarpSmem = kRing + 128;        // + the tile's probability factors
 constexpr float kRefFloor = -3e38f;           // softmax reference before the first token
 constexpr float kLazy = 4.f;                  // log2 of the largest probability between rescales
+constexpr float kLift = 11.f;                 // probabilities are held times 2^kLift: at most 2^15
+constexpr uint32_t kNoToken = 0xffffffffu;
 
 struct Item {
   int valid, req, kb, ke, slot, hg;
@@ -61,11 +62,13 @@ struct Item {
 // Shared memory: the warps' rings, the item, then the merge buffer (warps
 // that share a KV head): per warp and head 128 values, the reference and the
 // sum.
-template <int G> constexpr int smem_bytes() { return kWarps * kWarpSmem + 64 + kWarps * G * (D + 2) * 4; }
+constexpr int kMergeRow = D + 4;
+template <int G> constexpr int smem_bytes() { return kWarps * kWarpSmem + 64 + kWarps * G * kMergeRow * 4; }
 
 // Byte of 16-byte piece c (0..3) of token t's codes within a stage: the
 // fragment reads of K (two tokens t, t + 4 per 8 lanes) and V (tokens
 // 4 i .. 4 i + 3, two pieces each, per 16 lanes) touch every bank once.
+// Token t + 8 is 512 bytes behind token t.
 __device__ __forceinline__ uint32_t code_at(int t, int c) {
   return (uint32_t)(((t >> 1) << 7) + (((t ^ (t >> 2)) & 1) << 6) + ((c ^ (((t >> 1) & 1) << 1)) << 4));
 }
@@ -78,7 +81,9 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return d;
 }
 
-template <typename T, int G>
+// kAligned: the page size is a multiple of 16, so a tile (tokens 16 i ..
+// 16 i + 15) lies in one page.
+template <typename T, int G, bool kAligned>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     paged_decode_mx4_kernel(const __grid_constant__ Mx4DecodeParams mp) {
   const DecodeParams& p = mp.d;
@@ -132,89 +137,110 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     const Item it = *item_s;
     if (!it.valid) break;
     const int kvh = it.hg * HG + hh;
+    // This warp's tiles: number tile0 + j wph (tokens 16 x that), j < mine.
+    const int tile0 = (it.kb >> 4) + cls;
+    const int tiles_end = (it.ke + 15) >> 4;
+    const int mine = it.kb < it.ke && tiles_end > tile0 ? (tiles_end - tile0 + wph - 1) / wph : 0;
+    const int32_t* bt_row = p.block_table + (int64_t)it.req * p.bt_stride;
+    // Pool index (page * page_size + slot) of a token, or kNoToken.
+    auto pool_token = [&](int t) -> uint32_t {
+      int page, slot;
+      pages.split(t, page, slot);
+      const int32_t pid = bt_row[page];
+      if (pid < 0 || pid >= p.num_pages) {
+        report(p.status, PKC_ERR_BLOCK_TABLE);
+        return kNoToken;
+      }
+      return (uint32_t)pid * (uint32_t)p.page_size + (uint32_t)slot;
+    };
+    // Aligned: lane l holds the first token's pool index of tile j0 + l of a
+    // window of 32; the next window is loaded 32 tiles ahead.  Otherwise: of
+    // token l % 16 of the next tile.
+    auto load_window = [&](int j0) -> uint32_t {
+      const int j = j0 + lane;
+      return j < mine ? pool_token((tile0 + j * wph) * kTile) : kNoToken;
+    };
+    auto load_tokens = [&](int j) -> uint32_t {
+      const int t = (tile0 + j * wph) * kTile + (lane & 15);
+      return j < mine && t >= it.kb && t < it.ke ? pool_token(t) : kNoToken;
+    };
+    uint32_t win = kAligned ? load_window(0) : load_tokens(0);
+    uint32_t win_next = kAligned ? load_window(32) : 0u;
+
     uint32_t qf[4][4];
     const float q_undo = load_q_f16<T, G>(
         static_cast<const T*>(p.q) + ((int64_t)it.req * p.hq + (int64_t)kvh * G) * D, lane, qf);
     // factors of this lane's score columns (heads 2 tg, 2 tg + 1), base 2
     const float sc0 = p.scale_log2 * __shfl_sync(0xffffffffu, q_undo, 8 * tg);
     const float sc1 = p.scale_log2 * __shfl_sync(0xffffffffu, q_undo, 8 * tg + 4);
-    float o[4][4][4];  // [block][element i][rows g: high part, rows g + 8: remainder]
+    // O^T: [block][elements i = 0, 1 | 2, 3][element 2 x: heads 2 tg, + 1; element 2 x + 1: the same]
+    float o[4][2][4];
 #pragma unroll
     for (int b = 0; b < 4; ++b)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[b][i][0] = o[b][i][1] = o[b][i][2] = o[b][i][3] = 0.f;
-    float m0 = kRefFloor, m1 = kRefFloor, l0 = 0.f, l1 = 0.f;
-    int e_ref = 0;  // E_b of block lane % 4
+      for (int x = 0; x < 2; ++x) o[b][x][0] = o[b][x][1] = o[b][x][2] = o[b][x][3] = 0.f;
+    float m0 = kRefFloor, m1 = kRefFloor, l0 = 0.f, l1 = 0.f;  // l: times 2^kLift
+    int e_ref = 0;                                             // E_b of block lane % 4
 
-    const int n_tiles = it.kb < it.ke ? (it.ke - it.kb + kTile - 1) / kTile : 0;
-    const int mine = n_tiles > cls ? (n_tiles - cls + wph - 1) / wph : 0;  // this warp's tiles
-    const int32_t* bt_row = p.block_table + (int64_t)it.req * p.bt_stride;
-    // Lane's tokens of tile j: lane / 4 and lane / 4 + 8.
-    auto tile_token = [&](int j) { return it.kb + (cls + j * wph) * kTile; };
-    int32_t pid[2] = {0, 0};
-    auto load_pages = [&](int j) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        pid[k] = 0;
-        if (j >= mine) continue;
-        const int t = tile_token(j) + g + 8 * k;
-        if (t < it.ke) {
-          int page, slot;
-          pages.split(t, page, slot);
-          pid[k] = bt_row[page];
-        }
-      }
-    };
+    // Per lane: pools at this head's (and, of codes, this lane's) bytes.
+    const uint8_t* k_lane = static_cast<const uint8_t*>(p.k_cache) + kvh * kMx4RowBytes + 16 * tg;
+    const uint8_t* v_lane = static_cast<const uint8_t*>(p.v_cache) + kvh * kMx4RowBytes + 16 * tg;
+    const uint8_t* s_lane = static_cast<const uint8_t*>(lane < 16 ? mp.k_scales : mp.v_scales) + kvh * 4;
+    const uint32_t code_stride = (uint32_t)p.hkv * kMx4RowBytes, scale_stride = (uint32_t)p.hkv * 4;
+    uint32_t st_in = ring;  // stage of the next tile to be copied
+    uint64_t present = 0;   // 16 bits per tile in flight: its tokens that are there (latest in the low bits)
     auto issue = [&](int j) {  // copies of tile j (an empty group past the last one)
+      present <<= 16;
       if (j < mine) {
-        const uint32_t st = ring + (j % kStages) * kStage;
-        int64_t row[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const int t = tile_token(j) + g + 8 * k;
-          int page, slot;
-          pages.split(t, page, slot);
-          bool ok = t < it.ke;
-          if (ok && (pid[k] < 0 || pid[k] >= p.num_pages)) {
-            if (tg == 0) report(p.status, PKC_ERR_BLOCK_TABLE);
-            ok = false;
+        uint32_t ta, tb, ts;  // pool indices of tokens g, g + 8, lane % 16
+        if constexpr (kAligned) {
+          if ((j & 31) == 0 && j > 0) {
+            win = win_next;
+            win_next = load_window(j + 32);
           }
-          row[k] = ok ? ((int64_t)pid[k] * p.page_size + slot) * p.hkv + kvh : -1;
-          const uint32_t takes_part = __ballot_sync(0xffffffffu, ok);
-          if (lane == 0) sts32(st + kValid + 4 * k, takes_part);
-          const uint32_t dst = st + code_at(g + 8 * k, tg);
-          const int64_t at = max(row[k], (int64_t)0) * kMx4RowBytes + 16 * tg;
-          cp_async16(dst, static_cast<const uint8_t*>(p.k_cache) + at, ok);
-          cp_async16(dst + kCodes, static_cast<const uint8_t*>(p.v_cache) + at, ok);
+          const uint32_t first = __shfl_sync(0xffffffffu, win, j & 31);
+          const bool there = first != kNoToken;
+          present |= there ? 0xffffu : 0u;
+          ta = there ? first + g : kNoToken;
+          tb = there ? first + g + 8 : kNoToken;
+          // scales of slots outside the chunk become 0: whatever they hold
+          // must not count among the largest
+          const int t = (tile0 + j * wph) * kTile + (lane & 15);
+          ts = there && t >= it.kb && t < it.ke ? first + (lane & 15) : kNoToken;
+        } else {
+          ts = win;
+          present |= __ballot_sync(0xffffffffu, ts != kNoToken) & 0xffffu;
+          ta = __shfl_sync(0xffffffffu, ts, g);
+          tb = __shfl_sync(0xffffffffu, ts, g + 8);
+          win = load_tokens(j + 1);
         }
+        const uint32_t dst = st_in + code_at(g, tg);
+        const bool oka = ta != kNoToken, okb = tb != kNoToken, oks = ts != kNoToken;
+        const uint64_t at_a = oka ? (uint64_t)ta * code_stride : 0u, at_b = okb ? (uint64_t)tb * code_stride : 0u;
+        cp_async16(dst, k_lane + at_a, oka);
+        cp_async16(dst + 512, k_lane + at_b, okb);
+        cp_async16(dst + kCodes, v_lane + at_a, oka);
+        cp_async16(dst + kCodes + 512, v_lane + at_b, okb);
         // scales: lanes 0..15 K, 16..31 V, token lane % 16
-        const int64_t ra = __shfl_sync(0xffffffffu, row[0], 4 * (lane & 7));
-        const int64_t rb = __shfl_sync(0xffffffffu, row[1], 4 * (lane & 7));
-        const int64_t r = (lane & 8) ? rb : ra;
-        const uint8_t* src = static_cast<const uint8_t*>(lane < 16 ? mp.k_scales : mp.v_scales);
-        cp_async4(st + 2 * kCodes + (lane >> 4) * kScales + 4 * (lane & 15), src + max(r, (int64_t)0) * 4, r >= 0);
+        cp_async4(st_in + 2 * kCodes + 4 * lane, s_lane + (oks ? (uint64_t)ts * scale_stride : 0u), oks);
       }
       cp_async_commit();
+      st_in = st_in == ring + (kStages - 1) * kStage ? ring : st_in + kStage;
     };
-    load_pages(0);
 #pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) {
-      issue(s);
-      load_pages(s + 1);
-    }
+    for (int s = 0; s < kStages - 1; ++s) issue(s);
 
+    uint32_t st = ring;
     for (int j = 0; j < mine; ++j) {
       cp_async_wait<kStages - 2>();
       __syncwarp();  // tile j is in shared memory; tile j - 1's stage is free
       issue(j + kStages - 1);
-      load_pages(j + kStages);
-      const uint32_t st = ring + (j % kStages) * kStage;
       const uint32_t k_sc = st + 2 * kCodes, v_sc = k_sc + kScales;
-      // ---- this tile's probability factors 2^(e - E + 11) ----
+      // ---- this tile's probability factors 2^(e - E) ----
       // lane 4 x + b: block b of tokens token_of(2 x), token_of(2 x + 1)
       {
-        const int t = token_of(2 * g);
-        const uint32_t wa = lds32(v_sc + 4 * t), wc = lds32(v_sc + 4 * t + 16);
+        const uint32_t at = v_sc + 4 * token_of(2 * g);
+        const uint32_t wa = lds32(at), wc = lds32(at + 16);
         const int ea = (int)((wa >> (8 * tg)) & 255u), ec = (int)((wc >> (8 * tg)) & 255u);
         int top = max(ea, ec);
         if (__any_sync(0xffffffffu, top > e_ref)) {
@@ -228,21 +254,23 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
           for (int b = 0; b < 4; ++b) {
             const float fb = __shfl_sync(0xffffffffu, f, b);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              o[b][i][0] *= fb; o[b][i][1] *= fb; o[b][i][2] *= fb; o[b][i][3] *= fb;
+            for (int x = 0; x < 2; ++x) {
+              o[b][x][0] *= fb; o[b][x][1] *= fb; o[b][x][2] *= fb; o[b][x][3] *= fb;
             }
           }
         }
-        // fp16 bits of 2^(d + 11), d = e - E: (d + 26) << 10, zero below
-        const uint32_t fa = (uint32_t)max(ea - e_ref + 26, 0), fc = (uint32_t)max(ec - e_ref + 26, 0);
-        sts32(wbuf + 4 * lane, (fa << 10) | (fc << 26));
+        // (fp16 holds 2^-24; below it the factor is 0)
+        const float fa = __int_as_float(max(127 + ea - e_ref, 64) << 23);
+        const float fc = __int_as_float(max(127 + ec - e_ref, 64) << 23);
+        sts32(wbuf + 4 * lane, Elem<__half>::from_f2(fa, fc));
       }
       // ---- S^T = K Q^T ----
       float s[4] = {0.f, 0.f, 0.f, 0.f};
+      const int ta = token_of(g);  // this lane's rows: tokens ta, ta + 8
       {
-        const int ta = token_of(g), tb = ta + 8;
-        const uint4 ka = lds128(st + code_at(ta, tg)), kb = lds128(st + code_at(tb, tg));
-        const uint32_t sa = lds32(k_sc + 4 * ta), sb = lds32(k_sc + 4 * tb);
+        const uint32_t at = st + code_at(ta, tg);
+        const uint4 ka = lds128(at), kb = lds128(at + 512);
+        const uint32_t sa = lds32(k_sc + 4 * ta), sb = lds32(k_sc + 4 * ta + 32);
         // words 0, 1: elements 0..3 of blocks (0, 1), (2, 3); words 2, 3: elements 4..7
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -268,12 +296,18 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             s[3] = fmaf(acc[3], fb, s[3]);
           }
         }
-        const uint2 takes_part = lds64(st + kValid);
-        const bool ok_a = (takes_part.x >> (4 * ta)) & 1u, ok_b = (takes_part.y >> (4 * ta)) & 1u;
-        s[0] = ok_a ? s[0] * sc0 : neg_inf();
-        s[1] = ok_a ? s[1] * sc1 : neg_inf();
-        s[2] = ok_b ? s[2] * sc0 : neg_inf();
-        s[3] = ok_b ? s[3] * sc1 : neg_inf();
+        s[0] *= sc0; s[1] *= sc1; s[2] *= sc0; s[3] *= sc1;
+        // tokens outside the chunk, or without a page, take no part
+        const int t_tile = (tile0 + j * wph) * kTile;
+        const uint32_t here = (uint32_t)(present >> (16 * (kStages - 1))) & 0xffffu;
+        if (here != 0xffffu || t_tile < it.kb || t_tile + kTile > it.ke) {  // warp-uniform
+          const bool ok_a = ((here >> ta) & 1u) && t_tile + ta >= it.kb && t_tile + ta < it.ke;
+          const bool ok_b = ((here >> (ta + 8)) & 1u) && t_tile + ta + 8 >= it.kb && t_tile + ta + 8 < it.ke;
+          s[0] = ok_a ? s[0] : neg_inf();
+          s[1] = ok_a ? s[1] : neg_inf();
+          s[2] = ok_b ? s[2] : neg_inf();
+          s[3] = ok_b ? s[3] : neg_inf();
+        }
       }
       // ---- online softmax, base 2, lazy reference ----
       float t0 = fmaxf(s[0], s[2]), t1 = fmaxf(s[1], s[3]);
@@ -289,31 +323,30 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         m1 = n1;
         l0 *= c0;
         l1 *= c1;
-        // rows g of O are head g: column g of the scores, held by lanes tg = g / 2
-        const float ca = __shfl_sync(0xffffffffu, c0, g >> 1), cb = __shfl_sync(0xffffffffu, c1, g >> 1);
-        const float c = (g & 1) ? cb : ca;
 #pragma unroll
         for (int b = 0; b < 4; ++b)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            o[b][i][0] *= c; o[b][i][1] *= c; o[b][i][2] *= c; o[b][i][3] *= c;
+          for (int x = 0; x < 2; ++x) {
+            o[b][x][0] *= c0; o[b][x][1] *= c1; o[b][x][2] *= c0; o[b][x][3] *= c1;
           }
       }
-      const float p0 = ex2(s[0] - m0), p1 = ex2(s[1] - m1), p2 = ex2(s[2] - m0), p3 = ex2(s[3] - m1);
+      const float p0 = ex2(s[0] - (m0 - kLift)), p1 = ex2(s[1] - (m1 - kLift));
+      const float p2 = ex2(s[2] - (m0 - kLift)), p3 = ex2(s[3] - (m1 - kLift));
       l0 += p0 + p2;
       l1 += p1 + p3;
+      // high part and remainder, transposed into B fragments (tokens x heads)
       const uint32_t h01 = Elem<__half>::from_f2(p0, p1), h23 = Elem<__half>::from_f2(p2, p3);
       const float2 f01 = Elem<__half>::to_f2(h01), f23 = Elem<__half>::to_f2(h23);
-      const uint32_t r01 = Elem<__half>::from_f2((p0 - f01.x) * 2048.f, (p1 - f01.y) * 2048.f);
-      const uint32_t r23 = Elem<__half>::from_f2((p2 - f23.x) * 2048.f, (p3 - f23.y) * 2048.f);
-      const uint32_t pa = movm_t(h01), pb = movm_t(r01), pc = movm_t(h23), pd = movm_t(r23);
+      const uint32_t r01 = Elem<__half>::from_f2(p0 - f01.x, p1 - f01.y);
+      const uint32_t r23 = Elem<__half>::from_f2(p2 - f23.x, p3 - f23.y);
+      const uint32_t pa = movm_t(h01), pb = movm_t(h23), ra = movm_t(r01), rb = movm_t(r23);
       __syncwarp();  // the factors are in shared memory
       const uint4 wlo = lds128(wbuf + 16 * tg), whi = lds128(wbuf + 64 + 16 * tg);
       const uint32_t fl[4] = {wlo.x, wlo.y, wlo.z, wlo.w}, fh[4] = {whi.x, whi.y, whi.z, whi.w};
-      // ---- O_b += (p 2^(e_b - E_b + 11)) V_b ----
+      // ---- O_b^T += V_b^T (p 2^(e_b - E_b)) ----
       const uint32_t vst = st + kCodes + 8 * (g & 1);
-      const uint2 v0 = lds64(vst + code_at(tg, g >> 1)), v1 = lds64(vst + code_at(tg + 4, g >> 1));
-      const uint2 v2 = lds64(vst + code_at(tg + 8, g >> 1)), v3 = lds64(vst + code_at(tg + 12, g >> 1));
+      const uint32_t va = vst + code_at(tg, g >> 1), vb = vst + code_at(tg + 4, g >> 1);
+      const uint2 v0 = lds64(va), v1 = lds64(vb), v2 = lds64(va + 512), v3 = lds64(vb + 512);
 #pragma unroll
       for (int half = 0; half < 2; ++half) {  // blocks 2 half, 2 half + 1
         const uint32_t x0 = half ? v0.y : v0.x, x1 = half ? v1.y : v1.x;
@@ -328,13 +361,17 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           const int b = 2 * half + x;
-          const uint32_t a[4] = {hmul2(pa, fl[b]), hmul2(pb, fl[b]), hmul2(pc, fh[b]), hmul2(pd, fh[b])};
-          mma16816<__half>(o[b][0], a, e02[2 * x], f02[2 * x]);
-          mma16816<__half>(o[b][1], a, e13[2 * x], f13[2 * x]);
-          mma16816<__half>(o[b][2], a, e02[2 * x + 1], f02[2 * x + 1]);
-          mma16816<__half>(o[b][3], a, e13[2 * x + 1], f13[2 * x + 1]);
+          const uint32_t hb0 = hmul2(pa, fl[b]), hb1 = hmul2(pb, fh[b]);
+          const uint32_t rb0 = hmul2(ra, fl[b]), rb1 = hmul2(rb, fh[b]);
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {  // elements 2 y (rows g), 2 y + 1 (rows g + 8)
+            const uint32_t a[4] = {e02[2 * x + y], e13[2 * x + y], f02[2 * x + y], f13[2 * x + y]};
+            mma16816<__half>(o[b][y], a, hb0, hb1);
+            mma16816<__half>(o[b][y], a, rb0, rb1);
+          }
         }
       }
+      st = st == ring + (kStages - 1) * kStage ? ring : st + kStage;
     }
     cp_async_wait<0>();
 
@@ -344,88 +381,68 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       l0 += __shfl_xor_sync(0xffffffffu, l0, x);
       l1 += __shfl_xor_sync(0xffffffffu, l1, x);
     }
-    // lane's head is g: its reference and sum, from a lane of columns g
-    const float ma = __shfl_sync(0xffffffffu, m0, g >> 1), mb = __shfl_sync(0xffffffffu, m1, g >> 1);
-    const float la = __shfl_sync(0xffffffffu, l0, g >> 1), lb = __shfl_sync(0xffffffffu, l1, g >> 1);
-    const float m = (g & 1) ? mb : ma, l = (g & 1) ? lb : la;
-    float val[4][8];  // dims 32 b + 8 tg + 0..7 of head g
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const float f = mx4_scale((uint32_t)__shfl_sync(0xffffffffu, e_ref, b));
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        val[b][i] = fmaf(o[b][i][2], 0x1p-11f, o[b][i][0]) * 0x1p-11f * f;
-        val[b][4 + i] = fmaf(o[b][i][3], 0x1p-11f, o[b][i][1]) * 0x1p-11f * f;
-      }
-    }
-    // 8 dims of one (item, head): the partial slot, or the final output
-    auto write8 = [&](int hq, int dim, const float (&v)[8]) {
+    // 4 dims of one (item, head): the partial slot, or the final output
+    auto write4 = [&](int hq, int dim, float4 v) {
       if (it.slot >= 0) {
-        float4* dst = reinterpret_cast<float4*>(p.part_o + ((int64_t)it.slot * p.hq + hq) * D + dim);
-        dst[0] = make_float4(v[0], v[1], v[2], v[3]);
-        dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+        *reinterpret_cast<float4*>(p.part_o + ((int64_t)it.slot * p.hq + hq) * D + dim) = v;
       } else {
         T* dst = static_cast<T*>(p.o_direct) + ((int64_t)it.req * p.hq + hq) * D + dim;
-        *reinterpret_cast<uint4*>(dst) = make_uint4(Elem<T>::from_f2(v[0], v[1]), Elem<T>::from_f2(v[2], v[3]),
-                                                    Elem<T>::from_f2(v[4], v[5]), Elem<T>::from_f2(v[6], v[7]));
+        *reinterpret_cast<uint2*>(dst) = make_uint2(Elem<T>::from_f2(v.x, v.y), Elem<T>::from_f2(v.z, v.w));
       }
     };
     auto write_lse = [&](int hq, float mm, float ll) {
-      const float lse = ll == 0.f ? neg_inf() : (mm + lg2(ll)) * kLn2;
+      const float lse = ll == 0.f ? neg_inf() : (mm - kLift + lg2(ll)) * kLn2;
       if (it.slot >= 0) p.part_lse[(int64_t)it.slot * p.hq + hq] = lse;
       else p.lse_direct[(int64_t)it.req * p.hq + hq] = lse;
     };
-    if (wph == 1) {
-      if (g < G) {
-        const float inv = l == 0.f ? 0.f : 1.f / l;  // (a NaN sum gives NaN)
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {
+    for (int e = 0; e < 2; ++e) {  // heads 2 tg, 2 tg + 1: dims 32 b + 4 g .. + 3
+      const int hd = 2 * tg + e;
+      const float m = e ? m1 : m0, l = e ? l1 : l0;
+      const float inv = wph > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;  // (a NaN sum gives NaN)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) val[b][i] *= inv;
-          write8(kvh * G + g, 32 * b + 8 * tg, val[b]);
+      for (int b = 0; b < 4; ++b) {
+        const float f = mx4_scale((uint32_t)__shfl_sync(0xffffffffu, e_ref, b)) * inv;
+        const float4 v = make_float4(o[b][0][e] * f, o[b][0][2 + e] * f, o[b][1][e] * f, o[b][1][2 + e] * f);
+        if (hd < G) {
+          if (wph == 1) write4(kvh * G + hd, 32 * b + 4 * g, v);
+          else *reinterpret_cast<float4*>(merge + (warp * G + hd) * kMergeRow + 32 * b + 4 * g) = v;
         }
-        if (tg == 0) write_lse(kvh * G + g, m, l);
       }
-      __syncthreads();  // every warp has read the item
-      if (warp == 0) fetch();
-      __syncthreads();
-      continue;
-    }
-    // Warps of one head: unnormalised values, reference and sum through
-    // shared memory, merged by half a warp per (KV head, query head) row.
-    if (g < G) {
-      float* dst = merge + (warp * G + g) * (D + 2);
-#pragma unroll
-      for (int b = 0; b < 4; ++b)
-#pragma unroll
-        for (int i = 0; i < 8; i += 2)
-          *reinterpret_cast<float2*>(dst + 32 * b + 8 * tg + i) = make_float2(val[b][i], val[b][i + 1]);
-      if (tg == 0) {
-        dst[D] = m;
-        dst[D + 1] = l;
+      if (hd < G && g == 0) {
+        if (wph == 1) {
+          write_lse(kvh * G + hd, m, l);
+        } else {
+          merge[(warp * G + hd) * kMergeRow + D] = m;
+          merge[(warp * G + hd) * kMergeRow + D + 1] = l;
+        }
       }
     }
-    __syncthreads();
+    __syncthreads();  // every warp has read the item and written its state
     if (warp == 0) fetch();
-    for (int r = 2 * warp + (lane >> 4); r < HG * G; r += 2 * kWarps) {  // 8 dims per lane
-      const int h = r / G, hd = r - h * G, dim = 8 * (lane & 15);
-      float mm = kRefFloor, ll = 0.f, acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      for (int c = 0; c < wph; ++c) mm = fmaxf(mm, merge[((h + HG * c) * G + hd) * (D + 2) + D]);
-      for (int c = 0; c < wph; ++c) {
-        const float* src = merge + ((h + HG * c) * G + hd) * (D + 2);
-        const float w = ex2(src[D] - mm);
-        ll = fmaf(src[D + 1], w, ll);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) acc[i] = fmaf(src[dim + i], w, acc[i]);
+    if (wph > 1) {
+      // Warps of one head: unnormalised values, reference and sum, merged by a
+      // warp per (KV head, query head) row, 4 dims per lane.
+      for (int r = warp; r < HG * G; r += kWarps) {
+        const int h = r / G, hd = r - h * G;
+        float mm = kRefFloor, ll = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = 0; c < wph; ++c) mm = fmaxf(mm, merge[((h + HG * c) * G + hd) * kMergeRow + D]);
+        for (int c = 0; c < wph; ++c) {
+          const float* src = merge + ((h + HG * c) * G + hd) * kMergeRow;
+          const float w = ex2(src[D] - mm);
+          ll = fmaf(src[D + 1], w, ll);
+          const float4 v = *reinterpret_cast<const float4*>(src + 4 * lane);
+          acc.x = fmaf(v.x, w, acc.x); acc.y = fmaf(v.y, w, acc.y);
+          acc.z = fmaf(v.z, w, acc.z); acc.w = fmaf(v.w, w, acc.w);
+        }
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+        const int hq = (it.hg * HG + h) * G + hd;
+        write4(hq, 4 * lane, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+        if (lane == 0) write_lse(hq, mm, ll);
       }
-      const float inv = ll == 0.f ? 0.f : 1.f / ll;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc[i] *= inv;
-      const int hq = (it.hg * HG + h) * G + hd;
-      write8(hq, dim, acc);
-      if ((lane & 15) == 0) write_lse(hq, mm, ll);
     }
-    __syncthreads();  // the merge buffer and the item are free
+    __syncthreads();  // the next item is there; the merge buffer is free
   }
   if (dyn && warp == 0) queue.finish(lane);
 }
@@ -435,10 +452,10 @@ int launch_g(const Mx4DecodeParams& p, dim3 grid, cudaStream_t st) {
   constexpr int smem = smem_bytes<G>();
   static_assert(kBlocksPerSm * (smem + 1024) <= 228 * 1024, "resident blocks");
   // (an attribute of the current device: set on every call, it is cheap)
-  const cudaError_t e = cudaFuncSetAttribute(paged_decode_mx4_kernel<T, G>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  auto kernel = p.d.page_size % kTile == 0 ? paged_decode_mx4_kernel<T, G, true> : paged_decode_mx4_kernel<T, G, false>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return (int)e;
-  paged_decode_mx4_kernel<T, G><<<grid, kThreads, smem, st>>>(p);
+  kernel<<<grid, kThreads, smem, st>>>(p);
   return (int)cudaGetLastError();
 }
 
@@ -461,10 +478,10 @@ int launch_paged_decode_mx4(const Mx4DecodeParams& p_in, int n_work, int dtype, 
   p.d.sched = p.d.status + 16;
   const int hkv = p.d.hkv;
   p.hg = hkv % 4 == 0 ? 4 : hkv % 2 == 0 ? 2 : 1;
-  // Fewer heads per block (more warps per head) while the items leave SMs
-  // without a block: a small batch's time is that of one warp's tiles.
+  // Fewer heads per block (more warps per head) while the items leave room
+  // for more blocks: a small batch's time is that of one warp's tiles.
   const int64_t items = p.d.plan ? n_work : p.d.batch;
-  while (p.hg > 1 && items * (hkv / p.hg) < num_sms()) p.hg /= 2;
+  while (p.hg > 1 && items * (hkv / p.hg) < kBlocksPerSm * (int64_t)num_sms()) p.hg /= 2;
   dim3 grid;
   if (p.d.dynamic) {
     const int64_t n = items * (hkv / p.hg), most = kBlocksPerSm * (int64_t)num_sms();

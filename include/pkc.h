@@ -565,8 +565,8 @@ int pkc_gather_kv_mx4(const void* k_codes, const void* k_scales,
 /*
  * pkc_paged_decode_state over an mx4 cache: the same states, plan, workspace
  * and status codes, with q and o of dtype (F16 or BF16), any page size and
- * any number of KV heads.  Split requests are always joined by the
- * standalone contraction kernel.  Accuracy beyond the format's: the scores
+ * any number of KV heads.  Split requests are joined by a kernel of its own
+ * (pkc_set_contraction does not apply).  Accuracy beyond the format's: the scores
  * are those of the cached values with float32 sums; probabilities enter the
  * V product with 22 bits, and a value below 2^-24 of the largest cached
  * |V| of its block of dims may count as zero.  A page id < 0 or >= num_pages

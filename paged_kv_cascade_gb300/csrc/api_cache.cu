@@ -150,15 +150,17 @@ int pkc_paged_decode_state_mx4(const void* q, const void* k_codes, const void* k
   int e = launch_paged_decode_mx4(mp, plan_host ? plan_host[PKC_PLAN_N_WORK] : 0, dtype, stream);
   if (e) return cuda_error(e, "paged_decode_state_mx4 launch");
   if (plan_host) {  // split requests' partial states (+) into the output
-    ContractParams cp;
-    std::memset(&cp, 0, sizeof(cp));
-    cp.batch = batch; cp.hq = num_qo_heads; cp.mode = kContractPlanUnits; cp.plan = dp.plan;
-    cp.hkv = num_kv_heads; cp.g = num_qo_heads / num_kv_heads;
-    contract_plan_offsets(cp, plan_host);
-    cp.part_o = dp.part_o; cp.part_lse = dp.part_lse;
-    cp.o = o; cp.lse = lse; cp.out_dtype = dtype; cp.status = dp.status;
-    e = launch_contract(cp, batch, stream, true);
-    if (e) return cuda_error(e, "contraction launch");
+    Mx4JoinParams jp;
+    std::memset(&jp, 0, sizeof(jp));
+    jp.plan = dp.plan; jp.plan_words = dp.plan_words;
+    jp.off_unit_list = plan_host[PKC_PLAN_OFF_UNIT_LIST]; jp.off_unit_req = plan_host[PKC_PLAN_OFF_UNIT_REQ];
+    jp.off_unit_n_chunks = plan_host[PKC_PLAN_OFF_UNIT_N_CHUNKS];
+    jp.off_unit_partial_begin = plan_host[PKC_PLAN_OFF_UNIT_PARTIAL_BEGIN];
+    jp.batch = batch; jp.hq = num_qo_heads;
+    jp.part_o = dp.part_o; jp.part_lse = dp.part_lse;
+    jp.o = o; jp.lse = lse;
+    e = launch_join_mx4(jp, plan_host[PKC_PLAN_N_SPLIT] + plan_host[PKC_PLAN_N_EMPTY], dtype, stream);
+    if (e) return cuda_error(e, "paged_decode_state_mx4 join launch");
   }
   return PKC_OK;
 }

@@ -49,7 +49,7 @@ constexpr int kCodes = kTile * kMx4RowBytes;  // K (or V) code bytes per stage
 constexpr int kScales = kTile * 4;
 constexpr int kStage = 2 * (kCodes + kScales);
 constexpr int kRing = kStages * kStage;       // per warp
-constexpr int kWarpSmem = kRing + 128;        // + the tile's probability factors
+constexpr int kWarpSmem = kRing + 128 + 256;  // + the tile's probability factors and key scales
 constexpr float kRefFloor = -3e38f;           // softmax reference before the first token
 constexpr float kLazy = 4.f;                  // log2 of the largest probability between rescales
 constexpr float kLift = 11.f;                 // probabilities are held times 2^kLift: at most 2^15
@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   Item* item_s = reinterpret_cast<Item*>(smem + kWarps * kWarpSmem);
   float* merge = reinterpret_cast<float*>(smem + kWarps * kWarpSmem + 64);
   const uint32_t ring = smem_u32(smem) + warp * kWarpSmem;
-  const uint32_t wbuf = ring + kRing;
+  const uint32_t wbuf = ring + kRing, kbuf = wbuf + 128;
   const int HG = mp.hg, wph = kWarps / HG;
   const int hh = warp % HG, cls = warp / HG;
   const PageDiv pages{p.page_size, mp.page_shift};
@@ -187,42 +187,56 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     const uint8_t* v_lane = static_cast<const uint8_t*>(p.v_cache) + kvh * kMx4RowBytes + 16 * tg;
     const uint8_t* s_lane = static_cast<const uint8_t*>(lane < 16 ? mp.k_scales : mp.v_scales) + kvh * 4;
     const uint32_t code_stride = (uint32_t)p.hkv * kMx4RowBytes, scale_stride = (uint32_t)p.hkv * 4;
+    const uint64_t code_8 = (uint64_t)code_stride * 8;  // from token t to token t + 8 of a page
     uint32_t st_in = ring;  // stage of the next tile to be copied
-    uint64_t present = 0;   // 16 bits per tile in flight: its tokens that are there (latest in the low bits)
+    // Tokens that are there, of the tiles in flight, the latest in the low
+    // bits: one bit per tile (aligned), or 16.
+    using Present = std::conditional_t<kAligned, uint32_t, uint64_t>;
+    constexpr int kPresentBits = kAligned ? 1 : 16;
+    Present present = 0;
     auto issue = [&](int j) {  // copies of tile j (an empty group past the last one)
-      present <<= 16;
+      present <<= kPresentBits;
       if (j < mine) {
-        uint32_t ta, tb, ts;  // pool indices of tokens g, g + 8, lane % 16
+        const uint32_t dst = st_in + code_at(g, tg);
+        const uint32_t dst_s = st_in + 2 * kCodes + 4 * lane;  // scales: lanes 0..15 K, 16..31 V, token lane % 16
         if constexpr (kAligned) {
           if ((j & 31) == 0 && j > 0) {
             win = win_next;
             win_next = load_window(j + 32);
           }
           const uint32_t first = __shfl_sync(0xffffffffu, win, j & 31);
-          const bool there = first != kNoToken;
-          present |= there ? 0xffffu : 0u;
-          ta = there ? first + g : kNoToken;
-          tb = there ? first + g + 8 : kNoToken;
-          // scales of slots outside the chunk become 0: whatever they hold
-          // must not count among the largest
-          const int t = (tile0 + j * wph) * kTile + (lane & 15);
-          ts = there && t >= it.kb && t < it.ke ? first + (lane & 15) : kNoToken;
+          if (first != kNoToken) {
+            present |= 1u;
+            const uint64_t at = (uint64_t)(first + g) * code_stride;
+            const uint8_t *ks = k_lane + at, *vs = v_lane + at;
+            cp_async16(dst, ks, true);
+            cp_async16(dst + 512, ks + code_8, true);
+            cp_async16(dst + kCodes, vs, true);
+            cp_async16(dst + kCodes + 512, vs + code_8, true);
+            // scales of slots outside the chunk become 0: whatever they hold
+            // must not count among the largest
+            const int t = (tile0 + j * wph) * kTile + (lane & 15);
+            cp_async4(dst_s, s_lane + (uint64_t)(first + (lane & 15)) * scale_stride, t >= it.kb && t < it.ke);
+          } else {  // no such page: zeros
+            cp_async16(dst, k_lane, false);
+            cp_async16(dst + 512, k_lane, false);
+            cp_async16(dst + kCodes, v_lane, false);
+            cp_async16(dst + kCodes + 512, v_lane, false);
+            cp_async4(dst_s, s_lane, false);
+          }
         } else {
-          ts = win;
+          const uint32_t ts = win;
           present |= __ballot_sync(0xffffffffu, ts != kNoToken) & 0xffffu;
-          ta = __shfl_sync(0xffffffffu, ts, g);
-          tb = __shfl_sync(0xffffffffu, ts, g + 8);
+          const uint32_t ta = __shfl_sync(0xffffffffu, ts, g), tb = __shfl_sync(0xffffffffu, ts, g + 8);
           win = load_tokens(j + 1);
+          const bool oka = ta != kNoToken, okb = tb != kNoToken, oks = ts != kNoToken;
+          const uint64_t at_a = oka ? (uint64_t)ta * code_stride : 0u, at_b = okb ? (uint64_t)tb * code_stride : 0u;
+          cp_async16(dst, k_lane + at_a, oka);
+          cp_async16(dst + 512, k_lane + at_b, okb);
+          cp_async16(dst + kCodes, v_lane + at_a, oka);
+          cp_async16(dst + kCodes + 512, v_lane + at_b, okb);
+          cp_async4(dst_s, s_lane + (oks ? (uint64_t)ts * scale_stride : 0u), oks);
         }
-        const uint32_t dst = st_in + code_at(g, tg);
-        const bool oka = ta != kNoToken, okb = tb != kNoToken, oks = ts != kNoToken;
-        const uint64_t at_a = oka ? (uint64_t)ta * code_stride : 0u, at_b = okb ? (uint64_t)tb * code_stride : 0u;
-        cp_async16(dst, k_lane + at_a, oka);
-        cp_async16(dst + 512, k_lane + at_b, okb);
-        cp_async16(dst + kCodes, v_lane + at_a, oka);
-        cp_async16(dst + kCodes + 512, v_lane + at_b, okb);
-        // scales: lanes 0..15 K, 16..31 V, token lane % 16
-        cp_async4(st_in + 2 * kCodes + 4 * lane, s_lane + (oks ? (uint64_t)ts * scale_stride : 0u), oks);
       }
       cp_async_commit();
       st_in = st_in == ring + (kStages - 1) * kStage ? ring : st_in + kStage;
@@ -235,11 +249,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       cp_async_wait<kStages - 2>();
       __syncwarp();  // tile j is in shared memory; tile j - 1's stage is free
       issue(j + kStages - 1);
-      const uint32_t k_sc = st + 2 * kCodes, v_sc = k_sc + kScales;
-      // ---- this tile's probability factors 2^(e - E) ----
+      const uint32_t v_sc = st + 2 * kCodes + kScales;
+      // ---- this tile's key scales and probability factors 2^(e - E) ----
       // lane 4 x + b: block b of tokens token_of(2 x), token_of(2 x + 1)
       {
         const uint32_t at = v_sc + 4 * token_of(2 * g);
+        const uint32_t ya = lds32(at - kScales), yc = lds32(at - kScales + 16);
+        // (255: an infinity, NaN on the zero codes it comes with)
+        sts32(kbuf + 16 * token_of(2 * g) + 4 * tg, ((ya >> (8 * tg)) << 23) & 0x7f800000u);
+        sts32(kbuf + 16 * token_of(2 * g) + 64 + 4 * tg, ((yc >> (8 * tg)) << 23) & 0x7f800000u);
         const uint32_t wa = lds32(at), wc = lds32(at + 16);
         const int ea = (int)((wa >> (8 * tg)) & 255u), ec = (int)((wc >> (8 * tg)) & 255u);
         int top = max(ea, ec);
@@ -264,13 +282,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         const float fc = __int_as_float(max(127 + ec - e_ref, 64) << 23);
         sts32(wbuf + 4 * lane, Elem<__half>::from_f2(fa, fc));
       }
+      __syncwarp();
       // ---- S^T = K Q^T ----
       float s[4] = {0.f, 0.f, 0.f, 0.f};
       const int ta = token_of(g);  // this lane's rows: tokens ta, ta + 8
       {
         const uint32_t at = st + code_at(ta, tg);
         const uint4 ka = lds128(at), kb = lds128(at + 512);
-        const uint32_t sa = lds32(k_sc + 4 * ta), sb = lds32(k_sc + 4 * ta + 32);
+        const uint4 fa = lds128(kbuf + 16 * ta), fb = lds128(kbuf + 16 * ta + 128);
+        const uint32_t fka[4] = {fa.x, fa.y, fa.z, fa.w}, fkb[4] = {fb.x, fb.y, fb.z, fb.w};
         // words 0, 1: elements 0..3 of blocks (0, 1), (2, 3); words 2, 3: elements 4..7
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -287,19 +307,18 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             mma16816<__half>(acc, f0, qf[b][0], qf[b][1]);
             const uint32_t f1[4] = {a1[2 * x], c1[2 * x], a1[2 * x + 1], c1[2 * x + 1]};
             mma16816<__half>(acc, f1, qf[b][2], qf[b][3]);
-            // (255: an infinity, NaN on the zero codes it comes with)
-            const float fa = __uint_as_float((b < 3 ? sa << (23 - 8 * b) : sa >> 1) & 0x7f800000u);
-            const float fb = __uint_as_float((b < 3 ? sb << (23 - 8 * b) : sb >> 1) & 0x7f800000u);
-            s[0] = fmaf(acc[0], fa, s[0]);
-            s[1] = fmaf(acc[1], fa, s[1]);
-            s[2] = fmaf(acc[2], fb, s[2]);
-            s[3] = fmaf(acc[3], fb, s[3]);
+            s[0] = fmaf(acc[0], __uint_as_float(fka[b]), s[0]);
+            s[1] = fmaf(acc[1], __uint_as_float(fka[b]), s[1]);
+            s[2] = fmaf(acc[2], __uint_as_float(fkb[b]), s[2]);
+            s[3] = fmaf(acc[3], __uint_as_float(fkb[b]), s[3]);
           }
         }
         s[0] *= sc0; s[1] *= sc1; s[2] *= sc0; s[3] *= sc1;
         // tokens outside the chunk, or without a page, take no part
         const int t_tile = (tile0 + j * wph) * kTile;
-        const uint32_t here = (uint32_t)(present >> (16 * (kStages - 1))) & 0xffffu;
+        uint32_t here;  // one bit per token
+        if constexpr (kAligned) here = (present & (1u << (kStages - 1))) ? 0xffffu : 0u;
+        else here = (uint32_t)(present >> (16 * (kStages - 1))) & 0xffffu;
         if (here != 0xffffu || t_tile < it.kb || t_tile + kTile > it.ke) {  // warp-uniform
           const bool ok_a = ((here >> ta) & 1u) && t_tile + ta >= it.kb && t_tile + ta < it.ke;
           const bool ok_b = ((here >> (ta + 8)) & 1u) && t_tile + ta + 8 >= it.kb && t_tile + ta + 8 < it.ke;
@@ -340,7 +359,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       const uint32_t r01 = Elem<__half>::from_f2(p0 - f01.x, p1 - f01.y);
       const uint32_t r23 = Elem<__half>::from_f2(p2 - f23.x, p3 - f23.y);
       const uint32_t pa = movm_t(h01), pb = movm_t(h23), ra = movm_t(r01), rb = movm_t(r23);
-      __syncwarp();  // the factors are in shared memory
       const uint4 wlo = lds128(wbuf + 16 * tg), whi = lds128(wbuf + 64 + 16 * tg);
       const uint32_t fl[4] = {wlo.x, wlo.y, wlo.z, wlo.w}, fh[4] = {whi.x, whi.y, whi.z, whi.w};
       // ---- O_b^T += V_b^T (p 2^(e_b - E_b)) ----
@@ -447,6 +465,56 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   if (dyn && warp == 0) queue.finish(lane);
 }
 
+// The join of split requests: one block per (request, query head), its warps
+// taking every kWarps-th of the request's chunk states, lane i dims 4 i ..
+// + 3; then the warps' sums through shared memory.  The states are few per
+// row or many (a long request alone on the machine has one per CTA), and all
+// loads of a row are in flight together.  An empty request's row is (0, -inf).
+template <typename T>
+__global__ void __launch_bounds__(kThreads) join_mx4_kernel(const __grid_constant__ Mx4JoinParams p) {
+  __shared__ float4 part[kWarps][32];
+  __shared__ float part_l[kWarps];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = (int)(blockIdx.x / (unsigned)p.hq), hq = (int)(blockIdx.x % (unsigned)p.hq);
+  const int32_t* pl = p.plan;
+  grid_wait_prerequisites();  // the decode grid's states
+  if (!device_plan_ok(pl, p.plan_words, p.batch)) return;  // (reported by the decode)
+  const int unit = pl[p.off_unit_list + row];
+  const int n = pl[p.off_unit_n_chunks + unit], first = pl[p.off_unit_partial_begin + unit];
+  const int req = pl[p.off_unit_req + unit];
+  const int64_t base = (int64_t)first * p.hq + hq;  // state c at base + c hq
+  float m = neg_inf();
+  for (int c = lane; c < n; c += 32) m = fmaxf(m, p.part_lse[base + (int64_t)c * p.hq]);
+#pragma unroll
+  for (int x = 1; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+  const float ref = m == neg_inf() ? 0.f : m;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float l = 0.f;
+#pragma unroll 8
+  for (int c = warp; c < n; c += kWarps) {
+    const int64_t at = base + (int64_t)c * p.hq;
+    const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * D + 4 * lane);
+    const float w = ex2((p.part_lse[at] - ref) * kLog2e);
+    l += w;
+    acc.x = fmaf(v.x, w, acc.x); acc.y = fmaf(v.y, w, acc.y);
+    acc.z = fmaf(v.z, w, acc.z); acc.w = fmaf(v.w, w, acc.w);
+  }
+  part[warp][lane] = acc;
+  if (lane == 0) part_l[warp] = l;
+  __syncthreads();
+  if (warp != 0) return;
+  for (int x = 1; x < kWarps; ++x) {
+    const float4 v = part[x][lane];
+    acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+    l += part_l[x];
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  T* dst = static_cast<T*>(p.o) + ((int64_t)req * p.hq + hq) * D + 4 * lane;
+  *reinterpret_cast<uint2*>(dst) =
+      make_uint2(Elem<T>::from_f2(acc.x * inv, acc.y * inv), Elem<T>::from_f2(acc.z * inv, acc.w * inv));
+  if (lane == 0) p.lse[(int64_t)req * p.hq + hq] = l == 0.f ? neg_inf() : ref + lg2(l) * kLn2;
+}
+
 template <typename T, int G>
 int launch_g(const Mx4DecodeParams& p, dim3 grid, cudaStream_t st) {
   constexpr int smem = smem_bytes<G>();
@@ -491,6 +559,18 @@ int launch_paged_decode_mx4(const Mx4DecodeParams& p_in, int n_work, int dtype, 
   }
   cudaStream_t st = (cudaStream_t)stream;
   return dtype == PKC_BF16 ? launch_t<__nv_bfloat16>(p, grid, st) : launch_t<__half>(p, grid, st);
+}
+
+int launch_join_mx4(const Mx4JoinParams& p, int n_rows, int dtype, void* stream) {
+  const int64_t blocks = (int64_t)n_rows * p.hq;
+  if (blocks <= 0) return 0;
+  if (blocks > INT32_MAX) return (int)cudaErrorInvalidValue;
+  // the decode's programmatic dependent: its blocks start as the decode's end
+  return dtype == PKC_BF16
+             ? launch_programmatic(join_mx4_kernel<__nv_bfloat16>, dim3((unsigned)blocks), dim3(kThreads), 0,
+                                   (cudaStream_t)stream, p)
+             : launch_programmatic(join_mx4_kernel<__half>, dim3((unsigned)blocks), dim3(kThreads), 0,
+                                   (cudaStream_t)stream, p);
 }
 
 }  // namespace pkc

@@ -254,6 +254,17 @@ struct Mx4DecodeParams {
   int num_ctas;            // CTAs of the plan (static schedule)
 };
 
+// The join of a planned mx4 decode's split requests.
+struct Mx4JoinParams {
+  const int32_t* plan;     // device
+  int32_t plan_words, off_unit_list, off_unit_req, off_unit_n_chunks, off_unit_partial_begin;
+  int batch, hq;
+  const float* part_o;     // [slot, hq, 128]
+  const float* part_lse;   // [slot, hq]
+  void* o;                 // [batch, hq, 128] 16-bit
+  float* lse;
+};
+
 // Accumulated attention weights (weights.cu).
 struct WeightsParams {
   const void* q;             // [batch, hkv * g, 128]
@@ -303,6 +314,8 @@ int launch_evict_compact(const CompactParams& p, void* stream);
 int launch_weights(const WeightsParams& p, int q_dtype, int kv_dtype, void* stream);
 int launch_append_mx4(const Mx4RowsParams& p, int dtype, void* stream);
 int launch_gather_mx4(const Mx4RowsParams& p, int dtype, void* stream);
+// n_rows: the plan's split and empty requests
+int launch_join_mx4(const Mx4JoinParams& p, int n_rows, int dtype, void* stream);
 // n_work: chunks of the plan (0 without one)
 int launch_paged_decode_mx4(const Mx4DecodeParams& p, int n_work, int dtype, void* stream);
 int launch_merge_state(const void* va, const float* sa, const void* vb,

@@ -75,6 +75,13 @@ __device__ __forceinline__ uint32_t code_at(int t, int c) {
 // Token of tile row r: rows 2 x, 2 x + 1 hold tokens x, x + 4 (of each 8).
 __device__ __forceinline__ int token_of(int r) { return (r & 8) + ((r & 7) >> 1) + 4 * (r & 1); }
 
+// base + row * stride in one wide multiply-add.
+__device__ __forceinline__ const uint8_t* at_row(const uint8_t* base, uint32_t row, uint32_t stride) {
+  uint64_t d;
+  asm("mad.wide.u32 %0, %1, %2, %3;" : "=l"(d) : "r"(row), "r"(stride), "l"(base));
+  return reinterpret_cast<const uint8_t*>(d);
+}
+
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -86,6 +93,9 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 template <typename T, int G, bool kAligned>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     paged_decode_mx4_kernel(const __grid_constant__ Mx4DecodeParams mp) {
+  // With at most 4 query heads per KV head the tile's other 4 columns take
+  // the probabilities' remainders, at no cost.
+  constexpr bool kFold = G <= 4;
   const DecodeParams& p = mp.d;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -168,7 +178,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     uint32_t win_next = kAligned ? load_window(32) : 0u;
 
     uint32_t qf[4][4];
-    const float q_undo = load_q_f16<T, G>(
+    const float q_undo = load_q_f16<T, G, kFold>(
         static_cast<const T*>(p.q) + ((int64_t)it.req * p.hq + (int64_t)kvh * G) * D, lane, qf);
     // factors of this lane's score columns (heads 2 tg, 2 tg + 1), base 2
     const float sc0 = p.scale_log2 * __shfl_sync(0xffffffffu, q_undo, 8 * tg);
@@ -187,7 +197,6 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     const uint8_t* v_lane = static_cast<const uint8_t*>(p.v_cache) + kvh * kMx4RowBytes + 16 * tg;
     const uint8_t* s_lane = static_cast<const uint8_t*>(lane < 16 ? mp.k_scales : mp.v_scales) + kvh * 4;
     const uint32_t code_stride = (uint32_t)p.hkv * kMx4RowBytes, scale_stride = (uint32_t)p.hkv * 4;
-    const uint64_t code_8 = (uint64_t)code_stride * 8;  // from token t to token t + 8 of a page
     uint32_t st_in = ring;  // stage of the next tile to be copied
     // Tokens that are there, of the tiles in flight, the latest in the low
     // bits: one bit per tile (aligned), or 16.
@@ -207,16 +216,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
           const uint32_t first = __shfl_sync(0xffffffffu, win, j & 31);
           if (first != kNoToken) {
             present |= 1u;
-            const uint64_t at = (uint64_t)(first + g) * code_stride;
-            const uint8_t *ks = k_lane + at, *vs = v_lane + at;
-            cp_async16(dst, ks, true);
-            cp_async16(dst + 512, ks + code_8, true);
-            cp_async16(dst + kCodes, vs, true);
-            cp_async16(dst + kCodes + 512, vs + code_8, true);
+            const uint32_t ta = first + g, tb = ta + 8;
+            cp_async16(dst, at_row(k_lane, ta, code_stride), true);
+            cp_async16(dst + 512, at_row(k_lane, tb, code_stride), true);
+            cp_async16(dst + kCodes, at_row(v_lane, ta, code_stride), true);
+            cp_async16(dst + kCodes + 512, at_row(v_lane, tb, code_stride), true);
             // scales of slots outside the chunk become 0: whatever they hold
             // must not count among the largest
             const int t = (tile0 + j * wph) * kTile + (lane & 15);
-            cp_async4(dst_s, s_lane + (uint64_t)(first + (lane & 15)) * scale_stride, t >= it.kb && t < it.ke);
+            cp_async4(dst_s, at_row(s_lane, first + (lane & 15), scale_stride), t >= it.kb && t < it.ke);
           } else {  // no such page: zeros
             cp_async16(dst, k_lane, false);
             cp_async16(dst + 512, k_lane, false);
@@ -244,6 +252,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 #pragma unroll
     for (int s = 0; s < kStages - 1; ++s) issue(s);
 
+    // Tiles whose 16 tokens all belong to the chunk: j - whole_lo < n_whole.
+    const int whole_lo = (it.kb & 15) && cls == 0 ? 1 : 0;
+    const int whole_hi = mine - ((it.ke & 15) && tile0 + (mine - 1) * wph == (it.ke >> 4) ? 1 : 0);
+    const uint32_t n_whole = (uint32_t)max(whole_hi - whole_lo, 0);
     uint32_t st = ring;
     for (int j = 0; j < mine; ++j) {
       cp_async_wait<kStages - 2>();
@@ -315,11 +327,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         }
         s[0] *= sc0; s[1] *= sc1; s[2] *= sc0; s[3] *= sc1;
         // tokens outside the chunk, or without a page, take no part
-        const int t_tile = (tile0 + j * wph) * kTile;
         uint32_t here;  // one bit per token
         if constexpr (kAligned) here = (present & (1u << (kStages - 1))) ? 0xffffu : 0u;
         else here = (uint32_t)(present >> (16 * (kStages - 1))) & 0xffffu;
-        if (here != 0xffffu || t_tile < it.kb || t_tile + kTile > it.ke) {  // warp-uniform
+        if (here != 0xffffu || (uint32_t)(j - whole_lo) >= n_whole) {  // warp-uniform
+          const int t_tile = (tile0 + j * wph) * kTile;
           const bool ok_a = ((here >> ta) & 1u) && t_tile + ta >= it.kb && t_tile + ta < it.ke;
           const bool ok_b = ((here >> (ta + 8)) & 1u) && t_tile + ta + 8 >= it.kb && t_tile + ta + 8 < it.ke;
           s[0] = ok_a ? s[0] : neg_inf();
@@ -358,7 +370,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       const float2 f01 = Elem<__half>::to_f2(h01), f23 = Elem<__half>::to_f2(h23);
       const uint32_t r01 = Elem<__half>::from_f2(p0 - f01.x, p1 - f01.y);
       const uint32_t r23 = Elem<__half>::from_f2(p2 - f23.x, p3 - f23.y);
-      const uint32_t pa = movm_t(h01), pb = movm_t(h23), ra = movm_t(r01), rb = movm_t(r23);
+      // (kFold: columns 4 .. 7 repeat heads 0 .. 3 and carry the remainders)
+      const bool rest = kFold && tg >= 2;
+      const uint32_t pa = movm_t(rest ? r01 : h01), pb = movm_t(rest ? r23 : h23);
+      const uint32_t ra = kFold ? 0u : movm_t(r01), rb = kFold ? 0u : movm_t(r23);
       const uint4 wlo = lds128(wbuf + 16 * tg), whi = lds128(wbuf + 64 + 16 * tg);
       const uint32_t fl[4] = {wlo.x, wlo.y, wlo.z, wlo.w}, fh[4] = {whi.x, whi.y, whi.z, whi.w};
       // ---- O_b^T += V_b^T (p 2^(e_b - E_b)) ----
@@ -380,12 +395,16 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         for (int x = 0; x < 2; ++x) {
           const int b = 2 * half + x;
           const uint32_t hb0 = hmul2(pa, fl[b]), hb1 = hmul2(pb, fh[b]);
-          const uint32_t rb0 = hmul2(ra, fl[b]), rb1 = hmul2(rb, fh[b]);
+          uint32_t rb0 = 0, rb1 = 0;
+          if constexpr (!kFold) {
+            rb0 = hmul2(ra, fl[b]);
+            rb1 = hmul2(rb, fh[b]);
+          }
 #pragma unroll
           for (int y = 0; y < 2; ++y) {  // elements 2 y (rows g), 2 y + 1 (rows g + 8)
             const uint32_t a[4] = {e02[2 * x + y], e13[2 * x + y], f02[2 * x + y], f13[2 * x + y]};
             mma16816<__half>(o[b][y], a, hb0, hb1);
-            mma16816<__half>(o[b][y], a, rb0, rb1);
+            if constexpr (!kFold) mma16816<__half>(o[b][y], a, rb0, rb1);
           }
         }
       }
@@ -398,6 +417,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     for (int x = 4; x < 32; x <<= 1) {
       l0 += __shfl_xor_sync(0xffffffffu, l0, x);
       l1 += __shfl_xor_sync(0xffffffffu, l1, x);
+    }
+    if constexpr (kFold) {  // high parts (lanes tg < 2) + remainders (tg >= 2): both get the sum
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[b][x][i] += __shfl_xor_sync(0xffffffffu, o[b][x][i], 2);
     }
     // 4 dims of one (item, head): the partial slot, or the final output
     auto write4 = [&](int hq, int dim, float4 v) {
@@ -549,11 +576,17 @@ int launch_paged_decode_mx4(const Mx4DecodeParams& p_in, int n_work, int dtype, 
   // Fewer heads per block (more warps per head) while the items leave room
   // for more blocks: a small batch's time is that of one warp's tiles.
   const int64_t items = p.d.plan ? n_work : p.d.batch;
-  while (p.hg > 1 && items * (hkv / p.hg) < kBlocksPerSm * (int64_t)num_sms()) p.hg /= 2;
+  // Two heads also where four would give fewer than two items a block: half
+  // the item balances better (GQA batch of 256, 1000 items of four heads: 147
+  // -> 136 us), while one head per block costs more merging than it gains
+  // where two fill the machine (two long requests: 54 -> 59 us).
+  const int64_t slots = kBlocksPerSm * (int64_t)num_sms();
+  if (p.hg == 4 && items * (hkv / 4) < 2 * slots) p.hg = 2;
+  while (p.hg > 1 && items * (hkv / p.hg) < slots) p.hg /= 2;
   dim3 grid;
   if (p.d.dynamic) {
-    const int64_t n = items * (hkv / p.hg), most = kBlocksPerSm * (int64_t)num_sms();
-    grid = dim3((unsigned)(n < 1 ? 1 : n < most ? n : most));
+    const int64_t n = items * (hkv / p.hg);
+    grid = dim3((unsigned)(n < 1 ? 1 : n < slots ? n : slots));
   } else {
     grid = dim3((unsigned)(p.d.plan ? p.num_ctas : p.d.batch), (unsigned)(hkv / p.hg));
   }

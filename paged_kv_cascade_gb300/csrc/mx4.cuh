@@ -89,14 +89,14 @@ __device__ __forceinline__ uint2 lds64(uint32_t addr) {
 // Query fragments (B operand of m16n8k16, n = query head lane / 4) for
 // products with 4-bit or 8-bit keys, whose fragments are fp16: qf[b][k] are
 // elements 32 b + 8 (lane % 4) + 2 k, + 1 of head lane / 4 (zero for heads
-// >= G).  fp16 queries are used as they are.  A bf16 row is scaled by the
+// >= G; kRepeat, G <= 4: heads 4 .. 7 repeat 0 .. 3).  fp16 queries are used as they are.  A bf16 row is scaled by the
 // power of two that brings its largest magnitude into [2^14, 2^15): then
 // every element down to 2^-22 of the largest is exact in fp16, and the
 // others are off by at most 2^-39 of it, far below the float32 sums'
 // rounding.  Returns the factor that undoes the scaling.
-template <typename T, int G>
+template <typename T, int G, bool kRepeat = false>
 __device__ __forceinline__ float load_q_f16(const T* qrow0, int lane, uint32_t (&qf)[4][4]) {
-  const int g = lane >> 2, tg = lane & 3;
+  const int g = kRepeat ? (lane >> 2) & 3 : lane >> 2, tg = lane & 3;
   const T* row = qrow0 + (g < G ? g : 0) * PKC_HEAD_DIM;
 #pragma unroll
   for (int b = 0; b < 4; ++b) {

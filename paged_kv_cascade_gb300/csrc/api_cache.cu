@@ -159,7 +159,8 @@ int pkc_paged_decode_state_mx4(const void* q, const void* k_codes, const void* k
     jp.batch = batch; jp.hq = num_qo_heads;
     jp.part_o = dp.part_o; jp.part_lse = dp.part_lse;
     jp.o = o; jp.lse = lse;
-    e = launch_join_mx4(jp, plan_host[PKC_PLAN_N_SPLIT] + plan_host[PKC_PLAN_N_EMPTY], dtype, stream);
+    e = launch_join_mx4(jp, plan_host[PKC_PLAN_N_SPLIT] + plan_host[PKC_PLAN_N_EMPTY],
+                        plan_host[PKC_PLAN_N_PARTIALS], dtype, stream);
     if (e) return cuda_error(e, "paged_decode_state_mx4 join launch");
   }
   return PKC_OK;

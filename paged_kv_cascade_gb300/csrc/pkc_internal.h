@@ -314,8 +314,8 @@ int launch_evict_compact(const CompactParams& p, void* stream);
 int launch_weights(const WeightsParams& p, int q_dtype, int kv_dtype, void* stream);
 int launch_append_mx4(const Mx4RowsParams& p, int dtype, void* stream);
 int launch_gather_mx4(const Mx4RowsParams& p, int dtype, void* stream);
-// n_rows: the plan's split and empty requests
-int launch_join_mx4(const Mx4JoinParams& p, int n_rows, int dtype, void* stream);
+// n_rows: the plan's split and empty requests; n_states: its partial states
+int launch_join_mx4(const Mx4JoinParams& p, int n_rows, int n_states, int dtype, void* stream);
 // n_work: chunks of the plan (0 without one)
 int launch_paged_decode_mx4(const Mx4DecodeParams& p, int n_work, int dtype, void* stream);
 int launch_merge_state(const void* va, const float* sa, const void* vb,

@@ -53,7 +53,6 @@ constexpr int kWarpSmem = kRing + 128 + 256;  // + the tile's probability factor
 constexpr float kRefFloor = -3e38f;           // softmax reference before the first token
 constexpr float kLazy = 4.f;                  // log2 of the largest probability between rescales
 constexpr float kLift = 11.f;                 // probabilities are held times 2^kLift: at most 2^15
-constexpr uint32_t kNoToken = 0xffffffffu;
 
 struct Item {
   int valid, req, kb, ke, slot, hg;
@@ -74,13 +73,6 @@ __device__ __forceinline__ uint32_t code_at(int t, int c) {
 }
 // Token of tile row r: rows 2 x, 2 x + 1 hold tokens x, x + 4 (of each 8).
 __device__ __forceinline__ int token_of(int r) { return (r & 8) + ((r & 7) >> 1) + 4 * (r & 1); }
-
-// base + row * stride in one wide multiply-add.
-__device__ __forceinline__ const uint8_t* at_row(const uint8_t* base, uint32_t row, uint32_t stride) {
-  uint64_t d;
-  asm("mad.wide.u32 %0, %1, %2, %3;" : "=l"(d) : "r"(row), "r"(stride), "l"(base));
-  return reinterpret_cast<const uint8_t*>(d);
-}
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   uint32_t d;

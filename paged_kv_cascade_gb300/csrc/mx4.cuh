@@ -59,6 +59,16 @@ struct PageDiv {
   }
 };
 
+// Pool index (page * page_size + slot) of a token that is not there.
+constexpr uint32_t kNoToken = 0xffffffffu;
+
+// base + row * stride in one wide multiply-add.
+__device__ __forceinline__ const uint8_t* at_row(const uint8_t* base, uint32_t row, uint32_t stride) {
+  uint64_t d;
+  asm("mad.wide.u32 %0, %1, %2, %3;" : "=l"(d) : "r"(row), "r"(stride), "l"(base));
+  return reinterpret_cast<const uint8_t*>(d);
+}
+
 // Asynchronous copies to shared memory, `ok` false: the bytes become zero
 // and nothing is read.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool ok) {

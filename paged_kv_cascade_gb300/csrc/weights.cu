@@ -48,8 +48,10 @@ template <int KV> struct Loads {
   uint32_t ok;  // bit 2 u + i: row i of tile u is there
 };
 
-template <int KV, typename T, int G>
-__global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p) {
+// kAligned: the page size is a multiple of 16, so a tile (tokens 16 i ..
+// 16 i + 15) lies in one page.
+template <int KV, typename T, int G, bool kAligned>
+__global__ void __launch_bounds__(kThreads, 4) weights_kernel(const WeightsParams p) {
   using KT = KeyTraits<KV>;
   constexpr int U = KT::kTiles, P = KT::kPieces, kStep = 16 * U;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -78,55 +80,81 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
   const int32_t* bt_row = p.block_table + (int64_t)b * p.bt_stride;
   float* w_row = p.weights + ((int64_t)b * p.hkv + kvh) * p.w_stride;
   const PageDiv pages{p.page_size, p.page_shift};
-  int32_t pid[U][2];
-  auto load_pages = [&](int s) {
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int t = t_begin + s * t_step + 16 * u + 8 * i + g;
-        pid[u][i] = 0;
-        if (s < steps && t < t_end) {
-          int page, slot;
-          pages.split(t, page, slot);
-          pid[u][i] = bt_row[page];
-        }
-      }
+  // Pool index (page * page_size + slot) of a token, or kNoToken.
+  auto pool_token = [&](int t) -> uint32_t {
+    int page, slot;
+    pages.split(t, page, slot);
+    const int32_t pid = bt_row[page];
+    if (pid < 0 || pid >= p.num_pages) {
+      report(p.status, PKC_ERR_BLOCK_TABLE);
+      return kNoToken;
+    }
+    return (uint32_t)pid * (uint32_t)p.page_size + (uint32_t)slot;
   };
+  // Aligned: lane l holds the pool index of the first token of the warp's
+  // tile k0 + l (a window of 32, the next one loaded 32 tiles ahead).
+  // Otherwise: lane l that of token l of the next step's (at most 32).
+  auto load_window = [&](int k0) -> uint32_t {
+    const int k = k0 + lane, t = t_begin + (k / U) * t_step + 16 * (k % U);
+    return k < steps * U && t < t_end ? pool_token(t) : kNoToken;
+  };
+  auto load_tokens = [&](int s) -> uint32_t {
+    const int t = t_begin + s * t_step + lane;
+    return s < steps && lane < kStep && t < t_end ? pool_token(t) : kNoToken;
+  };
+  static_assert(kStep <= 32, "a step's tokens are held one per lane");
+  uint32_t win = kAligned ? load_window(0) : load_tokens(0);
+  uint32_t win_next = kAligned ? load_window(32) : 0u;
+
+  const uint8_t* k_lane = static_cast<const uint8_t*>(p.k_cache) + (int64_t)kvh * KT::kRow + 16 * tg;
+  const uint8_t* s_lane = static_cast<const uint8_t*>(p.k_scales) + kvh * 4;
+  const uint32_t row_stride = (uint32_t)p.hkv * KT::kRow, scale_stride = (uint32_t)p.hkv * 4;
+  float* w_lane = w_row + t_begin + 8 * (tg & 1) + g;  // token g + 8 (tg & 1) of a tile: written by lanes tg < 2
+  const int t_lane = t_begin + 8 * (tg & 1) + g;
   Loads<KV> buf[2];
   auto load = [&](int s, Loads<KV>& x) {
     x.ok = 0;
+    if (s >= steps) return;  // (warp-uniform)
+    if constexpr (kAligned) {
+      if (s > 0 && ((s * U) & 31) == 0) {
+        win = win_next;
+        win_next = load_window(s * U + 32);
+      }
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      uint32_t tok[2];
+      if constexpr (kAligned) {
+        const uint32_t first = __shfl_sync(0xffffffffu, win, (s * U + u) & 31);
+        tok[0] = first + g;
+        tok[1] = first + g + 8;
+        if (first != kNoToken) x.ok |= 3u << (2 * u);  // (slots behind the last token are read, not used)
+      } else {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int t = t_begin + s * t_step + 16 * u + 8 * i + g;
-        bool ok = s < steps && t < t_end;
-        if (ok && (pid[u][i] < 0 || pid[u][i] >= p.num_pages)) {
-          if (tg == 0) report(p.status, PKC_ERR_BLOCK_TABLE);
-          ok = false;
-        }
-        int page, slot;
-        pages.split(t, page, slot);
-        const int64_t row = ((int64_t)pid[u][i] * p.page_size + slot) * p.hkv + kvh;
-        const uint8_t* src = static_cast<const uint8_t*>(p.k_cache) + row * KT::kRow + 16 * tg;
-        x.scale[u][i] = 0;
-#pragma unroll
-        for (int c = 0; c < P; ++c) x.k[u][i][c] = make_uint4(0, 0, 0, 0);
-        if (ok) {
-          x.ok |= 1u << (2 * u + i);
-#pragma unroll
-          for (int c = 0; c < P; ++c) x.k[u][i][c] = ldg_stream(src + 64 * c);
-          if constexpr (KV == PKC_MX4) x.scale[u][i] = static_cast<const uint32_t*>(p.k_scales)[row];
+        for (int i = 0; i < 2; ++i) {
+          tok[i] = __shfl_sync(0xffffffffu, win, 16 * u + 8 * i + g);
+          if (tok[i] != kNoToken) x.ok |= 1u << (2 * u + i);
         }
       }
-      // weight of token g + 8 (tg & 1), written by lanes tg < 2
-      const int t = t_begin + s * t_step + 16 * u + 8 * (tg & 1) + g;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if ((x.ok >> (2 * u + i)) & 1u) {
+          const uint8_t* src = at_row(k_lane, tok[i], row_stride);
+#pragma unroll
+          for (int c = 0; c < P; ++c) x.k[u][i][c] = ldg_stream(src + 64 * c);
+          if constexpr (KV == PKC_MX4) x.scale[u][i] = *reinterpret_cast<const uint32_t*>(at_row(s_lane, tok[i], scale_stride));
+        } else {
+#pragma unroll
+          for (int c = 0; c < P; ++c) x.k[u][i][c] = make_uint4(0, 0, 0, 0);
+          x.scale[u][i] = 0;
+        }
+      }
+      const int at = s * t_step + 16 * u;
       x.old[u] = 0.f;
-      if (p.decay != 0.f && tg < 2 && s < steps && t < t_end) x.old[u] = w_row[t];
+      if (p.decay != 0.f && tg < 2 && t_lane + at < t_end) x.old[u] = w_lane[at];
     }
+    if constexpr (!kAligned) win = load_tokens(s + 1);
   };
-  load_pages(0);
 
   // Query fragments, elements in the order of the lane's key bytes.
   const T* q0 = static_cast<const T*>(p.q) + ((int64_t)b * p.hkv + kvh) * G * D;
@@ -157,7 +185,6 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
   }
 
   load(0, buf[0]);
-  load_pages(1);
   auto step = [&](int s, const Loads<KV>& x) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -223,31 +250,36 @@ __global__ void __launch_bounds__(kThreads) weights_kernel(const WeightsParams p
       float sum = (tg & 1) ? xb : xa;
       sum += __shfl_xor_sync(0xffffffffu, (tg & 1) ? xa : xb, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      const int t = t_begin + s * t_step + 16 * u + 8 * (tg & 1) + g;
-      if (tg < 2 && ((x.ok >> (2 * u + tg)) & 1u)) w_row[t] = p.decay != 0.f ? fmaf(p.decay, x.old[u], sum) : sum;
+      const int at = s * t_step + 16 * u;
+      if (tg < 2 && t_lane + at < t_end && ((x.ok >> (2 * u + tg)) & 1u))
+        w_lane[at] = p.decay != 0.f ? fmaf(p.decay, x.old[u], sum) : sum;
     }
   };
   for (int s = 0; s < steps; s += 2) {
     load(s + 1, buf[1]);
-    load_pages(s + 2);
     step(s, buf[0]);
     if (s + 1 >= steps) break;
     load(s + 2, buf[0]);
-    load_pages(s + 3);
     step(s + 1, buf[1]);
   }
+}
+
+template <int KV, typename T, int G>
+int launch_g(const WeightsParams& p, int64_t blocks, cudaStream_t st) {
+  if (p.page_size % 16 == 0) weights_kernel<KV, T, G, true><<<(unsigned)blocks, kThreads, 0, st>>>(p);
+  else weights_kernel<KV, T, G, false><<<(unsigned)blocks, kThreads, 0, st>>>(p);
+  return (int)cudaGetLastError();
 }
 
 template <int KV, typename T>
 int launch_t(const WeightsParams& p, int64_t blocks, cudaStream_t st) {
   switch (p.g) {
-    case 1: weights_kernel<KV, T, 1><<<(unsigned)blocks, kThreads, 0, st>>>(p); break;
-    case 2: weights_kernel<KV, T, 2><<<(unsigned)blocks, kThreads, 0, st>>>(p); break;
-    case 4: weights_kernel<KV, T, 4><<<(unsigned)blocks, kThreads, 0, st>>>(p); break;
-    case 8: weights_kernel<KV, T, 8><<<(unsigned)blocks, kThreads, 0, st>>>(p); break;
+    case 1: return launch_g<KV, T, 1>(p, blocks, st);
+    case 2: return launch_g<KV, T, 2>(p, blocks, st);
+    case 4: return launch_g<KV, T, 4>(p, blocks, st);
+    case 8: return launch_g<KV, T, 8>(p, blocks, st);
     default: return (int)cudaErrorInvalidValue;
   }
-  return (int)cudaGetLastError();
 }
 
 }  // namespace

@@ -40,7 +40,7 @@ namespace {
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kBinsPerThread = kBins / kSelThreads;
+constexpr uint32_t kZeroKey = 0x80000000u;  // the key of weight 0
 
 __device__ __forceinline__ uint32_t order_key(float w) {
   if (w != w) return 0xffffffffu;
@@ -49,19 +49,23 @@ __device__ __forceinline__ uint32_t order_key(float w) {
 }
 
 struct SelectShared {
-  uint32_t hist[2][kBins];  // alternate between digits: one barrier per digit
   int warp_sum[kSelWarps];
   int gt[kSelWarps], eq[kSelWarps];
   int cta_gt, cta_eq;
   int bin, rest;
 };
+static_assert(sizeof(SelectShared) % 16 == 0, "what follows is read 16 bytes at a time");
 
+// Shared memory: SelectShared, one histogram (two, alternating, when several
+// blocks share a row: then one cluster barrier per digit is enough), keys.
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectParams p) {
   extern __shared__ __align__(16) uint8_t smem_sel[];
   SelectShared& S = *reinterpret_cast<SelectShared*>(smem_sel);
-  uint32_t* keys = reinterpret_cast<uint32_t*>(smem_sel + sizeof(SelectShared));
+  uint32_t* hists = reinterpret_cast<uint32_t*>(smem_sel + sizeof(SelectShared));
+  const int n_cta = p.cluster, n_hist = n_cta > 1 ? 2 : 1;
+  uint32_t* keys = hists + n_hist * kBins;
   cg::cluster_group cluster = cg::this_cluster();
-  const int n_cta = p.cluster, rank = (int)(blockIdx.x % n_cta);
+  const int rank = (int)(blockIdx.x % n_cta);
   const int row = (int)(blockIdx.x / n_cta), b = row / p.hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int32_t* keep = p.keep + (int64_t)row * p.budget;
@@ -83,48 +87,75 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
   for (int j = at; j < p.recent; j += all) keep[p.budget - p.recent + j] = len - p.recent + j;
   if (m == 0) return;
 
-  // This block's part of the choice: keys [lo, lo + mine).
+  // This block's part of the choice: keys [lo, lo + mine).  In shared memory
+  // it is padded to whole groups of 4 with key 0, which no weight has but a
+  // negative NaN's bits (order_key gives NaN the largest): never chosen.
   const int per = (n + n_cta - 1) / n_cta;
   const int lo = min(rank * per, n), mine = min(per, n - lo);
   const bool cached = mine <= p.smem_keys;
   const float* src = w + p.sinks + lo;
-  auto key_at = [&](int i) { return cached ? keys[i] : order_key(src[i]); };
-  for (int i = tid; i < 2 * kBins; i += kSelThreads) (&S.hist[0][0])[i] = 0;
-  if (cached) {
-    for (int i = tid; i < mine; i += kSelThreads) keys[i] = order_key(__ldcs(src + i));
-  }
+  const int quads = (mine + 3) >> 2;
+  auto quad_at = [&](int q) -> uint4 {  // keys 4 q .. 4 q + 3
+    if (cached) return *reinterpret_cast<const uint4*>(keys + 4 * q);
+    uint32_t k[4];
+#pragma unroll
+    for (int x = 0; x < 4; ++x) k[x] = 4 * q + x < mine ? order_key(src[4 * q + x]) : 0u;
+    return make_uint4(k[0], k[1], k[2], k[3]);
+  };
+  for (int i = tid; i < n_hist * kBins; i += kSelThreads) hists[i] = 0;
   __syncthreads();
+
+  // First digit, as the keys come in.  Weights that are exactly 0 are often
+  // most of a row: each warp counts them apart, so they do not queue up on
+  // one bin.
+  int zeros = 0;
+#pragma unroll 8
+  for (int i0 = warp * 32; i0 < 4 * quads; i0 += kSelThreads) {
+    const int i = i0 + lane;
+    const uint32_t k = i < mine ? order_key(__ldcs(src + i)) : 0u;
+    if (cached && i < 4 * quads) keys[i] = k;
+    zeros += __popc(__ballot_sync(0xffffffffu, k == kZeroKey));
+    if (i < mine && k != kZeroKey) atomicAdd(&hists[k >> 21], 1u);
+  }
+  if (lane == 0 && zeros) atomicAdd(&hists[kZeroKey >> 21], (uint32_t)zeros);
 
   uint32_t prefix = 0;  // digits found, in place
   int rest = m;         // to be chosen among the keys that agree with them
   for (int d = 0; d < 3; ++d) {
     const int shift = d == 0 ? 21 : d == 1 ? 10 : 0, width = d == 2 ? 10 : 11;
-    uint32_t* hist = S.hist[d & 1];
-    for (int i0 = warp * 32; i0 < mine; i0 += kSelThreads) {  // (warp-uniform)
-      const int i = i0 + lane;
-      const uint32_t k = i < mine ? key_at(i) : 0u;
-      const bool in = i < mine && (d == 0 || (k >> (shift + width)) == (prefix >> (shift + width)));
-      const uint32_t digit = (k >> shift) & ((1u << width) - 1u);
-      // many keys alike (a row of zero weights) must not queue up on one bin
-      const uint32_t act = __ballot_sync(0xffffffffu, in);
-      if (act == 0u) continue;
-      const int first = __ffs(act) - 1;
-      const uint32_t lead = __shfl_sync(0xffffffffu, digit, first);
-      const uint32_t same = __ballot_sync(0xffffffffu, in && digit == lead);
-      if (lane == first) atomicAdd(&hist[lead], (uint32_t)__popc(same));
-      else if (in && digit != lead) atomicAdd(&hist[digit], 1u);
-    }
-    cluster.sync();  // every block's histogram is complete
-    // Total counts of this thread's bins, from the top: thread 0 has the highest.
-    uint32_t cnt[kBinsPerThread];
-    int sum = 0;
+    uint32_t* hist = hists + (n_cta > 1 ? (d & 1) * kBins : 0);
+    if (d > 0) {
+      const uint32_t want = prefix >> (shift + width), mask = (1u << width) - 1u;
+      if (!cached) __syncthreads();
+      for (int q = tid; q < quads; q += kSelThreads) {
+        const uint4 k4 = quad_at(q);
+        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
-    for (int x = 0; x < kBinsPerThread; ++x) {
-      const int bin = kBins - 1 - (tid * kBinsPerThread + x);
-      cnt[x] = 0;
-      for (int c = 0; c < n_cta; ++c) cnt[x] += cluster.map_shared_rank(hist, c)[bin];
-      sum += (int)cnt[x];
+        for (int x = 0; x < 4; ++x)
+          if ((k[x] >> (shift + width)) == want && k[x] != kZeroKey) atomicAdd(&hist[(k[x] >> shift) & mask], 1u);
+      }
+      if (lane == 0 && zeros && (kZeroKey >> (shift + width)) == want)
+        atomicAdd(&hist[(kZeroKey >> shift) & mask], (uint32_t)zeros);
     }
+    if (n_cta > 1) cluster.sync();  // every block's histogram is complete
+    else __syncthreads();
+    // Counts of this thread's four bins, from the top: thread 0 has the highest.
+    const int bin0 = kBins - 4 - 4 * tid;
+    uint4 cnt = *reinterpret_cast<const uint4*>(hist + bin0);
+    if (n_cta > 1) {
+      uint4 c[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        c[x] = make_uint4(0, 0, 0, 0);
+        if (x < n_cta && x != rank)
+          c[x] = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(hist, x) + bin0);
+      }
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        cnt.x += c[x].x; cnt.y += c[x].y; cnt.z += c[x].z; cnt.w += c[x].w;
+      }
+    }
+    const int sum = (int)(cnt.x + cnt.y + cnt.z + cnt.w);
     int above = sum;  // inclusive scan over the block
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
@@ -134,77 +165,95 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
     if (lane == 31) S.warp_sum[warp] = above;
     __syncthreads();
     int before = 0;
-    for (int x = 0; x < warp; ++x) before += S.warp_sum[x];
+#pragma unroll
+    for (int x = 0; x < kSelWarps; ++x) before += x < warp ? S.warp_sum[x] : 0;
     above += before - sum;  // keys in higher bins than this thread's
     if (above < rest && rest <= above + sum) {  // exactly one thread
+      const int c[4] = {(int)cnt.w, (int)cnt.z, (int)cnt.y, (int)cnt.x};
 #pragma unroll
-      for (int x = 0; x < kBinsPerThread; ++x) {
-        const int c = (int)cnt[x];
-        if (above < rest && rest <= above + c) {
-          S.bin = kBins - 1 - (tid * kBinsPerThread + x);
+      for (int x = 0; x < 4; ++x) {
+        if (above < rest && rest <= above + c[x]) {
+          S.bin = bin0 + 3 - x;
           S.rest = rest - above;
         }
-        above += c;
+        above += c[x];
       }
     }
+    // The next digit's histogram: with one, this; with two, the one before,
+    // which every block is past at this digit's barrier.
+    if (d < 2 && (n_cta == 1 || d == 1))
+      for (int i = tid; i < kBins; i += kSelThreads) hists[i] = 0;
     __syncthreads();
     prefix |= (uint32_t)S.bin << shift;
     rest = S.rest;
-    if (d == 0) {  // the third digit uses this buffer again: all blocks are past it at the next barrier
-      __syncthreads();
-    } else if (d == 1) {
-      for (int i = tid; i < kBins; i += kSelThreads) S.hist[0][i] = 0;
-      __syncthreads();
-    }
+    __syncthreads();
   }
   // Keys above T = prefix are kept, and the first `rest` of those equal to it.
   // Each warp takes a consecutive part: counts, then ranks.
-  const int part = ((mine + kSelWarps - 1) / kSelWarps + 31) & ~31;
-  const int w_lo = min(warp * part, mine), w_hi = min(w_lo + part, mine);
+  const int part = (quads + kSelWarps * 32 - 1) / (kSelWarps * 32) * 32;  // in groups of 4
+  const int w_lo = min(warp * part, quads), w_hi = min(w_lo + part, quads);
   int gt = 0, eq = 0;
-  for (int i0 = w_lo; i0 < w_hi; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t k = i < w_hi ? key_at(i) : 0u;
-    gt += __popc(__ballot_sync(0xffffffffu, i < w_hi && k > prefix));
-    eq += __popc(__ballot_sync(0xffffffffu, i < w_hi && k == prefix));
+  for (int q = w_lo + lane; q < w_hi; q += 32) {
+    const uint4 k = quad_at(q);
+    gt += (k.x > prefix) + (k.y > prefix) + (k.z > prefix) + (k.w > prefix);
+    eq += (k.x == prefix) + (k.y == prefix) + (k.z == prefix) + (k.w == prefix);
   }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
   if (lane == 0) {
     S.gt[warp] = gt;
     S.eq[warp] = eq;
   }
   __syncthreads();
-  if (tid == 0) {
-    int a = 0, c = 0;
-    for (int x = 0; x < kSelWarps; ++x) {
-      a += S.gt[x];
-      c += S.eq[x];
-    }
-    S.cta_gt = a;
-    S.cta_eq = c;
-  }
-  cluster.sync();
   int gt0 = 0, eq0 = 0;  // before this warp's part
-  for (int c = 0; c < rank; ++c) {
-    const SelectShared* o = cluster.map_shared_rank(&S, c);
-    gt0 += o->cta_gt;
-    eq0 += o->cta_eq;
-  }
   for (int x = 0; x < warp; ++x) {
     gt0 += S.gt[x];
     eq0 += S.eq[x];
   }
-  const uint32_t below = (1u << lane) - 1u;
-  for (int i0 = w_lo; i0 < w_hi; i0 += 32) {
-    const int i = i0 + lane;
-    const uint32_t k = i < w_hi ? key_at(i) : 0u;
-    const bool is_gt = i < w_hi && k > prefix, is_eq = i < w_hi && k == prefix;
-    const uint32_t bg = __ballot_sync(0xffffffffu, is_gt), be = __ballot_sync(0xffffffffu, is_eq);
-    const int g = gt0 + __popc(bg & below), e = eq0 + __popc(be & below);
-    if (is_gt || (is_eq && e < rest)) keep[p.sinks + g + min(e, rest)] = p.sinks + lo + i;
-    gt0 += __popc(bg);
-    eq0 += __popc(be);
+  if (n_cta > 1) {
+    if (tid == kSelThreads - 1) {
+      S.cta_gt = gt0 + gt;
+      S.cta_eq = eq0 + eq;
+    }
+    cluster.sync();
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      if (c < rank) {
+        const SelectShared* o = cluster.map_shared_rank(&S, c);
+        gt0 += o->cta_gt;
+        eq0 += o->cta_eq;
+      }
+    }
   }
-  cluster.sync();  // no block leaves while another reads its counts
+  for (int q0 = w_lo; q0 < w_hi; q0 += 32) {
+    const int q = q0 + lane;
+    const uint4 k4 = q < w_hi ? quad_at(q) : make_uint4(0, 0, 0, 0);
+    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+    int g = 0, e = 0;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      g += k[x] > prefix;
+      e += q < w_hi && k[x] == prefix;
+    }
+    int scan = g | (e << 16);  // both counts of at most 128
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, scan, x);
+      if (lane >= x) scan += y;
+    }
+    const int total = __shfl_sync(0xffffffffu, scan, 31);
+    int gr = gt0 + (scan & 0xffff) - g, er = eq0 + (scan >> 16) - e;
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const bool is_gt = k[x] > prefix, is_eq = q < w_hi && k[x] == prefix;
+      if (is_gt || (is_eq && er < rest)) keep[p.sinks + gr + min(er, rest)] = p.sinks + lo + 4 * q + x;
+      gr += is_gt;
+      er += is_eq;
+    }
+    gt0 += total & 0xffff;
+    eq0 += total >> 16;
+  }
+  if (n_cta > 1) cluster.sync();  // no block leaves while another reads its counts
 }
 
 // ---------------------------------------------------------------------------
@@ -356,8 +405,8 @@ int launch_evict_select(const SelectParams& p_in, void* stream) {
   p.cluster = 1;
   while (p.cluster < 8 && rows * p.cluster * 2 <= num_sms() && p.w_stride / (2 * p.cluster) >= 2048) p.cluster *= 2;
   const int64_t per = (p.w_stride + p.cluster - 1) / p.cluster;
-  p.smem_keys = (int)std::min<int64_t>(per, 48 * 1024);
-  const int smem = (int)sizeof(SelectShared) + 4 * p.smem_keys;
+  p.smem_keys = (int)std::min<int64_t>((per + 3) & ~int64_t(3), 48 * 1024);
+  const int smem = (int)sizeof(SelectShared) + 4 * kBins * (p.cluster > 1 ? 2 : 1) + 4 * p.smem_keys;
   cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return (int)e;
   cudaLaunchConfig_t cfg = {};

@@ -33,11 +33,12 @@ constexpr int kThreads = kWarps * 32;
 constexpr int D = PKC_HEAD_DIM;
 
 template <int KV> struct KeyTraits;
-// kPieces: 16-byte pieces of a row per lane; kTiles: tiles of 16 tokens per step
-template <> struct KeyTraits<PKC_F16> { static constexpr int kPieces = 4, kTiles = 1, kRow = 256; };
-template <> struct KeyTraits<PKC_BF16> { static constexpr int kPieces = 4, kTiles = 1, kRow = 256; };
-template <> struct KeyTraits<PKC_E4M3> { static constexpr int kPieces = 2, kTiles = 2, kRow = 128; };
-template <> struct KeyTraits<PKC_MX4> { static constexpr int kPieces = 1, kTiles = 2, kRow = kMx4RowBytes; };
+// kPieces: 16-byte pieces of a row per lane; kTiles: tiles of 16 tokens per
+// step; kSteps: steps in registers (the one in use and those on their way)
+template <> struct KeyTraits<PKC_F16> { static constexpr int kSteps = 2, kPieces = 4, kTiles = 1, kRow = 256; };
+template <> struct KeyTraits<PKC_BF16> { static constexpr int kSteps = 2, kPieces = 4, kTiles = 1, kRow = 256; };
+template <> struct KeyTraits<PKC_E4M3> { static constexpr int kSteps = 2, kPieces = 2, kTiles = 2, kRow = 128; };
+template <> struct KeyTraits<PKC_MX4> { static constexpr int kSteps = 4, kPieces = 1, kTiles = 1, kRow = kMx4RowBytes; };
 
 // One step's loads of a lane: rows g and g + 8 of each tile.
 template <int KV> struct Loads {
@@ -111,7 +112,8 @@ __global__ void __launch_bounds__(kThreads, 4) weights_kernel(const WeightsParam
   const uint32_t row_stride = (uint32_t)p.hkv * KT::kRow, scale_stride = (uint32_t)p.hkv * 4;
   float* w_lane = w_row + t_begin + 8 * (tg & 1) + g;  // token g + 8 (tg & 1) of a tile: written by lanes tg < 2
   const int t_lane = t_begin + 8 * (tg & 1) + g;
-  Loads<KV> buf[2];
+  constexpr int N = KT::kSteps;
+  Loads<KV> buf[N];
   auto load = [&](int s, Loads<KV>& x) {
     x.ok = 0;
     if (s >= steps) return;  // (warp-uniform)
@@ -184,7 +186,8 @@ __global__ void __launch_bounds__(kThreads, 4) weights_kernel(const WeightsParam
     ls[e] = lse == neg_inf() ? -neg_inf() : lse * kLog2e;
   }
 
-  load(0, buf[0]);
+#pragma unroll
+  for (int i = 0; i < N - 1; ++i) load(i, buf[i]);
   auto step = [&](int s, const Loads<KV>& x) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -255,12 +258,13 @@ __global__ void __launch_bounds__(kThreads, 4) weights_kernel(const WeightsParam
         w_lane[at] = p.decay != 0.f ? fmaf(p.decay, x.old[u], sum) : sum;
     }
   };
-  for (int s = 0; s < steps; s += 2) {
-    load(s + 1, buf[1]);
-    step(s, buf[0]);
-    if (s + 1 >= steps) break;
-    load(s + 2, buf[0]);
-    step(s + 1, buf[1]);
+  for (int s = 0; s < steps; s += N) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (i > 0 && s + i >= steps) break;
+      load(s + i + N - 1, buf[(i + N - 1) % N]);
+      step(s + i, buf[i]);
+    }
   }
 }
 
@@ -288,14 +292,15 @@ int launch_weights(const WeightsParams& p_in, int q_dtype, int kv_dtype, void* s
   WeightsParams p = p_in;
   // The lengths are on the device: segments are laid over the longest request
   // that the table and the weight rows hold, and blocks past a request's end
-  // return at once.  256 tokens per warp amortise a block's start (length ->
-  // page id -> key, three loads in a row); segments are halved while there
-  // are fewer than four blocks per SM.
+  // return at once.  256 tokens per warp (512 of the mx4 cache's short rows)
+  // amortise a block's start (length -> page id -> key, three loads in a row;
+  // mx4: 84 -> 78 us) and still balance the end (16-bit with 512: 58 -> 65
+  // us); segments are halved while there are fewer than four blocks per SM.
   p.hg = p.hkv % 4 == 0 ? 4 : p.hkv % 2 == 0 ? 2 : 1;
   const int64_t most = std::min(p.bt_stride * (int64_t)p.page_size, p.w_stride);
-  const int step = 16 * (kv_dtype == PKC_E4M3 || kv_dtype == PKC_MX4 ? 2 : 1) * (kWarps / p.hg);
+  const int step = 16 * (kv_dtype == PKC_E4M3 ? 2 : 1) * (kWarps / p.hg);
   const int64_t rows = (int64_t)p.batch * (p.hkv / p.hg);
-  int64_t seg = std::max<int64_t>(256 * (kWarps / p.hg), step);
+  int64_t seg = std::max<int64_t>((kv_dtype == PKC_MX4 ? 512 : 256) * (kWarps / p.hg), step);
   while (seg > step && rows * ((most + seg - 1) / seg) < 4 * (int64_t)num_sms()) seg /= 2;
   // (a grid has at most 2^31 - 1 blocks)
   while (rows * ((most + seg - 1) / seg) > INT32_MAX) seg *= 2;

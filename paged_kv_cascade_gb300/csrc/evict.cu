@@ -163,6 +163,10 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
       if (lane >= x) above += y;
     }
     if (lane == 31) S.warp_sum[warp] = above;
+    if (tid == 0) {  // (replaced below, unless the weights change under the kernel)
+      S.bin = 0;
+      S.rest = rest;
+    }
     __syncthreads();
     int before = 0;
 #pragma unroll
@@ -246,7 +250,8 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       const bool is_gt = k[x] > prefix, is_eq = q < w_hi && k[x] == prefix;
-      if (is_gt || (is_eq && er < rest)) keep[p.sinks + gr + min(er, rest)] = p.sinks + lo + 4 * q + x;
+      const int rank_of = gr + min(er, rest);  // (below m, unless the weights change under the kernel)
+      if ((is_gt || (is_eq && er < rest)) && rank_of < m) keep[p.sinks + rank_of] = p.sinks + lo + 4 * q + x;
       gr += is_gt;
       er += is_eq;
     }
@@ -261,51 +266,73 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
 // ---------------------------------------------------------------------------
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 4;  // rows per thread and chunk (two chunks in registers)
+constexpr int kMoveRows = 2;  // rows per thread and chunk (two chunks in registers)
 
 __device__ __forceinline__ uint4 load_cg(const uint4* p) { return __ldcg(p); }
 __device__ __forceinline__ uint32_t load_cg(const uint32_t* p) { return __ldcg(p); }
 
 // Move rows keep[j] -> j, j < n, in units of V (one unit of a row per
-// thread); at(slot) is this thread's unit of a slot, `row` its row within a
-// pass of `rows` rows.  Called by a whole block.
-template <typename V, typename At>
-__device__ __forceinline__ void move_rows(const int32_t* keep, int n, int row, int rows, At at) {
-  V buf[2][kMoveRows];
-  int32_t src[kMoveRows];
+// thread): place(slot) is a slot's place, at(place) this thread's unit of it,
+// `row` the thread's row within a pass of `rows` rows.  Called by a whole
+// block.  A chunk is kMoveRows passes.  While chunk c is stored, the rows of
+// chunk c + 1 are on their way, the places of chunk c + 2 and the slots of
+// chunk c + 3.
+template <typename V, typename Place, typename At>
+__device__ __forceinline__ void move_rows(const int32_t* keep, int n, int row, int rows, Place place, At at) {
   const int chunk = rows * kMoveRows;
-  auto indices = [&](int c) {
+  V buf[2][kMoveRows];
+  int32_t slot[kMoveRows];                  // chunk c + 3's slots (-1 past the end)
+  uint32_t from[kMoveRows], to[kMoveRows];  // chunk c + 2's places
+  auto load_slots = [&](int c) {
 #pragma unroll
     for (int u = 0; u < kMoveRows; ++u) {
       const int j = c + u * rows + row;
-      src[u] = j < n ? keep[j] : -1;
+      slot[u] = j < n ? keep[j] : -1;
     }
   };
-  auto load = [&](V (&x)[kMoveRows]) {
+  auto load_places = [&](int c) {
+#pragma unroll
+    for (int u = 0; u < kMoveRows; ++u) {
+      const int j = c + u * rows + row;
+      from[u] = to[u] = 0;
+      if (slot[u] >= 0) {
+        from[u] = place(slot[u]);
+        to[u] = place(j);
+      }
+    }
+  };
+  auto load = [&](V (&x)[kMoveRows], uint32_t (&dst)[kMoveRows]) {  // (from == to: nothing to move)
+#pragma unroll
+    for (int u = 0; u < kMoveRows; ++u) {
+      const bool moves = from[u] != to[u];
+      dst[u] = moves ? to[u] : kNoToken;
+      if (moves) x[u] = load_cg(at(from[u]));
+    }
+  };
+  auto store = [&](const V (&x)[kMoveRows], const uint32_t (&dst)[kMoveRows]) {
 #pragma unroll
     for (int u = 0; u < kMoveRows; ++u)
-      if (src[u] >= 0) x[u] = load_cg(at(src[u]));
+      if (dst[u] != kNoToken) *at(dst[u]) = x[u];
   };
-  auto store = [&](int c, const V (&x)[kMoveRows]) {
-#pragma unroll
-    for (int u = 0; u < kMoveRows; ++u) {
-      const int j = c + u * rows + row;
-      if (j < n) *at(j) = x[u];
-    }
-  };
-  indices(0);
-  load(buf[0]);
-  indices(chunk);
+  uint32_t dst[2][kMoveRows];
+  load_slots(0);
+  load_places(0);
+  load_slots(chunk);
+  load(buf[0], dst[0]);
+  load_places(chunk);
+  load_slots(2 * chunk);
   for (int c = 0; c < n; c += 2 * chunk) {
-    load(buf[1]);
-    indices(c + 2 * chunk);
+    load(buf[1], dst[1]);
+    load_places(c + 2 * chunk);
+    load_slots(c + 3 * chunk);
     __syncthreads();  // chunk c has been read by every thread
-    store(c, buf[0]);
+    store(buf[0], dst[0]);
     if (c + chunk >= n) break;
-    load(buf[0]);
-    indices(c + 3 * chunk);
+    load(buf[0], dst[0]);
+    load_places(c + 3 * chunk);
+    load_slots(c + 4 * chunk);
     __syncthreads();
-    store(c + chunk, buf[1]);
+    store(buf[1], dst[1]);
   }
 }
 
@@ -339,24 +366,26 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const Compa
       if (tid == 0) report(p.status, bad_page ? PKC_ERR_BLOCK_TABLE : PKC_ERR_PLAN);
     } else {
       // (strictly ascending and >= 0: keep[j] >= j)
-      auto token = [&](int slot) {  // row of (slot, this head) in the pools
-        int page, s;
-        pages.split(slot, page, s);
-        return ((int64_t)bt_row[page] * p.page_size + s) * p.hkv + h;
+      auto token = [&](int slot) {  // a slot's pool index
+        int page, x;
+        pages.split(slot, page, x);
+        return (uint32_t)bt_row[page] * (uint32_t)p.page_size + (uint32_t)x;
       };
       if (part < 2 * p.slices) {  // a slice of K's or V's rows
-        uint8_t* base = static_cast<uint8_t*>(part & 1 ? p.v_cache : p.k_cache);
         const int units = p.row_bytes / 16 / p.slices;  // 16-byte units of a row in the slice
-        const int unit = (part >> 1) * units + tid % units;
-        move_rows<uint4>(keep, n, tid / units, kMoveThreads / units, [&](int slot) {
-          return reinterpret_cast<uint4*>(base + token(slot) * p.row_bytes) + unit;
+        uint8_t* base = static_cast<uint8_t*>(part & 1 ? p.v_cache : p.k_cache) + (int64_t)h * p.row_bytes +
+                        16 * ((part >> 1) * units + tid % units);
+        const uint32_t stride = (uint32_t)p.hkv * (uint32_t)p.row_bytes;
+        move_rows<uint4>(keep, n, tid / units, kMoveThreads / units, token, [&](uint32_t t) {
+          return reinterpret_cast<uint4*>(const_cast<uint8_t*>(at_row(base, t, stride)));
         });
       } else if (part < 2 * p.slices + (p.k_scales ? 2 : 0)) {  // mx4 scales: 4 bytes a row
-        uint32_t* base = static_cast<uint32_t*>((part - 2 * p.slices) ? p.v_scales : p.k_scales);
-        move_rows<uint32_t>(keep, n, tid, kMoveThreads, [&](int slot) { return base + token(slot); });
+        uint32_t* base = static_cast<uint32_t*>((part - 2 * p.slices) ? p.v_scales : p.k_scales) + h;
+        move_rows<uint32_t>(keep, n, tid, kMoveThreads, token, [&](uint32_t t) { return base + (int64_t)t * p.hkv; });
       } else {  // weights: the kept ones, zeros behind them
         uint32_t* w = reinterpret_cast<uint32_t*>(p.weights) + (int64_t)row * p.w_stride;
-        move_rows<uint32_t>(keep, n, tid, kMoveThreads, [&](int slot) { return w + slot; });
+        move_rows<uint32_t>(keep, n, tid, kMoveThreads, [](int slot) { return (uint32_t)slot; },
+                            [&](uint32_t t) { return w + t; });
         __syncthreads();
         for (int j = n + tid; j < len; j += kMoveThreads) w[j] = 0u;
       }

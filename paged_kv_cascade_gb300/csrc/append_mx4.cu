@@ -22,8 +22,9 @@ namespace pkc {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kGroups = kThreads / 16;  // rows a block works on at once
-constexpr int kUnroll = 4;              // rows a 16-lane group has in flight
+constexpr int kWarps = kThreads / 32;
+constexpr int kUnroll = 4;           // rows a 16-lane group has in flight
+constexpr int kRows = 2 * kUnroll;   // rows of a token that a warp has in flight
 
 // Request of row t of the ragged token list: indptr[b] <= t < indptr[b + 1],
 // or -1 (rows that no request owns).
@@ -57,65 +58,65 @@ __device__ __forceinline__ Place place_of(const Mx4RowsParams& p, int t) {
   return {(int64_t)page * p.page_size + slot, false};
 }
 
+// A warp works on one token, 8 rows at a time: rows r = 0 .. 2 Hkv - 1 are
+// the token's K heads, then its V heads; lanes 0..15 and 16..31 take every
+// second one.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) append_mx4_kernel(const Mx4RowsParams p) {
-  const int lane16 = threadIdx.x & 15, group = threadIdx.x >> 4;
-  const int64_t rows = (int64_t)p.total * 2 * p.hkv;  // (token, K | V, head)
+  const int lane16 = threadIdx.x & 15, half = (threadIdx.x >> 4) & 1;
+  const int j = lane16 >> 2, v = lane16 & 3;
+  const int rows = 2 * p.hkv, n_warps = (int)gridDim.x * kWarps;
   bool any_bad = false;
-  for (int64_t r0 = (int64_t)blockIdx.x * kGroups; r0 < rows; r0 += (int64_t)gridDim.x * kGroups * kUnroll) {
-    uint4 x[kUnroll];
-    int64_t dst[kUnroll];
-    bool is_v[kUnroll];
+  for (int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); t < p.total; t += n_warps) {
+    Place at{-1, false};
+    for (int r0 = (int)blockIdx.y * kRows; r0 < rows; r0 += (int)gridDim.y * kRows) {
+      uint4 x[kUnroll];
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const int64_t r = r0 + (int64_t)i * gridDim.x * kGroups + group;
-      dst[i] = -1;
-      is_v[i] = false;
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (r < rows) {
-        const int64_t th = r / p.hkv;
-        const int h = (int)(r - th * p.hkv);
-        const int t = (int)(th >> 1);
-        is_v[i] = (th & 1) != 0;
-        const T* src = static_cast<const T*>(is_v[i] ? p.v_rows : p.k_rows);
-        x[i] = ldg_stream(src + ((int64_t)t * p.hkv + h) * PKC_HEAD_DIM + 8 * lane16);
-        const Place at = place_of(p, t);
-        any_bad = any_bad || at.bad;
-        if (at.slot >= 0) dst[i] = at.slot * p.hkv + h;
+      for (int i = 0; i < kUnroll; ++i) {
+        const int r = r0 + 2 * i + half;
+        const bool is_v = r >= p.hkv;
+        const T* src = static_cast<const T*>(is_v ? p.v_rows : p.k_rows) +
+                       (t * p.hkv + (is_v ? r - p.hkv : r)) * PKC_HEAD_DIM + 8 * lane16;
+        x[i] = r < rows ? ldg_stream(src) : make_uint4(0, 0, 0, 0);
       }
-    }
+      if (r0 == (int)blockIdx.y * kRows) {
+        at = place_of(p, (int)t);
+        any_bad = any_bad || at.bad;
+      }
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const float2 f[4] = {Elem<T>::to_f2(x[i].x), Elem<T>::to_f2(x[i].y), Elem<T>::to_f2(x[i].z),
-                           Elem<T>::to_f2(x[i].w)};
-      uint32_t top = 0;  // magnitude bits: ordered as integers, NaN above infinity
+      for (int i = 0; i < kUnroll; ++i) {
+        const int r = r0 + 2 * i + half;
+        const bool is_v = r >= p.hkv;
+        const float2 f[4] = {Elem<T>::to_f2(x[i].x), Elem<T>::to_f2(x[i].y), Elem<T>::to_f2(x[i].z),
+                             Elem<T>::to_f2(x[i].w)};
+        uint32_t top = 0;  // magnitude bits: ordered as integers, NaN above infinity
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        top = max(top, max(__float_as_uint(f[k].x) & 0x7fffffffu, __float_as_uint(f[k].y) & 0x7fffffffu));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const uint32_t e = top >> 23;
-      const bool nan = e == 255u;
-      const uint32_t s = nan ? 255u : (uint32_t)max((int)e - 2, 1);
-      const float mul = __uint_as_float(nan ? 0u : (254u - s) << 23);  // 2^(127 - s)
-      uint32_t w = to_e2m1x4(f[0].x * mul, f[0].y * mul, f[1].x * mul, f[1].y * mul) |
-                   (to_e2m1x4(f[2].x * mul, f[2].y * mul, f[3].x * mul, f[3].y * mul) << 16);
-      if (nan) w = 0;
-      // lane 4 b + v holds words (u = 2 v, b) and (u = 2 v + 1, b); lane
-      // 4 j + v stores 32-bit word j of 16-byte piece v: words
-      // (u = 2 v + j / 2, b = 2 (j % 2)) and (the same u, b + 1)
-      const int j = lane16 >> 2, v = lane16 & 3;
-      const uint32_t wa = __shfl_sync(0xffffffffu, w, 8 * (j & 1) + v, 16);
-      const uint32_t wb = __shfl_sync(0xffffffffu, w, 8 * (j & 1) + 4 + v, 16);
-      const uint32_t out = prmt(wa, wb, (j >> 1) ? 0x7632u : 0x5410u);
-      uint32_t sc = s << (8 * (lane16 >> 2));
-      sc |= __shfl_xor_sync(0xffffffffu, sc, 4);
-      sc |= __shfl_xor_sync(0xffffffffu, sc, 8);
-      if (dst[i] >= 0) {
-        uint8_t* codes = static_cast<uint8_t*>(is_v[i] ? p.v_codes : p.k_codes) + dst[i] * kMx4RowBytes;
-        *reinterpret_cast<uint32_t*>(codes + 16 * v + 4 * j) = out;
-        if (lane16 == 0)
-          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(is_v[i] ? p.v_scales : p.k_scales) + dst[i] * 4) = sc;
+        for (int k = 0; k < 4; ++k)
+          top = max(top, max(__float_as_uint(f[k].x) & 0x7fffffffu, __float_as_uint(f[k].y) & 0x7fffffffu));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const uint32_t e = top >> 23;
+        const bool nan = e == 255u;
+        const uint32_t s = nan ? 255u : (uint32_t)max((int)e - 2, 1);
+        const float mul = __uint_as_float(nan ? 0u : (254u - s) << 23);  // 2^(127 - s)
+        uint32_t w = to_e2m1x4(f[0].x * mul, f[0].y * mul, f[1].x * mul, f[1].y * mul) |
+                     (to_e2m1x4(f[2].x * mul, f[2].y * mul, f[3].x * mul, f[3].y * mul) << 16);
+        if (nan) w = 0;
+        // lane 4 b + v holds words (u = 2 v, b) and (u = 2 v + 1, b); lane
+        // 4 j + v stores 32-bit word j of 16-byte piece v: words
+        // (u = 2 v + j / 2, b = 2 (j % 2)) and (the same u, b + 1)
+        const uint32_t wa = __shfl_sync(0xffffffffu, w, 8 * (j & 1) + v, 16);
+        const uint32_t wb = __shfl_sync(0xffffffffu, w, 8 * (j & 1) + 4 + v, 16);
+        const uint32_t out = prmt(wa, wb, (j >> 1) ? 0x7632u : 0x5410u);
+        uint32_t sc = s << (8 * j);
+        sc |= __shfl_xor_sync(0xffffffffu, sc, 4);
+        sc |= __shfl_xor_sync(0xffffffffu, sc, 8);
+        if (at.slot >= 0 && r < rows) {
+          const int64_t row = at.slot * p.hkv + (is_v ? r - p.hkv : r);
+          uint8_t* codes = static_cast<uint8_t*>(is_v ? p.v_codes : p.k_codes) + row * kMx4RowBytes;
+          *reinterpret_cast<uint32_t*>(codes + 16 * v + 4 * j) = out;
+          if (lane16 == 0) static_cast<uint32_t*>(is_v ? p.v_scales : p.k_scales)[row] = sc;
+        }
       }
     }
   }
@@ -129,7 +130,7 @@ __global__ void __launch_bounds__(kThreads) append_mx4_kernel(const Mx4RowsParam
   }
   __threadfence();
   __syncthreads();
-  if (threadIdx.x == 0) last = atomicAdd(ctr, 1) == (int)gridDim.x - 1;
+  if (threadIdx.x == 0) last = atomicAdd(ctr, 1) == (int)(gridDim.x * gridDim.y) - 1;
   __syncthreads();
   if (!last) return;
   __threadfence();
@@ -158,78 +159,76 @@ __global__ void __launch_bounds__(kThreads) append_mx4_kernel(const Mx4RowsParam
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) gather_mx4_kernel(const Mx4RowsParams p) {
-  const int lane16 = threadIdx.x & 15, group = threadIdx.x >> 4;
-  const int64_t rows = (int64_t)p.total * 2 * p.hkv;
-  for (int64_t r0 = (int64_t)blockIdx.x * kGroups; r0 < rows; r0 += (int64_t)gridDim.x * kGroups * kUnroll) {
-    uint32_t w[kUnroll], sc[kUnroll];
-    int64_t dst[kUnroll];
-    bool is_v[kUnroll];
+  const int lane16 = threadIdx.x & 15, half = (threadIdx.x >> 4) & 1;
+  const int b = lane16 >> 2, v = lane16 & 3;
+  const int rows = 2 * p.hkv, n_warps = (int)gridDim.x * kWarps;
+  for (int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); t < p.total; t += n_warps) {
+    const Place at = place_of(p, (int)t);
+    if (at.bad && (threadIdx.x & 31) == 0) report(p.status, PKC_ERR_BLOCK_TABLE);
+    if (at.slot < 0 && !at.bad) continue;  // (warp-uniform) a row of no request
+    for (int r0 = (int)blockIdx.y * kRows; r0 < rows; r0 += (int)gridDim.y * kRows) {
+      uint32_t w[kUnroll], sc[kUnroll];
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      const int64_t r = r0 + (int64_t)i * gridDim.x * kGroups + group;
-      dst[i] = -1;
-      w[i] = sc[i] = 0;
-      is_v[i] = false;
-      if (r < rows) {
-        const int64_t th = r / p.hkv;
-        const int h = (int)(r - th * p.hkv);
-        const int t = (int)(th >> 1);
-        is_v[i] = (th & 1) != 0;
-        const Place at = place_of(p, t);
-        if (at.bad) report(p.status, PKC_ERR_BLOCK_TABLE);
-        if (at.slot >= 0 || at.bad) dst[i] = (int64_t)t * p.hkv + h;  // a row without a page reads as zeros
-        if (at.slot >= 0) {
-          const int64_t row = at.slot * p.hkv + h;
-          w[i] = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(is_v[i] ? p.v_codes : p.k_codes) +
-                                                   row * kMx4RowBytes)[4 * (lane16 & 3) + (lane16 >> 2)];
-          sc[i] = reinterpret_cast<const uint32_t*>(is_v[i] ? p.v_scales : p.k_scales)[row];
+      for (int i = 0; i < kUnroll; ++i) {
+        const int r = r0 + 2 * i + half;
+        const bool is_v = r >= p.hkv;
+        w[i] = sc[i] = 0;  // a row without a page reads as zeros
+        if (at.slot >= 0 && r < rows) {
+          const int64_t row = at.slot * p.hkv + (is_v ? r - p.hkv : r);
+          w[i] = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(is_v ? p.v_codes : p.k_codes) +
+                                                   row * kMx4RowBytes)[4 * v + b];
+          sc[i] = static_cast<const uint32_t*>(is_v ? p.v_scales : p.k_scales)[row];
         }
       }
-    }
 #pragma unroll
-    for (int i = 0; i < kUnroll; ++i) {
-      // the inverse of the append's re-ordering: lane 4 b + v takes the
-      // words (u = 2 v, b) and (u = 2 v + 1, b)
-      const int b = lane16 >> 2, v = lane16 & 3;
-      const uint32_t wa = __shfl_sync(0xffffffffu, w[i], 4 * (b >> 1) + v, 16);
-      const uint32_t wb = __shfl_sync(0xffffffffu, w[i], 4 * (2 + (b >> 1)) + v, 16);
-      uint32_t h2[4];
-      e2m1x8(prmt(wa, wb, (b & 1) ? 0x7632u : 0x5410u), h2);
-      const float s = mx4_scale((sc[i] >> (8 * b)) & 255u);
-      uint32_t out[4];
+      for (int i = 0; i < kUnroll; ++i) {
+        const int r = r0 + 2 * i + half;
+        const bool is_v = r >= p.hkv;
+        // the inverse of the append's re-ordering: lane 4 b + v takes the
+        // words (u = 2 v, b) and (u = 2 v + 1, b)
+        const uint32_t wa = __shfl_sync(0xffffffffu, w[i], 4 * (b >> 1) + v, 16);
+        const uint32_t wb = __shfl_sync(0xffffffffu, w[i], 4 * (2 + (b >> 1)) + v, 16);
+        uint32_t h2[4];
+        e2m1x8(prmt(wa, wb, (b & 1) ? 0x7632u : 0x5410u), h2);
+        const float s = mx4_scale((sc[i] >> (8 * b)) & 255u);
+        uint32_t out[4];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float2 f = Elem<__half>::to_f2(h2[k]);
-        out[k] = Elem<T>::from_f2(f.x * s, f.y * s);
-      }
-      if (dst[i] >= 0) {
-        T* row = static_cast<T*>(is_v[i] ? p.v_out : p.k_out) + dst[i] * PKC_HEAD_DIM;
-        *reinterpret_cast<uint4*>(row + 8 * lane16) = make_uint4(out[0], out[1], out[2], out[3]);
+        for (int k = 0; k < 4; ++k) {
+          const float2 f = Elem<__half>::to_f2(h2[k]);
+          out[k] = Elem<T>::from_f2(f.x * s, f.y * s);
+        }
+        if (r < rows) {
+          T* row = static_cast<T*>(is_v ? p.v_out : p.k_out) + (t * p.hkv + (is_v ? r - p.hkv : r)) * PKC_HEAD_DIM;
+          *reinterpret_cast<uint4*>(row + 8 * lane16) = make_uint4(out[0], out[1], out[2], out[3]);
+        }
       }
     }
   }
 }
 
-int blocks_for(const Mx4RowsParams& p) {
-  const int64_t rows = (int64_t)p.total * 2 * p.hkv;
-  const int64_t want = (rows + kGroups - 1) / kGroups;  // one row per 16 lanes while blocks are few
+// One warp per token; the 8-row parts of a token go to blocks of their own
+// while there are few tokens.
+dim3 grid_for(const Mx4RowsParams& p) {
+  const int parts = (2 * p.hkv + kRows - 1) / kRows;
+  const int64_t want = ((int64_t)p.total + kWarps - 1) / kWarps;
   const int64_t most = (int64_t)num_sms() * (2048 / kThreads);
-  return (int)(want < most ? want : most);
+  if (want * parts <= most && parts <= 65535) return dim3((unsigned)want, (unsigned)parts);
+  return dim3((unsigned)(want < most ? want : most), 1);
 }
 
 }  // namespace
 
 int launch_append_mx4(const Mx4RowsParams& p, int dtype, void* stream) {
   if (p.total <= 0 || p.batch <= 0) return 0;
-  if (dtype == PKC_BF16) append_mx4_kernel<__nv_bfloat16><<<blocks_for(p), kThreads, 0, (cudaStream_t)stream>>>(p);
-  else append_mx4_kernel<__half><<<blocks_for(p), kThreads, 0, (cudaStream_t)stream>>>(p);
+  if (dtype == PKC_BF16) append_mx4_kernel<__nv_bfloat16><<<grid_for(p), kThreads, 0, (cudaStream_t)stream>>>(p);
+  else append_mx4_kernel<__half><<<grid_for(p), kThreads, 0, (cudaStream_t)stream>>>(p);
   return (int)cudaGetLastError();
 }
 
 int launch_gather_mx4(const Mx4RowsParams& p, int dtype, void* stream) {
   if (p.total <= 0 || p.batch <= 0) return 0;
-  if (dtype == PKC_BF16) gather_mx4_kernel<__nv_bfloat16><<<blocks_for(p), kThreads, 0, (cudaStream_t)stream>>>(p);
-  else gather_mx4_kernel<__half><<<blocks_for(p), kThreads, 0, (cudaStream_t)stream>>>(p);
+  if (dtype == PKC_BF16) gather_mx4_kernel<__nv_bfloat16><<<grid_for(p), kThreads, 0, (cudaStream_t)stream>>>(p);
+  else gather_mx4_kernel<__half><<<grid_for(p), kThreads, 0, (cudaStream_t)stream>>>(p);
   return (int)cudaGetLastError();
 }
 

@@ -398,28 +398,39 @@ def _expect_current(t):
         raise ValueError(f"tensors are on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
 
 
-def _expect_bytes(name, t, device):
-    """A byte buffer of any size."""
-    torch = _torch or _t()
-    if not (isinstance(t, torch.Tensor) and t.dtype == torch.uint8 and t.dim() == 1 and t.is_contiguous()
-            and t.device == device):
-        _expect(name, t, (torch.uint8,), (None,), device)
+def _expect_all(device, *specs):
+    """_expect for many tensors of known dtype and shape: specs are
+    (name, tensor, dtype, shape)."""
+    for name, t, dtype, shape in specs:
+        try:
+            if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device:
+                continue
+        except AttributeError:
+            pass  # not a tensor: _expect says so
+        _expect(name, t, (dtype,), shape, device)
+
+
+def _sizes(t, n):
+    """t's sizes, with unknown ones to n where there are fewer (for a check)."""
+    s = getattr(t, "shape", ())
+    return tuple(s) if len(s) == n else (None,) * n
 
 
 def _check_mx4(k_codes, k_scales, v_codes, v_scales, block_table, workspace):
     """The four pools of an mx4 cache, its table and the workspace."""
     torch = _torch or _t()
-    u8 = (torch.uint8,)
-    _expect("k_codes", k_codes, u8, (None, None, None, 64))
-    _expect_current(k_codes)
-    P, ps, Hkv, _ = k_codes.shape
+    u8 = torch.uint8
+    P, ps, Hkv, _ = _sizes(k_codes, 4)
+    B, n_pages = _sizes(block_table, 2)
+    if P is None or not k_codes.is_cuda or k_codes.device.index != torch.cuda.current_device():
+        _expect("k_codes", k_codes, (u8,), (None, None, None, 64))
+        _expect_current(k_codes)
     dev = k_codes.device
-    _expect("v_codes", v_codes, u8, (P, ps, Hkv, 64), dev)
-    _expect("k_scales", k_scales, u8, (P, ps, Hkv, 4), dev)
-    _expect("v_scales", v_scales, u8, (P, ps, Hkv, 4), dev)
-    _expect("block_table", block_table, (torch.int32,), (None, None), dev)
-    _expect_bytes("workspace", workspace, dev)
-    return P, ps, Hkv, block_table.shape[0], dev
+    _expect_all(dev, ("k_codes", k_codes, u8, (P, ps, Hkv, 64)), ("k_scales", k_scales, u8, (P, ps, Hkv, 4)),
+                ("v_codes", v_codes, u8, (P, ps, Hkv, 64)), ("v_scales", v_scales, u8, (P, ps, Hkv, 4)),
+                ("block_table", block_table, torch.int32, (B, n_pages)),
+                ("workspace", workspace, u8, _sizes(workspace, 1)))
+    return P, ps, Hkv, B, dev
 
 
 def append_kv_mx4(k_new, v_new, new_indptr, k_codes, k_scales, v_codes, v_scales, block_table,
@@ -429,10 +440,11 @@ def append_kv_mx4(k_new, v_new, new_indptr, k_codes, k_scales, v_codes, v_scales
     request's mx4 cache and grow cache_seqlens, in place."""
     torch = _torch or _t()
     P, ps, Hkv, B, dev = _check_mx4(k_codes, k_scales, v_codes, v_scales, block_table, workspace)
-    _expect("k_new", k_new, (torch.float16, torch.bfloat16), (None, Hkv, 128), dev)
-    _expect("v_new", v_new, (k_new.dtype,), tuple(k_new.shape), dev)
-    _expect("new_indptr", new_indptr, (torch.int32,), (B + 1,), dev)
-    _expect("cache_seqlens", cache_seqlens, (torch.int32,), (B,), dev)
+    T = _sizes(k_new, 3)[0]
+    _expect("k_new", k_new, (torch.float16, torch.bfloat16), (T, Hkv, 128), dev)
+    _expect_all(dev, ("v_new", v_new, k_new.dtype, (T, Hkv, 128)),
+                ("new_indptr", new_indptr, torch.int32, (B + 1,)),
+                ("cache_seqlens", cache_seqlens, torch.int32, (B,)))
     _check(lib().pkc_append_kv_mx4(
         _ptr(k_new), _ptr(v_new), _ptr(new_indptr), k_new.shape[0], _ptr(k_codes), _ptr(k_scales),
         _ptr(v_codes), _ptr(v_scales), _ptr(block_table), block_table.shape[1], _ptr(cache_seqlens),
@@ -447,8 +459,7 @@ def gather_kv_mx4(k_codes, k_scales, v_codes, v_scales, block_table, first, out_
     as they were in given k and v (and are undefined in new ones)."""
     torch = _torch or _t()
     P, ps, Hkv, B, dev = _check_mx4(k_codes, k_scales, v_codes, v_scales, block_table, workspace)
-    _expect("first", first, (torch.int32,), (B,), dev)
-    _expect("out_indptr", out_indptr, (torch.int32,), (B + 1,), dev)
+    _expect_all(dev, ("first", first, torch.int32, (B,)), ("out_indptr", out_indptr, torch.int32, (B + 1,)))
     if dtype is None:
         dtype = torch.float16 if k is None else k.dtype
     if dtype not in (torch.float16, torch.bfloat16):
@@ -473,9 +484,9 @@ def paged_decode_state_mx4(q, k_codes, k_scales, v_codes, v_scales, block_table,
     """States of fp16 / bf16 q [B, Hq, 128] over each request's mx4 cache."""
     torch = _torch or _t()
     P, ps, Hkv, B, dev = _check_mx4(k_codes, k_scales, v_codes, v_scales, block_table, workspace)
-    _expect("q", q, (torch.float16, torch.bfloat16), (B, None, 128), dev)
-    _expect("cache_seqlens", cache_seqlens, (torch.int32,), (B,), dev)
-    Hq = q.shape[1]
+    Hq = _sizes(q, 3)[1]
+    _expect("q", q, (torch.float16, torch.bfloat16), (B, Hq, 128), dev)
+    _expect_all(dev, ("cache_seqlens", cache_seqlens, torch.int32, (B,)))
     if o is not None:
         _expect("o", o, (q.dtype,), (B, Hq, 128), dev)
     if lse is not None:
@@ -520,15 +531,15 @@ def accumulate_weights(q, lse, k_cache, block_table, cache_seqlens, sm_scale, we
     dev = k_cache.device
     _expect("k_cache", k_cache, (torch.uint8,) if k_scales is not None else (k_cache.dtype,),
             (P, ps, Hkv, row), dev)
+    B, Hq, _ = _sizes(q, 3)
+    _expect("q", q, (torch.float16, torch.bfloat16), (B, Hq, 128), dev)
+    _expect_all(dev, ("lse", lse, torch.float32, (B, Hq)),
+                ("block_table", block_table, torch.int32, (B, _sizes(block_table, 2)[1])),
+                ("cache_seqlens", cache_seqlens, torch.int32, (B,)),
+                ("weights", weights, torch.float32, (B, Hkv, _sizes(weights, 3)[2])),
+                ("workspace", workspace, torch.uint8, _sizes(workspace, 1)))
     if k_scales is not None:
         _expect("k_scales", k_scales, (torch.uint8,), (P, ps, Hkv, 4), dev)
-    _expect("q", q, (torch.float16, torch.bfloat16), (None, None, 128), dev)
-    B, Hq, _ = q.shape
-    _expect("lse", lse, (torch.float32,), (B, Hq), dev)
-    _expect("block_table", block_table, (torch.int32,), (B, None), dev)
-    _expect("cache_seqlens", cache_seqlens, (torch.int32,), (B,), dev)
-    _expect("weights", weights, (torch.float32,), (B, Hkv, None), dev)
-    _expect_bytes("workspace", workspace, dev)
     _check(lib().pkc_accumulate_weights(
         _ptr(q), _ptr(lse), _ptr(k_cache), _ptr(k_scales), _ptr(block_table), block_table.shape[1],
         _ptr(cache_seqlens), B, Hq, Hkv, 128, ps, P, float(sm_scale), float(k_scale), float(decay),
@@ -551,8 +562,8 @@ def evict_select(weights, cache_seqlens, budget, sinks, recent, workspace, keep=
     if budget < 1 or sinks < 0 or recent < 0 or sinks + recent > budget:
         raise ValueError("evict_select: budget must be >= 1, sinks and recent >= 0 and together at most the "
                          f"budget (got {budget}, {sinks}, {recent})")
-    _expect("cache_seqlens", cache_seqlens, (torch.int32,), (B,), dev)
-    _expect_bytes("workspace", workspace, dev)
+    _expect_all(dev, ("cache_seqlens", cache_seqlens, torch.int32, (B,)),
+                ("workspace", workspace, torch.uint8, _sizes(workspace, 1)))
     if keep is not None:
         _expect("keep", keep, (torch.int32,), (B, Hkv, budget), dev)
     keep = torch.empty((B, Hkv, budget), dtype=torch.int32, device=dev) if keep is None else keep
@@ -575,19 +586,18 @@ def evict_compact(keep, k_cache, v_cache, block_table, cache_seqlens, workspace,
     kind, row = _kv_kind(k_cache, k_scales)
     P, ps, Hkv, _ = k_cache.shape
     dev = k_cache.device
-    kv_dtypes = (torch.uint8,) if k_scales is not None else (k_cache.dtype,)
-    _expect("k_cache", k_cache, kv_dtypes, (P, ps, Hkv, row), dev)
-    _expect("v_cache", v_cache, kv_dtypes, (P, ps, Hkv, row), dev)
-    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-        if t is not None:
-            _expect(name, t, (torch.uint8,), (P, ps, Hkv, 4), dev)
-    _expect("keep", keep, (torch.int32,), (None, Hkv, None), dev)
-    B, _, budget = keep.shape
-    _expect("block_table", block_table, (torch.int32,), (B, None), dev)
-    _expect("cache_seqlens", cache_seqlens, (torch.int32,), (B,), dev)
-    _expect_bytes("workspace", workspace, dev)
+    kv_dtype = torch.uint8 if k_scales is not None else k_cache.dtype
+    B, _, budget = _sizes(keep, 3)
+    _expect_all(dev, ("k_cache", k_cache, kv_dtype, (P, ps, Hkv, row)), ("v_cache", v_cache, kv_dtype, (P, ps, Hkv, row)),
+                ("keep", keep, torch.int32, (B, Hkv, budget)),
+                ("block_table", block_table, torch.int32, (B, _sizes(block_table, 2)[1])),
+                ("cache_seqlens", cache_seqlens, torch.int32, (B,)),
+                ("workspace", workspace, torch.uint8, _sizes(workspace, 1)))
+    if k_scales is not None:
+        _expect_all(dev, ("k_scales", k_scales, torch.uint8, (P, ps, Hkv, 4)),
+                    ("v_scales", v_scales, torch.uint8, (P, ps, Hkv, 4)))
     if weights is not None:
-        _expect("weights", weights, (torch.float32,), (B, Hkv, None), dev)
+        _expect_all(dev, ("weights", weights, torch.float32, (B, Hkv, _sizes(weights, 3)[2])))
     _check(lib().pkc_evict_compact(
         _ptr(keep), budget, _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
         _ptr(block_table), block_table.shape[1], _ptr(cache_seqlens), _ptr(weights),

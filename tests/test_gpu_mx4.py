@@ -407,3 +407,48 @@ def test_slots_past_two_gigabytes():
     o, lse = pkc.paged_decode_state_mx4(q, *pools, bt, dl, 0.1, ws)
     check_decode(c, q, o, lse, 1, 0.1, "f16")
     assert pkc.device_status(ws) == pkc.PKC_OK
+
+
+def test_binding_refuses_wrong_device_tensors():
+    """Every tensor of every call: another dtype, another shape, strides."""
+    u8, i32, f32 = torch.uint8, torch.int32, torch.float32
+    z = lambda *s, d=u8: torch.zeros(s, dtype=d, device="cuda")  # noqa: E731
+    pools = [z(4, 16, 2, 64), z(4, 16, 2, 4), z(4, 16, 2, 64), z(4, 16, 2, 4)]
+    bt, lens, ws, ip = z(3, 4, d=i32), z(3, d=i32), ws_for(3, 4), z(4, d=i32)
+    x, q, lse, w = z(5, 2, 128, d=torch.float16), z(3, 4, 128, d=torch.float16), z(3, 4, d=f32), z(3, 2, 64, d=f32)
+    k16, keep = z(4, 16, 2, 128, d=torch.float16), z(3, 2, 8, d=i32)
+    calls = [
+        (pkc.append_kv_mx4, [x, x, ip, *pools, bt, lens, ws]),
+        (pkc.gather_kv_mx4, [*pools, bt, lens, ip, 5, ws]),
+        (pkc.paged_decode_state_mx4, [q, *pools, bt, lens, 0.1, ws]),
+        (pkc.accumulate_weights, [q, lse, k16, bt, lens, 0.1, w, ws]),
+        (pkc.evict_select, [w, lens, 8, 1, 1, ws]),
+        (pkc.evict_compact, [keep, k16, k16.clone(), bt, lens, ws]),
+    ]
+    for fn, args in calls:
+        fn(*args)  # (lengths 0: nothing happens)
+        for i, t in enumerate(args):
+            if not isinstance(t, torch.Tensor):
+                continue
+            doubled = torch.zeros(t.shape[:-1] + (2 * t.shape[-1],), dtype=t.dtype, device="cuda")[..., ::2]
+            bad = [t.to(torch.float64), t[None], t.cpu(), doubled, "tensor", None]
+            # one more row: refused but where that tensor alone gives the size (new rows, a pool's pages)
+            alone = (fn is pkc.append_kv_mx4 and i == 0) or (fn is pkc.accumulate_weights and i == 2)
+            if t is not ws and not alone:
+                bad.append(torch.cat([t, t[:1]]))
+            for b in bad:
+                with pytest.raises((TypeError, ValueError, AttributeError)):
+                    fn(*args[:i], b, *args[i + 1:])
+                    print(fn.__name__, i, b)  # (shown when nothing was raised)
+    assert pkc.device_status(ws) == pkc.PKC_OK
+    with pytest.raises((TypeError, ValueError)):
+        pkc.gather_kv_mx4(*pools, bt, lens, ip, 5, ws, dtype=f32)
+    with pytest.raises(ValueError):
+        pkc.gather_kv_mx4(*pools, bt, lens, ip, -1, ws)
+    with pytest.raises(ValueError):
+        pkc.evict_select(w, lens, 8, 5, 4, ws)
+    with pytest.raises(ValueError):
+        pkc.evict_compact(keep, pools[0], pools[2], bt, lens, ws, k_scales=pools[1])
+    for bad in (dict(decay=1.5), dict(decay=float("nan")), dict(k_scale=2.0)):
+        with pytest.raises(pkc.PkcError):
+            pkc.accumulate_weights(q, lse, k16, bt, lens, 0.1, w, ws, **bad)

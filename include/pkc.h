@@ -636,8 +636,9 @@ int pkc_accumulate_weights(const void* q, const float* lse,
  * `recent` with the largest weights (of equal weights the lower slot; NaN
  * counts as larger than any number, -0 as 0), and the last `recent`, all in
  * ascending order; for any other request 0 .. length - 1, then -1.
- * budget >= 1, sinks >= 0, recent >= 0, sinks + recent <= budget.  A request
- * longer than weights_stride gets -1 throughout (PKC_ERR_PLAN).
+ * budget >= 1, sinks >= 0, recent >= 0, sinks + recent <= budget;
+ * weights_stride <= 2^22 (PKC_ERR_UNSUPPORTED above).  A request longer than
+ * weights_stride gets -1 throughout (PKC_ERR_PLAN).
  */
 int pkc_evict_select(const float* weights, int64_t weights_stride,
                      const int32_t* cache_seqlens, int batch, int num_kv_heads,

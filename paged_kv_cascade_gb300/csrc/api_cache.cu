@@ -218,6 +218,8 @@ int pkc_evict_select(const float* weights, int64_t weights_stride, const int32_t
                      "evict_select: budget must be >= 1, sinks and recent >= 0 and together at most the budget "
                      "(got %d, %d, %d)",
                      budget, sinks, recent);
+  if (weights_stride > (int64_t)1 << 22)
+    return set_error(PKC_ERR_UNSUPPORTED, "evict_select: rows of more than 2^22 weights");
   if ((int64_t)batch * num_kv_heads > INT32_MAX / 8)
     return set_error(PKC_ERR_UNSUPPORTED, "evict_select: more than 2^28 rows");
   if (int rc = check_ws(workspace, workspace_bytes, PKC_STATUS_BYTES)) return rc;

@@ -8,11 +8,15 @@
 // two zeros equal), and the m-th largest key T is found digit by digit from
 // the top (11 + 11 + 10 bits): a histogram of the keys that agree with the
 // digits found so far, and the bin in which the count from above reaches m.
-// One more pass over the keys, in order, gives each kept slot its rank.  The
-// weights are read from memory once, into shared memory; a row is worked on
-// by a cluster of up to 8 blocks, which add up their histograms through
-// distributed shared memory, so that few long rows use the machine too.
-// What bounds it is the chain of passes and barriers per row, not HBM.
+// The first histogram reads the weights from memory; a second read (L2) sets
+// a bit for every key above the bin and lists the keys in it, a percent or
+// so, on which the other digits work (they read the weights again if the
+// list is too short, as for a row of equal weights).  Then the bits of the
+// kept slots are ranked: a thread per 32 of them, one scan.  A row takes
+// about 30 KB of shared memory, so four blocks share an SM; a cluster of up
+// to 8 blocks works on one row where there are few, adding up their
+// histograms through distributed shared memory.  What bounds it is the chain
+// of reads and barriers per row, not HBM.
 //
 // Compact.  Row j of a (request, head) becomes row keep[j]; keep ascends
 // strictly, so keep[j] >= j.  A block moves one slice of one head's K or V
@@ -39,8 +43,12 @@ namespace {
 
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
-constexpr int kBins = 2048;
-constexpr uint32_t kZeroKey = 0x80000000u;  // the key of weight 0
+constexpr int kBins = 4 * kSelThreads;  // (of 11 bits: four per thread where a digit's bin is looked for)
+static_assert(kBins == 2048, "digits of 11 bits");
+constexpr int kBatch = 8;                    // keys a thread has in flight
+constexpr int kListed = 1536;                // keys of a digit's bin that a block lists
+constexpr int kMostKeys = 1 << 19;           // keys of one block (two bits each in shared memory)
+constexpr uint32_t kZeroKey = 0x80000000u;   // the key of weight 0
 
 __device__ __forceinline__ uint32_t order_key(float w) {
   if (w != w) return 0xffffffffu;
@@ -49,113 +57,158 @@ __device__ __forceinline__ uint32_t order_key(float w) {
 }
 
 struct SelectShared {
+  uint32_t hist[2][kBins];     // alternate between digits: one barrier per digit
+  uint2 list[kListed];         // (key, index) of the first digit's bin
   int warp_sum[kSelWarps];
-  int gt[kSelWarps], eq[kSelWarps];
   int cta_gt, cta_eq;
-  int bin, rest;
+  int bin, rest, n_listed;
+  int pad[3];
 };
-static_assert(sizeof(SelectShared) % 16 == 0, "what follows is read 16 bytes at a time");
 
-// Shared memory: SelectShared, one histogram (two, alternating, when several
-// blocks share a row: then one cluster barrier per digit is enough), keys.
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectParams p) {
+// Shared memory: SelectShared, then two bits per key (kept for certain; equal
+// to T), then the keys where there are no more rows than SMs: those rows are
+// read once, as a block has an SM to itself (131072 weights: 33 -> 27 us),
+// while in a batch more blocks per SM are worth more (28 against 33 us).
+__global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const SelectParams p) {
   extern __shared__ __align__(16) uint8_t smem_sel[];
   SelectShared& S = *reinterpret_cast<SelectShared*>(smem_sel);
-  uint32_t* hists = reinterpret_cast<uint32_t*>(smem_sel + sizeof(SelectShared));
-  const int n_cta = p.cluster, n_hist = n_cta > 1 ? 2 : 1;
-  uint32_t* keys = hists + n_hist * kBins;
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)(blockIdx.x % n_cta);
+  const int n_cta = p.cluster, rank = (int)(blockIdx.x % n_cta);
   const int row = (int)(blockIdx.x / n_cta), b = row / p.hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int32_t* keep = p.keep + (int64_t)row * p.budget;
-  const float* w = p.weights + (int64_t)row * p.w_stride;
   int len = p.cache_seqlens[b];
-  const int at = rank * kSelThreads + tid, all = n_cta * kSelThreads;  // this thread in the row's cluster
 
   if (len > p.w_stride) {  // (uniform over the cluster, as every early return)
-    if (at == 0) report(p.status, PKC_ERR_PLAN);
+    if (rank == 0 && tid == 0) report(p.status, PKC_ERR_PLAN);
     len = 0;
   }
   if (len <= p.budget) {
-    for (int j = at; j < p.budget; j += all) keep[j] = j < len ? j : -1;
+    for (int j = rank * kSelThreads + tid; j < p.budget; j += n_cta * kSelThreads) keep[j] = j < len ? j : -1;
     return;
   }
   const int n = len - p.sinks - p.recent;       // slots to choose from
   const int m = p.budget - p.sinks - p.recent;  // slots to choose, m < n
-  for (int j = at; j < p.sinks; j += all) keep[j] = j;
-  for (int j = at; j < p.recent; j += all) keep[p.budget - p.recent + j] = len - p.recent + j;
+  for (int j = rank * kSelThreads + tid; j < p.sinks; j += n_cta * kSelThreads) keep[j] = j;
+  for (int j = rank * kSelThreads + tid; j < p.recent; j += n_cta * kSelThreads)
+    keep[p.budget - p.recent + j] = len - p.recent + j;
   if (m == 0) return;
 
-  // This block's part of the choice: keys [lo, lo + mine).  In shared memory
-  // it is padded to whole groups of 4 with key 0, which no weight has but a
-  // negative NaN's bits (order_key gives NaN the largest): never chosen.
-  const int per = (n + n_cta - 1) / n_cta;
+  // This block's part of the choice: keys [lo, lo + mine), 32 to a word.
+  const int per = ((n + n_cta - 1) / n_cta + 31) & ~31;
   const int lo = min(rank * per, n), mine = min(per, n - lo);
+  const float* src = p.weights + (int64_t)row * p.w_stride + p.sinks + lo;
+  const int words = (mine + 31) >> 5;
+  uint32_t* sure = reinterpret_cast<uint32_t*>(smem_sel + sizeof(SelectShared));
+  uint32_t* equal = sure + words;
+  uint32_t* keys = equal + words;  // the keys themselves, where the launch gave them room
   const bool cached = mine <= p.smem_keys;
-  const float* src = w + p.sinks + lo;
-  const int quads = (mine + 3) >> 2;
-  auto quad_at = [&](int q) -> uint4 {  // keys 4 q .. 4 q + 3
-    if (cached) return *reinterpret_cast<const uint4*>(keys + 4 * q);
-    uint32_t k[4];
-#pragma unroll
-    for (int x = 0; x < 4; ++x) k[x] = 4 * q + x < mine ? order_key(src[4 * q + x]) : 0u;
-    return make_uint4(k[0], k[1], k[2], k[3]);
-  };
-  for (int i = tid; i < n_hist * kBins; i += kSelThreads) hists[i] = 0;
+  for (int i = tid; i < 2 * kBins; i += kSelThreads) (&S.hist[0][0])[i] = 0;
+  if (tid == 0) S.n_listed = 0;
   __syncthreads();
 
-  // First digit, as the keys come in.  Weights that are exactly 0 are often
-  // most of a row: each warp counts them apart, so they do not queue up on
-  // one bin.
+  // kBatch keys of this lane, a block's width apart, all loads in flight
+  // together (a shared-memory atomic between two loads would hold the second
+  // one back); 0, which no weight has, past the end.
+  auto load_keys = [&](uint32_t (&k)[kBatch], int i, bool again) {
+    if (again && cached) {
+#pragma unroll
+      for (int x = 0; x < kBatch; ++x) k[x] = i + x * kSelThreads < mine ? keys[i + x * kSelThreads] : 0u;
+      return;
+    }
+    float f[kBatch];
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) f[x] = i + x * kSelThreads < mine ? src[i + x * kSelThreads] : 0.f;
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) k[x] = i + x * kSelThreads < mine ? order_key(f[x]) : 0u;
+  };
+
+  // First digit.  Weights that are exactly 0 are often most of a row: each
+  // warp counts them apart, so they do not queue up on one bin.
   int zeros = 0;
-#pragma unroll 8
-  for (int i0 = warp * 32; i0 < 4 * quads; i0 += kSelThreads) {
-    const int i = i0 + lane;
-    const uint32_t k = i < mine ? order_key(__ldcs(src + i)) : 0u;
-    if (cached && i < 4 * quads) keys[i] = k;
-    zeros += __popc(__ballot_sync(0xffffffffu, k == kZeroKey));
-    if (i < mine && k != kZeroKey) atomicAdd(&hists[k >> 21], 1u);
+  for (int i0 = warp * 32; i0 < mine; i0 += kBatch * kSelThreads) {
+    uint32_t k[kBatch];
+    load_keys(k, i0 + lane, false);
+#pragma unroll
+    for (int x = 0; x < kBatch; ++x) {
+      if (cached && k[x] != 0u) keys[i0 + lane + x * kSelThreads] = k[x];
+      zeros += __popc(__ballot_sync(0xffffffffu, k[x] == kZeroKey));
+      if (k[x] != 0u && k[x] != kZeroKey) atomicAdd(&S.hist[0][k[x] >> 21], 1u);
+    }
   }
-  if (lane == 0 && zeros) atomicAdd(&hists[kZeroKey >> 21], (uint32_t)zeros);
+  if (lane == 0 && zeros) atomicAdd(&S.hist[0][kZeroKey >> 21], (uint32_t)zeros);
 
   uint32_t prefix = 0;  // digits found, in place
   int rest = m;         // to be chosen among the keys that agree with them
+  bool listed = true;   // the list holds all keys of the first digit's bin
   for (int d = 0; d < 3; ++d) {
     const int shift = d == 0 ? 21 : d == 1 ? 10 : 0, width = d == 2 ? 10 : 11;
-    uint32_t* hist = hists + (n_cta > 1 ? (d & 1) * kBins : 0);
-    if (d > 0) {
-      const uint32_t want = prefix >> (shift + width), mask = (1u << width) - 1u;
-      if (!cached) __syncthreads();
-      for (int q = tid; q < quads; q += kSelThreads) {
-        const uint4 k4 = quad_at(q);
-        const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+    uint32_t* hist = S.hist[d & 1];
+    const uint32_t want = d == 0 ? 0u : prefix >> (shift + width), mask = (1u << width) - 1u;
+    if (d == 1) {  // the second read: bits of the keys above, list of the keys in the bin
+      for (int w0 = warp; w0 < words; w0 += kBatch * kSelWarps) {
+        uint32_t k[kBatch];
+        load_keys(k, 32 * w0 + lane, true);
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          if ((k[x] >> (shift + width)) == want && k[x] != kZeroKey) atomicAdd(&hist[(k[x] >> shift) & mask], 1u);
+        for (int x = 0; x < kBatch; ++x) {
+          const int wd = w0 + x * kSelWarps;
+          const uint32_t top = k[x] >> 21;
+          const uint32_t above = __ballot_sync(0xffffffffu, top > want);
+          const uint32_t zero = __ballot_sync(0xffffffffu, k[x] == kZeroKey && top == want);
+          if (lane == 0 && wd < words) {
+            sure[wd] = above;
+            equal[wd] = zero;
+          }
+          if (top == want && k[x] != 0u && k[x] != kZeroKey) {  // (zeros are counted already, and never listed)
+            const int at = atomicAdd(&S.n_listed, 1);
+            if (at < kListed) S.list[at] = make_uint2(k[x], (uint32_t)(32 * wd + lane));
+            atomicAdd(&hist[(k[x] >> shift) & mask], 1u);
+          }
+        }
       }
-      if (lane == 0 && zeros && (kZeroKey >> (shift + width)) == want)
-        atomicAdd(&hist[(kZeroKey >> shift) & mask], (uint32_t)zeros);
+      __syncthreads();
+      listed = S.n_listed <= kListed;
+    } else if (d == 2) {
+      if (listed) {
+        for (int i = tid; i < S.n_listed; i += kSelThreads) {
+          const uint32_t k = S.list[i].x;
+          if ((k >> (shift + width)) == want) atomicAdd(&hist[(k >> shift) & mask], 1u);
+        }
+      } else {
+        for (int i = tid; i < mine; i += kSelThreads) {
+          const uint32_t k = order_key(src[i]);
+          if ((k >> (shift + width)) == want && k != kZeroKey) atomicAdd(&hist[(k >> shift) & mask], 1u);
+        }
+      }
     }
+    if (d > 0 && lane == 0 && zeros && (kZeroKey >> (shift + width)) == want)
+      atomicAdd(&hist[(kZeroKey >> shift) & mask], (uint32_t)zeros);
     if (n_cta > 1) cluster.sync();  // every block's histogram is complete
     else __syncthreads();
     // Counts of this thread's four bins, from the top: thread 0 has the highest.
     const int bin0 = kBins - 4 - 4 * tid;
-    uint4 cnt = *reinterpret_cast<const uint4*>(hist + bin0);
+    int cnt[4];
+    {
+      const uint4 x = *reinterpret_cast<const uint4*>(hist + bin0);
+      cnt[0] = x.w; cnt[1] = x.z; cnt[2] = x.y; cnt[3] = x.x;
+    }
     if (n_cta > 1) {
-      uint4 c[8];
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        c[x] = make_uint4(0, 0, 0, 0);
-        if (x < n_cta && x != rank)
-          c[x] = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(hist, x) + bin0);
-      }
+      for (int c0 = 0; c0 < 8; c0 += 4) {
+        uint4 x[4];
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        cnt.x += c[x].x; cnt.y += c[x].y; cnt.z += c[x].z; cnt.w += c[x].w;
+        for (int c = 0; c < 4; ++c) {
+          x[c] = make_uint4(0, 0, 0, 0);
+          if (c0 + c < n_cta && c0 + c != rank)
+            x[c] = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(hist, c0 + c) + bin0);
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          cnt[0] += x[c].w; cnt[1] += x[c].z; cnt[2] += x[c].y; cnt[3] += x[c].x;
+        }
       }
     }
-    const int sum = (int)(cnt.x + cnt.y + cnt.z + cnt.w);
+    const int sum = cnt[0] + cnt[1] + cnt[2] + cnt[3];
     int above = sum;  // inclusive scan over the block
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) {
@@ -168,95 +221,103 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectP
       S.rest = rest;
     }
     __syncthreads();
-    int before = 0;
+    above -= sum;  // keys in higher bins than this thread's
 #pragma unroll
-    for (int x = 0; x < kSelWarps; ++x) before += x < warp ? S.warp_sum[x] : 0;
-    above += before - sum;  // keys in higher bins than this thread's
+    for (int x = 0; x < kSelWarps; ++x) above += x < warp ? S.warp_sum[x] : 0;
     if (above < rest && rest <= above + sum) {  // exactly one thread
-      const int c[4] = {(int)cnt.w, (int)cnt.z, (int)cnt.y, (int)cnt.x};
 #pragma unroll
       for (int x = 0; x < 4; ++x) {
-        if (above < rest && rest <= above + c[x]) {
+        if (above < rest && rest <= above + cnt[x]) {
           S.bin = bin0 + 3 - x;
           S.rest = rest - above;
         }
-        above += c[x];
+        above += cnt[x];
       }
     }
-    // The next digit's histogram: with one, this; with two, the one before,
-    // which every block is past at this digit's barrier.
-    if (d < 2 && (n_cta == 1 || d == 1))
-      for (int i = tid; i < kBins; i += kSelThreads) hists[i] = 0;
+    if (d == 1)  // the third digit's histogram is the first's: every block is past it
+      for (int i = tid; i < kBins; i += kSelThreads) S.hist[0][i] = 0;
     __syncthreads();
     prefix |= (uint32_t)S.bin << shift;
     rest = S.rest;
-    __syncthreads();
   }
-  // Keys above T = prefix are kept, and the first `rest` of those equal to it.
-  // Each warp takes a consecutive part: counts, then ranks.
-  const int part = (quads + kSelWarps * 32 - 1) / (kSelWarps * 32) * 32;  // in groups of 4
-  const int w_lo = min(warp * part, quads), w_hi = min(w_lo + part, quads);
-  int gt = 0, eq = 0;
-  for (int q = w_lo + lane; q < w_hi; q += 32) {
-    const uint4 k = quad_at(q);
-    gt += (k.x > prefix) + (k.y > prefix) + (k.z > prefix) + (k.w > prefix);
-    eq += (k.x == prefix) + (k.y == prefix) + (k.z == prefix) + (k.w == prefix);
-  }
-  gt = __reduce_add_sync(0xffffffffu, gt);
-  eq = __reduce_add_sync(0xffffffffu, eq);
-  if (lane == 0) {
-    S.gt[warp] = gt;
-    S.eq[warp] = eq;
-  }
-  __syncthreads();
-  int gt0 = 0, eq0 = 0;  // before this warp's part
-  for (int x = 0; x < warp; ++x) {
-    gt0 += S.gt[x];
-    eq0 += S.eq[x];
-  }
-  if (n_cta > 1) {
-    if (tid == kSelThreads - 1) {
-      S.cta_gt = gt0 + gt;
-      S.cta_eq = eq0 + eq;
+  // T = prefix.  Keys above T are kept, and the first `rest` of those equal
+  // to it.  The bits so far: `sure` has the keys above the first digit's bin,
+  // `equal` that bin's zeros; now the bin's other keys.
+  if (listed) {
+    if (prefix != kZeroKey) {
+      for (int i = tid; i < words; i += kSelThreads) equal[i] = 0u;
+      __syncthreads();
     }
-    cluster.sync();
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      if (c < rank) {
-        const SelectShared* o = cluster.map_shared_rank(&S, c);
-        gt0 += o->cta_gt;
-        eq0 += o->cta_eq;
+    for (int i = tid; i < S.n_listed; i += kSelThreads) {
+      const uint2 k = S.list[i];
+      if (k.x > prefix) atomicOr(&sure[k.y >> 5], 1u << (k.y & 31));
+      else if (k.x == prefix) atomicOr(&equal[k.y >> 5], 1u << (k.y & 31));
+    }
+  } else {
+    for (int wd = warp; wd < words; wd += kSelWarps) {
+      const int i = 32 * wd + lane;
+      const uint32_t k = i < mine ? order_key(src[i]) : 0u;
+      const uint32_t g = __ballot_sync(0xffffffffu, k > prefix), e = __ballot_sync(0xffffffffu, k == prefix && i < mine);
+      if (lane == 0) {
+        sure[wd] = g;
+        equal[wd] = e;
       }
     }
   }
-  for (int q0 = w_lo; q0 < w_hi; q0 += 32) {
-    const int q = q0 + lane;
-    const uint4 k4 = q < w_hi ? quad_at(q) : make_uint4(0, 0, 0, 0);
-    const uint32_t k[4] = {k4.x, k4.y, k4.z, k4.w};
+  __syncthreads();
+  // Keys above and equal in the blocks before this one.
+  int gt0 = 0, eq0 = 0;
+  if (n_cta > 1) {
     int g = 0, e = 0;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      g += k[x] > prefix;
-      e += q < w_hi && k[x] == prefix;
+    for (int i = tid; i < words; i += kSelThreads) {
+      g += __popc(sure[i]);
+      e += __popc(equal[i]);
     }
-    int scan = g | (e << 16);  // both counts of at most 128
-#pragma unroll
-    for (int x = 1; x < 32; x <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, scan, x);
-      if (lane >= x) scan += y;
+    g = __reduce_add_sync(0xffffffffu, g);
+    e = __reduce_add_sync(0xffffffffu, e);
+    if (tid == 0) S.cta_gt = S.cta_eq = 0;
+    __syncthreads();
+    if (lane == 0) {
+      atomicAdd(&S.cta_gt, g);
+      atomicAdd(&S.cta_eq, e);
     }
-    const int total = __shfl_sync(0xffffffffu, scan, 31);
-    int gr = gt0 + (scan & 0xffff) - g, er = eq0 + (scan >> 16) - e;
-#pragma unroll
-    for (int x = 0; x < 4; ++x) {
-      const bool is_gt = k[x] > prefix, is_eq = q < w_hi && k[x] == prefix;
-      const int rank_of = gr + min(er, rest);  // (below m, unless the weights change under the kernel)
-      if ((is_gt || (is_eq && er < rest)) && rank_of < m) keep[p.sinks + rank_of] = p.sinks + lo + 4 * q + x;
-      gr += is_gt;
-      er += is_eq;
+    cluster.sync();
+    for (int c = 0; c < rank; ++c) {
+      const SelectShared* o = cluster.map_shared_rank(&S, c);
+      gt0 += o->cta_gt;
+      eq0 += o->cta_eq;
     }
+  }
+  // Ranks: a thread per word, 512 words at a time.
+  for (int w0 = 0; w0 < words; w0 += kSelThreads) {
+    const int wd = w0 + tid;
+    const uint32_t s = wd < words ? sure[wd] : 0u;
+    uint32_t x = wd < words ? equal[wd] : 0u;
+    const int both = __popc(s) | (__popc(x) << 16);  // (512 words have at most 2^14 of each)
+    int scan = both;
+#pragma unroll
+    for (int y = 1; y < 32; y <<= 1) {
+      const int z = __shfl_up_sync(0xffffffffu, scan, y);
+      if (lane >= y) scan += z;
+    }
+    if (lane == 31) S.warp_sum[warp] = scan;
+    __syncthreads();
+    int before = scan - both, total = 0;
+#pragma unroll
+    for (int y = 0; y < kSelWarps; ++y) {
+      const int z = S.warp_sum[y];
+      before += y < warp ? z : 0;
+      total += z;
+    }
+    const int er = eq0 + (before >> 16);
+    int pos = gt0 + (before & 0xffff) + min(er, rest);
+    const int spare = (int)__popc(x) - max(min(rest - er, (int)__popc(x)), 0);  // equal ones not taken: the last
+    for (int y = 0; y < spare; ++y) x ^= 0x80000000u >> __clz(x);
+    for (uint32_t all = s | x; all != 0u; all &= all - 1u, ++pos)
+      if (pos < m) keep[p.sinks + pos] = p.sinks + lo + 32 * wd + __ffs(all) - 1;  // (always, unless the weights change under the kernel)
     gt0 += total & 0xffff;
     eq0 += total >> 16;
+    __syncthreads();  // warp_sum is free
   }
   if (n_cta > 1) cluster.sync();  // no block leaves while another reads its counts
 }
@@ -430,12 +491,15 @@ int launch_evict_select(const SelectParams& p_in, void* stream) {
   const int64_t rows = (int64_t)p.batch * p.hkv;
   if (rows <= 0) return 0;
   // Blocks per row: doubled while the machine has room for them and each
-  // still has 2048 keys of the longest row.
+  // still has 2048 keys of the longest row (or more than its bits hold).
   p.cluster = 1;
-  while (p.cluster < 8 && rows * p.cluster * 2 <= num_sms() && p.w_stride / (2 * p.cluster) >= 2048) p.cluster *= 2;
-  const int64_t per = (p.w_stride + p.cluster - 1) / p.cluster;
-  p.smem_keys = (int)std::min<int64_t>((per + 3) & ~int64_t(3), 48 * 1024);
-  const int smem = (int)sizeof(SelectShared) + 4 * kBins * (p.cluster > 1 ? 2 : 1) + 4 * p.smem_keys;
+  while (p.cluster < 8 && ((rows * p.cluster * 2 <= num_sms() && p.w_stride / (2 * p.cluster) >= 2048) ||
+                           p.w_stride / p.cluster > kMostKeys))
+    p.cluster *= 2;
+  const int64_t per = ((p.w_stride + p.cluster - 1) / p.cluster + 31) & ~int64_t(31);
+  if (per > kMostKeys) return (int)cudaErrorInvalidValue;
+  p.smem_keys = rows * p.cluster <= num_sms() && per <= 32 * 1024 ? (int)per : 0;
+  const int smem = (int)sizeof(SelectShared) + (int)(per / 32) * 8 + 4 * p.smem_keys;
   cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return (int)e;
   cudaLaunchConfig_t cfg = {};

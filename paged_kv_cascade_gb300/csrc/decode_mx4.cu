@@ -185,11 +185,17 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     float m0 = kRefFloor, m1 = kRefFloor, l0 = 0.f, l1 = 0.f;  // l: times 2^kLift
     int e_ref = 0;                                             // E_b of block lane % 4
 
-    // Per lane: pools at this head's (and, of codes, this lane's) bytes.
-    const uint8_t* k_lane = static_cast<const uint8_t*>(p.k_cache) + kvh * kMx4RowBytes + 16 * tg;
-    const uint8_t* v_lane = static_cast<const uint8_t*>(p.v_cache) + kvh * kMx4RowBytes + 16 * tg;
-    const uint8_t* s_lane = static_cast<const uint8_t*>(lane < 16 ? mp.k_scales : mp.v_scales) + kvh * 4;
+    // Per lane, the pools at this head's bytes of token 0 and (aligned) the
+    // lane's offset within a tile: codes at token g, piece tg, scales at token
+    // lane % 16.  A tile's addresses follow from its first token by one wide
+    // multiply-add and additions of uniform values.
     const uint32_t code_stride = (uint32_t)p.hkv * kMx4RowBytes, scale_stride = (uint32_t)p.hkv * 4;
+    const uint64_t k_lane = reinterpret_cast<uint64_t>(p.k_cache) + kvh * kMx4RowBytes + 16 * tg +
+                            (kAligned ? (uint64_t)g * code_stride : 0u);
+    const uint64_t s_lane = reinterpret_cast<uint64_t>(lane < 16 ? mp.k_scales : mp.v_scales) + kvh * 4 +
+                            (kAligned ? (uint64_t)(lane & 15) * scale_stride : 0u);
+    const uint64_t v_minus_k = reinterpret_cast<uint64_t>(p.v_cache) - reinterpret_cast<uint64_t>(p.k_cache);
+    const uint64_t code_8 = (uint64_t)code_stride * 8;
     uint32_t st_in = ring;  // stage of the next tile to be copied
     // Tokens that are there, of the tiles in flight, the latest in the low
     // bits: one bit per tile (aligned), or 16.
@@ -209,20 +215,20 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
           const uint32_t first = __shfl_sync(0xffffffffu, win, j & 31);
           if (first != kNoToken) {
             present |= 1u;
-            const uint32_t ta = first + g, tb = ta + 8;
-            cp_async16(dst, at_row(k_lane, ta, code_stride), true);
-            cp_async16(dst + 512, at_row(k_lane, tb, code_stride), true);
-            cp_async16(dst + kCodes, at_row(v_lane, ta, code_stride), true);
-            cp_async16(dst + kCodes + 512, at_row(v_lane, tb, code_stride), true);
+            const uint64_t ka = row_at(k_lane, first, code_stride), kb = ka + code_8;
+            cp_async16(dst, ka);
+            cp_async16(dst + 512, kb);
+            cp_async16(dst + kCodes, ka + v_minus_k);
+            cp_async16(dst + kCodes + 512, kb + v_minus_k);
             // scales of slots outside the chunk become 0: whatever they hold
             // must not count among the largest
             const int t = (tile0 + j * wph) * kTile + (lane & 15);
-            cp_async4(dst_s, at_row(s_lane, first + (lane & 15), scale_stride), t >= it.kb && t < it.ke);
+            cp_async4(dst_s, row_at(s_lane, first, scale_stride), t >= it.kb && t < it.ke);
           } else {  // no such page: zeros
             cp_async16(dst, k_lane, false);
             cp_async16(dst + 512, k_lane, false);
-            cp_async16(dst + kCodes, v_lane, false);
-            cp_async16(dst + kCodes + 512, v_lane, false);
+            cp_async16(dst + kCodes, k_lane, false);
+            cp_async16(dst + kCodes + 512, k_lane, false);
             cp_async4(dst_s, s_lane, false);
           }
         } else {
@@ -231,12 +237,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
           const uint32_t ta = __shfl_sync(0xffffffffu, ts, g), tb = __shfl_sync(0xffffffffu, ts, g + 8);
           win = load_tokens(j + 1);
           const bool oka = ta != kNoToken, okb = tb != kNoToken, oks = ts != kNoToken;
-          const uint64_t at_a = oka ? (uint64_t)ta * code_stride : 0u, at_b = okb ? (uint64_t)tb * code_stride : 0u;
-          cp_async16(dst, k_lane + at_a, oka);
-          cp_async16(dst + 512, k_lane + at_b, okb);
-          cp_async16(dst + kCodes, v_lane + at_a, oka);
-          cp_async16(dst + kCodes + 512, v_lane + at_b, okb);
-          cp_async4(dst_s, s_lane + (oks ? (uint64_t)ts * scale_stride : 0u), oks);
+          const uint64_t ka = row_at(k_lane, oka ? ta : 0u, code_stride), kb = row_at(k_lane, okb ? tb : 0u, code_stride);
+          cp_async16(dst, ka, oka);
+          cp_async16(dst + 512, kb, okb);
+          cp_async16(dst + kCodes, ka + v_minus_k, oka);
+          cp_async16(dst + kCodes + 512, kb + v_minus_k, okb);
+          cp_async4(dst_s, row_at(s_lane, oks ? ts : 0u, scale_stride), oks);
         }
       }
       cp_async_commit();
@@ -307,9 +313,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const int b = 2 * half + x;
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            float acc[4];
             const uint32_t f0[4] = {a0[2 * x], c0[2 * x], a0[2 * x + 1], c0[2 * x + 1]};
-            mma16816<__half>(acc, f0, qf[b][0], qf[b][1]);
+            mma16816_f16_new(acc, f0, qf[b][0], qf[b][1]);
             const uint32_t f1[4] = {a1[2 * x], c1[2 * x], a1[2 * x + 1], c1[2 * x + 1]};
             mma16816<__half>(acc, f1, qf[b][2], qf[b][3]);
             s[0] = fmaf(acc[0], __uint_as_float(fka[b]), s[0]);

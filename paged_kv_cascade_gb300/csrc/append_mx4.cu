@@ -68,54 +68,56 @@ __global__ void __launch_bounds__(kThreads) append_mx4_kernel(const Mx4RowsParam
   const int rows = 2 * p.hkv, n_warps = (int)gridDim.x * kWarps;
   bool any_bad = false;
   for (int64_t t = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5); t < p.total; t += n_warps) {
+    const int64_t src0 = t * p.hkv * PKC_HEAD_DIM + 8 * lane16;  // (V's row r is its head r - Hkv)
+    const T* k_src = static_cast<const T*>(p.k_rows) + src0;
+    const T* v_src = static_cast<const T*>(p.v_rows) + src0 - p.hkv * PKC_HEAD_DIM;
     Place at{-1, false};
+    uint8_t *k_dst = nullptr, *v_dst = nullptr, *k_sc = nullptr, *v_sc = nullptr;
     for (int r0 = (int)blockIdx.y * kRows; r0 < rows; r0 += (int)gridDim.y * kRows) {
       uint4 x[kUnroll];
 #pragma unroll
       for (int i = 0; i < kUnroll; ++i) {
         const int r = r0 + 2 * i + half;
-        const bool is_v = r >= p.hkv;
-        const T* src = static_cast<const T*>(is_v ? p.v_rows : p.k_rows) +
-                       (t * p.hkv + (is_v ? r - p.hkv : r)) * PKC_HEAD_DIM + 8 * lane16;
-        x[i] = r < rows ? ldg_stream(src) : make_uint4(0, 0, 0, 0);
+        x[i] = r < rows ? ldg_stream((r >= p.hkv ? v_src : k_src) + r * PKC_HEAD_DIM) : make_uint4(0, 0, 0, 0);
       }
       if (r0 == (int)blockIdx.y * kRows) {
         at = place_of(p, (int)t);
         any_bad = any_bad || at.bad;
+        const int64_t row0 = at.slot * p.hkv;
+        k_dst = static_cast<uint8_t*>(p.k_codes) + row0 * kMx4RowBytes + 16 * v + 4 * j;
+        v_dst = static_cast<uint8_t*>(p.v_codes) + (row0 - p.hkv) * kMx4RowBytes + 16 * v + 4 * j;
+        k_sc = static_cast<uint8_t*>(p.k_scales) + row0 * 4 + j;
+        v_sc = static_cast<uint8_t*>(p.v_scales) + (row0 - p.hkv) * 4 + j;
       }
 #pragma unroll
       for (int i = 0; i < kUnroll; ++i) {
         const int r = r0 + 2 * i + half;
-        const bool is_v = r >= p.hkv;
-        const float2 f[4] = {Elem<T>::to_f2(x[i].x), Elem<T>::to_f2(x[i].y), Elem<T>::to_f2(x[i].z),
-                             Elem<T>::to_f2(x[i].w)};
-        uint32_t top = 0;  // magnitude bits: ordered as integers, NaN above infinity
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          top = max(top, max(__float_as_uint(f[k].x) & 0x7fffffffu, __float_as_uint(f[k].y) & 0x7fffffffu));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const uint32_t e = top >> 23;
+        // the largest magnitude, on 16-bit patterns (ordered as integers, NaN
+        // above infinity), two at a time
+        uint32_t top = __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu));
+        top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        top = max(top & 0xffffu, top >> 16);
+        const uint32_t e = __float_as_uint(Elem<T>::to_f2(top).x) >> 23;
         const bool nan = e == 255u;
         const uint32_t s = nan ? 255u : (uint32_t)max((int)e - 2, 1);
         const float mul = __uint_as_float(nan ? 0u : (254u - s) << 23);  // 2^(127 - s)
-        uint32_t w = to_e2m1x4(f[0].x * mul, f[0].y * mul, f[1].x * mul, f[1].y * mul) |
-                     (to_e2m1x4(f[2].x * mul, f[2].y * mul, f[3].x * mul, f[3].y * mul) << 16);
-        if (nan) w = 0;
+        const float2 f[4] = {Elem<T>::to_f2(x[i].x), Elem<T>::to_f2(x[i].y), Elem<T>::to_f2(x[i].z),
+                             Elem<T>::to_f2(x[i].w)};
+        const float y[8] = {f[0].x * mul, f[0].y * mul, f[1].x * mul, f[1].y * mul,
+                            f[2].x * mul, f[2].y * mul, f[3].x * mul, f[3].y * mul};
+        const uint32_t w = nan ? 0u : to_e2m1x8(y);
         // lane 4 b + v holds words (u = 2 v, b) and (u = 2 v + 1, b); lane
         // 4 j + v stores 32-bit word j of 16-byte piece v: words
         // (u = 2 v + j / 2, b = 2 (j % 2)) and (the same u, b + 1)
         const uint32_t wa = __shfl_sync(0xffffffffu, w, 8 * (j & 1) + v, 16);
         const uint32_t wb = __shfl_sync(0xffffffffu, w, 8 * (j & 1) + 4 + v, 16);
-        const uint32_t out = prmt(wa, wb, (j >> 1) ? 0x7632u : 0x5410u);
-        uint32_t sc = s << (8 * j);
-        sc |= __shfl_xor_sync(0xffffffffu, sc, 4);
-        sc |= __shfl_xor_sync(0xffffffffu, sc, 8);
         if (at.slot >= 0 && r < rows) {
-          const int64_t row = at.slot * p.hkv + (is_v ? r - p.hkv : r);
-          uint8_t* codes = static_cast<uint8_t*>(is_v ? p.v_codes : p.k_codes) + row * kMx4RowBytes;
-          *reinterpret_cast<uint32_t*>(codes + 16 * v + 4 * j) = out;
-          if (lane16 == 0) static_cast<uint32_t*>(is_v ? p.v_scales : p.k_scales)[row] = sc;
+          const bool is_v = r >= p.hkv;
+          *reinterpret_cast<uint32_t*>((is_v ? v_dst : k_dst) + r * kMx4RowBytes) =
+              prmt(wa, wb, (j >> 1) ? 0x7632u : 0x5410u);
+          if (v == 0) (is_v ? v_sc : k_sc)[r * 4] = (uint8_t)s;
         }
       }
     }
@@ -166,6 +168,13 @@ __global__ void __launch_bounds__(kThreads) gather_mx4_kernel(const Mx4RowsParam
     const Place at = place_of(p, (int)t);
     if (at.bad && (threadIdx.x & 31) == 0) report(p.status, PKC_ERR_BLOCK_TABLE);
     if (at.slot < 0 && !at.bad) continue;  // (warp-uniform) a row of no request
+    const int64_t row0 = max(at.slot, (int64_t)0) * p.hkv;  // (V's row r is its head r - Hkv)
+    const uint8_t* k_src = static_cast<const uint8_t*>(p.k_codes) + row0 * kMx4RowBytes + 16 * v + 4 * b;
+    const uint8_t* v_src = static_cast<const uint8_t*>(p.v_codes) + (row0 - p.hkv) * kMx4RowBytes + 16 * v + 4 * b;
+    const uint8_t* k_sc = static_cast<const uint8_t*>(p.k_scales) + row0 * 4 + b;
+    const uint8_t* v_sc = static_cast<const uint8_t*>(p.v_scales) + (row0 - p.hkv) * 4 + b;
+    T* k_dst = static_cast<T*>(p.k_out) + t * p.hkv * PKC_HEAD_DIM + 8 * lane16;
+    T* v_dst = static_cast<T*>(p.v_out) + (t - 1) * p.hkv * PKC_HEAD_DIM + 8 * lane16;
     for (int r0 = (int)blockIdx.y * kRows; r0 < rows; r0 += (int)gridDim.y * kRows) {
       uint32_t w[kUnroll], sc[kUnroll];
 #pragma unroll
@@ -174,33 +183,29 @@ __global__ void __launch_bounds__(kThreads) gather_mx4_kernel(const Mx4RowsParam
         const bool is_v = r >= p.hkv;
         w[i] = sc[i] = 0;  // a row without a page reads as zeros
         if (at.slot >= 0 && r < rows) {
-          const int64_t row = at.slot * p.hkv + (is_v ? r - p.hkv : r);
-          w[i] = reinterpret_cast<const uint32_t*>(static_cast<const uint8_t*>(is_v ? p.v_codes : p.k_codes) +
-                                                   row * kMx4RowBytes)[4 * v + b];
-          sc[i] = static_cast<const uint32_t*>(is_v ? p.v_scales : p.k_scales)[row];
+          w[i] = *reinterpret_cast<const uint32_t*>((is_v ? v_src : k_src) + r * kMx4RowBytes);
+          sc[i] = (is_v ? v_sc : k_sc)[r * 4];
         }
       }
 #pragma unroll
       for (int i = 0; i < kUnroll; ++i) {
         const int r = r0 + 2 * i + half;
-        const bool is_v = r >= p.hkv;
         // the inverse of the append's re-ordering: lane 4 b + v takes the
         // words (u = 2 v, b) and (u = 2 v + 1, b)
         const uint32_t wa = __shfl_sync(0xffffffffu, w[i], 4 * (b >> 1) + v, 16);
         const uint32_t wb = __shfl_sync(0xffffffffu, w[i], 4 * (2 + (b >> 1)) + v, 16);
         uint32_t h2[4];
         e2m1x8(prmt(wa, wb, (b & 1) ? 0x7632u : 0x5410u), h2);
-        const float s = mx4_scale((sc[i] >> (8 * b)) & 255u);
+        const float s = mx4_scale(sc[i]);
         uint32_t out[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const float2 f = Elem<__half>::to_f2(h2[k]);
           out[k] = Elem<T>::from_f2(f.x * s, f.y * s);
         }
-        if (r < rows) {
-          T* row = static_cast<T*>(is_v ? p.v_out : p.k_out) + (t * p.hkv + (is_v ? r - p.hkv : r)) * PKC_HEAD_DIM;
-          *reinterpret_cast<uint4*>(row + 8 * lane16) = make_uint4(out[0], out[1], out[2], out[3]);
-        }
+        if (r < rows)
+          *reinterpret_cast<uint4*>((r >= p.hkv ? v_dst : k_dst) + r * PKC_HEAD_DIM) =
+              make_uint4(out[0], out[1], out[2], out[3]);
       }
     }
   }

@@ -28,15 +28,16 @@ __device__ __forceinline__ void e2m1x8(uint32_t w, uint32_t (&r)[4]) {
       : "r"(w));
 }
 
-// Four values -> one 16-bit word of e2m1 codes (x0 in the low nibble), to
+// Eight values -> a word of e2m1 codes (x[0] in the lowest nibble), to
 // nearest, ties to even, saturating at 6.
-__device__ __forceinline__ uint32_t to_e2m1x4(float x0, float x1, float x2, float x3) {
+__device__ __forceinline__ uint32_t to_e2m1x8(const float (&x)[8]) {
   uint32_t d;
-  asm("{\n.reg .b8 a, b;\ncvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n"
-      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\nmov.b32 %0, {a, b, a, b};\n}"
+  asm("{\n.reg .b8 a, b, c, d;\ncvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\ncvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n"
+      "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\nmov.b32 %0, {a, b, c, d};\n}"
       : "=r"(d)
-      : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
-  return d & 0xffffu;
+      : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+  return d;
 }
 
 // The float a scale byte stands for: 2^(s - 127), exactly (2^-127 is a

@@ -142,10 +142,15 @@ def _dtype_code(t) -> int:
     return F16 if d == torch.float16 else BF16 if d == torch.bfloat16 else {torch.float32: F32}[d]
 
 
+def _device():
+    """The current device's index (tensors on it exist: CUDA is initialised)."""
+    return (_torch or _t())._C._cuda_getDevice()
+
+
 def _stream(stream):
     torch = _torch or _t()
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -393,9 +398,8 @@ def append_kv(k_new, v_new, k_cache, v_cache, block_table, cache_seqlens, worksp
 
 def _expect_current(t):
     """The library launches on the current device: refuse tensors of another."""
-    torch = _torch or _t()
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    if t.get_device() != _device():
+        raise ValueError(f"tensors are on {t.device}, the current device is cuda:{_device()}")
 
 
 def _expect_all(device, *specs):
@@ -422,7 +426,7 @@ def _check_mx4(k_codes, k_scales, v_codes, v_scales, block_table, workspace):
     u8 = torch.uint8
     P, ps, Hkv, _ = _sizes(k_codes, 4)
     B, n_pages = _sizes(block_table, 2)
-    if P is None or not k_codes.is_cuda or k_codes.device.index != torch.cuda.current_device():
+    if P is None or not k_codes.is_cuda or k_codes.get_device() != _device():
         _expect("k_codes", k_codes, (u8,), (None, None, None, 64))
         _expect_current(k_codes)
     dev = k_codes.device

@@ -48,6 +48,17 @@ int num_sms() {
   return cache[dev];
 }
 
+int raise_smem_limit(const void* kernel, int bytes, std::atomic<uint64_t>& raised) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return (int)e;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (raised.load(std::memory_order_relaxed) & bit) return 0;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess) raised.fetch_or(bit, std::memory_order_relaxed);
+  return (int)e;
+}
+
 static size_t al256(size_t x) { return (x + 255) & ~size_t(255); }
 
 WsLayout ws_layout(int batch, int hq, int d, int num_ctas) {

@@ -552,10 +552,10 @@ template <typename T, int G>
 int launch_g(const Mx4DecodeParams& p, dim3 grid, cudaStream_t st) {
   constexpr int smem = smem_bytes<G>();
   static_assert(kBlocksPerSm * (smem + 1024) <= 228 * 1024, "resident blocks");
-  // (an attribute of the current device: set on every call, it is cheap)
-  auto kernel = p.d.page_size % kTile == 0 ? paged_decode_mx4_kernel<T, G, true> : paged_decode_mx4_kernel<T, G, false>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return (int)e;
+  const bool aligned = p.d.page_size % kTile == 0;
+  auto kernel = aligned ? paged_decode_mx4_kernel<T, G, true> : paged_decode_mx4_kernel<T, G, false>;
+  static std::atomic<uint64_t> raised[2];
+  if (const int e = raise_smem_limit(reinterpret_cast<const void*>(kernel), smem, raised[aligned])) return e;
   kernel<<<grid, kThreads, smem, st>>>(p);
   return (int)cudaGetLastError();
 }

@@ -48,6 +48,7 @@ static_assert(kBins == 2048, "digits of 11 bits");
 constexpr int kBatch = 8;                    // keys a thread has in flight
 constexpr int kListed = 1536;                // keys of a digit's bin that a block lists
 constexpr int kMostKeys = 1 << 19;           // keys of one block (two bits each in shared memory)
+constexpr int kMostHeld = 32 * 1024;         // keys of one block held in shared memory
 constexpr uint32_t kZeroKey = 0x80000000u;   // the key of weight 0
 
 __device__ __forceinline__ uint32_t order_key(float w) {
@@ -67,8 +68,9 @@ struct SelectShared {
 
 // Shared memory: SelectShared, then two bits per key (kept for certain; equal
 // to T), then the keys where there are no more rows than SMs: those rows are
-// read once, as a block has an SM to itself (131072 weights: 33 -> 27 us),
-// while in a batch more blocks per SM are worth more (28 against 33 us).
+// read once, as a block has an SM to itself (8 rows of 131072: 24 -> 22 us),
+// while in a batch more blocks per SM are worth more (512 rows: 28 against
+// 31 us).
 __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const SelectParams p) {
   extern __shared__ __align__(16) uint8_t smem_sel[];
   SelectShared& S = *reinterpret_cast<SelectShared*>(smem_sel);
@@ -498,10 +500,13 @@ int launch_evict_select(const SelectParams& p_in, void* stream) {
     p.cluster *= 2;
   const int64_t per = ((p.w_stride + p.cluster - 1) / p.cluster + 31) & ~int64_t(31);
   if (per > kMostKeys) return (int)cudaErrorInvalidValue;
-  p.smem_keys = rows * p.cluster <= num_sms() && per <= 32 * 1024 ? (int)per : 0;
+  p.smem_keys = rows * p.cluster <= num_sms() && per <= kMostHeld ? (int)per : 0;
   const int smem = (int)sizeof(SelectShared) + (int)(per / 32) * 8 + 4 * p.smem_keys;
-  cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return (int)e;
+  // (the most: bits of kMostKeys, or kMostHeld keys and their bits)
+  constexpr int kMostSmem = (int)sizeof(SelectShared) + std::max(kMostKeys / 4, kMostHeld * 17 / 4);
+  static_assert(kMostSmem <= 227 * 1024, "shared memory");
+  static std::atomic<uint64_t> raised;
+  if (const int e = raise_smem_limit(reinterpret_cast<const void*>(evict_select_kernel), kMostSmem, raised)) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * p.cluster));
   cfg.blockDim = dim3(kSelThreads);

@@ -1,5 +1,6 @@
 // Internal declarations shared by the library's translation units.
 #pragma once
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -367,6 +368,12 @@ int launch_prefix(const PrefixParams& p, const void* q, const void* k_prefix,
                   void* stream, void* start_event = nullptr);
 
 int num_sms();
+
+// Raise a kernel's dynamic shared memory limit on the current device to
+// `bytes`.  `raised` is the kernel's own record, one bit per device (a static
+// of the caller's): the runtime is asked once per device.  Returns a
+// cudaError_t value.
+int raise_smem_limit(const void* kernel, int bytes, std::atomic<uint64_t>& raised);
 
 // Encode a TMA tiled tensor map (a 128-byte CUtensorMap at `map`) over a
 // 16-bit (PKC_F16, PKC_BF16) or byte (PKC_E4M3) tensor; dims[0] is the

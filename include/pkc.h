@@ -530,10 +530,11 @@ int pkc_cascade_decode_paged_prefix(
  * NaN.  The pages of all new tokens must be in the block table.  A page id
  * < 0 or >= num_pages (or past the table) is recorded as
  * PKC_ERR_BLOCK_TABLE, and that request's length stays as it was (tokens of
- * it that have a page may have been written behind its end); a request whose
- * new_indptr range is not within 0 .. total_new keeps its length too and is
- * recorded as PKC_ERR_PLAN.  One launch; the workspace's status block holds
- * its counter, so a workspace must not be shared by two appends in flight.
+ * it that have a page may have been written behind its end).  A new_indptr
+ * that does not run upwards within 0 .. total_new is recorded as
+ * PKC_ERR_PLAN, and no length changes.  One launch; the workspace's status
+ * block holds its counter, so a workspace must not be shared by two appends
+ * in flight.
  */
 int pkc_append_kv_mx4(const void* k_new, const void* v_new,
                       const int32_t* new_indptr, int total_new, void* k_codes,
@@ -661,9 +662,10 @@ int pkc_evict_select(const float* weights, int64_t weights_stride,
  * Pages behind the new length are the caller's to free.  No page may be
  * shared between two requests (or used twice by one) that are cut.  A
  * request with a page id < 0 or >= num_pages below its length is left as it
- * was (PKC_ERR_BLOCK_TABLE).  A (request, head) whose keep row does not
- * ascend within the length, or whose weights row is shorter than it, is not
- * moved (PKC_ERR_PLAN), while the request's length still becomes the budget.
+ * was (PKC_ERR_BLOCK_TABLE), and so is one longer than weights_stride
+ * (PKC_ERR_PLAN).  A (request, head) whose keep row does not ascend within
+ * the length is not moved (PKC_ERR_PLAN), while the request's length still
+ * becomes the budget: its other heads have been cut.
  * One launch; the workspace's status block holds its counter, so a workspace
  * must not be shared by two compactions in flight.
  */

@@ -141,12 +141,20 @@ __global__ void __launch_bounds__(kThreads) append_mx4_kernel(const Mx4RowsParam
     atomicExch(ctr, 0);
   }
   __syncthreads();
+  // The ranges must run upwards within 0 .. total: were they to overlap, a
+  // request could count rows that another one got.
+  bool wrong = false;
+  for (int b = threadIdx.x; b < p.batch; b += kThreads)
+    wrong = wrong || p.indptr[b] < 0 || p.indptr[b + 1] < p.indptr[b] || p.indptr[b + 1] > p.total;
+  if (__syncthreads_or(wrong)) {
+    if (threadIdx.x == 0) report(p.status, PKC_ERR_PLAN);
+    return;
+  }
   for (int b = threadIdx.x; b < p.batch; b += kThreads) {
     const int t0 = p.indptr[b], t1 = p.indptr[b + 1], len = p.base[b];
     if (t0 == t1) continue;
-    bool ok = t0 >= 0 && t0 < t1 && t1 <= p.total;
-    if (!ok) report(p.status, PKC_ERR_PLAN);
-    if (ok && bad) {  // some token had no page: which requests have all of theirs?
+    bool ok = true;
+    if (bad) {  // some token had no page: which requests have all of theirs?
       for (int64_t pos = len; ok && pos < (int64_t)len + (t1 - t0);) {
         const int64_t page_idx = pos / p.page_size;
         int32_t page = -1;

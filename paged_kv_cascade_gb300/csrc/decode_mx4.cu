@@ -504,7 +504,9 @@ __global__ void __launch_bounds__(kW * 32) join_mx4_kernel(const __grid_constant
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = (int)(blockIdx.x / (unsigned)p.hq), hq = (int)(blockIdx.x % (unsigned)p.hq);
   const int32_t* pl = p.plan;
-  const bool plan_ok = device_plan_ok(pl, p.plan_words, p.batch);  // (reported by the decode)
+  // The list's length is the uploaded plan's, whatever the host's copy says
+  // (a plan that is not there is reported by the decode).
+  const bool plan_ok = device_plan_ok(pl, p.plan_words, p.batch) && row < pl[PKC_PLAN_N_SPLIT] + pl[PKC_PLAN_N_EMPTY];
   int n = 0, first = 0, req = 0;
   if (plan_ok) {
     const int unit = pl[p.off_unit_list + row];
@@ -601,7 +603,7 @@ int launch_paged_decode_mx4(const Mx4DecodeParams& p_in, int n_work, int dtype, 
 }
 
 int launch_join_mx4(const Mx4JoinParams& p, int n_rows, int n_states, int dtype, void* stream) {
-  const int64_t blocks = (int64_t)n_rows * p.hq;
+  const int64_t blocks = (int64_t)p.batch * p.hq;  // (the uploaded plan says how many rows there are)
   if (blocks <= 0) return 0;
   if (blocks > INT32_MAX) return (int)cudaErrorInvalidValue;
   // Launched as the decode's programmatic dependent: the blocks start as the

@@ -404,8 +404,9 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const Compa
   const int row = (int)(blockIdx.x / p.parts), b = row / p.hkv, h = row % p.hkv;
   const int tid = threadIdx.x;
   const int len = p.cache_seqlens[b], n = p.budget;
-  bool bad_page = false;
+  bool bad_request = false;
   if (len > n) {
+    bool bad_page = false;
     const int32_t* keep = p.keep + (int64_t)row * n;
     const int32_t* bt_row = p.block_table + (int64_t)b * p.bt_stride;
     const PageDiv pages{p.page_size, p.page_shift};
@@ -418,7 +419,8 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const Compa
         const int32_t id = bt_row[i];
         bad_page = bad_page || id < 0 || id >= p.num_pages;
       }
-    bool bad_keep = p.weights && len > p.w_stride;
+    const bool short_row = p.weights && len > p.w_stride;  // (of the whole request)
+    bool bad_keep = short_row;
     for (int j = tid; j < n; j += kMoveThreads) {
       const int32_t k = keep[j];
       bad_keep = bad_keep || k < (j > 0 ? keep[j - 1] + 1 : 0) || k >= len;
@@ -427,6 +429,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const Compa
     bad_keep = __syncthreads_or(bad_keep);
     if (bad_page || bad_keep) {
       if (tid == 0) report(p.status, bad_page ? PKC_ERR_BLOCK_TABLE : PKC_ERR_PLAN);
+      bad_request = bad_page || short_row;
     } else {
       // (strictly ascending and >= 0: keep[j] >= j)
       auto token = [&](int slot) {  // a slot's pool index
@@ -458,7 +461,7 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const Compa
   // finishes last, which also resets the counter for the next launch.
   int32_t* ctr = p.status + PKC_COMPACT_COUNTER;
   __shared__ int last, any_bad;
-  if (bad_page && tid == 0) atomicExch(ctr + 1, 1);
+  if (bad_request && tid == 0) atomicExch(ctr + 1, 1);
   __threadfence();
   __syncthreads();
   if (tid == 0) last = atomicAdd(ctr, 1) == (int)gridDim.x - 1;
@@ -474,9 +477,9 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const Compa
     const int l = p.cache_seqlens[r];
     if (l <= n) continue;
     bool ok = true;
-    if (any_bad) {  // a request with a missing page keeps its length
+    if (any_bad) {  // a request with a missing page, or short weights, keeps its length
       const int64_t n_pages = ((int64_t)l + p.page_size - 1) / p.page_size;
-      ok = n_pages <= p.bt_stride;
+      ok = n_pages <= p.bt_stride && !(p.weights && l > p.w_stride);
       for (int64_t i = 0; ok && i < n_pages; ++i) {
         const int32_t id = p.block_table[(int64_t)r * p.bt_stride + i];
         ok = id >= 0 && id < p.num_pages;

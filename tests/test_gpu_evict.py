@@ -329,6 +329,19 @@ def test_compact_leaves_requests_with_bad_pages_and_rows_with_bad_slots():
             np.testing.assert_array_equal(got, want)
     np.testing.assert_array_equal(dw.cpu().numpy(), want_w)
     assert c.dl.tolist() == [20, 60, 20]
+    # weights shorter than a request: that request is left as it was
+    c = Paged("f16", [50, 30], 1, 16, rng)
+    before = raw(c)
+    keep2 = np.stack([np.arange(30, 50), np.arange(10, 30)])[:, None].astype(np.int32)
+    ws, w = ws_for(2, 1), torch.rand(2, 1, 40, device="cuda")
+    w0 = w.clone()
+    want_w = compact_plain(c, before, keep2, [0, 30], w0.cpu().numpy())
+    c.compact(cuda(keep2), ws, w)
+    assert pkc.device_status(ws) == 7 and c.dl.tolist() == [50, 20]
+    for got, want in zip(raw(c), before):
+        if want is not None:
+            np.testing.assert_array_equal(got, want)
+    np.testing.assert_array_equal(w.cpu().numpy(), want_w)
     # slots out of range and descending ones: nothing is read or written through them
     for bad in (-1, 1 << 30, 2 ** 31 - 1):
         c = Paged("mx4", [50], 1, 16, rng)

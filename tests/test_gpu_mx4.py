@@ -167,13 +167,14 @@ def test_append_without_a_page_and_with_a_bad_range():
     pkc.append_kv_mx4(x, x, cuda(indptr_of(new)), *d, cuda(bt), lens, ws)
     assert pkc.device_status(ws) == 4  # PKC_ERR_BLOCK_TABLE
     assert lens.tolist() == [5, 16, 10, 30]
-    # a range that runs backwards, one past the rows: those requests keep their lengths
+    # ranges that run backwards, past the rows, from below 0: no length changes
     bt, P = table_for([20] * 4, 16, rng)
     d = [torch.zeros((P, 16, 2, n), dtype=torch.uint8, device="cuda") for n in (64, 4, 64, 4)]
-    lens = cuda(np.full(4, 2, np.int32))
-    pkc.append_kv_mx4(x, x, cuda(np.array([0, 4, 2, 6, 11], np.int32)), *d, cuda(bt), lens, ws)
-    assert pkc.device_status(ws) == 7  # PKC_ERR_PLAN
-    assert lens.tolist() == [6, 2, 6, 2]
+    for ranges in ([0, 4, 2, 6, 10], [0, 1, 2, 3, 11], [-3, 1, 2, 3, 4], [0, 2 ** 31 - 1, 5, 6, 7]):
+        lens = cuda(np.full(4, 2, np.int32))
+        pkc.append_kv_mx4(x, x, cuda(np.array(ranges, np.int32)), *d, cuda(bt), lens, ws)
+        assert pkc.device_status(ws) in (4, 7)  # PKC_ERR_PLAN (or first a token past the table)
+        assert lens.tolist() == [2, 2, 2, 2]
     # and the workspace's counters are clean again
     lens = cuda(np.full(4, 2, np.int32))
     pkc.append_kv_mx4(x, x, cuda(indptr_of(new)), *d, cuda(bt), lens, ws)
@@ -340,6 +341,27 @@ def test_plan_that_was_not_uploaded_is_reported():
     ws[256:4096] = 0
     pkc.paged_decode_state_mx4(torch.zeros(2, 4, 128, device="cuda").half(), *d, bt, dl, 0.1, ws,
                                plan_buf=pkc.plan([50, 40], 8))
+    assert pkc.device_status(ws) == 7
+
+
+def test_host_plan_that_is_not_the_uploaded_one():
+    """The join follows the uploaded plan: a host plan of the same sizes with
+    other splits changes no result."""
+    rng = np.random.default_rng(21)
+    lens, hkv, g, ctas = [900, 10, 0, 400], 2, 4, 16
+    c = Cache(lens, hkv, 16, rng)
+    d, bt, dl = c.device()
+    q = torch.from_numpy(rng.standard_normal((4, hkv * g, 128))).cuda().half()
+    ws = ws_for(4, hkv * g, ctas)
+    plan, other = pkc.plan(lens, ctas), pkc.plan([5, 5, 5, 5], ctas)
+    assert plan.size == other.size
+    pkc.plan_upload(plan, ws)
+    o, lse = pkc.paged_decode_state_mx4(q, *d, bt, dl, 0.1, ws, plan_buf=other)
+    assert pkc.device_status(ws) == pkc.PKC_OK
+    check_decode(c, q, o, lse, g, 0.1, "f16")
+    # and an uploaded plan of other lengths is reported
+    pkc.plan_upload(other, ws)
+    pkc.paged_decode_state_mx4(q, *d, bt, dl, 0.1, ws, plan_buf=plan)
     assert pkc.device_status(ws) == 7
 
 

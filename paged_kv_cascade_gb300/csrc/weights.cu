@@ -19,6 +19,11 @@
 //
 // No two warps touch the same weight: results do not depend on the order of
 // anything.
+//
+// Measured: bf16 keys, 64 requests, 164,506 tokens of 8 heads: 59 us (348 MB,
+// 5.9 TB/s of a measured copy rate of 6.8).  mx4 keys, 256 requests, 476,458
+// tokens: 78 us (292 MB, 3.7 TB/s), bound by the conversions' and scales'
+// instructions, not by bytes.
 #include <cuda_runtime.h>
 
 #include <algorithm>

@@ -153,9 +153,6 @@ int pkc_paged_decode_state_mx4(const void* q, const void* k_codes, const void* k
     Mx4JoinParams jp;
     std::memset(&jp, 0, sizeof(jp));
     jp.plan = dp.plan; jp.plan_words = dp.plan_words;
-    jp.off_unit_list = plan_host[PKC_PLAN_OFF_UNIT_LIST]; jp.off_unit_req = plan_host[PKC_PLAN_OFF_UNIT_REQ];
-    jp.off_unit_n_chunks = plan_host[PKC_PLAN_OFF_UNIT_N_CHUNKS];
-    jp.off_unit_partial_begin = plan_host[PKC_PLAN_OFF_UNIT_PARTIAL_BEGIN];
     jp.batch = batch; jp.hq = num_qo_heads;
     jp.part_o = dp.part_o; jp.part_lse = dp.part_lse;
     jp.o = o; jp.lse = lse;

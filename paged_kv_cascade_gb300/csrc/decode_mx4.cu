@@ -35,10 +35,10 @@
 // Measured: 124 us for a batch of 256 with 32 / 8 heads over 476,458 tokens
 // (523 MB, 4.2 TB/s of a measured copy rate of 6.8); 44 us for two requests
 // of 107,000 tokens with 32 / 4 heads (117 MB), where the join, begun early,
-// takes 11 us when it runs alone.  Bound
-// by instructions, about 350 per 16 tokens and head: 128 of them convert or
-// feed the tensor cores, the rest are addresses, scales, softmax.  Without
-// the copies' bytes the kernel takes 119 us, without the V product 103.
+// takes 11 us when it runs alone.  Bound by instructions, about 350 per 16
+// tokens and head: 128 of them convert or feed the tensor cores, the rest are
+// addresses, scales, softmax.  Without the copies' bytes the kernel takes 119
+// us, without the V product 103.
 #include <cuda_runtime.h>
 
 #include "decode_common.cuh"
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     for (int e = 0; e < 2; ++e) {  // heads 2 tg, 2 tg + 1: dims 32 b + 4 g .. + 3
       const int hd = 2 * tg + e;
       const float m = e ? m1 : m0, l = e ? l1 : l0;
-      const float inv = wph > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;  // (a NaN sum gives NaN)
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // (a NaN sum gives NaN)
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         const float f = mx4_scale((uint32_t)__shfl_sync(0xffffffffu, e_ref, b)) * inv;
@@ -475,8 +475,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     }
     __syncthreads();  // the next item is there; the warps' states are written
     if (wph > 1) {
-      // Warps of one head: unnormalised values, reference and sum, merged by a
-      // warp per (KV head, query head) row, 4 dims per lane.
+      // Warps of one head: values, reference and sum, merged by a warp per (KV
+      // head, query head) row, 4 dims per lane.  The weights add up to 1, so
+      // values near float32's largest stay finite.
       for (int r = warp; r < HG * G; r += kWarps) {
         const int h = r / G, hd = r - h * G;
         float mm = kRefFloor, ll = 0.f;
@@ -484,15 +485,18 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         for (int c = 0; c < wph; ++c) mm = fmaxf(mm, merge[((h + HG * c) * G + hd) * kMergeRow + D]);
         for (int c = 0; c < wph; ++c) {
           const float* src = merge + ((h + HG * c) * G + hd) * kMergeRow;
-          const float w = ex2(src[D] - mm);
-          ll = fmaf(src[D + 1], w, ll);
+          ll = fmaf(src[D + 1], ex2(src[D] - mm), ll);
+        }
+        const float inv = ll == 0.f ? 0.f : 1.f / ll;
+        for (int c = 0; c < wph; ++c) {
+          const float* src = merge + ((h + HG * c) * G + hd) * kMergeRow;
+          const float w = src[D + 1] * ex2(src[D] - mm) * inv;
           const float4 v = *reinterpret_cast<const float4*>(src + 4 * lane);
           acc.x = fmaf(v.x, w, acc.x); acc.y = fmaf(v.y, w, acc.y);
           acc.z = fmaf(v.z, w, acc.z); acc.w = fmaf(v.w, w, acc.w);
         }
-        const float inv = ll == 0.f ? 0.f : 1.f / ll;
         const int hq = (it.hg * HG + h) * G + hd;
-        write4(hq, 4 * lane, make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+        write4(hq, 4 * lane, acc);
         if (lane == 0) write_lse(hq, mm, ll);
       }
       __syncthreads();  // the merge buffer is free
@@ -512,15 +516,17 @@ __global__ void __launch_bounds__(kW * 32) join_mx4_kernel(const __grid_constant
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int row = (int)(blockIdx.x / (unsigned)p.hq), hq = (int)(blockIdx.x % (unsigned)p.hq);
   const int32_t* pl = p.plan;
-  // The list's length is the uploaded plan's, whatever the host's copy says
-  // (a plan that is not there is reported by the decode).
+  // The list and its places are the uploaded plan's, whatever the host's copy
+  // says (a plan that is not there is reported by the decode).
   const bool plan_ok = device_plan_ok(pl, p.plan_words, p.batch) && row < pl[PKC_PLAN_N_SPLIT] + pl[PKC_PLAN_N_EMPTY];
+  const int off_n = pl[PKC_PLAN_OFF_UNIT_N_CHUNKS], off_first = pl[PKC_PLAN_OFF_UNIT_PARTIAL_BEGIN];
+  const int off_req = pl[PKC_PLAN_OFF_UNIT_REQ];
   int n = 0, first = 0, req = 0;
   if (plan_ok) {
-    const int unit = pl[p.off_unit_list + row];
-    n = pl[p.off_unit_n_chunks + unit];
-    first = pl[p.off_unit_partial_begin + unit];
-    req = pl[p.off_unit_req + unit];
+    const int unit = pl[pl[PKC_PLAN_OFF_UNIT_LIST] + row];
+    n = pl[off_n + unit];
+    first = pl[off_first + unit];
+    req = pl[off_req + unit];
   }
   grid_wait_prerequisites();  // the decode grid's states
   if (!plan_ok) return;

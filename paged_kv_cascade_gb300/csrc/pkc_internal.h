@@ -258,7 +258,7 @@ struct Mx4DecodeParams {
 // The join of a planned mx4 decode's split requests.
 struct Mx4JoinParams {
   const int32_t* plan;     // device
-  int32_t plan_words, off_unit_list, off_unit_req, off_unit_n_chunks, off_unit_partial_begin;
+  int32_t plan_words;
   int batch, hq;
   const float* part_o;     // [slot, hq, 128]
   const float* part_lse;   // [slot, hq]

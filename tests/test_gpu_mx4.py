@@ -278,6 +278,18 @@ def test_decode_of_very_small_and_very_large_bf16_queries(mag):
     check_decode(c, q, o, lse, g, 0.1, "bf16")
 
 
+@pytest.mark.parametrize("hkv", [1, 4])
+def test_decode_of_values_near_the_largest_float(hkv):
+    """bf16 values of 1e37: their weighted sum stays finite, as it is a mean."""
+    rng = np.random.default_rng(10)
+    lens, g = [300, 33], 4
+    c = Cache(lens, hkv, 16, rng, v=rng.standard_normal((333, hkv, 128)) * 1e37)
+    d, bt, dl = c.device()
+    q = torch.from_numpy(rng.standard_normal((2, hkv * g, 128))).cuda().bfloat16()
+    o, lse = pkc.paged_decode_state_mx4(q, *d, bt, dl, 0.1, ws_for(2, hkv * g))
+    check_decode(c, q, o, lse, g, 0.1, "bf16")
+
+
 def test_decode_of_large_scores_moves_the_reference():
     """Scores that rise along the cache by hundreds: earlier tokens' weights vanish."""
     rng = np.random.default_rng(8)

@@ -637,9 +637,9 @@ int pkc_accumulate_weights(const void* q, const float* lse,
  * `recent` with the largest weights (of equal weights the lower slot; NaN
  * counts as larger than any number, -0 as 0), and the last `recent`, all in
  * ascending order; for any other request 0 .. length - 1, then -1.
- * budget >= 1, sinks >= 0, recent >= 0, sinks + recent <= budget;
- * weights_stride <= 2^22 (PKC_ERR_UNSUPPORTED above).  A request longer than
- * weights_stride gets -1 throughout (PKC_ERR_PLAN).
+ * budget >= 1, sinks >= 0, recent >= 0, sinks + recent <= budget; budget <=
+ * 2^30 and weights_stride <= 2^22 (PKC_ERR_UNSUPPORTED above).  A request
+ * longer than weights_stride gets -1 throughout (PKC_ERR_PLAN).
  */
 int pkc_evict_select(const float* weights, int64_t weights_stride,
                      const int32_t* cache_seqlens, int batch, int num_kv_heads,
@@ -659,13 +659,16 @@ int pkc_evict_select(const float* weights, int64_t weights_stride,
  *   weights  NULL, or the accumulated weights [batch, num_kv_heads,
  *            weights_stride]: they move along, and those between the budget
  *            and the old length become 0
- * Pages behind the new length are the caller's to free.  No page may be
- * shared between two requests (or used twice by one) that are cut.  A
+ * Pages behind the new length are the caller's to free.  The pages of a
+ * request that is cut must be its own: no other request's, and each only
+ * once in its table.  budget <= 2^30 (PKC_ERR_UNSUPPORTED above).  A
  * request with a page id < 0 or >= num_pages below its length is left as it
- * was (PKC_ERR_BLOCK_TABLE), and so is one longer than weights_stride
- * (PKC_ERR_PLAN).  A (request, head) whose keep row does not ascend within
- * the length is not moved (PKC_ERR_PLAN), while the request's length still
- * becomes the budget: its other heads have been cut.
+ * was (PKC_ERR_BLOCK_TABLE), and so is one longer than weights_stride or one
+ * with a head whose keep row ends below 0, as pkc_evict_select leaves it
+ * where it could not choose or the length was within the budget then
+ * (PKC_ERR_PLAN).  Any other (request, head) whose keep row does not ascend
+ * within the length is not moved (PKC_ERR_PLAN), while the request's length
+ * still becomes the budget: its other heads have been cut.
  * One launch; the workspace's status block holds its counter, so a workspace
  * must not be shared by two compactions in flight.
  */

@@ -215,6 +215,7 @@ int pkc_evict_select(const float* weights, int64_t weights_stride, const int32_t
                      "evict_select: budget must be >= 1, sinks and recent >= 0 and together at most the budget "
                      "(got %d, %d, %d)",
                      budget, sinks, recent);
+  if (budget > 1 << 30) return set_error(PKC_ERR_UNSUPPORTED, "evict_select: a budget of more than 2^30");
   if (weights_stride > (int64_t)1 << 22)
     return set_error(PKC_ERR_UNSUPPORTED, "evict_select: rows of more than 2^22 weights");
   if ((int64_t)batch * num_kv_heads > INT32_MAX / 8)
@@ -238,6 +239,7 @@ int pkc_evict_compact(const int32_t* keep, int budget, void* k_cache, void* v_ca
   if (int rc = check_pool("evict_compact", batch, num_kv_heads, head_dim, page_size, block_table_stride, num_pages))
     return rc;
   if (budget < 1) return set_error(PKC_ERR_INVALID_ARG, "evict_compact: budget must be >= 1 (got %d)", budget);
+  if (budget > 1 << 30) return set_error(PKC_ERR_UNSUPPORTED, "evict_compact: a budget of more than 2^30");
   if (kv_dtype != PKC_F16 && kv_dtype != PKC_BF16 && kv_dtype != PKC_E4M3 && kv_dtype != PKC_MX4)
     return set_error(PKC_ERR_INVALID_ARG, "evict_compact: kv_dtype must be PKC_F16, PKC_BF16, PKC_E4M3 or PKC_MX4 (got %d)",
                      kv_dtype);

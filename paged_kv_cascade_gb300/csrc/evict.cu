@@ -424,17 +424,23 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const Compa
         const int32_t id = bt_row[i];
         bad_page = bad_page || id < 0 || id >= p.num_pages;
       }
-    const bool short_row = p.weights && len > p.w_stride;  // (of the whole request)
-    bool bad_keep = short_row;
+    // Of the whole request: weights shorter than it, or a head with too few
+    // slots (as the select leaves it for a row too short, or a request that
+    // was within the budget then).
+    bool unchosen = p.weights && len > p.w_stride;
+    for (int i = tid; i < p.hkv; i += kMoveThreads)
+      unchosen = unchosen || p.keep[((int64_t)b * p.hkv + i + 1) * n - 1] < 0;
+    bool bad_keep = unchosen;
     for (int j = tid; j < n; j += kMoveThreads) {
       const int32_t k = keep[j];
       bad_keep = bad_keep || k < (j > 0 ? keep[j - 1] + 1 : 0) || k >= len;
     }
     bad_page = __syncthreads_or(bad_page);
     bad_keep = __syncthreads_or(bad_keep);
+    unchosen = __syncthreads_or(unchosen);
     if (bad_page || bad_keep) {
       if (tid == 0) report(p.status, bad_page ? PKC_ERR_BLOCK_TABLE : PKC_ERR_PLAN);
-      bad_request = bad_page || short_row;
+      bad_request = bad_page || unchosen;
     } else {
       // (strictly ascending and >= 0: keep[j] >= j)
       auto token = [&](int slot) {  // a slot's pool index
@@ -482,9 +488,10 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const Compa
     const int l = p.cache_seqlens[r];
     if (l <= n) continue;
     bool ok = true;
-    if (any_bad) {  // a request with a missing page, or short weights, keeps its length
+    if (any_bad) {  // a request with a missing page, short weights or a head of too few slots keeps its length
       const int64_t n_pages = ((int64_t)l + p.page_size - 1) / p.page_size;
       ok = n_pages <= p.bt_stride && !(p.weights && l > p.w_stride);
+      for (int i = 0; ok && i < p.hkv; ++i) ok = p.keep[((int64_t)r * p.hkv + i + 1) * n - 1] >= 0;
       for (int64_t i = 0; ok && i < n_pages; ++i) {
         const int32_t id = p.block_table[(int64_t)r * p.bt_stride + i];
         ok = id >= 0 && id < p.num_pages;

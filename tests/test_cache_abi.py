@@ -122,7 +122,7 @@ def test_evict_select_refuses(L):
     good = [F, 64, F, 2, 8, 16, 4, 8, F, WS, 1 << 20, None]
     for args, code in variants(good, [
             (0, None, 1), (2, None, 1), (8, None, 1), (1, 0, 1), (3, -1, 1), (4, 0, 1), (5, 0, 1), (5, 11, 1),
-            (6, -1, 1), (7, -1, 1), (7, 13, 1), (6, 2 ** 31 - 1, 1), (3, 1 << 28, 2), (10, 255, 3)]):
+            (6, -1, 1), (7, -1, 1), (7, 13, 1), (6, 2 ** 31 - 1, 1), (5, 2 ** 30 + 1, 2), (3, 1 << 28, 2), (10, 255, 3)]):
         assert L.pkc_evict_select(*args) == code, (args, L.pkc_last_error())
     assert L.pkc_evict_select(*good[:3], 0, *good[4:]) == 0
 
@@ -132,7 +132,7 @@ def test_evict_compact_refuses(L):
     good = [F, 16, F, F, None, None, F, 4, F, F, 64, 2, 8, 128, 16, 10, 1, WS, 1 << 20, None]
     for args, code in variants(good, [
             (0, None, 1), (2, None, 1), (3, None, 1), (6, None, 1), (8, None, 1), (1, 0, 1), (2, OFF, 1), (3, OFF, 1),
-            (7, 0, 1), (10, 0, 1), (11, -1, 1), (11, 1 << 26, 2), (12, 0, 1), (13, 64, 2), (14, 0, 1), (15, -1, 1),
+            (7, 0, 1), (1, 2 ** 30 + 1, 2), (10, 0, 1), (11, -1, 1), (11, 1 << 26, 2), (12, 0, 1), (13, 64, 2), (14, 0, 1), (15, -1, 1),
             (16, 0, 1), (16, 5, 1), (16, 4, 1), (18, 200, 3)]):
         assert L.pkc_evict_compact(*args) == code, (args, L.pkc_last_error())
     assert L.pkc_evict_compact(*good[:11], 0, *good[12:]) == 0

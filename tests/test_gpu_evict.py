@@ -355,6 +355,26 @@ def test_compact_leaves_requests_with_bad_pages_and_rows_with_bad_slots():
             np.testing.assert_array_equal(got, want)
 
 
+def test_compact_leaves_a_request_that_select_could_not_choose_for():
+    rng = np.random.default_rng(11)
+    lens, hkv, budget = [90, 40, 90, 17], 3, 16
+    c = Paged("bf16", lens, hkv, 8, rng)
+    w, ws = torch.rand(4, hkv, 64, device="cuda"), ws_for(4, hkv)  # requests 0 and 2 are longer than that
+    c.dl[3] = 12  # within the budget; request 3 grows afterwards
+    keep = pkc.evict_select(w, c.dl, budget, 2, 4, ws)
+    c.dl[3] = 17
+    keep[2] = torch.arange(budget, device="cuda")  # all of request 2's heads but one: the caller's own choice
+    keep[2, 1, -1] = -1
+    pools = raw(c)
+    compact_plain(c, pools, keep.cpu().numpy(), [0, 40, 0, 0], np.zeros((4, hkv, 90), np.float32))
+    ws = ws_for(4, hkv)
+    c.compact(keep, ws)
+    assert pkc.device_status(ws) == 7 and c.dl.tolist() == [90, 16, 90, 17]
+    for got, want in zip(raw(c), pools):
+        if want is not None:
+            np.testing.assert_array_equal(got, want)
+
+
 # ---------------------------------------------------------------------------
 # Together
 # ---------------------------------------------------------------------------

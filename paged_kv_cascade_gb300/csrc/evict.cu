@@ -34,6 +34,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "mx4.cuh"
 
@@ -56,19 +57,20 @@ constexpr int kMostKeys = 1 << 19;           // keys of one block (two bits each
 constexpr int kMostHeld = 32 * 1024;         // keys of one block held in shared memory
 constexpr uint32_t kZeroKey = 0x80000000u;   // the key of weight 0
 
+// (-0 + 0 is +0; no weight's key is below 2^21)
 __device__ __forceinline__ uint32_t order_key(float w) {
-  if (w != w) return 0xffffffffu;
-  const uint32_t u = __float_as_uint(w == 0.f ? 0.f : w);
-  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
+  const uint32_t u = __float_as_uint(w + 0.f);
+  return w != w ? 0xffffffffu : u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
 struct SelectShared {
-  uint32_t hist[2][kBins];     // alternate between digits: one barrier per digit
+  uint32_t hist[2][kBins];     // alternate between digits, as do their sums:
+  int sums[2][kSelWarps];      // of the 128 bins of a warp, warp 0's the highest
   uint2 list[kListed];         // (key, index) of the first digit's bin
   int warp_sum[kSelWarps];
   int cta_gt, cta_eq;
-  int bin, rest, n_listed;
-  int pad[3];
+  int bin, rest, in_bin, n_listed;
+  int pad[2];
 };
 
 // Shared memory: SelectShared, then two bits per key (kept for certain; equal
@@ -76,7 +78,8 @@ struct SelectShared {
 // read once, as a block has an SM to itself (8 rows of 131072: 24 -> 22 us),
 // while in a batch more blocks per SM are worth more (512 rows: 28 against
 // 31 us).
-__global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const SelectParams p) {
+template <bool kHeld>
+__global__ void __launch_bounds__(kSelThreads, kHeld ? 1 : 3) evict_select_kernel(const SelectParams p) {
   extern __shared__ __align__(16) uint8_t smem_sel[];
   SelectShared& S = *reinterpret_cast<SelectShared*>(smem_sel);
   cg::cluster_group cluster = cg::this_cluster();
@@ -106,43 +109,63 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const Sele
   const int lo = min(rank * per, n), mine = min(per, n - lo);
   const float* src = p.weights + (int64_t)row * p.w_stride + p.sinks + lo;
   const int words = (mine + 31) >> 5;
-  uint32_t* sure = reinterpret_cast<uint32_t*>(smem_sel + sizeof(SelectShared));
-  uint32_t* equal = sure + words;
-  uint32_t* keys = equal + words;  // the keys themselves, where the launch gave them room
-  const bool cached = mine <= p.smem_keys;
-  for (int i = tid; i < 2 * kBins; i += kSelThreads) (&S.hist[0][0])[i] = 0;
+  uint2* bits = reinterpret_cast<uint2*>(smem_sel + sizeof(SelectShared));  // x: kept for certain, y: equal to T
+  uint32_t* held = reinterpret_cast<uint32_t*>(bits + words);
+  for (int i = tid; i < 2 * kBins / 4; i += kSelThreads)
+    reinterpret_cast<uint4*>(&S.hist[0][0])[i] = make_uint4(0, 0, 0, 0);
   if (tid == 0) S.n_listed = 0;
   __syncthreads();
 
-  // kBatch keys of this lane, a block's width apart, all loads in flight
-  // together (a shared-memory atomic between two loads would hold the second
-  // one back); 0, which no weight has, past the end.
-  auto load_keys = [&](uint32_t (&k)[kBatch], int i, bool again) {
-    if (again && cached) {
+  // One pass over the keys: use(k, x, i) for steps x of a batch (kBatch keys
+  // of a lane, a block's width apart, all loads in flight together -- a
+  // shared-memory atomic between two loads would hold the second one back),
+  // i the key's index, then flush(k, i of step 0).  k is 0, which no weight
+  // has, past the end of the last batch, whose empty steps are left out.
+  const auto pass = [&](auto from_held, auto use, auto flush) {
+    for (int i0 = warp * 32; i0 < mine; i0 += kBatch * kSelThreads) {
+      uint32_t k[kBatch];
+      const int i = i0 + lane;
+      if (i0 + (kBatch - 1) * kSelThreads + 32 <= mine) {  // (warp-uniform)
 #pragma unroll
-      for (int x = 0; x < kBatch; ++x) k[x] = i + x * kSelThreads < mine ? keys[i + x * kSelThreads] : 0u;
-      return;
+        for (int x = 0; x < kBatch; ++x)
+          k[x] = from_held ? held[i + x * kSelThreads] : __float_as_uint(src[i + x * kSelThreads]);
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+          if (!from_held) k[x] = order_key(__uint_as_float(k[x]));
+          use(k[x], x, i + x * kSelThreads);
+        }
+      } else {
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+          k[x] = 0u;
+          if (i + x * kSelThreads < mine)
+            k[x] = from_held ? held[i + x * kSelThreads] : __float_as_uint(src[i + x * kSelThreads]);
+        }
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+          if (i0 + x * kSelThreads >= mine) break;  // (warp-uniform)
+          if (!from_held) k[x] = i + x * kSelThreads < mine ? order_key(__uint_as_float(k[x])) : 0u;
+          use(k[x], x, i + x * kSelThreads);
+        }
+      }
+      flush(k, i);
     }
-    float f[kBatch];
-#pragma unroll
-    for (int x = 0; x < kBatch; ++x) f[x] = i + x * kSelThreads < mine ? src[i + x * kSelThreads] : 0.f;
-#pragma unroll
-    for (int x = 0; x < kBatch; ++x) k[x] = i + x * kSelThreads < mine ? order_key(f[x]) : 0u;
   };
+  const auto no_flush = [](const uint32_t (&)[kBatch], int) {};
+  constexpr std::false_type from_memory{};
+  constexpr std::bool_constant<kHeld> again{};
 
   // First digit.  Weights that are exactly 0 are often most of a row: each
-  // warp counts them apart, so they do not queue up on one bin.
+  // thread counts them apart, so they do not queue up on one bin.  (What is
+  // past the end counts in bin 0, which has no weights and is not reached:
+  // there are more than m of them above it.)
   int zeros = 0;
-  for (int i0 = warp * 32; i0 < mine; i0 += kBatch * kSelThreads) {
-    uint32_t k[kBatch];
-    load_keys(k, i0 + lane, false);
-#pragma unroll
-    for (int x = 0; x < kBatch; ++x) {
-      if (cached && k[x] != 0u) keys[i0 + lane + x * kSelThreads] = k[x];
-      zeros += __popc(__ballot_sync(0xffffffffu, k[x] == kZeroKey));
-      if (k[x] != 0u && k[x] != kZeroKey) atomicAdd(&S.hist[0][k[x] >> 21], 1u);
-    }
-  }
+  pass(from_memory, [&](uint32_t k, int, int i) {
+    if (kHeld && i < mine) held[i] = k;
+    if (k == kZeroKey) ++zeros;
+    else atomicAdd(&S.hist[0][k >> 21], 1u);
+  }, no_flush);
+  zeros = __reduce_add_sync(0xffffffffu, zeros);
   if (lane == 0 && zeros) atomicAdd(&S.hist[0][kZeroKey >> 21], (uint32_t)zeros);
 
   uint32_t prefix = 0;  // digits found, in place
@@ -153,28 +176,36 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const Sele
     uint32_t* hist = S.hist[d & 1];
     const uint32_t want = d == 0 ? 0u : prefix >> (shift + width), mask = (1u << width) - 1u;
     if (d == 1) {  // the second read: bits of the keys above, list of the keys in the bin
-      for (int w0 = warp; w0 < words; w0 += kBatch * kSelWarps) {
-        uint32_t k[kBatch];
-        load_keys(k, 32 * w0 + lane, true);
+      const bool zero_bin = prefix == kZeroKey;  // (zero is the lowest key of its bin)
+      // the bin's keys but zeros, which are counted already and never listed
+      const uint32_t low = prefix + (zero_bin ? 1u : 0u), last = prefix | ((1u << 21) - 1u), span = last - low;
+      uint32_t in = 0;  // steps of the batch whose key is one of them
+      pass(again, [&](uint32_t k, int x, int i) {
+        const uint32_t above = __ballot_sync(0xffffffffu, k > last);
+        const uint32_t zero = zero_bin ? __ballot_sync(0xffffffffu, k == kZeroKey) : 0u;
+        if (lane == 0) bits[i >> 5] = make_uint2(above, zero);
+        if (k - low <= span) in |= 1u << x;
+      }, [&](const uint32_t (&k)[kBatch], int i) {
+        if (!__any_sync(0xffffffffu, in != 0u)) return;
+        int at = __popc(in);  // places in the list: one atomic per warp and batch
+#pragma unroll
+        for (int x = 1; x < 32; x <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, at, x);
+          if (lane >= x) at += y;
+        }
+        int first = 0;
+        if (lane == 31) first = atomicAdd(&S.n_listed, at);
+        at += __shfl_sync(0xffffffffu, first, 31) - __popc(in);
 #pragma unroll
         for (int x = 0; x < kBatch; ++x) {
-          const int wd = w0 + x * kSelWarps;
-          const uint32_t top = k[x] >> 21;
-          const uint32_t above = __ballot_sync(0xffffffffu, top > want);
-          const uint32_t zero = __ballot_sync(0xffffffffu, k[x] == kZeroKey && top == want);
-          if (lane == 0 && wd < words) {
-            sure[wd] = above;
-            equal[wd] = zero;
-          }
-          if (top == want && k[x] != 0u && k[x] != kZeroKey) {  // (zeros are counted already, and never listed)
-            const int at = atomicAdd(&S.n_listed, 1);
-            if (at < kListed) S.list[at] = make_uint2(k[x], (uint32_t)(32 * wd + lane));
+          if ((in >> x) & 1u) {
+            if (at < kListed) S.list[at] = make_uint2(k[x], (uint32_t)(i + x * kSelThreads));
+            ++at;
             atomicAdd(&hist[(k[x] >> shift) & mask], 1u);
           }
         }
-      }
-      __syncthreads();
-      listed = S.n_listed <= kListed;
+        in = 0;
+      });
     } else if (d == 2) {
       if (listed) {
         for (int i = tid; i < S.n_listed; i += kSelThreads) {
@@ -182,94 +213,106 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const Sele
           if ((k >> (shift + width)) == want) atomicAdd(&hist[(k >> shift) & mask], 1u);
         }
       } else {
-        for (int i = tid; i < mine; i += kSelThreads) {
-          const uint32_t k = order_key(src[i]);
+        pass(again, [&](uint32_t k, int, int) {
           if ((k >> (shift + width)) == want && k != kZeroKey) atomicAdd(&hist[(k >> shift) & mask], 1u);
-        }
+        }, no_flush);
       }
     }
     if (d > 0 && lane == 0 && zeros && (kZeroKey >> (shift + width)) == want)
       atomicAdd(&hist[(kZeroKey >> shift) & mask], (uint32_t)zeros);
-    if (n_cta > 1) cluster.sync();  // every block's histogram is complete
-    else __syncthreads();
-    // Counts of this thread's four bins, from the top: thread 0 has the highest.
-    const int bin0 = kBins - 4 - 4 * tid;
-    int cnt[4];
+    __syncthreads();  // this block's histogram (and, of the second digit, its list) is complete
+    if (d == 1) listed = S.n_listed <= kListed;
     {
-      const uint4 x = *reinterpret_cast<const uint4*>(hist + bin0);
-      cnt[0] = x.w; cnt[1] = x.z; cnt[2] = x.y; cnt[3] = x.x;
+      const uint4 x = *reinterpret_cast<const uint4*>(hist + kBins - 4 - 4 * tid);
+      const int sum = __reduce_add_sync(0xffffffffu, (int)(x.x + x.y + x.z + x.w));
+      if (lane == 0) S.sums[d & 1][warp] = sum;
     }
-    if (n_cta > 1) {
+    if (n_cta > 1) cluster.sync();
+    else __syncthreads();
+    if (warp == 0) {
+      // The bin in which the count from above reaches `rest`: first the group
+      // of 128 bins, then the bin, counts of all blocks added up.
+      int g = 0;
 #pragma unroll
-      for (int c0 = 0; c0 < 8; c0 += 4) {
-        uint4 x[4];
+      for (int c = 0; c < 8; ++c)
+        if (c < n_cta && lane < kSelWarps) g += (c == rank ? &S : cluster.map_shared_rank(&S, c))->sums[d & 1][lane];
+      int upto = g;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          x[c] = make_uint4(0, 0, 0, 0);
-          if (c0 + c < n_cta && c0 + c != rank)
-            x[c] = *reinterpret_cast<const uint4*>(cluster.map_shared_rank(hist, c0 + c) + bin0);
-        }
+      for (int x = 1; x < kSelWarps; x <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, x);
+        if (lane >= x) upto += y;
+      }
+      const uint32_t here = __ballot_sync(0xffffffffu, upto - g < rest && rest <= upto);
+      const int group = here ? __ffs(here) - 1 : 0;
+      const int left = rest - __shfl_sync(0xffffffffu, upto - g, group);
+      const int bin0 = kBins - 128 * group - 4 - 4 * lane;
+      int cnt[4] = {0, 0, 0, 0};  // from the top
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          cnt[0] += x[c].w; cnt[1] += x[c].z; cnt[2] += x[c].y; cnt[3] += x[c].x;
+      for (int c = 0; c < 8; ++c) {
+        if (c < n_cta) {
+          const uint4 x = *reinterpret_cast<const uint4*>((c == rank ? hist : cluster.map_shared_rank(hist, c)) + bin0);
+          cnt[0] += x.w; cnt[1] += x.z; cnt[2] += x.y; cnt[3] += x.x;
         }
       }
-    }
-    const int sum = cnt[0] + cnt[1] + cnt[2] + cnt[3];
-    int above = sum;  // inclusive scan over the block
+      const int sum = cnt[0] + cnt[1] + cnt[2] + cnt[3];
+      int above = sum;
 #pragma unroll
-    for (int x = 1; x < 32; x <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, above, x);
-      if (lane >= x) above += y;
-    }
-    if (lane == 31) S.warp_sum[warp] = above;
-    if (tid == 0) {  // (replaced below, unless the weights change under the kernel)
-      S.bin = 0;
-      S.rest = rest;
-    }
-    __syncthreads();
-    above -= sum;  // keys in higher bins than this thread's
-#pragma unroll
-    for (int x = 0; x < kSelWarps; ++x) above += x < warp ? S.warp_sum[x] : 0;
-    if (above < rest && rest <= above + sum) {  // exactly one thread
-#pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        if (above < rest && rest <= above + cnt[x]) {
-          S.bin = bin0 + 3 - x;
-          S.rest = rest - above;
-        }
-        above += cnt[x];
+      for (int x = 1; x < 32; x <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, above, x);
+        if (lane >= x) above += y;
       }
+      above -= sum;  // keys of the group in higher bins than this lane's
+      const bool mine_is_it = above < left && left <= above + sum;
+      if (mine_is_it) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          if (above < left && left <= above + cnt[x]) {
+            S.bin = bin0 + 3 - x;
+            S.rest = left - above;
+            S.in_bin = cnt[x];
+          }
+          above += cnt[x];
+        }
+      }
+      // (always found, unless the weights change under the kernel)
+      if (!__any_sync(0xffffffffu, mine_is_it) && lane == 0) {
+        S.bin = d == 0 ? kBins - 1 : 0;
+        S.rest = rest;
+        S.in_bin = 0;
+      }
+    } else if (d == 1) {  // the third digit's histogram is the first's: every block is past it
+      for (int i = tid - 32; i < kBins / 4; i += kSelThreads - 32)
+        reinterpret_cast<uint4*>(S.hist[0])[i] = make_uint4(0, 0, 0, 0);
     }
-    if (d == 1)  // the third digit's histogram is the first's: every block is past it
-      for (int i = tid; i < kBins; i += kSelThreads) S.hist[0][i] = 0;
     __syncthreads();
     prefix |= (uint32_t)S.bin << shift;
     rest = S.rest;
+    // All keys with these digits are kept (often there is one): T is just
+    // below them.  (Not where zeros are among them: they have no `sure` bit.)
+    if (d == 1 && S.in_bin == rest && prefix != kZeroKey) {
+      prefix -= 1u;
+      rest = 0;
+      break;
+    }
   }
   // T = prefix.  Keys above T are kept, and the first `rest` of those equal
-  // to it.  The bits so far: `sure` has the keys above the first digit's bin,
-  // `equal` that bin's zeros; now the bin's other keys.
+  // to it.  The bits so far: those of the keys above the first digit's bin,
+  // and that bin's zeros; now the bin's other keys.
   if (listed) {
     if (prefix != kZeroKey) {
-      for (int i = tid; i < words; i += kSelThreads) equal[i] = 0u;
+      for (int i = tid; i < words; i += kSelThreads) bits[i].y = 0u;
       __syncthreads();
     }
     for (int i = tid; i < S.n_listed; i += kSelThreads) {
       const uint2 k = S.list[i];
-      if (k.x > prefix) atomicOr(&sure[k.y >> 5], 1u << (k.y & 31));
-      else if (k.x == prefix) atomicOr(&equal[k.y >> 5], 1u << (k.y & 31));
+      if (k.x > prefix) atomicOr(&bits[k.y >> 5].x, 1u << (k.y & 31));
+      else if (k.x == prefix) atomicOr(&bits[k.y >> 5].y, 1u << (k.y & 31));
     }
   } else {
-    for (int wd = warp; wd < words; wd += kSelWarps) {
-      const int i = 32 * wd + lane;
-      const uint32_t k = i < mine ? order_key(src[i]) : 0u;
-      const uint32_t g = __ballot_sync(0xffffffffu, k > prefix), e = __ballot_sync(0xffffffffu, k == prefix && i < mine);
-      if (lane == 0) {
-        sure[wd] = g;
-        equal[wd] = e;
-      }
-    }
+    pass(again, [&](uint32_t k, int, int i) {
+      const uint32_t g = __ballot_sync(0xffffffffu, k > prefix), e = __ballot_sync(0xffffffffu, k == prefix);
+      if (lane == 0) bits[i >> 5] = make_uint2(g, e);
+    }, no_flush);
   }
   __syncthreads();
   // Keys above and equal in the blocks before this one.
@@ -277,8 +320,8 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const Sele
   if (n_cta > 1) {
     int g = 0, e = 0;
     for (int i = tid; i < words; i += kSelThreads) {
-      g += __popc(sure[i]);
-      e += __popc(equal[i]);
+      g += __popc(bits[i].x);
+      e += __popc(bits[i].y);
     }
     g = __reduce_add_sync(0xffffffffu, g);
     e = __reduce_add_sync(0xffffffffu, e);
@@ -298,8 +341,9 @@ __global__ void __launch_bounds__(kSelThreads, 3) evict_select_kernel(const Sele
   // Ranks: a thread per word, 512 words at a time.
   for (int w0 = 0; w0 < words; w0 += kSelThreads) {
     const int wd = w0 + tid;
-    const uint32_t s = wd < words ? sure[wd] : 0u;
-    uint32_t x = wd < words ? equal[wd] : 0u;
+    const uint2 both_bits = wd < words ? bits[wd] : make_uint2(0u, 0u);
+    const uint32_t s = both_bits.x;
+    uint32_t x = both_bits.y;
     const int both = __popc(s) | (__popc(x) << 16);  // (512 words have at most 2^14 of each)
     int scan = both;
 #pragma unroll
@@ -520,8 +564,10 @@ int launch_evict_select(const SelectParams& p_in, void* stream) {
   // (the most: bits of kMostKeys, or kMostHeld keys and their bits)
   constexpr int kMostSmem = (int)sizeof(SelectShared) + std::max(kMostKeys / 4, kMostHeld * 17 / 4);
   static_assert(kMostSmem <= 227 * 1024, "shared memory");
-  static std::atomic<uint64_t> raised;
-  if (const int e = raise_smem_limit(reinterpret_cast<const void*>(evict_select_kernel), kMostSmem, raised)) return e;
+  static std::atomic<uint64_t> raised[2];
+  const bool hold = p.smem_keys > 0;
+  const auto kernel = hold ? evict_select_kernel<true> : evict_select_kernel<false>;
+  if (const int e = raise_smem_limit(reinterpret_cast<const void*>(kernel), kMostSmem, raised[hold])) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(rows * p.cluster));
   cfg.blockDim = dim3(kSelThreads);
@@ -533,7 +579,7 @@ int launch_evict_select(const SelectParams& p_in, void* stream) {
   la[0].val.clusterDim.y = la[0].val.clusterDim.z = 1;
   cfg.attrs = la;
   cfg.numAttrs = 1;
-  return (int)cudaLaunchKernelEx(&cfg, evict_select_kernel, p);
+  return (int)cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 int launch_evict_compact(const CompactParams& p_in, void* stream) {

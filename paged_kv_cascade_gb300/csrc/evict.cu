@@ -79,7 +79,7 @@ struct SelectShared {
 // while in a batch more blocks per SM are worth more (512 rows: 28 against
 // 31 us).
 template <bool kHeld>
-__global__ void __launch_bounds__(kSelThreads, kHeld ? 1 : 3) evict_select_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kSelThreads, kHeld ? 1 : 2) evict_select_kernel(const SelectParams p) {
   extern __shared__ __align__(16) uint8_t smem_sel[];
   SelectShared& S = *reinterpret_cast<SelectShared*>(smem_sel);
   cg::cluster_group cluster = cg::this_cluster();
@@ -479,10 +479,9 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const Compa
       const int32_t k = keep[j];
       bad_keep = bad_keep || k < (j > 0 ? keep[j - 1] + 1 : 0) || k >= len;
     }
-    bad_page = __syncthreads_or(bad_page);
-    bad_keep = __syncthreads_or(bad_keep);
-    unchosen = __syncthreads_or(unchosen);
-    if (bad_page || bad_keep) {
+    if (__syncthreads_or(bad_page || bad_keep)) {
+      bad_page = __syncthreads_or(bad_page);
+      unchosen = __syncthreads_or(unchosen);
       if (tid == 0) report(p.status, bad_page ? PKC_ERR_BLOCK_TABLE : PKC_ERR_PLAN);
       bad_request = bad_page || unchosen;
     } else {

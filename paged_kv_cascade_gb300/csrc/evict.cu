@@ -12,24 +12,25 @@
 // a bit for every key above the bin and lists the keys in it, a percent or
 // so, on which the other digits work (they read the weights again if the
 // list is too short, as for a row of equal weights).  Then the bits of the
-// kept slots are ranked: a thread per 32 of them, one scan.  A row takes
-// 512 threads of 40 registers and about 30 KB of shared memory, so three
-// blocks share an SM; a cluster of up to 8 blocks works on one row where
-// there are few, adding up their histograms through distributed shared
-// memory.  What bounds it is the chain of reads and barriers per row, not
-// HBM: 29 us for 512 rows of 1024 to 16384 weights (one read of them at the
-// copy rate would be 3), 22 us for 8 rows of 131,056 on 64 blocks.
+// kept slots are ranked: a thread per 32 of them, one scan.  Two rows
+// share an SM (512 threads of 64 registers each); a cluster of up to 8 blocks
+// works on one row where there are few, adding up their histograms through
+// distributed shared memory.  What bounds it is instructions (about 100 per
+// 32 weights and pass, with the fixed part) and the chain of reads and
+// barriers per row, not HBM: 23 us for 512 rows of 1024 to 16384 weights (one
+// read of them at the copy rate would be 3), 16 us for 8 rows of 131,056 on
+// 64 blocks.
 //
 // Compact.  Row j of a (request, head) becomes row keep[j]; keep ascends
 // strictly, so keep[j] >= j.  A block moves one slice of one head's K or V
-// rows, chunk after chunk of new slots in order, each chunk in registers
-// before any of it is written.  The next chunk's rows lie at or behind its
-// own first slot, where nothing has been written yet, so its loads are in
-// flight while the current chunk is stored.  Bound by HBM: a kept row is
-// read once and written once, 256 bytes at a random slot: 116 us for 64
-// requests cut to 1024 of up to 6144 tokens, 8 heads of bf16 (549 MB, 4.7
-// TB/s of a measured copy rate of 6.8).  Two rows a thread and chunk: four
-// take 126 us, eight 137, for want of resident blocks.
+// rows, chunk after chunk of new slots in order, a chunk read by the whole
+// block before any of it is written.  The next chunk's rows lie at or behind
+// its own first slot, where nothing has been written yet, so its copies into
+// shared memory are in flight while the current chunk is stored.  Bound by
+// HBM: a kept row is read once and written once, 256 bytes at a random slot:
+// 100 us for 64 requests cut to 1024 of up to 6144 tokens, 8 heads of bf16
+// (549 MB, 5.5 TB/s of a measured copy rate of 6.8).  With the chunks in
+// registers, of half the size, it took 120 us.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -74,12 +75,11 @@ struct SelectShared {
 };
 
 // Shared memory: SelectShared, then two bits per key (kept for certain; equal
-// to T), then the keys where there are no more rows than SMs: those rows are
-// read once, as a block has an SM to itself (8 rows of 131072: 24 -> 22 us),
-// while in a batch more blocks per SM are worth more (512 rows: 28 against
-// 31 us).
+// to T), then (kHeld) the keys, so that the weights are read once.  Three
+// blocks an SM instead of two spill registers and hold no keys (512 rows:
+// 24.1 us; two blocks 23.1, with the keys 22.1).
 template <bool kHeld>
-__global__ void __launch_bounds__(kSelThreads, kHeld ? 1 : 2) evict_select_kernel(const SelectParams p) {
+__global__ void __launch_bounds__(kSelThreads, 2) evict_select_kernel(const SelectParams p) {
   extern __shared__ __align__(16) uint8_t smem_sel[];
   SelectShared& S = *reinterpret_cast<SelectShared*>(smem_sel);
   cg::cluster_group cluster = cg::this_cluster();
@@ -378,23 +378,29 @@ __global__ void __launch_bounds__(kSelThreads, kHeld ? 1 : 2) evict_select_kerne
 // ---------------------------------------------------------------------------
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRows = 2;  // rows per thread and chunk (two chunks in registers)
+// Few large chunks: a chunk costs a barrier and the latency of its copies (2
+// rows a thread and 3 chunks 109 us, 3 and 2 106, 4 and 2 100).
+constexpr int kMoveRows = 4;    // rows per thread and chunk
+constexpr int kMoveStages = 2;  // chunks on their way or being stored
 
-__device__ __forceinline__ uint4 load_cg(const uint4* p) { return __ldcg(p); }
-__device__ __forceinline__ uint32_t load_cg(const uint32_t* p) { return __ldcg(p); }
+struct MoveShared {
+  uint4 rows[kMoveStages][kMoveRows][kMoveThreads];
+  uint32_t to[kMoveStages][kMoveRows][kMoveThreads];
+};
 
 // Move rows keep[j] -> j, j < n, in units of V (one unit of a row per
 // thread): place(slot) is a slot's place, at(place) this thread's unit of it,
 // `row` the thread's row within a pass of `rows` rows.  Called by a whole
-// block.  A chunk is kMoveRows passes.  While chunk c is stored, the rows of
-// chunk c + 1 are on their way, the places of chunk c + 2 and the slots of
-// chunk c + 3.
+// block.  A chunk is kMoveRows passes.  While chunk c is stored, the chunks
+// up to c + kMoveStages - 1 are on their way into shared memory (each
+// thread's units in places of its own), the places of the next one and the
+// slots of the one after it into registers.
 template <typename V, typename Place, typename At>
-__device__ __forceinline__ void move_rows(const int32_t* keep, int n, int row, int rows, Place place, At at) {
-  const int chunk = rows * kMoveRows;
-  V buf[2][kMoveRows];
-  int32_t slot[kMoveRows];                  // chunk c + 3's slots (-1 past the end)
-  uint32_t from[kMoveRows], to[kMoveRows];  // chunk c + 2's places
+__device__ __forceinline__ void move_rows(MoveShared& S, const int32_t* keep, int n, int row, int rows, Place place,
+                                          At at) {
+  const int chunk = rows * kMoveRows, tid = threadIdx.x;
+  int32_t slot[kMoveRows];                  // (-1 past the end)
+  uint32_t from[kMoveRows], to[kMoveRows];
   auto load_slots = [&](int c) {
 #pragma unroll
     for (int u = 0; u < kMoveRows; ++u) {
@@ -413,42 +419,48 @@ __device__ __forceinline__ void move_rows(const int32_t* keep, int n, int row, i
       }
     }
   };
-  auto load = [&](V (&x)[kMoveRows], uint32_t (&dst)[kMoveRows]) {  // (from == to: nothing to move)
+  auto copy = [&](int stage) {  // (from == to: nothing to move)
 #pragma unroll
     for (int u = 0; u < kMoveRows; ++u) {
       const bool moves = from[u] != to[u];
-      dst[u] = moves ? to[u] : kNoToken;
-      if (moves) x[u] = load_cg(at(from[u]));
+      S.to[stage][u][tid] = moves ? to[u] : kNoToken;
+      if (moves) {
+        const uint32_t dst = smem_u32(&S.rows[stage][u][tid]);
+        const uint64_t src = reinterpret_cast<uint64_t>(at(from[u]));
+        if constexpr (sizeof(V) == 16) cp_async16(dst, src);
+        else cp_async4(dst, src, true);
+      }
     }
+    cp_async_commit();
   };
-  auto store = [&](const V (&x)[kMoveRows], const uint32_t (&dst)[kMoveRows]) {
-#pragma unroll
-    for (int u = 0; u < kMoveRows; ++u)
-      if (dst[u] != kNoToken) *at(dst[u]) = x[u];
-  };
-  uint32_t dst[2][kMoveRows];
   load_slots(0);
   load_places(0);
   load_slots(chunk);
-  load(buf[0], dst[0]);
-  load_places(chunk);
-  load_slots(2 * chunk);
-  for (int c = 0; c < n; c += 2 * chunk) {
-    load(buf[1], dst[1]);
-    load_places(c + 2 * chunk);
-    load_slots(c + 3 * chunk);
-    __syncthreads();  // chunk c has been read by every thread
-    store(buf[0], dst[0]);
-    if (c + chunk >= n) break;
-    load(buf[0], dst[0]);
-    load_places(c + 3 * chunk);
-    load_slots(c + 4 * chunk);
-    __syncthreads();
-    store(buf[1], dst[1]);
+#pragma unroll
+  for (int s = 0; s < kMoveStages - 1; ++s) {
+    copy(s);
+    load_places((s + 1) * chunk);
+    load_slots((s + 2) * chunk);
   }
+  int stage = 0;
+  for (int c = 0; c < n; c += chunk) {
+    cp_async_wait<kMoveStages - 2>();
+    __syncthreads();  // chunk c has been read by every thread
+#pragma unroll
+    for (int u = 0; u < kMoveRows; ++u) {
+      const uint32_t t = S.to[stage][u][tid];
+      if (t != kNoToken) *at(t) = *reinterpret_cast<const V*>(&S.rows[stage][u][tid]);
+    }
+    copy(stage ? stage - 1 : kMoveStages - 1);
+    load_places(c + kMoveStages * chunk);
+    load_slots(c + (kMoveStages + 1) * chunk);
+    stage = stage + 1 == kMoveStages ? 0 : stage + 1;
+  }
+  cp_async_wait<0>();
 }
 
 __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const CompactParams p) {
+  __shared__ MoveShared S;
   const int part = (int)(blockIdx.x % p.parts);
   const int row = (int)(blockIdx.x / p.parts), b = row / p.hkv, h = row % p.hkv;
   const int tid = threadIdx.x;
@@ -496,15 +508,15 @@ __global__ void __launch_bounds__(kMoveThreads) evict_compact_kernel(const Compa
         uint8_t* base = static_cast<uint8_t*>(part & 1 ? p.v_cache : p.k_cache) + (int64_t)h * p.row_bytes +
                         16 * ((part >> 1) * units + tid % units);
         const uint32_t stride = (uint32_t)p.hkv * (uint32_t)p.row_bytes;
-        move_rows<uint4>(keep, n, tid / units, kMoveThreads / units, token, [&](uint32_t t) {
+        move_rows<uint4>(S, keep, n, tid / units, kMoveThreads / units, token, [&](uint32_t t) {
           return reinterpret_cast<uint4*>(const_cast<uint8_t*>(at_row(base, t, stride)));
         });
       } else if (part < 2 * p.slices + (p.k_scales ? 2 : 0)) {  // mx4 scales: 4 bytes a row
         uint32_t* base = static_cast<uint32_t*>((part - 2 * p.slices) ? p.v_scales : p.k_scales) + h;
-        move_rows<uint32_t>(keep, n, tid, kMoveThreads, token, [&](uint32_t t) { return base + (int64_t)t * p.hkv; });
+        move_rows<uint32_t>(S, keep, n, tid, kMoveThreads, token, [&](uint32_t t) { return base + (int64_t)t * p.hkv; });
       } else {  // weights: the kept ones, zeros behind them
         uint32_t* w = reinterpret_cast<uint32_t*>(p.weights) + (int64_t)row * p.w_stride;
-        move_rows<uint32_t>(keep, n, tid, kMoveThreads, [](int slot) { return (uint32_t)slot; },
+        move_rows<uint32_t>(S, keep, n, tid, kMoveThreads, [](int slot) { return (uint32_t)slot; },
                             [&](uint32_t t) { return w + t; });
         __syncthreads();
         for (int j = n + tid; j < len; j += kMoveThreads) w[j] = 0u;
@@ -558,13 +570,14 @@ int launch_evict_select(const SelectParams& p_in, void* stream) {
     p.cluster *= 2;
   const int64_t per = ((p.w_stride + p.cluster - 1) / p.cluster + 31) & ~int64_t(31);
   if (per > kMostKeys) return (int)cudaErrorInvalidValue;
-  p.smem_keys = rows * p.cluster <= num_sms() && per <= kMostHeld ? (int)per : 0;
-  const int smem = (int)sizeof(SelectShared) + (int)(per / 32) * 8 + 4 * p.smem_keys;
+  // Keys are held where two blocks still share an SM, or each has one.
+  const int64_t base = (int64_t)sizeof(SelectShared) + per / 32 * 8;
+  const bool hold = base + 4 * per <= 113 * 1024 || (rows * p.cluster <= num_sms() && per <= kMostHeld);
+  const int smem = (int)(base + (hold ? 4 * per : 0));
   // (the most: bits of kMostKeys, or kMostHeld keys and their bits)
   constexpr int kMostSmem = (int)sizeof(SelectShared) + std::max(kMostKeys / 4, kMostHeld * 17 / 4);
   static_assert(kMostSmem <= 227 * 1024, "shared memory");
   static std::atomic<uint64_t> raised[2];
-  const bool hold = p.smem_keys > 0;
   const auto kernel = hold ? evict_select_kernel<true> : evict_select_kernel<false>;
   if (const int e = raise_smem_limit(reinterpret_cast<const void*>(kernel), kMostSmem, raised[hold])) return e;
   cudaLaunchConfig_t cfg = {};
@@ -585,10 +598,11 @@ int launch_evict_compact(const CompactParams& p_in, void* stream) {
   CompactParams p = p_in;
   const int64_t rows = (int64_t)p.batch * p.hkv;
   if (rows <= 0) return 0;
-  // Whole rows per block while that fills the machine (8 blocks per SM);
-  // else slices of a row, down to a 32-byte sector.
+  // Whole rows per block while that fills the machine (4 blocks per SM; twice
+  // as many half rows there: 100 -> 102 us); else slices of a row, down to a
+  // 32-byte sector.
   p.slices = 1;
-  while (p.row_bytes / p.slices > 32 && rows * 2 * p.slices < 8 * (int64_t)num_sms()) p.slices *= 2;
+  while (p.row_bytes / p.slices > 32 && rows * 2 * p.slices < 4 * (int64_t)num_sms()) p.slices *= 2;
   p.parts = 2 * p.slices + (p.k_scales ? 2 : 0) + (p.weights ? 1 : 0);
   if (rows * p.parts > INT32_MAX) return (int)cudaErrorInvalidValue;
   evict_compact_kernel<<<(unsigned)(rows * p.parts), kMoveThreads, 0, (cudaStream_t)stream>>>(p);

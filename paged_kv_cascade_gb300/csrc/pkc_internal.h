@@ -289,7 +289,7 @@ struct SelectParams {
   int32_t* keep;             // [batch, hkv, budget]
   int64_t w_stride;
   int batch, hkv, budget, sinks, recent;
-  int cluster, smem_keys;    // set by the launcher: blocks per row, keys that a block holds in shared memory
+  int cluster;               // set by the launcher: blocks per row
   int32_t* status;
 };
 

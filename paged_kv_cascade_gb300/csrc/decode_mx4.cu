@@ -454,7 +454,10 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     for (int e = 0; e < 2; ++e) {  // heads 2 tg, 2 tg + 1: dims 32 b + 4 g .. + 3
       const int hd = 2 * tg + e;
       const float m = e ? m1 : m0, l = e ? l1 : l0;
-      const float inv = l == 0.f ? 0.f : 1.f / l;  // (a NaN sum gives NaN)
+      // Unnormalised values go to the merge times 2^-32: sums are at most 2^15
+      // per token, so values near float32's largest stay finite (and those
+      // below 2^-101 lose bits, below 2^-117 some of bf16's).
+      const float inv = wph > 1 ? 0x1p-32f : l == 0.f ? 0.f : 1.f / l;  // (a NaN sum gives NaN)
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
         const float f = mx4_scale((uint32_t)__shfl_sync(0xffffffffu, e_ref, b)) * inv;
@@ -475,9 +478,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     }
     __syncthreads();  // the next item is there; the warps' states are written
     if (wph > 1) {
-      // Warps of one head: values, reference and sum, merged by a warp per (KV
-      // head, query head) row, 4 dims per lane.  The weights add up to 1, so
-      // values near float32's largest stay finite.
+      // Warps of one head: unnormalised values, reference and sum, merged by a
+      // warp per (KV head, query head) row, 4 dims per lane.
       for (int r = warp; r < HG * G; r += kWarps) {
         const int h = r / G, hd = r - h * G;
         float mm = kRefFloor, ll = 0.f;
@@ -485,16 +487,14 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         for (int c = 0; c < wph; ++c) mm = fmaxf(mm, merge[((h + HG * c) * G + hd) * kMergeRow + D]);
         for (int c = 0; c < wph; ++c) {
           const float* src = merge + ((h + HG * c) * G + hd) * kMergeRow;
-          ll = fmaf(src[D + 1], ex2(src[D] - mm), ll);
-        }
-        const float inv = ll == 0.f ? 0.f : 1.f / ll;
-        for (int c = 0; c < wph; ++c) {
-          const float* src = merge + ((h + HG * c) * G + hd) * kMergeRow;
-          const float w = src[D + 1] * ex2(src[D] - mm) * inv;
+          const float w = ex2(src[D] - mm);
+          ll = fmaf(src[D + 1], w, ll);
           const float4 v = *reinterpret_cast<const float4*>(src + 4 * lane);
           acc.x = fmaf(v.x, w, acc.x); acc.y = fmaf(v.y, w, acc.y);
           acc.z = fmaf(v.z, w, acc.z); acc.w = fmaf(v.w, w, acc.w);
         }
+        const float inv = ll == 0.f ? 0.f : 0x1p32f / ll;
+        acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
         const int hq = (it.hg * HG + h) * G + hd;
         write4(hq, 4 * lane, acc);
         if (lane == 0) write_lse(hq, mm, ll);
@@ -505,7 +505,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   if (dyn && warp == 0) queue.finish(lane);
 }
 
-// The join of split requests: one block per (request, query head), its kW
+// The join of split requests: one block per (request, query head) -- more
+// rows each if the uploaded plan has more than the host's copy of it -- its kW
 // warps taking every kW-th of the request's chunk states, lane i dims 4 i ..
 // + 3; then the warps' sums through shared memory.  An empty request's row is
 // (0, -inf).
@@ -514,54 +515,55 @@ __global__ void __launch_bounds__(kW * 32) join_mx4_kernel(const __grid_constant
   __shared__ float4 part[kW][32];
   __shared__ float part_l[kW];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int row = (int)(blockIdx.x / (unsigned)p.hq), hq = (int)(blockIdx.x % (unsigned)p.hq);
+  const int hq = (int)(blockIdx.x % (unsigned)p.hq), stride = (int)(gridDim.x / (unsigned)p.hq);
   const int32_t* pl = p.plan;
   // The list and its places are the uploaded plan's, whatever the host's copy
   // says (a plan that is not there is reported by the decode).
-  const bool plan_ok = device_plan_ok(pl, p.plan_words, p.batch) && row < pl[PKC_PLAN_N_SPLIT] + pl[PKC_PLAN_N_EMPTY];
+  const int rows = device_plan_ok(pl, p.plan_words, p.batch) ? pl[PKC_PLAN_N_SPLIT] + pl[PKC_PLAN_N_EMPTY] : 0;
+  const int off_list = pl[PKC_PLAN_OFF_UNIT_LIST], off_req = pl[PKC_PLAN_OFF_UNIT_REQ];
   const int off_n = pl[PKC_PLAN_OFF_UNIT_N_CHUNKS], off_first = pl[PKC_PLAN_OFF_UNIT_PARTIAL_BEGIN];
-  const int off_req = pl[PKC_PLAN_OFF_UNIT_REQ];
-  int n = 0, first = 0, req = 0;
-  if (plan_ok) {
-    const int unit = pl[pl[PKC_PLAN_OFF_UNIT_LIST] + row];
-    n = pl[off_n + unit];
-    first = pl[off_first + unit];
-    req = pl[off_req + unit];
-  }
-  grid_wait_prerequisites();  // the decode grid's states
-  if (!plan_ok) return;
-  const int64_t base = (int64_t)first * p.hq + hq;  // state c at base + c hq
-  float m = neg_inf();
-  for (int c = lane; c < n; c += 32) m = fmaxf(m, p.part_lse[base + (int64_t)c * p.hq]);
+  bool waited = false;
+  for (int row = (int)(blockIdx.x / (unsigned)p.hq); row < rows; row += stride) {
+    const int unit = pl[off_list + row];
+    const int n = pl[off_n + unit], first = pl[off_first + unit], req = pl[off_req + unit];
+    if (!waited) grid_wait_prerequisites();  // the decode grid's states
+    waited = true;
+    const int64_t base = (int64_t)first * p.hq + hq;  // state c at base + c hq
+    float m = neg_inf();
+    for (int c = lane; c < n; c += 32) m = fmaxf(m, p.part_lse[base + (int64_t)c * p.hq]);
 #pragma unroll
-  for (int x = 1; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-  const float ref = m == neg_inf() ? 0.f : m;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float l = 0.f;
+    for (int x = 1; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    const float ref = m == neg_inf() ? 0.f : m;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
 #pragma unroll 8
-  for (int c = warp; c < n; c += kW) {
-    const int64_t at = base + (int64_t)c * p.hq;
-    const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * D + 4 * lane);
-    const float w = ex2((p.part_lse[at] - ref) * kLog2e);
-    l += w;
-    acc.x = fmaf(v.x, w, acc.x); acc.y = fmaf(v.y, w, acc.y);
-    acc.z = fmaf(v.z, w, acc.z); acc.w = fmaf(v.w, w, acc.w);
-  }
-  part[warp][lane] = acc;
-  if (lane == 0) part_l[warp] = l;
-  __syncthreads();
-  if (warp != 0) return;
+    for (int c = warp; c < n; c += kW) {
+      const int64_t at = base + (int64_t)c * p.hq;
+      const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * D + 4 * lane);
+      const float w = ex2((p.part_lse[at] - ref) * kLog2e);
+      l += w;
+      acc.x = fmaf(v.x, w, acc.x); acc.y = fmaf(v.y, w, acc.y);
+      acc.z = fmaf(v.z, w, acc.z); acc.w = fmaf(v.w, w, acc.w);
+    }
+    part[warp][lane] = acc;
+    if (lane == 0) part_l[warp] = l;
+    __syncthreads();
+    if (warp == 0) {
 #pragma unroll
-  for (int x = 1; x < kW; ++x) {
-    const float4 v = part[x][lane];
-    acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
-    l += part_l[x];
+      for (int x = 1; x < kW; ++x) {
+        const float4 v = part[x][lane];
+        acc.x += v.x; acc.y += v.y; acc.z += v.z; acc.w += v.w;
+        l += part_l[x];
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      T* dst = static_cast<T*>(p.o) + ((int64_t)req * p.hq + hq) * D + 4 * lane;
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(Elem<T>::from_f2(acc.x * inv, acc.y * inv), Elem<T>::from_f2(acc.z * inv, acc.w * inv));
+      if (lane == 0) p.lse[(int64_t)req * p.hq + hq] = l == 0.f ? neg_inf() : ref + lg2(l) * kLn2;
+    }
+    __syncthreads();  // `part` is free
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  T* dst = static_cast<T*>(p.o) + ((int64_t)req * p.hq + hq) * D + 4 * lane;
-  *reinterpret_cast<uint2*>(dst) =
-      make_uint2(Elem<T>::from_f2(acc.x * inv, acc.y * inv), Elem<T>::from_f2(acc.z * inv, acc.w * inv));
-  if (lane == 0) p.lse[(int64_t)req * p.hq + hq] = l == 0.f ? neg_inf() : ref + lg2(l) * kLn2;
+  if (!waited) grid_wait_prerequisites();  // (at every exit: what follows this grid must not overtake the decode's)
 }
 
 template <typename T, int G>
@@ -617,8 +619,7 @@ int launch_paged_decode_mx4(const Mx4DecodeParams& p_in, int n_work, int dtype, 
 }
 
 int launch_join_mx4(const Mx4JoinParams& p, int n_rows, int n_states, int dtype, void* stream) {
-  const int64_t blocks = (int64_t)p.batch * p.hq;  // (the uploaded plan says how many rows there are)
-  if (blocks <= 0) return 0;
+  const int64_t blocks = (int64_t)(n_rows < 1 ? 1 : n_rows) * p.hq;
   if (blocks > INT32_MAX) return (int)cudaErrorInvalidValue;
   // Launched as the decode's programmatic dependent: the blocks start as the
   // decode's end.  Rows of many states (a long request alone on the machine

@@ -204,6 +204,7 @@ def rows_of(kind, shape, rng):
     (1, [9], 1, 0, 1),
     (1, [9], 1, 0, 0),
     (80, [5000, 4097], 1000, 4, 100),
+    (80, [30000, 26000], 5000, 4, 100),
 ])
 def test_select(kind, hkv, lens, budget, sinks, recent):
     rng = np.random.default_rng(hkv + budget)
@@ -216,6 +217,20 @@ def test_select(kind, hkv, lens, budget, sinks, recent):
     for b, n in enumerate(lens):
         for h in range(hkv):
             np.testing.assert_array_equal(keep[b, h], select_plain(w[b, h], n, budget, sinks, recent), str((b, h)))
+
+
+@pytest.mark.parametrize("m", [1, 5, 6, 8, 9, 13, 18, 19, 24])
+def test_select_around_zero(m):
+    """5 ordinary weights, 3 denormal ones, 10 zeros of both signs and 6
+    negative ones in a shuffled row: every place the choice can end at."""
+    rng = np.random.default_rng(m)
+    row = np.array([3, 1, 2, 1, 0.5] + [1e-45, 3e-45, 1e-45] + [0.0, -0.0] * 5 + [-1e-45, -2, -1, -1, -3, -np.inf] + [-7],
+                   np.float32)
+    w = np.stack([rng.permutation(row) for _ in range(3)])[:, None]
+    n = len(row)
+    keep = pkc.evict_select(cuda(w), torch.full((3,), n, dtype=torch.int32, device="cuda"), m, 0, 0, ws_for(3, 1)).cpu().numpy()
+    for b in range(3):
+        np.testing.assert_array_equal(keep[b, 0], select_plain(w[b, 0], n, m, 0, 0))
 
 
 def test_select_of_rows_longer_than_shared_memory():

@@ -290,6 +290,19 @@ def test_decode_of_values_near_the_largest_float(hkv):
     check_decode(c, q, o, lse, g, 0.1, "bf16")
 
 
+@pytest.mark.parametrize("hkv", [1, 4])
+def test_decode_of_tiny_values(hkv):
+    """bf16 values of 2^-100 keep their bits (compared times 2^100)."""
+    rng = np.random.default_rng(13)
+    lens, g = [300, 33], 2
+    c = Cache(lens, hkv, 16, rng, v=rng.standard_normal((333, hkv, 128)) * 2.0 ** -100)
+    d, bt, dl = c.device()
+    q = torch.from_numpy(rng.standard_normal((2, hkv * g, 128))).cuda().bfloat16()
+    o, lse = pkc.paged_decode_state_mx4(q, *d, bt, dl, 0.1, ws_for(2, hkv * g))
+    c.v = [v * 2.0 ** 100 for v in c.v]
+    check_decode(c, q, o.double() * 2.0 ** 100, lse, g, 0.1, "bf16")
+
+
 def test_decode_of_large_scores_moves_the_reference():
     """Scores that rise along the cache by hundreds: earlier tokens' weights vanish."""
     rng = np.random.default_rng(8)

@@ -32,13 +32,13 @@
 // warp waits for another until the item ends and any page size and head
 // count works.  Four blocks (16 warps of 128 registers) per SM.
 //
-// Measured: 124 us for a batch of 256 with 32 / 8 heads over 476,458 tokens
+// Measured: 125 us for a batch of 256 with 32 / 8 heads over 476,458 tokens
 // (523 MB, 4.2 TB/s of a measured copy rate of 6.8); 44 us for two requests
 // of 107,000 tokens with 32 / 4 heads (117 MB), where the join, begun early,
 // takes 11 us when it runs alone.  Bound by instructions, about 350 per 16
 // tokens and head: 128 of them convert or feed the tensor cores, the rest are
-// addresses, scales, softmax.  Without the copies' bytes the kernel takes 119
-// us, without the V product 103.
+// addresses, scales, softmax.  Without the copies' bytes the kernel takes 5
+// us less, without the V product 21.
 #include <cuda_runtime.h>
 
 #include "decode_common.cuh"

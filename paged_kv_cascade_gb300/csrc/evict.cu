@@ -17,7 +17,7 @@
 // works on one row where there are few, adding up their histograms through
 // distributed shared memory.  What bounds it is instructions (about 100 per
 // 32 weights and pass, with the fixed part) and the chain of reads and
-// barriers per row, not HBM: 23 us for 512 rows of 1024 to 16384 weights (one
+// barriers per row, not HBM: 22 us for 512 rows of 1024 to 16384 weights (one
 // read of them at the copy rate would be 3), 16 us for 8 rows of 131,056 on
 // 64 blocks.
 //

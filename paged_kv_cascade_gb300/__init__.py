@@ -405,9 +405,10 @@ def _expect_current(t):
 def _expect_all(device, *specs):
     """_expect for many tensors of known dtype and shape: specs are
     (name, tensor, dtype, shape)."""
+    index = device.index
     for name, t, dtype, shape in specs:
         try:
-            if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == device:
+            if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.get_device() == index:
                 continue
         except AttributeError:
             pass  # not a tensor: _expect says so
@@ -420,15 +421,22 @@ def _sizes(t, n):
     return tuple(s) if len(s) == n else (None,) * n
 
 
+def _leading(name, t, dtypes, n, last=None):
+    """Sizes of a call's first tensor, of n dimensions and on the current
+    device; all else is left to _expect_all."""
+    s = _sizes(t, n)
+    if s[0] is None or t.dtype not in dtypes or not t.is_cuda or t.get_device() != _device():
+        _expect(name, t, dtypes, (None,) * (n - 1) + (last,))
+        _expect_current(t)
+    return s
+
+
 def _check_mx4(k_codes, k_scales, v_codes, v_scales, block_table, workspace):
     """The four pools of an mx4 cache, its table and the workspace."""
     torch = _torch or _t()
     u8 = torch.uint8
-    P, ps, Hkv, _ = _sizes(k_codes, 4)
+    P, ps, Hkv, _ = _leading("k_codes", k_codes, (u8,), 4, 64)
     B, n_pages = _sizes(block_table, 2)
-    if P is None or not k_codes.is_cuda or k_codes.get_device() != _device():
-        _expect("k_codes", k_codes, (u8,), (None, None, None, 64))
-        _expect_current(k_codes)
     dev = k_codes.device
     _expect_all(dev, ("k_codes", k_codes, u8, (P, ps, Hkv, 64)), ("k_scales", k_scales, u8, (P, ps, Hkv, 4)),
                 ("v_codes", v_codes, u8, (P, ps, Hkv, 64)), ("v_scales", v_scales, u8, (P, ps, Hkv, 4)),
@@ -475,7 +483,7 @@ def gather_kv_mx4(k_codes, k_scales, v_codes, v_scales, block_table, first, out_
         if t is not None:
             _expect(name, t, (dtype,), (total, Hkv, 128), dev)
     k = torch.empty((total, Hkv, 128), dtype=dtype, device=dev) if k is None else k
-    v = torch.empty((total, Hkv, 128), dtype=dtype, device=dev) if v is None else v
+    v = torch.empty_like(k) if v is None else v
     _check(lib().pkc_gather_kv_mx4(
         _ptr(k_codes), _ptr(k_scales), _ptr(v_codes), _ptr(v_scales), _ptr(block_table),
         block_table.shape[1], _ptr(first), _ptr(out_indptr), total, B, Hkv, 128, ps, P, _ptr(k),
@@ -528,16 +536,14 @@ def accumulate_weights(q, lse, k_cache, block_table, cache_seqlens, sm_scale, we
     16-bit of q's dtype, e4m3 codes (fp16 q, k_scale), or mx4 codes with
     k_scales."""
     torch = _torch or _t()
-    _expect("k_cache", k_cache, (torch.float16, torch.bfloat16, torch.uint8), (None, None, None, None))
-    _expect_current(k_cache)
+    P, ps, Hkv, _ = _leading("k_cache", k_cache, (torch.float16, torch.bfloat16, torch.uint8), 4)
     kind, row = _kv_kind(k_cache, k_scales)
-    P, ps, Hkv, _ = k_cache.shape
     dev = k_cache.device
-    _expect("k_cache", k_cache, (torch.uint8,) if k_scales is not None else (k_cache.dtype,),
-            (P, ps, Hkv, row), dev)
+    kv_dtype = torch.uint8 if k_scales is not None else k_cache.dtype
     B, Hq, _ = _sizes(q, 3)
     _expect("q", q, (torch.float16, torch.bfloat16), (B, Hq, 128), dev)
-    _expect_all(dev, ("lse", lse, torch.float32, (B, Hq)),
+    _expect_all(dev, ("k_cache", k_cache, kv_dtype, (P, ps, Hkv, row)),
+                ("lse", lse, torch.float32, (B, Hq)),
                 ("block_table", block_table, torch.int32, (B, _sizes(block_table, 2)[1])),
                 ("cache_seqlens", cache_seqlens, torch.int32, (B,)),
                 ("weights", weights, torch.float32, (B, Hkv, _sizes(weights, 3)[2])),
@@ -558,15 +564,14 @@ def evict_select(weights, cache_seqlens, budget, sinks, recent, workspace, keep=
     weights [B, Hkv, W] between them (all, then -1, of a request within the
     budget)."""
     torch = _torch or _t()
-    _expect("weights", weights, (torch.float32,), (None, None, None))
-    _expect_current(weights)
-    B, Hkv, W = weights.shape
+    B, Hkv, W = _leading("weights", weights, (torch.float32,), 3)
     dev = weights.device
     budget, sinks, recent = int(budget), int(sinks), int(recent)
     if budget < 1 or sinks < 0 or recent < 0 or sinks + recent > budget:
         raise ValueError("evict_select: budget must be >= 1, sinks and recent >= 0 and together at most the "
                          f"budget (got {budget}, {sinks}, {recent})")
-    _expect_all(dev, ("cache_seqlens", cache_seqlens, torch.int32, (B,)),
+    _expect_all(dev, ("weights", weights, torch.float32, (B, Hkv, W)),
+                ("cache_seqlens", cache_seqlens, torch.int32, (B,)),
                 ("workspace", workspace, torch.uint8, _sizes(workspace, 1)))
     if keep is not None:
         _expect("keep", keep, (torch.int32,), (B, Hkv, budget), dev)
@@ -583,12 +588,10 @@ def evict_compact(keep, k_cache, v_cache, block_table, cache_seqlens, workspace,
     e4m3 codes, or mx4 codes with their scales) and, given, the accumulated
     weights [B, Hkv, W]."""
     torch = _torch or _t()
-    _expect("k_cache", k_cache, (torch.float16, torch.bfloat16, torch.uint8), (None, None, None, None))
-    _expect_current(k_cache)
+    P, ps, Hkv, _ = _leading("k_cache", k_cache, (torch.float16, torch.bfloat16, torch.uint8), 4)
     if (k_scales is None) != (v_scales is None):
         raise ValueError("evict_compact: k_scales and v_scales are given together")
     kind, row = _kv_kind(k_cache, k_scales)
-    P, ps, Hkv, _ = k_cache.shape
     dev = k_cache.device
     kv_dtype = torch.uint8 if k_scales is not None else k_cache.dtype
     B, _, budget = _sizes(keep, 3)

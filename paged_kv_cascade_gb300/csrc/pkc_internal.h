@@ -305,7 +305,7 @@ struct CompactParams {
   int32_t* cache_seqlens;
   int64_t bt_stride, num_pages, w_stride;
   int batch, hkv, budget, row_bytes, page_size, page_shift;
-  int slices, parts;         // set by the launcher: slices of a row, blocks per (request, head)
+  int slices, parts, cluster;  // set by the launcher: slices of a row, parts per (request, head), blocks per part
   int32_t* status;
 };
 

@@ -293,6 +293,7 @@ def compact_plain(c, pools, keep, lens, w):
     (2, 64, [5000], 1),
     (2, 1, [130], 129),
     (1, 24, [3000], 2999),
+    (2, 16, [30000, 9001], 8500),
 ])
 def test_compact_moves_the_kept_rows_and_nothing_else(kind, hkv, ps, lens, budget):
     rng = np.random.default_rng(hkv + budget)

@@ -30,7 +30,9 @@
 // HBM: a kept row is read once and written once, 256 bytes at a random slot:
 // 100 us for 64 requests cut to 1024 of up to 6144 tokens, 8 heads of bf16
 // (549 MB, 5.5 TB/s of a measured copy rate of 6.8).  With the chunks in
-// registers, of half the size, it took 120 us.
+// registers, of half the size, it took 120 us.  Where there are few rows, a
+// cluster works on each: its chunk is the blocks' chunks together, and its
+// barrier keeps a chunk's stores behind all of its reads.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 

@@ -511,7 +511,7 @@ int pkc_cascade_decode_paged_prefix(
  *   codes  [num_pages, page_size, num_kv_heads, 64] bytes, 16-byte aligned
  *   scales [num_pages, page_size, num_kv_heads, 4] bytes, 4-byte aligned
  * Block b of a row is elements 32 b .. 32 b + 31 and has scale byte s_b:
- * 2^(s_b - 127), 255 stands for NaN and comes with zero codes.  Element
+ * 2^(s_b - 127), 0 .. 254, or NaN whatever the codes, 255.  Element
  * 32 b + 4 u + i is nibble i (lowest first) of the 16-bit little-endian word
  * 4 u + b of the row's codes; a nibble is sign, two exponent bits, one
  * mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives.

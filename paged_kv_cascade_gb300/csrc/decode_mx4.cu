@@ -263,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     const int whole_lo = (it.kb & 15) && cls == 0 ? 1 : 0;
     const int whole_hi = mine - ((it.ke & 15) && tile0 + (mine - 1) * wph == (it.ke >> 4) ? 1 : 0);
     const uint32_t n_whole = (uint32_t)max(whole_hi - whole_lo, 0);
+    const uint32_t byte_sel = (uint32_t)(tg | (4 + tg) << 4);  // byte tg of two words
     uint32_t st = ring;
     for (int j = 0; j < mine; ++j) {
       cp_async_wait<kStages - 2>();
@@ -274,9 +275,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       {
         const uint32_t at = v_sc + 4 * token_of(2 * g);
         const uint32_t ya = lds32(at - kScales), yc = lds32(at - kScales + 16);
-        // (255: an infinity, NaN on the zero codes it comes with)
-        sts32(kbuf + 16 * token_of(2 * g) + 4 * tg, ((ya >> (8 * tg)) << 23) & 0x7f800000u);
-        sts32(kbuf + 16 * token_of(2 * g) + 64 + 4 * tg, ((yc >> (8 * tg)) << 23) & 0x7f800000u);
+        const uint32_t y2 = mx4_scale_pair(prmt(ya, yc, byte_sel));
+        sts32(kbuf + 16 * token_of(2 * g) + 4 * tg, y2 << 16);
+        sts32(kbuf + 16 * token_of(2 * g) + 64 + 4 * tg, y2 & 0xffff0000u);
         const uint32_t wa = lds32(at), wc = lds32(at + 16);
         const int ea = (int)((wa >> (8 * tg)) & 255u), ec = (int)((wc >> (8 * tg)) & 255u);
         int top = max(ea, ec);

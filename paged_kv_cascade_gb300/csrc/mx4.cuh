@@ -46,6 +46,14 @@ __device__ __forceinline__ float mx4_scale(uint32_t s) {
   return __uint_as_float(s == 255u ? 0x7fffffffu : s == 0u ? 0x00400000u : s << 23);
 }
 
+// The same of two scale bytes (the low 16 bits) as a bf16 pair, exactly: bf16
+// has denormals down to 2^-133.
+__device__ __forceinline__ uint32_t mx4_scale_pair(uint32_t two) {
+  uint32_t d;
+  asm("{\n.reg .b16 l, h;\nmov.b32 {l, h}, %1;\ncvt.rn.bf16x2.ue8m0x2 %0, l;\n}" : "=r"(d) : "r"(two));
+  return d;
+}
+
 // Quotient and remainder by the page size (shift >= 0: a power of two).
 struct PageDiv {
   int size, shift;

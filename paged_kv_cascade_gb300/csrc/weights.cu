@@ -233,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, 4) weights_kernel(const WeightsParam
           e2m1x8(half ? ka.w : ka.z, a1);
           e2m1x8(half ? kb.y : kb.x, c0);
           e2m1x8(half ? kb.w : kb.z, c1);
+          const uint32_t s2a = mx4_scale_pair(half ? sa >> 16 : sa), s2b = mx4_scale_pair(half ? sb >> 16 : sb);
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
             const int blk = 2 * half + v;
@@ -241,8 +242,8 @@ __global__ void __launch_bounds__(kThreads, 4) weights_kernel(const WeightsParam
             const uint32_t f1[4] = {a1[2 * v], c1[2 * v], a1[2 * v + 1], c1[2 * v + 1]};
             mma16816<__half>(part, f0, qf[blk][0], qf[blk][1]);
             mma16816<__half>(part, f1, qf[blk][2], qf[blk][3]);
-            const float fa = __uint_as_float((blk < 3 ? sa << (23 - 8 * blk) : sa >> 1) & 0x7f800000u);
-            const float fb = __uint_as_float((blk < 3 ? sb << (23 - 8 * blk) : sb >> 1) & 0x7f800000u);
+            const float fa = __uint_as_float(v ? s2a & 0xffff0000u : s2a << 16);
+            const float fb = __uint_as_float(v ? s2b & 0xffff0000u : s2b << 16);
             acc[0] = fmaf(part[0], fa, acc[0]);
             acc[1] = fmaf(part[1], fa, acc[1]);
             acc[2] = fmaf(part[2], fb, acc[2]);

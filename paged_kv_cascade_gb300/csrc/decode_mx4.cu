@@ -12,7 +12,7 @@
 // the codes converted exactly, two per instruction.  The scales differ by
 // token and block, so the four blocks have an accumulator each and
 //   s = sum_b 2^(s_b - 127) acc_b
-// is formed in float32.
+// is formed in float32 (of bf16 queries times 2^-22, see load_q_f16).
 //
 // Values.  O^T = V^T P^T, the dims on the tile's 16 rows.  The dims are 4
 // blocks whose scales differ by token, so the scale goes on the
@@ -96,6 +96,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
   // With at most 4 query heads per KV head the tile's other 4 columns take
   // the probabilities' remainders, at no cost.
   constexpr bool kFold = G <= 4;
+  constexpr bool kBf16 = std::is_same_v<T, __nv_bfloat16>;
   const DecodeParams& p = mp.d;
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -178,9 +179,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     uint32_t win = kAligned ? load_window(0) : load_tokens(0);
     uint32_t win_next = kAligned ? load_window(32) : 0u;
 
-    uint32_t qf[4][4];
+    uint32_t qf[4][4], key_mul;
     const float q_undo = load_q_f16<T, G, kFold>(
-        static_cast<const T*>(p.q) + ((int64_t)it.req * p.hq + (int64_t)kvh * G) * D, lane, qf);
+        static_cast<const T*>(p.q) + ((int64_t)it.req * p.hq + (int64_t)kvh * G) * D, lane, qf, key_mul);
     // factors of this lane's score columns (heads 2 tg, 2 tg + 1), base 2
     const float sc0 = p.scale_log2 * __shfl_sync(0xffffffffu, q_undo, 8 * tg);
     const float sc1 = p.scale_log2 * __shfl_sync(0xffffffffu, q_undo, 8 * tg + 4);
@@ -275,7 +276,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       {
         const uint32_t at = v_sc + 4 * token_of(2 * g);
         const uint32_t ya = lds32(at - kScales), yc = lds32(at - kScales + 16);
-        const uint32_t y2 = mx4_scale_pair(prmt(ya, yc, byte_sel));
+        uint32_t y2 = mx4_scale_pair(prmt(ya, yc, byte_sel));
+        if constexpr (kBf16) y2 = bmul2(y2, key_mul);
         sts32(kbuf + 16 * token_of(2 * g) + 4 * tg, y2 << 16);
         sts32(kbuf + 16 * token_of(2 * g) + 64 + 4 * tg, y2 & 0xffff0000u);
         const uint32_t wa = lds32(at), wc = lds32(at + 16);

@@ -54,6 +54,13 @@ __device__ __forceinline__ uint32_t mx4_scale_pair(uint32_t two) {
   return d;
 }
 
+// a * b, element by element, of bf16 pairs (denormals included).
+__device__ __forceinline__ uint32_t bmul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
 // Quotient and remainder by the page size (shift >= 0: a power of two).
 struct PageDiv {
   int size, shift;
@@ -127,15 +134,27 @@ __device__ __forceinline__ void mma16816_f16_new(float (&d)[4], const uint32_t (
 }
 
 // Query fragments (B operand of m16n8k16, n = query head lane / 4) for
-// products with 4-bit or 8-bit keys, whose fragments are fp16: qf[b][k] are
-// elements 32 b + 8 (lane % 4) + 2 k, + 1 of head lane / 4 (zero for heads
-// >= G; kRepeat, G <= 4: heads 4 .. 7 repeat 0 .. 3).  fp16 queries are used as they are.  A bf16 row is scaled by the
-// power of two that brings its largest magnitude into [2^14, 2^15): then
-// every element down to 2^-22 of the largest is exact in fp16, and the
-// others are off by at most 2^-39 of it, far below the float32 sums'
-// rounding.  Returns the factor that undoes the scaling.
+// products with 4-bit keys, whose fragments are fp16: qf[b][k] are elements
+// 32 b + 8 (lane % 4) + 2 k, + 1 of head lane / 4 (zero for heads >= G;
+// kRepeat, G <= 4: heads 4 .. 7 repeat 0 .. 3).  fp16 queries are used as
+// they are.  A bf16 row is scaled by the power of two that brings its largest
+// magnitude into [2^14, 2^15): then every element down to 2^-22 of the
+// largest is exact in fp16, and the others are off by at most 2^-39 of it, far
+// below the float32 sums' rounding.
+//
+// Its products with codes are below 2^15 * 192 per block, so a sum over the
+// blocks under their scales (2^125 at most for finite keys) could pass
+// float32's range although q.k does not.  The key scales are therefore first
+// multiplied by key_mul (a bf16 pair): 2^-22 keeps every such sum below
+// 2^127.6.  It also drops scales below 2^-111; those count for less than 2^-37
+// in a score as long as |q| < 2^64.  A warp with a larger query leaves the
+// scales whole (1): keys that overflow the sum then give that query scores
+// beyond float32 as well.
+//
+// Returns the factor that undoes both.
 template <typename T, int G, bool kRepeat = false>
-__device__ __forceinline__ float load_q_f16(const T* qrow0, int lane, uint32_t (&qf)[4][4]) {
+__device__ __forceinline__ float load_q_f16(const T* qrow0, int lane, uint32_t (&qf)[4][4],
+                                            uint32_t& key_mul) {
   const int g = kRepeat ? (lane >> 2) & 3 : lane >> 2, tg = lane & 3;
   const T* row = qrow0 + (g < G ? g : 0) * PKC_HEAD_DIM;
 #pragma unroll
@@ -146,6 +165,7 @@ __device__ __forceinline__ float load_q_f16(const T* qrow0, int lane, uint32_t (
     qf[b][2] = g < G ? u.z : 0u;
     qf[b][3] = g < G ? u.w : 0u;
   }
+  key_mul = 0x3f803f80u;  // (1; not used with fp16 queries)
   if constexpr (std::is_same_v<T, __half>) {
     return 1.f;
   } else {
@@ -159,6 +179,11 @@ __device__ __forceinline__ float load_q_f16(const T* qrow0, int lane, uint32_t (
     const int e = (int)(top >> 7);  // biased exponent; 255: not finite, 0: zero or denormal
     const int shift = e == 255 || top == 0u ? 0 : min(14 - (e - 127), 126);
     const float mul = __int_as_float((127 + shift) << 23);
+    uint32_t all = top;
+#pragma unroll
+    for (int x = 4; x < 32; x <<= 1) all = max(all, __shfl_xor_sync(0xffffffffu, all, x));
+    const int bias = all < (127u + 64u) << 7 ? 22 : 0;
+    if (bias) key_mul = 0x34803480u;  // 2^-22
 #pragma unroll
     for (int b = 0; b < 4; ++b)
 #pragma unroll
@@ -166,7 +191,7 @@ __device__ __forceinline__ float load_q_f16(const T* qrow0, int lane, uint32_t (
         const float2 f = Elem<__nv_bfloat16>::to_f2(qf[b][k]);
         qf[b][k] = Elem<__half>::from_f2(f.x * mul, f.y * mul);
       }
-    return __int_as_float((127 - shift) << 23);
+    return __int_as_float((127 - shift + bias) << 23);
   }
 }
 

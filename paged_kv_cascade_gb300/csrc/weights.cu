@@ -167,8 +167,9 @@ __global__ void __launch_bounds__(kThreads, 4) weights_kernel(const WeightsParam
   const T* q0 = static_cast<const T*>(p.q) + ((int64_t)b * p.hkv + kvh) * G * D;
   uint32_t qf[4][4];
   float undo = 1.f;
+  uint32_t key_mul = 0;
   if constexpr (KV == PKC_MX4) {
-    undo = load_q_f16<T, G>(q0, lane, qf);
+    undo = load_q_f16<T, G>(q0, lane, qf, key_mul);
   } else {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
@@ -233,7 +234,11 @@ __global__ void __launch_bounds__(kThreads, 4) weights_kernel(const WeightsParam
           e2m1x8(half ? ka.w : ka.z, a1);
           e2m1x8(half ? kb.y : kb.x, c0);
           e2m1x8(half ? kb.w : kb.z, c1);
-          const uint32_t s2a = mx4_scale_pair(half ? sa >> 16 : sa), s2b = mx4_scale_pair(half ? sb >> 16 : sb);
+          uint32_t s2a = mx4_scale_pair(half ? sa >> 16 : sa), s2b = mx4_scale_pair(half ? sb >> 16 : sb);
+          if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+            s2a = bmul2(s2a, key_mul);
+            s2b = bmul2(s2b, key_mul);
+          }
 #pragma unroll
           for (int v = 0; v < 2; ++v) {
             const int blk = 2 * half + v;

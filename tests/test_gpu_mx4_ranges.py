@@ -79,3 +79,67 @@ def test_scale_byte_255_is_nan_whatever_the_codes(ps, dtype):
     want_w = np.zeros((3, 1, 48), bool)
     want_w[0, 0, 7] = True
     np.testing.assert_array_equal(np.isnan(f64(w)), want_w)
+
+
+# ---------------------------------------------------------------------------
+# bf16 queries and keys whose sizes are far from 1 and cancel in the scores
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("g", [2, 8])
+@pytest.mark.parametrize("power", [-120, -112, -108, -70, -50, 50, 63, 64, 65, 66, 108, 112, 118])
+def test_decode_where_queries_and_keys_cancel(power, g):
+    """|q| about 2^power, |k| about 2^-power: ordinary scores."""
+    rng = np.random.default_rng(200 + power)
+    c = Cache([50, 17], 1, 16, rng, k=rng.standard_normal((67, 1, 128)) * 2.0 ** -power)
+    d, bt, dl = c.device()
+    q = torch.from_numpy(rng.standard_normal((2, g, 128)) * 2.0 ** power).cuda().to(torch.bfloat16)
+    ws = ws_for(2, g)
+    o, lse = pkc.paged_decode_state_mx4(q, *d, bt, dl, 0.1, ws)
+    check_decode(c, q, o, lse, g, 0.1, "bf16")
+    # the weights of the same step: 1 in all per query head
+    w = torch.zeros(2, 1, 64, device="cuda")
+    pkc.accumulate_weights(q, lse, d[0], bt, dl, 0.1, w, ws, k_scales=d[1])
+    want_w_of_decode(c, q, lse, w, g, 0.1)
+
+
+def test_decode_of_equal_tiny_queries_and_huge_keys():
+    """|q| = 2^-108, |k| = 2^108 throughout: q.k is 128 or -128."""
+    rng = np.random.default_rng(1)
+    n = 40
+    k = np.where(rng.random((n, 1, 1)) < 0.5, -1.0, 1.0) * np.full((n, 1, 128), 2.0 ** 108)
+    c = Cache([n], 1, 16, rng, k=k)
+    d, bt, dl = c.device()
+    q = torch.full((1, 4, 128), 2.0 ** -108, device="cuda", dtype=torch.bfloat16)
+    o, lse = pkc.paged_decode_state_mx4(q, *d, bt, dl, 0.02, ws_for(1, 4))
+    check_decode(c, q, o, lse, 4, 0.02, "bf16")
+
+
+@pytest.mark.parametrize("g", [4, 8])
+def test_decode_of_scores_that_are_large_and_finite(g):
+    """|q| about 1, |k| = 2^108: q.k of 4e34 is a float32 number; one token has
+    the largest score by far and is the result."""
+    rng = np.random.default_rng(2)
+    n, top = 37, 21
+    k = np.full((n, 1, 128), 2.0 ** 108)
+    k[:, :, ::2] *= -1
+    k[top, 0] = 2.0 ** 110
+    c = Cache([n], 1, 16, rng, k=k)
+    d, bt, dl = c.device()
+    q = torch.ones(1, g, 128, device="cuda", dtype=torch.bfloat16)
+    o, lse = pkc.paged_decode_state_mx4(q, *d, bt, dl, 1.0, ws_for(1, g))
+    # the top token's weight is 1 and the others' 0: its values, rounded once
+    want = torch.from_numpy(c.v[0][top]).to(torch.bfloat16)
+    assert torch.equal(o[0].cpu(), want.expand(g, 128))
+    # a float32 sum of 128 products, one rounding to base 2 and one back
+    np.testing.assert_allclose(f64(lse), 128 * 2.0 ** 110, rtol=140 * 2.0 ** -24)
+
+
+def test_heads_of_one_group_with_queries_of_very_different_sizes():
+    rng = np.random.default_rng(3)
+    g = 4
+    c = Cache([100], 1, 16, rng, k=rng.standard_normal((100, 1, 128)) * 2.0 ** -40)
+    d, bt, dl = c.device()
+    size = np.array([2.0 ** 40, 2.0 ** -120, 2.0 ** 44, 2.0 ** 0])[None, :, None]
+    q = torch.from_numpy(rng.standard_normal((1, g, 128)) * size).cuda().to(torch.bfloat16)
+    o, lse = pkc.paged_decode_state_mx4(q, *d, bt, dl, 0.05, ws_for(1, g))
+    check_decode(c, q, o, lse, g, 0.05, "bf16")

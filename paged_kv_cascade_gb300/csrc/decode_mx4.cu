@@ -19,9 +19,11 @@
 // probabilities, one power of two per token and block:
 //   O_b += (p 2^(e_b - E_b)) c_b
 // with E_b the largest scale byte seen so far in block b (O_b is rescaled
-// when it grows).  Probabilities are held times 2^11, at most 2^15 (the
-// softmax reference moves when a score exceeds it by more than 4), as an
-// fp16 high part and an fp16 remainder, one product each; the products with
+// when it grows).  Probabilities are 2^(s - r) with the reference r 11 below
+// the largest score when it was set, rounded up, and at most 2^15 (r moves
+// when a score exceeds it by more than 15; both hold for scores of any size,
+// also where s - 11 is no float32 number).  They enter as an fp16 high part
+// and an fp16 remainder, one product each; the products with
 // the power of two are exact down to 2^-24.  So a probability enters with 22
 // bits, and what is lost is below 2^-24 of the largest cached |V| of the
 // block of dims.
@@ -59,8 +61,8 @@ constexpr int kStage = 2 * (kCodes + kScales);
 constexpr int kRing = kStages * kStage;       // per warp
 constexpr int kWarpSmem = kRing + 128 + 256;  // + the tile's probability factors and key scales
 constexpr float kRefFloor = -3e38f;           // softmax reference before the first token
-constexpr float kLazy = 4.f;                  // log2 of the largest probability between rescales
-constexpr float kLift = 11.f;                 // probabilities are held times 2^kLift: at most 2^15
+constexpr float kLift = 11.f;                 // a new reference is this far below the largest score
+constexpr float kMost = kLift + 4.f;          // log2 of the largest probability between rescales
 
 struct Item {
   int valid, req, kb, ke, slot, hg;
@@ -191,7 +193,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
     for (int b = 0; b < 4; ++b)
 #pragma unroll
       for (int x = 0; x < 2; ++x) o[b][x][0] = o[b][x][1] = o[b][x][2] = o[b][x][3] = 0.f;
-    float m0 = kRefFloor, m1 = kRefFloor, l0 = 0.f, l1 = 0.f;  // l: times 2^kLift
+    float r0 = kRefFloor, r1 = kRefFloor, l0 = 0.f, l1 = 0.f;  // softmax references and sums
     int e_ref = 0;                                             // E_b of block lane % 4
 
     // Per lane, the pools at this head's bytes of token 0 and (aligned) the
@@ -352,16 +354,16 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       }
       // ---- online softmax, base 2, lazy reference ----
       float t0 = fmaxf(s[0], s[2]), t1 = fmaxf(s[1], s[3]);
-      if (__any_sync(0xffffffffu, t0 > m0 + kLazy || t1 > m1 + kLazy)) {
+      if (__any_sync(0xffffffffu, t0 - r0 > kMost || t1 - r1 > kMost)) {
 #pragma unroll
         for (int x = 4; x < 32; x <<= 1) {
           t0 = fmaxf(t0, __shfl_xor_sync(0xffffffffu, t0, x));
           t1 = fmaxf(t1, __shfl_xor_sync(0xffffffffu, t1, x));
         }
-        const float n0 = fmaxf(t0, m0), n1 = fmaxf(t1, m1);
-        const float c0 = ex2(m0 - n0), c1 = ex2(m1 - n1);
-        m0 = n0;
-        m1 = n1;
+        const float n0 = fmaxf(__fadd_ru(t0, -kLift), r0), n1 = fmaxf(__fadd_ru(t1, -kLift), r1);
+        const float c0 = ex2(r0 - n0), c1 = ex2(r1 - n1);
+        r0 = n0;
+        r1 = n1;
         l0 *= c0;
         l1 *= c1;
 #pragma unroll
@@ -371,8 +373,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
             o[b][x][0] *= c0; o[b][x][1] *= c1; o[b][x][2] *= c0; o[b][x][3] *= c1;
           }
       }
-      const float p0 = ex2(s[0] - (m0 - kLift)), p1 = ex2(s[1] - (m1 - kLift));
-      const float p2 = ex2(s[2] - (m0 - kLift)), p3 = ex2(s[3] - (m1 - kLift));
+      const float p0 = ex2(s[0] - r0), p1 = ex2(s[1] - r1), p2 = ex2(s[2] - r0), p3 = ex2(s[3] - r1);
       l0 += p0 + p2;
       l1 += p1 + p3;
       // high part and remainder, transposed into B fragments (tokens x heads)
@@ -448,15 +449,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         *reinterpret_cast<uint2*>(dst) = make_uint2(Elem<T>::from_f2(v.x, v.y), Elem<T>::from_f2(v.z, v.w));
       }
     };
-    auto write_lse = [&](int hq, float mm, float ll) {
-      const float lse = ll == 0.f ? neg_inf() : (mm - kLift + lg2(ll)) * kLn2;
+    auto write_lse = [&](int hq, float r, float ll) {
+      const float lse = ll == 0.f ? neg_inf() : (r + lg2(ll)) * kLn2;
       if (it.slot >= 0) p.part_lse[(int64_t)it.slot * p.hq + hq] = lse;
       else p.lse_direct[(int64_t)it.req * p.hq + hq] = lse;
     };
 #pragma unroll
     for (int e = 0; e < 2; ++e) {  // heads 2 tg, 2 tg + 1: dims 32 b + 4 g .. + 3
       const int hd = 2 * tg + e;
-      const float m = e ? m1 : m0, l = e ? l1 : l0;
+      const float r = e ? r1 : r0, l = e ? l1 : l0;
       // Unnormalised values go to the merge times 2^-32: sums are at most 2^15
       // per token, so values near float32's largest stay finite (and those
       // below 2^-101 lose bits, below 2^-117 some of bf16's).
@@ -472,9 +473,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       }
       if (hd < G && g == 0) {
         if (wph == 1) {
-          write_lse(kvh * G + hd, m, l);
+          write_lse(kvh * G + hd, r, l);
         } else {
-          merge[(warp * G + hd) * kMergeRow + D] = m;
+          merge[(warp * G + hd) * kMergeRow + D] = r;
           merge[(warp * G + hd) * kMergeRow + D + 1] = l;
         }
       }
@@ -485,12 +486,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       // warp per (KV head, query head) row, 4 dims per lane.
       for (int r = warp; r < HG * G; r += kWarps) {
         const int h = r / G, hd = r - h * G;
-        float mm = kRefFloor, ll = 0.f;
+        float ref = kRefFloor, ll = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = 0; c < wph; ++c) mm = fmaxf(mm, merge[((h + HG * c) * G + hd) * kMergeRow + D]);
+        for (int c = 0; c < wph; ++c) ref = fmaxf(ref, merge[((h + HG * c) * G + hd) * kMergeRow + D]);
         for (int c = 0; c < wph; ++c) {
           const float* src = merge + ((h + HG * c) * G + hd) * kMergeRow;
-          const float w = ex2(src[D] - mm);
+          const float w = ex2(src[D] - ref);
           ll = fmaf(src[D + 1], w, ll);
           const float4 v = *reinterpret_cast<const float4*>(src + 4 * lane);
           acc.x = fmaf(v.x, w, acc.x); acc.y = fmaf(v.y, w, acc.y);
@@ -500,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
         const int hq = (it.hg * HG + h) * G + hd;
         write4(hq, 4 * lane, acc);
-        if (lane == 0) write_lse(hq, mm, ll);
+        if (lane == 0) write_lse(hq, ref, ll);
       }
       __syncthreads();  // the merge buffer is free
     }

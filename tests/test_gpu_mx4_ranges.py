@@ -143,3 +143,52 @@ def test_heads_of_one_group_with_queries_of_very_different_sizes():
     q = torch.from_numpy(rng.standard_normal((1, g, 128)) * size).cuda().to(torch.bfloat16)
     o, lse = pkc.paged_decode_state_mx4(q, *d, bt, dl, 0.05, ws_for(1, g))
     check_decode(c, q, o, lse, g, 0.05, "bf16")
+
+
+# ---------------------------------------------------------------------------
+# Scores past 2^24, where a float32 no longer holds every whole number
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("g", [1, 8])
+@pytest.mark.parametrize("exp", [10, 18, 19, 20, 21, 22, 24])
+def test_decode_of_scores_beyond_whole_float32_numbers(exp, g, sign):
+    """Base-2 scores of +- 96 2^exp plus 0, 2, 4, 8, 16 or 32, as far as the type
+    tells them apart: every score, difference and probability is exact.
+
+    sm_scale is the float32 ln 2, whose product with the float32 log2 e is 1, so
+    q.k is the score in base 2.  Blocks 0 .. 2 make the large part (q 2^(exp / 2),
+    k the rest), block 3 one element the small one.
+    """
+    rng = np.random.default_rng(exp)
+    sm = np.float32(np.log(2.0))
+    assert sm * np.float32(1.4426950408889634) == 1
+    spacing = np.spacing(np.float32(96 * 2.0 ** exp))
+    steps = [float(x) for x in (2, 4, 8, 16, 32) if x % spacing == 0] or [0.0]
+    lens, offsets = [], []
+    for first in (0.0, *steps):  # (of a head's four warps each has 16 tokens of 64)
+        for second in (0.0, *steps):
+            offsets.append(np.concatenate([np.full(64, first), np.full(64, second), [0.0], rng.choice([0.0, *steps], 70)]))
+            lens.append(len(offsets[-1]))
+    n = sum(lens)
+    small = np.concatenate(offsets)
+    k = np.zeros((n, 1, 128))
+    k[:, 0, :96] = sign * 2.0 ** (exp - exp // 2)
+    k[:, 0, 96] = small
+    c = Cache(lens, 1, 16, rng, k=k)
+    d, bt, dl = c.device()
+    q = torch.zeros(len(lens), g, 128, device="cuda", dtype=torch.float16)
+    q[:, :, :96], q[:, :, 96] = 2.0 ** (exp // 2), 1.0
+    o, lse = pkc.paged_decode_state_mx4(q, *d, bt, dl, float(sm), ws_for(len(lens), g))
+    o, lse = f64(o), f64(lse)
+    for b, off in enumerate(offsets):
+        p = np.exp2(off - off.max())
+        want = (p / p.sum()) @ c.v[b][:, 0]
+        vmax = np.repeat(np.abs(c.v[b][:, 0]).reshape(-1, 4, 32).max((0, 2)), 32)
+        # the exponential and the two-part probabilities (2 2^-20), the sums (2^-18), one rounding to fp16
+        tol = (2.0 ** -19 + 2.0 ** -18) * vmax + np.abs(want) * 2.0 ** -11 + 2.0 ** -25
+        for h in range(g):
+            assert np.all(np.abs(o[b, h] - want) <= tol), (b, h, o[b, h], want)
+        want_l = (sign * 96 * 2.0 ** exp + off.max() + np.log2(p.sum())) * np.log(2.0)
+        # the score and the logarithm are added, then taken to base e: three roundings, and ln 2's own
+        assert np.all(np.abs(lse[b] - want_l) <= abs(want_l) * 2.0 ** -22 + 2.0 ** -18), (b, lse[b], want_l)

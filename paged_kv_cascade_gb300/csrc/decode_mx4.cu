@@ -69,8 +69,8 @@ struct Item {
 };
 
 // Shared memory: the warps' rings, the item, then the merge buffer (warps
-// that share a KV head): per warp and head 128 values, the reference and the
-// sum.
+// that share a KV head): per warp and head 128 values without the blocks'
+// scales, the reference, the sum and the four scale bytes.
 constexpr int kMergeRow = D + 4;
 template <int G> constexpr int smem_bytes() { return kWarps * kWarpSmem + 64 + kWarps * G * kMergeRow * 4; }
 
@@ -454,18 +454,23 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
       if (it.slot >= 0) p.part_lse[(int64_t)it.slot * p.hq + hq] = lse;
       else p.lse_direct[(int64_t)it.req * p.hq + hq] = lse;
     };
+    uint32_t e4 = (uint32_t)e_ref << (8 * tg);  // the scale bytes E_0 .. E_3
+    e4 |= __shfl_xor_sync(0xffffffffu, e4, 1);
+    e4 |= __shfl_xor_sync(0xffffffffu, e4, 2);
 #pragma unroll
     for (int e = 0; e < 2; ++e) {  // heads 2 tg, 2 tg + 1: dims 32 b + 4 g .. + 3
       const int hd = 2 * tg + e;
       const float r = e ? r1 : r0, l = e ? l1 : l0;
-      // Unnormalised values go to the merge times 2^-32: sums are at most 2^15
-      // per token, so values near float32's largest stay finite (and those
-      // below 2^-101 lose bits, below 2^-117 some of bf16's).
-      const float inv = wph > 1 ? 0x1p-32f : l == 0.f ? 0.f : 1.f / l;  // (a NaN sum gives NaN)
+      // The scale comes last: a value is a mean of codes times a power of two,
+      // which neither overflows nor loses bits where the result does not.
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // (a NaN sum gives NaN)
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        const float f = mx4_scale((uint32_t)__shfl_sync(0xffffffffu, e_ref, b)) * inv;
-        const float4 v = make_float4(o[b][0][e] * f, o[b][0][2 + e] * f, o[b][1][e] * f, o[b][1][2 + e] * f);
+        float4 v = make_float4(o[b][0][e], o[b][0][2 + e], o[b][1][e], o[b][1][2 + e]);
+        if (wph == 1) {
+          const float f = mx4_scale((e4 >> (8 * b)) & 255u);
+          v = make_float4(v.x * inv * f, v.y * inv * f, v.z * inv * f, v.w * inv * f);
+        }
         if (hd < G) {
           if (wph == 1) write4(kvh * G + hd, 32 * b + 4 * g, v);
           else *reinterpret_cast<float4*>(merge + (warp * G + hd) * kMergeRow + 32 * b + 4 * g) = v;
@@ -477,28 +482,36 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
         } else {
           merge[(warp * G + hd) * kMergeRow + D] = r;
           merge[(warp * G + hd) * kMergeRow + D + 1] = l;
+          merge[(warp * G + hd) * kMergeRow + D + 2] = __uint_as_float(e4);
         }
       }
     }
     __syncthreads();  // the next item is there; the warps' states are written
     if (wph > 1) {
-      // Warps of one head: unnormalised values, reference and sum, merged by a
-      // warp per (KV head, query head) row, 4 dims per lane.
+      // Warps of one head: values, reference, sum and scale bytes, merged by a
+      // warp per (KV head, query head) row, 4 dims (of block lane / 8) per lane.
       for (int r = warp; r < HG * G; r += kWarps) {
         const int h = r / G, hd = r - h * G;
         float ref = kRefFloor, ll = 0.f;
+        int top = 0;  // the largest scale byte
+        const auto scale_byte = [&](const float* src) { return (int)((__float_as_uint(src[D + 2]) >> (lane & 24)) & 255u); };
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = 0; c < wph; ++c) ref = fmaxf(ref, merge[((h + HG * c) * G + hd) * kMergeRow + D]);
+        for (int c = 0; c < wph; ++c) {
+          const float* src = merge + ((h + HG * c) * G + hd) * kMergeRow;
+          ref = fmaxf(ref, src[D]);
+          top = max(top, scale_byte(src));
+        }
         for (int c = 0; c < wph; ++c) {
           const float* src = merge + ((h + HG * c) * G + hd) * kMergeRow;
           const float w = ex2(src[D] - ref);
           ll = fmaf(src[D + 1], w, ll);
+          const float wv = w * __int_as_float(max(127 + scale_byte(src) - top, 0) << 23);  // (0 below 2^-126)
           const float4 v = *reinterpret_cast<const float4*>(src + 4 * lane);
-          acc.x = fmaf(v.x, w, acc.x); acc.y = fmaf(v.y, w, acc.y);
-          acc.z = fmaf(v.z, w, acc.z); acc.w = fmaf(v.w, w, acc.w);
+          acc.x = fmaf(v.x, wv, acc.x); acc.y = fmaf(v.y, wv, acc.y);
+          acc.z = fmaf(v.z, wv, acc.z); acc.w = fmaf(v.w, wv, acc.w);
         }
-        const float inv = ll == 0.f ? 0.f : 0x1p32f / ll;
-        acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        const float inv = ll == 0.f ? 0.f : 1.f / ll, f = mx4_scale((uint32_t)top);
+        acc = make_float4(acc.x * inv * f, acc.y * inv * f, acc.z * inv * f, acc.w * inv * f);
         const int hq = (it.hg * HG + h) * G + hd;
         write4(hq, 4 * lane, acc);
         if (lane == 0) write_lse(hq, ref, ll);

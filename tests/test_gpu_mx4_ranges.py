@@ -192,3 +192,39 @@ def test_decode_of_scores_beyond_whole_float32_numbers(exp, g, sign):
         want_l = (sign * 96 * 2.0 ** exp + off.max() + np.log2(p.sum())) * np.log(2.0)
         # the score and the logarithm are added, then taken to base e: three roundings, and ln 2's own
         assert np.all(np.abs(lse[b] - want_l) <= abs(want_l) * 2.0 ** -22 + 2.0 ** -18), (b, lse[b], want_l)
+
+
+# ---------------------------------------------------------------------------
+# Values near the smallest and the largest numbers
+# ---------------------------------------------------------------------------
+
+@pytest.mark.parametrize("batch,hkv", [(2, 1), (2, 4), (700, 4), (1300, 4)])
+@pytest.mark.parametrize("g", [2, 8])
+def test_values_near_the_smallest_numbers_keep_their_bits(batch, hkv, g):
+    """bf16 values of about 2^-120, in every split of the warps (four, two and
+    one per head: the large batch), compared times 2^120."""
+    rng = np.random.default_rng(4)
+    lens = [int(x) for x in rng.integers(1, 60, batch)]
+    v = (np.abs(rng.standard_normal((sum(lens), hkv, 128))) + 0.5) * 2.0 ** -120
+    c = Cache(lens, hkv, 16, rng, v=v)
+    d, bt, dl = c.device()
+    q = torch.from_numpy(rng.standard_normal((batch, hkv * g, 128))).cuda().bfloat16()
+    o, lse = pkc.paged_decode_state_mx4(q, *d, bt, dl, 0.1, ws_for(batch, hkv * g))
+    c.v = [x * 2.0 ** 120 for x in c.v]
+    check_decode(c, q, o.double() * 2.0 ** 120, lse, g, 0.1, "bf16")
+
+
+@pytest.mark.parametrize("ps", [16, 5])
+def test_values_of_scale_byte_0(ps):
+    """Values of 2^-127 and its small multiples, compared times 2^120."""
+    rng = np.random.default_rng(7)
+    c = Cache([70], 2, ps, rng)
+    smallest(c, 2, rng)
+    d, bt, dl = c.device()
+    q = torch.from_numpy(rng.standard_normal((1, 4, 128))).cuda().bfloat16()
+    o, lse = pkc.paged_decode_state_mx4(q, *d, bt, dl, 0.1, ws_for(1, 4))
+    ro, rl, sm, vm = ref.attention(f64(q)[0], c.k[0], c.v[0] * 2.0 ** 120, 2, 0.1)
+    ot, lt = ref.bounds(ro, rl, sm, vm, 2.0 ** -7)
+    # (bf16 results below 2^-126 are multiples of 2^-133: off by 2^-134 at most)
+    assert np.all(np.abs(f64(o)[0] * 2.0 ** 120 - ro) <= ot + 2.0 ** -14)
+    assert np.all(np.abs(f64(lse)[0] - rl) <= lt)

@@ -525,7 +525,9 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm)
 // The join of split requests: one block per (request, query head) -- more
 // rows each if the uploaded plan has more than the host's copy of it -- its kW
 // warps taking every kW-th of the request's chunk states, lane i dims 4 i ..
-// + 3; then the warps' sums through shared memory.  An empty request's row is
+// + 3; then the warps' sums through shared memory.  The n states' weights
+// carry a factor 2^-ceil(log2 n), so that a sum of states near float32's
+// largest number stays finite, as their mean does.  An empty request's row is
 // (0, -inf).
 template <typename T, int kW>
 __global__ void __launch_bounds__(kW * 32) join_mx4_kernel(const __grid_constant__ Mx4JoinParams p) {
@@ -567,11 +569,13 @@ __global__ void __launch_bounds__(kW * 32) join_mx4_kernel(const __grid_constant
 #pragma unroll
     for (int x = 1; x < 32; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
     const float ref = m == neg_inf() ? 0.f : m;
+    const int down = n > 1 ? 32 - __clz(n - 1) : 0;
+    const float share = __int_as_float((127 - down) << 23);  // 2^-down
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float l = 0.f;
 #pragma unroll
     for (int k = 0; k < kAhead; ++k) {
-      const float w = ex2((la[k] - ref) * kLog2e);  // (0 past the end)
+      const float w = ex2((la[k] - ref) * kLog2e) * share;  // (0 past the end)
       l += w;
       acc.x = fmaf(va[k].x, w, acc.x); acc.y = fmaf(va[k].y, w, acc.y);
       acc.z = fmaf(va[k].z, w, acc.z); acc.w = fmaf(va[k].w, w, acc.w);
@@ -580,7 +584,7 @@ __global__ void __launch_bounds__(kW * 32) join_mx4_kernel(const __grid_constant
     for (int c = warp + kAhead * kW; c < n; c += kW) {
       const int64_t at = base + (int64_t)c * p.hq;
       const float4 v = *reinterpret_cast<const float4*>(p.part_o + at * D + 4 * lane);
-      const float w = ex2((p.part_lse[at] - ref) * kLog2e);
+      const float w = ex2((p.part_lse[at] - ref) * kLog2e) * share;
       l += w;
       acc.x = fmaf(v.x, w, acc.x); acc.y = fmaf(v.y, w, acc.y);
       acc.z = fmaf(v.z, w, acc.z); acc.w = fmaf(v.w, w, acc.w);
@@ -599,7 +603,7 @@ __global__ void __launch_bounds__(kW * 32) join_mx4_kernel(const __grid_constant
       T* dst = static_cast<T*>(p.o) + ((int64_t)req * p.hq + hq) * D + 4 * lane;
       *reinterpret_cast<uint2*>(dst) =
           make_uint2(Elem<T>::from_f2(acc.x * inv, acc.y * inv), Elem<T>::from_f2(acc.z * inv, acc.w * inv));
-      if (lane == 0) p.lse[(int64_t)req * p.hq + hq] = l == 0.f ? neg_inf() : ref + lg2(l) * kLn2;
+      if (lane == 0) p.lse[(int64_t)req * p.hq + hq] = l == 0.f ? neg_inf() : ref + (lg2(l) + (float)down) * kLn2;
     }
     __syncthreads();  // `part` is free
   }

@@ -228,3 +228,19 @@ def test_values_of_scale_byte_0(ps):
     # (bf16 results below 2^-126 are multiples of 2^-133: off by 2^-134 at most)
     assert np.all(np.abs(f64(o)[0] * 2.0 ** 120 - ro) <= ot + 2.0 ** -14)
     assert np.all(np.abs(f64(lse)[0] - rl) <= lt)
+
+
+@pytest.mark.parametrize("size", [2.0 ** -100, 1e37])
+def test_values_of_one_sign_in_split_requests(size):
+    """Values of about `size`, all positive: their mean over a request that a
+    plan splits into many chunks is of that size too."""
+    rng = np.random.default_rng(5)
+    lens, hkv, g, ctas = [6000, 40, 0], 1, 4, 148
+    c = Cache(lens, hkv, 16, rng, v=(np.abs(rng.standard_normal((6040, hkv, 128))) + 0.5) * size)
+    d, bt, dl = c.device()
+    q = torch.from_numpy(rng.standard_normal((3, hkv * g, 128))).cuda().bfloat16()
+    ws, plan = ws_for(3, hkv * g, ctas), pkc.plan(lens, ctas)
+    pkc.plan_upload(plan, ws)
+    o, lse = pkc.paged_decode_state_mx4(q, *d, bt, dl, 0.1, ws, plan_buf=plan)
+    c.v = [x / size for x in c.v]
+    check_decode(c, q, o.double() / size, lse, g, 0.1, "bf16")

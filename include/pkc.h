@@ -514,7 +514,9 @@ int pkc_cascade_decode_paged_prefix(
  * 2^(s_b - 127), 0 .. 254, or NaN whatever the codes, 255.  Element
  * 32 b + 4 u + i is nibble i (lowest first) of the 16-bit little-endian word
  * 4 u + b of the row's codes; a nibble is sign, two exponent bits, one
- * mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives.
+ * mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives.  At most 2^16
+ * KV heads (PKC_ERR_UNSUPPORTED above; so in pkc_accumulate_weights and
+ * pkc_evict_compact too).
  *
  * pkc_append_kv_mx4: quantise new tokens of every request to the end of its
  * cache, in place (the mx4 counterpart of pkc_append_kv, for any number of
@@ -618,6 +620,7 @@ int pkc_paged_decode_state_mx4(const void* q, const void* k_codes,
  * A token whose page is not there keeps its weight (PKC_ERR_BLOCK_TABLE); a
  * request longer than weights_stride has its first weights_stride tokens
  * treated (PKC_ERR_PLAN).  Results do not depend on any order of execution.
+ * batch * num_kv_heads <= 2^26 (PKC_ERR_UNSUPPORTED above).
  */
 int pkc_accumulate_weights(const void* q, const float* lse,
                            const void* k_cache, const void* k_scales,

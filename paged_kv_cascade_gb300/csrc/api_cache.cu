@@ -31,6 +31,8 @@ int check_pool(const char* call, int batch, int hkv, int head_dim, int page_size
                      "%s: batch and num_pages must be >= 0, num_kv_heads, page_size and block_table_stride >= 1", call);
   if (head_dim != PKC_HEAD_DIM)
     return set_error(PKC_ERR_UNSUPPORTED, "%s: head_dim must be %d (got %d)", call, PKC_HEAD_DIM, head_dim);
+  if (hkv > 1 << 16)  // a token's rows are addressed with 32 bits
+    return set_error(PKC_ERR_UNSUPPORTED, "%s: more than 2^16 KV heads (got %d)", call, hkv);
   if ((int64_t)block_table_stride * page_size > INT32_MAX - 65536)  // token positions are 32-bit
     return set_error(PKC_ERR_UNSUPPORTED, "%s: a block table of more than 2^31 - 65537 tokens", call);
   if (num_pages > (int64_t)(UINT32_MAX - 1) / page_size)  // and slots of the pool
@@ -185,6 +187,8 @@ int pkc_accumulate_weights(const void* q, const float* lse, const void* k_cache,
   if (!(decay >= 0.f && decay <= 1.f))
     return set_error(PKC_ERR_INVALID_ARG, "accumulate_weights: decay must be in [0, 1]");
   if (weights_stride < 1) return set_error(PKC_ERR_INVALID_ARG, "accumulate_weights: weights_stride must be >= 1");
+  if ((int64_t)batch * num_kv_heads > INT32_MAX / 32)
+    return set_error(PKC_ERR_UNSUPPORTED, "accumulate_weights: more than 2^26 (request, head) rows");
   if (int rc = check_ws(workspace, workspace_bytes, PKC_STATUS_BYTES)) return rc;
   if (batch == 0) return PKC_OK;
   if (!q || !lse || !k_cache || !block_table || !cache_seqlens || !weights || (kv_dtype == PKC_MX4 && !k_scales))

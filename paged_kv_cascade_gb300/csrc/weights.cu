@@ -98,19 +98,18 @@ __global__ void __launch_bounds__(kThreads, 4) weights_kernel(const WeightsParam
     return (uint32_t)pid * (uint32_t)p.page_size + (uint32_t)slot;
   };
   // Aligned: lane l holds the pool index of the first token of the warp's
-  // tile k0 + l (a window of 32, the next one loaded 32 tiles ahead).
-  // Otherwise: lane l that of token l of the next step's (at most 32).
-  auto load_window = [&](int k0) -> uint32_t {
-    const int k = k0 + lane, t = t_begin + (k / U) * t_step + 16 * (k % U);
-    return k < steps * U && t < t_end ? pool_token(t) : kNoToken;
+  // tile l (a segment has at most 32 a warp).  Otherwise: lane l that of
+  // token l of the next step's (at most 32).
+  auto load_tiles = [&]() -> uint32_t {
+    const int t = t_begin + (lane / U) * t_step + 16 * (lane % U);
+    return lane < steps * U && t < t_end ? pool_token(t) : kNoToken;
   };
   auto load_tokens = [&](int s) -> uint32_t {
     const int t = t_begin + s * t_step + lane;
     return s < steps && lane < kStep && t < t_end ? pool_token(t) : kNoToken;
   };
   static_assert(kStep <= 32, "a step's tokens are held one per lane");
-  uint32_t win = kAligned ? load_window(0) : load_tokens(0);
-  uint32_t win_next = kAligned ? load_window(32) : 0u;
+  uint32_t win = kAligned ? load_tiles() : load_tokens(0);
 
   const uint8_t* k_lane = static_cast<const uint8_t*>(p.k_cache) + (int64_t)kvh * KT::kRow + 16 * tg;
   const uint8_t* s_lane = static_cast<const uint8_t*>(p.k_scales) + kvh * 4;
@@ -122,17 +121,11 @@ __global__ void __launch_bounds__(kThreads, 4) weights_kernel(const WeightsParam
   auto load = [&](int s, Loads<KV>& x) {
     x.ok = 0;
     if (s >= steps) return;  // (warp-uniform)
-    if constexpr (kAligned) {
-      if (s > 0 && ((s * U) & 31) == 0) {
-        win = win_next;
-        win_next = load_window(s * U + 32);
-      }
-    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       uint32_t tok[2];
       if constexpr (kAligned) {
-        const uint32_t first = __shfl_sync(0xffffffffu, win, (s * U + u) & 31);
+        const uint32_t first = __shfl_sync(0xffffffffu, win, s * U + u);
         tok[0] = first + g;
         tok[1] = first + g + 8;
         if (first != kNoToken) x.ok |= 3u << (2 * u);  // (slots behind the last token are read, not used)
@@ -311,14 +304,13 @@ int launch_weights(const WeightsParams& p_in, int q_dtype, int kv_dtype, void* s
   const int64_t most = std::min(p.bt_stride * (int64_t)p.page_size, p.w_stride);
   const int step = 16 * (kv_dtype == PKC_E4M3 ? 2 : 1) * (kWarps / p.hg);
   const int64_t rows = (int64_t)p.batch * (p.hkv / p.hg);
-  int64_t seg = std::max<int64_t>((kv_dtype == PKC_MX4 ? 512 : 256) * (kWarps / p.hg), step);
+  int64_t seg = (kv_dtype == PKC_MX4 ? 512 : 256) * (kWarps / p.hg);
   while (seg > step && rows * ((most + seg - 1) / seg) < 4 * (int64_t)num_sms()) seg /= 2;
-  // (a grid has at most 2^31 - 1 blocks)
-  while (rows * ((most + seg - 1) / seg) > INT32_MAX) seg *= 2;
   p.seg_tokens = (int)seg;
   p.n_seg = (int)((most + seg - 1) / seg);
   const int64_t blocks = rows * p.n_seg;
   if (blocks <= 0) return 0;
+  if (blocks > INT32_MAX) return (int)cudaErrorInvalidConfiguration;
   cudaStream_t st = (cudaStream_t)stream;
   switch (kv_dtype) {
     case PKC_F16: return launch_t<PKC_F16, __half>(p, blocks, st);

@@ -124,14 +124,24 @@ def _check(rc):
 # A small call's time is the host's: the helpers below run a dozen times per
 # call, so they import torch once, compare devices by index and hand plain
 # integers to ctypes.
-_torch = None
+_torch = _get_device = _get_stream = None
+
+
+def _getters(torch):
+    """Functions for the current device's index and for a device's current
+    stream (its handle): the ones torch's own wrappers call, which cost a
+    fraction of them, or the wrappers in a torch that lacks those."""
+    return (getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device,
+            getattr(torch._C, "_cuda_getCurrentRawStream", None)
+            or (lambda index: torch.cuda.current_stream(index).cuda_stream))
 
 
 def _t():
     """torch, imported on the first call that takes tensors."""
-    global _torch
+    global _torch, _get_device, _get_stream
     if _torch is None:
         import torch
+        _get_device, _get_stream = _getters(torch)
         _torch = torch
     return _torch
 
@@ -144,13 +154,15 @@ def _dtype_code(t) -> int:
 
 def _device():
     """The current device's index (tensors on it exist: CUDA is initialised)."""
-    return (_torch or _t())._C._cuda_getDevice()
+    if _torch is None:
+        _t()
+    return _get_device()
 
 
 def _stream(stream):
-    torch = _torch or _t()
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(_device())
+        index = _device()
+        return _get_stream(index)
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

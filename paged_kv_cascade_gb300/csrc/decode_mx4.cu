@@ -60,7 +60,7 @@ constexpr int kScales = kTile * 4;
 constexpr int kStage = 2 * (kCodes + kScales);
 constexpr int kRing = kStages * kStage;       // per warp
 constexpr int kWarpSmem = kRing + 128 + 256;  // + the tile's probability factors and key scales
-constexpr float kRefFloor = -3e38f;           // softmax reference before the first token
+constexpr float kRefFloor = -0x1.fffffep127f;  // softmax reference before the first token: the lowest number
 constexpr float kLift = 11.f;                 // a new reference is this far below the largest score
 constexpr float kMost = kLift + 4.f;          // log2 of the largest probability between rescales
 

@@ -114,6 +114,27 @@ def test_decode_of_equal_tiny_queries_and_huge_keys():
     check_decode(c, q, o, lse, 4, 0.02, "bf16")
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("hkv,batch", [(1, 1), (4, 1300)])
+def test_decode_where_every_score_is_near_the_lowest_number(dtype, hkv, batch):
+    """All scores -3.3e38 in base 2: equal, finite, so the result is the mean of the values."""
+    rng = np.random.default_rng(8)
+    lens = [int(x) for x in rng.integers(1, 70, batch)]
+    c = Cache(lens, hkv, 16, rng, k=np.full((sum(lens), hkv, 128), -6 * 2.0 ** 118))
+    d, bt, dl = c.device()
+    q = torch.ones(batch, 2 * hkv, 128, device="cuda", dtype=DT[dtype])
+    o, lse = pkc.paged_decode_state_mx4(q, *d, bt, dl, 0.9, ws_for(batch, 2 * hkv))
+    o, lse = f64(o), f64(lse)
+    np.testing.assert_allclose(lse, -0.9 * 128 * 6 * 2.0 ** 118, rtol=2.0 ** -20)
+    eps = torch.finfo(DT[dtype]).eps
+    for b in range(batch):
+        for h in range(2 * hkv):
+            want = c.v[b][:, h // 2].mean(0)
+            # sums of up to 70 float32 values, one rounding to the type
+            vmax = np.abs(c.v[b][:, h // 2]).max()
+            assert np.all(np.abs(o[b, h] - want) <= 2.0 ** -17 * vmax + np.abs(want) * eps / 2 + 2.0 ** -25)
+
+
 @pytest.mark.parametrize("g", [4, 8])
 def test_decode_of_scores_that_are_large_and_finite(g):
     """|q| about 1, |k| = 2^108: q.k of 4e34 is a float32 number; one token has

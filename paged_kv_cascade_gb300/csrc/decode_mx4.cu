@@ -23,24 +23,25 @@
 // the largest score when it was set, rounded up, and at most 2^15 (r moves
 // when a score exceeds it by more than 15; both hold for scores of any size,
 // also where s - 11 is no float32 number).  They enter as an fp16 high part
-// and an fp16 remainder, one product each; the products with
-// the power of two are exact down to 2^-24.  So a probability enters with 22
-// bits, and what is lost is below 2^-24 of the largest cached |V| of the
-// block of dims.
+// and an fp16 remainder, one product each; the products with the power of two
+// are exact down to 2^-24.  So a probability enters with 22 bits, and what is
+// lost is below 2^-24 of the largest cached |V| of the block of dims.
 //
 // Work split.  A block is one work item -- a planned chunk (or request)
 // x HG KV heads -- of 4 warps; a warp takes every (4 / HG)-th group of 16
 // tokens of one KV head and keeps its own ring of cp.async stages, so no
 // warp waits for another until the item ends and any page size and head
-// count works.  Four blocks (16 warps of 128 registers) per SM.
+// count works.  Four blocks (16 warps of 128 registers) per SM; most forms
+// spill 4 to 48 bytes a thread to stay within that.
 //
 // Measured: 125 us for a batch of 256 with 32 / 8 heads over 476,458 tokens
 // (523 MB, 4.2 TB/s of a measured copy rate of 6.8); 43 us for two requests
 // of 107,000 tokens with 32 / 4 heads (117 MB), where the join, begun early,
-// takes 11 us when it runs alone.  Bound by instructions, about 350 per 16
-// tokens and head: 128 of them convert or feed the tensor cores, the rest are
-// addresses, scales, softmax.  Without the copies' bytes the kernel takes 5
-// us less, without the V product 21.
+// takes 10 us when it runs alone.  Bound by instructions, 356 per 16 tokens
+// and head with up to 4 query heads per KV head, 432 with 8: 128 of the 356
+// convert or feed the tensor cores, the rest are addresses, scales, softmax.
+// Without the copies' bytes the first takes 5 us less, without the V product
+// 21.
 #include <cuda_runtime.h>
 
 #include "decode_common.cuh"

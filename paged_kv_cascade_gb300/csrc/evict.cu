@@ -617,7 +617,7 @@ int launch_evict_compact(const CompactParams& p_in, void* stream) {
   if (rows * p.parts > INT32_MAX) return (int)cudaErrorInvalidValue;
   // Few rows of many slots: a cluster of up to 8 blocks shares each one, while
   // every block keeps a chunk of its own (8 heads cut to 16384 of 131072
-  // tokens: 94 -> 68 us, one head to 25000: 88 -> 45).
+  // tokens: 94 -> 65 us, one head to 25000: 88 -> 45).
   const int64_t chunk = (int64_t)kMoveRows * kMoveThreads / (p.row_bytes / 16 / p.slices);
   p.cluster = 1;
   while (p.cluster < 8 && rows * p.parts * p.cluster * 2 <= 4 * (int64_t)num_sms() && p.budget >= 2 * p.cluster * chunk)

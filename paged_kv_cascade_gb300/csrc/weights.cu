@@ -22,7 +22,7 @@
 //
 // Measured: bf16 keys, 64 requests, 164,506 tokens of 8 heads: 59 us (348 MB,
 // 5.9 TB/s of a measured copy rate of 6.8).  mx4 keys, 256 requests, 476,458
-// tokens: 78 us (292 MB, 3.7 TB/s), bound by the conversions' and scales'
+// tokens: 74 us (292 MB, 3.9 TB/s), bound by the conversions' and scales'
 // instructions, not by bytes.
 #include <cuda_runtime.h>
 
@@ -298,8 +298,9 @@ int launch_weights(const WeightsParams& p_in, int q_dtype, int kv_dtype, void* s
   // that the table and the weight rows hold, and blocks past a request's end
   // return at once.  256 tokens per warp (512 of the mx4 cache's short rows)
   // amortise a block's start (length -> page id -> key, three loads in a row;
-  // mx4: 84 -> 78 us) and still balance the end (16-bit with 512: 58 -> 65
-  // us); segments are halved while there are fewer than four blocks per SM.
+  // mx4 with 256: 74 -> 79 us) and still balance the end (16-bit with 512: 58
+  // -> 65 us); segments are halved while there are fewer than four blocks per
+  // SM.
   p.hg = p.hkv % 4 == 0 ? 4 : p.hkv % 2 == 0 ? 2 : 1;
   const int64_t most = std::min(p.bt_stride * (int64_t)p.page_size, p.w_stride);
   const int step = 16 * (kv_dtype == PKC_E4M3 ? 2 : 1) * (kWarps / p.hg);

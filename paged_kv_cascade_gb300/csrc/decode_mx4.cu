@@ -35,7 +35,7 @@
 // spill 4 to 48 bytes a thread to stay within that.
 //
 // Measured: 125 us for a batch of 256 with 32 / 8 heads over 476,458 tokens
-// (523 MB, 4.2 TB/s of a measured copy rate of 6.8); 43 us for two requests
+// (523 MB, 4.2 TB/s of a measured copy rate of 6.8); 44 us for two requests
 // of 107,000 tokens with 32 / 4 heads (117 MB), where the join, begun early,
 // takes 10 us when it runs alone.  Bound by instructions, 356 per 16 tokens
 // and head with up to 4 query heads per KV head, 432 with 8: 128 of the 356

@@ -571,10 +571,11 @@ int pkc_gather_kv_mx4(const void* k_codes, const void* k_scales,
  * any number of KV heads.  Split requests are joined by a kernel of its own
  * (pkc_set_contraction does not apply).  Accuracy beyond the format's: the scores
  * are those of the cached values with float32 sums, which stay finite where
- * q.k is; probabilities enter the V product with 22 bits, with fewer where a
- * token's |V| is far below the largest cached |V| of the block of dims, and
- * a value below 2^-24 of that largest one may count as zero.  A page id < 0 or >= num_pages
- * is recorded as PKC_ERR_BLOCK_TABLE and its tokens take no part.
+ * q.k does (for queries below 2^64); probabilities enter the V product with
+ * 22 bits, with fewer where a token's |V| is far below the largest cached
+ * |V| of the block of dims, and a value below 2^-24 of that largest one may
+ * count as zero.  A page id < 0 or >= num_pages is recorded as
+ * PKC_ERR_BLOCK_TABLE and its tokens take no part.
  */
 int pkc_paged_decode_state_mx4(const void* q, const void* k_codes,
                                const void* k_scales, const void* v_codes,

@@ -148,8 +148,8 @@ __device__ __forceinline__ void mma16816_f16_new(float (&d)[4], const uint32_t (
 // multiplied by key_mul (a bf16 pair): 2^-22 keeps every such sum below
 // 2^127.6.  It also drops scales below 2^-111; those count for less than 2^-37
 // in a score as long as |q| < 2^64.  A warp with a larger query leaves the
-// scales whole (1): keys that overflow the sum then give that query scores
-// beyond float32 as well.
+// scales whole (1): keys of 2^105 and more, which may then overflow the sums
+// of all its heads, give that query scores beyond float32 in any case.
 //
 // Returns the factor that undoes both.
 template <typename T, int G, bool kRepeat = false>

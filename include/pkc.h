@@ -52,7 +52,8 @@ typedef enum {
   PKC_ERR_BLOCK_TABLE = 4, /* device: page id < 0 or >= num_pages in use */
   PKC_ERR_CUDA = 5,        /* a CUDA runtime call failed */
   PKC_ERR_TIMEOUT = 6,     /* device: a bounded wait ran out */
-  PKC_ERR_PLAN = 7         /* plan buffer invalid or inconsistent */
+  PKC_ERR_PLAN = 7,        /* plan buffer invalid or inconsistent */
+  PKC_ERR_NO_PAGES = 8     /* device: the pool has too few free pages */
 } pkc_status;
 
 /* Element types.  PKC_E4M3 (8-bit float: 1 sign, 4 exponent bits with
@@ -244,8 +245,8 @@ int pkc_workspace_init(void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Read (and clear) the device status word: *status = PKC_OK or the first
- * PKC_ERR_BLOCK_TABLE / PKC_ERR_PLAN / PKC_ERR_TIMEOUT a kernel recorded
- * since the last read.  Synchronises `stream`.
+ * PKC_ERR_BLOCK_TABLE / PKC_ERR_PLAN / PKC_ERR_TIMEOUT / PKC_ERR_NO_PAGES a
+ * kernel recorded since the last read.  Synchronises `stream`.
  */
 int pkc_device_status(void* workspace, void* stream, int32_t* status);
 
@@ -685,6 +686,141 @@ int pkc_evict_compact(const int32_t* keep, int budget, void* k_cache,
                       int head_dim, int page_size, int64_t num_pages,
                       int kv_dtype, void* workspace, size_t workspace_bytes,
                       void* stream);
+
+/* ------------------------------------------------------------------------
+ * A prompt's way into the cache: pages, rotary positions, chunk attention
+ * ---------------------------------------------------------------------- */
+
+/*
+ * The pool of free pages is a bit map in device memory: free_pages
+ * [ceil(num_pages / 32)] uint32, bit p % 32 of word p / 32 set where page p is
+ * free (bits behind the last page are ignored and kept).  num_pages <= 2^26
+ * and batch <= 2^14 in the two calls (PKC_ERR_UNSUPPORTED above).
+ *
+ * pkc_release_pages: give back the pages behind every request's length
+ * (after pkc_evict_compact, or of a request that is done: length 0).  Entries
+ * block_table[b][j], j >= ceil(cache_seqlens[b] / page_size), that hold a page
+ * become -1 and the page's bit is set; the result does not depend on any
+ * order.  Negative entries stay.  A page id >= num_pages stays where it is and
+ * a page that was free already becomes -1; both are recorded as
+ * PKC_ERR_BLOCK_TABLE.  A request with a negative length is left as it is
+ * (PKC_ERR_PLAN).  Pages that another request also holds are the caller's not
+ * to release.
+ */
+int pkc_release_pages(int32_t* block_table, int block_table_stride,
+                      const int32_t* cache_seqlens, int batch, int page_size,
+                      int64_t num_pages, uint32_t* free_pages, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/*
+ * Pages and slots for new tokens, from the requests' lengths alone.  Request b
+ * brings n_b = new_indptr[b + 1] - new_indptr[b] tokens (rows new_indptr[b] ..
+ * of the step's ragged batch; none, one or many) behind its cache_seqlens[b]
+ * cached ones and needs need_b = ceil((cache_seqlens[b] + n_b) / page_size) -
+ * ceil(cache_seqlens[b] / page_size) pages.
+ *   new_indptr [batch + 1] int32, device
+ *   block_table [batch, block_table_stride] int32: the pages are written
+ *            behind the used entries; what stands there is overwritten
+ *            (release first)
+ *   free_pages the pool (above): the lowest-numbered free pages are taken, in
+ *            request order, and their bits cleared
+ *   slots    [total_new] int64: page * page_size + slot of every new token,
+ *            -1 for a token without a place and a row of no request
+ *   positions [total_new] int32: the token's position, cache_seqlens[b] + i
+ *            (0 for a row of no request)
+ *   seqlens_out NULL, or [batch] int32: the lengths with the new tokens;
+ *            cache_seqlens itself may be given
+ * Requests are served in order until the pages run out: one whose pages,
+ * together with those of all requests before it, exceed the free ones gets
+ * none, its length stays and PKC_ERR_NO_PAGES is recorded (one that needs no
+ * page is always served).  A request with a negative length, one that would
+ * outgrow the table, and one whose last, partly filled page is not there are
+ * not served either and count for no pages (PKC_ERR_BLOCK_TABLE).  A
+ * new_indptr that does not run upwards within 0 .. total_new serves nobody
+ * (PKC_ERR_PLAN).  One launch.
+ */
+int pkc_assign_pages(int32_t* block_table, int block_table_stride,
+                     const int32_t* cache_seqlens, const int32_t* new_indptr,
+                     int total_new, int batch, int page_size,
+                     int64_t num_pages, uint32_t* free_pages, int64_t* slots,
+                     int32_t* positions, int32_t* seqlens_out, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/*
+ * Rotary positions applied to a step's queries and keys, and its keys and
+ * values written to their slots of the paged cache.
+ *   q        [total, num_qo_heads, 128] of dtype (F16 or BF16), a token's rows
+ *            q_stride elements apart; k_new, v_new [total, num_kv_heads, 128]
+ *            with kv_stride (so the three may be parts of one projection's
+ *            output).  Strides are multiples of 8 and at least a token's size
+ *   positions [total] int32;  slots [total] int64 (pkc_assign_pages): a
+ *            negative slot's token is not cached, one >= num_pages * page_size
+ *            neither (PKC_ERR_BLOCK_TABLE).  Slots are distinct
+ *   inv_freq [rotary_dim / 2] float64, device, finite: radians per token of
+ *            each pair, of any scaling for long contexts
+ *            (position * inv_freq is reduced to a fraction of a turn in
+ *            64 bits, so far positions keep their angles)
+ *   rotary_dim a multiple of 16 in 16 .. 128: the first rotary_dim elements of
+ *            a row are turned, the others pass.  Pair i is elements (2 i,
+ *            2 i + 1) if interleaved is 1, (i, i + rotary_dim / 2) if 0:
+ *            (x, y) -> amplitude (x cos a - y sin a, x sin a + y cos a)
+ *   q_out    [total, num_qo_heads, 128] of dtype, dense; may be q if q is
+ *   k_cache, v_cache [num_pages, page_size, num_kv_heads, 128] of kv_dtype:
+ *            dtype itself (k_scale = v_scale = 1), or E4M3: the nearest codes
+ *            of the turned key / k_scale and of the value / v_scale (ties to
+ *            even, +-448 beyond it and for infinities; NaN stays NaN)
+ * Formed in float32 and rounded once.  One launch.
+ */
+int pkc_rope_append_kv(const void* q, int64_t q_stride, const void* k_new,
+                       const void* v_new, int64_t kv_stride,
+                       const int32_t* positions, const int64_t* slots,
+                       const double* inv_freq, int rotary_dim, int interleaved,
+                       float amplitude, int total, int num_qo_heads,
+                       int num_kv_heads, int head_dim, void* q_out,
+                       void* k_cache, void* v_cache, int page_size,
+                       int64_t num_pages, float k_scale, float v_scale,
+                       int dtype, int kv_dtype, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * Bytes of workspace of pkc_paged_chunk_state, for any problem: the status
+ * block and the partial states.  The call uses the status block and the end
+ * of the workspace it is given, so one of pkc_workspace_size(...) +
+ * pkc_chunk_workspace_size() bytes can hold a decode's plan too.
+ */
+int pkc_chunk_workspace_size(size_t* bytes);
+
+/*
+ * Attention states of a chunk of new tokens per request over its paged cache,
+ * which holds them already: a prompt, a part of one, speculated tokens, or a
+ * single token, in any mix.  Request b's n_b = q_indptr[b + 1] - q_indptr[b]
+ * rows are its last ones: row i stands at position p = cache_seqlens[b] - n_b +
+ * i and attends to tokens t < cache_seqlens[b] with t <= p (causal = 1) and
+ * t > p - window (window > 0).  A row that attends to nothing gets (0, -inf).
+ *   q        [total_q, num_qo_heads, 128] of dtype (F16 or BF16)
+ *   q_indptr [batch + 1] int32, device; rows of no request are not written
+ *   k_cache, v_cache [num_pages, page_size, num_kv_heads, 128] of dtype, any
+ *            page size; block_table, cache_seqlens as in
+ *            pkc_paged_decode_state (the lengths count the new tokens)
+ *   sm_scale finite, >= 0
+ *   o        [total_q, num_qo_heads, 128] of out_dtype: dtype, or F32 for a
+ *            state that is merged further (pkc_merge_states_to); lse
+ *            [total_q, num_qo_heads] float32, natural log
+ * A token that a row does not attend to has no influence on it, whatever its
+ * key and value hold.  Probabilities enter the V product in dtype.  A page id
+ * < 0 or >= num_pages (or past the table) is read as zeros and recorded as
+ * PKC_ERR_BLOCK_TABLE.  A request whose rows do not lie within 0 .. total_q, or
+ * with a negative length, is not computed (PKC_ERR_PLAN).
+ */
+int pkc_paged_chunk_state(const void* q, const int32_t* q_indptr, int total_q,
+                          const void* k_cache, const void* v_cache,
+                          const int32_t* block_table, int block_table_stride,
+                          const int32_t* cache_seqlens, int batch,
+                          int num_qo_heads, int num_kv_heads, int head_dim,
+                          int page_size, int64_t num_pages, float sm_scale,
+                          int causal, int window, void* workspace,
+                          size_t workspace_bytes, void* o, float* lse,
+                          int dtype, int out_dtype, void* stream);
 
 /* ------------------------------------------------------------------------
  * Stage timing

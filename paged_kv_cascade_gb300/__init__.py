@@ -20,7 +20,7 @@ LIB_PATH = os.path.join(_HERE, "_build", "libpkc.so")
 PKC_OK = 0
 STATUS_NAMES = {0: "PKC_OK", 1: "PKC_ERR_INVALID_ARG", 2: "PKC_ERR_UNSUPPORTED",
                 3: "PKC_ERR_WORKSPACE", 4: "PKC_ERR_BLOCK_TABLE", 5: "PKC_ERR_CUDA",
-                6: "PKC_ERR_TIMEOUT", 7: "PKC_ERR_PLAN"}
+                6: "PKC_ERR_TIMEOUT", 7: "PKC_ERR_PLAN", 8: "PKC_ERR_NO_PAGES"}
 F32, F16, BF16, E4M3, MX4 = 0, 1, 2, 3, 4
 
 # Header indices of the plan buffer (include/pkc.h).
@@ -84,6 +84,13 @@ SIGNATURES = {
     "pkc_evict_select": (_I, [_P, _I64, _P, _I, _I, _I, _I, _I, _P, _P, _SZ, _P]),
     "pkc_evict_compact": (_I, [_P, _I, _P, _P, _P, _P, _P, _I, _P, _P, _I64, _I, _I, _I, _I, _I64, _I,
                                _P, _SZ, _P]),
+    "pkc_release_pages": (_I, [_P, _I, _P, _I, _I, _I64, _P, _P, _SZ, _P]),
+    "pkc_assign_pages": (_I, [_P, _I, _P, _P, _I, _I, _I, _I64, _P, _P, _P, _P, _P, _SZ, _P]),
+    "pkc_rope_append_kv": (_I, [_P, _I64, _P, _P, _I64, _P, _P, _P, _I, _I, _F, _I, _I, _I, _I, _P, _P, _P,
+                                _I, _I64, _F, _F, _I, _I, _P, _SZ, _P]),
+    "pkc_chunk_workspace_size": (_I, [_c.POINTER(_SZ)]),
+    "pkc_paged_chunk_state": (_I, [_P, _P, _I, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I64, _F, _I, _I,
+                                   _P, _SZ, _P, _P, _I, _I, _P]),
 }
 
 _lib = None
@@ -622,6 +629,195 @@ def evict_compact(keep, k_cache, v_cache, block_table, cache_seqlens, workspace,
         _ptr(block_table), block_table.shape[1], _ptr(cache_seqlens), _ptr(weights),
         0 if weights is None else weights.shape[2], B, Hkv, 128, ps, P, kind, _ptr(workspace),
         workspace.numel(), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# A prompt's way into the cache: pages, rotary positions, chunk attention
+# ---------------------------------------------------------------------------
+
+def page_pool(num_pages, device="cuda"):
+    """The map of a pool whose pages are all free: int32 words, bit p % 32 of
+    word p / 32 for page p (release_pages and assign_pages keep it)."""
+    torch = _torch or _t()
+    num_pages = int(num_pages)
+    if num_pages < 0:
+        raise ValueError(f"page_pool: num_pages must be >= 0 (got {num_pages})")
+    words = np.full((num_pages + 31) // 32, 0xFFFFFFFF, np.uint32)
+    if num_pages % 32:
+        words[-1] = (1 << num_pages % 32) - 1
+    return torch.from_numpy(words.view(np.int32)).to(device)
+
+
+def _check_pages(block_table, cache_seqlens, free_pages, num_pages, workspace):
+    torch = _torch or _t()
+    B, n_pages = _leading("block_table", block_table, (torch.int32,), 2)
+    dev = block_table.device
+    num_pages = int(num_pages)
+    if num_pages < 0:
+        raise ValueError(f"num_pages must be >= 0 (got {num_pages})")
+    _expect_all(dev, ("block_table", block_table, torch.int32, (B, n_pages)),
+                ("cache_seqlens", cache_seqlens, torch.int32, (B,)),
+                ("free_pages", free_pages, torch.int32, ((num_pages + 31) // 32,)),
+                ("workspace", workspace, torch.uint8, _sizes(workspace, 1)))
+    return B, n_pages, num_pages, dev
+
+
+def release_pages(block_table, cache_seqlens, free_pages, page_size, num_pages, workspace, stream=None):
+    """Give the pages behind every request's length back to the pool
+    free_pages (of page_pool), in place: their table entries become -1."""
+    B, stride, num_pages, _ = _check_pages(block_table, cache_seqlens, free_pages, num_pages, workspace)
+    _check(lib().pkc_release_pages(
+        _ptr(block_table), stride, _ptr(cache_seqlens), B, int(page_size), num_pages, _ptr(free_pages),
+        _ptr(workspace), workspace.numel(), _stream(stream)))
+
+
+def assign_pages(block_table, cache_seqlens, new_indptr, total_new, free_pages, page_size, num_pages, workspace,
+                 slots=None, positions=None, seqlens_out=None, stream=None):
+    """Pages for total_new new tokens (request b's are new_indptr[b] ..
+    new_indptr[b+1]-1, device int32) taken from free_pages into block_table, in
+    place.  Returns (slots [total_new] int64: page * page_size + slot, or -1;
+    positions [total_new] int32; the lengths with the new tokens [B] int32,
+    a new tensor unless seqlens_out is given -- cache_seqlens itself may be)."""
+    torch = _torch or _t()
+    B, stride, num_pages, dev = _check_pages(block_table, cache_seqlens, free_pages, num_pages, workspace)
+    total = int(total_new)
+    if total < 0:
+        raise ValueError(f"assign_pages: total_new must be >= 0 (got {total})")
+    slots = torch.empty(total, dtype=torch.int64, device=dev) if slots is None else slots
+    positions = torch.empty(total, dtype=torch.int32, device=dev) if positions is None else positions
+    seqlens_out = torch.empty(B, dtype=torch.int32, device=dev) if seqlens_out is None else seqlens_out
+    _expect_all(dev, ("new_indptr", new_indptr, torch.int32, (B + 1,)), ("slots", slots, torch.int64, (total,)),
+                ("positions", positions, torch.int32, (total,)), ("seqlens_out", seqlens_out, torch.int32, (B,)))
+    _check(lib().pkc_assign_pages(
+        _ptr(block_table), stride, _ptr(cache_seqlens), _ptr(new_indptr), total, B, int(page_size), num_pages,
+        _ptr(free_pages), _ptr(slots), _ptr(positions), _ptr(seqlens_out), _ptr(workspace), workspace.numel(),
+        _stream(stream)))
+    return slots, positions, seqlens_out
+
+
+def rope_frequencies(rotary_dim=128, base=10000.0, factor=1.0, context=None, slow=1.0, fast=32.0, device="cuda"):
+    """(inv_freq [rotary_dim / 2] float64, amplitude) for rope_append_kv: base
+    ** (-2 i / rotary_dim) radians per token.  factor > 1 stretches positions
+    that many times: all pairs alike without `context` (amplitude 1), else by
+    parts -- pairs that turn `fast` times or more within `context` tokens keep
+    their frequency, those that turn `slow` times or less are slowed by the
+    factor, with a linear blend between (amplitude 0.1 ln factor + 1)."""
+    torch = _torch or _t()
+    rotary_dim, base, factor = int(rotary_dim), float(base), float(factor)
+    if rotary_dim < 2 or rotary_dim % 2 or not base > 0 or not factor >= 1:
+        raise ValueError("rope_frequencies: rotary_dim must be even and >= 2, base > 0, factor >= 1 "
+                         f"(got {rotary_dim}, {base}, {factor})")
+    f = base ** (-np.arange(0, rotary_dim, 2, dtype=np.float64) / rotary_dim)
+    amplitude = 1.0
+    if factor > 1 and context is None:
+        f = f / factor
+    elif factor > 1:
+        if not (float(context) > 0 and fast > slow):
+            raise ValueError("rope_frequencies: context must be > 0 and fast > slow")
+        keep = np.clip((float(context) * f / (2 * np.pi) - slow) / (fast - slow), 0.0, 1.0)
+        f = f * (keep + (1 - keep) / factor)
+        amplitude = 0.1 * float(np.log(factor)) + 1.0
+    return torch.from_numpy(f).to(device), amplitude
+
+
+def _expect_rows(name, t, dtype, shape, device):
+    """t [T, H, 128] with dense heads: the tokens may lie apart, as in a part
+    of a larger projection.  Returns the distance of two tokens in elements."""
+    if not isinstance(t, _torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    st = t.stride()
+    if st[2] != 1 or (st[1] != 128 and shape[1] != 1):
+        raise ValueError(f"{name} must have dense heads (strides {st})")
+    return st[0] if shape[0] > 1 else shape[1] * 128
+
+
+def rope_append_kv(q, k_new, v_new, positions, slots, inv_freq, k_cache, v_cache, workspace, interleaved=False,
+                   amplitude=1.0, k_scale=1.0, v_scale=1.0, q_out=None, stream=None):
+    """Turn q [T, Hq, 128] and k_new [T, Hkv, 128] by their positions [T] int32
+    (pairs of the first 2 * len(inv_freq) elements; inv_freq float64 as of
+    rope_frequencies), write k and v_new [T, Hkv, 128] to slots [T] int64 of the
+    paged pools (of q's dtype, or uint8 e4m3 codes with scales) and return the
+    turned q (dense).  q, k_new and v_new may be slices of one projection."""
+    torch = _torch or _t()
+    P, ps, Hkv, _ = _leading("k_cache", k_cache, (torch.float16, torch.bfloat16, torch.uint8), 4, 128)
+    dev = k_cache.device
+    T, Hq, _ = _sizes(q, 3)
+    if T is None or q.dtype not in (torch.float16, torch.bfloat16):
+        _expect("q", q, (torch.float16, torch.bfloat16), (None, None, 128), dev)
+    dtype = q.dtype
+    q_stride = _expect_rows("q", q, dtype, (T, Hq, 128), dev)
+    kv_stride = _expect_rows("k_new", k_new, dtype, (T, Hkv, 128), dev)
+    if _expect_rows("v_new", v_new, dtype, (T, Hkv, 128), dev) != kv_stride:
+        raise ValueError("k_new and v_new must have the same strides")
+    kv_dtype = torch.uint8 if k_cache.dtype == torch.uint8 else dtype
+    half = _sizes(inv_freq, 1)[0]
+    _expect_all(dev, ("k_cache", k_cache, kv_dtype, (P, ps, Hkv, 128)), ("v_cache", v_cache, kv_dtype, (P, ps, Hkv, 128)),
+                ("positions", positions, torch.int32, (T,)), ("slots", slots, torch.int64, (T,)),
+                ("inv_freq", inv_freq, torch.float64, (half,)),
+                ("workspace", workspace, torch.uint8, _sizes(workspace, 1)))
+    if q_out is None:
+        q_out = torch.empty((T, Hq, 128), dtype=dtype, device=dev)
+    else:
+        _expect("q_out", q_out, (dtype,), (T, Hq, 128), dev)
+    code = F16 if dtype is torch.float16 else BF16
+    _check(lib().pkc_rope_append_kv(
+        _ptr(q), q_stride, _ptr(k_new), _ptr(v_new), kv_stride, _ptr(positions), _ptr(slots), _ptr(inv_freq),
+        2 * half, 1 if interleaved else 0, float(amplitude), T, Hq, Hkv, 128, _ptr(q_out), _ptr(k_cache),
+        _ptr(v_cache), ps, P, float(k_scale), float(v_scale), code, E4M3 if kv_dtype is torch.uint8 else code,
+        _ptr(workspace), workspace.numel(), _stream(stream)))
+    return q_out
+
+
+def chunk_workspace_size() -> int:
+    """Bytes of workspace that paged_chunk_state needs, for any problem (added
+    to workspace_size(...) where one workspace serves other calls too)."""
+    out = ctypes.c_size_t()
+    _check(lib().pkc_chunk_workspace_size(ctypes.byref(out)))
+    return out.value
+
+
+def paged_chunk_state(q, q_indptr, k_cache, v_cache, block_table, cache_seqlens, sm_scale, workspace, causal=True,
+                      window=0, out_dtype=None, o=None, lse=None, stream=None):
+    """States of a chunk of new tokens per request over its paged cache, which
+    holds them already: q [T, Hq, 128], rows q_indptr[b] .. q_indptr[b+1]-1
+    (device int32) are the last of request b's cache_seqlens[b] tokens.  A row
+    attends to the tokens up to its own (all, if not causal), at most the last
+    `window` of them (0: no limit).  o has q's dtype, or float32 (out_dtype)
+    for states merged further."""
+    torch = _torch or _t()
+    P, ps, Hkv, _ = _leading("k_cache", k_cache, (torch.float16, torch.bfloat16), 4, 128)
+    dev, dtype = k_cache.device, k_cache.dtype
+    T, Hq, _ = _sizes(q, 3)
+    B, stride = _sizes(block_table, 2)
+    _expect_all(dev, ("q", q, dtype, (T, Hq, 128)), ("k_cache", k_cache, dtype, (P, ps, Hkv, 128)),
+                ("v_cache", v_cache, dtype, (P, ps, Hkv, 128)), ("block_table", block_table, torch.int32, (B, stride)),
+                ("q_indptr", q_indptr, torch.int32, (None if B is None else B + 1,)),
+                ("cache_seqlens", cache_seqlens, torch.int32, (B,)),
+                ("workspace", workspace, torch.uint8, _sizes(workspace, 1)))
+    if out_dtype is None:
+        out_dtype = dtype if o is None else o.dtype
+    if out_dtype is not dtype and out_dtype is not torch.float32:
+        raise TypeError(f"paged_chunk_state: out_dtype must be {dtype} or torch.float32 (got {out_dtype})")
+    if o is None:
+        o = torch.empty((T, Hq, 128), dtype=out_dtype, device=dev)
+    else:
+        _expect("o", o, (out_dtype,), (T, Hq, 128), dev)
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    else:
+        _expect("lse", lse, (torch.float32,), (T, Hq), dev)
+    code = F16 if dtype is torch.float16 else BF16
+    _check(lib().pkc_paged_chunk_state(
+        _ptr(q), _ptr(q_indptr), T, _ptr(k_cache), _ptr(v_cache), _ptr(block_table), stride, _ptr(cache_seqlens), B,
+        Hq, Hkv, 128, ps, P, float(sm_scale), 1 if causal else 0, int(window), _ptr(workspace), workspace.numel(),
+        _ptr(o), _ptr(lse), code, F32 if out_dtype is torch.float32 else code, _stream(stream)))
+    return o, lse
 
 
 DECODE_KERNELS = {"auto": 0, "simt": 1, "mma": 2}

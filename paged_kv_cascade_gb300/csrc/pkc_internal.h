@@ -18,6 +18,10 @@
 #define PKC_STATUS_BYTES 256
 #define PKC_APPEND_COUNTER 18
 #define PKC_COMPACT_COUNTER 20
+// Limits of the calls over the pool of free pages (pages.cu keeps the
+// requests' offsets and the pool's counts in shared memory).
+#define PKC_PAGES_MAX_BATCH 16384
+#define PKC_PAGES_MAX_PAGES (int64_t(1) << 26)
 
 namespace pkc {
 
@@ -309,7 +313,64 @@ struct CompactParams {
   int32_t* status;
 };
 
+// Pages and slots for new tokens (pages.cu).
+struct PagesParams {
+  int32_t* block_table;
+  const int32_t* cache_seqlens;
+  const int32_t* indptr;     // assign: [batch + 1]
+  uint32_t* free_pages;      // [ceil(num_pages / 32)]
+  int64_t* slots;            // [total]
+  int32_t* positions;        // [total]
+  int32_t* seqlens_out;      // [batch] or nullptr; may be cache_seqlens
+  int64_t bt_stride, num_pages;
+  int batch, page_size, total;
+  int32_t* status;
+};
+
+// Rotary positions on the way into the cache (rope.cu).
+struct RopeParams {
+  const void* q;             // [total, hq, 128], tokens q_stride elements apart
+  const void* k_new;
+  const void* v_new;
+  int64_t q_stride, kv_stride;
+  const int32_t* positions;
+  const int64_t* slots;
+  const double* inv_freq;    // [rotary_dim / 2]
+  void* q_out;
+  void* k_cache;             // [pool_tokens, hkv, 128] of kv_dtype
+  void* v_cache;
+  int64_t pool_tokens;
+  int rotary_dim, interleaved, total, hq, hkv;
+  float amplitude, k_inv_scale, v_inv_scale;
+  int32_t* status;
+};
+
+// Attention of a chunk of new tokens over a paged cache (chunk.cu).
+struct ChunkParams {
+  const void* q;             // [total_q, hq, 128]
+  const int32_t* q_indptr;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* block_table;
+  const int32_t* cache_seqlens;
+  int64_t bt_stride, num_pages;
+  int total_q, batch, hq, hkv, g, page_size;
+  int causal, window;        // window 0: none
+  float scale_log2;
+  void* o;
+  float* lse;
+  int out_dtype;
+  float* part_o;             // partial states [slot, 256, 128], [slot, 256]
+  float* part_lse;
+  int32_t* status;
+};
+
 // Launchers (defined in the .cu files); return a cudaError_t value.
+int launch_release_pages(const PagesParams& p, void* stream);
+int launch_assign_pages(const PagesParams& p, void* stream);
+int launch_rope_append(const RopeParams& p, int dtype, int kv_dtype, void* stream);
+size_t chunk_partial_bytes();
+int launch_paged_chunk(const ChunkParams& p, int dtype, void* stream);
 int launch_evict_select(const SelectParams& p, void* stream);
 int launch_evict_compact(const CompactParams& p, void* stream);
 int launch_weights(const WeightsParams& p, int q_dtype, int kv_dtype, void* stream);

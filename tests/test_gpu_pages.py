@@ -1,0 +1,194 @@
+"""Pages and slots for new tokens, and pages given back, against the plain definitions."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cascade_gb300 as pkc
+import prompt_reference as ref
+
+pytestmark = pytest.mark.gpu
+I32 = torch.int32
+
+
+def workspace(n=256):
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    pkc.workspace_init(ws)
+    return ws
+
+
+def state(batch, page, num_pages, most, stride, seed, held=0):
+    """Random lengths whose pages come from a permuted pool; `held` further entries behind each length."""
+    rng = np.random.default_rng(seed)
+    perm = rng.permutation(num_pages).tolist()
+    lens, table = [], []
+    for _ in range(batch):
+        n = int(rng.integers(0, min(most, (stride - held) * page) + 1))
+        need = -(-n // page) + held
+        if need > len(perm):
+            n, need = 0, 0
+        row = [perm.pop() for _ in range(need)]
+        lens.append(n)
+        table.append(row + [-1] * (stride - len(row)))
+    return lens, table, set(perm)
+
+
+class Run:
+    def __init__(self, lens, table, free, page, num_pages):
+        self.lens, self.table, self.free, self.page, self.num_pages = lens, [list(r) for r in table], set(free), page, num_pages
+        self.d_lens = torch.tensor(lens, dtype=I32, device="cuda")
+        self.d_table = torch.tensor(table, dtype=I32, device="cuda")
+        self.d_free = ref.pool_words(free, num_pages).cuda()
+        self.ws = workspace()
+
+    def release(self, want=0):
+        pkc.release_pages(self.d_table, self.d_lens, self.d_free, self.page, self.num_pages, self.ws)
+        ref.release(self.table, self.lens, self.free, self.page)
+        self.check(want)
+
+    def assign(self, new, lead=0, trail=0, want=None, in_place=False):
+        indptr = [lead]
+        for n in new:
+            indptr.append(indptr[-1] + n)
+        total = indptr[-1] + trail
+        out = self.d_lens if in_place else None
+        got = pkc.assign_pages(self.d_table, self.d_lens, torch.tensor(indptr, dtype=I32, device="cuda"), total, self.d_free,
+                               self.page, self.num_pages, self.ws, seqlens_out=out)
+        slots, pos, lens, status = ref.assign(self.table, self.lens, indptr, total, self.free, self.page)
+        assert got[0].tolist() == slots
+        assert got[1].tolist() == pos
+        assert got[2].tolist() == lens
+        self.check(status if want is None else want)
+        if in_place:
+            self.lens = lens
+        return got
+
+    def check(self, want):
+        assert self.d_table.tolist() == self.table
+        assert ref.pool_set(self.d_free, self.num_pages) == self.free
+        assert pkc.device_status(self.ws) == want
+
+
+@pytest.mark.parametrize("batch,page,num_pages,most_new", [
+    (1, 16, 1, 16), (1, 1, 33, 33), (3, 16, 40, 5), (5, 7, 300, 60), (64, 16, 8000, 1), (130, 20, 4096, 90),
+    (1500, 16, 70001, 40), (7, 64, 5000, 9000), (40, 8, 200000, 3000),
+])
+def test_assign(batch, page, num_pages, most_new):
+    rng = np.random.default_rng(batch + page)
+    stride = max(1, num_pages // batch)
+    lens, table, free = state(batch, page, num_pages, stride * page // 2, stride, 5)
+    run = Run(lens, table, free, page, num_pages)
+    run.assign(rng.integers(0, most_new + 1, batch).tolist())
+
+
+def test_steps_until_the_pool_is_empty():
+    """One token each, lengths grown in place, until requests find no pages;
+    then a request ends and others go on with its pages."""
+    page, num_pages = 4, 37
+    lens, table, free = state(9, page, num_pages, 10, 40, 3)
+    run = Run(lens, table, free, page, num_pages)
+    for _ in range(12):
+        run.assign([1] * 9, in_place=True)
+    assert not run.free
+    run.lens[2] = 0
+    run.d_lens[2] = 0
+    run.release()
+    assert run.free
+    run.assign([1] * 9, lead=2, trail=3, in_place=True)
+
+
+def test_release_gives_back_in_any_order():
+    lens, table, free = state(60, 16, 5000, 900, 70, 9, held=5)
+    run = Run(lens, table, free, 16, 5000)
+    before = set(run.free)
+    run.release()
+    assert len(run.free) > len(before)
+    run.assign([17] * 60)
+    run.release()  # the lengths did not grow: the same pages come back
+    run.assign([17] * 60)
+
+
+def test_rows_of_no_request_and_empty_batches():
+    run = Run([3, 0], [[1, -1], [-1, -1]], {0, 2}, 4, 3)
+    slots, pos, _ = run.assign([0, 2], lead=4, trail=2)
+    assert slots.tolist() == [-1] * 4 + [0, 1] + [-1] * 2 and pos.tolist() == [0] * 4 + [0, 1] + [0] * 2
+    run.assign([0, 0])
+    s, p, n = pkc.assign_pages(run.d_table[:0], run.d_lens[:0], torch.zeros(1, dtype=I32, device="cuda"), 3, run.d_free, 4, 3, run.ws)
+    assert s.tolist() == [-1] * 3 and p.tolist() == [0] * 3 and n.numel() == 0
+    pkc.release_pages(run.d_table[:0], run.d_lens[:0], run.d_free, 4, 3, run.ws)
+    run.check(0)
+
+
+def test_served_in_order():
+    """The second request is too large for what is left; a third that needs no page is served, a fourth that does is not."""
+    run = Run([0, 0, 1, 0], [[-1] * 4, [-1] * 4, [9, -1, -1, -1], [-1] * 4], {3, 4, 5}, 4, 10)
+    run.assign([5, 8, 2, 1])
+    assert run.table[0][:2] == [3, 4] and run.free == {5}
+
+
+def test_bits_behind_the_pool_are_kept():
+    words = torch.full((1,), -1, dtype=I32, device="cuda")
+    ws, table = workspace(), torch.full((1, 40), -1, dtype=I32, device="cuda")
+    pkc.assign_pages(table, torch.zeros(1, dtype=I32, device="cuda"), torch.tensor([0, 11], dtype=I32, device="cuda"), 11, words, 1, 10, ws)
+    assert pkc.device_status(ws) == 8 and words.tolist() == [-1]  # ten pages, eleven asked for
+    pkc.assign_pages(table, torch.zeros(1, dtype=I32, device="cuda"), torch.tensor([0, 10], dtype=I32, device="cuda"), 10, words, 1, 10, ws)
+    assert pkc.device_status(ws) == 0 and words.tolist() == [-1024] and table[0, :10].tolist() == list(range(10))
+
+
+def test_what_cannot_be_served_is_left():
+    """A negative length, a table that is too narrow, a partly filled page that is not there."""
+    lens = torch.tensor([-1, 7, 5, 6, 2], dtype=I32, device="cuda")
+    table = torch.tensor([[0, 1], [2, 3], [4, -1], [5, 99], [6, -1]], dtype=I32, device="cuda")
+    free, ws = ref.pool_words({8, 9}, 12).cuda(), workspace()
+    indptr = torch.tensor([0, 1, 3, 4, 5, 8], dtype=I32, device="cuda")
+    slots, pos, out = pkc.assign_pages(table, lens, indptr, 8, free, 4, 12, ws)
+    assert pkc.device_status(ws) == 4
+    assert slots.tolist() == [-1, -1, -1, -1, -1, 26, 27, 32] and out.tolist() == [-1, 7, 5, 6, 5]
+    assert pos.tolist() == [-1, 7, 8, 5, 6, 2, 3, 4]
+    assert table.tolist() == [[0, 1], [2, 3], [4, -1], [5, 99], [6, 8]] and ref.pool_set(free, 12) == {9}
+
+
+@pytest.mark.parametrize("indptr,total", [([0, 3, 2], 4), ([-1, 1, 2], 2), ([0, 2, 5], 4)])
+def test_bad_ranges_serve_nobody(indptr, total):
+    lens, table = torch.tensor([1, 2], dtype=I32, device="cuda"), torch.tensor([[0, -1], [1, -1]], dtype=I32, device="cuda")
+    free, ws = ref.pool_words({2, 3}, 4).cuda(), workspace()
+    slots, pos, out = pkc.assign_pages(table, lens, torch.tensor(indptr, dtype=I32, device="cuda"), total, free, 4, 4, ws)
+    assert pkc.device_status(ws) == 7 and slots.tolist() == [-1] * total and out.tolist() == [1, 2]
+    assert table.tolist() == [[0, -1], [1, -1]] and ref.pool_set(free, 4) == {2, 3}
+
+
+def test_release_reports():
+    """A page that is free already, one held twice, one outside the pool, a negative length."""
+    table = torch.tensor([[0, 5, 5, 3], [1, 77, -1, 4], [6, 7, 8, 9]], dtype=I32, device="cuda")
+    lens, ws = torch.tensor([4, 4, -2], dtype=I32, device="cuda"), workspace()
+    free = ref.pool_words({3}, 12).cuda()
+    pkc.release_pages(table, lens, free, 4, 12, ws)
+    assert pkc.device_status(ws) in (4, 7)
+    assert table.tolist() == [[0, -1, -1, -1], [1, 77, -1, -1], [6, 7, 8, 9]]
+    assert ref.pool_set(free, 12) == {3, 4, 5}
+
+
+def test_graph_and_another_stream():
+    lens, table, free = state(20, 16, 3000, 300, 60, 4, held=2)
+    run = Run(lens, table, free, 16, 3000)
+    indptr = torch.arange(21, dtype=I32, device="cuda") * 33
+    args = (run.d_table, run.d_lens, indptr, 660, run.d_free, 16, 3000, run.ws)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    pkc.release_pages(run.d_table, run.d_lens, run.d_free, 16, 3000, run.ws, stream=side)
+    slots, pos, out = (torch.empty(660, dtype=torch.int64, device="cuda"), torch.empty(660, dtype=I32, device="cuda"), torch.empty(20, dtype=I32, device="cuda"))
+    side.wait_stream(torch.cuda.current_stream())
+    pkc.assign_pages(*args, slots=slots, positions=pos, seqlens_out=out, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    want = slots.clone(), pos.clone(), out.clone(), run.d_table.clone(), run.d_free.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pkc.release_pages(run.d_table, run.d_lens, run.d_free, 16, 3000, run.ws)
+        pkc.assign_pages(*args, slots=slots, positions=pos, seqlens_out=out)
+    for _ in range(3):
+        slots.fill_(-7)
+        g.replay()
+    for a, b in zip((slots, pos, out, run.d_table, run.d_free), want):
+        assert torch.equal(a, b)
+    ref.release(run.table, lens, run.free, 16)
+    ref.assign(run.table, lens, indptr.tolist(), 660, run.free, 16)
+    run.check(0)

@@ -1,12 +1,49 @@
-// Attention states of a chunk of new tokens per request over its paged cache.
+// Attention states of a chunk of new tokens per request over its paged cache,
+// on the 5th-generation tensor cores.
 //
 // Row i of request b's n rows stands at position p = len - n + i and attends to
 // the tokens t < len with t <= p (causal) and t > p - window:
 //   s_t = scale q.k_t,  LSE = log sum exp s_t,  O = sum exp(s_t - LSE) v_t.
-// One warp per (row, query head), a key at a time, four elements a lane.
+//
+// An item is 256 query rows of one KV head -- the G query heads of 256 / G
+// consecutive tokens -- against the KV tiles of 128 tokens in their reach.  Its
+// two halves A and B of 128 rows (the MMA's M) share every K and V tile:
+//   S_X = Q_X K_j^T              tcgen05.mma, A and B from shared memory
+//   P_X = exp2(S_X c - m_ref)    softmax warps, TMEM -> registers -> TMEM, 16 bits
+//   O_X += P_X V_j               tcgen05.mma, P_X read from TMEM
+// While one half is in its softmax the tensor cores work for the other: they are
+// issued PV_A(j - 1) QK_A(j) PV_B(j - 1) QK_B(j) .., each waiting only for the P
+// of its own half.  P takes the columns of the S it was made from; TMEM is S_A,
+// S_B, O_A, O_B, 128 columns each.  P never passes through shared memory, whose
+// bandwidth the MMA's operands need.
+// m_ref, a row's reference maximum, moves (and the row of O is rescaled, in
+// TMEM) only when a tile's maximum passes it by more than 2^8.
+//
+// Work split.  An item costs its KV tiles and kOver; all items are laid end to
+// end (request, KV head, row tile) and cut evenly over the blocks, one per SM.
+// So a block gets whole items but for its ends, few rows over a long cache are
+// split over the cache, and no order of execution matters.  A block works the
+// cut out for itself, from the lengths on the device: the sums over a request's
+// items have a closed form.  A piece of a cut item leaves a partial state; the
+// block that finishes last among the item's pieces (bits in the status block
+// tell) merges them, always in the order of the cache.
+//
+// Warps: 0-3 softmax of A, 4-7 of B (a row per thread, epilogue and merge too),
+// 8 MMA issue, 9 K and V copies, 10 scheduler, 11 Q copies.  K and V tiles take
+// turns in one ring; a tile is one TMA box per page and 64 dims (pages that are
+// not a power of two: boxes of their largest power-of-two part).  All waits are
+// bounded (2 s) and set PKC_ERR_TIMEOUT when they run out.
+//
+// Values that a row does not attend to meet P = 0, and 0 times an infinity or a
+// NaN would be NaN: slots behind the length are zeroed in the V tile, and a row
+// whose O is not finite is computed again key by key (slow_row), so such a value
+// reaches exactly the rows that attend to it, at no cost where there is none.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cfloat>
+#include <type_traits>
 
 #include "pkc_device.cuh"
 #include "pkc_internal.h"
@@ -14,39 +51,152 @@
 namespace pkc {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kHalf = 128;               // rows of a half (MMA M)
+constexpr int kRows = 2 * kHalf;         // rows of an item
+constexpr int kKv = 128;                 // tokens of a KV tile
+constexpr int kSub = 16384;              // 128 rows x 64 elements, 128-byte swizzle
+constexpr int kTileBytes = 2 * kSub;
+constexpr int kStages = 5;               // K and V tiles in flight
+constexpr int kItems = 4;                // items the scheduler runs ahead
+constexpr int kThreads = 384;
+constexpr int kMmaWarp = 8, kKvWarp = 9, kSchedWarp = 10, kQWarp = 11;
+constexpr int kMaxBlocks = 160;
+constexpr int kOver = 2;                 // an item's cost next to its tiles
+constexpr int kMinCost = 4;              // least cost of a block
+constexpr float kMoveLog2 = 8.f;
 
+struct Item {
+  int b;                 // request; -1: no more items
+  int kvh, q_row, n_tok; // KV head, first row of q, tokens
+  int pos0, len;         // position of the first token, cached tokens
+  int t0, t1;            // KV tiles of the piece
+  int lo[2], hi[2];      // those of half A, B (lo == hi: none)
+  int c0, c1;            // blocks with pieces of the item (c0 == c1: whole)
+};
+
+struct __align__(8) Barriers {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t kv_full[kStages], kv_empty[kStages];
+  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+  uint64_t it_full[kItems], it_empty[kItems];
+  uint64_t part_done, merge_go;
+  uint64_t drain;
+  uint32_t tmem_base;
+  int abort;
+  int merge;
+};
+
+constexpr int kKvOffset = 2 * kTileBytes;
+constexpr int kItemOffset = kKvOffset + kStages * kTileBytes;
+constexpr int kBarOffset = kItemOffset + kItems * 64;
+constexpr int kSmemBytes = kBarOffset + 512;
+static_assert(sizeof(Item) <= 64 && sizeof(Barriers) <= 512 && kSmemBytes <= 227 * 1024, "shared memory");
+
+// ---------------------------------------------------------------- schedule
+
+struct Request {
+  int r0, n, len;
+};
+
+// sum over i < m of floor(max(a + i s, 0) / 128), s a power of two
+PKC_HD inline int64_t sum_floor(int64_t a, int s, int64_t m) {
+  int64_t i0 = a >= 0 ? 0 : (-a + s - 1) / s;
+  if (i0 >= m) return 0;
+  a += i0 * s;
+  m -= i0;
+  if (s >= 128) return m * (a / 128) + (s / 128) * (m * (m - 1) / 2);
+  const int per = 128 / s;
+  int64_t sum = 0;
+  for (int r = 0; r < per; ++r) {
+    const int64_t u = (m - r + per - 1) / per;  // r, r + per, ..
+    if (m > r) sum += u * ((a + r * s) / 128) + u * (u - 1) / 2;
+  }
+  return sum;
+}
+
+PKC_HD inline int n_items(const ChunkParams& p, const Request& q) {
+  const int s = kRows / p.g;
+  return (q.n + s - 1) / s;
+}
+
+// Cost of the first m items of a request's KV head.
+PKC_HD inline int64_t cost_of(const ChunkParams& p, const Request& q, int m) {
+  const int s = kRows / p.g, nt = n_items(p, q);
+  const int64_t pos = (int64_t)q.len - q.n;
+  const int64_t last = ((int64_t)q.len + kKv - 1) / kKv;
+  int64_t sum = (int64_t)m * kOver;
+  if (p.causal) sum += sum_floor(pos + s + kKv - 1, s, m < nt ? m : nt - 1) + (m == nt ? last : 0);
+  else sum += m * last;
+  if (p.window) sum -= sum_floor(pos - p.window + 1, s, m);
+  return sum;
+}
+
+// KV tiles [lo, hi) in the reach of tokens j0 .. j1 - 1 of a request.
+PKC_HD inline void reach(const ChunkParams& p, const Request& q, int j0, int j1, int& lo, int& hi) {
+  const int64_t pos = (int64_t)q.len - q.n;
+  const int64_t end = p.causal ? pos + j1 : q.len, begin = p.window ? pos + j0 - p.window + 1 : 0;
+  hi = end > 0 ? (int)((end + kKv - 1) / kKv) : 0;
+  lo = begin > 0 ? (int)(begin / kKv) : 0;
+  if (lo > hi) lo = hi;
+}
+
+// ---------------------------------------------------------------- helpers
+
+// D[tmem] (+)= A[tmem] * B[smem]: A 16-bit, two elements a column.
+__device__ __forceinline__ void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.u32 p, %4, 0;"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Registers per thread from here on; the warps of a warpgroup call it together.
+template <int kRegs> __device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs> __device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+__device__ __forceinline__ void fence_sc() { asm volatile("fence.sc.gpu;" ::: "memory"); }
+
+// 32 columns of row `o` (float32, already normalised) to column `col` of output row `row`.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) chunk_kernel(const ChunkParams p) {
+__device__ __forceinline__ void store_out(const ChunkParams& p, int64_t row, int col, const float* o, int n) {
+  if (p.out_dtype == PKC_F32) {
+    float* dst = static_cast<float*>(p.o) + row * PKC_HEAD_DIM + col;
+#pragma unroll
+    for (int i = 0; i < n; i += 4) *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+  } else {
+    T* dst = static_cast<T*>(p.o) + row * PKC_HEAD_DIM + col;
+#pragma unroll
+    for (int i = 0; i < n; i += 8)
+      *reinterpret_cast<uint4*>(dst + i) =
+          make_uint4(Elem<T>::from_f2(o[i], o[i + 1]), Elem<T>::from_f2(o[i + 2], o[i + 3]),
+                     Elem<T>::from_f2(o[i + 4], o[i + 5]), Elem<T>::from_f2(o[i + 6], o[i + 7]));
+  }
+}
+
+// Partial states: part_o[slot][column / 4][row][4], part_lse[slot][row] (base 2).
+__device__ __forceinline__ float* part_row(const ChunkParams& p, int slot, int chunk, int row) {
+  return p.part_o + (((int64_t)slot * 32 + chunk) * kRows + row) * 4;
+}
+__device__ __forceinline__ int slot_of(int c, int c0) { return 2 * c + (c == c0 ? 1 : 0); }
+
+// One row again, by one warp, key by key over tokens [lo, hi): for rows whose O
+// is not finite, where a value that the row does not attend to may have met
+// P = 0.  Four elements a lane; returns the row's state.
+template <typename T>
+__device__ __noinline__ void slow_row(const ChunkParams& p, int b, int kvh, int64_t q_index, int lo, int hi, float (&o)[4],
+                                      float& lse2) {
   const int lane = threadIdx.x & 31;
-  const int64_t u = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
-  const int64_t row = u / p.hq;
-  const int h = (int)(u % p.hq);
-  if (blockIdx.x == 0)
-    for (int b = threadIdx.x; b < p.batch; b += kThreads)
-      if (p.q_indptr[b] < 0 || p.q_indptr[b + 1] < p.q_indptr[b] || p.q_indptr[b + 1] > p.total_q)
-        report(p.status, PKC_ERR_PLAN);
-  if (row >= p.total_q) return;
-  // the request of the row
-  int lo = 0, hi = p.batch;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (p.q_indptr[mid] <= row) lo = mid; else hi = mid;
-  }
-  const int b = lo, r0 = p.q_indptr[b], r1 = p.q_indptr[b + 1], len = p.cache_seqlens[b];
-  if (row < r0 || row >= r1) return;
-  if (r0 < 0 || r1 > p.total_q || len < 0) {
-    if (lane == 0) report(p.status, PKC_ERR_PLAN);
-    return;
-  }
-  const int64_t pos = (int64_t)len - (r1 - row);
-  const int64_t t1 = p.causal ? min((int64_t)len, pos + 1) : len;
-  const int64_t t0 = p.window ? max((int64_t)0, pos - p.window + 1) : 0;
-  const int kvh = h / p.g;
-  const uint2 qw = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.q) + u * PKC_HEAD_DIM + 4 * lane);
+  const uint2 qw = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.q) + q_index * PKC_HEAD_DIM + 4 * lane);
   const float2 q0 = Elem<T>::to_f2(qw.x), q1 = Elem<T>::to_f2(qw.y);
-  float m = neg_inf(), l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int64_t t = t0; t < t1; ++t) {
+  float m = neg_inf(), l = 0.f;
+  o[0] = o[1] = o[2] = o[3] = 0.f;
+  for (int t = lo; t < hi; ++t) {
     const int64_t pi = t / p.page_size;
     const int page = pi < p.bt_stride ? p.block_table[(int64_t)b * p.bt_stride + pi] : -1;
     uint2 kw = make_uint2(0, 0), vw = make_uint2(0, 0);
@@ -54,8 +204,6 @@ __global__ void __launch_bounds__(kThreads) chunk_kernel(const ChunkParams p) {
       const int64_t at = (((int64_t)page * p.page_size + t % p.page_size) * p.hkv + kvh) * PKC_HEAD_DIM + 4 * lane;
       kw = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.k_cache) + at);
       vw = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.v_cache) + at);
-    } else if (lane == 0) {
-      report(p.status, PKC_ERR_BLOCK_TABLE);
     }
     const float2 k0 = Elem<T>::to_f2(kw.x), k1 = Elem<T>::to_f2(kw.y);
     float s = q0.x * k0.x + q0.y * k0.y + q1.x * k1.x + q1.y * k1.y;
@@ -72,28 +220,660 @@ __global__ void __launch_bounds__(kThreads) chunk_kernel(const ChunkParams p) {
     o[2] = o[2] * w + e * v1.x;
     o[3] = o[3] * w + e * v1.y;
   }
-  const bool any = t1 > t0;
-  const float inv = any ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = any ? o[i] * inv : 0.f;
-  if (p.out_dtype == PKC_F32)
-    *reinterpret_cast<float4*>(static_cast<float*>(p.o) + u * PKC_HEAD_DIM + 4 * lane) =
-        make_float4(o[0], o[1], o[2], o[3]);
-  else
-    *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + u * PKC_HEAD_DIM + 4 * lane) =
-        make_uint2(Elem<T>::from_f2(o[0], o[1]), Elem<T>::from_f2(o[2], o[3]));
-  if (lane == 0) p.lse[u] = any ? (m + lg2(l)) * kLn2 : neg_inf();
+  for (int i = 0; i < 4; ++i) o[i] = o[i] * inv;
+  lse2 = l == 0.f ? neg_inf() : m + lg2(l);
+}
+
+// The merge of an item's pieces by the eight softmax warps: a warp takes 32 rows
+// and 16 columns at a time.
+template <typename T>
+__device__ __forceinline__ void merge_item(const ChunkParams& p, const Item& it, int warp, int lane) {
+  const int rows = it.n_tok * p.g, groups = (rows + 31) / 32;
+  for (int u = warp; u < 8 * groups; u += 8) {
+    const int row = (u >> 3) * 32 + lane, chunk = (u & 7) * 4;
+    float m = neg_inf();
+    for (int c = it.c0; c <= it.c1; ++c) m = fmaxf(m, __ldcg(p.part_lse + slot_of(c, it.c0) * kRows + row));
+    const float ref = m == neg_inf() ? 0.f : m;
+    float l = 0.f, o[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] = 0.f;
+#pragma unroll 2
+    for (int c = it.c0; c <= it.c1; ++c) {
+      const int slot = slot_of(c, it.c0);
+      const float w = ex2(__ldcg(p.part_lse + slot * kRows + row) - ref);
+      l += w;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float4 x = __ldcg(reinterpret_cast<const float4*>(part_row(p, slot, chunk + k, row)));
+        o[4 * k] += w * x.x;
+        o[4 * k + 1] += w * x.y;
+        o[4 * k + 2] += w * x.z;
+        o[4 * k + 3] += w * x.w;
+      }
+    }
+    if (row >= rows) continue;
+    const float inv = m == neg_inf() ? 0.f : 1.f / l;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) o[i] *= inv;
+    const int64_t out = ((int64_t)it.q_row + row / p.g) * p.hq + it.kvh * p.g + row % p.g;
+    store_out<T>(p, out, 4 * chunk, o, 16);
+    if (chunk == 0) p.lse[out] = m == neg_inf() ? neg_inf() : (m + lg2(l)) * kLn2;
+  }
+}
+
+// ---------------------------------------------------------------- kernel
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1)
+    chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ ChunkParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if ((smem_u32(smem) & 1023) != 0) {  // uniform: no thread has started yet
+    if (threadIdx.x == 0) report(p.status, PKC_ERR_UNSUPPORTED);
+    return;
+  }
+  const uint32_t s_q = smem_u32(smem), s_kv = s_q + kKvOffset;
+  Barriers* bars = reinterpret_cast<Barriers*>(smem + kBarOffset);
+  volatile int* abort = &bars->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto bar = [&](uint64_t& b) { return smem_u32(&b); };
+  if (threadIdx.x == 0) {
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(bar(bars->q_full[x]), 1);
+      mbar_init(bar(bars->q_empty[x]), 1);
+      mbar_init(bar(bars->s_full[x]), 1);
+      mbar_init(bar(bars->p_full[x]), 4);
+      mbar_init(bar(bars->o_full[x]), 1);
+      mbar_init(bar(bars->o_free[x]), 4);
+    }
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(bar(bars->kv_full[s]), 1);
+      mbar_init(bar(bars->kv_empty[s]), 1);
+    }
+    for (int s = 0; s < kItems; ++s) {
+      mbar_init(bar(bars->it_full[s]), 1);
+      mbar_init(bar(bars->it_empty[s]), 11);  // softmax warps, MMA, K/V and Q copies
+    }
+    mbar_init(bar(bars->part_done), 8);
+    mbar_init(bar(bars->merge_go), 1);
+    mbar_init(bar(bars->drain), 1);
+    bars->abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kKvWarp && lane == 0) {
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(smem_u32(&bars->tmem_base), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  // The k-th item of the block, by a whole warp (lane 0 waits and gives the
+  // place back); false at the end.
+  auto next_item = [&](int k, Item& it) -> bool {
+    bool got = true;
+    if (lane == 0) got = mbar_wait(bar(bars->it_full[k % kItems]), (k / kItems) & 1, abort, p.status);
+    got = __shfl_sync(0xffffffffu, got, 0);
+    __syncwarp();
+    if (!got) return false;
+    const int* src = reinterpret_cast<const int*>(smem + kItemOffset + (k % kItems) * 64);
+    int* dst = reinterpret_cast<int*>(&it);
+#pragma unroll
+    for (int i = 0; i < (int)(sizeof(Item) / 4); ++i) dst[i] = src[i];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(bars->it_empty[k % kItems]));
+    return it.b >= 0;
+  };
+
+  // 384 threads start with 168 registers each (64,512): the softmax warps take
+  // 208 and leave the others 80 (63,488 together).
+  if (warp >= kMmaWarp) regs_down<80>();
+  if (warp == kSchedWarp) {
+    // ---------------- scheduler ----------------
+    const int s = kRows / p.g;
+    auto load = [&](int b) -> Request {  // an empty request where there is nothing to do
+      Request q = {0, 0, 0};
+      if (b < p.batch) {
+        const int r0 = p.q_indptr[b], r1 = p.q_indptr[b + 1], len = p.cache_seqlens[b];
+        if (r0 < 0 || r1 < r0 || r1 > p.total_q || (len < 0 && r1 > r0)) {
+          if (blockIdx.x == 0) report(p.status, PKC_ERR_PLAN);
+        } else if (r1 > r0) {
+          q = {r0, r1 - r0, len};
+        }
+      }
+      return q;
+    };
+    int64_t total = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+      const Request q = load(b0 + lane);
+      if (q.n) total += cost_of(p, q, n_items(p, q));
+    }
+#pragma unroll
+    for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+    total *= p.hkv;
+    const int n_blocks = (int)max((int64_t)1, min((int64_t)gridDim.x, total / kMinCost));
+    const int c = (int)blockIdx.x;
+    auto begin_of = [&](int i) { return (int64_t)i * total / n_blocks; };
+    auto block_of = [&](int64_t x) { return (int)(((x + 1) * n_blocks - 1) / total); };
+    const int64_t s0 = c < n_blocks ? begin_of(c) : total, s1 = c < n_blocks ? begin_of(c + 1) : total;
+
+    int k = 0;
+    bool ok = true;
+    auto publish = [&](const Item& it) {
+      if (lane == 0 && k >= kItems) ok = mbar_wait(bar(bars->it_empty[k % kItems]), ((k / kItems) & 1) ^ 1, abort, p.status);
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (ok && lane == 0) {
+        *reinterpret_cast<Item*>(smem + kItemOffset + (k % kItems) * 64) = it;
+        mbar_arrive(bar(bars->it_full[k % kItems]));
+      }
+      ++k;
+    };
+    // The request that holds s0, 32 at a time; then request by request.
+    int64_t base = 0;  // cost of the requests before b0
+    for (int b0 = 0; ok && b0 < p.batch && base < s1; b0 += 32) {
+      const Request mine = load(b0 + lane);
+      const int64_t per_head = mine.n ? cost_of(p, mine, n_items(p, mine)) : 0;
+      int64_t before = per_head * p.hkv;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, before, d);
+        if (lane >= d) before += y;
+      }
+      const int64_t all = __shfl_sync(0xffffffffu, before, 31);
+      before = base + before - per_head * p.hkv;
+      uint32_t todo = __ballot_sync(0xffffffffu, mine.n > 0 && before < s1 && before + per_head * p.hkv > s0);
+      for (; ok && todo; todo &= todo - 1) {
+        const int j = __ffs(todo) - 1, b = b0 + j;
+        const Request q = {__shfl_sync(0xffffffffu, mine.r0, j), __shfl_sync(0xffffffffu, mine.n, j),
+                           __shfl_sync(0xffffffffu, mine.len, j)};
+        const int64_t ph = __shfl_sync(0xffffffffu, per_head, j), rb = __shfl_sync(0xffffffffu, before, j);
+        const int nt = n_items(p, q);
+        int h = 0, i = 0;
+        int64_t x0 = rb;  // where item (h, i) begins
+        if (s0 > rb) {
+          h = (int)((s0 - rb) / ph);
+          const int64_t rel = s0 - rb - h * ph;
+          int lo = 0, hi = nt;  // the last i with cost_of(i) <= rel
+          while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (cost_of(p, q, mid) <= rel) lo = mid; else hi = mid;
+          }
+          i = lo;
+          x0 = rb + h * ph + cost_of(p, q, i);
+        }
+        for (; ok && h < p.hkv && x0 < s1; i = 0, ++h) {
+          for (; ok && i < nt && x0 < s1; ++i) {
+            const int j0 = i * s, n_tok = min(s, q.n - j0);
+            int lo, hi;
+            reach(p, q, j0, j0 + n_tok, lo, hi);
+            const int64_t first = x0 + kOver, end = first + (hi - lo);  // its tiles lie at first .. end - 1
+            Item it;
+            it.b = b; it.kvh = h; it.q_row = q.r0 + j0; it.n_tok = n_tok;
+            it.pos0 = (int)((int64_t)q.len - q.n + j0); it.len = q.len;
+            it.t0 = lo + (int)max((int64_t)0, s0 - first);
+            it.t1 = lo + (int)max((int64_t)0, min(s1, end) - first);
+            it.c0 = it.c1 = c;
+            if (hi > lo) {
+              it.c0 = block_of(first);
+              it.c1 = block_of(end - 1);
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int a = x * (kHalf / p.g), e = min(n_tok, (x + 1) * (kHalf / p.g));
+              it.lo[x] = it.hi[x] = it.t0;
+              if (e > a) {
+                int l, r;
+                reach(p, q, j0 + a, j0 + e, l, r);
+                it.lo[x] = max(l, it.t0);
+                it.hi[x] = max(it.lo[x], min(r, it.t1));
+              }
+            }
+            // a piece with tiles, or the one place of an item without any
+            if (it.t0 < it.t1 || (hi == lo && x0 >= s0)) publish(it);
+            x0 = end;
+          }
+        }
+      }
+      base += all;
+    }
+    if (ok) {
+      Item it;
+      it.b = -1;
+      publish(it);
+    }
+  } else if (warp == kQWarp) {
+    // ---------------- Q copies ----------------
+    const uint64_t pol = l2_policy_evict_first();
+    int n[2] = {0, 0};
+    Item it = {};
+    bool ok = true;
+    for (int k = 0; ok && next_item(k, it); ++k) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (it.lo[x] == it.hi[x]) continue;
+        if (lane == 0) {
+          if (n[x] > 0) ok = mbar_wait(bar(bars->q_empty[x]), (n[x] - 1) & 1, abort, p.status);
+          if (ok) {
+            const int row = it.q_row + x * (kHalf / p.g);
+            mbar_arrive_expect_tx(bar(bars->q_full[x]), kTileBytes);
+            tma_load_3d(s_q + x * kTileBytes, &tm_q, bar(bars->q_full[x]), 0, it.kvh * p.g, row, pol);
+            tma_load_3d(s_q + x * kTileBytes + kSub, &tm_q, bar(bars->q_full[x]), 64, it.kvh * p.g, row, pol);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        ++n[x];
+      }
+    }
+    if (*abort && lane == 0) {  // the copies already issued land before the block exits
+      volatile int no_abort = 0;
+      for (int x = 0; x < 2; ++x)
+        if (n[x] > 0) mbar_wait(bar(bars->q_full[x]), (n[x] - 1) & 1, &no_abort, p.status);
+    }
+  } else if (warp == kKvWarp) {
+    // ---------------- K and V copies ----------------
+    const uint64_t pol = l2_policy_evict_last();
+    const int bs = p.box_tokens, boxes = 2 * (kKv / bs);  // box c: tokens (c / 2) bs .. of the tile, dims 64 (c % 2) ..
+    const int no_page = (int)max((int64_t)1, p.num_pages);   // outside the pool: read as zeros
+    int g = 0;
+    Item it = {};
+    bool ok = true;
+    for (int k = 0; ok && next_item(k, it); ++k) {
+      const int32_t* table = p.block_table + (int64_t)it.b * p.bt_stride;
+      // Page of the lane's box of tile t (the first 32 boxes), loaded a tile ahead.
+      auto page_of = [&](int t, int c) -> int {
+        const int token = t * kKv + (c >> 1) * bs;
+        if (t >= it.t1 || c >= boxes || token >= it.len) return no_page;
+        const int64_t pi = token / p.page_size;
+        return pi < p.bt_stride ? table[pi] : -1;
+      };
+      int ahead = page_of(it.t0, lane);
+      for (int t = it.t0; ok && t < it.t1; ++t) {
+        int page = ahead;
+        ahead = page_of(t + 1, lane);
+        for (int kv = 0; ok && kv < 2; ++kv, ++g) {
+          const int st = g % kStages;
+          if (lane == 0) {
+            if (g >= kStages) ok = mbar_wait(bar(bars->kv_empty[st]), ((g / kStages) & 1) ^ 1, abort, p.status);
+            if (ok) mbar_arrive_expect_tx(bar(bars->kv_full[st]), kTileBytes);
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          const void* tmap = kv ? (const void*)&tm_v : (const void*)&tm_k;
+          for (int c = lane; c < boxes; c += 32) {
+            const int r = (c >> 1) * bs;
+            int pg = c == lane ? page : page_of(t, c);
+            if (t * kKv + r < it.len && (pg < 0 || pg >= p.num_pages)) {
+              report(p.status, PKC_ERR_BLOCK_TABLE);
+              pg = no_page;
+            }
+            tma_load_4d(s_kv + st * kTileBytes + (c & 1) * kSub + r * 128, tmap, bar(bars->kv_full[st]), (c & 1) * 64, it.kvh,
+                        (t * kKv + r) % p.page_size, pg, pol);
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (*abort && lane == 0) {
+      volatile int no_abort = 0;
+      for (int j = g > kStages ? g - kStages : 0; j < g; ++j)
+        mbar_wait(bar(bars->kv_full[j % kStages]), (j / kStages) & 1, &no_abort, p.status);
+    }
+  } else if (warp == kMmaWarp) {
+    // ---------------- MMA issue ----------------
+    constexpr uint32_t kBf16 = std::is_same<T, __half>::value ? 0 : 1;
+    constexpr uint32_t idesc_qk = idesc_f16(128, 128, kBf16, 0, 0);
+    constexpr uint32_t idesc_pv = idesc_f16(128, 128, kBf16, 0, 1);
+    int g = 0;                                // ring place of the next K tile
+    int n_q[2] = {0, 0}, n_s[2] = {0, 0};     // Q tiles used, P tiles used
+    int n_o[2] = {0, 0};                      // O accumulators begun
+    bool pend[2] = {false, false};            // S of the tile before is in its softmax
+    bool first[2] = {false, false}, last[2] = {false, false};
+    int v_place = -1;                         // ring place of the pending V tile
+    Item it = {};
+    bool ok = true;
+    // P V of a half's pending tile.
+    auto pv = [&](int x) -> bool {
+      if (!pend[x]) return true;
+      pend[x] = false;
+      const int sv = v_place % kStages;
+      if (!mbar_wait(bar(bars->p_full[x]), n_s[x] & 1, abort, p.status) ||
+          !mbar_wait(bar(bars->kv_full[sv]), (v_place / kStages) & 1, abort, p.status))
+        return false;
+      ++n_s[x];
+      if (first[x]) {  // it overwrites O: the one before has been read out
+        if (n_o[x] > 0 && !mbar_wait(bar(bars->o_free[x]), (n_o[x] - 1) & 1, abort, p.status)) return false;
+        ++n_o[x];
+      }
+      tc_fence_after();
+      const uint32_t vb = s_kv + sv * kTileBytes;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        tc_mma_f16_ta(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, smem_desc_sw128(vb + kk * 2048, kSub, 1024), idesc_pv,
+                      (!first[x] || kk > 0) ? 1u : 0u);
+      if (last[x]) tc_commit(bar(bars->o_full[x]));
+      return true;
+    };
+    auto qk = [&](int x, int t) -> bool {
+      if (t < it.lo[x] || t >= it.hi[x]) return true;
+      const int sk = g % kStages;
+      if (!mbar_wait(bar(bars->kv_full[sk]), (g / kStages) & 1, abort, p.status)) return false;
+      first[x] = t == it.lo[x];
+      last[x] = t == it.hi[x] - 1;
+      if (first[x] && !mbar_wait(bar(bars->q_full[x]), n_q[x] & 1, abort, p.status)) return false;
+      tc_fence_after();
+      const uint32_t qb = s_q + x * kTileBytes, kb = s_kv + sk * kTileBytes;
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        const uint32_t off = (kk >> 2) * kSub + (kk & 3) * 32;
+        tc_mma_f16(tmem + x * 128, smem_desc_sw128(qb + off, 16, 1024), smem_desc_sw128(kb + off, 16, 1024), idesc_qk, kk > 0);
+      }
+      tc_commit(bar(bars->s_full[x]));
+      if (last[x]) {
+        tc_commit(bar(bars->q_empty[x]));
+        ++n_q[x];
+      }
+      pend[x] = true;
+      return true;
+    };
+    for (int k = 0; ok && next_item(k, it); ++k) {
+      if (lane == 0) {
+        for (int t = it.t0; ok && t < it.t1; ++t, g += 2) {
+          ok = pv(0) && qk(0, t) && pv(1);
+          if (!ok) break;
+          if (v_place >= 0) tc_commit(bar(bars->kv_empty[v_place % kStages]));
+          ok = qk(1, t);
+          if (!ok) break;
+          tc_commit(bar(bars->kv_empty[g % kStages]));
+          v_place = g + 1;
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+    }
+    if (lane == 0) {
+      if (ok && !*abort) ok = pv(0) && pv(1);
+      // Every MMA issued above completes before TMEM is released.
+      tc_commit(bar(bars->drain));
+      volatile int no_abort = 0;
+      mbar_wait(bar(bars->drain), 0, &no_abort, p.status);
+    }
+    __syncwarp();
+  } else {
+    // ---------------- softmax, epilogue, merge: a row per thread ----------------
+    regs_up<208>();
+    const int x = warp >> 2, quad = warp & 3;
+    const int row = x * kHalf + quad * 32 + lane;  // of the item
+    const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
+    const uint32_t t_s = t_lane + x * 128, t_o = t_lane + 256 + x * 128;
+    const uint64_t c2 = pk2(p.scale_log2, p.scale_log2);
+    uint32_t* ready = reinterpret_cast<uint32_t*>(p.status) + PKC_CHUNK_READY;
+    int g = 0;  // ring place of the item's first K tile
+    int n_s = 0, n_o = 0, n_merge = 0;
+    Item it = {};
+    bool ok = true;
+    for (int k = 0; ok && next_item(k, it); ++k) {
+      const int pos = it.pos0 + row / p.g;
+      const bool valid = row < it.n_tok * p.g;
+      const int rhi = p.causal ? min(it.len, pos + 1) : it.len;
+      const int rlo = p.window ? (int)max((int64_t)0, (int64_t)pos - p.window + 1) : 0;
+      const int lo = x ? it.lo[1] : it.lo[0], hi = x ? it.hi[1] : it.hi[0];
+      float m_ref = neg_inf();
+      uint64_t l2a = 0ull, l2b = 0ull;
+      for (int t = lo; t < hi; ++t, ++n_s) {
+        const bool got = mbar_wait(bar(bars->s_full[x]), n_s & 1, abort, p.status);
+        if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t v[4][32];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tmem_ld_32x32b_x32(t_s + 32 * j, v[j]);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 4; ++j) reg_fence32(v[j]);
+        const int c_lo = rlo - t * kKv, c_hi = rhi - t * kKv;  // columns the row attends to
+        if (__any_sync(0xffffffffu, c_lo > 0 || c_hi < kKv)) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * j + i < c_lo || 32 * j + i >= c_hi) v[j][i] = 0xff800000u;
+        }
+        float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+#pragma unroll
+        for (int i = 0; i < 32; i += 2)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) mx[j] = max3(mx[j], __uint_as_float(v[j][i]), __uint_as_float(v[j][i + 1]));
+        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
+        if (__any_sync(0xffffffffu, top > m_ref + kMoveLog2)) {
+          const float now = fmaxf(m_ref, top);
+          const float f = m_ref == neg_inf() ? 0.f : ex2(m_ref - now);
+          const uint64_t f2 = pk2(f, f);
+          l2a = fmul2(l2a, f2);
+          l2b = fmul2(l2b, f2);
+          if (t > lo) {
+            // O holds the tiles before this one: S of this tile was committed behind their P V.
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+              uint32_t o[32];
+              tmem_ld_32x32b_x32(t_o + 32 * j, o);
+              tmem_ld_wait();
+              reg_fence32(o);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st_32x32b_x32(t_o + 32 * j, o);
+            }
+          }
+          m_ref = now;
+        }
+        const float neg = m_ref == neg_inf() ? 0.f : -m_ref;
+        const uint64_t n2 = pk2(neg, neg);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t pw[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            const int j = 2 * h + (i >> 4), e = 2 * (i & 15);
+            const float2 a = upk2(ffma2(pk2(__uint_as_float(v[j][e]), __uint_as_float(v[j][e + 1])), c2, n2));
+            const float p0 = ex2(a.x), p1 = ex2(a.y);
+            if (i & 1) l2b = fadd2(l2b, pk2(p0, p1));
+            else l2a = fadd2(l2a, pk2(p0, p1));
+            pw[i] = Elem<T>::from_f2(p0, p1);
+          }
+          tmem_st_32x32b_x32(t_s + 32 * h, pw);
+        }
+        if (const int live = it.len - t * kKv; live < kKv) {
+          // Slots behind the length may hold anything, even NaN: zero their V
+          // once the tile has landed (each half does, whichever MMA comes first).
+          const int place = g + 2 * (t - it.t0) + 1, sv = place % kStages;
+          const bool landed = mbar_wait(bar(bars->kv_full[sv]), (place / kStages) & 1, abort, p.status);
+          if (!__all_sync(0xffffffffu, landed)) { ok = false; break; }
+          const uint32_t vst = s_kv + sv * kTileBytes;
+          for (int c = quad * 32 + lane; c < (kKv - live) * 16; c += kHalf)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vst + ((c >> 3) & 1) * kSub + (live + (c >> 4)) * 128 +
+                                                                        (c & 7) * 16),
+                         "r"(0u)
+                         : "memory");
+          fence_proxy_async_smem();
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bars->p_full[x]));
+      }
+      if (!ok) break;
+      g += 2 * (it.t1 - it.t0);
+
+      // The row's state.
+      const bool whole = it.c0 == it.c1, mine = hi > lo;
+      const int slot = slot_of((int)blockIdx.x, it.c0);
+      const int k_lo = max(rlo, it.t0 * kKv), k_hi = min(rhi, it.t1 * kKv);  // tokens of the piece that the row attends to
+      const bool none = k_lo >= k_hi;
+      const int64_t out = ((int64_t)it.q_row + row / p.g) * p.hq + it.kvh * p.g + row % p.g;
+      float l;
+      {
+        const float2 a = upk2(l2a), b = upk2(l2b);
+        l = (a.x + a.y) + (b.x + b.y);
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const float lse2 = none || l == 0.f ? neg_inf() : m_ref + lg2(l);
+      if (mine) {
+        const bool got = mbar_wait(bar(bars->o_full[x]), n_o & 1, abort, p.status);
+        if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+        ++n_o;
+        tc_fence_after();
+      }
+      bool bad = false;
+#pragma unroll 1
+      for (int j = 0; j < 4; ++j) {
+        uint32_t v[32];
+        float o[32];
+        if (mine) {  // uniform over the half
+          tmem_ld_32x32b_x32(t_o + 32 * j, v);
+          tmem_ld_wait();
+          reg_fence32(v);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          o[i] = mine && !none ? __uint_as_float(v[i]) * inv : 0.f;
+          bad = bad || !(fabsf(o[i]) <= FLT_MAX);
+        }
+        if (!valid) continue;
+        if (whole) {
+          store_out<T>(p, out, 32 * j, o, 32);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            *reinterpret_cast<float4*>(part_row(p, slot, 8 * j + i, row)) =
+                make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+        }
+      }
+      if (valid) {
+        if (whole) p.lse[out] = lse2 * kLn2;
+        else p.part_lse[slot * kRows + row] = lse2;
+      }
+      if (mine) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bars->o_free[x]));
+      }
+      for (uint32_t todo = __ballot_sync(0xffffffffu, bad && valid); todo; todo &= todo - 1) {
+        const int j = __ffs(todo) - 1, r = x * kHalf + quad * 32 + j;
+        const int64_t at = __shfl_sync(0xffffffffu, out, j);
+        float o[4], again;
+        slow_row<T>(p, it.b, it.kvh, at, __shfl_sync(0xffffffffu, k_lo, j), __shfl_sync(0xffffffffu, k_hi, j), o, again);
+        if (!whole) {
+          *reinterpret_cast<float4*>(part_row(p, slot, lane, r)) = make_float4(o[0], o[1], o[2], o[3]);
+        } else if (p.out_dtype == PKC_F32) {
+          *reinterpret_cast<float4*>(static_cast<float*>(p.o) + at * PKC_HEAD_DIM + 4 * lane) =
+              make_float4(o[0], o[1], o[2], o[3]);
+        } else {
+          *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + at * PKC_HEAD_DIM + 4 * lane) =
+              make_uint2(Elem<T>::from_f2(o[0], o[1]), Elem<T>::from_f2(o[2], o[3]));
+        }
+        if (lane == 0) {
+          if (whole) p.lse[at] = again * kLn2;
+          else p.part_lse[slot * kRows + r] = again;
+        }
+      }
+
+      if (!whole) {
+        // The block whose piece is the item's last one to be there merges all.
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bars->part_done));
+        if (warp == 0) {
+          const bool done = mbar_wait(bar(bars->part_done), n_merge & 1, abort, p.status);
+          if (!__all_sync(0xffffffffu, done)) { ok = false; break; }
+          if (lane == 0) atomicOr(ready + (slot >> 5), 1u << (slot & 31));
+          __syncwarp();
+          fence_sc();  // each block sets its bit before it looks for the others'
+          bool there = true;
+          for (int c = it.c0 + lane; c <= it.c1; c += 32) {
+            const int s = slot_of(c, it.c0);
+            there = there && ((atomicOr(ready + (s >> 5), 0u) >> (s & 31)) & 1);
+          }
+          int win = 0;
+          if (__all_sync(0xffffffffu, there)) {
+            // Two blocks may see all bits set: the one that takes the first bit merges.
+            if (lane == 0) {
+              const int s = slot_of(it.c0, it.c0);
+              win = (atomicAnd(ready + (s >> 5), ~(1u << (s & 31))) >> (s & 31)) & 1;
+            }
+            win = __shfl_sync(0xffffffffu, win, 0);
+            if (win)
+              for (int c = it.c0 + 1 + lane; c <= it.c1; c += 32) {
+                const int s = slot_of(c, it.c0);
+                atomicAnd(ready + (s >> 5), ~(1u << (s & 31)));
+              }
+          }
+          __threadfence();
+          __syncwarp();
+          if (lane == 0) {
+            bars->merge = win;
+            mbar_arrive(bar(bars->merge_go));
+          }
+        }
+        const bool go = mbar_wait(bar(bars->merge_go), n_merge & 1, abort, p.status);
+        if (!__all_sync(0xffffffffu, go)) { ok = false; break; }
+        ++n_merge;
+        if (*(volatile int*)&bars->merge) {
+          __threadfence();
+          merge_item<T>(p, it, warp, lane);
+        }
+        __syncwarp();
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+}
+
+bool make_maps(const ChunkParams& p, int dtype, CUtensorMap& mq, CUtensorMap& mk, CUtensorMap& mv) {
+  const uint64_t row = PKC_HEAD_DIM * 2;
+  const uint64_t qd[3] = {(uint64_t)PKC_HEAD_DIM, (uint64_t)p.hq, (uint64_t)p.total_q};
+  const uint64_t qs[2] = {row, row * p.hq};
+  const uint32_t qb[3] = {64u, (uint32_t)p.g, (uint32_t)(kHalf / p.g)};
+  // (dim, head, slot, page) of the pool [num_pages][page_size][Hkv][128]
+  const uint64_t d[4] = {(uint64_t)PKC_HEAD_DIM, (uint64_t)p.hkv, (uint64_t)p.page_size,
+                         (uint64_t)std::max<int64_t>(1, p.num_pages)};
+  const uint64_t st[3] = {row, row * p.hkv, row * p.hkv * p.page_size};
+  const uint32_t box[4] = {64u, 1u, (uint32_t)p.box_tokens, 1u};
+  return encode_tiled_map(&mq, p.q, dtype, 3, qd, qs, qb, true) &&
+         encode_tiled_map(&mk, p.k_cache, dtype, 4, d, st, box, true) &&
+         encode_tiled_map(&mv, p.v_cache, dtype, 4, d, st, box, true);
+}
+
+template <typename T>
+int launch_t(const ChunkParams& p, const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
+  static std::atomic<uint64_t> raised{0};
+  if (const int e = raise_smem_limit((const void*)chunk_kernel<T>, kSmemBytes, raised)) return e;
+  chunk_kernel<T><<<std::min(num_sms(), kMaxBlocks), kThreads, kSmemBytes, st>>>(mq, mk, mv, p);
+  return (int)cudaGetLastError();
 }
 
 }  // namespace
 
-size_t chunk_partial_bytes() { return 256; }
+size_t chunk_partial_bytes() { return (size_t)2 * kMaxBlocks * kRows * (PKC_HEAD_DIM + 1) * 4; }
 
-int launch_paged_chunk(const ChunkParams& p, int dtype, void* stream) {
-  const int64_t blocks = ((int64_t)p.total_q * p.hq + kThreads / 32 - 1) / (kThreads / 32);
-  if (dtype == PKC_BF16) chunk_kernel<__nv_bfloat16><<<(unsigned)blocks, kThreads, 0, (cudaStream_t)stream>>>(p);
-  else chunk_kernel<__half><<<(unsigned)blocks, kThreads, 0, (cudaStream_t)stream>>>(p);
-  return (int)cudaGetLastError();
+int launch_paged_chunk(const ChunkParams& params, int dtype, void* stream) {
+  ChunkParams p = params;
+  p.part_lse = p.part_o + (size_t)2 * kMaxBlocks * kRows * PKC_HEAD_DIM;
+  p.scale_log2 = std::max(p.scale_log2, FLT_MIN);  // a scale of 0 must not meet a masked score's infinity
+  for (p.box_tokens = 1; p.box_tokens < kKv && p.page_size % (2 * p.box_tokens) == 0;) p.box_tokens *= 2;
+  CUtensorMap mq, mk, mv;
+  if (!make_maps(p, dtype, mq, mk, mv)) return -1;
+  return dtype == PKC_BF16 ? launch_t<__nv_bfloat16>(p, mq, mk, mv, (cudaStream_t)stream)
+                           : launch_t<__half>(p, mq, mk, mv, (cudaStream_t)stream);
 }
 
 }  // namespace pkc

@@ -118,6 +118,11 @@ __device__ __forceinline__ uint64_t fmul2(uint64_t a, uint64_t b) {
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 // Two 16-bit elements packed in a 32-bit word -> an fp32 pair.
 template <typename T> __device__ __forceinline__ uint64_t widen2(uint32_t x);
 template <> __device__ __forceinline__ uint64_t widen2<__nv_bfloat16>(uint32_t x) {

@@ -14,10 +14,12 @@
 // word (pkc_device_status), words 16-17 the dynamic decode queue's counters,
 // words 18-19 the mx4 append's count of finished blocks and its flag for a
 // missing page, words 20-21 the same of the eviction's compact, word 32 the
-// result of pkc_selftest_wait_timeout.
+// result of pkc_selftest_wait_timeout, words 40-49 the chunk attention's bits
+// for partial states that are there.
 #define PKC_STATUS_BYTES 256
 #define PKC_APPEND_COUNTER 18
 #define PKC_COMPACT_COUNTER 20
+#define PKC_CHUNK_READY 40
 // Limits of the calls over the pool of free pages (pages.cu keeps the
 // requests' offsets and the pool's counts in shared memory).
 #define PKC_PAGES_MAX_BATCH 16384
@@ -356,6 +358,7 @@ struct ChunkParams {
   int64_t bt_stride, num_pages;
   int total_q, batch, hq, hkv, g, page_size;
   int causal, window;        // window 0: none
+  int box_tokens;            // set by the launcher: tokens of a copy, a power of two dividing page_size
   float scale_log2;
   void* o;
   float* lse;

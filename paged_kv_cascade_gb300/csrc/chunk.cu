@@ -11,9 +11,9 @@
 //   S_X = Q_X K_j^T              tcgen05.mma, A and B from shared memory
 //   P_X = exp2(S_X c - m_ref)    softmax warps, TMEM -> registers -> TMEM, 16 bits
 //   O_X += P_X V_j               tcgen05.mma, P_X read from TMEM
-// While one half is in its softmax the tensor cores work for the other: they are
-// issued PV_A(j - 1) QK_A(j) PV_B(j - 1) QK_B(j) .., each waiting only for the P
-// of its own half.  P takes the columns of the S it was made from; TMEM is S_A,
+// While one half is in its softmax the tensor cores work for the other: each half
+// has a warp that issues its P V of tile j - 1 and Q K of tile j as soon as its own
+// P is there.  P takes the columns of the S it was made from; TMEM is S_A,
 // S_B, O_A, O_B, 128 columns each.  P never passes through shared memory, whose
 // bandwidth the MMA's operands need.
 // m_ref, a row's reference maximum, moves (and the row of O is rescaled, in
@@ -29,10 +29,12 @@
 // tell) merges them, always in the order of the cache.
 //
 // Warps: 0-3 softmax of A, 4-7 of B (a row per thread, epilogue and merge too),
-// 8 MMA issue, 9 K and V copies, 10 scheduler, 11 Q copies.  K and V tiles take
-// turns in one ring; a tile is one TMA box per page and 64 dims (pages that are
-// not a power of two: boxes of their largest power-of-two part).  All waits are
-// bounded (2 s) and set PKC_ERR_TIMEOUT when they run out.
+// 8 and 9 MMA issue for A and B, 10 K copies, 11 V copies, 12 scheduler, 13 Q
+// copies.  K and V tiles take turns in one ring; a tile is one TMA box per page
+// and 64 dims (pages that are not a power of two: boxes of their largest
+// power-of-two part).  The lanes of a warp issue their boxes one after another,
+// some 50 cycles each, so pages of 16 tokens need a warp for K and one for V.
+// All waits are bounded (2 s) and set PKC_ERR_TIMEOUT when they run out.
 //
 // Values that a row does not attend to meet P = 0, and 0 times an infinity or a
 // NaN would be NaN: slots behind the length are zeroed in the V tile, and a row
@@ -58,8 +60,8 @@ constexpr int kSub = 16384;              // 128 rows x 64 elements, 128-byte swi
 constexpr int kTileBytes = 2 * kSub;
 constexpr int kStages = 5;               // K and V tiles in flight
 constexpr int kItems = 4;                // items the scheduler runs ahead
-constexpr int kThreads = 384;
-constexpr int kMmaWarp = 8, kKvWarp = 9, kSchedWarp = 10, kQWarp = 11;
+constexpr int kThreads = 512;
+constexpr int kMmaWarp = 8, kKWarp = 10, kVWarp = 11, kSchedWarp = 12, kQWarp = 13;  // (MMA: 8 for A, 9 for B)
 constexpr int kMaxBlocks = 160;
 constexpr int kOver = 2;                 // an item's cost next to its tiles
 constexpr int kMinCost = 4;              // least cost of a block
@@ -158,6 +160,21 @@ template <int kRegs> __device__ __forceinline__ void regs_up() {
 }
 template <int kRegs> __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+
+// True in one lane of a warp whose lanes are all here.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(one));
+  return one != 0;
+}
+
+// mbar_wait that looks at the clock only where the wait is a long one.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
+#pragma unroll 1
+  for (int i = 0; i < 16; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  return mbar_wait(bar, parity, abort, status);
 }
 
 __device__ __forceinline__ void fence_sc() { asm volatile("fence.sc.gpu;" ::: "memory"); }
@@ -290,19 +307,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int s = 0; s < kStages; ++s) {
       mbar_init(bar(bars->kv_full[s]), 1);
-      mbar_init(bar(bars->kv_empty[s]), 1);
+      mbar_init(bar(bars->kv_empty[s]), 2);  // both halves
     }
     for (int s = 0; s < kItems; ++s) {
       mbar_init(bar(bars->it_full[s]), 1);
-      mbar_init(bar(bars->it_empty[s]), 11);  // softmax warps, MMA, K/V and Q copies
+      mbar_init(bar(bars->it_empty[s]), 13);  // all warps but the scheduler
     }
     mbar_init(bar(bars->part_done), 8);
     mbar_init(bar(bars->merge_go), 1);
-    mbar_init(bar(bars->drain), 1);
+    mbar_init(bar(bars->drain), 2);
     bars->abort = 0;
     fence_mbar_init();
   }
-  if (warp == kKvWarp && lane == 0) {
+  if (warp == kKWarp && lane == 0) {
     prefetch_tmap(&tm_q);
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
@@ -320,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // place back); false at the end.
   auto next_item = [&](int k, Item& it) -> bool {
     bool got = true;
-    if (lane == 0) got = mbar_wait(bar(bars->it_full[k % kItems]), (k / kItems) & 1, abort, p.status);
+    if (lane == 0) got = wait_for(bar(bars->it_full[k % kItems]), (k / kItems) & 1, abort, p.status);
     got = __shfl_sync(0xffffffffu, got, 0);
     __syncwarp();
     if (!got) return false;
@@ -333,9 +350,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     return it.b >= 0;
   };
 
-  // 384 threads start with 168 registers each (64,512): the softmax warps take
-  // 208 and leave the others 80 (63,488 together).
-  if (warp >= kMmaWarp) regs_down<80>();
+  // 512 threads start with 128 registers each: the softmax warps take 192 and
+  // leave the others 64 (65,536 together).
+  if (warp >= kMmaWarp) regs_down<64>();
   if (warp == kSchedWarp) {
     // ---------------- scheduler ----------------
     const int s = kRows / p.g;
@@ -368,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int k = 0;
     bool ok = true;
     auto publish = [&](const Item& it) {
-      if (lane == 0 && k >= kItems) ok = mbar_wait(bar(bars->it_empty[k % kItems]), ((k / kItems) & 1) ^ 1, abort, p.status);
+      if (lane == 0 && k >= kItems) ok = wait_for(bar(bars->it_empty[k % kItems]), ((k / kItems) & 1) ^ 1, abort, p.status);
       ok = __shfl_sync(0xffffffffu, ok, 0);
       if (ok && lane == 0) {
         *reinterpret_cast<Item*>(smem + kItemOffset + (k % kItems) * 64) = it;
@@ -460,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = 0; x < 2; ++x) {
         if (it.lo[x] == it.hi[x]) continue;
         if (lane == 0) {
-          if (n[x] > 0) ok = mbar_wait(bar(bars->q_empty[x]), (n[x] - 1) & 1, abort, p.status);
+          if (n[x] > 0) ok = wait_for(bar(bars->q_empty[x]), (n[x] - 1) & 1, abort, p.status);
           if (ok) {
             const int row = it.q_row + x * (kHalf / p.g);
             mbar_arrive_expect_tx(bar(bars->q_full[x]), kTileBytes);
@@ -478,137 +495,140 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int x = 0; x < 2; ++x)
         if (n[x] > 0) mbar_wait(bar(bars->q_full[x]), (n[x] - 1) & 1, &no_abort, p.status);
     }
-  } else if (warp == kKvWarp) {
-    // ---------------- K and V copies ----------------
+  } else if (warp == kKWarp || warp == kVWarp) {
+    // ---------------- K copies, V copies ----------------
     const uint64_t pol = l2_policy_evict_last();
     const int bs = p.box_tokens, boxes = 2 * (kKv / bs);  // box c: tokens (c / 2) bs .. of the tile, dims 64 (c % 2) ..
     const int no_page = (int)max((int64_t)1, p.num_pages);   // outside the pool: read as zeros
-    int g = 0;
+    const void* tmap = warp == kVWarp ? (const void*)&tm_v : (const void*)&tm_k;
+    int g = warp == kVWarp;  // ring place: K tiles take the even ones, V tiles the odd ones
     Item it = {};
     bool ok = true;
     for (int k = 0; ok && next_item(k, it); ++k) {
       const int32_t* table = p.block_table + (int64_t)it.b * p.bt_stride;
-      // Page of the lane's box of tile t (the first 32 boxes), loaded a tile ahead.
+      // Page of box c of tile t; the lane's first one is loaded a tile ahead.
       auto page_of = [&](int t, int c) -> int {
         const int token = t * kKv + (c >> 1) * bs;
         if (t >= it.t1 || c >= boxes || token >= it.len) return no_page;
-        const int64_t pi = token / p.page_size;
+        const int pi = token / p.page_size;
         return pi < p.bt_stride ? table[pi] : -1;
       };
       int ahead = page_of(it.t0, lane);
-      for (int t = it.t0; ok && t < it.t1; ++t) {
-        int page = ahead;
+      for (int t = it.t0; t < it.t1; ++t, g += 2) {
+        const int page = ahead, st = g % kStages;
         ahead = page_of(t + 1, lane);
-        for (int kv = 0; ok && kv < 2; ++kv, ++g) {
-          const int st = g % kStages;
-          if (lane == 0) {
-            if (g >= kStages) ok = mbar_wait(bar(bars->kv_empty[st]), ((g / kStages) & 1) ^ 1, abort, p.status);
-            if (ok) mbar_arrive_expect_tx(bar(bars->kv_full[st]), kTileBytes);
-          }
-          ok = __shfl_sync(0xffffffffu, ok, 0);
-          if (!ok) break;
-          const void* tmap = kv ? (const void*)&tm_v : (const void*)&tm_k;
-          for (int c = lane; c < boxes; c += 32) {
-            const int r = (c >> 1) * bs;
-            int pg = c == lane ? page : page_of(t, c);
-            if (t * kKv + r < it.len && (pg < 0 || pg >= p.num_pages)) {
-              report(p.status, PKC_ERR_BLOCK_TABLE);
-              pg = no_page;
-            }
-            tma_load_4d(s_kv + st * kTileBytes + (c & 1) * kSub + r * 128, tmap, bar(bars->kv_full[st]), (c & 1) * 64, it.kvh,
-                        (t * kKv + r) % p.page_size, pg, pol);
-          }
-          __syncwarp();
+        if (lane == 0) {
+          if (g >= kStages) ok = wait_for(bar(bars->kv_empty[st]), ((g / kStages) & 1) ^ 1, abort, p.status);
+          if (ok) mbar_arrive_expect_tx(bar(bars->kv_full[st]), kTileBytes);
         }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        __syncwarp();
+        for (int c = lane; c < boxes; c += 32) {
+          const int r = (c >> 1) * bs;
+          int pg = c == lane ? page : page_of(t, c);
+          if (t * kKv + r < it.len && (pg < 0 || pg >= p.num_pages)) {
+            report(p.status, PKC_ERR_BLOCK_TABLE);
+            pg = no_page;
+          }
+          tma_load_4d(s_kv + st * kTileBytes + (c & 1) * kSub + r * 128, tmap, bar(bars->kv_full[st]), (c & 1) * 64, it.kvh,
+                      (t * kKv + r) % p.page_size, pg, pol);
+        }
+        __syncwarp();
       }
     }
     if (*abort && lane == 0) {
       volatile int no_abort = 0;
-      for (int j = g > kStages ? g - kStages : 0; j < g; ++j)
+      for (int j = g - 2; j >= 0 && j > g - 2 - kStages; j -= 2)
         mbar_wait(bar(bars->kv_full[j % kStages]), (j / kStages) & 1, &no_abort, p.status);
     }
-  } else if (warp == kMmaWarp) {
-    // ---------------- MMA issue ----------------
+  } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
+    // ---------------- MMA issue for one half ----------------
+    // The whole warp runs the loop and one elected lane issues: with uniform
+    // control flow the descriptors stay in uniform registers.
+    const int x = __shfl_sync(0xffffffffu, warp - kMmaWarp, 0);
     constexpr uint32_t kBf16 = std::is_same<T, __half>::value ? 0 : 1;
     constexpr uint32_t idesc_qk = idesc_f16(128, 128, kBf16, 0, 0);
     constexpr uint32_t idesc_pv = idesc_f16(128, 128, kBf16, 0, 1);
-    int g = 0;                                // ring place of the next K tile
-    int n_q[2] = {0, 0}, n_s[2] = {0, 0};     // Q tiles used, P tiles used
-    int n_o[2] = {0, 0};                      // O accumulators begun
-    bool pend[2] = {false, false};            // S of the tile before is in its softmax
-    bool first[2] = {false, false}, last[2] = {false, false};
-    int v_place = -1;                         // ring place of the pending V tile
+    const uint64_t desc_q = smem_desc_sw128(s_q + x * kTileBytes, 16, 1024);
+    const uint64_t desc_k = smem_desc_sw128(s_kv, 16, 1024), desc_v = smem_desc_sw128(s_kv, kSub, 1024);
+    const uint32_t t_s = tmem + x * 128, t_o = tmem + 256 + x * 128;
+    int place = 0;         // ring place (0 .. kStages - 1) of the next tile, K and V in turn, and its phase
+    uint32_t phase = 0;
+    uint32_t q_par = 0, p_par = 0, o_par = 1;
     Item it = {};
     bool ok = true;
-    // P V of a half's pending tile.
-    auto pv = [&](int x) -> bool {
-      if (!pend[x]) return true;
-      pend[x] = false;
-      const int sv = v_place % kStages;
-      if (!mbar_wait(bar(bars->p_full[x]), n_s[x] & 1, abort, p.status) ||
-          !mbar_wait(bar(bars->kv_full[sv]), (v_place / kStages) & 1, abort, p.status))
-        return false;
-      ++n_s[x];
-      if (first[x]) {  // it overwrites O: the one before has been read out
-        if (n_o[x] > 0 && !mbar_wait(bar(bars->o_free[x]), (n_o[x] - 1) & 1, abort, p.status)) return false;
-        ++n_o[x];
-      }
-      tc_fence_after();
-      const uint32_t vb = s_kv + sv * kTileBytes;
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
-        tc_mma_f16_ta(tmem + 256 + x * 128, tmem + x * 128 + kk * 8, smem_desc_sw128(vb + kk * 2048, kSub, 1024), idesc_pv,
-                      (!first[x] || kk > 0) ? 1u : 0u);
-      if (last[x]) tc_commit(bar(bars->o_full[x]));
-      return true;
-    };
-    auto qk = [&](int x, int t) -> bool {
-      if (t < it.lo[x] || t >= it.hi[x]) return true;
-      const int sk = g % kStages;
-      if (!mbar_wait(bar(bars->kv_full[sk]), (g / kStages) & 1, abort, p.status)) return false;
-      first[x] = t == it.lo[x];
-      last[x] = t == it.hi[x] - 1;
-      if (first[x] && !mbar_wait(bar(bars->q_full[x]), n_q[x] & 1, abort, p.status)) return false;
-      tc_fence_after();
-      const uint32_t qb = s_q + x * kTileBytes, kb = s_kv + sk * kTileBytes;
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        const uint32_t off = (kk >> 2) * kSub + (kk & 3) * 32;
-        tc_mma_f16(tmem + x * 128, smem_desc_sw128(qb + off, 16, 1024), smem_desc_sw128(kb + off, 16, 1024), idesc_qk, kk > 0);
-      }
-      tc_commit(bar(bars->s_full[x]));
-      if (last[x]) {
-        tc_commit(bar(bars->q_empty[x]));
-        ++n_q[x];
-      }
-      pend[x] = true;
-      return true;
+    auto wait = [&](uint64_t& b, uint32_t parity) { return __all_sync(0xffffffffu, wait_for(bar(b), parity, abort, p.status)); };
+    auto advance = [&] {
+      if (++place == kStages) place = 0, phase ^= 1;
     };
     for (int k = 0; ok && next_item(k, it); ++k) {
-      if (lane == 0) {
-        for (int t = it.t0; ok && t < it.t1; ++t, g += 2) {
-          ok = pv(0) && qk(0, t) && pv(1);
+      const int lo = x ? it.lo[1] : it.lo[0], hi = x ? it.hi[1] : it.hi[0];
+      for (int t = it.t0; t < it.t1; ++t) {
+        if (t < lo || t >= hi) {
+          // The other half's tile.  It is given back once it is there, never
+          // ahead: each half counts once for every time a place is filled.
+          for (int kv = 0; ok && kv < 2; ++kv) {
+            ok = wait(bars->kv_full[place], phase);
+            if (ok && elect_one()) mbar_arrive(bar(bars->kv_empty[place]));
+            __syncwarp();
+            advance();
+          }
           if (!ok) break;
-          if (v_place >= 0) tc_commit(bar(bars->kv_empty[v_place % kStages]));
-          ok = qk(1, t);
-          if (!ok) break;
-          tc_commit(bar(bars->kv_empty[g % kStages]));
-          v_place = g + 1;
+          continue;
         }
+        // S = Q K^T, behind the P V of the tile before.
+        if (t == lo) {
+          ok = wait(bars->q_full[x], q_par);
+          q_par ^= 1;
+        }
+        ok = ok && wait(bars->kv_full[place], phase);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t dk = desc_k + (uint32_t)place * (kTileBytes >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = (kk >> 2) * (kSub >> 4) + (kk & 3) * 2;
+            tc_mma_f16(t_s, desc_q + off, dk + off, idesc_qk, kk > 0);
+          }
+          tc_commit(bar(bars->s_full[x]));
+          tc_commit(bar(bars->kv_empty[place]));
+          if (t == hi - 1) tc_commit(bar(bars->q_empty[x]));
+        }
+        __syncwarp();
+        advance();
+        // O += P V once the softmax has left P where S was.
+        ok = wait(bars->kv_full[place], phase);
+        if (ok && t == lo) {  // it overwrites O: the one before has been read out
+          ok = wait(bars->o_free[x], o_par);
+          o_par ^= 1;
+        }
+        ok = ok && wait(bars->p_full[x], p_par);
+        if (!ok) break;
+        p_par ^= 1;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t dv = desc_v + (uint32_t)place * (kTileBytes >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            tc_mma_f16_ta(t_o, t_s + kk * 8, dv + kk * (2048 >> 4), idesc_pv, (t > lo || kk > 0) ? 1u : 0u);
+          tc_commit(bar(bars->kv_empty[place]));
+          if (t == hi - 1) tc_commit(bar(bars->o_full[x]));
+        }
+        __syncwarp();
+        advance();
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
     }
-    if (lane == 0) {
-      if (ok && !*abort) ok = pv(0) && pv(1);
-      // Every MMA issued above completes before TMEM is released.
-      tc_commit(bar(bars->drain));
-      volatile int no_abort = 0;
-      mbar_wait(bar(bars->drain), 0, &no_abort, p.status);
-    }
+    // Every MMA issued above completes before TMEM is released.
+    if (elect_one()) tc_commit(bar(bars->drain));
     __syncwarp();
-  } else {
+    volatile int no_abort = 0;
+    mbar_wait(bar(bars->drain), 0, &no_abort, p.status);
+    __syncwarp();
+  } else if (warp < kMmaWarp) {
     // ---------------- softmax, epilogue, merge: a row per thread ----------------
-    regs_up<208>();
+    regs_up<192>();
     const int x = warp >> 2, quad = warp & 3;
     const int row = x * kHalf + quad * 32 + lane;  // of the item
     const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
@@ -628,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m_ref = neg_inf();
       uint64_t l2a = 0ull, l2b = 0ull;
       for (int t = lo; t < hi; ++t, ++n_s) {
-        const bool got = mbar_wait(bar(bars->s_full[x]), n_s & 1, abort, p.status);
+        const bool got = wait_for(bar(bars->s_full[x]), n_s & 1, abort, p.status);
         if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
         tc_fence_after();
         uint32_t v[4][32];
@@ -660,14 +680,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (t > lo) {
             // O holds the tiles before this one: S of this tile was committed behind their P V.
 #pragma unroll 1
-            for (int j = 0; j < 4; ++j) {
-              uint32_t o[32];
-              tmem_ld_32x32b_x32(t_o + 32 * j, o);
+            for (int j = 0; j < 8; ++j) {
+              uint32_t o[16];
+              tmem_ld_32x32b_x16(t_o + 16 * j, o);
               tmem_ld_wait();
-              reg_fence32(o);
+              reg_fence16(o);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st_32x32b_x32(t_o + 32 * j, o);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+              tmem_st_32x32b_x16(t_o + 16 * j, o);
             }
           }
           m_ref = now;
@@ -675,18 +695,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float neg = m_ref == neg_inf() ? 0.f : -m_ref;
         const uint64_t n2 = pk2(neg, neg);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t pw[32];
+        for (int j = 0; j < 4; ++j) {
+          uint32_t pw[16];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            const int j = 2 * h + (i >> 4), e = 2 * (i & 15);
-            const float2 a = upk2(ffma2(pk2(__uint_as_float(v[j][e]), __uint_as_float(v[j][e + 1])), c2, n2));
+          for (int i = 0; i < 16; ++i) {
+            const float2 a =
+                upk2(ffma2(pk2(__uint_as_float(v[j][2 * i]), __uint_as_float(v[j][2 * i + 1])), c2, n2));
             const float p0 = ex2(a.x), p1 = ex2(a.y);
             if (i & 1) l2b = fadd2(l2b, pk2(p0, p1));
             else l2a = fadd2(l2a, pk2(p0, p1));
             pw[i] = Elem<T>::from_f2(p0, p1);
           }
-          tmem_st_32x32b_x32(t_s + 32 * h, pw);
+          tmem_st_32x32b_x16(t_s + 16 * j, pw);
         }
         if (const int live = it.len - t * kKv; live < kKv) {
           // Slots behind the length may hold anything, even NaN: zero their V
@@ -724,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const float lse2 = none || l == 0.f ? neg_inf() : m_ref + lg2(l);
       if (mine) {
-        const bool got = mbar_wait(bar(bars->o_full[x]), n_o & 1, abort, p.status);
+        const bool got = wait_for(bar(bars->o_full[x]), n_o & 1, abort, p.status);
         if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
         ++n_o;
         tc_fence_after();

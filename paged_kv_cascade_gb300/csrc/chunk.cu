@@ -11,11 +11,13 @@
 //   S_X = Q_X K_j^T              tcgen05.mma, A and B from shared memory
 //   P_X = exp2(S_X c - m_ref)    softmax warps, TMEM -> registers -> TMEM, 16 bits
 //   O_X += P_X V_j               tcgen05.mma, P_X read from TMEM
-// While one half is in its softmax the tensor cores work for the other: each half
-// has a warp that issues its P V of tile j - 1 and Q K of tile j as soon as its own
-// P is there.  P takes the columns of the S it was made from; TMEM is S_A,
-// S_B, O_A, O_B, 128 columns each.  P never passes through shared memory, whose
-// bandwidth the MMA's operands need.
+// TMEM is one S (128 columns) that the halves use in turn, P_A, P_B (64 columns
+// of 16-bit pairs) and O_A, O_B (128).  S is only in use until the softmax warps
+// have read it into registers, so the other half's Q K runs while they work, and
+// the next S of a half is there when its softmax is done: a half's chain per tile
+// is its softmax, the MMAs run beside it.  (With an S per half and P in its
+// columns, Q K of tile j + 1 waited for P V of tile j: 3650 cycles a tile.)  P never
+// passes through shared memory, whose bandwidth the MMA's operands need.
 // m_ref, a row's reference maximum, moves (and the row of O is rescaled, in
 // TMEM) only when a tile's maximum passes it by more than 2^8.
 //
@@ -29,8 +31,9 @@
 // tell) merges them, always in the order of the cache.
 //
 // Warps: 0-3 softmax of A, 4-7 of B (a row per thread, epilogue and merge too),
-// 8 and 9 MMA issue for A and B, 10 K copies, 11 V copies, 12 scheduler, 13 Q
-// copies.  K and V tiles take turns in one ring; a tile is one TMA box per page
+// 8 issues Q K, 9 P V, 10 K copies, 11 V copies, 12 scheduler, 13 Q
+// copies.  K and V have a ring each (a wait names a phase modulo 2, so whoever
+// fills a place has to have seen every phase of it); a tile is one TMA box per page
 // and 64 dims (pages that are not a power of two: boxes of their largest
 // power-of-two part).  The lanes of a warp issue their boxes one after another,
 // some 50 cycles each, so pages of 16 tokens need a warp for K and one for V.
@@ -58,10 +61,10 @@ constexpr int kRows = 2 * kHalf;         // rows of an item
 constexpr int kKv = 128;                 // tokens of a KV tile
 constexpr int kSub = 16384;              // 128 rows x 64 elements, 128-byte swizzle
 constexpr int kTileBytes = 2 * kSub;
-constexpr int kStages = 5;               // K and V tiles in flight
+constexpr int kStagesK = 2, kStagesV = 3;  // tiles in flight
 constexpr int kItems = 4;                // items the scheduler runs ahead
 constexpr int kThreads = 512;
-constexpr int kMmaWarp = 8, kKWarp = 10, kVWarp = 11, kSchedWarp = 12, kQWarp = 13;  // (MMA: 8 for A, 9 for B)
+constexpr int kQkWarp = 8, kPvWarp = 9, kKWarp = 10, kVWarp = 11, kSchedWarp = 12, kQWarp = 13;
 constexpr int kMaxBlocks = 160;
 constexpr int kOver = 2;                 // an item's cost next to its tiles
 constexpr int kMinCost = 4;              // least cost of a block
@@ -78,8 +81,9 @@ struct Item {
 
 struct __align__(8) Barriers {
   uint64_t q_full[2], q_empty[2];
-  uint64_t kv_full[kStages], kv_empty[kStages];
-  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+  uint64_t kv_full[kStagesK + kStagesV], kv_empty[kStagesK + kStagesV];  // K's places, then V's
+  uint64_t s_full[2], s_free, p_full[2];
+  uint64_t pv_done[2];   // P read, O up to date
   uint64_t it_full[kItems], it_empty[kItems];
   uint64_t part_done, merge_go;
   uint64_t drain;
@@ -89,7 +93,7 @@ struct __align__(8) Barriers {
 };
 
 constexpr int kKvOffset = 2 * kTileBytes;
-constexpr int kItemOffset = kKvOffset + kStages * kTileBytes;
+constexpr int kItemOffset = kKvOffset + (kStagesK + kStagesV) * kTileBytes;
 constexpr int kBarOffset = kItemOffset + kItems * 64;
 constexpr int kSmemBytes = kBarOffset + 512;
 static_assert(sizeof(Item) <= 64 && sizeof(Barriers) <= 512 && kSmemBytes <= 227 * 1024, "shared memory");
@@ -302,17 +306,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(bar(bars->q_empty[x]), 1);
       mbar_init(bar(bars->s_full[x]), 1);
       mbar_init(bar(bars->p_full[x]), 4);
-      mbar_init(bar(bars->o_full[x]), 1);
-      mbar_init(bar(bars->o_free[x]), 4);
+      mbar_init(bar(bars->pv_done[x]), 1);
     }
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kStagesK + kStagesV; ++s) {
       mbar_init(bar(bars->kv_full[s]), 1);
-      mbar_init(bar(bars->kv_empty[s]), 2);  // both halves
+      mbar_init(bar(bars->kv_empty[s]), 1);
     }
     for (int s = 0; s < kItems; ++s) {
       mbar_init(bar(bars->it_full[s]), 1);
       mbar_init(bar(bars->it_empty[s]), 13);  // all warps but the scheduler
     }
+    mbar_init(bar(bars->s_free), 4);
     mbar_init(bar(bars->part_done), 8);
     mbar_init(bar(bars->merge_go), 1);
     mbar_init(bar(bars->drain), 2);
@@ -324,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
   }
-  if (warp == kMmaWarp) {
+  if (warp == kQkWarp) {
     tmem_alloc(smem_u32(&bars->tmem_base), 512);
     tmem_relinquish();
   }
@@ -351,8 +355,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   // 512 threads start with 128 registers each: the softmax warps take 192 and
-  // leave the others 64 (65,536 together).
-  if (warp >= kMmaWarp) regs_down<64>();
+  // leave the others 64 (65,536 together).  Every role's code lies behind its own
+  // setmaxnreg, so the compiler keeps within it.
+  if (warp >= kQkWarp) {
+  regs_down<64>();
   if (warp == kSchedWarp) {
     // ---------------- scheduler ----------------
     const int s = kRows / p.g;
@@ -501,7 +507,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int bs = p.box_tokens, boxes = 2 * (kKv / bs);  // box c: tokens (c / 2) bs .. of the tile, dims 64 (c % 2) ..
     const int no_page = (int)max((int64_t)1, p.num_pages);   // outside the pool: read as zeros
     const void* tmap = warp == kVWarp ? (const void*)&tm_v : (const void*)&tm_k;
-    int g = warp == kVWarp;  // ring place: K tiles take the even ones, V tiles the odd ones
+    const int first = warp == kVWarp ? kStagesK : 0, stages = warp == kVWarp ? kStagesV : kStagesK;
+    int g = 0;  // tiles so far
     Item it = {};
     bool ok = true;
     for (int k = 0; ok && next_item(k, it); ++k) {
@@ -514,11 +521,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         return pi < p.bt_stride ? table[pi] : -1;
       };
       int ahead = page_of(it.t0, lane);
-      for (int t = it.t0; t < it.t1; ++t, g += 2) {
-        const int page = ahead, st = g % kStages;
+      for (int t = it.t0; t < it.t1; ++t, ++g) {
+        const int page = ahead, st = first + g % stages;
         ahead = page_of(t + 1, lane);
         if (lane == 0) {
-          if (g >= kStages) ok = wait_for(bar(bars->kv_empty[st]), ((g / kStages) & 1) ^ 1, abort, p.status);
+          if (g >= stages) ok = wait_for(bar(bars->kv_empty[st]), ((g / stages) & 1) ^ 1, abort, p.status);
           if (ok) mbar_arrive_expect_tx(bar(bars->kv_full[st]), kTileBytes);
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -539,85 +546,87 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (*abort && lane == 0) {
       volatile int no_abort = 0;
-      for (int j = g - 2; j >= 0 && j > g - 2 - kStages; j -= 2)
-        mbar_wait(bar(bars->kv_full[j % kStages]), (j / kStages) & 1, &no_abort, p.status);
+      for (int j = max(0, g - stages); j < g; ++j)
+        mbar_wait(bar(bars->kv_full[first + j % stages]), (j / stages) & 1, &no_abort, p.status);
     }
-  } else if (warp == kMmaWarp || warp == kMmaWarp + 1) {
-    // ---------------- MMA issue for one half ----------------
+  } else if (warp == kQkWarp || warp == kPvWarp) {
+    // ---------------- MMA issue: Q K, P V ----------------
     // The whole warp runs the loop and one elected lane issues: with uniform
-    // control flow the descriptors stay in uniform registers.
-    const int x = __shfl_sync(0xffffffffu, warp - kMmaWarp, 0);
+    // control flow the descriptors stay in uniform registers.  Both go tile by
+    // tile, A before B.
     constexpr uint32_t kBf16 = std::is_same<T, __half>::value ? 0 : 1;
     constexpr uint32_t idesc_qk = idesc_f16(128, 128, kBf16, 0, 0);
     constexpr uint32_t idesc_pv = idesc_f16(128, 128, kBf16, 0, 1);
-    const uint64_t desc_q = smem_desc_sw128(s_q + x * kTileBytes, 16, 1024);
+    const uint64_t desc_q = smem_desc_sw128(s_q, 16, 1024);
     const uint64_t desc_k = smem_desc_sw128(s_kv, 16, 1024), desc_v = smem_desc_sw128(s_kv, kSub, 1024);
-    const uint32_t t_s = tmem + x * 128, t_o = tmem + 256 + x * 128;
-    int place = 0;         // ring place (0 .. kStages - 1) of the next tile, K and V in turn, and its phase
-    uint32_t phase = 0;
-    uint32_t q_par = 0, p_par = 0, o_par = 1;
+    const bool is_pv = warp == kPvWarp;
+    const int first = is_pv ? kStagesK : 0, behind = is_pv ? kStagesK + kStagesV : kStagesK;
+    int place = first;             // ring place of the next K or V tile, and its phase
+    uint32_t phase = 0, s_par = 1;
+    uint32_t par = 0;              // phases of q_full or p_full, a bit per half
     Item it = {};
     bool ok = true;
     auto wait = [&](uint64_t& b, uint32_t parity) { return __all_sync(0xffffffffu, wait_for(bar(b), parity, abort, p.status)); };
-    auto advance = [&] {
-      if (++place == kStages) place = 0, phase ^= 1;
-    };
     for (int k = 0; ok && next_item(k, it); ++k) {
-      const int lo = x ? it.lo[1] : it.lo[0], hi = x ? it.hi[1] : it.hi[0];
       for (int t = it.t0; t < it.t1; ++t) {
-        if (t < lo || t >= hi) {
-          // The other half's tile.  It is given back once it is there, never
-          // ahead: each half counts once for every time a place is filled.
-          for (int kv = 0; ok && kv < 2; ++kv) {
-            ok = wait(bars->kv_full[place], phase);
-            if (ok && elect_one()) mbar_arrive(bar(bars->kv_empty[place]));
-            __syncwarp();
-            advance();
-          }
-          if (!ok) break;
-          continue;
-        }
-        // S = Q K^T, behind the P V of the tile before.
-        if (t == lo) {
-          ok = wait(bars->q_full[x], q_par);
-          q_par ^= 1;
-        }
-        ok = ok && wait(bars->kv_full[place], phase);
-        if (!ok) break;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t dk = desc_k + (uint32_t)place * (kTileBytes >> 4);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = (kk >> 2) * (kSub >> 4) + (kk & 3) * 2;
-            tc_mma_f16(t_s, desc_q + off, dk + off, idesc_qk, kk > 0);
-          }
-          tc_commit(bar(bars->s_full[x]));
-          tc_commit(bar(bars->kv_empty[place]));
-          if (t == hi - 1) tc_commit(bar(bars->q_empty[x]));
-        }
-        __syncwarp();
-        advance();
-        // O += P V once the softmax has left P where S was.
         ok = wait(bars->kv_full[place], phase);
-        if (ok && t == lo) {  // it overwrites O: the one before has been read out
-          ok = wait(bars->o_free[x], o_par);
-          o_par ^= 1;
-        }
-        ok = ok && wait(bars->p_full[x], p_par);
         if (!ok) break;
-        p_par ^= 1;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t dv = desc_v + (uint32_t)place * (kTileBytes >> 4);
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            tc_mma_f16_ta(t_o, t_s + kk * 8, dv + kk * (2048 >> 4), idesc_pv, (t > lo || kk > 0) ? 1u : 0u);
-          tc_commit(bar(bars->kv_empty[place]));
-          if (t == hi - 1) tc_commit(bar(bars->o_full[x]));
+        if (const int live = it.len - t * kKv; is_pv && live < kKv) {
+          // Slots behind the length may hold anything, even NaN: zero their V.
+          const uint32_t vst = s_kv + place * kTileBytes + live * 128;
+          for (int c = lane; c < (kKv - live) * 16; c += 32)
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vst + ((c >> 3) & 1) * kSub + (c >> 4) * 128 +
+                                                                        (c & 7) * 16),
+                         "r"(0u)
+                         : "memory");
+          fence_proxy_async_smem();
+          __syncwarp();
         }
+        const uint32_t at = (uint32_t)place * (kTileBytes >> 4);
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (t < it.lo[x] || t >= it.hi[x]) continue;
+          if (!is_pv) {
+            // S = Q K^T once the S before has been read
+            if (t == it.lo[x]) {
+              ok = ok && wait(bars->q_full[x], (par >> x) & 1);
+              par ^= 1u << x;
+            }
+            ok = ok && wait(bars->s_free, s_par);
+            if (!ok) break;
+            s_par ^= 1;
+            tc_fence_after();
+            if (elect_one()) {
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk) {
+                const uint32_t off = (kk >> 2) * (kSub >> 4) + (kk & 3) * 2;
+                tc_mma_f16(tmem, desc_q + x * (kTileBytes >> 4) + off, desc_k + at + off, idesc_qk, kk > 0);
+              }
+              tc_commit(bar(bars->s_full[x]));
+              if (t == it.hi[x] - 1) tc_commit(bar(bars->q_empty[x]));
+            }
+          } else {
+            // O += P V once P is there (and O of the piece before has been read
+            // out: by the warps that made this P)
+            ok = ok && wait(bars->p_full[x], (par >> x) & 1);
+            if (!ok) break;
+            par ^= 1u << x;
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t more = t > it.lo[x] ? 1u : 0u;
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                tc_mma_f16_ta(tmem + 256 + x * 128, tmem + 128 + x * 64 + kk * 8, desc_v + at + kk * (2048 >> 4), idesc_pv,
+                              kk > 0 ? 1u : more);
+              tc_commit(bar(bars->pv_done[x]));
+            }
+          }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (elect_one()) tc_commit(bar(bars->kv_empty[place]));
         __syncwarp();
-        advance();
+        if (++place == behind) place = first, phase ^= 1;
       }
     }
     // Every MMA issued above completes before TMEM is released.
@@ -626,17 +635,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     volatile int no_abort = 0;
     mbar_wait(bar(bars->drain), 0, &no_abort, p.status);
     __syncwarp();
-  } else if (warp < kMmaWarp) {
+  }
+  } else {
     // ---------------- softmax, epilogue, merge: a row per thread ----------------
     regs_up<192>();
     const int x = warp >> 2, quad = warp & 3;
     const int row = x * kHalf + quad * 32 + lane;  // of the item
     const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
-    const uint32_t t_s = t_lane + x * 128, t_o = t_lane + 256 + x * 128;
+    const uint32_t t_s = t_lane, t_p = t_lane + 128 + x * 64, t_o = t_lane + 256 + x * 128;
     const uint64_t c2 = pk2(p.scale_log2, p.scale_log2);
     uint32_t* ready = reinterpret_cast<uint32_t*>(p.status) + PKC_CHUNK_READY;
-    int g = 0;  // ring place of the item's first K tile
-    int n_s = 0, n_o = 0, n_merge = 0;
+    int n_s = 0, n_merge = 0;  // tiles, cut items so far
     Item it = {};
     bool ok = true;
     for (int k = 0; ok && next_item(k, it); ++k) {
@@ -657,6 +666,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 4; ++j) reg_fence32(v[j]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bars->s_free));
         const int c_lo = rlo - t * kKv, c_hi = rhi - t * kKv;  // columns the row attends to
         if (__any_sync(0xffffffffu, c_lo > 0 || c_hi < kKv)) {
 #pragma unroll
@@ -671,6 +683,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) mx[j] = max3(mx[j], __uint_as_float(v[j][i]), __uint_as_float(v[j][i + 1]));
         const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
+        // P V of the half's tile before has read P and brought O up to date.
+        const bool done = n_s == 0 || wait_for(bar(bars->pv_done[x]), (n_s - 1) & 1, abort, p.status);
+        if (!__all_sync(0xffffffffu, done)) { ok = false; break; }
+        tc_fence_after();
         if (__any_sync(0xffffffffu, top > m_ref + kMoveLog2)) {
           const float now = fmaxf(m_ref, top);
           const float f = m_ref == neg_inf() ? 0.f : ex2(m_ref - now);
@@ -678,7 +694,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           l2a = fmul2(l2a, f2);
           l2b = fmul2(l2b, f2);
           if (t > lo) {
-            // O holds the tiles before this one: S of this tile was committed behind their P V.
 #pragma unroll 1
             for (int j = 0; j < 8; ++j) {
               uint32_t o[16];
@@ -706,21 +721,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             else l2a = fadd2(l2a, pk2(p0, p1));
             pw[i] = Elem<T>::from_f2(p0, p1);
           }
-          tmem_st_32x32b_x16(t_s + 16 * j, pw);
-        }
-        if (const int live = it.len - t * kKv; live < kKv) {
-          // Slots behind the length may hold anything, even NaN: zero their V
-          // once the tile has landed (each half does, whichever MMA comes first).
-          const int place = g + 2 * (t - it.t0) + 1, sv = place % kStages;
-          const bool landed = mbar_wait(bar(bars->kv_full[sv]), (place / kStages) & 1, abort, p.status);
-          if (!__all_sync(0xffffffffu, landed)) { ok = false; break; }
-          const uint32_t vst = s_kv + sv * kTileBytes;
-          for (int c = quad * 32 + lane; c < (kKv - live) * 16; c += kHalf)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vst + ((c >> 3) & 1) * kSub + (live + (c >> 4)) * 128 +
-                                                                        (c & 7) * 16),
-                         "r"(0u)
-                         : "memory");
-          fence_proxy_async_smem();
+          tmem_st_32x32b_x16(t_p + 16 * j, pw);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -728,7 +729,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(bars->p_full[x]));
       }
       if (!ok) break;
-      g += 2 * (it.t1 - it.t0);
 
       // The row's state.
       const bool whole = it.c0 == it.c1, mine = hi > lo;
@@ -744,9 +744,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const float lse2 = none || l == 0.f ? neg_inf() : m_ref + lg2(l);
       if (mine) {
-        const bool got = wait_for(bar(bars->o_full[x]), n_o & 1, abort, p.status);
+        const bool got = wait_for(bar(bars->pv_done[x]), (n_s - 1) & 1, abort, p.status);
         if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
-        ++n_o;
         tc_fence_after();
       }
       bool bad = false;
@@ -754,6 +753,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; j < 4; ++j) {
         uint32_t v[32];
         float o[32];
+        __syncwarp();  // the TMEM loads are the whole warp's
         if (mine) {  // uniform over the half
           tmem_ld_32x32b_x32(t_o + 32 * j, v);
           tmem_ld_wait();
@@ -764,10 +764,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           o[i] = mine && !none ? __uint_as_float(v[i]) * inv : 0.f;
           bad = bad || !(fabsf(o[i]) <= FLT_MAX);
         }
-        if (!valid) continue;
-        if (whole) {
-          store_out<T>(p, out, 32 * j, o, 32);
-        } else {
+        if (valid && whole) store_out<T>(p, out, 32 * j, o, 32);
+        if (valid && !whole) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             *reinterpret_cast<float4*>(part_row(p, slot, 8 * j + i, row)) =
@@ -778,11 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (whole) p.lse[out] = lse2 * kLn2;
         else p.part_lse[slot * kRows + row] = lse2;
       }
-      if (mine) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(bars->o_free[x]));
-      }
+      tc_fence_before();  // O has been read out: the next P's arrival says so
       for (uint32_t todo = __ballot_sync(0xffffffffu, bad && valid); todo; todo &= todo - 1) {
         const int j = __ffs(todo) - 1, r = x * kHalf + quad * 32 + j;
         const int64_t at = __shfl_sync(0xffffffffu, out, j);
@@ -855,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarp) tmem_dealloc(tmem, 512);
+  if (warp == kQkWarp) tmem_dealloc(tmem, 512);
 }
 
 bool make_maps(const ChunkParams& p, int dtype, CUtensorMap& mq, CUtensorMap& mk, CUtensorMap& mv) {

@@ -104,45 +104,54 @@ struct Request {
   int r0, n, len;
 };
 
-// sum over i < m of floor(max(a + i s, 0) / 128), s a power of two
-PKC_HD inline int64_t sum_floor(int64_t a, int s, int64_t m) {
-  int64_t i0 = a >= 0 ? 0 : (-a + s - 1) / s;
-  if (i0 >= m) return 0;
-  a += i0 * s;
-  m -= i0;
-  if (s >= 128) return m * (a / 128) + (s / 128) * (m * (m - 1) / 2);
-  const int per = 128 / s;
-  int64_t sum = 0;
-  for (int r = 0; r < per; ++r) {
-    const int64_t u = (m - r + per - 1) / per;  // r, r + per, ..
-    if (m > r) sum += u * ((a + r * s) / 128) + u * (u - 1) / 2;
+// sum over i < m of floor(max(a + i s, 0) / 128), s = 2^e
+PKC_HD inline int64_t sum_floor(int64_t a, int e, int64_t m) {
+  if (a < 0) {  // the terms before the first positive a are 0
+    const int64_t skip = (-a + (int64_t(1) << e) - 1) >> e;
+    a += skip << e;
+    m -= skip;
+    if (m <= 0) return 0;
   }
-  return sum;
+  const int64_t whole = m * (a >> 7), r = a & 127;
+  if (e >= 7) return whole + ((m * (m - 1) / 2) << (e - 7));
+  // floor((r + i s) / 128) = floor((r / s + i) / per), per = 128 / s, and the sum
+  // of floor(i / per) over i < n = per u + v is per u (u - 1) / 2 + v u
+  const int d = 7 - e;
+  int64_t n[2] = {(r >> e) + m, r >> e}, g[2];
+  for (int k = 0; k < 2; ++k) {
+    const int64_t u = n[k] >> d, v = n[k] - (u << d);
+    g[k] = ((u * (u - 1) / 2) << d) + v * u;
+  }
+  return whole + g[0] - g[1];
 }
 
+// Tokens of an item: 2^shift.
+PKC_HD inline int item_shift(const ChunkParams& p) { return p.g == 1 ? 8 : p.g == 2 ? 7 : p.g == 4 ? 6 : 5; }
+
 PKC_HD inline int n_items(const ChunkParams& p, const Request& q) {
-  const int s = kRows / p.g;
-  return (q.n + s - 1) / s;
+  const int e = item_shift(p);
+  return (q.n + (1 << e) - 1) >> e;
 }
 
 // Cost of the first m items of a request's KV head.
 PKC_HD inline int64_t cost_of(const ChunkParams& p, const Request& q, int m) {
-  const int s = kRows / p.g, nt = n_items(p, q);
+  const int e = item_shift(p), nt = n_items(p, q);
   const int64_t pos = (int64_t)q.len - q.n;
-  const int64_t last = ((int64_t)q.len + kKv - 1) / kKv;
+  const int64_t last = ((int64_t)q.len + kKv - 1) >> 7;
   int64_t sum = (int64_t)m * kOver;
-  if (p.causal) sum += sum_floor(pos + s + kKv - 1, s, m < nt ? m : nt - 1) + (m == nt ? last : 0);
+  if (p.causal) sum += sum_floor(pos + (1 << e) + kKv - 1, e, m < nt ? m : nt - 1) + (m == nt ? last : 0);
   else sum += m * last;
-  if (p.window) sum -= sum_floor(pos - p.window + 1, s, m);
+  if (p.window) sum -= sum_floor(pos - p.window + 1, e, m);
   return sum;
 }
 
 // KV tiles [lo, hi) in the reach of tokens j0 .. j1 - 1 of a request.
 PKC_HD inline void reach(const ChunkParams& p, const Request& q, int j0, int j1, int& lo, int& hi) {
-  const int64_t pos = (int64_t)q.len - q.n;
-  const int64_t end = p.causal ? pos + j1 : q.len, begin = p.window ? pos + j0 - p.window + 1 : 0;
-  hi = end > 0 ? (int)((end + kKv - 1) / kKv) : 0;
-  lo = begin > 0 ? (int)(begin / kKv) : 0;
+  const int pos = q.len - q.n;
+  const int end = p.causal ? pos + j1 : q.len;
+  const int64_t begin = p.window ? (int64_t)pos + j0 - p.window + 1 : 0;
+  hi = end > 0 ? (int)(((uint32_t)end + kKv - 1) >> 7) : 0;
+  lo = begin > 0 ? (int)(begin >> 7) : 0;
   if (lo > hi) lo = hi;
 }
 
@@ -175,11 +184,11 @@ __device__ __forceinline__ bool elect_one() {
 
 // mbar_wait that looks at the clock only where the wait is a long one.
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
-#pragma unroll 1
-  for (int i = 0; i < 16; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait(bar, parity, abort, status);
+  return mbar_try_wait(bar, parity) || mbar_wait(bar, parity, abort, status);
 }
+
+// The n lowest bits (none for n <= 0, all from 32 on).
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
 
 __device__ __forceinline__ void fence_sc() { asm volatile("fence.sc.gpu;" ::: "memory"); }
 
@@ -361,7 +370,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   regs_down<64>();
   if (warp == kSchedWarp) {
     // ---------------- scheduler ----------------
-    const int s = kRows / p.g;
     auto load = [&](int b) -> Request {  // an empty request where there is nothing to do
       Request q = {0, 0, 0};
       if (b < p.batch) {
@@ -374,22 +382,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return q;
     };
-    int64_t total = 0;
-    for (int b0 = 0; b0 < p.batch; b0 += 32) {
-      const Request q = load(b0 + lane);
-      if (q.n) total += cost_of(p, q, n_items(p, q));
-    }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-    total *= p.hkv;
-    const int n_blocks = (int)max((int64_t)1, min((int64_t)gridDim.x, total / kMinCost));
+    // The cost of all requests, then those that hold some of the block's share:
+    // one loop for both, for its code is long and shares the instruction cache
+    // with the softmax.
+    int64_t total = 0, s0 = 0, s1 = 0;
+    int n_blocks = 1, k = 0;
     const int c = (int)blockIdx.x;
-    auto begin_of = [&](int i) { return (int64_t)i * total / n_blocks; };
-    auto block_of = [&](int64_t x) { return (int)(((x + 1) * n_blocks - 1) / total); };
-    const int64_t s0 = c < n_blocks ? begin_of(c) : total, s1 = c < n_blocks ? begin_of(c + 1) : total;
-
-    int k = 0;
     bool ok = true;
+    auto block_of = [&](int64_t x) { return (int)(((x + 1) * n_blocks - 1) / total); };
     auto publish = [&](const Item& it) {
       if (lane == 0 && k >= kItems) ok = wait_for(bar(bars->it_empty[k % kItems]), ((k / kItems) & 1) ^ 1, abort, p.status);
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -399,73 +399,86 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ++k;
     };
-    // The request that holds s0, 32 at a time; then request by request.
-    int64_t base = 0;  // cost of the requests before b0
-    for (int b0 = 0; ok && b0 < p.batch && base < s1; b0 += 32) {
-      const Request mine = load(b0 + lane);
-      const int64_t per_head = mine.n ? cost_of(p, mine, n_items(p, mine)) : 0;
-      int64_t before = per_head * p.hkv;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, before, d);
-        if (lane >= d) before += y;
-      }
-      const int64_t all = __shfl_sync(0xffffffffu, before, 31);
-      before = base + before - per_head * p.hkv;
-      uint32_t todo = __ballot_sync(0xffffffffu, mine.n > 0 && before < s1 && before + per_head * p.hkv > s0);
-      for (; ok && todo; todo &= todo - 1) {
-        const int j = __ffs(todo) - 1, b = b0 + j;
-        const Request q = {__shfl_sync(0xffffffffu, mine.r0, j), __shfl_sync(0xffffffffu, mine.n, j),
-                           __shfl_sync(0xffffffffu, mine.len, j)};
-        const int64_t ph = __shfl_sync(0xffffffffu, per_head, j), rb = __shfl_sync(0xffffffffu, before, j);
-        const int nt = n_items(p, q);
-        int h = 0, i = 0;
-        int64_t x0 = rb;  // where item (h, i) begins
-        if (s0 > rb) {
-          h = (int)((s0 - rb) / ph);
-          const int64_t rel = s0 - rb - h * ph;
-          int lo = 0, hi = nt;  // the last i with cost_of(i) <= rel
-          while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (cost_of(p, q, mid) <= rel) lo = mid; else hi = mid;
-          }
-          i = lo;
-          x0 = rb + h * ph + cost_of(p, q, i);
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+      int64_t base = 0;  // cost of the requests before b0
+#pragma unroll 1
+      for (int b0 = 0; ok && b0 < p.batch && (pass == 0 || base < s1); b0 += 32) {
+        const Request mine = load(b0 + lane);
+        const int64_t per_head = mine.n ? cost_of(p, mine, n_items(p, mine)) : 0;
+        int64_t before = per_head * p.hkv;
+#pragma unroll 1
+        for (int d = 1; d < 32; d <<= 1) {
+          const int64_t y = __shfl_up_sync(0xffffffffu, before, d);
+          if (lane >= d) before += y;
         }
-        for (; ok && h < p.hkv && x0 < s1; i = 0, ++h) {
-          for (; ok && i < nt && x0 < s1; ++i) {
-            const int j0 = i * s, n_tok = min(s, q.n - j0);
-            int lo, hi;
-            reach(p, q, j0, j0 + n_tok, lo, hi);
-            const int64_t first = x0 + kOver, end = first + (hi - lo);  // its tiles lie at first .. end - 1
+        const int64_t all = __shfl_sync(0xffffffffu, before, 31);
+        before = base + before - per_head * p.hkv;
+        base += all;
+        if (pass == 0) continue;
+        uint32_t todo = __ballot_sync(0xffffffffu, mine.n > 0 && before < s1 && before + per_head * p.hkv > s0);
+#pragma unroll 1
+        for (; ok && todo; todo &= todo - 1) {
+          const int j = __ffs(todo) - 1;
+          const Request q = {__shfl_sync(0xffffffffu, mine.r0, j), __shfl_sync(0xffffffffu, mine.n, j),
+                             __shfl_sync(0xffffffffu, mine.len, j)};
+          const int64_t ph = __shfl_sync(0xffffffffu, per_head, j);
+          const int nt = n_items(p, q);
+          int h = 0, i = 0;
+          int64_t x0 = __shfl_sync(0xffffffffu, before, j);  // where item (h, i) begins
+          if (s0 > x0) {
+            h = (int)((s0 - x0) / ph);
+            x0 += h * ph;
+            // the last i whose items before it cost at most s0 - x0
+            int hi = nt;
+            int64_t at = 0;
+#pragma unroll 1
+            while (hi - i > 1) {
+              const int mid = (i + hi) >> 1;
+              const int64_t cost = cost_of(p, q, mid);
+              if (cost <= s0 - x0) i = mid, at = cost;
+              else hi = mid;
+            }
+            x0 += at;
+          }
+#pragma unroll 1
+          while (ok && h < p.hkv && x0 < s1) {
+            const int j0 = i << item_shift(p), n_tok = min(1 << item_shift(p), q.n - j0);
             Item it;
-            it.b = b; it.kvh = h; it.q_row = q.r0 + j0; it.n_tok = n_tok;
-            it.pos0 = (int)((int64_t)q.len - q.n + j0); it.len = q.len;
+            it.b = b0 + j; it.kvh = h; it.q_row = q.r0 + j0; it.n_tok = n_tok;
+            it.pos0 = q.len - q.n + j0; it.len = q.len;
+            const int half = kHalf / p.g;
+            reach(p, q, j0, j0 + min(n_tok, half), it.lo[0], it.hi[0]);
+            it.lo[1] = it.hi[1] = it.hi[0];
+            if (n_tok > half) reach(p, q, j0 + half, j0 + n_tok, it.lo[1], it.hi[1]);
+            const int lo = it.lo[0], hi = it.hi[1];  // (a later token's reach begins and ends no earlier)
+            const int64_t first = x0 + kOver, end = first + (hi - lo);  // its tiles lie at first .. end - 1
             it.t0 = lo + (int)max((int64_t)0, s0 - first);
             it.t1 = lo + (int)max((int64_t)0, min(s1, end) - first);
             it.c0 = it.c1 = c;
-            if (hi > lo) {
-              it.c0 = block_of(first);
-              it.c1 = block_of(end - 1);
-            }
+            if (hi > lo && first < s0) it.c0 = block_of(first);
+            if (hi > lo && end > s1) it.c1 = block_of(end - 1);
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              const int a = x * (kHalf / p.g), e = min(n_tok, (x + 1) * (kHalf / p.g));
-              it.lo[x] = it.hi[x] = it.t0;
-              if (e > a) {
-                int l, r;
-                reach(p, q, j0 + a, j0 + e, l, r);
-                it.lo[x] = max(l, it.t0);
-                it.hi[x] = max(it.lo[x], min(r, it.t1));
-              }
+              it.lo[x] = max(it.lo[x], it.t0);
+              it.hi[x] = max(it.lo[x], min(it.hi[x], it.t1));
             }
             // a piece with tiles, or the one place of an item without any
             if (it.t0 < it.t1 || (hi == lo && x0 >= s0)) publish(it);
             x0 = end;
+            if (++i == nt) i = 0, ++h;
           }
         }
       }
-      base += all;
+      if (pass == 0) {
+        total = base;
+        n_blocks = (int)max((int64_t)1, min((int64_t)gridDim.x, total / kMinCost));
+        s0 = s1 = total;
+        if (c < n_blocks) {
+          s0 = c * total / n_blocks;
+          s1 = (c + 1) * total / n_blocks;
+        }
+      }
     }
     if (ok) {
       Item it;
@@ -499,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (*abort && lane == 0) {  // the copies already issued land before the block exits
       volatile int no_abort = 0;
       for (int x = 0; x < 2; ++x)
-        if (n[x] > 0) mbar_wait(bar(bars->q_full[x]), (n[x] - 1) & 1, &no_abort, p.status);
+        if (n[x] > 0) wait_for(bar(bars->q_full[x]), (n[x] - 1) & 1, &no_abort, p.status);
     }
   } else if (warp == kKWarp || warp == kVWarp) {
     // ---------------- K copies, V copies ----------------
@@ -547,7 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (*abort && lane == 0) {
       volatile int no_abort = 0;
       for (int j = max(0, g - stages); j < g; ++j)
-        mbar_wait(bar(bars->kv_full[first + j % stages]), (j / stages) & 1, &no_abort, p.status);
+        wait_for(bar(bars->kv_full[first + j % stages]), (j / stages) & 1, &no_abort, p.status);
     }
   } else if (warp == kQkWarp || warp == kPvWarp) {
     // ---------------- MMA issue: Q K, P V ----------------
@@ -583,12 +596,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
         }
         const uint32_t at = (uint32_t)place * (kTileBytes >> 4);
-#pragma unroll
+#pragma unroll 1
         for (int x = 0; x < 2; ++x) {
-          if (t < it.lo[x] || t >= it.hi[x]) continue;
+          const int lo = x ? it.lo[1] : it.lo[0], hi = x ? it.hi[1] : it.hi[0];
+          if (t < lo || t >= hi) continue;
           if (!is_pv) {
             // S = Q K^T once the S before has been read
-            if (t == it.lo[x]) {
+            if (t == lo) {
               ok = ok && wait(bars->q_full[x], (par >> x) & 1);
               par ^= 1u << x;
             }
@@ -603,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tc_mma_f16(tmem, desc_q + x * (kTileBytes >> 4) + off, desc_k + at + off, idesc_qk, kk > 0);
               }
               tc_commit(bar(bars->s_full[x]));
-              if (t == it.hi[x] - 1) tc_commit(bar(bars->q_empty[x]));
+              if (t == hi - 1) tc_commit(bar(bars->q_empty[x]));
             }
           } else {
             // O += P V once P is there (and O of the piece before has been read
@@ -613,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             par ^= 1u << x;
             tc_fence_after();
             if (elect_one()) {
-              const uint32_t more = t > it.lo[x] ? 1u : 0u;
+              const uint32_t more = t > lo ? 1u : 0u;
 #pragma unroll
               for (int kk = 0; kk < 8; ++kk)
                 tc_mma_f16_ta(tmem + 256 + x * 128, tmem + 128 + x * 64 + kk * 8, desc_v + at + kk * (2048 >> 4), idesc_pv,
@@ -633,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect_one()) tc_commit(bar(bars->drain));
     __syncwarp();
     volatile int no_abort = 0;
-    mbar_wait(bar(bars->drain), 0, &no_abort, p.status);
+    wait_for(bar(bars->drain), 0, &no_abort, p.status);
     __syncwarp();
   }
   } else {
@@ -672,10 +686,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int c_lo = rlo - t * kKv, c_hi = rhi - t * kKv;  // columns the row attends to
         if (__any_sync(0xffffffffu, c_lo > 0 || c_hi < kKv)) {
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t keep = low_bits(c_hi - 32 * j) & ~low_bits(c_lo - 32 * j);
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * j + i < c_lo || 32 * j + i >= c_hi) v[j][i] = 0xff800000u;
+            for (int i = 0; i < 32; ++i) v[j][i] = (keep >> i) & 1 ? v[j][i] : 0xff800000u;
+          }
         }
         float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
@@ -803,7 +818,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(bars->part_done));
         if (warp == 0) {
-          const bool done = mbar_wait(bar(bars->part_done), n_merge & 1, abort, p.status);
+          const bool done = wait_for(bar(bars->part_done), n_merge & 1, abort, p.status);
           if (!__all_sync(0xffffffffu, done)) { ok = false; break; }
           if (lane == 0) atomicOr(ready + (slot >> 5), 1u << (slot & 31));
           __syncwarp();
@@ -834,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_arrive(bar(bars->merge_go));
           }
         }
-        const bool go = mbar_wait(bar(bars->merge_go), n_merge & 1, abort, p.status);
+        const bool go = wait_for(bar(bars->merge_go), n_merge & 1, abort, p.status);
         if (!__all_sync(0xffffffffu, go)) { ok = false; break; }
         ++n_merge;
         if (*(volatile int*)&bars->merge) {

@@ -18,8 +18,11 @@
 // is its softmax, the MMAs run beside it.  (With an S per half and P in its
 // columns, Q K of tile j + 1 waited for P V of tile j: 3650 cycles a tile.)  P never
 // passes through shared memory, whose bandwidth the MMA's operands need.
-// m_ref, a row's reference maximum, moves (and the row of O is rescaled, in
-// TMEM) only when a tile's maximum passes it by more than 2^8.
+// m_ref, a row's reference maximum, is that of its first tile.  It moves (and the
+// row of O is rescaled, in TMEM) only when a tile's P would sum to more than 2^13:
+// P is formed at once, and again where the sum says so, so the other tiles need
+// no maximum at all (64 instructions and a chain ahead of the exponentials).  P
+// stays far below fp16's largest number, and a row's sum is at least 1.
 //
 // Work split.  An item costs its KV tiles and kOver; all items are laid end to
 // end (request, KV head, row tile) and cut evenly over the blocks, one per SM.
@@ -68,7 +71,8 @@ constexpr int kQkWarp = 8, kPvWarp = 9, kKWarp = 10, kVWarp = 11, kSchedWarp = 1
 constexpr int kMaxBlocks = 160;
 constexpr int kOver = 2;                 // an item's cost next to its tiles
 constexpr int kMinCost = 4;              // least cost of a block
-constexpr float kMoveLog2 = 8.f;
+constexpr int kShort = 8;                // items of at most so many tiles are not cut
+constexpr float kMoveSum = 8192.f;       // a tile's sum of P above which its reference maximum moves
 
 struct Item {
   int b;                 // request; -1: no more items
@@ -76,7 +80,7 @@ struct Item {
   int pos0, len;         // position of the first token, cached tokens
   int t0, t1;            // KV tiles of the piece
   int lo[2], hi[2];      // those of half A, B (lo == hi: none)
-  int c0, c1;            // blocks with pieces of the item (c0 == c1: whole)
+  int c0, c1;            // first and last block with a piece of the item (c0 == c1: whole)
 };
 
 struct __align__(8) Barriers {
@@ -389,7 +393,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     int n_blocks = 1, k = 0;
     const int c = (int)blockIdx.x;
     bool ok = true;
-    auto block_of = [&](int64_t x) { return (int)(((x + 1) * n_blocks - 1) / total); };
+    // The block that holds place x: the last i with i total / n_blocks <= x.
+    auto block_of = [&](int64_t x) {
+      int n = 0;
+#pragma unroll 1
+      for (int i = lane; i < kMaxBlocks; i += 32)
+        n += __popc(__ballot_sync(0xffffffffu, i < n_blocks && i * total < (x + 1) * n_blocks));
+      return n - 1;
+    };
+    // i total / n_blocks, in divisions of 32 bits (total < 2^54, n_blocks < 2^8)
+    auto share_of = [&](int i) {
+      const uint32_t a = (uint32_t)(total >> 24), n = (uint32_t)n_blocks;
+      const uint64_t rest = ((uint64_t)(a % n) << 24) | (uint32_t)(total & 0xffffff);  // < n 2^24 <= 2^32
+      const uint64_t q = ((uint64_t)(a / n) << 24) + (uint32_t)rest / n;
+      return (int64_t)(q * i + (uint32_t)rest % n * i / n);
+    };
     auto publish = [&](const Item& it) {
       if (lane == 0 && k >= kItems) ok = wait_for(bar(bars->it_empty[k % kItems]), ((k / kItems) & 1) ^ 1, abort, p.status);
       ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -427,8 +445,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           int h = 0, i = 0;
           int64_t x0 = __shfl_sync(0xffffffffu, before, j);  // where item (h, i) begins
           if (s0 > x0) {
-            h = (int)((s0 - x0) / ph);
-            x0 += h * ph;
+#pragma unroll 1
+            for (int step = 1 << 16; step; step >>= 1)
+              if (x0 + step * ph <= s0) h += step, x0 += step * ph;
             // the last i whose items before it cost at most s0 - x0
             int hi = nt;
             int64_t at = 0;
@@ -453,18 +472,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (n_tok > half) reach(p, q, j0 + half, j0 + n_tok, it.lo[1], it.hi[1]);
             const int lo = it.lo[0], hi = it.hi[1];  // (a later token's reach begins and ends no earlier)
             const int64_t first = x0 + kOver, end = first + (hi - lo);  // its tiles lie at first .. end - 1
-            it.t0 = lo + (int)max((int64_t)0, s0 - first);
-            it.t1 = lo + (int)max((int64_t)0, min(s1, end) - first);
+            it.t0 = lo;
+            it.t1 = hi;
             it.c0 = it.c1 = c;
-            if (hi > lo && first < s0) it.c0 = block_of(first);
-            if (hi > lo && end > s1) it.c1 = block_of(end - 1);
+            bool ours = end > s0 && end <= s1;  // a short item is whole, its last place's block has it
+            if (hi - lo > kShort) {
+              it.t0 = lo + (int)max((int64_t)0, s0 - first);
+              it.t1 = lo + (int)max((int64_t)0, min(s1, end) - first);
+              if (first < s0) it.c0 = block_of(first);
+              if (end > s1) it.c1 = block_of(end - 1);
+              ours = it.t0 < it.t1;
+            }
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
               it.lo[x] = max(it.lo[x], it.t0);
               it.hi[x] = max(it.lo[x], min(it.hi[x], it.t1));
             }
-            // a piece with tiles, or the one place of an item without any
-            if (it.t0 < it.t1 || (hi == lo && x0 >= s0)) publish(it);
+            if (ours) publish(it);
             x0 = end;
             if (++i == nt) i = 0, ++h;
           }
@@ -475,8 +499,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         n_blocks = (int)max((int64_t)1, min((int64_t)gridDim.x, total / kMinCost));
         s0 = s1 = total;
         if (c < n_blocks) {
-          s0 = c * total / n_blocks;
-          s1 = (c + 1) * total / n_blocks;
+          s0 = share_of(c);
+          s1 = share_of(c + 1);
         }
       }
     }
@@ -668,7 +692,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rhi = p.causal ? min(it.len, pos + 1) : it.len;
       const int rlo = p.window ? (int)max((int64_t)0, (int64_t)pos - p.window + 1) : 0;
       const int lo = x ? it.lo[1] : it.lo[0], hi = x ? it.hi[1] : it.hi[0];
+      // tiles [full_lo, full_hi) that all the warp's rows attend to whole: the first
+      // row's end and the last row's begin decide
+      const int full_hi = __shfl_sync(0xffffffffu, rhi, 0) >> 7;
+      const int full_lo = (int)(((uint32_t)__shfl_sync(0xffffffffu, rlo, 31) + kKv - 1) >> 7);
       float m_ref = neg_inf();
+      bool all_set = false;  // every row of the warp has a reference
       uint64_t l2a = 0ull, l2b = 0ull;
       for (int t = lo; t < hi; ++t, ++n_s) {
         const bool got = wait_for(bar(bars->s_full[x]), n_s & 1, abort, p.status);
@@ -677,14 +706,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t v[4][32];
 #pragma unroll
         for (int j = 0; j < 4; ++j) tmem_ld_32x32b_x32(t_s + 32 * j, v[j]);
+        // P V of the half's tile before has read P and brought O up to date (asked
+        // while S is on its way).
+        const bool early = n_s == 0 || mbar_try_wait(bar(bars->pv_done[x]), (n_s - 1) & 1);
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 4; ++j) reg_fence32(v[j]);
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(bars->s_free));
-        const int c_lo = rlo - t * kKv, c_hi = rhi - t * kKv;  // columns the row attends to
-        if (__any_sync(0xffffffffu, c_lo > 0 || c_hi < kKv)) {
+        if (t < full_lo || t >= full_hi) {
+          const int c_lo = rlo - t * kKv, c_hi = rhi - t * kKv;  // columns the row attends to
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint32_t keep = low_bits(c_hi - 32 * j) & ~low_bits(c_lo - 32 * j);
@@ -692,51 +724,62 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 32; ++i) v[j][i] = (keep >> i) & 1 ? v[j][i] : 0xff800000u;
           }
         }
-        float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
-#pragma unroll
-        for (int i = 0; i < 32; i += 2)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) mx[j] = max3(mx[j], __uint_as_float(v[j][i]), __uint_as_float(v[j][i + 1]));
-        const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
-        // P V of the half's tile before has read P and brought O up to date.
-        const bool done = n_s == 0 || wait_for(bar(bars->pv_done[x]), (n_s - 1) & 1, abort, p.status);
+        const bool done = early || wait_for(bar(bars->pv_done[x]), (n_s - 1) & 1, abort, p.status);
         if (!__all_sync(0xffffffffu, done)) { ok = false; break; }
         tc_fence_after();
-        if (__any_sync(0xffffffffu, top > m_ref + kMoveLog2)) {
-          const float now = fmaxf(m_ref, top);
-          const float f = m_ref == neg_inf() ? 0.f : ex2(m_ref - now);
-          const uint64_t f2 = pk2(f, f);
-          l2a = fmul2(l2a, f2);
-          l2b = fmul2(l2b, f2);
-          if (t > lo) {
+        bool move = t == lo || !all_set;
 #pragma unroll 1
-            for (int j = 0; j < 8; ++j) {
-              uint32_t o[16];
-              tmem_ld_32x32b_x16(t_o + 16 * j, o);
-              tmem_ld_wait();
-              reg_fence16(o);
+        for (;;) {
+          if (move) {
+            float mx[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-              tmem_st_32x32b_x16(t_o + 16 * j, o);
+            for (int i = 0; i < 32; i += 2)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) mx[j] = max3(mx[j], __uint_as_float(v[j][i]), __uint_as_float(v[j][i + 1]));
+            const float now = fmaxf(m_ref, fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2);
+            const float f = m_ref == neg_inf() ? 0.f : ex2(m_ref - now);
+            const uint64_t f2 = pk2(f, f);
+            l2a = fmul2(l2a, f2);
+            l2b = fmul2(l2b, f2);
+            m_ref = now;
+            all_set = !__any_sync(0xffffffffu, now == neg_inf());
+            if (t > lo) {
+#pragma unroll 1
+              for (int j = 0; j < 8; ++j) {
+                uint32_t o[16];
+                tmem_ld_32x32b_x16(t_o + 16 * j, o);
+                tmem_ld_wait();
+                reg_fence16(o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tmem_st_32x32b_x16(t_o + 16 * j, o);
+              }
             }
           }
-          m_ref = now;
-        }
-        const float neg = m_ref == neg_inf() ? 0.f : -m_ref;
-        const uint64_t n2 = pk2(neg, neg);
+          const float neg = m_ref == neg_inf() ? 0.f : -m_ref;
+          const uint64_t n2 = pk2(neg, neg);
+          uint64_t sa = 0ull, sb = 0ull;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          uint32_t pw[16];
+          for (int j = 0; j < 4; ++j) {
+            uint32_t pw[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float2 a =
-                upk2(ffma2(pk2(__uint_as_float(v[j][2 * i]), __uint_as_float(v[j][2 * i + 1])), c2, n2));
-            const float p0 = ex2(a.x), p1 = ex2(a.y);
-            if (i & 1) l2b = fadd2(l2b, pk2(p0, p1));
-            else l2a = fadd2(l2a, pk2(p0, p1));
-            pw[i] = Elem<T>::from_f2(p0, p1);
+            for (int i = 0; i < 16; ++i) {
+              const float2 a =
+                  upk2(ffma2(pk2(__uint_as_float(v[j][2 * i]), __uint_as_float(v[j][2 * i + 1])), c2, n2));
+              const float p0 = ex2(a.x), p1 = ex2(a.y);
+              if (i & 1) sb = fadd2(sb, pk2(p0, p1));
+              else sa = fadd2(sa, pk2(p0, p1));
+              pw[i] = Elem<T>::from_f2(p0, p1);
+            }
+            tmem_st_32x32b_x16(t_p + 16 * j, pw);
           }
-          tmem_st_32x32b_x16(t_p + 16 * j, pw);
+          const float2 s2 = upk2(fadd2(sa, sb));
+          move = __any_sync(0xffffffffu, s2.x + s2.y > kMoveSum);
+          if (!move) {
+            l2a = fadd2(l2a, sa);
+            l2b = fadd2(l2b, sb);
+            break;
+          }
         }
         tmem_st_wait();
         tc_fence_before();

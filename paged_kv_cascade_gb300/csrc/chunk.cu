@@ -69,7 +69,7 @@ constexpr int kItems = 4;                // items the scheduler runs ahead
 constexpr int kThreads = 512;
 constexpr int kQkWarp = 8, kPvWarp = 9, kKWarp = 10, kVWarp = 11, kSchedWarp = 12, kQWarp = 13;
 constexpr int kMaxBlocks = 160;
-constexpr int kOver = 2;                 // an item's cost next to its tiles
+constexpr int kOver = 4;                 // an item's cost next to its tiles
 constexpr int kMinCost = 4;              // least cost of a block
 constexpr int kShort = 8;                // items of at most so many tiles are not cut
 constexpr float kMoveSum = 8192.f;       // a tile's sum of P above which its reference maximum moves
@@ -260,40 +260,54 @@ __device__ __noinline__ void slow_row(const ChunkParams& p, int b, int kvh, int6
   lse2 = l == 0.f ? neg_inf() : m + lg2(l);
 }
 
-// The merge of an item's pieces by the eight softmax warps: a warp takes 32 rows
-// and 16 columns at a time.
+// The merge of an item's partial states by the eight softmax warps: a warp takes
+// 32 rows and 32 columns at a time, two states' loads in flight.
 template <typename T>
 __device__ __forceinline__ void merge_item(const ChunkParams& p, const Item& it, int warp, int lane) {
-  const int rows = it.n_tok * p.g, groups = (rows + 31) / 32;
-  for (int u = warp; u < 8 * groups; u += 8) {
-    const int row = (u >> 3) * 32 + lane, chunk = (u & 7) * 4;
+  const int rows = it.n_tok * p.g, groups = (rows + 31) / 32, n = it.c1 - it.c0 + 1;
+#pragma unroll 1
+  for (int u = warp; u < 4 * groups; u += 8) {
+    const int row = (u >> 2) * 32 + lane, chunk = (u & 3) * 8;
     float m = neg_inf();
-    for (int c = it.c0; c <= it.c1; ++c) m = fmaxf(m, __ldcg(p.part_lse + slot_of(c, it.c0) * kRows + row));
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) m = fmaxf(m, __ldcg(p.part_lse + slot_of(it.c0 + i, it.c0) * kRows + row));
     const float ref = m == neg_inf() ? 0.f : m;
-    float l = 0.f, o[16];
+    float l = 0.f, o[32];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] = 0.f;
-#pragma unroll 2
-    for (int c = it.c0; c <= it.c1; ++c) {
-      const int slot = slot_of(c, it.c0);
-      const float w = ex2(__ldcg(p.part_lse + slot * kRows + row) - ref);
-      l += w;
+    for (int i = 0; i < 32; ++i) o[i] = 0.f;
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += 2) {
+      float4 x[2][8];
+      float w[2];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        const float4 x = __ldcg(reinterpret_cast<const float4*>(part_row(p, slot, chunk + k, row)));
-        o[4 * k] += w * x.x;
-        o[4 * k + 1] += w * x.y;
-        o[4 * k + 2] += w * x.z;
-        o[4 * k + 3] += w * x.w;
+      for (int i = 0; i < 2; ++i) {
+        const int slot = slot_of(it.c0 + min(i0 + i, n - 1), it.c0);
+        w[i] = __ldcg(p.part_lse + slot * kRows + row);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[i][k] = __ldcg(reinterpret_cast<const float4*>(part_row(p, slot, chunk + k, row)));
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (i0 + i >= n) break;
+        const float f = ex2(w[i] - ref);
+        l += f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          o[4 * k] += f * x[i][k].x;
+          o[4 * k + 1] += f * x[i][k].y;
+          o[4 * k + 2] += f * x[i][k].z;
+          o[4 * k + 3] += f * x[i][k].w;
+        }
       }
     }
-    if (row >= rows) continue;
-    const float inv = m == neg_inf() ? 0.f : 1.f / l;
+    if (row < rows) {
+      const float inv = m == neg_inf() ? 0.f : 1.f / l;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) o[i] *= inv;
-    const int64_t out = ((int64_t)it.q_row + row / p.g) * p.hq + it.kvh * p.g + row % p.g;
-    store_out<T>(p, out, 4 * chunk, o, 16);
-    if (chunk == 0) p.lse[out] = m == neg_inf() ? neg_inf() : (m + lg2(l)) * kLn2;
+      for (int i = 0; i < 32; ++i) o[i] *= inv;
+      const int64_t out = ((int64_t)it.q_row + row / p.g) * p.hq + it.kvh * p.g + row % p.g;
+      store_out<T>(p, out, 4 * chunk, o, 32);
+      if (chunk == 0) p.lse[out] = m == neg_inf() ? neg_inf() : (m + lg2(l)) * kLn2;
+    }
   }
 }
 
@@ -789,41 +803,44 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
 
       // The row's state.
-      const bool whole = it.c0 == it.c1, mine = hi > lo;
+      const bool cut = it.c0 != it.c1, mine = hi > lo;
       const int slot = slot_of((int)blockIdx.x, it.c0);
       const int k_lo = max(rlo, it.t0 * kKv), k_hi = min(rhi, it.t1 * kKv);  // tokens of the piece that the row attends to
-      const bool none = k_lo >= k_hi;
       const int64_t out = ((int64_t)it.q_row + row / p.g) * p.hq + it.kvh * p.g + row % p.g;
       float l;
       {
         const float2 a = upk2(l2a), b = upk2(l2b);
-        l = (a.x + a.y) + (b.x + b.y);
+        l = k_lo < k_hi ? (a.x + a.y) + (b.x + b.y) : 0.f;
       }
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const float lse2 = none || l == 0.f ? neg_inf() : m_ref + lg2(l);
-      if (mine) {
-        const bool got = wait_for(bar(bars->pv_done[x]), (n_s - 1) & 1, abort, p.status);
-        if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
-        tc_fence_after();
-      }
-      bool bad = false;
+      const bool any = mine && l != 0.f;
+      const float inv = any ? 1.f / l : 0.f;
+      const float lse2 = any ? m_ref + lg2(l) : neg_inf();
+      bool ready_now = true;
+      if (mine) ready_now = wait_for(bar(bars->pv_done[x]), (n_s - 1) & 1, abort, p.status);
+      if (!__all_sync(0xffffffffu, ready_now)) { ok = false; break; }
+      tc_fence_after();
+      uint64_t finite = 0ull;  // 0 times all of the row's O
+      const uint64_t inv2 = pk2(inv, inv);
 #pragma unroll 1
       for (int j = 0; j < 4; ++j) {
         uint32_t v[32];
         float o[32];
         __syncwarp();  // the TMEM loads are the whole warp's
-        if (mine) {  // uniform over the half
+        if (mine) {    // uniform over the half
           tmem_ld_32x32b_x32(t_o + 32 * j, v);
           tmem_ld_wait();
           reg_fence32(v);
         }
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          o[i] = mine && !none ? __uint_as_float(v[i]) * inv : 0.f;
-          bad = bad || !(fabsf(o[i]) <= FLT_MAX);
+        for (int i = 0; i < 32; i += 2) {
+          const uint64_t y = any ? fmul2(pk2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), inv2) : 0ull;
+          finite = ffma2(y, 0ull, finite);
+          const float2 z = upk2(y);
+          o[i] = z.x;
+          o[i + 1] = z.y;
         }
-        if (valid && whole) store_out<T>(p, out, 32 * j, o, 32);
-        if (valid && !whole) {
+        if (valid && !cut) store_out<T>(p, out, 32 * j, o, 32);
+        if (valid && cut) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             *reinterpret_cast<float4*>(part_row(p, slot, 8 * j + i, row)) =
@@ -831,8 +848,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (valid) {
-        if (whole) p.lse[out] = lse2 * kLn2;
+        if (!cut) p.lse[out] = lse2 * kLn2;
         else p.part_lse[slot * kRows + row] = lse2;
+      }
+      bool bad;
+      {
+        const float2 z = upk2(finite);
+        bad = !(z.x + z.y == 0.f);
       }
       tc_fence_before();  // O has been read out: the next P's arrival says so
       for (uint32_t todo = __ballot_sync(0xffffffffu, bad && valid); todo; todo &= todo - 1) {
@@ -840,7 +862,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int64_t at = __shfl_sync(0xffffffffu, out, j);
         float o[4], again;
         slow_row<T>(p, it.b, it.kvh, at, __shfl_sync(0xffffffffu, k_lo, j), __shfl_sync(0xffffffffu, k_hi, j), o, again);
-        if (!whole) {
+        if (cut) {
           *reinterpret_cast<float4*>(part_row(p, slot, lane, r)) = make_float4(o[0], o[1], o[2], o[3]);
         } else if (p.out_dtype == PKC_F32) {
           *reinterpret_cast<float4*>(static_cast<float*>(p.o) + at * PKC_HEAD_DIM + 4 * lane) =
@@ -850,12 +872,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               make_uint2(Elem<T>::from_f2(o[0], o[1]), Elem<T>::from_f2(o[2], o[3]));
         }
         if (lane == 0) {
-          if (whole) p.lse[at] = again * kLn2;
-          else p.part_lse[slot * kRows + r] = again;
+          if (cut) p.part_lse[slot * kRows + r] = again;
+          else p.lse[at] = again * kLn2;
         }
       }
 
-      if (!whole) {
+      if (cut) {
         // The block whose piece is the item's last one to be there merges all.
         __threadfence();
         __syncwarp();

@@ -69,9 +69,12 @@ constexpr int kItems = 4;                // items the scheduler runs ahead
 constexpr int kThreads = 512;
 constexpr int kQkWarp = 8, kPvWarp = 9, kKWarp = 10, kVWarp = 11, kSchedWarp = 12, kQWarp = 13;
 constexpr int kMaxBlocks = 160;
-constexpr int kOver = 4;                 // an item's cost next to its tiles
-constexpr int kMinCost = 4;              // least cost of a block
-constexpr int kShort = 8;                // items of at most so many tiles are not cut
+// What an item costs, measured (0.35 us a unit): a KV tile where both halves have
+// rows 1.74 us, where only A has 1.41 (as fast as HBM brings it), and 5.9 us for
+// the item itself (first tile, epilogue).
+constexpr int kTileCost = 5, kHalfTileCost = 4, kOver = 17;
+constexpr int kMinCost = 20;             // least cost of a block
+constexpr int kShort = 16;               // items of at most so many tiles are not cut: a cut costs some 16 us
 constexpr float kMoveSum = 8192.f;       // a tile's sum of P above which its reference maximum moves
 
 struct Item {
@@ -137,18 +140,6 @@ PKC_HD inline int n_items(const ChunkParams& p, const Request& q) {
   return (q.n + (1 << e) - 1) >> e;
 }
 
-// Cost of the first m items of a request's KV head.
-PKC_HD inline int64_t cost_of(const ChunkParams& p, const Request& q, int m) {
-  const int e = item_shift(p), nt = n_items(p, q);
-  const int64_t pos = (int64_t)q.len - q.n;
-  const int64_t last = ((int64_t)q.len + kKv - 1) >> 7;
-  int64_t sum = (int64_t)m * kOver;
-  if (p.causal) sum += sum_floor(pos + (1 << e) + kKv - 1, e, m < nt ? m : nt - 1) + (m == nt ? last : 0);
-  else sum += m * last;
-  if (p.window) sum -= sum_floor(pos - p.window + 1, e, m);
-  return sum;
-}
-
 // KV tiles [lo, hi) in the reach of tokens j0 .. j1 - 1 of a request.
 PKC_HD inline void reach(const ChunkParams& p, const Request& q, int j0, int j1, int& lo, int& hi) {
   const int pos = q.len - q.n;
@@ -157,6 +148,29 @@ PKC_HD inline void reach(const ChunkParams& p, const Request& q, int j0, int j1,
   hi = end > 0 ? (int)(((uint32_t)end + kKv - 1) >> 7) : 0;
   lo = begin > 0 ? (int)(begin >> 7) : 0;
   if (lo > hi) lo = hi;
+}
+
+// Cost of a KV tile of a request's item i.
+PKC_HD inline int tile_cost(const ChunkParams& p, const Request& q, int i) {
+  return (q.n - (i << item_shift(p))) * p.g <= kHalf ? kHalfTileCost : kTileCost;
+}
+
+// Cost of the first m items of a request's KV head.
+PKC_HD inline int64_t cost_of(const ChunkParams& p, const Request& q, int m) {
+  const int e = item_shift(p), nt = n_items(p, q);
+  const int64_t pos = (int64_t)q.len - q.n;
+  const int64_t all = ((int64_t)q.len + kKv - 1) >> 7;
+  // the last item ends at the length and may have rows for A alone
+  const int whole = m < nt ? m : nt - 1;
+  int64_t tiles = p.causal ? sum_floor(pos + (1 << e) + kKv - 1, e, whole) : whole * all;
+  if (p.window) tiles -= sum_floor(pos - p.window + 1, e, whole);
+  int64_t sum = (int64_t)m * kOver + tiles * kTileCost;
+  if (m == nt) {
+    int lo, hi;
+    reach(p, q, (nt - 1) << e, q.n, lo, hi);
+    sum += (int64_t)(hi - lo) * tile_cost(p, q, nt - 1);
+  }
+  return sum;
 }
 
 // ---------------------------------------------------------------- helpers
@@ -485,15 +499,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             it.lo[1] = it.hi[1] = it.hi[0];
             if (n_tok > half) reach(p, q, j0 + half, j0 + n_tok, it.lo[1], it.hi[1]);
             const int lo = it.lo[0], hi = it.hi[1];  // (a later token's reach begins and ends no earlier)
-            const int64_t first = x0 + kOver, end = first + (hi - lo);  // its tiles lie at first .. end - 1
+            const int cost = tile_cost(p, q, i);
+            const int64_t first = x0 + kOver, end = first + (int64_t)(hi - lo) * cost;  // its tiles lie at first .. end - 1
             it.t0 = lo;
             it.t1 = hi;
             it.c0 = it.c1 = c;
             bool ours = end > s0 && end <= s1;  // a short item is whole, its last place's block has it
             if (hi - lo > kShort) {
-              it.t0 = lo + (int)max((int64_t)0, s0 - first);
-              it.t1 = lo + (int)max((int64_t)0, min(s1, end) - first);
-              if (first < s0) it.c0 = block_of(first);
+              // (a block's share is larger than a tile's cost: no piece between is empty)
+              const uint32_t from = (uint32_t)max((int64_t)0, s0 - first), to = (uint32_t)max((int64_t)0, min(s1, end) - first);
+              it.t0 = lo + (int)(cost == kTileCost ? from / kTileCost : from / kHalfTileCost);
+              it.t1 = lo + (int)(cost == kTileCost ? to / kTileCost : to / kHalfTileCost);
+              if (first + cost - 1 < s0) it.c0 = block_of(first + cost - 1);
               if (end > s1) it.c1 = block_of(end - 1);
               ours = it.t0 < it.t1;
             }

@@ -200,6 +200,14 @@ __device__ __forceinline__ bool elect_one() {
   return one != 0;
 }
 
+// Arrive for a warp that is all here: a predicate in place of a branch, which
+// costs some 200 cycles in the softmax loop.
+__device__ __forceinline__ void arrive_warp(uint32_t bar, int lane) {
+  __syncwarp();
+  asm volatile("{ .reg .pred p; .reg .b64 st; setp.eq.s32 p, %1, 0; @p mbarrier.arrive.shared::cta.b64 st, [%0]; }" ::"r"(bar),
+               "r"(lane)
+               : "memory");
+}
 // mbar_wait that looks at the clock only where the wait is a long one.
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile int* abort, int32_t* status) {
   return mbar_try_wait(bar, parity) || mbar_wait(bar, parity, abort, status);
@@ -210,20 +218,31 @@ __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 
 
 __device__ __forceinline__ void fence_sc() { asm volatile("fence.sc.gpu;" ::: "memory"); }
 
-// 32 columns of row `o` (float32, already normalised) to column `col` of output row `row`.
+// 32 columns (float32, already normalised) to column `col` of output row `row`.
+// A thread has a row of its own, so a store is as wide as it gets: 32 bytes, a
+// sector, where o allows it.
 template <typename T>
-__device__ __forceinline__ void store_out(const ChunkParams& p, int64_t row, int col, const float* o, int n) {
+__device__ __forceinline__ void store_out(const ChunkParams& p, int64_t row, int col, const float (&o)[32]) {
   if (p.out_dtype == PKC_F32) {
     float* dst = static_cast<float*>(p.o) + row * PKC_HEAD_DIM + col;
 #pragma unroll
-    for (int i = 0; i < n; i += 4) *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-  } else {
-    T* dst = static_cast<T*>(p.o) + row * PKC_HEAD_DIM + col;
+    for (int i = 0; i < 32; i += 4) *reinterpret_cast<float4*>(dst + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+    return;
+  }
+  T* dst = static_cast<T*>(p.o) + row * PKC_HEAD_DIM + col;
+  uint32_t w[16];
 #pragma unroll
-    for (int i = 0; i < n; i += 8)
-      *reinterpret_cast<uint4*>(dst + i) =
-          make_uint4(Elem<T>::from_f2(o[i], o[i + 1]), Elem<T>::from_f2(o[i + 2], o[i + 3]),
-                     Elem<T>::from_f2(o[i + 4], o[i + 5]), Elem<T>::from_f2(o[i + 6], o[i + 7]));
+  for (int i = 0; i < 16; ++i) w[i] = Elem<T>::from_f2(o[2 * i], o[2 * i + 1]);
+  if (p.o_wide) {
+#pragma unroll
+    for (int i = 0; i < 16; i += 8)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 2 * i), "r"(w[i]), "r"(w[i + 1]),
+                   "r"(w[i + 2]), "r"(w[i + 3]), "r"(w[i + 4]), "r"(w[i + 5]), "r"(w[i + 6]), "r"(w[i + 7])
+                   : "memory");
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; i += 4)
+      *reinterpret_cast<uint4*>(dst + 2 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
   }
 }
 
@@ -319,7 +338,7 @@ __device__ __forceinline__ void merge_item(const ChunkParams& p, const Item& it,
 #pragma unroll
       for (int i = 0; i < 32; ++i) o[i] *= inv;
       const int64_t out = ((int64_t)it.q_row + row / p.g) * p.hq + it.kvh * p.g + row % p.g;
-      store_out<T>(p, out, 4 * chunk, o, 32);
+      store_out<T>(p, out, 4 * chunk, o);
       if (chunk == 0) p.lse[out] = m == neg_inf() ? neg_inf() : (m + lg2(l)) * kLn2;
     }
   }
@@ -378,6 +397,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
+  // A wait in the loops over tiles.  Where it runs out nobody leaves the loop: the
+  // other waits end at once then, what is computed is not used (the status says
+  // so), and the warps stay whole without a vote per wait (50 us of 690 on
+  // prompts).  Items and copies are not begun on such a wait.
+  auto pass = [&](uint64_t& b, uint32_t parity) {
+    wait_for(bar(b), parity, abort, p.status);
+    __syncwarp();
+  };
   // The k-th item of the block, by a whole warp (lane 0 waits and gives the
   // place back); false at the end.
   auto next_item = [&](int k, Item& it) -> bool {
@@ -390,8 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int* dst = reinterpret_cast<int*>(&it);
 #pragma unroll
     for (int i = 0; i < (int)(sizeof(Item) / 4); ++i) dst[i] = src[i];
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar(bars->it_empty[k % kItems]));
+    arrive_warp(bar(bars->it_empty[k % kItems]), lane);
     return it.b >= 0;
   };
 
@@ -633,12 +659,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t phase = 0, s_par = 1;
     uint32_t par = 0;              // phases of q_full or p_full, a bit per half
     Item it = {};
-    bool ok = true;
-    auto wait = [&](uint64_t& b, uint32_t parity) { return __all_sync(0xffffffffu, wait_for(bar(b), parity, abort, p.status)); };
-    for (int k = 0; ok && next_item(k, it); ++k) {
+    for (int k = 0; next_item(k, it); ++k) {
       for (int t = it.t0; t < it.t1; ++t) {
-        ok = wait(bars->kv_full[place], phase);
-        if (!ok) break;
+        pass(bars->kv_full[place], phase);
         if (const int live = it.len - t * kKv; is_pv && live < kKv) {
           // Slots behind the length may hold anything, even NaN: zero their V.
           const uint32_t vst = s_kv + place * kTileBytes + live * 128;
@@ -658,11 +681,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!is_pv) {
             // S = Q K^T once the S before has been read
             if (t == lo) {
-              ok = ok && wait(bars->q_full[x], (par >> x) & 1);
+              pass(bars->q_full[x], (par >> x) & 1);
               par ^= 1u << x;
             }
-            ok = ok && wait(bars->s_free, s_par);
-            if (!ok) break;
+            pass(bars->s_free, s_par);
             s_par ^= 1;
             tc_fence_after();
             if (elect_one()) {
@@ -677,8 +699,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           } else {
             // O += P V once P is there (and O of the piece before has been read
             // out: by the warps that made this P)
-            ok = ok && wait(bars->p_full[x], (par >> x) & 1);
-            if (!ok) break;
+            pass(bars->p_full[x], (par >> x) & 1);
             par ^= 1u << x;
             tc_fence_after();
             if (elect_one()) {
@@ -692,7 +713,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           __syncwarp();
         }
-        if (!ok) break;
         if (elect_one()) tc_commit(bar(bars->kv_empty[place]));
         __syncwarp();
         if (++place == behind) place = first, phase ^= 1;
@@ -731,21 +751,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       bool all_set = false;  // every row of the warp has a reference
       uint64_t l2a = 0ull, l2b = 0ull;
       for (int t = lo; t < hi; ++t, ++n_s) {
-        const bool got = wait_for(bar(bars->s_full[x]), n_s & 1, abort, p.status);
-        if (!__all_sync(0xffffffffu, got)) { ok = false; break; }
+        pass(bars->s_full[x], n_s & 1);
         tc_fence_after();
         uint32_t v[4][32];
 #pragma unroll
         for (int j = 0; j < 4; ++j) tmem_ld_32x32b_x32(t_s + 32 * j, v[j]);
-        // P V of the half's tile before has read P and brought O up to date (asked
-        // while S is on its way).
-        const bool early = n_s == 0 || mbar_try_wait(bar(bars->pv_done[x]), (n_s - 1) & 1);
         tmem_ld_wait();
 #pragma unroll
         for (int j = 0; j < 4; ++j) reg_fence32(v[j]);
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(bars->s_free));
+        arrive_warp(bar(bars->s_free), lane);
         if (t < full_lo || t >= full_hi) {
           const int c_lo = rlo - t * kKv, c_hi = rhi - t * kKv;  // columns the row attends to
 #pragma unroll
@@ -755,8 +770,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 32; ++i) v[j][i] = (keep >> i) & 1 ? v[j][i] : 0xff800000u;
           }
         }
-        const bool done = early || wait_for(bar(bars->pv_done[x]), (n_s - 1) & 1, abort, p.status);
-        if (!__all_sync(0xffffffffu, done)) { ok = false; break; }
+        // P V of the half's tile before has read P and brought O up to date.
+        if (n_s > 0) pass(bars->pv_done[x], (n_s - 1) & 1);
         tc_fence_after();
         bool move = t == lo || !all_set;
 #pragma unroll 1
@@ -814,10 +829,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tmem_st_wait();
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(bars->p_full[x]));
+        arrive_warp(bar(bars->p_full[x]), lane);
       }
-      if (!ok) break;
 
       // The row's state.
       const bool cut = it.c0 != it.c1, mine = hi > lo;
@@ -832,9 +845,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool any = mine && l != 0.f;
       const float inv = any ? 1.f / l : 0.f;
       const float lse2 = any ? m_ref + lg2(l) : neg_inf();
-      bool ready_now = true;
-      if (mine) ready_now = wait_for(bar(bars->pv_done[x]), (n_s - 1) & 1, abort, p.status);
-      if (!__all_sync(0xffffffffu, ready_now)) { ok = false; break; }
+      if (mine) pass(bars->pv_done[x], (n_s - 1) & 1);
       tc_fence_after();
       uint64_t finite = 0ull;  // 0 times all of the row's O
       const uint64_t inv2 = pk2(inv, inv);
@@ -856,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           o[i] = z.x;
           o[i + 1] = z.y;
         }
-        if (valid && !cut) store_out<T>(p, out, 32 * j, o, 32);
+        if (valid && !cut) store_out<T>(p, out, 32 * j, o);
         if (valid && cut) {
 #pragma unroll
           for (int i = 0; i < 8; ++i)
@@ -979,6 +990,7 @@ size_t chunk_partial_bytes() { return (size_t)2 * kMaxBlocks * kRows * (PKC_HEAD
 int launch_paged_chunk(const ChunkParams& params, int dtype, void* stream) {
   ChunkParams p = params;
   p.part_lse = p.part_o + (size_t)2 * kMaxBlocks * kRows * PKC_HEAD_DIM;
+  p.o_wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
   p.scale_log2 = std::max(p.scale_log2, FLT_MIN);  // a scale of 0 must not meet a masked score's infinity
   for (p.box_tokens = 1; p.box_tokens < kKv && p.page_size % (2 * p.box_tokens) == 0;) p.box_tokens *= 2;
   CUtensorMap mq, mk, mv;

@@ -83,6 +83,7 @@ struct Item {
   int pos0, len;         // position of the first token, cached tokens
   int t0, t1;            // KV tiles of the piece
   int lo[2], hi[2];      // those of half A, B (lo == hi: none)
+  int off;               // 0: rows 0-127 are A's; 128: B's, and A has none
   int c0, c1;            // first and last block with a piece of the item (c0 == c1: whole)
 };
 
@@ -445,6 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // with the softmax.
     int64_t total = 0, s0 = 0, s1 = 0;
     int n_blocks = 1, k = 0;
+    bool turn = false;
     const int c = (int)blockIdx.x;
     bool ok = true;
     // The block that holds place x: the last i with i total / n_blocks <= x.
@@ -545,6 +547,12 @@ __global__ void __launch_bounds__(kThreads, 1)
               it.lo[x] = max(it.lo[x], it.t0);
               it.hi[x] = max(it.lo[x], min(it.hi[x], it.t1));
             }
+            it.off = 0;
+            if (n_tok <= half) {  // every second item of few rows goes to B: one's epilogue runs beside the other's tiles
+              it.off = turn ? kHalf : 0;
+              if (ours) turn = !turn;
+              if (it.off) it.lo[1] = it.lo[0], it.hi[1] = it.hi[0], it.lo[0] = it.hi[0] = it.t0;
+            }
             if (ours) publish(it);
             x0 = end;
             if (++i == nt) i = 0, ++h;
@@ -579,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           if (n[x] > 0) ok = wait_for(bar(bars->q_empty[x]), (n[x] - 1) & 1, abort, p.status);
           if (ok) {
-            const int row = it.q_row + x * (kHalf / p.g);
+            const int row = it.q_row + (x * kHalf - it.off) / p.g;
             mbar_arrive_expect_tx(bar(bars->q_full[x]), kTileBytes);
             tma_load_3d(s_q + x * kTileBytes, &tm_q, bar(bars->q_full[x]), 0, it.kvh * p.g, row, pol);
             tma_load_3d(s_q + x * kTileBytes + kSub, &tm_q, bar(bars->q_full[x]), 64, it.kvh * p.g, row, pol);
@@ -729,7 +737,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- softmax, epilogue, merge: a row per thread ----------------
     regs_up<192>();
     const int x = warp >> 2, quad = warp & 3;
-    const int row = x * kHalf + quad * 32 + lane;  // of the item
     const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t t_s = t_lane, t_p = t_lane + 128 + x * 64, t_o = t_lane + 256 + x * 128;
     const uint64_t c2 = pk2(p.scale_log2, p.scale_log2);
@@ -738,15 +745,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     Item it = {};
     bool ok = true;
     for (int k = 0; ok && next_item(k, it); ++k) {
+      const int row0 = x * kHalf - it.off + quad * 32, row = row0 + lane;  // of the item; the warp's first one
+      const int n_rows = it.n_tok * p.g;
       const int pos = it.pos0 + row / p.g;
-      const bool valid = row < it.n_tok * p.g;
+      const bool valid = row >= 0 && row < n_rows;
       const int rhi = p.causal ? min(it.len, pos + 1) : it.len;
       const int rlo = p.window ? (int)max((int64_t)0, (int64_t)pos - p.window + 1) : 0;
       const int lo = x ? it.lo[1] : it.lo[0], hi = x ? it.hi[1] : it.hi[0];
       // tiles [full_lo, full_hi) that all the warp's rows attend to whole: the first
       // row's end and the last row's begin decide
-      const int full_hi = __shfl_sync(0xffffffffu, rhi, 0) >> 7;
-      const int full_lo = (int)(((uint32_t)__shfl_sync(0xffffffffu, rlo, 31) + kKv - 1) >> 7);
+      const int hi_min = __shfl_sync(0xffffffffu, rhi, 0), lo_max = __shfl_sync(0xffffffffu, rlo, 31);
+      const int full_hi = hi_min >> 7, full_lo = (int)(((uint32_t)lo_max + kKv - 1) >> 7);
       float m_ref = neg_inf();
       bool all_set = false;  // every row of the warp has a reference
       uint64_t l2a = 0ull, l2b = 0ull;
@@ -765,6 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int c_lo = rlo - t * kKv, c_hi = rhi - t * kKv;  // columns the row attends to
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
+            if (t * kKv + 32 * j >= lo_max && hi_min - t * kKv >= 32 * j + 32) continue;  // uniform: kept by all rows
             const uint32_t keep = low_bits(c_hi - 32 * j) & ~low_bits(c_lo - 32 * j);
 #pragma unroll
             for (int i = 0; i < 32; ++i) v[j][i] = (keep >> i) & 1 ? v[j][i] : 0xff800000u;
@@ -833,7 +843,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 
       // The row's state.
-      const bool cut = it.c0 != it.c1, mine = hi > lo;
+      const bool cut = it.c0 != it.c1, mine = hi > lo, rows_here = row0 >= 0 && row0 < n_rows;  // (uniform)
+      if (!cut && !mine && !rows_here) continue;
       const int slot = slot_of((int)blockIdx.x, it.c0);
       const int k_lo = max(rlo, it.t0 * kKv), k_hi = min(rhi, it.t1 * kKv);  // tokens of the piece that the row attends to
       const int64_t out = ((int64_t)it.q_row + row / p.g) * p.hq + it.kvh * p.g + row % p.g;
@@ -850,7 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t finite = 0ull;  // 0 times all of the row's O
       const uint64_t inv2 = pk2(inv, inv);
 #pragma unroll 1
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 4 && rows_here; ++j) {
         uint32_t v[32];
         float o[32];
         __syncwarp();  // the TMEM loads are the whole warp's
@@ -886,7 +897,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();  // O has been read out: the next P's arrival says so
       for (uint32_t todo = __ballot_sync(0xffffffffu, bad && valid); todo; todo &= todo - 1) {
-        const int j = __ffs(todo) - 1, r = x * kHalf + quad * 32 + j;
+        const int j = __ffs(todo) - 1, r = row0 + j;
         const int64_t at = __shfl_sync(0xffffffffu, out, j);
         float o[4], again;
         slow_row<T>(p, it.b, it.kvh, at, __shfl_sync(0xffffffffu, k_lo, j), __shfl_sync(0xffffffffu, k_hi, j), o, again);

@@ -44,7 +44,7 @@
 //
 // Values that a row does not attend to meet P = 0, and 0 times an infinity or a
 // NaN would be NaN: slots behind the length are zeroed in the V tile, and a row
-// whose O is not finite is computed again key by key (slow_row), so such a value
+// whose O is not finite is computed again key by key (slow_rows), so such a value
 // reaches exactly the rows that attend to it, at no cost where there is none.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -253,45 +253,72 @@ __device__ __forceinline__ float* part_row(const ChunkParams& p, int slot, int c
 }
 __device__ __forceinline__ int slot_of(int c, int c0) { return 2 * c + (c == c0 ? 1 : 0); }
 
-// One row again, by one warp, key by key over tokens [lo, hi): for rows whose O
-// is not finite, where a value that the row does not attend to may have met
-// P = 0.  Four elements a lane; returns the row's state.
+// The tokens [lo, hi) that a row at position pos attends to.
+__device__ __forceinline__ void tokens_of(const ChunkParams& p, int pos, int len, int& lo, int& hi) {
+  hi = p.causal ? min(len, pos + 1) : len;
+  lo = p.window ? (int)max((int64_t)0, (int64_t)pos - p.window + 1) : 0;
+}
+
+// Rows again (row0 + the bits of todo), by one warp, key by key over the piece's
+// tiles [t0, t1): for rows whose O is not finite, where a value that the row does
+// not attend to may have met P = 0.  Four elements a lane.  slot: the partial
+// states' place, or -1 for an item that is not cut.  (Out of line, with the item's
+// fields by value: nothing of it is held in the loops of those who call it.)
 template <typename T>
-__device__ __noinline__ void slow_row(const ChunkParams& p, int b, int kvh, int64_t q_index, int lo, int hi, float (&o)[4],
-                                      float& lse2) {
+__device__ __noinline__ void slow_rows(const ChunkParams& p, uint32_t todo, int row0, int b, int kvh, int q_row, int pos0,
+                                       int len, int t0, int t1, int slot) {
   const int lane = threadIdx.x & 31;
-  const uint2 qw = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.q) + q_index * PKC_HEAD_DIM + 4 * lane);
-  const float2 q0 = Elem<T>::to_f2(qw.x), q1 = Elem<T>::to_f2(qw.y);
-  float m = neg_inf(), l = 0.f;
-  o[0] = o[1] = o[2] = o[3] = 0.f;
-  for (int t = lo; t < hi; ++t) {
-    const int64_t pi = t / p.page_size;
-    const int page = pi < p.bt_stride ? p.block_table[(int64_t)b * p.bt_stride + pi] : -1;
-    uint2 kw = make_uint2(0, 0), vw = make_uint2(0, 0);
-    if (page >= 0 && page < p.num_pages) {
-      const int64_t at = (((int64_t)page * p.page_size + t % p.page_size) * p.hkv + kvh) * PKC_HEAD_DIM + 4 * lane;
-      kw = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.k_cache) + at);
-      vw = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.v_cache) + at);
+  for (; todo; todo &= todo - 1) {
+    const int row = row0 + __ffs(todo) - 1;
+    const int64_t out = ((int64_t)q_row + row / p.g) * p.hq + kvh * p.g + row % p.g;
+    int lo, hi;
+    tokens_of(p, pos0 + row / p.g, len, lo, hi);
+    lo = max(lo, t0 * kKv);
+    hi = min(hi, t1 * kKv);
+    const uint2 qw = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.q) + out * PKC_HEAD_DIM + 4 * lane);
+    const float2 q0 = Elem<T>::to_f2(qw.x), q1 = Elem<T>::to_f2(qw.y);
+    float m = neg_inf(), l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int t = lo; t < hi; ++t) {
+      const int pi = t / p.page_size;
+      const int page = pi < p.bt_stride ? p.block_table[(int64_t)b * p.bt_stride + pi] : -1;
+      uint2 kw = make_uint2(0, 0), vw = make_uint2(0, 0);
+      if (page >= 0 && page < p.num_pages) {
+        const int64_t at = (((int64_t)page * p.page_size + t % p.page_size) * p.hkv + kvh) * PKC_HEAD_DIM + 4 * lane;
+        kw = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.k_cache) + at);
+        vw = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.v_cache) + at);
+      }
+      const float2 k0 = Elem<T>::to_f2(kw.x), k1 = Elem<T>::to_f2(kw.y);
+      float s = q0.x * k0.x + q0.y * k0.y + q1.x * k1.x + q1.y * k1.y;
+#pragma unroll
+      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
+      s *= p.scale_log2;
+      const float mn = fmaxf(m, s), ref = mn == neg_inf() ? 0.f : mn;
+      const float w = ex2(m - ref), e = ex2(s - ref);
+      m = mn;
+      l = l * w + e;
+      const float2 v0 = Elem<T>::to_f2(vw.x), v1 = Elem<T>::to_f2(vw.y);
+      o[0] = o[0] * w + e * v0.x;
+      o[1] = o[1] * w + e * v0.y;
+      o[2] = o[2] * w + e * v1.x;
+      o[3] = o[3] * w + e * v1.y;
     }
-    const float2 k0 = Elem<T>::to_f2(kw.x), k1 = Elem<T>::to_f2(kw.y);
-    float s = q0.x * k0.x + q0.y * k0.y + q1.x * k1.x + q1.y * k1.y;
+    const float inv = l == 0.f ? 0.f : 1.f / l, lse2 = l == 0.f ? neg_inf() : m + lg2(l);
 #pragma unroll
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    s *= p.scale_log2;
-    const float mn = fmaxf(m, s), ref = mn == neg_inf() ? 0.f : mn;
-    const float w = ex2(m - ref), e = ex2(s - ref);
-    m = mn;
-    l = l * w + e;
-    const float2 v0 = Elem<T>::to_f2(vw.x), v1 = Elem<T>::to_f2(vw.y);
-    o[0] = o[0] * w + e * v0.x;
-    o[1] = o[1] * w + e * v0.y;
-    o[2] = o[2] * w + e * v1.x;
-    o[3] = o[3] * w + e * v1.y;
+    for (int i = 0; i < 4; ++i) o[i] *= inv;
+    if (slot >= 0) {
+      *reinterpret_cast<float4*>(part_row(p, slot, lane, row)) = make_float4(o[0], o[1], o[2], o[3]);
+    } else if (p.out_dtype == PKC_F32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(p.o) + out * PKC_HEAD_DIM + 4 * lane) =
+          make_float4(o[0], o[1], o[2], o[3]);
+    } else {
+      *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + out * PKC_HEAD_DIM + 4 * lane) =
+          make_uint2(Elem<T>::from_f2(o[0], o[1]), Elem<T>::from_f2(o[2], o[3]));
+    }
+    if (lane == 0) {
+      if (slot >= 0) p.part_lse[slot * kRows + row] = lse2;
+      else p.lse[out] = lse2 * kLn2;
+    }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = o[i] * inv;
-  lse2 = l == 0.f ? neg_inf() : m + lg2(l);
 }
 
 // The merge of an item's partial states by the eight softmax warps: a warp takes
@@ -422,11 +449,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     return it.b >= 0;
   };
 
-  // 512 threads start with 128 registers each: the softmax warps take 192 and
-  // leave the others 64 (65,536 together).  Every role's code lies behind its own
+  // 512 threads start with 128 registers each: the softmax warps take 216 and
+  // leave the others 40 (65,536 together).  Every role's code lies behind its own
   // setmaxnreg, so the compiler keeps within it.
   if (warp >= kQkWarp) {
-  regs_down<64>();
+  regs_down<40>();
   if (warp == kSchedWarp) {
     // ---------------- scheduler ----------------
     auto load = [&](int b) -> Request {  // an empty request where there is nothing to do
@@ -696,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             s_par ^= 1;
             tc_fence_after();
             if (elect_one()) {
-#pragma unroll
+#pragma unroll 2
               for (int kk = 0; kk < 8; ++kk) {
                 const uint32_t off = (kk >> 2) * (kSub >> 4) + (kk & 3) * 2;
                 tc_mma_f16(tmem, desc_q + x * (kTileBytes >> 4) + off, desc_k + at + off, idesc_qk, kk > 0);
@@ -712,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
             if (elect_one()) {
               const uint32_t more = t > lo ? 1u : 0u;
-#pragma unroll
+#pragma unroll 2
               for (int kk = 0; kk < 8; ++kk)
                 tc_mma_f16_ta(tmem + 256 + x * 128, tmem + 128 + x * 64 + kk * 8, desc_v + at + kk * (2048 >> 4), idesc_pv,
                               kk > 0 ? 1u : more);
@@ -735,7 +762,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   } else {
     // ---------------- softmax, epilogue, merge: a row per thread ----------------
-    regs_up<192>();
+    regs_up<216>();
     const int x = warp >> 2, quad = warp & 3;
     const uint32_t t_lane = tmem + ((uint32_t)(quad * 32) << 16);
     const uint32_t t_s = t_lane, t_p = t_lane + 128 + x * 64, t_o = t_lane + 256 + x * 128;
@@ -749,8 +776,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n_rows = it.n_tok * p.g;
       const int pos = it.pos0 + row / p.g;
       const bool valid = row >= 0 && row < n_rows;
-      const int rhi = p.causal ? min(it.len, pos + 1) : it.len;
-      const int rlo = p.window ? (int)max((int64_t)0, (int64_t)pos - p.window + 1) : 0;
+      int rlo, rhi;
+      tokens_of(p, pos, it.len, rlo, rhi);
       const int lo = x ? it.lo[1] : it.lo[0], hi = x ? it.hi[1] : it.hi[0];
       // tiles [full_lo, full_hi) that all the warp's rows attend to whole: the first
       // row's end and the last row's begin decide
@@ -896,25 +923,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         bad = !(z.x + z.y == 0.f);
       }
       tc_fence_before();  // O has been read out: the next P's arrival says so
-      for (uint32_t todo = __ballot_sync(0xffffffffu, bad && valid); todo; todo &= todo - 1) {
-        const int j = __ffs(todo) - 1, r = row0 + j;
-        const int64_t at = __shfl_sync(0xffffffffu, out, j);
-        float o[4], again;
-        slow_row<T>(p, it.b, it.kvh, at, __shfl_sync(0xffffffffu, k_lo, j), __shfl_sync(0xffffffffu, k_hi, j), o, again);
-        if (cut) {
-          *reinterpret_cast<float4*>(part_row(p, slot, lane, r)) = make_float4(o[0], o[1], o[2], o[3]);
-        } else if (p.out_dtype == PKC_F32) {
-          *reinterpret_cast<float4*>(static_cast<float*>(p.o) + at * PKC_HEAD_DIM + 4 * lane) =
-              make_float4(o[0], o[1], o[2], o[3]);
-        } else {
-          *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + at * PKC_HEAD_DIM + 4 * lane) =
-              make_uint2(Elem<T>::from_f2(o[0], o[1]), Elem<T>::from_f2(o[2], o[3]));
-        }
-        if (lane == 0) {
-          if (cut) p.part_lse[slot * kRows + r] = again;
-          else p.lse[at] = again * kLn2;
-        }
-      }
+      if (const uint32_t todo = __ballot_sync(0xffffffffu, bad && valid); todo)
+        slow_rows<T>(p, todo, row0, it.b, it.kvh, it.q_row, it.pos0, it.len, it.t0, it.t1, cut ? slot : -1);
 
       if (cut) {
         // The block whose piece is the item's last one to be there merges all.

@@ -737,7 +737,9 @@ int pkc_release_pages(int32_t* block_table, int block_table_stride,
  * outgrow the table, and one whose last, partly filled page is not there are
  * not served either and count for no pages (PKC_ERR_BLOCK_TABLE).  A
  * new_indptr that does not run upwards within 0 .. total_new serves nobody
- * (PKC_ERR_PLAN).  One launch.
+ * (PKC_ERR_PLAN).  One launch, two from 8193 tokens on; the second reads a word
+ * of the workspace's status block, so a workspace must not be shared by two of
+ * these calls in flight.
  */
 int pkc_assign_pages(int32_t* block_table, int block_table_stride,
                      const int32_t* cache_seqlens, const int32_t* new_indptr,

@@ -8,11 +8,13 @@
 // position len_b + i has in that table.  A map instead of a list of free pages
 // makes the result independent of the order in which pages came back.
 //
-// assign: one launch of one cluster, for all of it is a chain of scans
-// (lengths, map) with a few bytes behind it.  Every block scans the lengths and
-// counts the map for itself (both small, from L2); the map's chunks and the
-// tokens are shared out over the blocks, with a cluster barrier before the map
-// changes and one before the tokens read the table.
+// assign is a chain of scans (lengths, map) with a few bytes behind it, so it is
+// bound by latency: one cluster of blocks, every one of which scans the lengths
+// and counts the map for itself (both small, from L2), with the map's chunks
+// shared out over the blocks.  Up to kFewTokens tokens the same launch fills in
+// their places; more go to a second launch over all SMs, which begins while the
+// first one runs and finds what it needs of a request at its first token (220,453
+// tokens of 300 requests: a cluster of 8 took 44 us for all, the two take 15).
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -30,6 +32,7 @@ namespace cg = cooperative_groups;
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;  // portable
+constexpr int kFewTokens = 8192;
 constexpr int kMaxChunks = (int)(PKC_PAGES_MAX_PAGES / 32 / kThreads);
 
 __device__ __forceinline__ int sat_add(int a, int b) {  // both >= 0
@@ -79,17 +82,37 @@ __device__ __forceinline__ int last_not_above(const int* a, int n, int x) {
   return lo;
 }
 
+// The place of request b's token at position pos.
+__device__ __forceinline__ int64_t slot_at(const PagesParams& p, int b, int pos) {
+  return (int64_t)__ldcg(p.block_table + (int64_t)b * p.bt_stride + pos / p.page_size) * p.page_size + pos % p.page_size;
+}
+
+// kAll: every token's place; else that of each request's first one, which with
+// the flag in the status block is all that places_kernel needs.
+template <bool kAll>
 __global__ void __launch_bounds__(kThreads, 1) assign_pages_kernel(const PagesParams p) {
   extern __shared__ int smem[];
   int* off = smem;                       // [batch + 1] pages needed by the requests before b
   int* start = off + p.batch + 1;        // [batch + 1] new_indptr
-  int* ends = start + p.batch + 1;       // [batch] length with the new tokens, -1: not served for its own sake
-  int* chunk_base = ends + p.batch;      // [chunks + 1] free pages before each chunk of the map
+  int* lens = start + p.batch + 1;       // [batch] length; ~length: not served for its own sake
+  int* chunk_base = lens + p.batch;      // [chunks + 1] free pages before each chunk of the map
   __shared__ int sums[kWarps + 1];
   cg::cluster_group cluster = cg::this_cluster();
   const int n_blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31;
   const bool first_block = rank == 0;
+  auto sync_all = [&] {
+    if (n_blocks > 1) {
+      __threadfence();
+      cluster.sync();
+    } else {
+      __syncthreads();
+    }
+  };
+  grid_launch_dependents();
+  const int64_t words = (p.num_pages + 31) / 32;
+  const int chunks = (int)((words + kThreads - 1) / kThreads);
+  const uint32_t first_word = free_word(p, tid, words);  // on its way while the lengths are scanned
 
   // The ranges have to run upwards within 0 .. total, or nobody is served.
   bool wrong = false;
@@ -98,6 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1) assign_pages_kernel(const PagesPa
     start[b] = t;
     wrong = wrong || t < 0 || t > p.total || (b > 0 && t < p.indptr[b - 1]);
   }
+  for (int c = tid; c <= chunks; c += kThreads) chunk_base[c] = 0;
   wrong = __syncthreads_or(wrong);
   if (wrong && first_block && tid == 0) report(p.status, PKC_ERR_PLAN);
 
@@ -108,9 +132,8 @@ __global__ void __launch_bounds__(kThreads, 1) assign_pages_kernel(const PagesPa
     int need = 0;
     if (b < p.batch) {
       const int len = p.cache_seqlens[b], n = wrong ? 0 : start[b + 1] - start[b];
-      const int64_t end = (int64_t)len + n;
       const int64_t have = ((int64_t)len + p.page_size - 1) / p.page_size;
-      const int64_t want = (end + p.page_size - 1) / p.page_size;
+      const int64_t want = ((int64_t)len + n + p.page_size - 1) / p.page_size;
       bool ok = len >= 0 && !wrong;
       if (ok && n > 0) {
         ok = want <= p.bt_stride;
@@ -120,7 +143,7 @@ __global__ void __launch_bounds__(kThreads, 1) assign_pages_kernel(const PagesPa
         }
       }
       if (!ok && !wrong && (len < 0 || n > 0) && first_block) report(p.status, PKC_ERR_BLOCK_TABLE);
-      ends[b] = ok ? (int)end : -1;
+      lens[b] = ok ? len : ~max(len, 0);
       if (ok) need = (int)(want - have);
     }
     int total;
@@ -131,32 +154,45 @@ __global__ void __launch_bounds__(kThreads, 1) assign_pages_kernel(const PagesPa
   if (tid == 0) off[p.batch] = needed;
 
   // Free pages before each chunk of kThreads words.
-  const int64_t words = (p.num_pages + 31) / 32;
-  const int chunks = (int)((words + kThreads - 1) / kThreads);
-  int n_free = 0;
   if (needed > 0) {  // uniform
     for (int c = 0; c < chunks; ++c) {
-      if (tid == 0) chunk_base[c] = n_free;
-      int total;
-      block_scan(__popc(free_word(p, (int64_t)c * kThreads + tid, words)), sums, total);
-      n_free += total;
+      const uint32_t x = c == 0 ? first_word : free_word(p, (int64_t)c * kThreads + tid, words);
+      const int n = __reduce_add_sync(0xffffffffu, __popc(x));
+      if (lane == 0) atomicAdd(chunk_base + c, n);
+    }
+    __syncthreads();
+    if (tid < 32) {  // exclusive, in place
+      int before = 0;
+      for (int c0 = 0; c0 <= chunks; c0 += 32) {
+        const int c = c0 + lane, n = c < chunks ? chunk_base[c] : 0;
+        int x = n;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, x, d);
+          if (lane >= d) x += y;
+        }
+        if (c <= chunks) chunk_base[c] = before + x - n;
+        before += __shfl_sync(0xffffffffu, x, 31);
+      }
     }
   }
+  __syncthreads();
+  const int n_free = chunk_base[chunks];
   // Requests are served while the pages last; off does not descend, so the
   // first that does not fit ends it for all that need a page.
-  __syncthreads();
   int taken = needed;
   if (needed > n_free) {  // uniform
     taken = off[last_not_above(off, p.batch + 1, n_free)];
     if (first_block && tid == 0) report(p.status, PKC_ERR_NO_PAGES);
   }
-  cluster.sync();  // every block has read the map
+  auto served = [&](int b) { return lens[b] >= 0 && (off[b + 1] <= taken || off[b + 1] == off[b]); };
+  if (n_blocks > 1) sync_all();  // every block has read the map
 
   // The taken pages to the table, their bits cleared.
   for (int c = rank; c < chunks && taken > 0; c += n_blocks) {
     if (chunk_base[c] >= taken) break;  // uniform
     const int64_t w = (int64_t)c * kThreads + tid;
-    const uint32_t x = free_word(p, w, words);
+    const uint32_t x = c == 0 ? first_word : free_word(p, w, words);
     int total;
     int r = chunk_base[c] + block_scan(__popc(x), sums, total);
     uint32_t gone = 0;
@@ -165,37 +201,75 @@ __global__ void __launch_bounds__(kThreads, 1) assign_pages_kernel(const PagesPa
       for (uint32_t y = x; y && r < taken; y &= y - 1, ++r) {
         const int bit = __ffs(y) - 1;
         while (off[b + 1] <= r) ++b;
-        const int have = (int)(((int64_t)p.cache_seqlens[b] + p.page_size - 1) / p.page_size);
+        const int have = (int)(((int64_t)lens[b] + p.page_size - 1) / p.page_size);
         p.block_table[(int64_t)b * p.bt_stride + have + (r - off[b])] = (int)(32 * w) + bit;
         gone |= 1u << bit;
       }
       p.free_pages[w] &= ~gone;
     }
   }
-  __threadfence();
-  cluster.sync();  // the table is complete
+  sync_all();  // the table is complete
 
-  // Where every token goes, and the lengths.
-  for (int t = rank * kThreads + tid; t < p.total; t += n_blocks * kThreads) {
-    int64_t slot = -1;
-    int pos = 0;
-    if (!wrong && p.batch && t >= start[0] && t < start[p.batch]) {
-      const int b = last_not_above(start, p.batch + 1, t);
-      const int end = ends[b];
-      pos = p.cache_seqlens[b] + (t - start[b]);
-      if (end >= 0 && (off[b + 1] <= taken || off[b + 1] == off[b]))
-        slot = (int64_t)__ldcg(p.block_table + (int64_t)b * p.bt_stride + pos / p.page_size) * p.page_size +
-               pos % p.page_size;
+  // Where the tokens go, and the lengths.
+  if (kAll) {
+    for (int t = rank * kThreads + tid; t < p.total; t += n_blocks * kThreads) {
+      int64_t slot = -1;
+      int pos = 0;
+      if (!wrong && p.batch && t >= start[0] && t < start[p.batch]) {
+        const int b = last_not_above(start, p.batch + 1, t);
+        pos = (lens[b] >= 0 ? lens[b] : p.cache_seqlens[b]) + (t - start[b]);
+        if (served(b)) slot = slot_at(p, b, pos);
+      }
+      p.slots[t] = slot;
+      p.positions[t] = pos;
     }
-    p.slots[t] = slot;
+  } else {
+    for (int b = rank * kThreads + tid; b < p.batch; b += n_blocks * kThreads)
+      if (!wrong && start[b + 1] > start[b]) {
+        const int len = lens[b] >= 0 ? lens[b] : p.cache_seqlens[b];
+        p.slots[start[b]] = served(b) ? slot_at(p, b, len) : -1;
+        p.positions[start[b]] = len;
+      }
+    if (first_block && tid == 0) p.status[PKC_ASSIGN_FLAG] = wrong || p.batch == 0;
+  }
+  sync_all();  // the lengths have been read: they may be the ones that grow
+  if (first_block && p.seqlens_out)
+    for (int b = tid; b < p.batch; b += kThreads)
+      p.seqlens_out[b] = served(b) ? lens[b] + (start[b + 1] - start[b]) : p.cache_seqlens[b];
+}
+
+constexpr int kPlaceThreads = 256;
+constexpr int kPlaceTokens = 4;  // a thread's, one after another
+
+// The places of the tokens behind each request's first one.
+__global__ void __launch_bounds__(kPlaceThreads) places_kernel(const PagesParams p) {
+  grid_wait_prerequisites();
+  const bool wrong = __ldcg(p.status + PKC_ASSIGN_FLAG) != 0;  // (or no requests at all)
+  const int64_t t0 = ((int64_t)blockIdx.x * kPlaceThreads + threadIdx.x) * kPlaceTokens;
+  if (t0 >= p.total) return;
+  const int t1 = (int)min((int64_t)p.total, t0 + kPlaceTokens);
+  const int begin = wrong ? p.total : p.indptr[0], end = wrong ? p.total : p.indptr[p.batch];
+  int b = -1, from = 0, to = 0, len = 0;  // the request of the tokens [from, to)
+  bool served = false;
+  for (int t = (int)t0; t < t1; ++t) {
+    if (t < begin || t >= end) {
+      p.slots[t] = -1;
+      p.positions[t] = 0;
+      continue;
+    }
+    if (b < 0 || t >= to) {
+      if (b < 0) b = last_not_above(p.indptr, p.batch + 1, t);
+      else do ++b; while (p.indptr[b + 1] <= t);
+      from = p.indptr[b];
+      to = p.indptr[b + 1];
+      served = __ldcg(p.slots + from) >= 0;
+      len = __ldcg(p.positions + from);
+    }
+    if (t == from) continue;
+    const int pos = len + (t - from);
+    p.slots[t] = served ? slot_at(p, b, pos) : -1;
     p.positions[t] = pos;
   }
-  cluster.sync();  // the lengths have been read: they may be the ones that grow
-  if (first_block && p.seqlens_out)
-    for (int b = tid; b < p.batch; b += kThreads) {
-      const bool served = ends[b] >= 0 && (off[b + 1] <= taken || off[b + 1] == off[b]);
-      p.seqlens_out[b] = served ? ends[b] : p.cache_seqlens[b];
-    }
 }
 
 constexpr int kReleaseThreads = 256;
@@ -243,22 +317,15 @@ int launch_release_pages(const PagesParams& p, void* stream) {
   return (int)cudaGetLastError();
 }
 
-int launch_assign_pages(const PagesParams& p, void* stream) {
-  if (p.batch <= 0 && p.total <= 0) return 0;
+template <bool kAll>
+static int launch_assign(const PagesParams& p, int blocks, int smem, void* stream) {
   static std::atomic<uint64_t> raised{0};
   constexpr int kMost = 4 * (3 * PKC_PAGES_MAX_BATCH + 2 + kMaxChunks + 1);
-  if (const int e = raise_smem_limit((const void*)assign_pages_kernel, kMost, raised)) return e;
-  const int64_t words = (p.num_pages + 31) / 32;
-  const int chunks = (int)((words + kThreads - 1) / kThreads);
-  // A block per 4096 tokens or per chunk of the map, whichever are more, in
-  // one cluster.
-  const int64_t parts = std::max<int64_t>(((int64_t)p.total + 4095) / 4096, chunks);
-  int blocks = 1;
-  while (blocks < kMaxCluster && blocks < parts) blocks *= 2;
+  if (const int e = raise_smem_limit((const void*)assign_pages_kernel<kAll>, kMost, raised)) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(blocks);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = 4 * (size_t)(3 * p.batch + 2 + chunks + 1);
+  cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = (cudaStream_t)stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -266,7 +333,24 @@ int launch_assign_pages(const PagesParams& p, void* stream) {
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return (int)cudaLaunchKernelEx(&cfg, assign_pages_kernel, p);
+  return (int)cudaLaunchKernelEx(&cfg, assign_pages_kernel<kAll>, p);
+}
+
+int launch_assign_pages(const PagesParams& p, void* stream) {
+  if (p.batch <= 0 && p.total <= 0) return 0;
+  const int64_t words = (p.num_pages + 31) / 32;
+  const int chunks = (int)((words + kThreads - 1) / kThreads);
+  const int smem = 4 * (3 * p.batch + 2 + chunks + 1);
+  const bool all = p.total <= kFewTokens;
+  // a block per 4096 tokens or per chunk of the map, whichever are more
+  const int64_t parts = std::max<int64_t>(all ? ((int64_t)p.total + 4095) / 4096 : 1, chunks);
+  int blocks = 1;
+  while (blocks < kMaxCluster && blocks < parts) blocks *= 2;
+  if (all) return launch_assign<true>(p, blocks, smem, stream);
+  if (const int e = launch_assign<false>(p, blocks, smem, stream)) return e;
+  const int per = kPlaceThreads * kPlaceTokens;
+  return launch_programmatic(places_kernel, dim3((unsigned)(((int64_t)p.total + per - 1) / per)), dim3(kPlaceThreads), 0,
+                             (cudaStream_t)stream, p);
 }
 
 }  // namespace pkc

@@ -13,12 +13,14 @@
 // The status block at the start of every workspace: word 0 is the status
 // word (pkc_device_status), words 16-17 the dynamic decode queue's counters,
 // words 18-19 the mx4 append's count of finished blocks and its flag for a
-// missing page, words 20-21 the same of the eviction's compact, word 32 the
-// result of pkc_selftest_wait_timeout, words 40-49 the chunk attention's bits
-// for partial states that are there.
+// missing page, words 20-21 the same of the eviction's compact, word 22 a flag
+// between assign_pages' launches, word 32 the result of
+// pkc_selftest_wait_timeout, words 40-49 the chunk attention's bits for partial
+// states that are there.
 #define PKC_STATUS_BYTES 256
 #define PKC_APPEND_COUNTER 18
 #define PKC_COMPACT_COUNTER 20
+#define PKC_ASSIGN_FLAG 22
 #define PKC_CHUNK_READY 40
 // Limits of the calls over the pool of free pages (pages.cu keeps the
 // requests' offsets and the pool's counts in shared memory).

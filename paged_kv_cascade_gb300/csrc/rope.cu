@@ -151,13 +151,12 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams 
 
 template <typename T, bool kE4m3>
 int launch_t(const RopeParams& p, cudaStream_t st) {
-  // One warp per token; a token's groups of rows go to blocks of their own
-  // while there are few tokens.
+  // One warp per token.  While that leaves room on the SMs, a token's groups of
+  // rows are shared out over blocks of their own (each works out the sines again).
   const int64_t parts = ((int64_t)p.hq + 2 * p.hkv + kGroup - 1) / kGroup;
   const int64_t want = ((int64_t)p.total + kWarps - 1) / kWarps;
   const int64_t most = (int64_t)num_sms() * (2048 / kThreads);
-  dim3 grid((unsigned)std::min(want, most), 1);
-  if (want * parts <= most && parts <= 65535) grid.y = (unsigned)parts;
+  const dim3 grid((unsigned)std::min(want, most), (unsigned)std::max<int64_t>(1, std::min<int64_t>(parts, most / want)));
   rope_append_kernel<T, kE4m3><<<grid, kThreads, 0, st>>>(p);
   return (int)cudaGetLastError();
 }

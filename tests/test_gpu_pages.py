@@ -118,6 +118,29 @@ def test_rows_of_no_request_and_empty_batches():
     run.check(0)
 
 
+@pytest.mark.parametrize("num_pages", [700, 1400])
+def test_many_tokens(num_pages):
+    """More tokens than one launch places, with and without enough pages, rows of no request on both sides."""
+    rng = np.random.default_rng(7)
+    new = rng.integers(0, 900, 25).tolist()
+    new[3] = new[24] = 0
+    lens, table, free = state(25, 16, num_pages, 200, 80, 11)
+    run = Run(lens, table, free, 16, num_pages)
+    run.assign(new, lead=37, trail=401, in_place=True)
+    run.assign(new)
+
+
+def test_many_tokens_of_nobody():
+    run = Run([3, 0], [[1, -1], [-1, -1]], {0, 2}, 4, 3)
+    table, lens = run.d_table[:0], run.d_lens[:0]
+    s, p, _ = pkc.assign_pages(table, lens, torch.zeros(1, dtype=I32, device="cuda"), 9000, run.d_free, 4, 3, run.ws)
+    assert (s == -1).all() and (p == 0).all()
+    wrong = torch.tensor([0, 8999, 8000], dtype=I32, device="cuda")
+    s, p, n = pkc.assign_pages(run.d_table, run.d_lens, wrong, 9000, run.d_free, 4, 3, run.ws)
+    assert (s == -1).all() and n.tolist() == [3, 0]
+    run.check(7)
+
+
 def test_served_in_order():
     """The second request is too large for what is left; a third that needs no page is served, a fourth that does is not."""
     run = Run([0, 0, 1, 0], [[-1] * 4, [-1] * 4, [9, -1, -1, -1], [-1] * 4], {3, 4, 5}, 4, 10)

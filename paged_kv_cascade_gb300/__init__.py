@@ -667,8 +667,8 @@ def release_pages(block_table, cache_seqlens, free_pages, page_size, num_pages, 
     free_pages (of page_pool), in place: their table entries become -1."""
     B, stride, num_pages, _ = _check_pages(block_table, cache_seqlens, free_pages, num_pages, workspace)
     _check(lib().pkc_release_pages(
-        _ptr(block_table), stride, _ptr(cache_seqlens), B, int(page_size), num_pages, _ptr(free_pages),
-        _ptr(workspace), workspace.numel(), _stream(stream)))
+        block_table.data_ptr(), stride, cache_seqlens.data_ptr(), B, int(page_size), num_pages, free_pages.data_ptr(),
+        workspace.data_ptr(), workspace.numel(), _stream(stream)))
 
 
 def assign_pages(block_table, cache_seqlens, new_indptr, total_new, free_pages, page_size, num_pages, workspace,
@@ -689,8 +689,8 @@ def assign_pages(block_table, cache_seqlens, new_indptr, total_new, free_pages, 
     _expect_all(dev, ("new_indptr", new_indptr, torch.int32, (B + 1,)), ("slots", slots, torch.int64, (total,)),
                 ("positions", positions, torch.int32, (total,)), ("seqlens_out", seqlens_out, torch.int32, (B,)))
     _check(lib().pkc_assign_pages(
-        _ptr(block_table), stride, _ptr(cache_seqlens), _ptr(new_indptr), total, B, int(page_size), num_pages,
-        _ptr(free_pages), _ptr(slots), _ptr(positions), _ptr(seqlens_out), _ptr(workspace), workspace.numel(),
+        block_table.data_ptr(), stride, cache_seqlens.data_ptr(), new_indptr.data_ptr(), total, B, int(page_size), num_pages,
+        free_pages.data_ptr(), slots.data_ptr(), positions.data_ptr(), seqlens_out.data_ptr(), workspace.data_ptr(), workspace.numel(),
         _stream(stream)))
     return slots, positions, seqlens_out
 
@@ -729,7 +729,7 @@ def _expect_rows(name, t, dtype, shape, device):
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
+    if t.get_device() != device.index:
         raise ValueError(f"{name} must be on {device}")
     st = t.stride()
     if st[2] != 1 or (st[1] != 128 and shape[1] != 1):
@@ -767,10 +767,10 @@ def rope_append_kv(q, k_new, v_new, positions, slots, inv_freq, k_cache, v_cache
         _expect("q_out", q_out, (dtype,), (T, Hq, 128), dev)
     code = F16 if dtype is torch.float16 else BF16
     _check(lib().pkc_rope_append_kv(
-        _ptr(q), q_stride, _ptr(k_new), _ptr(v_new), kv_stride, _ptr(positions), _ptr(slots), _ptr(inv_freq),
-        2 * half, 1 if interleaved else 0, float(amplitude), T, Hq, Hkv, 128, _ptr(q_out), _ptr(k_cache),
-        _ptr(v_cache), ps, P, float(k_scale), float(v_scale), code, E4M3 if kv_dtype is torch.uint8 else code,
-        _ptr(workspace), workspace.numel(), _stream(stream)))
+        q.data_ptr(), q_stride, k_new.data_ptr(), v_new.data_ptr(), kv_stride, positions.data_ptr(), slots.data_ptr(), inv_freq.data_ptr(),
+        2 * half, 1 if interleaved else 0, float(amplitude), T, Hq, Hkv, 128, q_out.data_ptr(), k_cache.data_ptr(),
+        v_cache.data_ptr(), ps, P, float(k_scale), float(v_scale), code, E4M3 if kv_dtype is torch.uint8 else code,
+        workspace.data_ptr(), workspace.numel(), _stream(stream)))
     return q_out
 
 
@@ -814,9 +814,9 @@ def paged_chunk_state(q, q_indptr, k_cache, v_cache, block_table, cache_seqlens,
         _expect("lse", lse, (torch.float32,), (T, Hq), dev)
     code = F16 if dtype is torch.float16 else BF16
     _check(lib().pkc_paged_chunk_state(
-        _ptr(q), _ptr(q_indptr), T, _ptr(k_cache), _ptr(v_cache), _ptr(block_table), stride, _ptr(cache_seqlens), B,
-        Hq, Hkv, 128, ps, P, float(sm_scale), 1 if causal else 0, int(window), _ptr(workspace), workspace.numel(),
-        _ptr(o), _ptr(lse), code, F32 if out_dtype is torch.float32 else code, _stream(stream)))
+        q.data_ptr(), q_indptr.data_ptr(), T, k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), stride, cache_seqlens.data_ptr(), B,
+        Hq, Hkv, 128, ps, P, float(sm_scale), 1 if causal else 0, int(window), workspace.data_ptr(), workspace.numel(),
+        o.data_ptr(), lse.data_ptr(), code, F32 if out_dtype is torch.float32 else code, _stream(stream)))
     return o, lse
 
 

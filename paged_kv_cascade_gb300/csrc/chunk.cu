@@ -83,6 +83,7 @@ struct Item {
   int pos0, len;         // position of the first token, cached tokens
   int t0, t1;            // KV tiles of the piece
   int lo[2], hi[2];      // those of half A, B (lo == hi: none)
+  int once;              // 1: no other item reads these keys
   int off;               // 0: rows 0-127 are A's; 128: B's, and A has none
   int c0, c1;            // first and last block with a piece of the item (c0 == c1: whole)
 };
@@ -329,17 +330,13 @@ __device__ __forceinline__ void merge_item(const ChunkParams& p, const Item& it,
 #pragma unroll 1
   for (int u = warp; u < 4 * groups; u += 8) {
     const int row = (u >> 2) * 32 + lane, chunk = (u & 3) * 8;
-    float m = neg_inf();
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) m = fmaxf(m, __ldcg(p.part_lse + slot_of(it.c0 + i, it.c0) * kRows + row));
-    const float ref = m == neg_inf() ? 0.f : m;
-    float l = 0.f, o[32];
+    float m = neg_inf(), l = 0.f, o[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) o[i] = 0.f;
 #pragma unroll 1
     for (int i0 = 0; i0 < n; i0 += 2) {
       float4 x[2][8];
-      float w[2];
+      float w[2], now = m;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int slot = slot_of(it.c0 + min(i0 + i, n - 1), it.c0);
@@ -348,16 +345,23 @@ __device__ __forceinline__ void merge_item(const ChunkParams& p, const Item& it,
         for (int k = 0; k < 8; ++k) x[i][k] = __ldcg(reinterpret_cast<const float4*>(part_row(p, slot, chunk + k, row)));
       }
 #pragma unroll
+      for (int i = 0; i < 2; ++i) now = fmaxf(now, w[i]);  // (the last one again where there are fewer)
+      const float ref = now == neg_inf() ? 0.f : now, f = ex2(m - ref);
+      m = now;
+      l *= f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) o[i] *= f;
+#pragma unroll
       for (int i = 0; i < 2; ++i) {
         if (i0 + i >= n) break;
-        const float f = ex2(w[i] - ref);
-        l += f;
+        const float e = ex2(w[i] - ref);
+        l += e;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          o[4 * k] += f * x[i][k].x;
-          o[4 * k + 1] += f * x[i][k].y;
-          o[4 * k + 2] += f * x[i][k].z;
-          o[4 * k + 3] += f * x[i][k].w;
+          o[4 * k] += e * x[i][k].x;
+          o[4 * k + 1] += e * x[i][k].y;
+          o[4 * k + 2] += e * x[i][k].z;
+          o[4 * k + 3] += e * x[i][k].w;
         }
       }
     }
@@ -574,6 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               it.lo[x] = max(it.lo[x], it.t0);
               it.hi[x] = max(it.lo[x], min(it.hi[x], it.t1));
             }
+            it.once = nt == 1;
             it.off = 0;
             if (n_tok <= half) {  // every second item of few rows goes to B: one's epilogue runs beside the other's tiles
               it.off = turn ? kHalf : 0;
@@ -632,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kKWarp || warp == kVWarp) {
     // ---------------- K copies, V copies ----------------
-    const uint64_t pol = l2_policy_evict_last();
+    const uint64_t keep = l2_policy_evict_last(), pass_by = l2_policy_evict_first();
     const int bs = p.box_tokens, boxes = 2 * (kKv / bs);  // box c: tokens (c / 2) bs .. of the tile, dims 64 (c % 2) ..
     const int no_page = (int)max((int64_t)1, p.num_pages);   // outside the pool: read as zeros
     const void* tmap = warp == kVWarp ? (const void*)&tm_v : (const void*)&tm_k;
@@ -649,6 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int pi = token / p.page_size;
         return pi < p.bt_stride ? table[pi] : -1;
       };
+      const uint64_t pol = it.once ? pass_by : keep;
       int ahead = page_of(it.t0, lane);
       for (int t = it.t0; t < it.t1; ++t, ++g) {
         const int page = ahead, st = first + g % stages;

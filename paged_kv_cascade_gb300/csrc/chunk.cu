@@ -44,8 +44,10 @@
 //
 // Values that a row does not attend to meet P = 0, and 0 times an infinity or a
 // NaN would be NaN: slots behind the length are zeroed in the V tile, and a row
-// whose O is not finite is computed again key by key (slow_rows), so such a value
-// reaches exactly the rows that attend to it, at no cost where there is none.
+// whose O is not finite is computed again key by key (slow_rows) where its boundary
+// tiles hold such a value, so it reaches exactly the rows that attend to it, at no
+// cost where there is none.  So are rows whose scores pass 2^20: a float32 exponent
+// holds too little of them for one rounding.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -76,6 +78,11 @@ constexpr int kTileCost = 5, kHalfTileCost = 4, kOver = 17;
 constexpr int kMinCost = 20;             // least cost of a block
 constexpr int kShort = 16;               // items of at most so many tiles are not cut: a cut costs some 16 us
 constexpr float kMoveSum = 8192.f;       // a tile's sum of P above which its reference maximum moves
+
+// P = exp2(s c - m_ref) in one rounding: m_ref = max s c is rounded, P's largest is
+// exp2 of that rounding, at most 2^(m_ref / 2^24).  Rows with |m_ref| from here on are
+// computed again with the product rounded too (slow_rows).
+constexpr float kFar = 1048576.f;
 
 struct Item {
   int b;                 // request; -1: no more items
@@ -260,48 +267,102 @@ __device__ __forceinline__ void tokens_of(const ChunkParams& p, int pos, int len
   lo = p.window ? (int)max((int64_t)0, (int64_t)pos - p.window + 1) : 0;
 }
 
-// Rows again (row0 + the bits of todo), by one warp, key by key over the piece's
-// tiles [t0, t1): for rows whose O is not finite, where a value that the row does
-// not attend to may have met P = 0.  Four elements a lane.  slot: the partial
+// Pages of the keys t0 .. t0 + 31 of request b, a lane each (-1: none there).
+__device__ __forceinline__ int page_of_key(const ChunkParams& p, int b, int t, int end) {
+  if (t < 0 || t >= end) return -1;  // (t < 0: past 2^31)
+  const int pi = t / p.page_size;
+  const int page = pi < p.bt_stride ? p.block_table[(int64_t)b * p.bt_stride + pi] : -1;
+  return page < p.num_pages ? page : -1;
+}
+
+// Rows again (row0 + a bit), by one warp, key by key over the piece's tiles
+// [t0, t1).  `far`: rows whose scores lie so far out (kFar) that s c - m_ref in one
+// rounding is off by too much; here the product is rounded before the maximum is
+// taken off, so the largest weight is 1.  `odd`: rows whose O is not finite.  They
+// are right as they are unless a value that not all rows attend to, in the tiles
+// [t0, t0 x) and [y t1, t1) -- the keys outside [all_lo, all_hi) -- is not finite
+// itself.  Lanes hold four elements each; eight keys go at once.  slot: the partial
 // states' place, or -1 for an item that is not cut.  (Out of line, with the item's
 // fields by value: nothing of it is held in the loops of those who call it.)
 template <typename T>
-__device__ __noinline__ void slow_rows(const ChunkParams& p, uint32_t todo, int row0, int b, int kvh, int q_row, int pos0,
-                                       int len, int t0, int t1, int slot) {
+__device__ __noinline__ void slow_rows(const ChunkParams& p, uint32_t far, uint32_t odd, int row0, int b, int kvh, int q_row,
+                                       int pos0, int len, int t0, int t1, int all_lo, int all_hi, int slot) {
   const int lane = threadIdx.x & 31;
-  for (; todo; todo &= todo - 1) {
-    const int row = row0 + __ffs(todo) - 1;
+  const int begin = t0 * kKv, end = (int)min((int64_t)len, (int64_t)t1 * kKv);
+  auto at = [&](int page, int t) { return (((int64_t)page * p.page_size + t % p.page_size) * p.hkv + kvh) * PKC_HEAD_DIM + 4 * lane; };
+  if (odd) {
+    float sum = 0.f;  // 0 times the values
+    for (int64_t t = begin; t < end; t += 32) {
+      if (t >= all_lo && t + 32 <= all_hi) {
+        t += (all_hi - t - 32) & ~31;
+        continue;
+      }
+      const int pages = page_of_key(p, b, (int)t + lane, end);
+#pragma unroll 8
+      for (int i = 0; i < 32; ++i) {
+        const int page = __shfl_sync(0xffffffffu, pages, i);
+        if (page < 0) continue;
+        const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.v_cache) + at(page, (int)t + i));
+        const float2 a = Elem<T>::to_f2(w.x), c = Elem<T>::to_f2(w.y);
+        sum += 0.f * a.x + 0.f * a.y + 0.f * c.x + 0.f * c.y;
+      }
+    }
+    if (__any_sync(0xffffffffu, !(sum == 0.f))) far |= odd;
+  }
+  for (; far; far &= far - 1) {
+    const int row = row0 + __ffs(far) - 1;
     const int64_t out = ((int64_t)q_row + row / p.g) * p.hq + kvh * p.g + row % p.g;
     int lo, hi;
     tokens_of(p, pos0 + row / p.g, len, lo, hi);
-    lo = max(lo, t0 * kKv);
-    hi = min(hi, t1 * kKv);
+    lo = max(lo, begin);
+    hi = min(hi, end);
     const uint2 qw = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.q) + out * PKC_HEAD_DIM + 4 * lane);
     const float2 q0 = Elem<T>::to_f2(qw.x), q1 = Elem<T>::to_f2(qw.y);
     float m = neg_inf(), l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int t = lo; t < hi; ++t) {
-      const int pi = t / p.page_size;
-      const int page = pi < p.bt_stride ? p.block_table[(int64_t)b * p.bt_stride + pi] : -1;
-      uint2 kw = make_uint2(0, 0), vw = make_uint2(0, 0);
-      if (page >= 0 && page < p.num_pages) {
-        const int64_t at = (((int64_t)page * p.page_size + t % p.page_size) * p.hkv + kvh) * PKC_HEAD_DIM + 4 * lane;
-        kw = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.k_cache) + at);
-        vw = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.v_cache) + at);
-      }
-      const float2 k0 = Elem<T>::to_f2(kw.x), k1 = Elem<T>::to_f2(kw.y);
-      float s = q0.x * k0.x + q0.y * k0.y + q1.x * k1.x + q1.y * k1.y;
+    for (int64_t tb = lo; tb < hi; tb += 32) {
+      const int pages = page_of_key(p, b, (int)tb + lane, hi);
+#pragma unroll 1
+      for (int i0 = 0; i0 < 32 && tb + i0 < hi; i0 += 8) {
+        uint2 vw[8];
+        float s[8];
 #pragma unroll
-      for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-      s *= p.scale_log2;
-      const float mn = fmaxf(m, s), ref = mn == neg_inf() ? 0.f : mn;
-      const float w = ex2(m - ref), e = ex2(s - ref);
-      m = mn;
-      l = l * w + e;
-      const float2 v0 = Elem<T>::to_f2(vw.x), v1 = Elem<T>::to_f2(vw.y);
-      o[0] = o[0] * w + e * v0.x;
-      o[1] = o[1] * w + e * v0.y;
-      o[2] = o[2] * w + e * v1.x;
-      o[3] = o[3] * w + e * v1.y;
+        for (int i = 0; i < 8; ++i) {
+          const int page = __shfl_sync(0xffffffffu, pages, i0 + i);
+          uint2 kw = make_uint2(0, 0);
+          vw[i] = make_uint2(0, 0);
+          if (page >= 0) {
+            const int64_t x = at(page, (int)tb + i0 + i);
+            kw = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.k_cache) + x);
+            vw[i] = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.v_cache) + x);
+          }
+          const float2 k0 = Elem<T>::to_f2(kw.x), k1 = Elem<T>::to_f2(kw.y);
+          s[i] = q0.x * k0.x + q0.y * k0.y + q1.x * k1.x + q1.y * k1.y;
+        }
+        float mn = m;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+#pragma unroll
+          for (int d = 16; d; d >>= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], d);
+          s[i] = tb + i0 + i < hi ? __fmul_rn(s[i], p.scale_log2) : neg_inf();
+          mn = fmaxf(mn, s[i]);
+        }
+        const float ref = mn == neg_inf() ? 0.f : mn, w = ex2(m - ref);
+        m = mn;
+        l *= w;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] *= w;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (tb + i0 + i >= hi) break;
+          const float e = ex2(__fsub_rn(s[i], ref));
+          const float2 v0 = Elem<T>::to_f2(vw[i].x), v1 = Elem<T>::to_f2(vw[i].y);
+          l += e;
+          o[0] += e * v0.x;
+          o[1] += e * v0.y;
+          o[2] += e * v1.x;
+          o[3] += e * v1.y;
+        }
+      }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l, lse2 = l == 0.f ? neg_inf() : m + lg2(l);
 #pragma unroll
@@ -863,7 +924,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st_32x32b_x16(t_p + 16 * j, pw);
           }
           const float2 s2 = upk2(fadd2(sa, sb));
-          move = __any_sync(0xffffffffu, s2.x + s2.y > kMoveSum);
+          // (Not twice for a tile: rows that are still above are far out, kFar.)
+          move = !move && __any_sync(0xffffffffu, s2.x + s2.y > kMoveSum);
           if (!move) {
             l2a = fadd2(l2a, sa);
             l2b = fadd2(l2b, sb);
@@ -923,14 +985,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!cut) p.lse[out] = lse2 * kLn2;
         else p.part_lse[slot * kRows + row] = lse2;
       }
-      bool bad;
+      bool odd;
       {
         const float2 z = upk2(finite);
-        bad = !(z.x + z.y == 0.f);
+        odd = !(z.x + z.y == 0.f);
       }
       tc_fence_before();  // O has been read out: the next P's arrival says so
-      if (const uint32_t todo = __ballot_sync(0xffffffffu, bad && valid); todo)
-        slow_rows<T>(p, todo, row0, it.b, it.kvh, it.q_row, it.pos0, it.len, it.t0, it.t1, cut ? slot : -1);
+      const bool far = mine && m_ref != neg_inf() && !(fabsf(m_ref) < kFar);
+      if (const uint32_t todo = __ballot_sync(0xffffffffu, (odd || far) && valid); todo) {
+        const uint32_t f = __ballot_sync(0xffffffffu, far && valid);
+        slow_rows<T>(p, f, todo & ~f, row0, it.b, it.kvh, it.q_row, it.pos0, it.len, lo, hi, lo_max, hi_min, cut ? slot : -1);
+      }
 
       if (cut) {
         // The block whose piece is the item's last one to be there merges all.

@@ -118,7 +118,7 @@ def chunk(q, q_indptr, k_cache, v_cache, table, lens, scale, causal=True, window
                 x = kh[m] @ qh[i] * scale
                 size = float((kh[m].abs() @ qh[i].abs()).max() * scale)
                 lse[lo + i, h] = torch.logsumexp(x, 0)
-                w = torch.exp(x - lse[lo + i, h])
+                w = torch.softmax(x, 0)  # (64 bits of x - lse are not enough where x passes 2^50)
                 o[lo + i, h] = w @ vh[m]
                 d = 2.0 ** -17 * size + 2.0 ** -19
                 spread = w @ vh[m].abs()

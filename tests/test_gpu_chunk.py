@@ -139,6 +139,33 @@ def test_later_tokens_have_no_influence(hq, hkv, bad):
     ref.check_chunk(o, lse, want, F16, mask)
 
 
+@pytest.mark.parametrize("dtype,q_exp,k_exp", [(F16, 2, 8), (F16, 14, 8), (BF16, 14, 8), (BF16, 30, 40)])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_far_out(dtype, q_exp, k_exp, sign):
+    """Scores of 2^16 to 2^77, where a float32 holds no fraction, or no units, of the
+    exponent: the largest one's value comes out, or the mean of those that share it.
+
+    q holds a power of two in dim 0 and zeros, so a score is its key's dim 0 times
+    that power, exactly, and two different ones lie more than 2^9 apart (weights
+    exp(-2^9) = 0 in 32 bits).  The rows that share the largest one share its weight
+    too, which need not be 1: it is exp2 of what is lost where scale q.k log2(e) is
+    rounded (up to 2^17 2^-24 below the scores that are computed again), so it is
+    rounded to 16 bits where it meets V, half a step, and O is rounded, another half.
+    The values are below 2^3 and sum in 32 bits: 2^-19 for a few roundings.  LSE has
+    the rounding of the scaled score and of the sum's logarithm."""
+    c = Case([(150, 700), (3, 200), (1, 0), (140, 0)], 4, 1, dtype, seed=11, scale=1.0)
+    gen = torch.Generator().manual_seed(12)
+    c.q[:] = 0
+    c.q[..., 0] = 2.0 ** q_exp
+    rank = torch.randint(1, 100, c.k.shape[:3], generator=gen)
+    c.k[..., 0] = torch.where(c.k[..., 0].isnan(), c.k[..., 0], (sign * rank * 2.0 ** k_exp).to(dtype))
+    o, lse = c.run()
+    assert pkc.device_status(c.ws) == 0
+    want, want_lse, _, _ = c.reference()
+    assert float(((o.double().cpu() - want).abs() - 2 * ref.HALF_STEP[dtype] * want.abs()).max()) <= 2.0 ** -19
+    assert torch.all((lse.double().cpu() - want_lse).abs() <= 2.0 ** -21 * want_lse.abs())
+
+
 @pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
 def test_a_value_that_is_not_finite(bad):
     """Only V is bad: the scores are ordinary, and O is what the sum gives in that element alone."""

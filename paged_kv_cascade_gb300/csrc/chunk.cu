@@ -71,11 +71,13 @@ constexpr int kItems = 4;                // items the scheduler runs ahead
 constexpr int kThreads = 512;
 constexpr int kQkWarp = 8, kPvWarp = 9, kKWarp = 10, kVWarp = 11, kSchedWarp = 12, kQWarp = 13;
 constexpr int kMaxBlocks = 160;
-// What an item costs, measured (0.35 us a unit): a KV tile where both halves have
-// rows 1.74 us, where only A has 1.41 (as fast as HBM brings it), and 5.9 us for
-// the item itself (first tile, epilogue).
-constexpr int kTileCost = 5, kHalfTileCost = 4, kOver = 17;
-constexpr int kMinCost = 20;             // least cost of a block
+// What an item costs, measured over whole launches (0.32 us a unit): a KV tile where
+// both halves have rows 1.58 us, where only one has 1.35 (as fast as HBM brings it),
+// and 3.7 us for the item itself (first tile, epilogue).  With 17 for the item, the
+// blocks that got short items were done 70 us before the others (prompts 542 us, 533
+// with 12; a mixed batch 161, 155).
+constexpr int kTileCost = 5, kHalfTileCost = 4, kOver = 12;
+constexpr int kMinCost = 16;             // least cost of a block: a short item has one to itself
 constexpr int kShort = 16;               // items of at most so many tiles are not cut: a cut costs some 16 us
 constexpr float kMoveSum = 8192.f;       // a tile's sum of P above which its reference maximum moves
 
@@ -142,7 +144,7 @@ PKC_HD inline int64_t sum_floor(int64_t a, int e, int64_t m) {
 }
 
 // Tokens of an item: 2^shift.
-PKC_HD inline int item_shift(const ChunkParams& p) { return p.g == 1 ? 8 : p.g == 2 ? 7 : p.g == 4 ? 6 : 5; }
+PKC_HD inline int item_shift(const ChunkParams& p) { return 8 - p.g_log2; }
 
 PKC_HD inline int n_items(const ChunkParams& p, const Request& q) {
   const int e = item_shift(p);
@@ -161,7 +163,7 @@ PKC_HD inline void reach(const ChunkParams& p, const Request& q, int j0, int j1,
 
 // Cost of a KV tile of a request's item i.
 PKC_HD inline int tile_cost(const ChunkParams& p, const Request& q, int i) {
-  return (q.n - (i << item_shift(p))) * p.g <= kHalf ? kHalfTileCost : kTileCost;
+  return (q.n - (i << item_shift(p))) << p.g_log2 <= kHalf ? kHalfTileCost : kTileCost;
 }
 
 // Cost of the first m items of a request's KV head.
@@ -225,8 +227,6 @@ __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, volatile
 // The n lowest bits (none for n <= 0, all from 32 on).
 __device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; }
 
-__device__ __forceinline__ void fence_sc() { asm volatile("fence.sc.gpu;" ::: "memory"); }
-
 // 32 columns (float32, already normalised) to column `col` of output row `row`.
 // A thread has a row of its own, so a store is as wide as it gets: 32 bytes, a
 // sector, where o allows it.
@@ -260,6 +260,23 @@ __device__ __forceinline__ float* part_row(const ChunkParams& p, int slot, int c
   return p.part_o + (((int64_t)slot * 32 + chunk) * kRows + row) * 4;
 }
 __device__ __forceinline__ int slot_of(int c, int c0) { return 2 * c + (c == c0 ? 1 : 0); }
+
+// The row of q, o and lse that row `row` of an item stands for.
+__device__ __forceinline__ int64_t out_row(const ChunkParams& p, int q_row, int kvh, int row) {
+  return ((int64_t)q_row + (row >> p.g_log2)) * p.hq + (kvh << p.g_log2) + (row & (p.g - 1));
+}
+
+// The bits, within a word, of pieces c0 .. c1 (which may lie outside it): slot_of.
+__device__ __forceinline__ uint32_t pieces_of(int c0, int c1) {
+  const uint32_t first = c0 >= 0 ? 2u << 2 * c0 : 0u;
+  return (0x55555555u & low_bits(2 * c1 + 1) & ~low_bits(2 * c0 + 2)) | first;
+}
+// Set a bit; true for the one that completes `all`, which are cleared again then.
+__device__ __forceinline__ bool set_bit(uint32_t* word, int bit, uint32_t all) {
+  if (((atomicOr(word, 1u << bit) | 1u << bit) & all) != all) return false;
+  atomicAnd(word, ~all);
+  return true;
+}
 
 // The tokens [lo, hi) that a row at position pos attends to.
 __device__ __forceinline__ void tokens_of(const ChunkParams& p, int pos, int len, int& lo, int& hi) {
@@ -311,9 +328,9 @@ __device__ __noinline__ void slow_rows(const ChunkParams& p, uint32_t far, uint3
   }
   for (; far; far &= far - 1) {
     const int row = row0 + __ffs(far) - 1;
-    const int64_t out = ((int64_t)q_row + row / p.g) * p.hq + kvh * p.g + row % p.g;
+    const int64_t out = out_row(p, q_row, kvh, row);
     int lo, hi;
-    tokens_of(p, pos0 + row / p.g, len, lo, hi);
+    tokens_of(p, pos0 + (row >> p.g_log2), len, lo, hi);
     lo = max(lo, begin);
     hi = min(hi, end);
     const uint2 qw = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.q) + out * PKC_HEAD_DIM + 4 * lane);
@@ -384,36 +401,36 @@ __device__ __noinline__ void slow_rows(const ChunkParams& p, uint32_t far, uint3
 }
 
 // The merge of an item's partial states by the eight softmax warps: a warp takes
-// 32 rows and 32 columns at a time, two states' loads in flight.
+// 32 rows and 32 columns at a time, three states' loads in flight.
 template <typename T>
 __device__ __forceinline__ void merge_item(const ChunkParams& p, const Item& it, int warp, int lane) {
-  const int rows = it.n_tok * p.g, groups = (rows + 31) / 32, n = it.c1 - it.c0 + 1;
+  const int rows = it.n_tok << p.g_log2, groups = (rows + 31) / 32, n = it.c1 - it.c0 + 1;
 #pragma unroll 1
   for (int u = warp; u < 4 * groups; u += 8) {
-    const int row = (u >> 2) * 32 + lane, chunk = (u & 3) * 8;
+    const int row = (u >> 2) * 32 + lane, from = min(row, rows - 1), chunk = (u & 3) * 8;
     float m = neg_inf(), l = 0.f, o[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) o[i] = 0.f;
 #pragma unroll 1
-    for (int i0 = 0; i0 < n; i0 += 2) {
-      float4 x[2][8];
-      float w[2], now = m;
+    for (int i0 = 0; i0 < n; i0 += 3) {
+      float4 x[3][8];
+      float w[3], now = m;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 3; ++i) {
         const int slot = slot_of(it.c0 + min(i0 + i, n - 1), it.c0);
-        w[i] = __ldcg(p.part_lse + slot * kRows + row);
+        w[i] = __ldcg(p.part_lse + slot * kRows + from);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[i][k] = __ldcg(reinterpret_cast<const float4*>(part_row(p, slot, chunk + k, row)));
+        for (int k = 0; k < 8; ++k) x[i][k] = __ldcg(reinterpret_cast<const float4*>(part_row(p, slot, chunk + k, from)));
       }
 #pragma unroll
-      for (int i = 0; i < 2; ++i) now = fmaxf(now, w[i]);  // (the last one again where there are fewer)
+      for (int i = 0; i < 3; ++i) now = fmaxf(now, w[i]);  // (the last one again where there are fewer)
       const float ref = now == neg_inf() ? 0.f : now, f = ex2(m - ref);
       m = now;
       l *= f;
 #pragma unroll
       for (int i = 0; i < 32; ++i) o[i] *= f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
+      for (int i = 0; i < 3; ++i) {
         if (i0 + i >= n) break;
         const float e = ex2(w[i] - ref);
         l += e;
@@ -430,7 +447,7 @@ __device__ __forceinline__ void merge_item(const ChunkParams& p, const Item& it,
       const float inv = m == neg_inf() ? 0.f : 1.f / l;
 #pragma unroll
       for (int i = 0; i < 32; ++i) o[i] *= inv;
-      const int64_t out = ((int64_t)it.q_row + row / p.g) * p.hq + it.kvh * p.g + row % p.g;
+      const int64_t out = out_row(p, it.q_row, it.kvh, row);
       store_out<T>(p, out, 4 * chunk, o);
       if (chunk == 0) p.lse[out] = m == neg_inf() ? neg_inf() : (m + lg2(l)) * kLn2;
     }
@@ -614,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Item it;
             it.b = b0 + j; it.kvh = h; it.q_row = q.r0 + j0; it.n_tok = n_tok;
             it.pos0 = q.len - q.n + j0; it.len = q.len;
-            const int half = kHalf / p.g;
+            const int half = kHalf >> p.g_log2;
             reach(p, q, j0, j0 + min(n_tok, half), it.lo[0], it.hi[0]);
             it.lo[1] = it.hi[1] = it.hi[0];
             if (n_tok > half) reach(p, q, j0 + half, j0 + n_tok, it.lo[1], it.hi[1]);
@@ -680,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) {
           if (n[x] > 0) ok = wait_for(bar(bars->q_empty[x]), (n[x] - 1) & 1, abort, p.status);
           if (ok) {
-            const int row = it.q_row + (x * kHalf - it.off) / p.g;
+            const int row = it.q_row + ((x * kHalf - it.off) >> p.g_log2);
             mbar_arrive_expect_tx(bar(bars->q_full[x]), kTileBytes);
             tma_load_3d(s_q + x * kTileBytes, &tm_q, bar(bars->q_full[x]), 0, it.kvh * p.g, row, pol);
             tma_load_3d(s_q + x * kTileBytes + kSub, &tm_q, bar(bars->q_full[x]), 64, it.kvh * p.g, row, pol);
@@ -840,8 +857,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int k = 0; ok && next_item(k, it); ++k) {
       const int row0 = x * kHalf - it.off + quad * 32, row = row0 + lane;  // of the item; the warp's first one
-      const int n_rows = it.n_tok * p.g;
-      const int pos = it.pos0 + row / p.g;
+      const int n_rows = it.n_tok << p.g_log2;
+      const int pos = it.pos0 + (row >> p.g_log2);
       const bool valid = row >= 0 && row < n_rows;
       int rlo, rhi;
       tokens_of(p, pos, it.len, rlo, rhi);
@@ -942,7 +959,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!cut && !mine && !rows_here) continue;
       const int slot = slot_of((int)blockIdx.x, it.c0);
       const int k_lo = max(rlo, it.t0 * kKv), k_hi = min(rhi, it.t1 * kKv);  // tokens of the piece that the row attends to
-      const int64_t out = ((int64_t)it.q_row + row / p.g) * p.hq + it.kvh * p.g + row % p.g;
+      const int64_t out = out_row(p, it.q_row, it.kvh, row);
       float l;
       {
         const float2 a = upk2(l2a), b = upk2(l2b);
@@ -998,49 +1015,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
 
       if (cut) {
-        // The block whose piece is the item's last one to be there merges all.
-        __threadfence();
+        // The block whose piece is the item's last one to be there merges all: a bit
+        // per piece, and one per word of them where an item's pieces fill several.
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(bars->part_done));
         if (warp == 0) {
           const bool done = wait_for(bar(bars->part_done), n_merge & 1, abort, p.status);
           if (!__all_sync(0xffffffffu, done)) { ok = false; break; }
-          if (lane == 0) atomicOr(ready + (slot >> 5), 1u << (slot & 31));
-          __syncwarp();
-          fence_sc();  // each block sets its bit before it looks for the others'
-          bool there = true;
-          for (int c = it.c0 + lane; c <= it.c1; c += 32) {
-            const int s = slot_of(c, it.c0);
-            there = there && ((atomicOr(ready + (s >> 5), 0u) >> (s & 31)) & 1);
-          }
-          int win = 0;
-          if (__all_sync(0xffffffffu, there)) {
-            // Two blocks may see all bits set: the one that takes the first bit merges.
-            if (lane == 0) {
-              const int s = slot_of(it.c0, it.c0);
-              win = (atomicAnd(ready + (s >> 5), ~(1u << (s & 31))) >> (s & 31)) & 1;
-            }
-            win = __shfl_sync(0xffffffffu, win, 0);
-            if (win)
-              for (int c = it.c0 + 1 + lane; c <= it.c1; c += 32) {
-                const int s = slot_of(c, it.c0);
-                atomicAnd(ready + (s >> 5), ~(1u << (s & 31)));
-              }
-          }
-          __threadfence();
-          __syncwarp();
           if (lane == 0) {
-            bars->merge = win;
+            const int w = slot >> 5, w0 = it.c0 >> 4, w1 = it.c1 >> 4;
+            __threadfence();
+            bool last = set_bit(ready + w, slot & 31, pieces_of(it.c0 - 16 * w, it.c1 - 16 * w));
+            if (last && w0 != w1) {
+              __threadfence();
+              last = set_bit(ready + kMaxBlocks / 16, slot_of(w, w0), pieces_of(w0, w1));
+            }
+            __threadfence();
+            bars->merge = last;
             mbar_arrive(bar(bars->merge_go));
           }
+          __syncwarp();
         }
         const bool go = wait_for(bar(bars->merge_go), n_merge & 1, abort, p.status);
         if (!__all_sync(0xffffffffu, go)) { ok = false; break; }
         ++n_merge;
-        if (*(volatile int*)&bars->merge) {
-          __threadfence();
-          merge_item<T>(p, it, warp, lane);
-        }
+        if (*(volatile int*)&bars->merge) merge_item<T>(p, it, warp, lane);
         __syncwarp();
       }
     }
@@ -1082,6 +1081,7 @@ size_t chunk_partial_bytes() { return (size_t)2 * kMaxBlocks * kRows * (PKC_HEAD
 int launch_paged_chunk(const ChunkParams& params, int dtype, void* stream) {
   ChunkParams p = params;
   p.part_lse = p.part_o + (size_t)2 * kMaxBlocks * kRows * PKC_HEAD_DIM;
+  for (p.g_log2 = 0; 1 << p.g_log2 < p.g;) ++p.g_log2;
   p.o_wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
   p.scale_log2 = std::max(p.scale_log2, FLT_MIN);  // a scale of 0 must not meet a masked score's infinity
   for (p.box_tokens = 1; p.box_tokens < kKv && p.page_size % (2 * p.box_tokens) == 0;) p.box_tokens *= 2;

@@ -360,6 +360,7 @@ struct ChunkParams {
   int64_t bt_stride, num_pages;
   int total_q, batch, hq, hkv, g, page_size;
   int causal, window;        // window 0: none
+  int g_log2;                // set by the launcher: g is a power of two
   int o_wide;                // set by the launcher: o is 32-byte aligned
   int box_tokens;            // set by the launcher: tokens of a copy, a power of two dividing page_size
   float scale_log2;

@@ -13,8 +13,10 @@
 // and counts the map for itself (both small, from L2), with the map's chunks
 // shared out over the blocks.  Up to kFewTokens tokens the same launch fills in
 // their places; more go to a second launch over all SMs, which begins while the
-// first one runs and finds what it needs of a request at its first token (220,453
-// tokens of 300 requests: a cluster of 8 took 44 us for all, the two take 15).
+// first one runs and finds what it needs of a request at its first token.  Both calls
+// for 220,453 tokens of 300 requests: 60.7 us with one launch, 31.9 with the second,
+// 26.4 with the requests of a block's tokens found while the first one runs, 32-bit
+// divisions and a released row's entries loaded together; 64 single tokens: 10.0 us.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -62,6 +64,12 @@ __device__ __forceinline__ int block_scan(int v, int* sums, int& total) {
   const int before = __shfl_sync(0xffffffffu, w, max(warp - 1, 0));
   const int prev = __shfl_up_sync(0xffffffffu, x, 1);
   return sat_add(warp ? before : 0, lane ? prev : 0);
+}
+
+// Pages of x tokens (x < 2^32; 64-bit divisions are a hundred instructions each).
+__device__ __forceinline__ int pages_of(const PagesParams& p, uint32_t x) {
+  const uint32_t n = x / (uint32_t)p.page_size;
+  return (int)(n + (n * (uint32_t)p.page_size != x));
 }
 
 // The set bits of word w of the map that stand for pages.
@@ -132,12 +140,11 @@ __global__ void __launch_bounds__(kThreads, 1) assign_pages_kernel(const PagesPa
     int need = 0;
     if (b < p.batch) {
       const int len = p.cache_seqlens[b], n = wrong ? 0 : start[b + 1] - start[b];
-      const int64_t have = ((int64_t)len + p.page_size - 1) / p.page_size;
-      const int64_t want = ((int64_t)len + n + p.page_size - 1) / p.page_size;
+      const uint32_t have = (uint32_t)pages_of(p, (uint32_t)max(len, 0)), want = (uint32_t)pages_of(p, (uint32_t)max(len, 0) + (uint32_t)n);
       bool ok = len >= 0 && !wrong;
       if (ok && n > 0) {
         ok = want <= p.bt_stride;
-        if (ok && len % p.page_size != 0) {  // the new tokens begin in a page that is there
+        if (ok && have * (uint32_t)p.page_size != (uint32_t)len) {  // the new tokens begin in a page that is there
           const int page = p.block_table[(int64_t)b * p.bt_stride + have - 1];
           ok = page >= 0 && page < p.num_pages;
         }
@@ -201,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) assign_pages_kernel(const PagesPa
       for (uint32_t y = x; y && r < taken; y &= y - 1, ++r) {
         const int bit = __ffs(y) - 1;
         while (off[b + 1] <= r) ++b;
-        const int have = (int)(((int64_t)lens[b] + p.page_size - 1) / p.page_size);
+        const int have = pages_of(p, (uint32_t)lens[b]);
         p.block_table[(int64_t)b * p.bt_stride + have + (r - off[b])] = (int)(32 * w) + bit;
         gone |= 1u << bit;
       }
@@ -241,15 +248,34 @@ __global__ void __launch_bounds__(kThreads, 1) assign_pages_kernel(const PagesPa
 constexpr int kPlaceThreads = 256;
 constexpr int kPlaceTokens = 4;  // a thread's, one after another
 
-// The places of the tokens behind each request's first one.
+// The places of the tokens behind each request's first one.  While the launch
+// before runs, a block finds the requests that its tokens belong to.
 __global__ void __launch_bounds__(kPlaceThreads) places_kernel(const PagesParams p) {
+  constexpr int kBlockTokens = kPlaceThreads * kPlaceTokens;
+  __shared__ int counts[2];  // ranges that begin at or before the block's first and last token
+  if (threadIdx.x < 2) counts[threadIdx.x] = 0;
+  __syncthreads();
+  const int64_t block_t0 = (int64_t)blockIdx.x * kBlockTokens;
+  int n[2] = {0, 0};
+  for (int b = threadIdx.x; b <= p.batch; b += kPlaceThreads) {
+    const int at = p.indptr[b];
+    n[0] += at <= block_t0;
+    n[1] += at < block_t0 + kBlockTokens;
+  }
+  for (int i = 0; i < 2; ++i) {
+    const int sum = __reduce_add_sync(0xffffffffu, n[i]);
+    if (threadIdx.x % 32 == 0 && sum) atomicAdd(counts + i, sum);
+  }
+  __syncthreads();
+  const int b0 = max(counts[0] - 1, 0), near = max(counts[1], b0 + 1) - b0;
   grid_wait_prerequisites();
   const bool wrong = __ldcg(p.status + PKC_ASSIGN_FLAG) != 0;  // (or no requests at all)
-  const int64_t t0 = ((int64_t)blockIdx.x * kPlaceThreads + threadIdx.x) * kPlaceTokens;
+  const int64_t t0 = block_t0 + threadIdx.x * kPlaceTokens;
   if (t0 >= p.total) return;
   const int t1 = (int)min((int64_t)p.total, t0 + kPlaceTokens);
   const int begin = wrong ? p.total : p.indptr[0], end = wrong ? p.total : p.indptr[p.batch];
   int b = -1, from = 0, to = 0, len = 0;  // the request of the tokens [from, to)
+  int entry = -1, page = 0;               // the table entry at hand
   bool served = false;
   for (int t = (int)t0; t < t1; ++t) {
     if (t < begin || t >= end) {
@@ -258,51 +284,59 @@ __global__ void __launch_bounds__(kPlaceThreads) places_kernel(const PagesParams
       continue;
     }
     if (b < 0 || t >= to) {
-      if (b < 0) b = last_not_above(p.indptr, p.batch + 1, t);
+      if (b < 0) b = b0 + last_not_above(p.indptr + b0, near, t);
       else do ++b; while (p.indptr[b + 1] <= t);
       from = p.indptr[b];
       to = p.indptr[b + 1];
       served = __ldcg(p.slots + from) >= 0;
       len = __ldcg(p.positions + from);
+      entry = -1;
     }
     if (t == from) continue;
     const int pos = len + (t - from);
-    p.slots[t] = served ? slot_at(p, b, pos) : -1;
+    int64_t slot = -1;
+    if (served) {
+      const int e = pos / p.page_size;
+      if (e != entry) page = __ldcg(p.block_table + (int64_t)b * p.bt_stride + e);
+      entry = e;
+      slot = (int64_t)page * p.page_size + (pos - e * p.page_size);
+    }
+    p.slots[t] = slot;
     p.positions[t] = pos;
   }
 }
 
-constexpr int kReleaseThreads = 256;
-constexpr int kSegment = 1024;  // table entries of a warp's turn
+constexpr int kReleaseThreads = 128;
+constexpr int kReleaseEntries = 8;  // a thread's, loaded together
 
-// A warp per segment of a table row: entries behind the used ones become -1
-// and their pages' bits are set (a commutative update: any order gives the
-// same map).
+// Entries behind the used ones become -1 and their pages' bits are set (a
+// commutative update: any order gives the same map).  Blocks: (entries, requests).
 __global__ void __launch_bounds__(kReleaseThreads) release_pages_kernel(const PagesParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t segs = (p.bt_stride + kSegment - 1) / kSegment;
-  const int64_t units = segs * p.batch, n_warps = (int64_t)gridDim.x * (kReleaseThreads / 32);
-  for (int64_t u = (int64_t)blockIdx.x * (kReleaseThreads / 32) + (threadIdx.x >> 5); u < units; u += n_warps) {
-    const int64_t b = u / segs, lo = (u - b * segs) * kSegment;
-    const int len = p.cache_seqlens[b];
-    if (len < 0) {
-      if (lane == 0) report(p.status, PKC_ERR_PLAN);
+  const int b = blockIdx.y, len = p.cache_seqlens[b];
+  const int64_t lo = (int64_t)blockIdx.x * (kReleaseThreads * kReleaseEntries) + threadIdx.x;
+  if (len < 0) {
+    if (lo == 0) report(p.status, PKC_ERR_PLAN);
+    return;
+  }
+  const int64_t used = pages_of(p, (uint32_t)len);
+  int32_t* row = p.block_table + (int64_t)b * p.bt_stride;
+  int pages[kReleaseEntries];
+#pragma unroll
+  for (int i = 0; i < kReleaseEntries; ++i) {
+    const int64_t j = lo + i * kReleaseThreads;
+    pages[i] = j >= used && j < p.bt_stride ? row[j] : -1;
+  }
+#pragma unroll
+  for (int i = 0; i < kReleaseEntries; ++i) {
+    const int page = pages[i];
+    if (page < 0) continue;
+    if (page >= p.num_pages) {
+      report(p.status, PKC_ERR_BLOCK_TABLE);
       continue;
     }
-    const int64_t used = ((int64_t)len + p.page_size - 1) / p.page_size;
-    const int64_t hi = min(p.bt_stride, lo + kSegment);
-    int32_t* row = p.block_table + b * p.bt_stride;
-    for (int64_t j = max(lo, used) + lane; j < hi; j += 32) {
-      const int page = row[j];
-      if (page < 0) continue;
-      if (page >= p.num_pages) {
-        report(p.status, PKC_ERR_BLOCK_TABLE);
-        continue;
-      }
-      row[j] = -1;
-      const uint32_t bit = 1u << (page & 31);
-      if (atomicOr(p.free_pages + (page >> 5), bit) & bit) report(p.status, PKC_ERR_BLOCK_TABLE);
-    }
+    row[lo + i * kReleaseThreads] = -1;
+    const uint32_t bit = 1u << (page & 31);
+    if (atomicOr(p.free_pages + (page >> 5), bit) & bit) report(p.status, PKC_ERR_BLOCK_TABLE);
   }
 }
 
@@ -310,10 +344,9 @@ __global__ void __launch_bounds__(kReleaseThreads) release_pages_kernel(const Pa
 
 int launch_release_pages(const PagesParams& p, void* stream) {
   if (p.batch <= 0) return 0;
-  const int64_t units = (p.bt_stride + kSegment - 1) / kSegment * p.batch;
-  const int64_t want = (units + kReleaseThreads / 32 - 1) / (kReleaseThreads / 32);
-  const int64_t most = (int64_t)num_sms() * (2048 / kReleaseThreads);
-  release_pages_kernel<<<(unsigned)std::min(want, most), kReleaseThreads, 0, (cudaStream_t)stream>>>(p);
+  const int64_t per = kReleaseThreads * kReleaseEntries;
+  static_assert(PKC_PAGES_MAX_BATCH <= 65535, "grid.y");
+  release_pages_kernel<<<dim3((unsigned)((p.bt_stride + per - 1) / per), p.batch), kReleaseThreads, 0, (cudaStream_t)stream>>>(p);
   return (int)cudaGetLastError();
 }
 

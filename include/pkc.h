@@ -767,6 +767,7 @@ int pkc_assign_pages(int32_t* block_table, int block_table_stride,
  *            2 i + 1) if interleaved is 1, (i, i + rotary_dim / 2) if 0:
  *            (x, y) -> amplitude (x cos a - y sin a, x sin a + y cos a)
  *   q_out    [total, num_qo_heads, 128] of dtype, dense; may be q if q is
+ *            dense too
  *   k_cache, v_cache [num_pages, page_size, num_kv_heads, 128] of kv_dtype:
  *            dtype itself (k_scale = v_scale = 1), or E4M3: the nearest codes
  *            of the turned key / k_scale and of the value / v_scale (ties to
@@ -809,10 +810,15 @@ int pkc_chunk_workspace_size(size_t* bytes);
  *            state that is merged further (pkc_merge_states_to); lse
  *            [total_q, num_qo_heads] float32, natural log
  * A token that a row does not attend to has no influence on it, whatever its
- * key and value hold.  Probabilities enter the V product in dtype.  A page id
- * < 0 or >= num_pages (or past the table) is read as zeros and recorded as
+ * key and value hold.  Probabilities enter the V product in dtype.  Rows whose
+ * largest scaled score passes 2^20 / log2(e) in magnitude, and rows next to a
+ * value that is not finite and not theirs, are computed a key at a time (slow,
+ * and right).  A page id < 0 or >= num_pages (or past the table) is read as zeros and recorded as
  * PKC_ERR_BLOCK_TABLE.  A request whose rows do not lie within 0 .. total_q, or
- * with a negative length, is not computed (PKC_ERR_PLAN).
+ * with a negative length, is not computed (PKC_ERR_PLAN).  The results do not
+ * depend on the order in which blocks run.  The status block holds which partial
+ * states are there: two of these calls in flight need a workspace each, and after
+ * PKC_ERR_TIMEOUT the workspace is initialised again.
  */
 int pkc_paged_chunk_state(const void* q, const int32_t* q_indptr, int total_q,
                           const void* k_cache, const void* v_cache,

@@ -683,11 +683,19 @@ def assign_pages(block_table, cache_seqlens, new_indptr, total_new, free_pages, 
     total = int(total_new)
     if total < 0:
         raise ValueError(f"assign_pages: total_new must be >= 0 (got {total})")
-    slots = torch.empty(total, dtype=torch.int64, device=dev) if slots is None else slots
-    positions = torch.empty(total, dtype=torch.int32, device=dev) if positions is None else positions
-    seqlens_out = torch.empty(B, dtype=torch.int32, device=dev) if seqlens_out is None else seqlens_out
-    _expect_all(dev, ("new_indptr", new_indptr, torch.int32, (B + 1,)), ("slots", slots, torch.int64, (total,)),
-                ("positions", positions, torch.int32, (total,)), ("seqlens_out", seqlens_out, torch.int32, (B,)))
+    _expect_all(dev, ("new_indptr", new_indptr, torch.int32, (B + 1,)))
+    if slots is None:
+        slots = torch.empty(total, dtype=torch.int64, device=dev)
+    else:
+        _expect("slots", slots, (torch.int64,), (total,), dev)
+    if positions is None:
+        positions = torch.empty(total, dtype=torch.int32, device=dev)
+    else:
+        _expect("positions", positions, (torch.int32,), (total,), dev)
+    if seqlens_out is None:
+        seqlens_out = torch.empty_like(cache_seqlens)
+    else:
+        _expect("seqlens_out", seqlens_out, (torch.int32,), (B,), dev)
     _check(lib().pkc_assign_pages(
         block_table.data_ptr(), stride, cache_seqlens.data_ptr(), new_indptr.data_ptr(), total, B, int(page_size), num_pages,
         free_pages.data_ptr(), slots.data_ptr(), positions.data_ptr(), seqlens_out.data_ptr(), workspace.data_ptr(), workspace.numel(),

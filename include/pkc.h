@@ -807,8 +807,8 @@ int pkc_chunk_workspace_size(size_t* bytes);
  *            pkc_paged_decode_state (the lengths count the new tokens)
  *   sm_scale finite, >= 0
  *   o        [total_q, num_qo_heads, 128] of out_dtype: dtype, or F32 for a
- *            state that is merged further (pkc_merge_states_to); lse
- *            [total_q, num_qo_heads] float32, natural log
+ *            state that is merged further (pkc_merge_states_to), not in the
+ *            place of q; lse [total_q, num_qo_heads] float32, natural log
  * A token that a row does not attend to has no influence on it, whatever its
  * key and value hold.  Probabilities enter the V product in dtype.  Rows whose
  * largest scaled score passes 2^20 / log2(e) in magnitude, and rows next to a

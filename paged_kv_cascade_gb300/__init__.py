@@ -648,6 +648,14 @@ def page_pool(num_pages, device="cuda"):
     return torch.from_numpy(words.view(np.int32)).to(device)
 
 
+def _c_int(name, x):
+    """x as the C int that ctypes would cut it to."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name} must fit in 32 bits (got {x})")
+    return x
+
+
 def _check_pages(block_table, cache_seqlens, free_pages, num_pages, workspace):
     torch = _torch or _t()
     B, n_pages = _leading("block_table", block_table, (torch.int32,), 2)
@@ -667,7 +675,7 @@ def release_pages(block_table, cache_seqlens, free_pages, page_size, num_pages, 
     free_pages (of page_pool), in place: their table entries become -1."""
     B, stride, num_pages, _ = _check_pages(block_table, cache_seqlens, free_pages, num_pages, workspace)
     _check(lib().pkc_release_pages(
-        block_table.data_ptr(), stride, cache_seqlens.data_ptr(), B, int(page_size), num_pages, free_pages.data_ptr(),
+        block_table.data_ptr(), stride, cache_seqlens.data_ptr(), B, _c_int("page_size", page_size), num_pages, free_pages.data_ptr(),
         workspace.data_ptr(), workspace.numel(), _stream(stream)))
 
 
@@ -680,7 +688,7 @@ def assign_pages(block_table, cache_seqlens, new_indptr, total_new, free_pages, 
     a new tensor unless seqlens_out is given -- cache_seqlens itself may be)."""
     torch = _torch or _t()
     B, stride, num_pages, dev = _check_pages(block_table, cache_seqlens, free_pages, num_pages, workspace)
-    total = int(total_new)
+    total = _c_int("total_new", total_new)
     if total < 0:
         raise ValueError(f"assign_pages: total_new must be >= 0 (got {total})")
     _expect_all(dev, ("new_indptr", new_indptr, torch.int32, (B + 1,)))
@@ -697,7 +705,7 @@ def assign_pages(block_table, cache_seqlens, new_indptr, total_new, free_pages, 
     else:
         _expect("seqlens_out", seqlens_out, (torch.int32,), (B,), dev)
     _check(lib().pkc_assign_pages(
-        block_table.data_ptr(), stride, cache_seqlens.data_ptr(), new_indptr.data_ptr(), total, B, int(page_size), num_pages,
+        block_table.data_ptr(), stride, cache_seqlens.data_ptr(), new_indptr.data_ptr(), total, B, _c_int("page_size", page_size), num_pages,
         free_pages.data_ptr(), slots.data_ptr(), positions.data_ptr(), seqlens_out.data_ptr(), workspace.data_ptr(), workspace.numel(),
         _stream(stream)))
     return slots, positions, seqlens_out
@@ -813,7 +821,7 @@ def paged_chunk_state(q, q_indptr, k_cache, v_cache, block_table, cache_seqlens,
     if out_dtype is not dtype and out_dtype is not torch.float32:
         raise TypeError(f"paged_chunk_state: out_dtype must be {dtype} or torch.float32 (got {out_dtype})")
     if o is None:
-        o = torch.empty((T, Hq, 128), dtype=out_dtype, device=dev)
+        o = torch.empty_like(q, dtype=out_dtype)
     else:
         _expect("o", o, (out_dtype,), (T, Hq, 128), dev)
     if lse is None:
@@ -823,7 +831,7 @@ def paged_chunk_state(q, q_indptr, k_cache, v_cache, block_table, cache_seqlens,
     code = F16 if dtype is torch.float16 else BF16
     _check(lib().pkc_paged_chunk_state(
         q.data_ptr(), q_indptr.data_ptr(), T, k_cache.data_ptr(), v_cache.data_ptr(), block_table.data_ptr(), stride, cache_seqlens.data_ptr(), B,
-        Hq, Hkv, 128, ps, P, float(sm_scale), 1 if causal else 0, int(window), workspace.data_ptr(), workspace.numel(),
+        Hq, Hkv, 128, ps, P, float(sm_scale), 1 if causal else 0, _c_int("window", window), workspace.data_ptr(), workspace.numel(),
         o.data_ptr(), lse.data_ptr(), code, F32 if out_dtype is torch.float32 else code, _stream(stream)))
     return o, lse
 

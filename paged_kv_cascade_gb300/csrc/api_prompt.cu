@@ -173,6 +173,11 @@ int pkc_paged_chunk_state(const void* q, const int32_t* q_indptr, int total_q, c
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(o) || !aligned(lse, 4) ||
       !aligned(q_indptr, 4) || !aligned(block_table, 4) || !aligned(cache_seqlens, 4))
     return set_error(PKC_ERR_INVALID_ARG, "paged_chunk_state: q, o and the caches must be 16-byte aligned");
+  // a row of q may be read after the rows next to it are written
+  const uintptr_t rows = (uintptr_t)total_q * num_qo_heads * PKC_HEAD_DIM;
+  const uintptr_t q0 = reinterpret_cast<uintptr_t>(q), o0 = reinterpret_cast<uintptr_t>(o);
+  if (q0 < o0 + rows * (out_dtype == PKC_F32 ? 4 : 2) && o0 < q0 + rows * 2)
+    return set_error(PKC_ERR_INVALID_ARG, "paged_chunk_state: o must not overlap q");
   ChunkParams p;
   std::memset(&p, 0, sizeof(p));
   p.q = q; p.q_indptr = q_indptr; p.total_q = total_q; p.k_cache = k_cache; p.v_cache = v_cache;

@@ -221,3 +221,39 @@ def test_a_chunk_behind_a_shared_prefix(dtype):
     want = want[0], want[1], 2 * want[2] + 2.0 ** -21, 2 * want[3] + 2.0 ** -21
     ref.check_chunk(o, lse, want, dtype)
     assert pkc.device_status(ws) == 0 and pkc.device_status(s.ws) == 0
+
+
+def test_a_pool_past_32_bits():
+    """Pages whose rows lie more than 2^32 elements into the pool."""
+    page, hkv, num_pages = 16, 16, 140_000  # 4.6 G elements a pool
+    k, v = (torch.empty((num_pages, page, hkv, 128), dtype=BF16, device="cuda") for _ in "kv")
+    gen = torch.Generator().manual_seed(6)
+    lens, free = [70, 0, 33], set(range(num_pages - 12, num_pages)) - {num_pages - 3}
+    table = [[num_pages - 20 - j for j in range(5)] + [-1] * 15, [-1] * 20, [num_pages - 30, 3, num_pages - 31] + [-1] * 17]
+    past = torch.randn((2, 3, 80, hkv, 128), generator=gen).to(BF16)
+    for b, n in enumerate(lens):
+        for j in range(-(-n // page)):
+            k[table[b][j]], v[table[b][j]] = (x[b, j * page:(j + 1) * page].cuda() for x in past)
+    ws = torch.empty(pkc.chunk_workspace_size(), dtype=torch.uint8, device="cuda")
+    pkc.workspace_init(ws)
+    indptr = [0, 40, 47, 60]
+    d_table, d_free, d_lens = dev(table), ref.pool_words(free, num_pages).cuda(), dev(lens)
+    slots, pos, _ = pkc.assign_pages(d_table, d_lens, dev(indptr), 60, d_free, page, num_pages, ws, seqlens_out=d_lens)
+    h_slots, h_pos, h_lens, status = ref.assign(table, lens, indptr, 60, free, page)
+    assert status == 0 and slots.tolist() == h_slots and pos.tolist() == h_pos and d_lens.tolist() == h_lens and d_table.tolist() == table
+    freq, _ = pkc.rope_frequencies(128)
+    qkv = torch.randn((60, 3 * hkv, 128), generator=gen).to(BF16)
+    d = qkv.cuda()
+    q = pkc.rope_append_kv(d[:, :hkv], d[:, hkv:2 * hkv], d[:, 2 * hkv:], pos, slots, freq, k, v, ws)
+    rows = v.view(-1, hkv, 128)[slots]
+    assert torch.equal(rows.cpu(), qkv[:, 2 * hkv:])
+    o, lse = pkc.paged_chunk_state(q, dev(indptr), k, v, d_table, d_lens, SCALE, ws)
+    # the same tokens in a small pool
+    small = sorted({p for r in table for p in r if p >= 0})
+    near = [[small.index(p) if p >= 0 else -1 for p in r] for r in table]
+    at = torch.tensor(small, device="cuda")
+    ref.check_chunk(o, lse, ref.chunk(q.cpu(), indptr, k[at].cpu(), v[at].cpu(), torch.tensor(near), h_lens, SCALE), BF16)
+    pkc.release_pages(d_table, torch.zeros_like(d_lens), d_free, page, num_pages, ws)
+    ref.release(table, [0, 0, 0], free, page)
+    assert ref.pool_set(d_free, num_pages) == free and d_table.tolist() == table
+    assert pkc.device_status(ws) == 0

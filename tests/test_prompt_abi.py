@@ -11,7 +11,7 @@ import paged_kv_cascade_gb300 as pkc
 import prompt_reference as ref
 from paged_kv_cascade_gb300 import build as pkc_build
 
-F, WS = ctypes.c_void_p(0x1000), ctypes.c_void_p(0x100000)
+F, WS, OUT = ctypes.c_void_p(0x1000), ctypes.c_void_p(0x100000), ctypes.c_void_p(0x80000)
 OFF8, OFF4, OFF2 = ctypes.c_void_p(0x1008), ctypes.c_void_p(0x1004), ctypes.c_void_p(0x1002)
 NAN, INF = float("nan"), float("inf")
 
@@ -72,7 +72,7 @@ def test_chunk_refuses(L):
     need = pkc.chunk_workspace_size()
     assert need % 256 == 0 and L.pkc_chunk_workspace_size(None) == 1
     # q qip total kc vc table stride lens batch hq hkv d ps pages scale causal window ws bytes o lse dtype odt stream
-    good = [F, F, 5, F, F, F, 4, F, 2, 16, 8, 128, 16, 10, 1.0, 1, 0, WS, need, F, F, 1, 1, None]
+    good = [F, F, 5, F, F, F, 4, F, 2, 16, 8, 128, 16, 10, 1.0, 1, 0, WS, need, OUT, F, 1, 1, None]
     for args, code in variants(good, [
             (0, None, 1), (1, None, 1), (3, None, 1), (4, None, 1), (5, None, 1), (7, None, 1), (19, None, 1),
             (20, None, 1), (0, OFF8, 1), (3, OFF8, 1), (4, OFF8, 1), (19, OFF8, 1), (20, OFF2, 1), (1, OFF2, 1),
@@ -81,6 +81,10 @@ def test_chunk_refuses(L):
             (15, 2, 1), (16, -1, 1), (17, None, 3), (17, OFF8, 3), (18, need - 1, 3), (21, 0, 1), (21, 3, 1), (22, 2, 1),
             (22, 3, 1)]):
         assert L.pkc_paged_chunk_state(*args) == code, (args, L.pkc_last_error())
+    # o on q, on its last row, and as float32 with its own last row on q (5 rows of 16 heads)
+    for o, q, out in ((0x1000, 0x1000, 1), (0x1000 + 79 * 256, 0x1000, 1), (0x1000, 0x1000 + 79 * 512, 0)):
+        args = [ctypes.c_void_p(q)] + good[1:19] + [ctypes.c_void_p(o)] + good[20:22] + [out, None]
+        assert L.pkc_paged_chunk_state(*args) == 1 and b"overlap" in L.pkc_last_error()
     assert L.pkc_paged_chunk_state(*good[:2], 0, *good[3:]) == 0
     assert L.pkc_paged_chunk_state(*good[:8], 0, *good[9:]) == 0
 
@@ -102,6 +106,13 @@ def test_binding_refuses_host_tensors():
         pkc.paged_chunk_state(q, ip, k, k, bt, lens, 0.1, ws)
     with pytest.raises(TypeError, match="dtype"):
         pkc.paged_chunk_state(q.float(), ip, k.float(), k.float(), bt, lens, 0.1, ws)
+
+
+def test_integers_that_a_c_int_would_cut():
+    for bad in (2 ** 31, 2 ** 32 + 16, -2 ** 31 - 1):
+        with pytest.raises(ValueError, match="window must fit in 32 bits"):
+            pkc._c_int("window", bad)
+    assert pkc._c_int("window", 2 ** 31 - 1) == 2 ** 31 - 1
 
 
 def test_frequencies():

@@ -31,7 +31,8 @@
 // cut out for itself, from the lengths on the device: the sums over a request's
 // items have a closed form.  A piece of a cut item leaves a partial state; the
 // block that finishes last among the item's pieces (bits in the status block
-// tell) merges them, always in the order of the cache.
+// tell) merges them, always in the order of the cache.  Few tokens over two caches
+// of 128k (19 pieces an item): 99 us, 79 of them bytes; the merge is 9 of the rest.
 //
 // Warps: 0-3 softmax of A, 4-7 of B (a row per thread, epilogue and merge too),
 // 8 issues Q K, 9 P V, 10 K copies, 11 V copies, 12 scheduler, 13 Q
@@ -40,7 +41,20 @@
 // and 64 dims (pages that are not a power of two: boxes of their largest
 // power-of-two part).  The lanes of a warp issue their boxes one after another,
 // some 50 cycles each, so pages of 16 tokens need a warp for K and one for V.
-// All waits are bounded (2 s) and set PKC_ERR_TIMEOUT when they run out.
+// All waits are bounded (2 s) and set PKC_ERR_TIMEOUT when they run out.  Keys that
+// one item alone reads pass L2 by (evict first: speculated tokens 111 -> 104 us), all
+// others stay (prompts 544 us, 596 if they pass by too).
+//
+// What bounds it.  A long chunk (2047 tokens over 65,001, 32 / 8 heads) takes 1.57 to
+// 1.62 ms, 1.37 to 1.41 PFLOP/s, at the power limit (1390 W, 1.70 GHz; a plain
+// product in a loop holds 1.76 PFLOP/s).  Below it the chain of a half's tile does:
+// S out of TMEM, 128 exponentials a thread, P back, with the waits, votes and fences
+// between them some 2400 cycles, against 1024 of MMA, two halves at a time (tensor
+// pipe 58 % busy on prompts, 49 % with a window; exponentials 30 %).  An item's first
+// tile and epilogue cost 3.7 us beside that.  The softmax warps have 216 registers
+// for 128 scores, and code that holds more spills (a branch over masked columns: a
+// window 161 -> 316 us); the instruction cache keeps the softmax, the epilogue and
+// the scheduler only while they are short, so most steps here took code away.
 //
 // Values that a row does not attend to meet P = 0, and 0 times an infinity or a
 // NaN would be NaN: slots behind the length are zeroed in the V tile, and a row
@@ -52,6 +66,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cfloat>
 #include <type_traits>
 
@@ -78,7 +93,10 @@ constexpr int kMaxBlocks = 160;
 // with 12; a mixed batch 161, 155).
 constexpr int kTileCost = 5, kHalfTileCost = 4, kOver = 12;
 constexpr int kMinCost = 16;             // least cost of a block: a short item has one to itself
-constexpr int kShort = 12;               // items of at most so many tiles are not cut (prompts 533 us with 16, 523 with 12 and 4, a window's 162 and 171 with 8)
+// Items of at most so many tiles are not cut: a cut costs partial states and a merge
+// (prompts 533 us with 16, 523 with 12 and 4; a window's items of 11 tiles 162 with
+// 12, 171 with 8).
+constexpr int kShort = 12;
 constexpr float kMoveSum = 8192.f;       // a tile's sum of P above which its reference maximum moves
 
 // P = exp2(s c - m_ref) in one rounding: m_ref = max s c is rounded, P's largest is
@@ -284,7 +302,7 @@ __device__ __forceinline__ void tokens_of(const ChunkParams& p, int pos, int len
   lo = p.window ? (int)max((int64_t)0, (int64_t)pos - p.window + 1) : 0;
 }
 
-// Pages of the keys t0 .. t0 + 31 of request b, a lane each (-1: none there).
+// The page of key t of request b (-1: none there).
 __device__ __forceinline__ int page_of_key(const ChunkParams& p, int b, int t, int end) {
   if (t < 0 || t >= end) return -1;  // (t < 0: past 2^31)
   const int pi = t / p.page_size;
@@ -292,21 +310,23 @@ __device__ __forceinline__ int page_of_key(const ChunkParams& p, int b, int t, i
   return page < p.num_pages ? page : -1;
 }
 
-// Rows again (row0 + a bit), by one warp, key by key over the piece's tiles
+// Rows again (row0 + a bit), by one warp, key by key over the half's tiles
 // [t0, t1).  `far`: rows whose scores lie so far out (kFar) that s c - m_ref in one
 // rounding is off by too much; here the product is rounded before the maximum is
 // taken off, so the largest weight is 1.  `odd`: rows whose O is not finite.  They
-// are right as they are unless a value that not all rows attend to, in the tiles
-// [t0, t0 x) and [y t1, t1) -- the keys outside [all_lo, all_hi) -- is not finite
-// itself.  Lanes hold four elements each; eight keys go at once.  slot: the partial
-// states' place, or -1 for an item that is not cut.  (Out of line, with the item's
-// fields by value: nothing of it is held in the loops of those who call it.)
+// are right as they are unless a value of the tiles that not all of the warp's rows
+// attend to (a key outside [all_lo, all_hi)) is not finite itself.  Lanes hold four
+// elements each; eight keys go at once.  slot: the partial states' place, or -1 for
+// an item that is not cut.  (Out of line, with the item's fields by value: nothing
+// of it is held in the loops of those who call it.)
 template <typename T>
 __device__ __noinline__ void slow_rows(const ChunkParams& p, uint32_t far, uint32_t odd, int row0, int b, int kvh, int q_row,
                                        int pos0, int len, int t0, int t1, int all_lo, int all_hi, int slot) {
   const int lane = threadIdx.x & 31;
   const int begin = t0 * kKv, end = (int)min((int64_t)len, (int64_t)t1 * kKv);
-  auto at = [&](int page, int t) { return (((int64_t)page * p.page_size + t % p.page_size) * p.hkv + kvh) * PKC_HEAD_DIM + 4 * lane; };
+  auto at = [&](int page, int t) {
+    return (((int64_t)page * p.page_size + t % p.page_size) * p.hkv + kvh) * PKC_HEAD_DIM + 4 * lane;
+  };
   if (odd) {
     float sum = 0.f;  // 0 times the values
     for (int64_t t = begin; t < end; t += 32) {
@@ -535,315 +555,315 @@ __global__ void __launch_bounds__(kThreads, 1)
   // leave the others 40 (65,536 together).  Every role's code lies behind its own
   // setmaxnreg, so the compiler keeps within it.
   if (warp >= kQkWarp) {
-  regs_down<40>();
-  if (warp == kSchedWarp) {
-    // ---------------- scheduler ----------------
-    auto load = [&](int b) -> Request {  // an empty request where there is nothing to do
-      Request q = {0, 0, 0};
-      if (b < p.batch) {
-        const int r0 = p.q_indptr[b], r1 = p.q_indptr[b + 1], len = p.cache_seqlens[b];
-        if (r0 < 0 || r1 < r0 || r1 > p.total_q || (len < 0 && r1 > r0)) {
-          if (blockIdx.x == 0) report(p.status, PKC_ERR_PLAN);
-        } else if (r1 > r0) {
-          q = {r0, r1 - r0, len};
-        }
-      }
-      return q;
-    };
-    // The cost of all requests, then those that hold some of the block's share:
-    // one loop for both, for its code is long and shares the instruction cache
-    // with the softmax.
-    int64_t total = 0, s0 = 0, s1 = 0;
-    int n_blocks = 1, k = 0;
-    bool turn = false;
-    const int c = (int)blockIdx.x;
-    bool ok = true;
-    // The block that holds place x: the last i with i total / n_blocks <= x.
-    auto block_of = [&](int64_t x) {
-      int n = 0;
-#pragma unroll 1
-      for (int i = lane; i < kMaxBlocks; i += 32)
-        n += __popc(__ballot_sync(0xffffffffu, i < n_blocks && i * total < (x + 1) * n_blocks));
-      return n - 1;
-    };
-    // i total / n_blocks, in divisions of 32 bits (total < 2^54, n_blocks < 2^8)
-    auto share_of = [&](int i) {
-      const uint32_t a = (uint32_t)(total >> 24), n = (uint32_t)n_blocks;
-      const uint64_t rest = ((uint64_t)(a % n) << 24) | (uint32_t)(total & 0xffffff);  // < n 2^24 <= 2^32
-      const uint64_t q = ((uint64_t)(a / n) << 24) + (uint32_t)rest / n;
-      return (int64_t)(q * i + (uint32_t)rest % n * i / n);
-    };
-    auto publish = [&](const Item& it) {
-      if (lane == 0 && k >= kItems) ok = wait_for(bar(bars->it_empty[k % kItems]), ((k / kItems) & 1) ^ 1, abort, p.status);
-      ok = __shfl_sync(0xffffffffu, ok, 0);
-      if (ok && lane == 0) {
-        *reinterpret_cast<Item*>(smem + kItemOffset + (k % kItems) * 64) = it;
-        mbar_arrive(bar(bars->it_full[k % kItems]));
-      }
-      ++k;
-    };
-#pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
-      int64_t base = 0;  // cost of the requests before b0
-#pragma unroll 1
-      for (int b0 = 0; ok && b0 < p.batch && (pass == 0 || base < s1); b0 += 32) {
-        const Request mine = load(b0 + lane);
-        const int64_t per_head = mine.n ? cost_of(p, mine, n_items(p, mine)) : 0;
-        int64_t before = per_head * p.hkv;
-#pragma unroll 1
-        for (int d = 1; d < 32; d <<= 1) {
-          const int64_t y = __shfl_up_sync(0xffffffffu, before, d);
-          if (lane >= d) before += y;
-        }
-        const int64_t all = __shfl_sync(0xffffffffu, before, 31);
-        before = base + before - per_head * p.hkv;
-        base += all;
-        if (pass == 0) continue;
-        uint32_t todo = __ballot_sync(0xffffffffu, mine.n > 0 && before < s1 && before + per_head * p.hkv > s0);
-#pragma unroll 1
-        for (; ok && todo; todo &= todo - 1) {
-          const int j = __ffs(todo) - 1;
-          const Request q = {__shfl_sync(0xffffffffu, mine.r0, j), __shfl_sync(0xffffffffu, mine.n, j),
-                             __shfl_sync(0xffffffffu, mine.len, j)};
-          const int64_t ph = __shfl_sync(0xffffffffu, per_head, j);
-          const int nt = n_items(p, q);
-          int h = 0, i = 0;
-          int64_t x0 = __shfl_sync(0xffffffffu, before, j);  // where item (h, i) begins
-          if (s0 > x0) {
-#pragma unroll 1
-            for (int step = 1 << 16; step; step >>= 1)
-              if (x0 + step * ph <= s0) h += step, x0 += step * ph;
-            // the last i whose items before it cost at most s0 - x0
-            int hi = nt;
-            int64_t at = 0;
-#pragma unroll 1
-            while (hi - i > 1) {
-              const int mid = (i + hi) >> 1;
-              const int64_t cost = cost_of(p, q, mid);
-              if (cost <= s0 - x0) i = mid, at = cost;
-              else hi = mid;
-            }
-            x0 += at;
-          }
-#pragma unroll 1
-          while (ok && h < p.hkv && x0 < s1) {
-            const int j0 = i << item_shift(p), n_tok = min(1 << item_shift(p), q.n - j0);
-            Item it;
-            it.b = b0 + j; it.kvh = h; it.q_row = q.r0 + j0; it.n_tok = n_tok;
-            it.pos0 = q.len - q.n + j0; it.len = q.len;
-            const int half = kHalf >> p.g_log2;
-            reach(p, q, j0, j0 + min(n_tok, half), it.lo[0], it.hi[0]);
-            it.lo[1] = it.hi[1] = it.hi[0];
-            if (n_tok > half) reach(p, q, j0 + half, j0 + n_tok, it.lo[1], it.hi[1]);
-            const int lo = it.lo[0], hi = it.hi[1];  // (a later token's reach begins and ends no earlier)
-            const int cost = tile_cost(p, q, i);
-            const int64_t first = x0 + kOver, end = first + (int64_t)(hi - lo) * cost;  // its tiles lie at first .. end - 1
-            it.t0 = lo;
-            it.t1 = hi;
-            it.c0 = it.c1 = c;
-            bool ours = end > s0 && end <= s1;  // a short item is whole, its last place's block has it
-            if (hi - lo > kShort) {
-              // (a block's share is larger than a tile's cost: no piece between is empty)
-              const uint32_t from = (uint32_t)max((int64_t)0, s0 - first), to = (uint32_t)max((int64_t)0, min(s1, end) - first);
-              it.t0 = lo + (int)(cost == kTileCost ? from / kTileCost : from / kHalfTileCost);
-              it.t1 = lo + (int)(cost == kTileCost ? to / kTileCost : to / kHalfTileCost);
-              if (first + cost - 1 < s0) it.c0 = block_of(first + cost - 1);
-              if (end > s1) it.c1 = block_of(end - 1);
-              ours = it.t0 < it.t1;
-            }
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              it.lo[x] = max(it.lo[x], it.t0);
-              it.hi[x] = max(it.lo[x], min(it.hi[x], it.t1));
-            }
-            it.once = nt == 1;
-            it.off = 0;
-            if (n_tok <= half) {  // every second item of few rows goes to B: one's epilogue runs beside the other's tiles
-              it.off = turn ? kHalf : 0;
-              if (ours) turn = !turn;
-              if (it.off) it.lo[1] = it.lo[0], it.hi[1] = it.hi[0], it.lo[0] = it.hi[0] = it.t0;
-            }
-            if (ours) publish(it);
-            x0 = end;
-            if (++i == nt) i = 0, ++h;
+    regs_down<40>();
+    if (warp == kSchedWarp) {
+      // ---------------- scheduler ----------------
+      auto load = [&](int b) -> Request {  // an empty request where there is nothing to do
+        Request q = {0, 0, 0};
+        if (b < p.batch) {
+          const int r0 = p.q_indptr[b], r1 = p.q_indptr[b + 1], len = p.cache_seqlens[b];
+          if (r0 < 0 || r1 < r0 || r1 > p.total_q || (len < 0 && r1 > r0)) {
+            if (blockIdx.x == 0) report(p.status, PKC_ERR_PLAN);
+          } else if (r1 > r0) {
+            q = {r0, r1 - r0, len};
           }
         }
-      }
-      if (pass == 0) {
-        total = base;
-        n_blocks = (int)max((int64_t)1, min((int64_t)gridDim.x, total / kMinCost));
-        s0 = s1 = total;
-        if (c < n_blocks) {
-          s0 = share_of(c);
-          s1 = share_of(c + 1);
-        }
-      }
-    }
-    if (ok) {
-      Item it;
-      it.b = -1;
-      publish(it);
-    }
-  } else if (warp == kQWarp) {
-    // ---------------- Q copies ----------------
-    const uint64_t pol = l2_policy_evict_first();
-    int n[2] = {0, 0};
-    Item it = {};
-    bool ok = true;
-    for (int k = 0; ok && next_item(k, it); ++k) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (it.lo[x] == it.hi[x]) continue;
-        if (lane == 0) {
-          if (n[x] > 0) ok = wait_for(bar(bars->q_empty[x]), (n[x] - 1) & 1, abort, p.status);
-          if (ok) {
-            const int row = it.q_row + ((x * kHalf - it.off) >> p.g_log2);
-            mbar_arrive_expect_tx(bar(bars->q_full[x]), kTileBytes);
-            tma_load_3d(s_q + x * kTileBytes, &tm_q, bar(bars->q_full[x]), 0, it.kvh * p.g, row, pol);
-            tma_load_3d(s_q + x * kTileBytes + kSub, &tm_q, bar(bars->q_full[x]), 64, it.kvh * p.g, row, pol);
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        ++n[x];
-      }
-    }
-    if (*abort && lane == 0) {  // the copies already issued land before the block exits
-      volatile int no_abort = 0;
-      for (int x = 0; x < 2; ++x)
-        if (n[x] > 0) wait_for(bar(bars->q_full[x]), (n[x] - 1) & 1, &no_abort, p.status);
-    }
-  } else if (warp == kKWarp || warp == kVWarp) {
-    // ---------------- K copies, V copies ----------------
-    const uint64_t keep = l2_policy_evict_last(), pass_by = l2_policy_evict_first();
-    const int bs = p.box_tokens, boxes = 2 * (kKv / bs);  // box c: tokens (c / 2) bs .. of the tile, dims 64 (c % 2) ..
-    const int no_page = (int)max((int64_t)1, p.num_pages);   // outside the pool: read as zeros
-    const void* tmap = warp == kVWarp ? (const void*)&tm_v : (const void*)&tm_k;
-    const int first = warp == kVWarp ? kStagesK : 0, stages = warp == kVWarp ? kStagesV : kStagesK;
-    int g = 0;  // tiles so far
-    Item it = {};
-    bool ok = true;
-    for (int k = 0; ok && next_item(k, it); ++k) {
-      const int32_t* table = p.block_table + (int64_t)it.b * p.bt_stride;
-      // Page of box c of tile t; the lane's first one is loaded a tile ahead.
-      auto page_of = [&](int t, int c) -> int {
-        const int token = t * kKv + (c >> 1) * bs;
-        if (t >= it.t1 || c >= boxes || token >= it.len) return no_page;
-        const int pi = token / p.page_size;
-        return pi < p.bt_stride ? table[pi] : -1;
+        return q;
       };
-      const uint64_t pol = it.once ? pass_by : keep;
-      int ahead = page_of(it.t0, lane);
-      for (int t = it.t0; t < it.t1; ++t, ++g) {
-        const int page = ahead, st = first + g % stages;
-        ahead = page_of(t + 1, lane);
-        if (lane == 0) {
-          if (g >= stages) ok = wait_for(bar(bars->kv_empty[st]), ((g / stages) & 1) ^ 1, abort, p.status);
-          if (ok) mbar_arrive_expect_tx(bar(bars->kv_full[st]), kTileBytes);
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        __syncwarp();
-        for (int c = lane; c < boxes; c += 32) {
-          const int r = (c >> 1) * bs;
-          int pg = c == lane ? page : page_of(t, c);
-          if (t * kKv + r < it.len && (pg < 0 || pg >= p.num_pages)) {
-            report(p.status, PKC_ERR_BLOCK_TABLE);
-            pg = no_page;
-          }
-          tma_load_4d(s_kv + st * kTileBytes + (c & 1) * kSub + r * 128, tmap, bar(bars->kv_full[st]), (c & 1) * 64, it.kvh,
-                      (t * kKv + r) % p.page_size, pg, pol);
-        }
-        __syncwarp();
-      }
-    }
-    if (*abort && lane == 0) {
-      volatile int no_abort = 0;
-      for (int j = max(0, g - stages); j < g; ++j)
-        wait_for(bar(bars->kv_full[first + j % stages]), (j / stages) & 1, &no_abort, p.status);
-    }
-  } else if (warp == kQkWarp || warp == kPvWarp) {
-    // ---------------- MMA issue: Q K, P V ----------------
-    // The whole warp runs the loop and one elected lane issues: with uniform
-    // control flow the descriptors stay in uniform registers.  Both go tile by
-    // tile, A before B.
-    constexpr uint32_t kBf16 = std::is_same<T, __half>::value ? 0 : 1;
-    constexpr uint32_t idesc_qk = idesc_f16(128, 128, kBf16, 0, 0);
-    constexpr uint32_t idesc_pv = idesc_f16(128, 128, kBf16, 0, 1);
-    const uint64_t desc_q = smem_desc_sw128(s_q, 16, 1024);
-    const uint64_t desc_k = smem_desc_sw128(s_kv, 16, 1024), desc_v = smem_desc_sw128(s_kv, kSub, 1024);
-    const bool is_pv = warp == kPvWarp;
-    const int first = is_pv ? kStagesK : 0, behind = is_pv ? kStagesK + kStagesV : kStagesK;
-    int place = first;             // ring place of the next K or V tile, and its phase
-    uint32_t phase = 0, s_par = 1;
-    uint32_t par = 0;              // phases of q_full or p_full, a bit per half
-    Item it = {};
-    for (int k = 0; next_item(k, it); ++k) {
-      for (int t = it.t0; t < it.t1; ++t) {
-        pass(bars->kv_full[place], phase);
-        if (const int live = it.len - t * kKv; is_pv && live < kKv) {
-          // Slots behind the length may hold anything, even NaN: zero their V.
-          const uint32_t vst = s_kv + place * kTileBytes + live * 128;
-          for (int c = lane; c < (kKv - live) * 16; c += 32)
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vst + ((c >> 3) & 1) * kSub + (c >> 4) * 128 +
-                                                                        (c & 7) * 16),
-                         "r"(0u)
-                         : "memory");
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        const uint32_t at = (uint32_t)place * (kTileBytes >> 4);
+      // The cost of all requests, then those that hold some of the block's share:
+      // one loop for both, for its code is long and shares the instruction cache
+      // with the softmax.
+      int64_t total = 0, s0 = 0, s1 = 0;
+      int n_blocks = 1, k = 0;
+      bool turn = false;
+      const int c = (int)blockIdx.x;
+      bool ok = true;
+      // The block that holds place x: the last i with i total / n_blocks <= x.
+      auto block_of = [&](int64_t x) {
+        int n = 0;
 #pragma unroll 1
-        for (int x = 0; x < 2; ++x) {
-          const int lo = x ? it.lo[1] : it.lo[0], hi = x ? it.hi[1] : it.hi[0];
-          if (t < lo || t >= hi) continue;
-          if (!is_pv) {
-            // S = Q K^T once the S before has been read
-            if (t == lo) {
-              pass(bars->q_full[x], (par >> x) & 1);
-              par ^= 1u << x;
-            }
-            pass(bars->s_free, s_par);
-            s_par ^= 1;
-            tc_fence_after();
-            if (elect_one()) {
-#pragma unroll 2
-              for (int kk = 0; kk < 8; ++kk) {
-                const uint32_t off = (kk >> 2) * (kSub >> 4) + (kk & 3) * 2;
-                tc_mma_f16(tmem, desc_q + x * (kTileBytes >> 4) + off, desc_k + at + off, idesc_qk, kk > 0);
+        for (int i = lane; i < kMaxBlocks; i += 32)
+          n += __popc(__ballot_sync(0xffffffffu, i < n_blocks && i * total < (x + 1) * n_blocks));
+        return n - 1;
+      };
+      // i total / n_blocks, in divisions of 32 bits (total < 2^54, n_blocks < 2^8)
+      auto share_of = [&](int i) {
+        const uint32_t a = (uint32_t)(total >> 24), n = (uint32_t)n_blocks;
+        const uint64_t rest = ((uint64_t)(a % n) << 24) | (uint32_t)(total & 0xffffff);  // < n 2^24 <= 2^32
+        const uint64_t q = ((uint64_t)(a / n) << 24) + (uint32_t)rest / n;
+        return (int64_t)(q * i + (uint32_t)rest % n * i / n);
+      };
+      auto publish = [&](const Item& it) {
+        if (lane == 0 && k >= kItems) ok = wait_for(bar(bars->it_empty[k % kItems]), ((k / kItems) & 1) ^ 1, abort, p.status);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (ok && lane == 0) {
+          *reinterpret_cast<Item*>(smem + kItemOffset + (k % kItems) * 64) = it;
+          mbar_arrive(bar(bars->it_full[k % kItems]));
+        }
+        ++k;
+      };
+#pragma unroll 1
+      for (int pass = 0; pass < 2; ++pass) {
+        int64_t base = 0;  // cost of the requests before b0
+#pragma unroll 1
+        for (int b0 = 0; ok && b0 < p.batch && (pass == 0 || base < s1); b0 += 32) {
+          const Request mine = load(b0 + lane);
+          const int64_t per_head = mine.n ? cost_of(p, mine, n_items(p, mine)) : 0;
+          int64_t before = per_head * p.hkv;
+#pragma unroll 1
+          for (int d = 1; d < 32; d <<= 1) {
+            const int64_t y = __shfl_up_sync(0xffffffffu, before, d);
+            if (lane >= d) before += y;
+          }
+          const int64_t all = __shfl_sync(0xffffffffu, before, 31);
+          before = base + before - per_head * p.hkv;
+          base += all;
+          if (pass == 0) continue;
+          uint32_t todo = __ballot_sync(0xffffffffu, mine.n > 0 && before < s1 && before + per_head * p.hkv > s0);
+#pragma unroll 1
+          for (; ok && todo; todo &= todo - 1) {
+            const int j = __ffs(todo) - 1;
+            const Request q = {__shfl_sync(0xffffffffu, mine.r0, j), __shfl_sync(0xffffffffu, mine.n, j),
+                               __shfl_sync(0xffffffffu, mine.len, j)};
+            const int64_t ph = __shfl_sync(0xffffffffu, per_head, j);
+            const int nt = n_items(p, q);
+            int h = 0, i = 0;
+            int64_t x0 = __shfl_sync(0xffffffffu, before, j);  // where item (h, i) begins
+            if (s0 > x0) {
+#pragma unroll 1
+              for (int step = 1 << 16; step; step >>= 1)
+                if (x0 + step * ph <= s0) h += step, x0 += step * ph;
+              // the last i whose items before it cost at most s0 - x0
+              int hi = nt;
+              int64_t at = 0;
+#pragma unroll 1
+              while (hi - i > 1) {
+                const int mid = (i + hi) >> 1;
+                const int64_t cost = cost_of(p, q, mid);
+                if (cost <= s0 - x0) i = mid, at = cost;
+                else hi = mid;
               }
-              tc_commit(bar(bars->s_full[x]));
-              if (t == hi - 1) tc_commit(bar(bars->q_empty[x]));
+              x0 += at;
             }
-          } else {
-            // O += P V once P is there (and O of the piece before has been read
-            // out: by the warps that made this P)
-            pass(bars->p_full[x], (par >> x) & 1);
-            par ^= 1u << x;
-            tc_fence_after();
-            if (elect_one()) {
-              const uint32_t more = t > lo ? 1u : 0u;
-#pragma unroll 2
-              for (int kk = 0; kk < 8; ++kk)
-                tc_mma_f16_ta(tmem + 256 + x * 128, tmem + 128 + x * 64 + kk * 8, desc_v + at + kk * (2048 >> 4), idesc_pv,
-                              kk > 0 ? 1u : more);
-              tc_commit(bar(bars->pv_done[x]));
+#pragma unroll 1
+            while (ok && h < p.hkv && x0 < s1) {
+              const int j0 = i << item_shift(p), n_tok = min(1 << item_shift(p), q.n - j0);
+              Item it;
+              it.b = b0 + j; it.kvh = h; it.q_row = q.r0 + j0; it.n_tok = n_tok;
+              it.pos0 = q.len - q.n + j0; it.len = q.len;
+              const int half = kHalf >> p.g_log2;
+              reach(p, q, j0, j0 + min(n_tok, half), it.lo[0], it.hi[0]);
+              it.lo[1] = it.hi[1] = it.hi[0];
+              if (n_tok > half) reach(p, q, j0 + half, j0 + n_tok, it.lo[1], it.hi[1]);
+              const int lo = it.lo[0], hi = it.hi[1];  // (a later token's reach begins and ends no earlier)
+              const int cost = tile_cost(p, q, i);
+              const int64_t first = x0 + kOver, end = first + (int64_t)(hi - lo) * cost;  // its tiles lie at first .. end - 1
+              it.t0 = lo;
+              it.t1 = hi;
+              it.c0 = it.c1 = c;
+              bool ours = end > s0 && end <= s1;  // a short item is whole, its last place's block has it
+              if (hi - lo > kShort) {
+                // (a block's share is larger than a tile's cost: no piece between is empty)
+                const uint32_t from = (uint32_t)max((int64_t)0, s0 - first), to = (uint32_t)max((int64_t)0, min(s1, end) - first);
+                it.t0 = lo + (int)(cost == kTileCost ? from / kTileCost : from / kHalfTileCost);
+                it.t1 = lo + (int)(cost == kTileCost ? to / kTileCost : to / kHalfTileCost);
+                if (first + cost - 1 < s0) it.c0 = block_of(first + cost - 1);
+                if (end > s1) it.c1 = block_of(end - 1);
+                ours = it.t0 < it.t1;
+              }
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                it.lo[x] = max(it.lo[x], it.t0);
+                it.hi[x] = max(it.lo[x], min(it.hi[x], it.t1));
+              }
+              it.once = nt == 1;
+              it.off = 0;
+              if (n_tok <= half) {  // every second item of few rows goes to B: one's epilogue runs beside the other's tiles
+                it.off = turn ? kHalf : 0;
+                if (ours) turn = !turn;
+                if (it.off) it.lo[1] = it.lo[0], it.hi[1] = it.hi[0], it.lo[0] = it.hi[0] = it.t0;
+              }
+              if (ours) publish(it);
+              x0 = end;
+              if (++i == nt) i = 0, ++h;
             }
+          }
+        }
+        if (pass == 0) {
+          total = base;
+          n_blocks = (int)max((int64_t)1, min((int64_t)gridDim.x, total / kMinCost));
+          s0 = s1 = total;
+          if (c < n_blocks) {
+            s0 = share_of(c);
+            s1 = share_of(c + 1);
+          }
+        }
+      }
+      if (ok) {
+        Item it;
+        it.b = -1;
+        publish(it);
+      }
+    } else if (warp == kQWarp) {
+      // ---------------- Q copies ----------------
+      const uint64_t pol = l2_policy_evict_first();
+      int n[2] = {0, 0};
+      Item it = {};
+      bool ok = true;
+      for (int k = 0; ok && next_item(k, it); ++k) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (it.lo[x] == it.hi[x]) continue;
+          if (lane == 0) {
+            if (n[x] > 0) ok = wait_for(bar(bars->q_empty[x]), (n[x] - 1) & 1, abort, p.status);
+            if (ok) {
+              const int row = it.q_row + ((x * kHalf - it.off) >> p.g_log2);
+              mbar_arrive_expect_tx(bar(bars->q_full[x]), kTileBytes);
+              tma_load_3d(s_q + x * kTileBytes, &tm_q, bar(bars->q_full[x]), 0, it.kvh * p.g, row, pol);
+              tma_load_3d(s_q + x * kTileBytes + kSub, &tm_q, bar(bars->q_full[x]), 64, it.kvh * p.g, row, pol);
+            }
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          ++n[x];
+        }
+      }
+      if (*abort && lane == 0) {  // the copies already issued land before the block exits
+        volatile int no_abort = 0;
+        for (int x = 0; x < 2; ++x)
+          if (n[x] > 0) wait_for(bar(bars->q_full[x]), (n[x] - 1) & 1, &no_abort, p.status);
+      }
+    } else if (warp == kKWarp || warp == kVWarp) {
+      // ---------------- K copies, V copies ----------------
+      const uint64_t keep = l2_policy_evict_last(), pass_by = l2_policy_evict_first();
+      const int bs = p.box_tokens, boxes = 2 * (kKv / bs);  // box c: tokens (c / 2) bs .. of the tile, dims 64 (c % 2) ..
+      const int no_page = (int)max((int64_t)1, p.num_pages);   // outside the pool: read as zeros
+      const void* tmap = warp == kVWarp ? (const void*)&tm_v : (const void*)&tm_k;
+      const int first = warp == kVWarp ? kStagesK : 0, stages = warp == kVWarp ? kStagesV : kStagesK;
+      int g = 0;  // tiles so far
+      Item it = {};
+      bool ok = true;
+      for (int k = 0; ok && next_item(k, it); ++k) {
+        const int32_t* table = p.block_table + (int64_t)it.b * p.bt_stride;
+        // Page of box c of tile t; the lane's first one is loaded a tile ahead.
+        auto page_of = [&](int t, int c) -> int {
+          const int token = t * kKv + (c >> 1) * bs;
+          if (t >= it.t1 || c >= boxes || token >= it.len) return no_page;
+          const int pi = token / p.page_size;
+          return pi < p.bt_stride ? table[pi] : -1;
+        };
+        const uint64_t pol = it.once ? pass_by : keep;
+        int ahead = page_of(it.t0, lane);
+        for (int t = it.t0; t < it.t1; ++t, ++g) {
+          const int page = ahead, st = first + g % stages;
+          ahead = page_of(t + 1, lane);
+          if (lane == 0) {
+            if (g >= stages) ok = wait_for(bar(bars->kv_empty[st]), ((g / stages) & 1) ^ 1, abort, p.status);
+            if (ok) mbar_arrive_expect_tx(bar(bars->kv_full[st]), kTileBytes);
+          }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          __syncwarp();
+          for (int c = lane; c < boxes; c += 32) {
+            const int r = (c >> 1) * bs;
+            int pg = c == lane ? page : page_of(t, c);
+            if (t * kKv + r < it.len && (pg < 0 || pg >= p.num_pages)) {
+              report(p.status, PKC_ERR_BLOCK_TABLE);
+              pg = no_page;
+            }
+            tma_load_4d(s_kv + st * kTileBytes + (c & 1) * kSub + r * 128, tmap, bar(bars->kv_full[st]), (c & 1) * 64, it.kvh,
+                        (t * kKv + r) % p.page_size, pg, pol);
           }
           __syncwarp();
         }
-        if (elect_one()) tc_commit(bar(bars->kv_empty[place]));
-        __syncwarp();
-        if (++place == behind) place = first, phase ^= 1;
       }
+      if (*abort && lane == 0) {
+        volatile int no_abort = 0;
+        for (int j = max(0, g - stages); j < g; ++j)
+          wait_for(bar(bars->kv_full[first + j % stages]), (j / stages) & 1, &no_abort, p.status);
+      }
+    } else if (warp == kQkWarp || warp == kPvWarp) {
+      // ---------------- MMA issue: Q K, P V ----------------
+      // The whole warp runs the loop and one elected lane issues: with uniform
+      // control flow the descriptors stay in uniform registers.  Both go tile by
+      // tile, A before B.
+      constexpr uint32_t kBf16 = std::is_same<T, __half>::value ? 0 : 1;
+      constexpr uint32_t idesc_qk = idesc_f16(128, 128, kBf16, 0, 0);
+      constexpr uint32_t idesc_pv = idesc_f16(128, 128, kBf16, 0, 1);
+      const uint64_t desc_q = smem_desc_sw128(s_q, 16, 1024);
+      const uint64_t desc_k = smem_desc_sw128(s_kv, 16, 1024), desc_v = smem_desc_sw128(s_kv, kSub, 1024);
+      const bool is_pv = warp == kPvWarp;
+      const int first = is_pv ? kStagesK : 0, behind = is_pv ? kStagesK + kStagesV : kStagesK;
+      int place = first;             // ring place of the next K or V tile, and its phase
+      uint32_t phase = 0, s_par = 1;
+      uint32_t par = 0;              // phases of q_full or p_full, a bit per half
+      Item it = {};
+      for (int k = 0; next_item(k, it); ++k) {
+        for (int t = it.t0; t < it.t1; ++t) {
+          pass(bars->kv_full[place], phase);
+          if (const int live = it.len - t * kKv; is_pv && live < kKv) {
+            // Slots behind the length may hold anything, even NaN: zero their V.
+            const uint32_t vst = s_kv + place * kTileBytes + live * 128;
+            for (int c = lane; c < (kKv - live) * 16; c += 32)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vst + ((c >> 3) & 1) * kSub + (c >> 4) * 128 +
+                                                                          (c & 7) * 16),
+                           "r"(0u)
+                           : "memory");
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          const uint32_t at = (uint32_t)place * (kTileBytes >> 4);
+#pragma unroll 1
+          for (int x = 0; x < 2; ++x) {
+            const int lo = x ? it.lo[1] : it.lo[0], hi = x ? it.hi[1] : it.hi[0];
+            if (t < lo || t >= hi) continue;
+            if (!is_pv) {
+              // S = Q K^T once the S before has been read
+              if (t == lo) {
+                pass(bars->q_full[x], (par >> x) & 1);
+                par ^= 1u << x;
+              }
+              pass(bars->s_free, s_par);
+              s_par ^= 1;
+              tc_fence_after();
+              if (elect_one()) {
+#pragma unroll 2
+                for (int kk = 0; kk < 8; ++kk) {
+                  const uint32_t off = (kk >> 2) * (kSub >> 4) + (kk & 3) * 2;
+                  tc_mma_f16(tmem, desc_q + x * (kTileBytes >> 4) + off, desc_k + at + off, idesc_qk, kk > 0);
+                }
+                tc_commit(bar(bars->s_full[x]));
+                if (t == hi - 1) tc_commit(bar(bars->q_empty[x]));
+              }
+            } else {
+              // O += P V once P is there (and O of the piece before has been read
+              // out: by the warps that made this P)
+              pass(bars->p_full[x], (par >> x) & 1);
+              par ^= 1u << x;
+              tc_fence_after();
+              if (elect_one()) {
+                const uint32_t more = t > lo ? 1u : 0u;
+#pragma unroll 2
+                for (int kk = 0; kk < 8; ++kk)
+                  tc_mma_f16_ta(tmem + 256 + x * 128, tmem + 128 + x * 64 + kk * 8, desc_v + at + kk * (2048 >> 4), idesc_pv,
+                                kk > 0 ? 1u : more);
+                tc_commit(bar(bars->pv_done[x]));
+              }
+            }
+            __syncwarp();
+          }
+          if (elect_one()) tc_commit(bar(bars->kv_empty[place]));
+          __syncwarp();
+          if (++place == behind) place = first, phase ^= 1;
+        }
+      }
+      // Every MMA issued above completes before TMEM is released.
+      if (elect_one()) tc_commit(bar(bars->drain));
+      __syncwarp();
+      volatile int no_abort = 0;
+      wait_for(bar(bars->drain), 0, &no_abort, p.status);
+      __syncwarp();
     }
-    // Every MMA issued above completes before TMEM is released.
-    if (elect_one()) tc_commit(bar(bars->drain));
-    __syncwarp();
-    volatile int no_abort = 0;
-    wait_for(bar(bars->drain), 0, &no_abort, p.status);
-    __syncwarp();
-  }
   } else {
     // ---------------- softmax, epilogue, merge: a row per thread ----------------
     regs_up<216>();

@@ -60,8 +60,9 @@
 // NaN would be NaN: slots behind the length are zeroed in the V tile, and a row
 // whose O is not finite is computed again key by key (slow_rows) where its boundary
 // tiles hold such a value, so it reaches exactly the rows that attend to it, at no
-// cost where there is none.  So are rows whose scores pass 2^20: a float32 exponent
-// holds too little of them for one rounding.
+// cost where there is none.  So are rows whose scores pass 2^26 (bf16: 2^30), which
+// one rounding moves too far.  A key costs such rows some 25 ns each; a launch of
+// which they take more than the 2 s that the others wait ends with the time-out.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -102,7 +103,8 @@ constexpr float kMoveSum = 8192.f;       // a tile's sum of P above which its re
 // P = exp2(s c - m_ref) in one rounding: m_ref = max s c is rounded, P's largest is
 // exp2 of that rounding, at most 2^(m_ref / 2^24).  Rows with |m_ref| from here on are
 // computed again with the product rounded too (slow_rows).
-constexpr float kFar = 1048576.f;
+// Below, that factor is at most 2^4 in fp16 and 2^64 in bf16, which their P hold.
+template <typename T> constexpr float kFar = std::is_same<T, __half>::value ? 0x1p26f : 0x1p30f;
 
 struct Item {
   int b;                 // request; -1: no more items
@@ -321,11 +323,17 @@ __device__ __forceinline__ int page_of_key(const ChunkParams& p, int b, int t, i
 // of it is held in the loops of those who call it.)
 template <typename T>
 __device__ __noinline__ void slow_rows(const ChunkParams& p, uint32_t far, uint32_t odd, int row0, int b, int kvh, int q_row,
-                                       int pos0, int len, int t0, int t1, int all_lo, int all_hi, int slot) {
+                                       int pos0, int len, int t0, int t1, int all_lo, int all_hi, int slot,
+                                       volatile int* abort) {
   const int lane = threadIdx.x & 31;
   const int begin = t0 * kKv, end = (int)min((int64_t)len, (int64_t)t1 * kKv);
-  auto at = [&](int page, int t) {
-    return (((int64_t)page * p.page_size + t % p.page_size) * p.hkv + kvh) * PKC_HEAD_DIM + 4 * lane;
+  const T* q = static_cast<const T*>(p.q) + 4 * lane;
+  // Four elements of key t; a page that is not there is read as zeros (the load goes
+  // somewhere all the same, so that eight are on their way together).
+  auto load = [&](const void* pool, int page, int t) {
+    const int64_t at = (((int64_t)page * p.page_size + t % p.page_size) * p.hkv + kvh) * PKC_HEAD_DIM;
+    const uint2 w = *reinterpret_cast<const uint2*>(page < 0 ? q : static_cast<const T*>(pool) + at + 4 * lane);
+    return page < 0 ? make_uint2(0, 0) : w;
   };
   if (odd) {
     float sum = 0.f;  // 0 times the values
@@ -337,85 +345,102 @@ __device__ __noinline__ void slow_rows(const ChunkParams& p, uint32_t far, uint3
       const int pages = page_of_key(p, b, (int)t + lane, end);
 #pragma unroll 8
       for (int i = 0; i < 32; ++i) {
-        const int page = __shfl_sync(0xffffffffu, pages, i);
-        if (page < 0) continue;
-        const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.v_cache) + at(page, (int)t + i));
-        const float2 a = Elem<T>::to_f2(w.x), c = Elem<T>::to_f2(w.y);
-        sum += 0.f * a.x + 0.f * a.y + 0.f * c.x + 0.f * c.y;
+        const uint2 w = load(p.v_cache, __shfl_sync(0xffffffffu, pages, i), (int)t + i);
+        const float2 x = Elem<T>::to_f2(w.x), y = Elem<T>::to_f2(w.y);
+        sum += 0.f * x.x + 0.f * x.y + 0.f * y.x + 0.f * y.y;
       }
     }
     if (__any_sync(0xffffffffu, !(sum == 0.f))) far |= odd;
   }
-  for (; far; far &= far - 1) {
-    const int row = row0 + __ffs(far) - 1;
-    const int64_t out = out_row(p, q_row, kvh, row);
-    int lo, hi;
-    tokens_of(p, pos0 + (row >> p.g_log2), len, lo, hi);
-    lo = max(lo, begin);
-    hi = min(hi, end);
-    const uint2 qw = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.q) + out * PKC_HEAD_DIM + 4 * lane);
-    const float2 q0 = Elem<T>::to_f2(qw.x), q1 = Elem<T>::to_f2(qw.y);
-    float m = neg_inf(), l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int64_t tb = lo; tb < hi; tb += 32) {
-      const int pages = page_of_key(p, b, (int)tb + lane, hi);
+  constexpr int kAtOnce = 4;
+  while (far) {
+    int row[kAtOnce], lo[kAtOnce], hi[kAtOnce], n = 0, first = end, last = begin;
+    float2 q0[kAtOnce], q1[kAtOnce];
+    float m[kAtOnce], l[kAtOnce], o[kAtOnce][4];
+#pragma unroll
+    for (int r = 0; r < kAtOnce; ++r) {
+      row[r] = r && !far ? row[r - 1] : row0 + __ffs(far) - 1;  // (the last one again where there are fewer)
+      n += far != 0;
+      far &= far - 1;
+      tokens_of(p, pos0 + (row[r] >> p.g_log2), len, lo[r], hi[r]);
+      lo[r] = max(lo[r], begin);
+      hi[r] = min(hi[r], end);
+      first = min(first, lo[r]);
+      last = max(last, hi[r]);
+      const uint2 w = *reinterpret_cast<const uint2*>(q + out_row(p, q_row, kvh, row[r]) * PKC_HEAD_DIM);
+      q0[r] = Elem<T>::to_f2(w.x);
+      q1[r] = Elem<T>::to_f2(w.y);
+      m[r] = neg_inf();
+      l[r] = o[r][0] = o[r][1] = o[r][2] = o[r][3] = 0.f;
+    }
+    for (int64_t tb = first; tb < last && !*abort; tb += 32) {
+      const int pages = page_of_key(p, b, (int)tb + lane, last);
 #pragma unroll 1
-      for (int i0 = 0; i0 < 32 && tb + i0 < hi; i0 += 8) {
-        uint2 vw[8];
-        float s[8];
+      for (int i0 = 0; i0 < 32 && tb + i0 < last; i0 += 8) {
+        uint2 kw[8], vw[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int page = __shfl_sync(0xffffffffu, pages, i0 + i);
-          uint2 kw = make_uint2(0, 0);
-          vw[i] = make_uint2(0, 0);
-          if (page >= 0) {
-            const int64_t x = at(page, (int)tb + i0 + i);
-            kw = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.k_cache) + x);
-            vw[i] = *reinterpret_cast<const uint2*>(static_cast<const T*>(p.v_cache) + x);
+          kw[i] = load(p.k_cache, page, (int)tb + i0 + i);
+          vw[i] = load(p.v_cache, page, (int)tb + i0 + i);
+        }
+#pragma unroll
+        for (int r = 0; r < kAtOnce; ++r) {
+          float s[8], mn = m[r];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 k0 = Elem<T>::to_f2(kw[i].x), k1 = Elem<T>::to_f2(kw[i].y);
+            s[i] = q0[r].x * k0.x + q0[r].y * k0.y + q1[r].x * k1.x + q1[r].y * k1.y;
           }
-          const float2 k0 = Elem<T>::to_f2(kw.x), k1 = Elem<T>::to_f2(kw.y);
-          s[i] = q0.x * k0.x + q0.y * k0.y + q1.x * k1.x + q1.y * k1.y;
-        }
-        float mn = m;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
+          for (int d = 16; d; d >>= 1)
 #pragma unroll
-          for (int d = 16; d; d >>= 1) s[i] += __shfl_xor_sync(0xffffffffu, s[i], d);
-          s[i] = tb + i0 + i < hi ? __fmul_rn(s[i], p.scale_log2) : neg_inf();
-          mn = fmaxf(mn, s[i]);
-        }
-        const float ref = mn == neg_inf() ? 0.f : mn, w = ex2(m - ref);
-        m = mn;
-        l *= w;
+            for (int i = 0; i < 8; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], d);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] *= w;
+          for (int i = 0; i < 8; ++i) {
+            const int64_t t = tb + i0 + i;
+            s[i] = t >= lo[r] && t < hi[r] ? __fmul_rn(s[i], p.scale_log2) : neg_inf();
+            mn = fmaxf(mn, s[i]);
+          }
+          const float ref = mn == neg_inf() ? 0.f : mn, w = ex2(m[r] - ref);
+          m[r] = mn;
+          l[r] *= w;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (tb + i0 + i >= hi) break;
-          const float e = ex2(__fsub_rn(s[i], ref));
-          const float2 v0 = Elem<T>::to_f2(vw[i].x), v1 = Elem<T>::to_f2(vw[i].y);
-          l += e;
-          o[0] += e * v0.x;
-          o[1] += e * v0.y;
-          o[2] += e * v1.x;
-          o[3] += e * v1.y;
+          for (int i = 0; i < 4; ++i) o[r][i] *= w;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int64_t t = tb + i0 + i;
+            if (t < lo[r] || t >= hi[r]) continue;  // (uniform; the value may be anything)
+            const float e = ex2(__fsub_rn(s[i], ref));
+            const float2 v0 = Elem<T>::to_f2(vw[i].x), v1 = Elem<T>::to_f2(vw[i].y);
+            l[r] += e;
+            o[r][0] += e * v0.x;
+            o[r][1] += e * v0.y;
+            o[r][2] += e * v1.x;
+            o[r][3] += e * v1.y;
+          }
         }
       }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l, lse2 = l == 0.f ? neg_inf() : m + lg2(l);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] *= inv;
-    if (slot >= 0) {
-      *reinterpret_cast<float4*>(part_row(p, slot, lane, row)) = make_float4(o[0], o[1], o[2], o[3]);
-    } else if (p.out_dtype == PKC_F32) {
-      *reinterpret_cast<float4*>(static_cast<float*>(p.o) + out * PKC_HEAD_DIM + 4 * lane) =
-          make_float4(o[0], o[1], o[2], o[3]);
-    } else {
-      *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + out * PKC_HEAD_DIM + 4 * lane) =
-          make_uint2(Elem<T>::from_f2(o[0], o[1]), Elem<T>::from_f2(o[2], o[3]));
-    }
-    if (lane == 0) {
-      if (slot >= 0) p.part_lse[slot * kRows + row] = lse2;
-      else p.lse[out] = lse2 * kLn2;
+    for (int r = 0; r < kAtOnce; ++r) {
+      if (r >= n) break;
+      const float inv = l[r] == 0.f ? 0.f : 1.f / l[r], lse2 = l[r] == 0.f ? neg_inf() : m[r] + lg2(l[r]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[r][i] *= inv;
+      const int64_t out = out_row(p, q_row, kvh, row[r]);
+      if (slot >= 0)
+        *reinterpret_cast<float4*>(part_row(p, slot, lane, row[r])) = make_float4(o[r][0], o[r][1], o[r][2], o[r][3]);
+      else if (p.out_dtype == PKC_F32)
+        *reinterpret_cast<float4*>(static_cast<float*>(p.o) + out * PKC_HEAD_DIM + 4 * lane) =
+            make_float4(o[r][0], o[r][1], o[r][2], o[r][3]);
+      else
+        *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + out * PKC_HEAD_DIM + 4 * lane) =
+            make_uint2(Elem<T>::from_f2(o[r][0], o[r][1]), Elem<T>::from_f2(o[r][2], o[r][3]));
+      if (lane == 0) {
+        if (slot >= 0) p.part_lse[slot * kRows + row[r]] = lse2;
+        else p.lse[out] = lse2 * kLn2;
+      }
     }
   }
 }
@@ -1028,10 +1053,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         odd = !(z.x + z.y == 0.f);
       }
       tc_fence_before();  // O has been read out: the next P's arrival says so
-      const bool far = mine && m_ref != neg_inf() && !(fabsf(m_ref) < kFar);
+      const bool far = mine && m_ref != neg_inf() && !(fabsf(m_ref) < kFar<T>);
       if (const uint32_t todo = __ballot_sync(0xffffffffu, (odd || far) && valid); todo) {
         const uint32_t f = __ballot_sync(0xffffffffu, far && valid);
-        slow_rows<T>(p, f, todo & ~f, row0, it.b, it.kvh, it.q_row, it.pos0, it.len, lo, hi, lo_max, hi_min, cut ? slot : -1);
+        slow_rows<T>(p, f, todo & ~f, row0, it.b, it.kvh, it.q_row, it.pos0, it.len, lo, hi, lo_max, hi_min, cut ? slot : -1, abort);
       }
 
       if (cut) {

@@ -149,8 +149,8 @@ def test_scores_far_out(dtype, q_exp, k_exp, sign):
     that power, exactly, and two different ones lie more than 2^9 apart (weights
     exp(-2^9) = 0 in 32 bits).  The rows that share the largest one share its weight
     too, which need not be 1: it is exp2 of what is lost where scale q.k log2(e) is
-    rounded (up to 2^17 2^-24 below the scores that are computed again), so it is
-    rounded to 16 bits where it meets V, half a step, and O is rounded, another half.
+    rounded, so it is rounded to 16 bits where it meets V, half a step, and O is
+    rounded, another half.
     The values are below 2^3 and sum in 32 bits: 2^-19 for a few roundings.  LSE has
     the rounding of the scaled score and of the sum's logarithm."""
     c = Case([(150, 700), (3, 200), (1, 0), (140, 0)], 4, 1, dtype, seed=11, scale=1.0)

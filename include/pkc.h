@@ -813,8 +813,9 @@ int pkc_chunk_workspace_size(size_t* bytes);
  * key and value hold.  Probabilities enter the V product in dtype.  Rows whose
  * largest scaled score passes 2^26 / log2(e) in magnitude (BF16: 2^30 / log2(e)),
  * and rows next to a value that is not finite and not theirs, are computed a key
- * at a time: right, at some 25 ns a key, and ended by PKC_ERR_TIMEOUT where that
- * takes a block's other warps past their 2 s.  A page id < 0 or >= num_pages (or past the table) is read as zeros and recorded as
+ * at a time: right, at up to 100 ns a key, and ended by PKC_ERR_TIMEOUT where that
+ * takes a block's other warps past their 2 s (rows next to such a value over some
+ * 10^6 tokens).  A page id < 0 or >= num_pages (or past the table) is read as zeros and recorded as
  * PKC_ERR_BLOCK_TABLE.  A request whose rows do not lie within 0 .. total_q, or
  * with a negative length, is not computed (PKC_ERR_PLAN).  The results do not
  * depend on the order in which blocks run.  The status block holds which partial

@@ -61,8 +61,9 @@
 // whose O is not finite is computed again key by key (slow_rows) where its boundary
 // tiles hold such a value, so it reaches exactly the rows that attend to it, at no
 // cost where there is none.  So are rows whose scores pass 2^26 (bf16: 2^30), which
-// one rounding moves too far.  A key costs such rows some 25 ns each; a launch of
-// which they take more than the 2 s that the others wait ends with the time-out.
+// one rounding moves too far.  A key costs such a row 60 to 100 ns (a NaN among
+// 2047 new tokens over 65,001: 209 ms); where that takes more than the 2 s that a
+// block's other warps wait, the launch ends with the time-out.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -318,8 +319,7 @@ __device__ __forceinline__ int page_of_key(const ChunkParams& p, int b, int t, i
 // taken off, so the largest weight is 1.  `odd`: rows whose O is not finite.  They
 // are right as they are unless a value of the tiles that not all of the warp's rows
 // attend to (a key outside [all_lo, all_hi)) is not finite itself.  Lanes hold four
-// elements each; eight keys go at once.  slot: the partial states' place, or -1 for
-// an item that is not cut.  (Out of line, with the item's fields by value: nothing
+// elements each.  slot: the partial states' place, or -1 for an item that is not cut.  (Out of line, with the item's fields by value: nothing
 // of it is held in the loops of those who call it.)
 template <typename T>
 __device__ __noinline__ void slow_rows(const ChunkParams& p, uint32_t far, uint32_t odd, int row0, int b, int kvh, int q_row,
@@ -352,82 +352,94 @@ __device__ __noinline__ void slow_rows(const ChunkParams& p, uint32_t far, uint3
     }
     if (__any_sync(0xffffffffu, !(sum == 0.f))) far |= odd;
   }
+  // Four rows and eight keys at a time: 32 scores, summed over the lanes so that
+  // lane 8 r + i ends with that of row r and key i, and holds row r's maximum and sum.
   constexpr int kAtOnce = 4;
   while (far) {
-    int row[kAtOnce], lo[kAtOnce], hi[kAtOnce], n = 0, first = end, last = begin;
+    int row[kAtOnce], n = 0, first = end, last = begin, lo = 0, hi = 0;
     float2 q0[kAtOnce], q1[kAtOnce];
-    float m[kAtOnce], l[kAtOnce], o[kAtOnce][4];
+    float m = neg_inf(), l = 0.f, o[kAtOnce][4] = {};
 #pragma unroll
     for (int r = 0; r < kAtOnce; ++r) {
       row[r] = r && !far ? row[r - 1] : row0 + __ffs(far) - 1;  // (the last one again where there are fewer)
       n += far != 0;
       far &= far - 1;
-      tokens_of(p, pos0 + (row[r] >> p.g_log2), len, lo[r], hi[r]);
-      lo[r] = max(lo[r], begin);
-      hi[r] = min(hi[r], end);
-      first = min(first, lo[r]);
-      last = max(last, hi[r]);
+      int a, z;
+      tokens_of(p, pos0 + (row[r] >> p.g_log2), len, a, z);
+      a = max(a, begin);
+      z = min(z, end);
+      first = min(first, a);
+      last = max(last, z);
+      if (lane >> 3 == r) lo = a, hi = z;
       const uint2 w = *reinterpret_cast<const uint2*>(q + out_row(p, q_row, kvh, row[r]) * PKC_HEAD_DIM);
       q0[r] = Elem<T>::to_f2(w.x);
       q1[r] = Elem<T>::to_f2(w.y);
-      m[r] = neg_inf();
-      l[r] = o[r][0] = o[r][1] = o[r][2] = o[r][3] = 0.f;
     }
     for (int64_t tb = first; tb < last && !*abort; tb += 32) {
       const int pages = page_of_key(p, b, (int)tb + lane, last);
 #pragma unroll 1
       for (int i0 = 0; i0 < 32 && tb + i0 < last; i0 += 8) {
-        uint2 kw[8], vw[8];
+        uint2 vw[8];
+        float s[8 * kAtOnce];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int page = __shfl_sync(0xffffffffu, pages, i0 + i);
-          kw[i] = load(p.k_cache, page, (int)tb + i0 + i);
+          const uint2 kw = load(p.k_cache, page, (int)tb + i0 + i);
           vw[i] = load(p.v_cache, page, (int)tb + i0 + i);
+          const float2 k0 = Elem<T>::to_f2(kw.x), k1 = Elem<T>::to_f2(kw.y);
+#pragma unroll
+          for (int r = 0; r < kAtOnce; ++r) s[8 * r + i] = q0[r].x * k0.x + q0[r].y * k0.y + q1[r].x * k1.x + q1[r].y * k1.y;
         }
 #pragma unroll
+        for (int d = 16; d; d >>= 1) {
+          const bool up = lane & d;
+#pragma unroll
+          for (int j = 0; j < d; ++j) {
+            const float other = __shfl_xor_sync(0xffffffffu, up ? s[j] : s[j + d], d);
+            s[j] = (up ? s[j + d] : s[j]) + other;
+          }
+        }
+        const int64_t t = tb + i0 + (lane & 7);
+        const bool in = t >= lo && t < hi;
+        const float score = in ? __fmul_rn(s[0], p.scale_log2) : neg_inf();
+        float now = fmaxf(m, score);
+#pragma unroll
+        for (int d = 4; d; d >>= 1) now = fmaxf(now, __shfl_xor_sync(0xffffffffu, now, d));
+        const float ref = now == neg_inf() ? 0.f : now, w = ex2(m - ref), e = in ? ex2(__fsub_rn(score, ref)) : 0.f;
+        float sum = e;
+#pragma unroll
+        for (int d = 4; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        m = now;
+        l = l * w + sum;
+        const uint32_t ins = __ballot_sync(0xffffffffu, in);
+#pragma unroll
         for (int r = 0; r < kAtOnce; ++r) {
-          float s[8], mn = m[r];
+          const float wr = __shfl_sync(0xffffffffu, w, 8 * r);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 k0 = Elem<T>::to_f2(kw[i].x), k1 = Elem<T>::to_f2(kw[i].y);
-            s[i] = q0[r].x * k0.x + q0[r].y * k0.y + q1[r].x * k1.x + q1[r].y * k1.y;
-          }
+          for (int i = 0; i < 4; ++i) o[r][i] *= wr;
+        }
 #pragma unroll
-          for (int d = 16; d; d >>= 1)
+        for (int i = 0; i < 8; ++i) {
+          const float2 v0 = Elem<T>::to_f2(vw[i].x), v1 = Elem<T>::to_f2(vw[i].y);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], d);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int64_t t = tb + i0 + i;
-            s[i] = t >= lo[r] && t < hi[r] ? __fmul_rn(s[i], p.scale_log2) : neg_inf();
-            mn = fmaxf(mn, s[i]);
-          }
-          const float ref = mn == neg_inf() ? 0.f : mn, w = ex2(m[r] - ref);
-          m[r] = mn;
-          l[r] *= w;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) o[r][i] *= w;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int64_t t = tb + i0 + i;
-            if (t < lo[r] || t >= hi[r]) continue;  // (uniform; the value may be anything)
-            const float e = ex2(__fsub_rn(s[i], ref));
-            const float2 v0 = Elem<T>::to_f2(vw[i].x), v1 = Elem<T>::to_f2(vw[i].y);
-            l[r] += e;
-            o[r][0] += e * v0.x;
-            o[r][1] += e * v0.y;
-            o[r][2] += e * v1.x;
-            o[r][3] += e * v1.y;
+          for (int r = 0; r < kAtOnce; ++r) {
+            const float er = __shfl_sync(0xffffffffu, e, 8 * r + i);
+            if (!(ins >> (8 * r + i) & 1)) continue;  // (uniform; the value may be anything)
+            o[r][0] += er * v0.x;
+            o[r][1] += er * v0.y;
+            o[r][2] += er * v1.x;
+            o[r][3] += er * v1.y;
           }
         }
       }
     }
+    const float inv = l == 0.f ? 0.f : 1.f / l, lse2 = l == 0.f ? neg_inf() : m + lg2(l);
 #pragma unroll
     for (int r = 0; r < kAtOnce; ++r) {
+      const float f = __shfl_sync(0xffffffffu, inv, 8 * r);
       if (r >= n) break;
-      const float inv = l[r] == 0.f ? 0.f : 1.f / l[r], lse2 = l[r] == 0.f ? neg_inf() : m[r] + lg2(l[r]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) o[r][i] *= inv;
+      for (int i = 0; i < 4; ++i) o[r][i] *= f;
       const int64_t out = out_row(p, q_row, kvh, row[r]);
       if (slot >= 0)
         *reinterpret_cast<float4*>(part_row(p, slot, lane, row[r])) = make_float4(o[r][0], o[r][1], o[r][2], o[r][3]);
@@ -437,7 +449,7 @@ __device__ __noinline__ void slow_rows(const ChunkParams& p, uint32_t far, uint3
       else
         *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + out * PKC_HEAD_DIM + 4 * lane) =
             make_uint2(Elem<T>::from_f2(o[r][0], o[r][1]), Elem<T>::from_f2(o[r][2], o[r][3]));
-      if (lane == 0) {
+      if (lane == 8 * r) {
         if (slot >= 0) p.part_lse[slot * kRows + row[r]] = lse2;
         else p.lse[out] = lse2 * kLn2;
       }

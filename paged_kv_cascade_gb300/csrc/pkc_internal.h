@@ -15,7 +15,7 @@
 // words 18-19 the mx4 append's count of finished blocks and its flag for a
 // missing page, words 20-21 the same of the eviction's compact, word 22 a flag
 // between assign_pages' launches, word 32 the result of
-// pkc_selftest_wait_timeout, words 40-49 the chunk attention's bits for partial
+// pkc_selftest_wait_timeout, words 40-50 the chunk attention's bits for partial
 // states that are there.
 #define PKC_STATUS_BYTES 256
 #define PKC_APPEND_COUNTER 18

@@ -656,8 +656,23 @@ def _c_int(name, x):
     return x
 
 
+# The calls of a step pass their tensors through one expression: all as they
+# should be, or _expect says what is not (a check after another costs 2 us more
+# of a call's 16).
+
 def _check_pages(block_table, cache_seqlens, free_pages, num_pages, workspace):
     torch = _torch or _t()
+    try:
+        B, n_pages = block_table.shape
+        i32, at = torch.int32, block_table.get_device()
+        if (at >= 0 and at == _get_device() and num_pages >= 0 and type(num_pages) is int
+                and block_table.dtype is i32 and cache_seqlens.dtype is i32 and free_pages.dtype is i32 and workspace.dtype is torch.uint8
+                and cache_seqlens.shape == (B,) and free_pages.shape == ((num_pages + 31) // 32,) and workspace.dim() == 1
+                and block_table.is_contiguous() and cache_seqlens.is_contiguous() and free_pages.is_contiguous() and workspace.is_contiguous()
+                and cache_seqlens.get_device() == at and free_pages.get_device() == at and workspace.get_device() == at):
+            return B, n_pages, num_pages, block_table.device
+    except (AttributeError, TypeError, ValueError):
+        pass
     B, n_pages = _leading("block_table", block_table, (torch.int32,), 2)
     dev = block_table.device
     num_pages = int(num_pages)
@@ -761,22 +776,44 @@ def rope_append_kv(q, k_new, v_new, positions, slots, inv_freq, k_cache, v_cache
     paged pools (of q's dtype, or uint8 e4m3 codes with scales) and return the
     turned q (dense).  q, k_new and v_new may be slices of one projection."""
     torch = _torch or _t()
-    P, ps, Hkv, _ = _leading("k_cache", k_cache, (torch.float16, torch.bfloat16, torch.uint8), 4, 128)
+    try:
+        pool, (T, Hq, D), (half,) = k_cache.shape, q.shape, inv_freq.shape
+        P, ps, Hkv, row = pool
+        rows, dtype, kv_dtype, at = (T, Hkv, 128), q.dtype, k_cache.dtype, k_cache.get_device()
+        (q_stride, q_head, q_one), kv_strides = q.stride(), k_new.stride()
+        kv_stride, kv_head, kv_one = kv_strides
+        plain = (at >= 0 and at == _get_device() and T > 1 and D == 128 and row == 128
+                 and (dtype is torch.float16 or dtype is torch.bfloat16) and (kv_dtype is dtype or kv_dtype is torch.uint8)
+                 and k_new.dtype is dtype and v_new.dtype is dtype and v_cache.dtype is kv_dtype and positions.dtype is torch.int32
+                 and slots.dtype is torch.int64 and inv_freq.dtype is torch.float64 and workspace.dtype is torch.uint8
+                 and k_new.shape == rows and v_new.shape == rows and v_cache.shape == pool and positions.shape == (T,)
+                 and slots.shape == (T,) and workspace.dim() == 1
+                 and q_head == 128 and q_one == 1 and kv_head == 128 and kv_one == 1 and v_new.stride() == kv_strides
+                 and k_cache.is_contiguous() and v_cache.is_contiguous() and positions.is_contiguous() and slots.is_contiguous()
+                 and inv_freq.is_contiguous() and workspace.is_contiguous()
+                 and q.get_device() == at and k_new.get_device() == at and v_new.get_device() == at and v_cache.get_device() == at
+                 and positions.get_device() == at and slots.get_device() == at and inv_freq.get_device() == at
+                 and workspace.get_device() == at)
+    except (AttributeError, TypeError, ValueError):
+        plain = False
+    if not plain:
+        P, ps, Hkv, _ = _leading("k_cache", k_cache, (torch.float16, torch.bfloat16, torch.uint8), 4, 128)
+        dev = k_cache.device
+        T, Hq, _ = _sizes(q, 3)
+        if T is None or q.dtype not in (torch.float16, torch.bfloat16):
+            _expect("q", q, (torch.float16, torch.bfloat16), (None, None, 128), dev)
+        dtype = q.dtype
+        q_stride = _expect_rows("q", q, dtype, (T, Hq, 128), dev)
+        kv_stride = _expect_rows("k_new", k_new, dtype, (T, Hkv, 128), dev)
+        if _expect_rows("v_new", v_new, dtype, (T, Hkv, 128), dev) != kv_stride:
+            raise ValueError("k_new and v_new must have the same strides")
+        kv_dtype = torch.uint8 if k_cache.dtype == torch.uint8 else dtype
+        half = _sizes(inv_freq, 1)[0]
+        _expect_all(dev, ("k_cache", k_cache, kv_dtype, (P, ps, Hkv, 128)), ("v_cache", v_cache, kv_dtype, (P, ps, Hkv, 128)),
+                    ("positions", positions, torch.int32, (T,)), ("slots", slots, torch.int64, (T,)),
+                    ("inv_freq", inv_freq, torch.float64, (half,)),
+                    ("workspace", workspace, torch.uint8, _sizes(workspace, 1)))
     dev = k_cache.device
-    T, Hq, _ = _sizes(q, 3)
-    if T is None or q.dtype not in (torch.float16, torch.bfloat16):
-        _expect("q", q, (torch.float16, torch.bfloat16), (None, None, 128), dev)
-    dtype = q.dtype
-    q_stride = _expect_rows("q", q, dtype, (T, Hq, 128), dev)
-    kv_stride = _expect_rows("k_new", k_new, dtype, (T, Hkv, 128), dev)
-    if _expect_rows("v_new", v_new, dtype, (T, Hkv, 128), dev) != kv_stride:
-        raise ValueError("k_new and v_new must have the same strides")
-    kv_dtype = torch.uint8 if k_cache.dtype == torch.uint8 else dtype
-    half = _sizes(inv_freq, 1)[0]
-    _expect_all(dev, ("k_cache", k_cache, kv_dtype, (P, ps, Hkv, 128)), ("v_cache", v_cache, kv_dtype, (P, ps, Hkv, 128)),
-                ("positions", positions, torch.int32, (T,)), ("slots", slots, torch.int64, (T,)),
-                ("inv_freq", inv_freq, torch.float64, (half,)),
-                ("workspace", workspace, torch.uint8, _sizes(workspace, 1)))
     if q_out is None:
         q_out = torch.empty((T, Hq, 128), dtype=dtype, device=dev)
     else:
@@ -807,15 +844,31 @@ def paged_chunk_state(q, q_indptr, k_cache, v_cache, block_table, cache_seqlens,
     `window` of them (0: no limit).  o has q's dtype, or float32 (out_dtype)
     for states merged further."""
     torch = _torch or _t()
-    P, ps, Hkv, _ = _leading("k_cache", k_cache, (torch.float16, torch.bfloat16), 4, 128)
-    dev, dtype = k_cache.device, k_cache.dtype
-    T, Hq, _ = _sizes(q, 3)
-    B, stride = _sizes(block_table, 2)
-    _expect_all(dev, ("q", q, dtype, (T, Hq, 128)), ("k_cache", k_cache, dtype, (P, ps, Hkv, 128)),
-                ("v_cache", v_cache, dtype, (P, ps, Hkv, 128)), ("block_table", block_table, torch.int32, (B, stride)),
-                ("q_indptr", q_indptr, torch.int32, (None if B is None else B + 1,)),
-                ("cache_seqlens", cache_seqlens, torch.int32, (B,)),
-                ("workspace", workspace, torch.uint8, _sizes(workspace, 1)))
+    try:
+        pool, (T, Hq, D), (B, stride) = k_cache.shape, q.shape, block_table.shape
+        P, ps, Hkv, row = pool
+        dtype, i32, at = k_cache.dtype, torch.int32, k_cache.get_device()
+        plain = (at >= 0 and at == _get_device() and D == 128 and row == 128
+                 and (dtype is torch.float16 or dtype is torch.bfloat16) and q.dtype is dtype and v_cache.dtype is dtype
+                 and block_table.dtype is i32 and q_indptr.dtype is i32 and cache_seqlens.dtype is i32 and workspace.dtype is torch.uint8
+                 and v_cache.shape == pool and q_indptr.shape == (B + 1,) and cache_seqlens.shape == (B,) and workspace.dim() == 1
+                 and q.is_contiguous() and k_cache.is_contiguous() and v_cache.is_contiguous() and block_table.is_contiguous()
+                 and q_indptr.is_contiguous() and cache_seqlens.is_contiguous() and workspace.is_contiguous()
+                 and q.get_device() == at and v_cache.get_device() == at and block_table.get_device() == at
+                 and q_indptr.get_device() == at and cache_seqlens.get_device() == at and workspace.get_device() == at)
+    except (AttributeError, TypeError, ValueError):
+        plain = False
+    if not plain:
+        P, ps, Hkv, _ = _leading("k_cache", k_cache, (torch.float16, torch.bfloat16), 4, 128)
+        dtype = k_cache.dtype
+        T, Hq, _ = _sizes(q, 3)
+        B, stride = _sizes(block_table, 2)
+        _expect_all(k_cache.device, ("q", q, dtype, (T, Hq, 128)), ("k_cache", k_cache, dtype, (P, ps, Hkv, 128)),
+                    ("v_cache", v_cache, dtype, (P, ps, Hkv, 128)), ("block_table", block_table, torch.int32, (B, stride)),
+                    ("q_indptr", q_indptr, torch.int32, (None if B is None else B + 1,)),
+                    ("cache_seqlens", cache_seqlens, torch.int32, (B,)),
+                    ("workspace", workspace, torch.uint8, _sizes(workspace, 1)))
+    dev = k_cache.device
     if out_dtype is None:
         out_dtype = dtype if o is None else o.dtype
     if out_dtype is not dtype and out_dtype is not torch.float32:

@@ -109,15 +109,12 @@ __global__ void __launch_bounds__(kThreads, 1) assign_pages_kernel(const PagesPa
   const int n_blocks = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int tid = threadIdx.x, lane = tid & 31;
   const bool first_block = rank == 0;
+  // (A cluster's barrier releases and acquires what its blocks wrote before it.)
   auto sync_all = [&] {
-    if (n_blocks > 1) {
-      __threadfence();
-      cluster.sync();
-    } else {
-      __syncthreads();
-    }
+    if (n_blocks > 1) cluster.sync();
+    else __syncthreads();
   };
-  grid_launch_dependents();
+  if (!kAll) grid_launch_dependents();  // places_kernel
   const int64_t words = (p.num_pages + 31) / 32;
   const int chunks = (int)((words + kThreads - 1) / kThreads);
   const uint32_t first_word = free_word(p, tid, words);  // on its way while the lengths are scanned

@@ -16,7 +16,9 @@
 // first one runs and finds what it needs of a request at its first token.  Both calls
 // for 220,453 tokens of 300 requests: 60.7 us with one launch, 31.9 with the second,
 // 26.4 with the requests of a block's tokens found while the first one runs, 32-bit
-// divisions and a released row's entries loaded together; 64 single tokens: 10.0 us.
+// divisions and a released row's entries loaded together, 19.8 with eight threads to a
+// word of the map (a thread gave out up to 32 pages, one after another: 9 us of the
+// launch's 17); 64 single tokens: 9.5 us.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -116,8 +118,12 @@ __global__ void __launch_bounds__(kThreads, 1) assign_pages_kernel(const PagesPa
   };
   if (!kAll) grid_launch_dependents();  // places_kernel
   const int64_t words = (p.num_pages + 31) / 32;
-  const int chunks = (int)((words + kThreads - 1) / kThreads);
-  const uint32_t first_word = free_word(p, tid, words);  // on its way while the lengths are scanned
+  const int per_chunk = kThreads / p.split, chunks = (int)((words + per_chunk - 1) / per_chunk);
+  // On their way while the lengths are scanned: the first word to count and the first
+  // one of the block's own chunks, where `split` threads share a word's bits.
+  const uint32_t bits = p.split == 1 ? ~0u : 15u << 4 * (tid & 7);
+  const uint32_t first_word = free_word(p, tid, words);
+  const uint32_t own_word = free_word(p, (int64_t)rank * per_chunk + tid / p.split, words);
 
   // The ranges have to run upwards within 0 .. total, or nobody is served.
   bool wrong = false;
@@ -157,12 +163,12 @@ __global__ void __launch_bounds__(kThreads, 1) assign_pages_kernel(const PagesPa
   }
   if (tid == 0) off[p.batch] = needed;
 
-  // Free pages before each chunk of kThreads words.
+  // Free pages before each chunk of words (a warp's 32 words lie in one).
   if (needed > 0) {  // uniform
-    for (int c = 0; c < chunks; ++c) {
-      const uint32_t x = c == 0 ? first_word : free_word(p, (int64_t)c * kThreads + tid, words);
+    for (int64_t w0 = 0; w0 < words; w0 += kThreads) {
+      const uint32_t x = w0 == 0 ? first_word : free_word(p, w0 + tid, words);
       const int n = __reduce_add_sync(0xffffffffu, __popc(x));
-      if (lane == 0) atomicAdd(chunk_base + c, n);
+      if (lane == 0 && n) atomicAdd(chunk_base + (int)((w0 + tid) / per_chunk), n);
     }
     __syncthreads();
     if (tid < 32) {  // exclusive, in place
@@ -195,8 +201,8 @@ __global__ void __launch_bounds__(kThreads, 1) assign_pages_kernel(const PagesPa
   // The taken pages to the table, their bits cleared.
   for (int c = rank; c < chunks && taken > 0; c += n_blocks) {
     if (chunk_base[c] >= taken) break;  // uniform
-    const int64_t w = (int64_t)c * kThreads + tid;
-    const uint32_t x = c == 0 ? first_word : free_word(p, w, words);
+    const int64_t w = (int64_t)c * per_chunk + tid / p.split;
+    const uint32_t x = (c == rank ? own_word : free_word(p, w, words)) & bits;
     int total;
     int r = chunk_base[c] + block_scan(__popc(x), sums, total);
     uint32_t gone = 0;
@@ -209,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) assign_pages_kernel(const PagesPa
         p.block_table[(int64_t)b * p.bt_stride + have + (r - off[b])] = (int)(32 * w) + bit;
         gone |= 1u << bit;
       }
-      p.free_pages[w] &= ~gone;
+      atomicAnd(p.free_pages + w, ~gone);
     }
   }
   sync_all();  // the table is complete
@@ -369,15 +375,17 @@ static int launch_assign(const PagesParams& p, int blocks, int smem, void* strea
 int launch_assign_pages(const PagesParams& p, void* stream) {
   if (p.batch <= 0 && p.total <= 0) return 0;
   const int64_t words = (p.num_pages + 31) / 32;
-  const int chunks = (int)((words + kThreads - 1) / kThreads);
+  PagesParams q = p;
+  q.split = words <= 65536 ? 8 : 1;  // (the chunks' counts have to fit in shared memory)
+  const int chunks = (int)((words + kThreads / q.split - 1) / (kThreads / q.split));
   const int smem = 4 * (3 * p.batch + 2 + chunks + 1);
   const bool all = p.total <= kFewTokens;
-  // a block per 4096 tokens or per chunk of the map, whichever are more
-  const int64_t parts = std::max<int64_t>(all ? ((int64_t)p.total + 4095) / 4096 : 1, chunks);
+  // a block per 4096 tokens or per kThreads words of the map, whichever are more
+  const int64_t parts = std::max<int64_t>(all ? ((int64_t)p.total + 4095) / 4096 : 1, (words + kThreads - 1) / kThreads);
   int blocks = 1;
   while (blocks < kMaxCluster && blocks < parts) blocks *= 2;
-  if (all) return launch_assign<true>(p, blocks, smem, stream);
-  if (const int e = launch_assign<false>(p, blocks, smem, stream)) return e;
+  if (all) return launch_assign<true>(q, blocks, smem, stream);
+  if (const int e = launch_assign<false>(q, blocks, smem, stream)) return e;
   const int per = kPlaceThreads * kPlaceTokens;
   return launch_programmatic(places_kernel, dim3((unsigned)(((int64_t)p.total + per - 1) / per)), dim3(kPlaceThreads), 0,
                              (cudaStream_t)stream, p);

@@ -328,6 +328,7 @@ struct PagesParams {
   int32_t* seqlens_out;      // [batch] or nullptr; may be cache_seqlens
   int64_t bt_stride, num_pages;
   int batch, page_size, total;
+  int split;                 // assign: set by the launcher, threads that share a word of free_pages
   int32_t* status;
 };
 

@@ -215,3 +215,38 @@ def test_graph_and_another_stream():
     ref.release(run.table, lens, run.free, 16)
     ref.assign(run.table, lens, indptr.tolist(), 660, run.free, 16)
     run.check(0)
+
+
+@pytest.mark.parametrize("batch,most_new", [(50, 1500), (16384, 3)])
+@pytest.mark.parametrize("num_pages", [40_001, 2 ** 21, 2 ** 21 + 1, 2 ** 26])
+def test_free_pages_far_apart(num_pages, batch, most_new):
+    """Few free pages, some side by side, in pools up to the largest; the largest batch."""
+    rng = np.random.default_rng(num_pages % 1000 + batch)
+    free = set(rng.integers(0, num_pages, 6000).tolist()) | {0, num_pages - 1} | set(range(9000, 9700))
+    page, new = 16, rng.integers(0, most_new + 1, batch).tolist()
+    stride = 4 + -(-most_new // page)
+    lens, table, held = [], [], num_pages // 2
+    for _ in range(batch):
+        n = int(rng.integers(0, 4 * page))
+        row = []
+        while len(row) < -(-n // page):  # any pages that are not free
+            held = (held + 1) % num_pages
+            if held not in free:
+                row.append(held)
+        lens.append(n)
+        table.append(row + [-1] * (stride - len(row)))
+    indptr = np.concatenate(([0], np.cumsum(new))).tolist()
+    d_table, d_lens, d_free = torch.tensor(table, dtype=I32, device="cuda"), torch.tensor(lens, dtype=I32, device="cuda"), ref.pool_words(free, num_pages).cuda()
+    ws = workspace()
+    for _ in range(2):
+        got = pkc.assign_pages(d_table, d_lens, torch.tensor(indptr, dtype=I32, device="cuda"), indptr[-1], d_free, page, num_pages, ws, seqlens_out=d_lens)
+        slots, pos, lens, status = ref.assign(table, lens, indptr, indptr[-1], free, page)
+        assert got[0].tolist() == slots and got[1].tolist() == pos and got[2].tolist() == lens
+        assert d_table.tolist() == table and torch.equal(d_free.cpu(), ref.pool_words(free, num_pages))
+        assert pkc.device_status(ws) == status
+        pkc.workspace_init(ws)
+    d_lens.zero_()
+    pkc.release_pages(d_table, d_lens, d_free, page, num_pages, ws)
+    ref.release(table, [0] * batch, free, page)
+    want = ref.pool_words(free, num_pages)
+    assert torch.equal(d_free.cpu(), want) and (d_table == -1).all()

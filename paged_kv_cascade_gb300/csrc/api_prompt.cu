@@ -34,6 +34,11 @@ int check_free(const char* call, int batch, int64_t num_pages) {
   return PKC_OK;
 }
 
+bool power_of_two(float x) {
+  int e;
+  return std::frexp(x, &e) == 0.5f;
+}
+
 }  // namespace
 
 extern "C" {
@@ -111,7 +116,7 @@ int pkc_rope_append_kv(const void* q, int64_t q_stride, const void* k_new, const
   if (kv_dtype != dtype && kv_dtype != PKC_E4M3)
     return set_error(PKC_ERR_INVALID_ARG, "rope_append_kv: kv_dtype must be dtype or PKC_E4M3 (got %d)", kv_dtype);
   if (!std::isfinite(amplitude)) return set_error(PKC_ERR_INVALID_ARG, "rope_append_kv: amplitude must be finite");
-  // the kernel multiplies by the reciprocals: they have to be normal numbers
+  // (the reciprocal of a power of two has to be a normal number)
   if (!(k_scale >= 0x1p-100f && k_scale <= 0x1p100f && v_scale >= 0x1p-100f && v_scale <= 0x1p100f) ||
       (kv_dtype != PKC_E4M3 && (k_scale != 1.f || v_scale != 1.f)))
     return set_error(PKC_ERR_INVALID_ARG,
@@ -134,7 +139,9 @@ int pkc_rope_append_kv(const void* q, int64_t q_stride, const void* k_new, const
   p.positions = positions; p.slots = slots; p.inv_freq = inv_freq;
   p.q_out = q_out; p.k_cache = k_cache; p.v_cache = v_cache; p.pool_tokens = num_pages * page_size;
   p.rotary_dim = rotary_dim; p.interleaved = interleaved; p.total = total; p.hq = num_qo_heads; p.hkv = num_kv_heads;
-  p.amplitude = amplitude; p.k_inv_scale = 1.f / k_scale; p.v_inv_scale = 1.f / v_scale;
+  p.amplitude = amplitude; p.k_scale = k_scale; p.v_scale = v_scale;
+  p.k_inv_scale = 1.f / k_scale; p.v_inv_scale = 1.f / v_scale;
+  p.divide = !(power_of_two(k_scale) && power_of_two(v_scale));
   p.status = static_cast<int32_t*>(workspace);
   const int e = launch_rope_append(p, dtype, kv_dtype, stream);
   return e ? cuda_error(e, "rope_append_kv launch") : PKC_OK;

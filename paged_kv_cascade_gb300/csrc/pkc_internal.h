@@ -346,7 +346,9 @@ struct RopeParams {
   void* v_cache;
   int64_t pool_tokens;
   int rotary_dim, interleaved, total, hq, hkv;
-  float amplitude, k_inv_scale, v_inv_scale;
+  float amplitude, k_scale, v_scale;
+  float k_inv_scale, v_inv_scale;
+  int divide;                // 0: both scales are powers of two, so their reciprocals are exact
   int32_t* status;
 };
 

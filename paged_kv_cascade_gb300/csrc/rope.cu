@@ -128,14 +128,23 @@ __global__ void __launch_bounds__(kThreads) rope_append_kernel(const RopeParams 
           }
         }
         if (kE4m3 && r >= p.hq) {
-          const float m = is_v ? p.v_inv_scale : p.k_inv_scale;
+          // The quotient by the scale, rounded as a quotient: a product with a rounded
+          // reciprocal is off by its last bit where that decides between two codes.  The
+          // reciprocal of a power of two is exact, and saves a fifth (22.3 us, 28.6 with
+          // divisions, for the case above; 32.2 where powers of two are divided by too).
+          const float m = is_v ? p.v_scale : p.k_scale, inv = is_v ? p.v_inv_scale : p.k_inv_scale;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            x[i] = p.divide ? __fdiv_rn(x[i], m) : x[i] * inv;
+            y[i] = p.divide ? __fdiv_rn(y[i], m) : y[i] * inv;
+          }
           uint8_t* dst = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) +
                          (slot * p.hkv + (r - p.hq - (is_v ? p.hkv : 0))) * PKC_HEAD_DIM;
           uint32_t w[4];
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            w[i] = e4m3x2(x[4 * i] * m, x[4 * i + 1] * m) | e4m3x2(x[4 * i + 2] * m, x[4 * i + 3] * m) << 16;
-            w[2 + i] = e4m3x2(y[4 * i] * m, y[4 * i + 1] * m) | e4m3x2(y[4 * i + 2] * m, y[4 * i + 3] * m) << 16;
+            w[i] = e4m3x2(x[4 * i], x[4 * i + 1]) | e4m3x2(x[4 * i + 2], x[4 * i + 3]) << 16;
+            w[2 + i] = e4m3x2(y[4 * i], y[4 * i + 1]) | e4m3x2(y[4 * i + 2], y[4 * i + 3]) << 16;
           }
           *reinterpret_cast<uint2*>(dst + e0) = make_uint2(w[0], w[1]);
           *reinterpret_cast<uint2*>(dst + e1) = make_uint2(w[2], w[3]);

@@ -180,3 +180,25 @@ def test_refuses():
         pkc.rope_append_kv(c.q, c.k, c.v, pos, slots, f, *c.pools, c.ws, k_scale=2.0)
     with pytest.raises(ValueError, match="shape"):
         pkc.rope_append_kv(c.q, c.k, c.v, pos[:5], slots, f, *c.pools, c.ws)
+
+
+def nearest_codes(x):
+    """The e4m3 values nearest to float64 x, ties to the even code, at most 448."""
+    a = x.abs().clamp(max=448.0)
+    step = torch.pow(2.0, torch.floor(torch.log2(a.clamp(min=2.0 ** -6))) - 3)
+    return torch.copysign(torch.round(a / step) * step, x)
+
+
+@pytest.mark.parametrize("dtype,scale", [(BF16, 224.0), (F16, 1632.0), (F16, 1312.0), (BF16, 0.25), (F16, 0.0371), (BF16, 3.3e-4), (F16, 2.0 ** -100)])
+def test_codes_of_the_quotient(dtype, scale):
+    """Every 16-bit value over the scale, as value and as the part of a key that is not turned: the code nearest to
+    the float32 quotient.  350 / 224 lies between two codes, and so do other values that a rounded reciprocal moves."""
+    scale = float(np.float32(scale))
+    x = torch.arange(65536, dtype=torch.int32).to(torch.uint16).view(dtype).reshape(512, 1, 128)
+    c = Case(512, 1, 1, dtype, "e4m3", rot=16, seed=6)
+    c.k, c.v, c.k_scale, c.v_scale = x.cuda(), x.cuda(), scale, scale
+    c.run(False)
+    want = nearest_codes((x.float() / torch.tensor(scale)).double())
+    for pool, cols in zip(c.pools, (slice(16, 128), slice(0, 128))):
+        got = e4m3_values()[pool.cpu().reshape(-1, 1, 128)[c.slots].long()]
+        assert torch.equal(got[..., cols].nan_to_num(nan=1000.0), want[..., cols].nan_to_num(nan=1000.0))

@@ -810,7 +810,9 @@ int pkc_chunk_workspace_size(size_t* bytes);
  *            state that is merged further (pkc_merge_states_to), not in the
  *            place of q; lse [total_q, num_qo_heads] float32, natural log
  * A token that a row does not attend to has no influence on it, whatever its
- * key and value hold.  Probabilities enter the V product in dtype.  Rows whose
+ * key and value hold.  Probabilities enter the V product in dtype (F16: those
+ * below 2^-31 of a row's largest drop out of O, 2^-11 of it at most for 2^20
+ * tokens; LSE counts them).  Rows whose
  * largest scaled score passes 2^26 / log2(e) in magnitude (BF16: 2^30 / log2(e)),
  * and rows next to a value that is not finite and not theirs, are computed a key
  * at a time: right, at up to 100 ns a key, and ended by PKC_ERR_TIMEOUT where that

@@ -18,11 +18,11 @@
 // is its softmax, the MMAs run beside it.  (With an S per half and P in its
 // columns, Q K of tile j + 1 waited for P V of tile j: 3650 cycles a tile.)  P never
 // passes through shared memory, whose bandwidth the MMA's operands need.
-// m_ref, a row's reference maximum, is that of its first tile.  It moves (and the
-// row of O is rescaled, in TMEM) only when a tile's P would sum to more than 2^13:
-// P is formed at once, and again where the sum says so, so the other tiles need
-// no maximum at all (64 instructions and a chain ahead of the exponentials).  P
-// stays far below fp16's largest number, and a row's sum is at least 1.
+// m_ref, a row's reference, is its first tile's maximum (fp16: less kLift).  It moves
+// (and the row of O is rescaled, in TMEM) only when a tile's P would sum to more than
+// kMoveSum: P is formed at once, and again where the sum says so, so the other tiles
+// need no maximum at all (64 instructions and a chain ahead of the exponentials).  P
+// stays within fp16's largest number, and a row's sum is at least about 1.
 //
 // Work split.  An item costs its KV tiles and kOver; all items are laid end to
 // end (request, KV head, row tile) and cut evenly over the blocks, one per SM.
@@ -99,11 +99,19 @@ constexpr int kMinCost = 16;             // least cost of a block: a short item 
 // (prompts 533 us with 16, 523 with 12 and 4; a window's items of 11 tiles 162 with
 // 12, 171 with 8).
 constexpr int kShort = 12;
-constexpr float kMoveSum = 8192.f;       // a tile's sum of P above which its reference maximum moves
+// A row's reference is its maximum less kLift: fp16 has no P below 2^-25, and what it
+// drops from O stays in the sum.  With the lift a weight is lost below 2^-31 of the
+// largest, so 2^20 of them are at most half a step of fp16.  bf16 has the exponents.
+// (fp16, 5 / 6 / 8 / 10 powers of two against none: prompts 533 / 543 / 543 / 586 us
+// against 531, window 173 / 173 / 177 / 193 against 170, mixed 150 / 151 / 152 / 205
+// against 150: with more, the reference moves more often.)
+template <typename T> constexpr float kLift = std::is_same<T, __half>::value ? 6.f : 0.f;
+// A tile's sum of P above which its reference moves (no P is above its sum).
+template <typename T> constexpr float kMoveSum = std::is_same<T, __half>::value ? 65504.f : 8192.f;
 
-// P = exp2(s c - m_ref) in one rounding: m_ref = max s c is rounded, P's largest is
-// exp2 of that rounding, at most 2^(m_ref / 2^24).  Rows with |m_ref| from here on are
-// computed again with the product rounded too (slow_rows).
+// P = exp2(s c - m_ref) in one rounding: m_ref = max s c - kLift is rounded, P's largest
+// is exp2 of that rounding, at most 2^(m_ref / 2^24), and of the lift.  Rows with |m_ref|
+// from here on are computed again with the product rounded too (slow_rows).
 // Below, that factor is at most 2^4 in fp16 and 2^64 in bf16, which their P hold.
 template <typename T> constexpr float kFar = std::is_same<T, __half>::value ? 0x1p26f : 0x1p30f;
 
@@ -960,7 +968,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 32; i += 2)
 #pragma unroll
               for (int j = 0; j < 4; ++j) mx[j] = max3(mx[j], __uint_as_float(v[j][i]), __uint_as_float(v[j][i + 1]));
-            const float now = fmaxf(m_ref, fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2);
+            const float now = fmaxf(m_ref, __fmaf_rn(fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]), p.scale_log2, -kLift<T>));
             const float f = m_ref == neg_inf() ? 0.f : ex2(m_ref - now);
             const uint64_t f2 = pk2(f, f);
             l2a = fmul2(l2a, f2);
@@ -999,7 +1007,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           const float2 s2 = upk2(fadd2(sa, sb));
           // (Not twice for a tile: rows that are still above are far out, kFar.)
-          move = !move && __any_sync(0xffffffffu, s2.x + s2.y > kMoveSum);
+          move = !move && __any_sync(0xffffffffu, s2.x + s2.y > kMoveSum<T>);
           if (!move) {
             l2a = fadd2(l2a, sa);
             l2b = fadd2(l2b, sb);

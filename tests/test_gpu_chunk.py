@@ -326,3 +326,31 @@ def test_refuses():
         pkc.paged_chunk_state(q, ip, k, v, t, lens, -0.1, c.ws)
     with pytest.raises(pkc.PkcError):
         pkc.paged_chunk_state(q, ip, k, v, t, lens, 0.1, c.ws, window=-1)
+
+
+@pytest.mark.parametrize("below", [12.0, 20.0, 25.5, 28.0])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_many_small_weights_beside_a_large_one(dtype, below):
+    """The first token holds the attention, 1500 others lie so many powers of two below it, and only they have a value.
+
+    Each weight is half a step of its type off, and in fp16, where the largest stands for 2^6 or more and the smallest
+    step is 2^-24, at most 2^-31 of the largest.  The scores are float32 products of one term: 2^-22 of the exponent,
+    and as much again for the exponential; the sum and the quotient 2^-19.  LSE, up to 29 in powers of two: 2^-23 of
+    it for the scale times log2(e), and half a step each, 2^-20, for the sum with the logarithm, the factor and the
+    product."""
+    c = Case([(1, 1500)], 1, 1, dtype, seed=21, scale=1.0)
+    c.q[:] = 0
+    c.q[..., 0] = 1.0
+    key = torch.tensor(below * math.log(2)).to(dtype)
+    for x, first, other in ((c.k, key, 0.0), (c.v, 0.0, 1.0)):
+        page, rest = int(c.table[0, 0]), ~x.isnan()
+        x[rest] = other
+        x[page, 0, 0, :] = first
+    c.k[..., 1:] = 0
+    o, lse = c.run(out_dtype=torch.float32)
+    assert pkc.device_status(c.ws) == 0
+    w = math.exp(-float(key))
+    want = 1500 * w / (1 + 1500 * w)
+    tol = (ref.HALF_STEP[dtype] + 2.0 ** -17) * want + (1500 * 2.0 ** -31 if dtype == F16 else 0)
+    assert float((o.double().cpu() - want).abs().max()) <= tol
+    assert float((lse.double().cpu() - math.log(math.exp(float(key)) + 1500)).abs().max()) <= 2.0 ** -17

@@ -509,12 +509,12 @@ __device__ __forceinline__ void merge_item(const ChunkParams& p, const Item& it,
       }
     }
     if (row < rows) {
-      const float inv = m == neg_inf() ? 0.f : 1.f / l;
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // (not m: that of a row whose scores are NaN is -inf too)
 #pragma unroll
       for (int i = 0; i < 32; ++i) o[i] *= inv;
       const int64_t out = out_row(p, it.q_row, it.kvh, row);
       store_out<T>(p, out, 4 * chunk, o);
-      if (chunk == 0) p.lse[out] = m == neg_inf() ? neg_inf() : (m + lg2(l)) * kLn2;
+      if (chunk == 0) p.lse[out] = l == 0.f ? neg_inf() : (m + lg2(l)) * kLn2;
     }
   }
 }

@@ -354,3 +354,16 @@ def test_many_small_weights_beside_a_large_one(dtype, below):
     tol = (ref.HALF_STEP[dtype] + 2.0 ** -17) * want + (1500 * 2.0 ** -31 if dtype == F16 else 0)
     assert float((o.double().cpu() - want).abs().max()) <= tol
     assert float((lse.double().cpu() - math.log(math.exp(float(key)) + 1500)).abs().max()) <= 2.0 ** -17
+
+
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (8, 1)])
+def test_a_query_that_is_not_a_number(hq, hkv):
+    """Its states are NaN, LSE too, whether its item is cut or not; the other rows are whole."""
+    for reqs in ([(3, 6000)], [(3, 600)]):
+        c = Case(reqs, hq, hkv, BF16, seed=22)
+        want = c.reference()
+        c.q[1, :, 7] = math.nan
+        o, lse = c.run()
+        assert pkc.device_status(c.ws) == 0
+        assert o[1].isnan().all() and lse[1].isnan().all()
+        ref.check_chunk(o, lse, want, BF16, [0, 2])

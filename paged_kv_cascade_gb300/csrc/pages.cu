@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(kPlaceThreads) places_kernel(const PagesParams
   const int64_t block_t0 = (int64_t)blockIdx.x * kBlockTokens;
   int n[2] = {0, 0};
   for (int b = threadIdx.x; b <= p.batch; b += kPlaceThreads) {
-    const int at = p.indptr[b];
+    const int at = p.batch ? p.indptr[b] : 0;
     n[0] += at <= block_t0;
     n[1] += at < block_t0 + kBlockTokens;
   }
@@ -374,8 +374,9 @@ static int launch_assign(const PagesParams& p, int blocks, int smem, void* strea
 
 int launch_assign_pages(const PagesParams& p, void* stream) {
   if (p.batch <= 0 && p.total <= 0) return 0;
-  const int64_t words = (p.num_pages + 31) / 32;
   PagesParams q = p;
+  if (q.batch == 0) q.num_pages = 0;  // rows of no request alone: neither ranges nor map are read (they may be NULL)
+  const int64_t words = (q.num_pages + 31) / 32;
   q.split = words <= 65536 ? 8 : 1;  // (the chunks' counts have to fit in shared memory)
   const int chunks = (int)((words + kThreads / q.split - 1) / (kThreads / q.split));
   const int smem = 4 * (3 * p.batch + 2 + chunks + 1);

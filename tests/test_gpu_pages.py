@@ -250,3 +250,14 @@ def test_free_pages_far_apart(num_pages, batch, most_new):
     ref.release(table, [0] * batch, free, page)
     want = ref.pool_words(free, num_pages)
     assert torch.equal(d_free.cpu(), want) and (d_table == -1).all()
+
+
+@pytest.mark.parametrize("total", [3, 8192, 9000])
+def test_no_requests_need_no_arrays(total):
+    """A batch of none: its arrays may be NULL, and every token is nobody's."""
+    slots, pos = torch.full((total,), 7, dtype=torch.int64, device="cuda"), torch.full((total,), 7, dtype=I32, device="cuda")
+    ws = workspace()
+    stream = torch.cuda.current_stream().cuda_stream
+    assert pkc.lib().pkc_assign_pages(None, 4, None, None, total, 0, 16, 1000, None, slots.data_ptr(), pos.data_ptr(), None, ws.data_ptr(),
+                                      ws.numel(), stream) == 0
+    assert (slots == -1).all() and (pos == 0).all() and pkc.device_status(ws) == 0

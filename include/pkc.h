@@ -767,7 +767,7 @@ int pkc_assign_pages(int32_t* block_table, int block_table_stride,
  *            2 i + 1) if interleaved is 1, (i, i + rotary_dim / 2) if 0:
  *            (x, y) -> amplitude (x cos a - y sin a, x sin a + y cos a)
  *   q_out    [total, num_qo_heads, 128] of dtype, dense; may be q if q is
- *            dense too
+ *            dense too, and overlaps q, k_new and v_new in no other way
  *   k_cache, v_cache [num_pages, page_size, num_kv_heads, 128] of kv_dtype:
  *            dtype itself (k_scale = v_scale = 1), or E4M3: the nearest codes
  *            of the turned key / k_scale and of the value / v_scale (ties to

@@ -39,6 +39,14 @@ bool power_of_two(float x) {
   return std::frexp(x, &e) == 0.5f;
 }
 
+// Whether n dense rows of o_row 16-bit elements from o on meet n rows of x_row elements,
+// `stride` apart, from x on.  (In elements: addresses are even, and sums stay below 2^64.)
+bool rows_meet(const void* o, const void* x, uint64_t o_row, uint64_t x_row, uint64_t stride, uint64_t n) {
+  const uint64_t o0 = reinterpret_cast<uintptr_t>(o) / 2, x0 = reinterpret_cast<uintptr_t>(x) / 2;
+  const uint64_t first = o0 < x0 + x_row ? 0 : (o0 - x0 - x_row) / stride + 1;  // the first row that ends behind o
+  return first < n && x0 + first * stride < o0 + n * o_row;
+}
+
 }  // namespace
 
 extern "C" {
@@ -133,6 +141,14 @@ int pkc_rope_append_kv(const void* q, int64_t q_stride, const void* k_new, const
       !aligned16(v_cache) || !aligned(slots, 8) || !aligned(inv_freq, 8) || !aligned(positions, 4))
     return set_error(PKC_ERR_INVALID_ARG,
                      "rope_append_kv: rows and pools must be 16-byte aligned, slots and inv_freq 8-byte");
+  // a row of q, k_new or v_new may be read after the rows of other tokens are written
+  const uint64_t q_row = (uint64_t)num_qo_heads * PKC_HEAD_DIM;
+  const bool in_place = q_out == q && (total == 1 || (uint64_t)q_stride == q_row);
+  if (!in_place && rows_meet(q_out, q, q_row, q_row, q_stride, total))
+    return set_error(PKC_ERR_INVALID_ARG, "rope_append_kv: q_out must not overlap q, but may be q if q is dense");
+  const uint64_t kv_row = (uint64_t)num_kv_heads * PKC_HEAD_DIM;
+  if (rows_meet(q_out, k_new, q_row, kv_row, kv_stride, total) || rows_meet(q_out, v_new, q_row, kv_row, kv_stride, total))
+    return set_error(PKC_ERR_INVALID_ARG, "rope_append_kv: q_out must not overlap k_new or v_new");
   RopeParams p;
   std::memset(&p, 0, sizeof(p));
   p.q = q; p.k_new = k_new; p.v_new = v_new; p.q_stride = q_stride; p.kv_stride = kv_stride;

@@ -202,3 +202,23 @@ def test_codes_of_the_quotient(dtype, scale):
     for pool, cols in zip(c.pools, (slice(16, 128), slice(0, 128))):
         got = e4m3_values()[pool.cpu().reshape(-1, 1, 128)[c.slots].long()]
         assert torch.equal(got[..., cols].nan_to_num(nan=1000.0), want[..., cols].nan_to_num(nan=1000.0))
+
+
+def test_outputs_beside_the_inputs():
+    """q_out right before and right behind the projection, between two tokens' rows, and on the only token's query."""
+    c = Case(9, 4, 2, BF16, "16", seed=9)
+    buf = torch.zeros(9 * (8 + 4 + 4) * 128, dtype=BF16, device="cuda")
+    rows = buf[9 * 4 * 128:9 * 12 * 128].view(9, 8, 128)
+    rows[:, :4], rows[:, 4:6], rows[:, 6:] = c.q, c.k, c.v
+    c.q, c.k, c.v = rows[:, :4], rows[:, 4:6], rows[:, 6:]
+    c.check(c.run(False, q_out=buf[:9 * 4 * 128].view(9, 4, 128)), False)
+    c.check(c.run(False, q_out=buf[9 * 12 * 128:].view(9, 4, 128)), False)
+    c = Case(2, 4, 2, BF16, "16", seed=10, gap=8)
+    gap = torch.as_strided(c.q, (2, 4, 128), (512, 128, 1), c.v.storage_offset() + 256)
+    c.check(c.run(True, q_out=gap), True)
+    c = Case(1, 4, 2, BF16, "16", seed=11)
+    c.check(c.run(True, q_out=c.q), True)
+    c = Case(2, 4, 2, BF16, "16", seed=11)
+    with pytest.raises(pkc.PkcError, match="overlap"):
+        pkc.rope_append_kv(c.q, c.k, c.v, c.positions.cuda(), c.slots.cuda(), c.freq.cuda(), *c.pools, c.ws,
+                           q_out=torch.as_strided(c.q, (2, 4, 128), (512, 128, 1)))

@@ -68,6 +68,26 @@ def test_rope_refuses(L):
     assert L.pkc_rope_append_kv(*good[:11], 0, *good[12:]) == 0
 
 
+def test_rope_refuses_outputs_on_its_inputs(L):
+    """5 tokens of 8 query heads (2 KB) and 2 KV heads (512 bytes), parts of one projection of 12 heads (3 KB) at
+    0x100000, or dense: q_out on q's rows, on q itself where they lie apart, on keys or values, by one element's worth."""
+    base = 0x100000
+    end = base + 4 * 3072  # the last token's row
+    apart = [(base, 1536, base + 2048, base + 2560, 1536)]
+    for q, qs, k, v, kvs in apart:
+        for out in (base, base + 16, base - 16, base + 3072, end + 2048 - 16, base - 5 * 2048 + 16,  # q
+                    base + 2048, base + 2560 + 512 - 16, end + 2048, end + 2560 + 512 - 16):  # k, v
+            args = [q, qs, k, v, kvs, 0x1000, 0x1000, 0x1000, 128, 0, 1.0, 5, 8, 2, 128, out, 0x800000, 0x900000, 16, 10, 1.0, 1.0, 1, 1,
+                    WS, 1 << 20, None]
+            args = [ctypes.c_void_p(a) if i in (0, 2, 3, 5, 6, 7, 15, 16, 17) else a for i, a in enumerate(args)]
+            assert L.pkc_rope_append_kv(*args) == 1 and b"overlap" in L.pkc_last_error(), hex(out)
+    for out in (base + 16, base - 16, base + 0x8000, base + 0x8000 - 5 * 2048 + 16, base + 0x8000 + 5 * 512 - 16, base + 0x10000 + 16):  # dense
+        args = [base, 1024, base + 0x8000, base + 0x10000, 256, 0x1000, 0x1000, 0x1000, 128, 0, 1.0, 5, 8, 2, 128, out, 0x800000, 0x900000, 16,
+                10, 1.0, 1.0, 1, 1, WS, 1 << 20, None]
+        args = [ctypes.c_void_p(a) if i in (0, 2, 3, 5, 6, 7, 15, 16, 17) else a for i, a in enumerate(args)]
+        assert L.pkc_rope_append_kv(*args) == 1 and b"overlap" in L.pkc_last_error(), hex(out)
+
+
 def test_chunk_refuses(L):
     need = pkc.chunk_workspace_size()
     assert need % 256 == 0 and L.pkc_chunk_workspace_size(None) == 1

@@ -1013,6 +1013,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             l2b = fadd2(l2b, sb);
             break;
           }
+          tmem_st_wait();  // P again, to the same columns: stores are ordered by this alone
         }
         tmem_st_wait();
         tc_fence_before();

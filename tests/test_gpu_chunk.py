@@ -367,3 +367,16 @@ def test_a_query_that_is_not_a_number(hq, hkv):
         assert pkc.device_status(c.ws) == 0
         assert o[1].isnan().all() and lse[1].isnan().all()
         ref.check_chunk(o, lse, want, BF16, [0, 2])
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_scores_that_rise_from_tile_to_tile(dtype):
+    """Each tile of 128 keys lies 2^23 to 2^29 above the one before: what is formed against the old reference is
+    infinite in fp16 and formed again."""
+    c = Case([(150, 700), (1, 1000), (260, 0)], 4, 1, dtype, seed=23, scale=1.0)
+    c.q *= 0.1
+    c.q[..., 0] = 1.0
+    for b, n in enumerate(c.lens):
+        for t in range(n):
+            c.k[c.table[b, t // 16], t % 16, :, 0] = 16.0 * (t // 128) + 4.0 * (t // 128 % 2)
+    c.check()

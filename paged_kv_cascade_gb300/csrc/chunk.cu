@@ -1076,6 +1076,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();  // O has been read out: the next P's arrival says so
       const bool far = mine && m_ref != neg_inf() && !(fabsf(m_ref) < kFar<T>);
       if (const uint32_t todo = __ballot_sync(0xffffffffu, (odd || far) && valid); todo) {
+        __syncwarp();  // the rows' stores by their own lanes come before those by all lanes
         const uint32_t f = __ballot_sync(0xffffffffu, far && valid);
         slow_rows<T>(p, f, todo & ~f, row0, it.b, it.kvh, it.q_row, it.pos0, it.len, lo, hi, lo_max, hi_min, cut ? slot : -1, abort);
       }

@@ -213,7 +213,7 @@ int pkc_paged_chunk_state(const void* q, const int32_t* q_indptr, int total_q, c
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   const size_t at = (workspace_bytes - partial) & ~size_t(255);  // >= PKC_STATUS_BYTES, a multiple of 256 like partial
   p.part_o = reinterpret_cast<float*>(ws + at);
-  p.part_lse = nullptr;  // set by the launcher, behind part_o
+  p.part_ml = nullptr;  // set by the launcher, behind part_o
   p.status = reinterpret_cast<int32_t*>(ws);
   const int e = launch_paged_chunk(p, dtype, stream);
   return e ? cuda_error(e, "paged_chunk_state launch") : PKC_OK;

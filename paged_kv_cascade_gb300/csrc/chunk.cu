@@ -284,9 +284,14 @@ __device__ __forceinline__ void store_out(const ChunkParams& p, int64_t row, int
   }
 }
 
-// Partial states: part_o[slot][column / 4][row][4], part_lse[slot][row] (base 2).
+// Partial states: part_o[slot][column / 4][row][4] and part_ml[slot][row], a row's
+// reference and its sum of exp2(s c - reference).  (Not their LSE: where that is far
+// from 0 a float32 holds little or nothing of the sum.)
 __device__ __forceinline__ float* part_row(const ChunkParams& p, int slot, int chunk, int row) {
   return p.part_o + (((int64_t)slot * 32 + chunk) * kRows + row) * 4;
+}
+__device__ __forceinline__ float2* part_sum(const ChunkParams& p, int slot, int row) {
+  return reinterpret_cast<float2*>(p.part_ml) + slot * kRows + row;
 }
 __device__ __forceinline__ int slot_of(int c, int c0) { return 2 * c + (c == c0 ? 1 : 0); }
 
@@ -441,7 +446,7 @@ __device__ __noinline__ void slow_rows(const ChunkParams& p, uint32_t far, uint3
         }
       }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l, lse2 = l == 0.f ? neg_inf() : m + lg2(l);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
     for (int r = 0; r < kAtOnce; ++r) {
       const float f = __shfl_sync(0xffffffffu, inv, 8 * r);
@@ -458,8 +463,8 @@ __device__ __noinline__ void slow_rows(const ChunkParams& p, uint32_t far, uint3
         *reinterpret_cast<uint2*>(static_cast<T*>(p.o) + out * PKC_HEAD_DIM + 4 * lane) =
             make_uint2(Elem<T>::from_f2(o[r][0], o[r][1]), Elem<T>::from_f2(o[r][2], o[r][3]));
       if (lane == 8 * r) {
-        if (slot >= 0) p.part_lse[slot * kRows + row[r]] = lse2;
-        else p.lse[out] = lse2 * kLn2;
+        if (slot >= 0) *part_sum(p, slot, row[r]) = make_float2(m, l);
+        else p.lse[out] = l == 0.f ? neg_inf() : (m + lg2(l)) * kLn2;
       }
     }
   }
@@ -479,16 +484,17 @@ __device__ __forceinline__ void merge_item(const ChunkParams& p, const Item& it,
 #pragma unroll 1
     for (int i0 = 0; i0 < n; i0 += 3) {
       float4 x[3][8];
-      float w[3], now = m;
+      float2 w[3];
+      float now = m;
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
         const int slot = slot_of(it.c0 + min(i0 + i, n - 1), it.c0);
-        w[i] = __ldcg(p.part_lse + slot * kRows + from);
+        w[i] = __ldcg(part_sum(p, slot, from));
 #pragma unroll
         for (int k = 0; k < 8; ++k) x[i][k] = __ldcg(reinterpret_cast<const float4*>(part_row(p, slot, chunk + k, from)));
       }
 #pragma unroll
-      for (int i = 0; i < 3; ++i) now = fmaxf(now, w[i]);  // (the last one again where there are fewer)
+      for (int i = 0; i < 3; ++i) now = fmaxf(now, w[i].x);  // (the last one again where there are fewer)
       const float ref = now == neg_inf() ? 0.f : now, f = ex2(m - ref);
       m = now;
       l *= f;
@@ -497,7 +503,7 @@ __device__ __forceinline__ void merge_item(const ChunkParams& p, const Item& it,
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
         if (i0 + i >= n) break;
-        const float e = ex2(w[i] - ref);
+        const float e = w[i].y * ex2(w[i].x - ref);
         l += e;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -1033,7 +1039,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const bool any = mine && l != 0.f;
       const float inv = any ? 1.f / l : 0.f;
-      const float lse2 = any ? m_ref + lg2(l) : neg_inf();
       if (mine) pass(bars->pv_done[x], (n_s - 1) & 1);
       tc_fence_after();
       uint64_t finite = 0ull;  // 0 times all of the row's O
@@ -1065,8 +1070,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (valid) {
-        if (!cut) p.lse[out] = lse2 * kLn2;
-        else p.part_lse[slot * kRows + row] = lse2;
+        if (!cut) p.lse[out] = any ? (m_ref + lg2(l)) * kLn2 : neg_inf();
+        else *part_sum(p, slot, row) = make_float2(any ? m_ref : neg_inf(), any ? l : 0.f);
       }
       bool odd;
       {
@@ -1143,11 +1148,11 @@ int launch_t(const ChunkParams& p, const CUtensorMap& mq, const CUtensorMap& mk,
 
 }  // namespace
 
-size_t chunk_partial_bytes() { return (size_t)2 * kMaxBlocks * kRows * (PKC_HEAD_DIM + 1) * 4; }
+size_t chunk_partial_bytes() { return (size_t)2 * kMaxBlocks * kRows * (PKC_HEAD_DIM + 2) * 4; }
 
 int launch_paged_chunk(const ChunkParams& params, int dtype, void* stream) {
   ChunkParams p = params;
-  p.part_lse = p.part_o + (size_t)2 * kMaxBlocks * kRows * PKC_HEAD_DIM;
+  p.part_ml = p.part_o + (size_t)2 * kMaxBlocks * kRows * PKC_HEAD_DIM;
   for (p.g_log2 = 0; 1 << p.g_log2 < p.g;) ++p.g_log2;
   p.o_wide = (reinterpret_cast<uintptr_t>(p.o) & 31) == 0;
   p.scale_log2 = std::max(p.scale_log2, FLT_MIN);  // a scale of 0 must not meet a masked score's infinity

@@ -370,8 +370,8 @@ struct ChunkParams {
   void* o;
   float* lse;
   int out_dtype;
-  float* part_o;             // partial states [slot, 256, 128], [slot, 256]
-  float* part_lse;
+  float* part_o;             // partial states [slot, 256, 128], [slot, 256, 2]
+  float* part_ml;
   int32_t* status;
 };
 

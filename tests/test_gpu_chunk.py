@@ -380,3 +380,8 @@ def test_scores_that_rise_from_tile_to_tile(dtype):
         for t in range(n):
             c.k[c.table[b, t // 16], t % 16, :, 0] = 16.0 * (t // 128) + 4.0 * (t // 128 % 2)
     c.check()
+
+
+@pytest.mark.parametrize("hq,hkv", [(3, 3), (5, 5), (12, 3), (7, 7), (40, 5)])
+def test_odd_numbers_of_heads(hq, hkv):
+    Case([(37, 91), (1, 300), (3, 0)], hq, hkv, F16, seed=hq).check()

@@ -261,3 +261,39 @@ def test_no_requests_need_no_arrays(total):
     assert pkc.lib().pkc_assign_pages(None, 4, None, None, total, 0, 16, 1000, None, slots.data_ptr(), pos.data_ptr(), None, ws.data_ptr(),
                                       ws.numel(), stream) == 0
     assert (slots == -1).all() and (pos == 0).all() and pkc.device_status(ws) == 0
+
+
+def test_many_tokens_captured_and_on_another_stream():
+    """Both launches of a call for many tokens in a graph, replayed over a table and a pool that are put back."""
+    rng = np.random.default_rng(8)
+    new = rng.integers(0, 900, 25).tolist()
+    lens, table, free = state(25, 16, 1400, 200, 80, 12)
+    run = Run(lens, table, free, 16, 1400)
+    indptr = [5] + (5 + np.cumsum(new)).tolist()
+    total = indptr[-1] + 11
+    d_indptr = torch.tensor(indptr, dtype=I32, device="cuda")
+    assert total > 8192
+    slots, pos, out = (torch.empty(total, dtype=torch.int64, device="cuda"), torch.empty(total, dtype=I32, device="cuda"), torch.empty(25, dtype=I32, device="cuda"))
+    old = run.d_table.clone(), run.d_free.clone()
+
+    def call(stream=None):
+        pkc.assign_pages(run.d_table, run.d_lens, d_indptr, total, run.d_free, 16, 1400, run.ws, slots=slots, positions=pos, seqlens_out=out, stream=stream)
+
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    want = ref.assign(run.table, run.lens, indptr, total, run.free, 16)
+    side = torch.cuda.Stream()
+    for replay in (True, True, False, True):
+        run.d_table.copy_(old[0])
+        run.d_free.copy_(old[1])
+        for x in (slots, pos, out):
+            x.fill_(-9)
+        if replay:
+            g.replay()
+        else:
+            side.wait_stream(torch.cuda.current_stream())
+            call(side)
+            torch.cuda.current_stream().wait_stream(side)
+        assert slots.tolist() == want[0] and pos.tolist() == want[1] and out.tolist() == want[2]
+        run.check(want[3])

@@ -114,3 +114,36 @@ def test_pages_that_are_not_there_in_a_cut_item():
     for i, j in enumerate((100, 101, 300)):
         c.table[0, j] = spare[i]
     ref.check_chunk(o, lse, c.reference(), F16)
+
+
+@pytest.mark.parametrize("dtype,score", [(F16, 6.875), (BF16, 8.875)])
+@pytest.mark.parametrize("late", [130, 1000, 1530])
+def test_a_late_key_that_holds_the_row(dtype, score, late):
+    """Single tokens whose attention is on one key, less than 2^13 above the first tile's best: its weight is the row's
+    largest, so it is exact, and the others' half steps are all that is lost.
+
+    The scores are products of one term: 2^-17 of a weight for them and the exponential.  An error e of a weight w moves
+    O by w e |v - O|; in fp16 e w is at least 2^-31 of the largest.  O is summed in 32 bits, 16 keys at a time: at most
+    a step of 2^-23 of its size for each of n / 16 additions, which need not round to nearest, and for eight roundings
+    of the sum, the quotient and the merge of pieces."""
+    reqs = [(1, 1530), (1, 5000)]
+    c = Case(reqs, 4, 1, dtype, seed=37, scale=1.0)
+    c.q[:] = 0
+    c.q[..., 0] = 1.0
+    c.k[..., 0] = torch.where(c.k[..., 0].isnan(), c.k[..., 0], torch.full_like(c.k[..., 0], -8.0))
+    for b in range(2):
+        for t, x in ((3, 0.0), (late, score)):
+            c.k[c.table[b, t // 16], t % 16, 0, 0] = x
+    o, lse = c.run(out_dtype=torch.float32)
+    assert pkc.device_status(c.ws) == 0
+    for b, n in enumerate(c.lens):
+        pages = c.table[b, :-(-n // 16)].long()
+        x, v = c.k[pages, :, 0, 0].flatten()[:n].double(), c.v[pages, :, 0].flatten(0, 1)[:n].double()
+        w = torch.softmax(x, 0)
+        want = w @ v
+        w[late] = 0
+        tol = (ref.HALF_STEP[dtype] + 2.0 ** -17) * (w @ (v - want).abs()) + 2.0 ** -17 * (v[late] - want).abs() + (n / 16 + 8) * 2.0 ** -23 * (want.abs() + w @ v.abs())
+        if dtype == F16:
+            tol += 2.0 ** -31 * (v - want).abs().sum(0)
+        assert float(((o[b].double().cpu() - want).abs() - tol).max()) <= 0
+        assert torch.all((lse[b].double().cpu() - torch.logsumexp(x, 0)).abs() <= 2.0 ** -18)

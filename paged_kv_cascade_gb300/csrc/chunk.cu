@@ -39,7 +39,7 @@
 // items have a closed form.  A piece of a cut item leaves a partial state; the
 // block that finishes last among the item's pieces (bits in the status block
 // tell) merges them, always in the order of the cache.  Few tokens over two caches
-// of 128k (19 pieces an item): 99 us, 79 of them bytes; the merge is 9 of the rest.
+// of 128k (19 pieces an item): 101 us, 79 of them bytes; the merge is 9 of the rest.
 //
 // Warps: 0-3 softmax of A, 4-7 of B (a row per thread, epilogue and merge too),
 // 8 issues Q K, 9 P V, 10 K copies, 11 V copies, 12 scheduler, 13 Q
@@ -47,20 +47,23 @@
 // fills a place has to have seen every phase of it); a tile is one TMA box per page
 // and 64 dims (pages that are not a power of two: boxes of their largest
 // power-of-two part).  The lanes of a warp issue their boxes one after another,
-// some 50 cycles each, so pages of 16 tokens need a warp for K and one for V.
+// some 50 cycles each, so pages of 16 tokens need a warp for K and one for V, and
+// smaller boxes are what bounds the kernel (prompts 505 us with pages of 64, 525 of 16,
+// 1040 of 20 or 4, whose boxes hold 4 tokens, 3560 to 3670 of 5 or 1).
 // All waits are bounded (2 s) and set PKC_ERR_TIMEOUT when they run out.  Keys that
 // one item alone reads pass L2 by (evict first: speculated tokens 111 -> 104 us), all
 // others stay (prompts 544 us, 596 if they pass by too).
 //
-// What bounds it.  A long chunk (2047 tokens over 65,001, 32 / 8 heads) takes 1.57 to
-// 1.62 ms, 1.37 to 1.41 PFLOP/s, at the power limit (1390 W, 1.70 GHz; a plain
-// product in a loop holds 1.76 PFLOP/s).  Below it the chain of a half's tile does:
+// What bounds it.  A long chunk (2047 tokens over 65,001, 32 / 8 heads) takes 1.55 to
+// 1.70 ms by board and run, 1.30 to 1.43 PFLOP/s, at the power limit (1390 W, 1.70 GHz; a
+// plain product in a loop holds 1.76 PFLOP/s).  Below it the chain of a half's tile does:
 // S out of TMEM, 128 exponentials a thread, P back, with the waits, votes and fences
 // between them some 2400 cycles, against 1024 of MMA, two halves at a time (tensor
-// pipe 58 % busy on prompts, 49 % with a window; exponentials 30 %).  An item's first
+// pipe 57 % busy on prompts, 48 % with a window; exponentials 30 %).  An item's first
 // tile and epilogue cost 3.7 us beside that.  The softmax warps have 216 registers
 // for 128 scores, and code that holds more spills (a branch over masked columns: a
-// window 161 -> 316 us); the instruction cache keeps the softmax, the epilogue and
+// window 161 -> 316 us).  Of the 284 bytes that are spilled the scheduler's 40 registers
+// cost 244, outside the loops over tiles; the instruction cache keeps the softmax, the epilogue and
 // the scheduler only while they are short, so most steps here took code away.
 //
 // Values that a row does not attend to meet P = 0, and 0 times an infinity or a
@@ -96,15 +99,15 @@ constexpr int kThreads = 512;
 constexpr int kQkWarp = 8, kPvWarp = 9, kKWarp = 10, kVWarp = 11, kSchedWarp = 12, kQWarp = 13;
 constexpr int kMaxBlocks = 160;
 // What an item costs, measured over whole launches (0.32 us a unit): a KV tile where
-// both halves have rows 1.58 us, where only one has 1.35 (as fast as HBM brings it),
-// and 3.7 us for the item itself (first tile, epilogue).  With 17 for the item, the
-// blocks that got short items were done 70 us before the others (prompts 542 us, 533
-// with 12; a mixed batch 161, 155).
+// both halves have rows 1.58 us, where only one has 1.35 (1.45 where all SMs run such
+// tiles, which is as fast as HBM brings them), and 3.7 us for the item itself (first
+// tile, epilogue).  With 17 for the item, the blocks that got short items were done 70 us
+// before the others (prompts 542 us, 533 with 12; a mixed batch 161, 155).
 constexpr int kTileCost = 5, kHalfTileCost = 4, kOver = 12;
 constexpr int kMinCost = 16;             // least cost of a block: a short item has one to itself
 // Items of at most so many tiles are not cut: a cut costs partial states and a merge
-// (prompts 533 us with 16, 523 with 12 and 4; a window's items of 11 tiles 162 with
-// 12, 171 with 8).
+// (prompts 533 us with 16, 523 with 12; a window's items of 11 tiles 162 with 12, 171
+// with 8).
 constexpr int kShort = 12;
 // A row's reference is its maximum less kLift: fp16 has no P below 2^-25, and what it
 // drops from O stays in the sum.  With the lift a weight is lost below 2^-31 of the

@@ -18,11 +18,12 @@
 // is its softmax, the MMAs run beside it.  (With an S per half and P in its
 // columns, Q K of tile j + 1 waited for P V of tile j: 3650 cycles a tile.)  P never
 // passes through shared memory, whose bandwidth the MMA's operands need.
-// m_ref, a row's reference, is its first tile's maximum (fp16: less kLift).  It moves
-// (and the row of O is rescaled, in TMEM) only when a tile's P would sum to more than
-// kMoveSum: P is formed at once, and again where the sum says so, so the other tiles
-// need no maximum at all (64 instructions and a chain ahead of the exponentials).  P
-// stays within fp16's largest number, and a row's sum is at least about 1.
+// m_ref, a row's reference, is its first tile's maximum (fp16: less kLift; items of at
+// most 128 rows: that of every tile, below).  It moves (and the row of O is rescaled, in
+// TMEM) only when a tile's P would sum to more than kMoveSum: P is formed at once, and
+// again where the sum says so, so the other tiles need no maximum at all (64 instructions
+// and a chain ahead of the exponentials).  P stays within fp16's largest number, and a
+// row's sum is at least about 1.
 // P enters the V product in 16 bits: a remainder beside it, as the decode holds one,
 // would be twice the product and columns that tensor memory does not have.  What that
 // costs is most where one key holds much of a row and its P is not a power of two, so
@@ -63,8 +64,8 @@
 // tile and epilogue cost 3.7 us beside that.  The softmax warps have 216 registers
 // for 128 scores, and code that holds more spills (a branch over masked columns: a
 // window 161 -> 316 us).  Of the 284 bytes that are spilled the scheduler's 40 registers
-// cost 244, outside the loops over tiles; the instruction cache keeps the softmax, the epilogue and
-// the scheduler only while they are short, so most steps here took code away.
+// cost 244, outside the loops over tiles.  The instruction cache keeps the softmax, the
+// epilogue and the scheduler only while they are short, so most steps here took code away.
 //
 // Values that a row does not attend to meet P = 0, and 0 times an infinity or a
 // NaN would be NaN: slots behind the length are zeroed in the V tile, and a row
@@ -975,7 +976,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // P V of the half's tile before has read P and brought O up to date.
         if (n_s > 0) pass(bars->pv_done[x], (n_s - 1) & 1);
         tc_fence_after();
-        bool move = t == lo || !all_set || n_rows <= kHalf;
+        bool move = t == lo || !all_set || n_rows <= kHalf;  // (few rows: every tile's maximum)
 #pragma unroll 1
         for (;;) {
           if (move) {

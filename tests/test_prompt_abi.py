@@ -69,13 +69,13 @@ def test_rope_refuses(L):
 
 
 def test_rope_refuses_outputs_on_its_inputs(L):
-    """5 tokens of 8 query heads (2 KB) and 2 KV heads (512 bytes), parts of one projection of 12 heads (3 KB) at
-    0x100000, or dense: q_out on q's rows, on q itself where they lie apart, on keys or values, by one element's worth."""
+    """5 tokens of 8 query heads (2 KB) and 2 KV heads (512 bytes), parts of one projection of 13 heads (3328
+    bytes) at 0x100000, or dense: q_out on q's rows, on q itself where they lie apart, on keys or values, by one element's worth."""
     base = 0x100000
-    end = base + 4 * 3072  # the last token's row
-    apart = [(base, 1536, base + 2048, base + 2560, 1536)]
+    end = base + 4 * 3328  # the last token's row
+    apart = [(base, 1664, base + 2048, base + 2560, 1664)]
     for q, qs, k, v, kvs in apart:
-        for out in (base, base + 16, base - 16, base + 3072, end + 2048 - 16, base - 5 * 2048 + 16,  # q
+        for out in (base, base + 16, base - 16, base + 3328, end + 2048 - 16, base - 5 * 2048 + 16,  # q
                     base + 2048, base + 2560 + 512 - 16, end + 2048, end + 2560 + 512 - 16):  # k, v
             args = [q, qs, k, v, kvs, 0x1000, 0x1000, 0x1000, 128, 0, 1.0, 5, 8, 2, 128, out, 0x800000, 0x900000, 16, 10, 1.0, 1.0, 1, 1,
                     WS, 1 << 20, None]

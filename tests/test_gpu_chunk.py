@@ -385,3 +385,25 @@ def test_scores_that_rise_from_tile_to_tile(dtype):
 @pytest.mark.parametrize("hq,hkv", [(3, 3), (5, 5), (12, 3), (7, 7), (40, 5)])
 def test_odd_numbers_of_heads(hq, hkv):
     Case([(37, 91), (1, 300), (3, 0)], hq, hkv, F16, seed=hq).check()
+
+
+def shifted(x, by):
+    """x in memory that begins `by` bytes behind a multiple of 256."""
+    n, size = x.numel(), x.element_size()
+    buf = torch.zeros(n + 256 // size, dtype=x.dtype, device="cuda")
+    out = buf[by // size:by // size + n].view(x.shape)
+    out.copy_(x)
+    assert out.data_ptr() % 256 == by
+    return out
+
+
+@pytest.mark.parametrize("out_dtype", [None, torch.float32])
+def test_least_alignment(out_dtype):
+    """Rows, pools and results on 16 bytes, whole numbers and LSE on 4."""
+    c = Case([(37, 91), (1, 1900), (140, 0)], 4, 2, F16, seed=24)
+    o = shifted(torch.full(c.q.shape, 7.0, dtype=out_dtype or F16), 16)
+    lse = shifted(torch.full(c.q.shape[:2], 7.0), 4)
+    pkc.paged_chunk_state(shifted(c.q, 48), shifted(torch.tensor(c.indptr, dtype=I32), 4), shifted(c.k, 16), shifted(c.v, 80), shifted(c.table, 4),
+                          shifted(torch.tensor(c.lens, dtype=I32), 12), c.scale, c.ws, o=o, lse=lse)
+    ref.check_chunk(o, lse, c.reference(), o.dtype)
+    assert pkc.device_status(c.ws) == 0

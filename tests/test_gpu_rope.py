@@ -222,3 +222,21 @@ def test_outputs_beside_the_inputs():
     with pytest.raises(pkc.PkcError, match="overlap"):
         pkc.rope_append_kv(c.q, c.k, c.v, c.positions.cuda(), c.slots.cuda(), c.freq.cuda(), *c.pools, c.ws,
                            q_out=torch.as_strided(c.q, (2, 4, 128), (512, 128, 1)))
+
+
+@pytest.mark.parametrize("kind", ["16", "e4m3"])
+def test_least_alignment(kind):
+    """Rows and pools on 16 bytes, slots and frequencies on 8, positions on 4."""
+    def shifted(x, by):
+        buf = torch.zeros(x.numel() + 256 // x.element_size(), dtype=x.dtype, device="cuda")
+        out = buf[by // x.element_size():][:x.numel()].view(x.shape)
+        assert out.data_ptr() % 256 == by
+        return out.copy_(x)
+
+    c = Case(61, 4, 2, F16, kind, rot=64, seed=12)
+    rows = shifted(torch.cat(c.host, 1), 16)
+    c.q, c.k, c.v = rows[:, :4], rows[:, 4:6], rows[:, 6:]
+    c.pools = [shifted(p, by) for p, by in zip(c.pools, (16, 48))]
+    out = pkc.rope_append_kv(c.q, c.k, c.v, shifted(c.positions, 4), shifted(c.slots, 8), shifted(c.freq, 8), *c.pools, c.ws, amplitude=c.amp,
+                             k_scale=c.k_scale, v_scale=c.v_scale, q_out=shifted(torch.zeros((61, 4, 128), dtype=F16), 16))
+    c.check(out, False)
